@@ -56,7 +56,9 @@ typedef enum {
   FM_ERR_UNSUPPORTED = 3,  /* valid but not built: head_dim other than 64 or 128 */
   FM_ERR_WORKSPACE = 4,    /* workspace pointer null/misaligned or smaller than fm_workspace_size */
   FM_ERR_CUDA = 5,         /* a CUDA runtime call failed */
-  FM_ERR_TIMEOUT = 6       /* a device-side wait expired; outputs are undefined */
+  FM_ERR_TIMEOUT = 6,      /* a device-side wait expired; outputs are undefined */
+  FM_ERR_CACHE = 7,        /* a length, page, node or row index out of range (device-detected) */
+  FM_ERR_PAGES = 8         /* the pool has too few free pages (device-detected) */
 } fm_status;
 
 /* Problem description.  H query heads; Hkv K/V heads (grouped-query
@@ -283,6 +285,150 @@ fm_status fm_fwd_fp8(const fm_desc* desc, const void* q8, const void* k8, const 
 fm_status fm_varlen_bounds(const int32_t* cu_seqlens, int n_seqs, int total, int causal,
                            int32_t* bounds, int* bad, void* stream);
 
+/* ------------------------------------------------------------ paged K/V cache
+ * Serving operators: a cache of K and V in pages, the attention of new tokens
+ * over it, and the page bookkeeping of a batch of growing sequences.  The
+ * pages the library follows describe no cache; these entry points have no
+ * counterpart there.
+ *
+ * The cache: K and V pools of n_pages pages of page_size tokens (16, 32, 64
+ * or 128) with Hkv heads of d (64 or 128) bf16 elements, for `layers` layers.
+ * Element (layer, page, slot, head, c) of a pool is at layer*stride[0] +
+ * page*stride[1] + slot*stride[2] + head*stride[3] + c (elements; multiples
+ * of 8, bases 16-byte aligned).  One page index means the same page in every
+ * layer.  Device arrays, all int32 and contiguous:
+ *   table [B][max_pages]  page of every page_size tokens of sequence b (a
+ *                         row); entries past its last page are not read,
+ *                         and not written
+ *   lens [B]              tokens of sequence b, 0 <= lens[b] <= max_pages * page_size
+ *   ref [n_pages]         rows that hold the page; 0: the page is free
+ *   cu [B + 1]            rows of a packed batch of new tokens: cu[0] = 0,
+ *                         sequence b's are [cu[b], cu[b+1]), cu[B] <= total;
+ *                         packed rows past cu[B] are neither read nor written
+ * Tokens with index above 2^30 are not supported.
+ *
+ * `status`: a device int32 owned by the caller, or null.  What the kernels
+ * find wrong is or-ed into it and never cleared by the library; it is read
+ * with fm_device_status(status, stream).  FM_ERR_CACHE: an entry of the
+ * arrays above out of range; each entry point says what it does with the
+ * sequence concerned.  No array index is followed out of its range. */
+typedef struct {
+  int B;           /* sequences (rows of the page table) */
+  int Hkv, d, page_size, n_pages;
+  int max_pages;   /* entries of a row of the page table */
+  int layers;      /* layers of the pools; fm_cache_append and fm_tree_fwd work on the one whose
+                      pools they are given */
+  int64_t k_stride[4], v_stride[4];  /* layer, page, slot, head */
+} fm_cache;
+
+/* Write the K and V of new tokens to the cache (one layer): packed row i of
+ * sequence b goes to token lens[b] - (cu[b+1] - cu[b]) + i - cu[b], so lens
+ * already counts the new tokens.  k, v: bf16, element (token, head, c) at
+ * token*k_stride[0] + head*k_stride[1] + c (v_stride likewise; multiples of
+ * 8), with `total` tokens.  A page that two rows share must not be written:
+ * fm_pages_reserve gives a row that grows a last page of its own.  Sequences
+ * with lens or cu out of range, and tokens whose page is out of range, are
+ * skipped (FM_ERR_CACHE). */
+fm_status fm_cache_append(const fm_cache* cache, const void* k, const void* v,
+                          const int64_t* k_stride, const int64_t* v_stride, const int32_t* cu,
+                          int total, void* k_pool, void* v_pool, const int32_t* table,
+                          const int32_t* lens, int32_t* status, void* stream);
+
+/* Attention of a batch of packed query tokens over the cache.  Sequence b
+ * has n = cu[b+1] - cu[b] query tokens, its nodes, whose K and V are the last
+ * n of its lens[b] cached tokens (fm_cache_append them first); the tokens
+ * before are its context.
+ *   parents != NULL: int32 [total]; parents[cu[b] + t] is the node (0 <=
+ *     parent < t, counted within the sequence) that node t was drafted after,
+ *     -1 for a root, -2 for a padding node.  Node t sees the whole context,
+ *     itself and its ancestors.  A padding node sees nothing and is seen by
+ *     none; a node drafted after one is a root.  At most
+ *     FM_TREE_MAX_NODES nodes per sequence.
+ *   parents == NULL: node t sees the context and nodes 0..t (one new token,
+ *     or a causal run of any length).
+ * O = softmax(scale * q k^T) v over the visible keys, exactly as fm_fwd, with
+ * query head h reading K/V head h / (H / Hkv); a key that a row does not see
+ * has no part in its result, whatever its K and V hold (NaN and infinities
+ * included).  Rows that see no key get O = 0 and LSE = -inf.
+ * q, o: bf16, element (token, head, c) at token*stride[0] + head*stride[1] +
+ * c; lse: fp32 [H][total].  scale: positive and finite.  max_nodes: an upper bound of n over the batch.
+ * Sequences with lens or cu out of range or more than max_nodes nodes get
+ * O = 0, LSE = -inf on those of their rows that lie in [0, total); keys on
+ * a page that is out of range read as 0, and a parent that is out of range
+ * counts as -1 (FM_ERR_CACHE).  The result of a call
+ * does not depend on the order in which its parts run: equal inputs give
+ * equal bits on the same GPU.  `ws`: fm_tree_workspace_size() bytes, 256-byte
+ * aligned, scratch of this call only; calls that may overlap on the GPU need
+ * one each. */
+#define FM_TREE_MAX_NODES 256
+typedef struct {
+  int H;          /* query heads, a multiple of Hkv */
+  int total;      /* packed query tokens: rows of q, o, parents, lse */
+  int max_nodes;  /* 1 <= max_nodes; at most FM_TREE_MAX_NODES with parents */
+  int64_t q_stride[2], o_stride[2];  /* token, head */
+} fm_tree_desc;
+size_t fm_tree_workspace_size(const fm_cache* cache, const fm_tree_desc* desc);
+fm_status fm_tree_fwd(const fm_cache* cache, const fm_tree_desc* desc, const void* q,
+                      const void* k_pool, const void* v_pool, const int32_t* table,
+                      const int32_t* lens, const int32_t* cu, const int32_t* parents, float scale,
+                      void* o, float* lse, void* ws, size_t ws_bytes, int32_t* status,
+                      void* stream);
+
+/* After the verification of a tree: keep the accepted nodes.  accept: int32
+ * [B][max_accept], of row b the first n_accept[b] entries are its accepted
+ * nodes, strictly ascending in [0, cu[b+1] - cu[b]).  In all layers, the K
+ * and V of node accept[b][i] move to token base + i, base = lens[b] -
+ * (cu[b+1] - cu[b]); lens_out[b] = base + n_accept[b].  ref, if
+ * not null: the row's pages past its new length lose its hold (those that
+ * no other row holds are free).  A sequence with anything out of range is
+ * left as it is, lens_out[b] = lens[b] (FM_ERR_CACHE).  lens_out may not
+ * overlap lens. */
+fm_status fm_cache_accept(const fm_cache* cache, const int32_t* accept, int max_accept,
+                          const int32_t* n_accept, const int32_t* cu, void* k_pool, void* v_pool,
+                          const int32_t* table, const int32_t* lens, int32_t* lens_out, int32_t* ref,
+                          int32_t* status, void* stream);
+
+/* Rows after a step of a search or of a scheduler: new row b is old row
+ * parent[b] (-1: an empty row), sharing its pages; ref_out = ref plus the
+ * new rows' holds minus the old rows'.  This forks, copies, reorders and
+ * frees sequences.  table_out and lens_out may not overlap table and lens;
+ * ref_out may be ref itself.  Of table_out, the entries of each row's pages
+ * are written.  An old row with lens out of range counts as empty, a parent
+ * out of range as -1 and a page out of range is not counted (FM_ERR_CACHE).
+ * Only B, page_size, n_pages and max_pages of `cache` are used.  A page whose
+ * last row is freed is free at once: its contents are no longer needed. */
+fm_status fm_pages_fork(const fm_cache* cache, const int32_t* parent, const int32_t* table,
+                        const int32_t* lens, const int32_t* ref, int32_t* table_out,
+                        int32_t* lens_out, int32_t* ref_out, int32_t* status, void* stream);
+
+/* Room for grow[b] >= 0 more tokens of every row: lens_out = lens + grow, and
+ * rows take the free pages (ref 0) in ascending order, row by row.  A row
+ * that grows and whose last page is not full and held by other rows too
+ * (ref > 1 at the start of the call) first takes a page that replaces it, and
+ * its tokens there are copied, in all layers.  All or nothing: if the free
+ * pages do not suffice (FM_ERR_PAGES), or a row would not fit in max_pages,
+ * or an entry is out of range (FM_ERR_CACHE), every row and count stays as
+ * it is.  info: int32 [2], free pages after the call and pages that the rows asked
+ * for (a row out of range asks for none).  Each of table_out, lens_out, ref_out is its input itself or does not
+ * overlap it.  `ws`: fm_pages_workspace_size() bytes, 256-byte aligned,
+ * scratch of this call only. */
+size_t fm_pages_workspace_size(const fm_cache* cache);
+fm_status fm_pages_reserve(const fm_cache* cache, const int32_t* grow, void* k_pool, void* v_pool,
+                           const int32_t* table, const int32_t* lens, const int32_t* ref,
+                           int32_t* table_out, int32_t* lens_out, int32_t* ref_out, int32_t* info,
+                           void* ws, size_t ws_bytes, int32_t* status, void* stream);
+
+/* Compact the pool: its n_live held pages become pages [0, n_live).  The k-th
+ * held page at or past n_live moves to the k-th free page below it (contents
+ * in all layers, its count, and every row's table entry); the others stay.
+ * n_live: int32 [1].  table_out, ref_out, ws as in fm_pages_reserve (lens
+ * does not change).  A row with lens out of range counts as empty, and a table
+ * entry out of range stays as it is (FM_ERR_CACHE). */
+fm_status fm_pages_compact(const fm_cache* cache, void* k_pool, void* v_pool, const int32_t* table,
+                           const int32_t* lens, const int32_t* ref, int32_t* table_out,
+                           int32_t* ref_out, int32_t* n_live, void* ws, size_t ws_bytes,
+                           int32_t* status, void* stream);
+
 /* Kernel timing, for benchmarks.  While enabled, every kernel the library
  * launches is bracketed by a pair of CUDA events recorded on its own stream
  * (event objects are created on first use and reused; no device memory is
@@ -291,7 +437,9 @@ fm_status fm_varlen_bounds(const int32_t* cu_seqlens, int n_seqs, int total, int
  * total_ms[0..n) and launches[0..n) (either may be NULL), and clears the
  * record.  Kernel ids: 0 block summary, 1 classify, 2 unit order,
  * 3 localize, 4 forward, 5 backward preprocess, 6 backward dK/dV, 7 backward
- * dQ, 8 partial-tile visibility masks, 9 FP8 quantisation, 10 FP8 forward;
+ * dQ, 8 partial-tile visibility masks, 9 FP8 quantisation, 10 FP8 forward,
+ * 11 cache append, 12 tree attention, 13 its joining of split rows, 14 cache
+ * accept, 15 page fork, 16 page plan (reserve and compact), 17 page copies;
  * fm_kernel_name(id) names them.  At most 65536 launches are recorded per
  * read; later launches are counted but not timed. */
 fm_status fm_profile_enable(int on);
@@ -324,9 +472,11 @@ fm_status fm_measure_exp2_rate(double* per_second, void* stream);
  * FM_ERR_INVALID for other withhold values. */
 fm_status fm_test_hooks(uint64_t wait_limit_ns, int withhold_release);
 
-/* Synchronise `stream` and read the device status word of `ws`: FM_OK,
- * FM_ERR_BOUNDS, FM_ERR_TIMEOUT, or FM_ERR_CUDA if a kernel found its shared
- * memory misaligned and did nothing (precedence: CUDA, timeout, bounds). */
+/* Synchronise `stream` and read the device status word of `ws` (or a cache
+ * entry point's `status` word): FM_OK, FM_ERR_BOUNDS, FM_ERR_TIMEOUT,
+ * FM_ERR_CACHE, FM_ERR_PAGES, or FM_ERR_CUDA if a kernel found its shared
+ * memory misaligned and did nothing (precedence: CUDA, timeout, bounds,
+ * cache, pages). */
 fm_status fm_device_status(const void* ws, void* stream);
 
 /* Static description of a status code. */

@@ -12,6 +12,10 @@ aligned storage such as torch's own allocations, take the kernels' faster
 32-byte stores).  ``bounds`` is an int32 CUDA tensor [4][B][Hm][Skv] holding
 LTS, LTE, UTS, UTE; key j is hidden from query row i iff LTS[j] <= i < LTE[j]
 or UTS[j] <= i < UTE[j].
+
+For serving, ``cache.py`` has the paged K/V cache: appending tokens, attention
+of single tokens, causal runs and drafted trees over it, and its pages'
+bookkeeping.
 """
 from __future__ import annotations
 
@@ -21,10 +25,13 @@ from typing import NamedTuple
 import torch
 
 from ._abi import FMError, FmDesc, FmWsLayout, check, lib  # noqa: F401
+from .cache import (cache_accept, cache_append, make_cache, pages_compact,  # noqa: F401
+                    pages_fork, pages_reserve, pages_workspace, tree_forward, tree_workspace)
 
 __all__ = ["FMError", "make_desc", "workspace_size", "workspace_layout", "workspace", "plan",
            "forward", "backward", "localize", "device_status", "lib", "profile_enable",
-           "profile_read"]
+           "profile_read", "make_cache", "cache_append", "tree_forward", "tree_workspace",
+           "cache_accept", "pages_fork", "pages_reserve", "pages_compact", "pages_workspace"]
 
 
 def _stream_ptr(stream):
@@ -235,7 +242,8 @@ def localize(bounds, chunks, out=None, stream=None):
 
 
 def device_status(ws, stream=None) -> int:
-    """Synchronise and return the device status code of a workspace (0 = OK)."""
+    """Synchronise and return the device status code of a workspace, or of the
+    ``status`` tensor given to the cache's calls (0 = OK)."""
     return lib().fm_device_status(_p(ws), _stream_ptr(stream))
 
 

@@ -9,12 +9,13 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libfm.so")
 
 FM_OK, FM_ERR_INVALID, FM_ERR_BOUNDS, FM_ERR_UNSUPPORTED, FM_ERR_WORKSPACE, FM_ERR_CUDA, \
-    FM_ERR_TIMEOUT = range(7)
+    FM_ERR_TIMEOUT, FM_ERR_CACHE, FM_ERR_PAGES = range(9)
 
 STATUS_NAMES = {
     FM_OK: "FM_OK", FM_ERR_INVALID: "FM_ERR_INVALID", FM_ERR_BOUNDS: "FM_ERR_BOUNDS",
     FM_ERR_UNSUPPORTED: "FM_ERR_UNSUPPORTED", FM_ERR_WORKSPACE: "FM_ERR_WORKSPACE",
-    FM_ERR_CUDA: "FM_ERR_CUDA", FM_ERR_TIMEOUT: "FM_ERR_TIMEOUT",
+    FM_ERR_CUDA: "FM_ERR_CUDA", FM_ERR_TIMEOUT: "FM_ERR_TIMEOUT", FM_ERR_CACHE: "FM_ERR_CACHE",
+    FM_ERR_PAGES: "FM_ERR_PAGES",
 }
 
 
@@ -31,6 +32,18 @@ class FmWsLayout(ctypes.Structure):
         "status", "summary", "table", "row_count", "row_list", "col_count", "col_list",
         "fwd_order", "bwd_order", "row_mask", "masks", "pair_info", "pair_list", "delta",
         "lse_log2", "row_order", "total")]
+
+
+class FmCache(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("Hkv", ctypes.c_int), ("d", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("n_pages", ctypes.c_int),
+                ("max_pages", ctypes.c_int), ("layers", ctypes.c_int),
+                ("k_stride", ctypes.c_int64 * 4), ("v_stride", ctypes.c_int64 * 4)]
+
+
+class FmTreeDesc(ctypes.Structure):
+    _fields_ = [("H", ctypes.c_int), ("total", ctypes.c_int), ("max_nodes", ctypes.c_int),
+                ("q_stride", ctypes.c_int64 * 2), ("o_stride", ctypes.c_int64 * 2)]
 
 
 class FMError(RuntimeError):
@@ -69,6 +82,22 @@ SIGNATURES = {
                                         P]),
     "fm_localize": (ctypes.c_int, [I32P, ctypes.c_int, ctypes.c_int, ctypes.c_int, P, P,
                                    ctypes.c_int, I32P, P]),
+    "fm_cache_append": (ctypes.c_int, [ctypes.POINTER(FmCache), P, P, P, P, I32P, ctypes.c_int, P, P,
+                                       I32P, I32P, P, P]),
+    "fm_tree_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(FmCache),
+                                                 ctypes.POINTER(FmTreeDesc)]),
+    "fm_tree_fwd": (ctypes.c_int, [ctypes.POINTER(FmCache), ctypes.POINTER(FmTreeDesc), P, P, P,
+                                   I32P, I32P, I32P, I32P, ctypes.c_float, P, P, P, ctypes.c_size_t,
+                                   P, P]),
+    "fm_cache_accept": (ctypes.c_int, [ctypes.POINTER(FmCache), I32P, ctypes.c_int, I32P, I32P, P, P,
+                                       I32P, I32P, I32P, I32P, P, P]),
+    "fm_pages_fork": (ctypes.c_int, [ctypes.POINTER(FmCache), I32P, I32P, I32P, I32P, I32P, I32P,
+                                     I32P, P, P]),
+    "fm_pages_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(FmCache)]),
+    "fm_pages_reserve": (ctypes.c_int, [ctypes.POINTER(FmCache), I32P, P, P, I32P, I32P, I32P, I32P,
+                                        I32P, I32P, I32P, P, ctypes.c_size_t, P, P]),
+    "fm_pages_compact": (ctypes.c_int, [ctypes.POINTER(FmCache), P, P, I32P, I32P, I32P, I32P, I32P,
+                                        I32P, P, ctypes.c_size_t, P, P]),
     "fm_device_status": (ctypes.c_int, [P, P]),
     "fm_test_hooks": (ctypes.c_int, [ctypes.c_uint64, ctypes.c_int]),
     "fm_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -79,7 +108,7 @@ SIGNATURES = {
     "fm_measure_exp2_rate": (ctypes.c_int, [P, P]),
 }
 
-KERNEL_IDS = 11
+KERNEL_IDS = 18
 
 
 def lib():

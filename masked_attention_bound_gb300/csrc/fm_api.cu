@@ -321,6 +321,8 @@ fm_status fm_device_status(const void* ws, void* stream) {
   if (word & DEV_LAYOUT) return FM_ERR_CUDA;
   if (word & DEV_TIMEOUT) return FM_ERR_TIMEOUT;
   if (word & DEV_BOUNDS) return FM_ERR_BOUNDS;
+  if (word & DEV_CACHE) return FM_ERR_CACHE;
+  if (word & DEV_PAGES) return FM_ERR_PAGES;
   return FM_OK;
 }
 
@@ -340,6 +342,8 @@ const char* fm_status_string(fm_status s) {
     case FM_ERR_WORKSPACE: return "workspace missing, misaligned or too small";
     case FM_ERR_CUDA: return "CUDA runtime error";
     case FM_ERR_TIMEOUT: return "device wait timed out";
+    case FM_ERR_CACHE: return "cache length, page, node or row index out of range";
+    case FM_ERR_PAGES: return "not enough free pages";
   }
   return "unknown status";
 }

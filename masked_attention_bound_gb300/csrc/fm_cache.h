@@ -1,0 +1,42 @@
+// Host-side declarations of the paged K/V cache's translation units.
+#pragma once
+#include "fm_internal.h"
+
+namespace fm {
+
+constexpr int kMaxTokenIndex = 1 << 30;   // tokens of a row (32-bit positions)
+constexpr int kMaxPoolPages = 1 << 24;
+
+// Sizes of `c` that every cache entry point needs; `pools`: its pools' too.
+fm_status check_cache(const fm_cache* c, bool pools);
+
+inline bool aligned_to(const void* p, uintptr_t n) {
+  return p && (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0;
+}
+
+// [a, a + na) and [b, b + nb) share a byte.
+inline bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
+  const char* x = static_cast<const char*>(a);
+  const char* y = static_cast<const char*>(b);
+  return x < y + nb && y < x + na;
+}
+
+// A launch that may start while the kernel before it in the stream still
+// runs (it calls grid_dependency_wait() before it touches memory).
+template <typename... P, typename... A>
+inline cudaError_t launch_dependent(void (*kern)(P...), dim3 grid, int threads, size_t smem,
+                                    cudaStream_t s, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...);
+}
+
+}  // namespace fm

@@ -101,7 +101,8 @@ TestHooks test_hooks();
 
 // Kernel ids for the timing hooks (fm_profile_*).
 enum KernelId : int { K_SUMMARY = 0, K_CLASSIFY, K_ORDER, K_LOCALIZE, K_FWD, K_BWD_PRE, K_BWD,
-                      K_BWD_DQ, K_TILE_MASKS, K_QUANT, K_FWD8, K_COUNT };
+                      K_BWD_DQ, K_TILE_MASKS, K_QUANT, K_FWD8, K_CACHE_APPEND, K_TREE, K_TREE_JOIN,
+                      K_CACHE_ACCEPT, K_PAGES_FORK, K_PAGES_PLAN, K_PAGES_COPY, K_COUNT };
 void prof_begin(int id, cudaStream_t s);
 void prof_end(int id, cudaStream_t s);
 

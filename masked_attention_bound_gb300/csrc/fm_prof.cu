@@ -128,7 +128,9 @@ const char* fm_kernel_name(int id) {
   static const char* names[K_COUNT] = {"summary_kernel", "classify_kernel", "order_kernel",
                                        "localize_kernel", "fwd_kernel", "bwd_pre_kernel",
                                        "bwd_kv_kernel", "bwd_dq_kernel", "tile_mask_kernel",
-                                       "quant_kernel", "fwd_fp8_kernel"};
+                                       "quant_kernel", "fwd_fp8_kernel", "append_kernel",
+                                       "tree_kernel", "tree_join_kernel", "accept_kernel",
+                                       "fork_kernel", "page_plan_kernel", "page_copy_kernel"};
   return (id >= 0 && id < K_COUNT) ? names[id] : "unknown";
 }
 

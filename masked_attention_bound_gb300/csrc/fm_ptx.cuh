@@ -24,6 +24,8 @@ enum : int {
   DEV_BOUNDS = 1,     // a bound value outside [0, Sq]
   DEV_TIMEOUT = 2,    // an mbarrier wait ran past its time limit
   DEV_LAYOUT = 4,     // shared memory not 1024-byte aligned: the kernel did nothing
+  DEV_CACHE = 8,      // a cache length, page, node or row index out of range
+  DEV_PAGES = 16,     // the pool has too few free pages
 };
 
 #ifndef FM_WAIT_LIMIT_NS
@@ -123,6 +125,19 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
           dst),
       "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
       : "memory");
+}
+
+// ---------------------------------------------------------------- launches
+// A kernel launched with programmatic stream serialisation starts while the
+// one before it in the stream still runs: it may set up, and waits here until
+// that kernel has ended and its writes are visible.
+__device__ __forceinline__ void grid_dependency_wait() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+// Lets the next kernel of the stream start early (it still waits above for
+// this one's end).
+__device__ __forceinline__ void grid_launch_dependents() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
 // ---------------------------------------------------------------- tcgen05

@@ -1,0 +1,624 @@
+// Attention of drafted trees and single tokens over the paged cache: the
+// entry point, the kernel for units of up to 16 rows, and the join of units
+// that several blocks worked on.
+#include <cmath>
+
+#include "fm_tree.h"
+
+namespace fm {
+
+// ---------------------------------------------------------------- narrow kernel
+// Units of up to 16 rows (one token of up to 16 query heads per K/V head, or
+// a few nodes).  Bound by reading K and V once: 512 bytes per key and head at
+// d = 128 against 8 KFLOP.  A warp loads K and V tiles by TMA through a ring
+// of tiles; eight warps each take 16 keys of every 128-key tile and keep
+// their own running maximum, sum and O in registers, so no warp waits for
+// another inside a unit.  S and O come from mma.sync (16 x 8 x 16, bf16): its
+// fragments leave P in registers as the A operand of the second product, and
+// 16 rows fill its M, where a tcgen05.mma would pad them to 128.
+template <int D>
+struct NarrowCfg {
+  static constexpr int R = 16;
+  static constexpr int WARPS = 8;                  // consumers
+  static constexpr int THREADS = 32 * (WARPS + 1);
+  static constexpr int TILE = kTile * D * 2;       // bytes of a K or V tile
+  static constexpr int SLOTS = D == 128 ? 5 : 10;  // ring of tiles: K0 V0 K1 V1 ...
+  static constexpr int PITCH = D + 8;              // floats of a row of the merge buffer
+  static constexpr int OFF_MERGE = SLOTS * TILE;
+  static constexpr int OFF_ML = OFF_MERGE + 4 * R * PITCH * 4;   // [WARPS][R] max, then sum
+  static constexpr int OFF_SEEN = OFF_ML + 2 * WARPS * R * 4;    // [R][8] ancestors
+  static constexpr int OFF_NF = OFF_SEEN + R * 8 * 4;            // [8] keys with values not finite
+  static constexpr int OFF_BAR = OFF_NF + 32;
+  static constexpr int OFF_SCAN = OFF_BAR + (2 * SLOTS + 1) * 8;  // after the barriers: abort flag
+  static constexpr int SMEM = OFF_SCAN + sizeof(TreeScan);
+};
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void named_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+template <int D>
+__global__ void __launch_bounds__(NarrowCfg<D>::THREADS, 1)
+    tree_narrow_kernel(const __grid_constant__ TreeParams P, const __grid_constant__ CUtensorMap tmK,
+                       const __grid_constant__ CUtensorMap tmV) {
+  using C = NarrowCfg<D>;
+  constexpr int R = C::R;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  TreeScan& scan = *reinterpret_cast<TreeScan*>(smem + C::OFF_SCAN);
+  volatile int& abort_flag = *reinterpret_cast<volatile int*>(smem + C::OFF_SCAN - 8);
+  if (smem_u32(smem) & 1023u) {
+    if (threadIdx.x == 0 && P.status) atomicOr(P.status, DEV_LAYOUT);
+    return;
+  }
+  const uint32_t sbase = smem_u32(smem);
+  const uint32_t bar0 = sbase + C::OFF_BAR;
+  auto full = [&](int i) { return bar0 + 8u * i; };
+  auto empty = [&](int i) { return bar0 + 8u * (C::SLOTS + i); };
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int i = 0; i < C::SLOTS; ++i) {
+      mbar_init(full(i), 1);
+      mbar_init(empty(i), C::WARPS);
+    }
+    abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == C::WARPS && lane == 0) {
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+  }
+  grid_launch_dependents();
+  TreeWalk<R> walk;
+  walk.run = tree_run<R, C::THREADS>(P, scan);   // synchronises the block
+  __syncthreads();
+
+  // every lane gets the same answer
+  auto wait_all = [&](uint32_t bar, uint32_t parity) -> bool {
+    bool ok = !abort_flag;
+    if (ok) ok = mbar_wait(bar, parity, P.status, P.wait_ns);
+    if (!ok) abort_flag = 1;
+    return __all_sync(0xffffffffu, ok);
+  };
+
+  if (warp == C::WARPS) {
+    // ------------------------------------------------------------ loads
+    uint32_t i = 0;   // ring position: 2 e for K of the e-th tile, 2 e + 1 for V
+    TreePiece u;
+    bool ok = true;
+    while (ok && walk.next(P, u)) {
+      if (u.keys == 0) continue;
+      int page = TileLoad<D>::lane_page(P, u, u.t0, lane);
+      for (int t = u.t0; ok && t < u.t1; ++t) {
+        const int next = t + 1 < u.t1 ? TileLoad<D>::lane_page(P, u, t + 1, lane) : 0;
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv, ++i) {
+          const int slot = i % C::SLOTS;
+          const uint32_t use = i / C::SLOTS;
+          if (use > 0) ok = wait_all(empty(slot), (use - 1) & 1);
+          if (!ok) break;
+          TileLoad<D>::issue(P, u, t, lane, page, kv ? &tmV : &tmK, sbase + slot * C::TILE,
+                             full(slot));
+        }
+        page = next;
+      }
+    }
+    // every issued copy has landed before the block may exit
+    __syncwarp();
+    if (lane == 0)
+      for (uint32_t x = i > C::SLOTS ? i - C::SLOTS : 0; x < i; ++x)
+        mbar_wait(full(x % C::SLOTS), (x / C::SLOTS) & 1, P.status, P.wait_ns);
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ attention
+    // A warp whose wait gave up goes on without waiting or computing: the
+    // block-wide merges of every piece still find all eight warps.
+    bool ok = true;
+    uint32_t i = 0;
+    const int g = lane >> 2, tq = lane & 3;      // fragment row and column pair
+    uint32_t* seen = reinterpret_cast<uint32_t*>(smem + C::OFF_SEEN);
+    uint32_t* nf = reinterpret_cast<uint32_t*>(smem + C::OFF_NF);
+    float* merge = reinterpret_cast<float*>(smem + C::OFF_MERGE);
+    float* ml = reinterpret_cast<float*>(smem + C::OFF_ML);
+    int4 rec = make_int4(-1, 0, 0, 0);
+    TreePiece u;
+    while (walk.next(P, u)) {
+      // tiles from this one on hold keys that not every row sees
+      const int part0 = u.origin / kTile;
+      // which keys past origin a row sees: bit j is key origin + j
+      if (warp == 0) {
+        uint32_t w[8];
+        const int node = (u.row_first + min(lane, u.rows - 1)) / P.G;
+        if (P.tree) {
+          if (lane < R && u.s.base >= 0) tree_ancestors(P, u.s, node, w);
+        } else {
+          const int upto = u.s.base + node - u.origin;   // 0 .. R - 1
+#pragma unroll
+          for (int x = 0; x < 8; ++x)
+            w[x] = upto >= 32 * x + 31 ? 0xffffffffu
+                                       : (upto < 32 * x ? 0u : (2u << (upto - 32 * x)) - 1u);
+        }
+        if (lane < R && u.s.base >= 0)
+#pragma unroll
+          for (int x = 0; x < 8; ++x) seen[lane * 8 + x] = w[x];
+        if (lane < 8) nf[lane] = 0;
+      }
+      // Q of rows g and g + 8 as A fragments, straight from memory
+      uint32_t qf[D / 16][4];
+#pragma unroll
+      for (int hh = 0; hh < 2; ++hh) {
+        const int r = g + 8 * hh;
+        const int rr = u.row_first + r;
+        const int node = rr / P.G;
+        const __nv_bfloat16* src = P.q + (u.s.row0 + node) * P.q_stride[0] +
+                                   (u.hk * P.G + rr - node * P.G) * P.q_stride[1] + 2 * tq;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          qf[kk][hh] = r < u.rows ? *reinterpret_cast<const uint32_t*>(src + kk * 16) : 0u;
+          qf[kk][hh + 2] = r < u.rows ? *reinterpret_cast<const uint32_t*>(src + kk * 16 + 8) : 0u;
+        }
+      }
+      named_sync(1, 32 * C::WARPS);     // seen, nf
+      float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+      float acc[D / 8][4];
+#pragma unroll
+      for (int x = 0; x < D / 8; ++x)
+#pragma unroll
+        for (int y = 0; y < 4; ++y) acc[x][y] = 0.f;
+
+      for (int t = u.t0; u.keys > 0 && t < u.t1; ++t) {
+        const int ks = i % C::SLOTS, vs = (i + 1) % C::SLOTS;
+        const uint32_t kp = (i / C::SLOTS) & 1, vp = ((i + 1) / C::SLOTS) & 1;
+        i += 2;
+        const int k0 = t * kTile + warp * 16;          // first key of this warp
+        const uint32_t sk = sbase + ks * C::TILE, sv = sbase + vs * C::TILE;
+        const bool mine = k0 < u.keys;                 // any keys at all
+        if (ok) ok = wait_all(full(ks), kp);
+        float s[2][4];
+        if (ok && mine) {
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int y = 0; y < 4; ++y) s[x][y] = 0.f;
+          // matrices of one ldmatrix: keys 0-7 d 0-7, keys 0-7 d 8-15, keys
+          // 8-15 d 0-7, keys 8-15 d 8-15
+          const int key = warp * 16 + (lane & 7) + ((lane >> 4) << 3);
+          const int chunk0 = (lane >> 3) & 1;
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            uint32_t b[4];
+            const int ch = kk * 2 + chunk0;
+            ldsm4(sk + (ch >> 3) * (kTile * 128) + key * 128 + (((ch & 7) ^ (key & 7)) << 4), b);
+            mma16816(s[0], qf[kk], b[0], b[1]);
+            mma16816(s[1], qf[kk], b[2], b[3]);
+          }
+        }
+        mbar_arrive_warp(empty(ks));
+        uint32_t pf[4];
+        if (ok && mine) {
+          if (t >= part0 || k0 + 16 > u.keys) {
+            // keys past origin: only what the row sees
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+              for (int y = 0; y < 4; ++y) {
+                const int key = k0 + x * 8 + 2 * tq + (y & 1), r = g + 8 * (y >> 1);
+                const int j = key - u.origin;
+                const bool vis = key < u.keys && (j < 0 || ((seen[r * 8 + (j >> 5)] >> (j & 31)) & 1u));
+                if (!vis) s[x][y] = -INFINITY;
+              }
+          }
+          bool grow = false;
+          float alpha[2], ref[2];
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {
+            float mx = fmaxf(fmaxf(s[0][2 * hh], s[0][2 * hh + 1]),
+                             fmaxf(s[1][2 * hh], s[1][2 * hh + 1]));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+            mx *= P.scale_log2;
+            // the reference moves only when the maximum grows by more than
+            // 2^8: until then P stays in range and nothing is rescaled
+            const bool up = mx > m[hh] + 8.f;
+            alpha[hh] = up ? ex2(m[hh] - mx) : 1.f;
+            m[hh] = up ? mx : m[hh];
+            ref[hh] = m[hh] == -INFINITY ? 0.f : m[hh];
+            grow |= up;
+          }
+          if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+            for (int x = 0; x < D / 8; ++x)
+#pragma unroll
+              for (int y = 0; y < 4; ++y) acc[x][y] *= alpha[y >> 1];
+            l[0] *= alpha[0];
+            l[1] *= alpha[1];
+          }
+          float p[2][4];
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              p[x][y] = ex2(fmaf(s[x][y], P.scale_log2, -ref[y >> 1]));
+              l[y >> 1] += p[x][y];
+            }
+          // P rounded to bf16 for the second product, as in the other
+          // forwards (the sum l keeps its 32 bits)
+          pf[0] = pack_bf16(p[0][0], p[0][1]);
+          pf[1] = pack_bf16(p[0][2], p[0][3]);
+          pf[2] = pack_bf16(p[1][0], p[1][1]);
+          pf[3] = pack_bf16(p[1][2], p[1][3]);
+        }
+        if (ok) ok = wait_all(full(vs), vp);
+        if (ok && mine) {
+          if (t >= part0 || k0 + 16 > u.keys) {
+            // this warp's 16 rows of V: zeros past the unit's keys, and clean
+            // where not every row sees the key
+            const int row = warp * 16 + (lane >> 1);
+            const int key = k0 + (lane >> 1), j = key - u.origin;
+            bool dirty = false;
+            for (int ch = (lane & 1) * (D / 16); ch < ((lane & 1) + 1) * (D / 16); ++ch) {
+              const uint32_t at = (ch >> 3) * (kTile * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4);
+              uint4* ptr = reinterpret_cast<uint4*>(smem + vs * C::TILE + at);
+              if (key >= u.keys) {
+                *ptr = make_uint4(0u, 0u, 0u, 0u);
+              } else if (j >= 0) {
+                uint4 x = *ptr;
+                if (bf16x2_not_finite(x.x) || bf16x2_not_finite(x.y) || bf16x2_not_finite(x.z) ||
+                    bf16x2_not_finite(x.w)) {
+                  dirty = true;
+                  x.x = bf16x2_clean(x.x);
+                  x.y = bf16x2_clean(x.y);
+                  x.z = bf16x2_clean(x.z);
+                  x.w = bf16x2_clean(x.w);
+                  *ptr = x;
+                }
+              }
+            }
+            if (dirty) atomicOr(nf + (j >> 5), 1u << (j & 31));
+            fence_proxy_async_smem();   // before the next copy into this slot
+            __syncwarp();
+          }
+          // matrices: keys 0-7 d 0-7, keys 8-15 d 0-7, keys 0-7 d 8-15, keys 8-15 d 8-15
+          const int row = warp * 16 + (lane & 15);
+          const int chunk0 = lane >> 4;
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            uint32_t b[4];
+            const int ch = kk * 2 + chunk0;
+            ldsm4_t(sv + (ch >> 3) * (kTile * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4), b);
+            mma16816(acc[2 * kk], pf, b[0], b[1]);
+            mma16816(acc[2 * kk + 1], pf, b[2], b[3]);
+          }
+        }
+        mbar_arrive_warp(empty(vs));
+      }
+
+      // ---------------------------------------------------------- merge the eight warps
+#pragma unroll
+      for (int hh = 0; hh < 2; ++hh) {
+        l[hh] += __shfl_xor_sync(0xffffffffu, l[hh], 1);
+        l[hh] += __shfl_xor_sync(0xffffffffu, l[hh], 2);
+        if (P.tree) {
+          // a padding node's row sees nothing, the context included
+          const uint4* w = reinterpret_cast<const uint4*>(seen + (g + 8 * hh) * 8);
+          const uint4 a = w[0], b = w[1];
+          if ((a.x | a.y | a.z | a.w | b.x | b.y | b.z | b.w) == 0) {
+            m[hh] = -INFINITY;
+            l[hh] = 0.f;
+          }
+        }
+        if (tq == 0) {
+          ml[warp * R + g + 8 * hh] = m[hh];
+          ml[(C::WARPS + warp) * R + g + 8 * hh] = l[hh];
+        }
+      }
+      named_sync(1, 32 * C::WARPS);
+#pragma unroll
+      for (int hh = 0; hh < 2; ++hh) {
+        float mm = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < C::WARPS; ++w) mm = fmaxf(mm, ml[w * R + g + 8 * hh]);
+        const float f = ex2(m[hh] - mm);
+        if (l[hh] == 0.f) {           // nothing seen: all zeros, also where V was not finite
+#pragma unroll
+          for (int x = 0; x < D / 8; ++x) acc[x][2 * hh] = acc[x][2 * hh + 1] = 0.f;
+        } else {
+#pragma unroll
+          for (int x = 0; x < D / 8; ++x) {
+            acc[x][2 * hh] *= f;
+            acc[x][2 * hh + 1] *= f;
+          }
+        }
+      }
+      auto cell = [&](int w, int x, int hh) {
+        return reinterpret_cast<float2*>(merge + (w * R + g + 8 * hh) * C::PITCH + x * 8 + 2 * tq);
+      };
+      if (warp >= 4)
+#pragma unroll
+        for (int x = 0; x < D / 8; ++x)
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh)
+            *cell(warp - 4, x, hh) = make_float2(acc[x][2 * hh], acc[x][2 * hh + 1]);
+      named_sync(1, 32 * C::WARPS);
+      if (warp < 4)
+#pragma unroll
+        for (int x = 0; x < D / 8; ++x)
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {
+            float2 y = *cell(warp, x, hh);
+            y.x += acc[x][2 * hh];
+            y.y += acc[x][2 * hh + 1];
+            *cell(warp, x, hh) = y;
+          }
+      named_sync(1, 32 * C::WARPS);
+      {
+        // 16 threads a row, D / 16 columns each
+        constexpr int CPT = D / 16;
+        const int r = tid >> 4, c0 = (tid & 15) * CPT;
+        float mm = -INFINITY, ll = 0.f;
+#pragma unroll
+        for (int w = 0; w < C::WARPS; ++w) mm = fmaxf(mm, ml[w * R + r]);
+#pragma unroll
+        for (int w = 0; w < C::WARPS; ++w) {
+          const float lw = ml[(C::WARPS + w) * R + r];   // 0: that warp's keys were not seen
+          if (lw != 0.f) ll += lw * ex2(ml[w * R + r] - mm);
+        }
+        float v[CPT];
+#pragma unroll
+        for (int c = 0; c < CPT; ++c)
+          v[c] = (merge[r * C::PITCH + c0 + c] + merge[(R + r) * C::PITCH + c0 + c]) +
+                 (merge[(2 * R + r) * C::PITCH + c0 + c] + merge[(3 * R + r) * C::PITCH + c0 + c]);
+        uint32_t any = 0;
+#pragma unroll
+        for (int x = 0; x < 8; ++x) any |= nf[x];
+        if (any && r < u.rows)
+#pragma unroll
+          for (int c = 0; c < CPT; ++c) v[c] = fix_value(P, u, nf, seen + r * 8, c0 + c, v[c]);
+        if (r < u.rows) {
+          if (u.whole()) {
+            const int rr = u.row_first + r, node = rr / P.G, h = u.hk * P.G + rr - node * P.G;
+            const float inv = ll > 0.f ? 1.f / ll : 0.f;
+            if (ll == 0.f)
+#pragma unroll
+              for (int c = 0; c < CPT; ++c) v[c] = 0.f;
+            uint32_t w[CPT / 2];
+#pragma unroll
+            for (int c = 0; c < CPT / 2; ++c) w[c] = pack_bf16(v[2 * c] * inv, v[2 * c + 1] * inv);
+            __nv_bfloat16* dst = P.o + (u.s.row0 + node) * P.o_stride[0] + h * P.o_stride[1] + c0;
+            if constexpr (CPT == 8)
+              *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+            else
+              *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+            if (c0 == 0)
+              P.lse[static_cast<int64_t>(h) * P.total + u.s.row0 + node] =
+                  ll > 0.f || ll != ll ? (mm + __log2f(ll)) * 0.69314718055994530942f : -INFINITY;
+          } else {
+            const int slot = 2 * blockIdx.x + (u.t0 == 0 ? 1 : 0);
+            const int64_t at = static_cast<int64_t>(slot) * R + r;
+            float4* dst = reinterpret_cast<float4*>(P.part_o + at * D + c0);
+#pragma unroll
+            for (int c = 0; c < CPT / 4; ++c)
+              dst[c] = make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+            if (c0 == 0) P.part_ml[at] = make_float2(mm, ll);
+          }
+        }
+      }
+      if (!u.whole()) {
+        if (u.t0 == 0) rec = make_int4(u.b, u.hk, u.rt, rec.w);
+        else rec.w = u.t1 == u.tiles ? 1 : 2;
+      }
+      named_sync(1, 32 * C::WARPS);     // ml, merge, seen and nf have been read
+    }
+    if (tid == 0) P.rec[blockIdx.x] = rec;
+  }
+  __syncthreads();
+}
+
+// ---------------------------------------------------------------- join
+// A unit that block c starts and does not finish has parts in slot 2 c + 1
+// and in slot 2 x of the blocks x after it up to the one that finishes it
+// (rec.w == 1).  One warp a row: the maximum of the parts' maxima, then their
+// sums and O weighted by 2^(m - maximum), in ascending order.
+constexpr int kJoinThreads = 256;
+
+template <int R, int D>
+__global__ void __launch_bounds__(kJoinThreads)
+    tree_join_kernel(const __grid_constant__ TreeParams P, int blocks) {
+  grid_dependency_wait();
+  const int c = blockIdx.x;
+  const int4 rec = P.rec[c];
+  if (rec.x < 0) return;
+  const TreeSeq s = tree_seq(P, rec.x);
+  const int row_first = rec.z * R;
+  const int rows = static_cast<int>(min(static_cast<int64_t>(R), static_cast<int64_t>(s.n) * P.G - row_first));
+  int last = c + 1;
+  while (last < blocks - 1 && P.rec[last].w == 2) ++last;
+  const int lane = threadIdx.x & 31;
+  constexpr int CPT = D / 32;
+  for (int r = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5); r < rows;
+       r += gridDim.y * (kJoinThreads / 32)) {
+    auto at = [&](int x) -> int64_t {
+      return static_cast<int64_t>(x == c ? 2 * c + 1 : 2 * x) * R + r;
+    };
+    float mm = -INFINITY;
+    for (int x = c + lane; x <= last; x += 32) mm = fmaxf(mm, P.part_ml[at(x)].x);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
+    float ll = 0.f, v[CPT];
+#pragma unroll
+    for (int i = 0; i < CPT; ++i) v[i] = 0.f;
+#pragma unroll 4
+    for (int x = c; x <= last; ++x) {
+      const float2 p = P.part_ml[at(x)];
+      const float f = ex2(p.x - mm);
+      const float* src = P.part_o + at(x) * D + lane * CPT;
+      float y[CPT];
+      if constexpr (CPT == 4) {
+        const float4 z = *reinterpret_cast<const float4*>(src);
+        y[0] = z.x; y[1] = z.y; y[2] = z.z; y[3] = z.w;
+      } else {
+        const float2 z = *reinterpret_cast<const float2*>(src);
+        y[0] = z.x; y[1] = z.y;
+      }
+      if (p.y != 0.f) {                  // 0: the part's keys were not seen
+        ll += p.y * f;
+#pragma unroll
+        for (int i = 0; i < CPT; ++i) v[i] += y[i] * f;
+      }
+    }
+    const int rr = row_first + r, node = rr / P.G, h = rec.y * P.G + rr - node * P.G;
+    const float inv = ll > 0.f ? 1.f / ll : 0.f;
+    uint32_t w[CPT / 2];
+#pragma unroll
+    for (int i = 0; i < CPT / 2; ++i)
+      w[i] = ll == 0.f ? 0u : pack_bf16(v[2 * i] * inv, v[2 * i + 1] * inv);
+    __nv_bfloat16* dst = P.o + (s.row0 + node) * P.o_stride[0] + h * P.o_stride[1] + lane * CPT;
+    if constexpr (CPT == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+    else *reinterpret_cast<uint32_t*>(dst) = w[0];
+    if (lane == 0)
+      P.lse[static_cast<int64_t>(h) * P.total + s.row0 + node] =
+          ll > 0.f || ll != ll ? (mm + __log2f(ll)) * 0.69314718055994530942f : -INFINITY;
+  }
+}
+
+template <int R, int D>
+static fm_status launch_join(const TreeParams& P, int grid, int max_rows, cudaStream_t s) {
+  if (grid < 2) return FM_OK;
+  const int rows = max_rows < R ? max_rows : R;
+  prof_begin(K_TREE_JOIN, s);
+  const cudaError_t e = launch_dependent(tree_join_kernel<R, D>,
+                                         dim3(grid - 1, ceil_div(rows, kJoinThreads / 32)),
+                                         kJoinThreads, 0, s, P, grid);
+  prof_end(K_TREE_JOIN, s);
+  return e == cudaSuccess ? FM_OK : FM_ERR_CUDA;
+}
+
+template <int D>
+static fm_status launch_narrow_d(TreeParams& P, int max_rows, const CUtensorMap& tk,
+                                 const CUtensorMap& tv, int grid, cudaStream_t s) {
+  using C = NarrowCfg<D>;
+  auto kern = tree_narrow_kernel<D>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
+    return FM_ERR_CUDA;
+  prof_begin(K_TREE, s);
+  kern<<<grid, C::THREADS, C::SMEM, s>>>(P, tk, tv);
+  prof_end(K_TREE, s);
+  if (cudaGetLastError() != cudaSuccess) return FM_ERR_CUDA;
+  return launch_join<C::R, D>(P, grid, max_rows, s);
+}
+
+fm_status launch_tree_narrow(TreeParams& P, int d, int max_rows, const CUtensorMap& tk,
+                             const CUtensorMap& tv, int grid, cudaStream_t s) {
+  return d == 64 ? launch_narrow_d<64>(P, max_rows, tk, tv, grid, s)
+                 : launch_narrow_d<128>(P, max_rows, tk, tv, grid, s);
+}
+
+namespace {
+
+fm_status check_tree(const fm_cache* c, const fm_tree_desc* t) {
+  fm_status st = check_cache(c, true);
+  if (st != FM_OK) return st;
+  if (!t || t->H < 1 || t->H % c->Hkv != 0 || t->total < 1 || t->max_nodes < 1) return FM_ERR_INVALID;
+  if (static_cast<int64_t>(t->total) * t->H > kMaxTokenIndex) return FM_ERR_UNSUPPORTED;
+  for (const int64_t* s : {t->q_stride, t->o_stride})
+    for (int i = 0; i < 2; ++i)
+      if (s[i] <= 0 || s[i] % 8 != 0 || s[i] >= (int64_t(1) << 36)) return FM_ERR_INVALID;
+  return FM_OK;
+}
+
+// Workspace: the blocks' records, then their parts (up to two units' rows each).
+constexpr int kMaxUnitRows = 16;
+struct TreeWs {
+  size_t rec, ml, o, bytes;
+};
+TreeWs tree_ws(int grid, int d) {
+  auto up = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
+  TreeWs W;
+  W.rec = 0;
+  W.ml = up(static_cast<size_t>(grid) * sizeof(int4));
+  W.o = W.ml + up(2ull * grid * kMaxUnitRows * sizeof(float2));
+  W.bytes = W.o + 2ull * grid * kMaxUnitRows * d * sizeof(float);
+  return W;
+}
+
+}  // namespace
+}  // namespace fm
+
+using namespace fm;
+
+extern "C" {
+
+size_t fm_tree_workspace_size(const fm_cache* c, const fm_tree_desc* t) {
+  if (check_tree(c, t) != FM_OK) return 0;
+  return tree_ws(num_sms(), c->d).bytes;
+}
+
+fm_status fm_tree_fwd(const fm_cache* c, const fm_tree_desc* t, const void* q, const void* k_pool,
+                      const void* v_pool, const int32_t* table, const int32_t* lens,
+                      const int32_t* cu, const int32_t* parents, float scale, void* o, float* lse,
+                      void* ws, size_t ws_bytes, int32_t* status, void* stream) {
+  fm_status st = check_tree(c, t);
+  if (st != FM_OK) return st;
+  if (parents && t->max_nodes > FM_TREE_MAX_NODES) return FM_ERR_UNSUPPORTED;
+  if (!aligned_to(q, 16) || !aligned_to(k_pool, 16) || !aligned_to(v_pool, 16) || !aligned_to(o, 16))
+    return FM_ERR_INVALID;
+  if (!table || !lens || !cu || !lse) return FM_ERR_INVALID;
+  // masked scores are -inf and the largest score is the largest product
+  if (!(scale > 0.f && scale < INFINITY)) return FM_ERR_INVALID;
+  const int grid = num_sms();
+  const TreeWs W = tree_ws(grid, c->d);
+  if (!aligned_to(ws, 256) || ws_bytes < W.bytes) return FM_ERR_WORKSPACE;
+  char* w = static_cast<char*>(ws);
+  TreeParams P{};
+  P.B = c->B; P.H = t->H; P.Hkv = c->Hkv; P.G = t->H / c->Hkv;
+  P.total = t->total; P.max_nodes = t->max_nodes;
+  P.page_size = c->page_size; P.n_pages = c->n_pages; P.max_pages = c->max_pages;
+  P.tree = parents != nullptr;
+  P.scale_log2 = scale * 1.4426950408889634f;
+  P.q = static_cast<const __nv_bfloat16*>(q);
+  P.o = static_cast<__nv_bfloat16*>(o);
+  for (int i = 0; i < 2; ++i) {
+    P.q_stride[i] = t->q_stride[i];
+    P.o_stride[i] = t->o_stride[i];
+  }
+  P.lse = lse;
+  P.v_pool = static_cast<const __nv_bfloat16*>(v_pool);
+  for (int i = 0; i < 3; ++i) P.v_stride[i] = c->v_stride[i + 1];
+  P.table = table; P.lens = lens; P.cu = cu; P.parents = parents;
+  P.rec = reinterpret_cast<int4*>(w + W.rec);
+  P.part_ml = reinterpret_cast<float2*>(w + W.ml);
+  P.part_o = reinterpret_cast<float*>(w + W.o);
+  P.status = status;
+  const TestHooks th = test_hooks();
+  P.wait_ns = th.wait_ns;
+  P.withhold = th.withhold;
+  // one page of one head is a box: page_size rows of 64 columns
+  CUtensorMap tk, tv;
+  if (!make_tmap_bshd(&tk, k_pool, c->n_pages, c->page_size, c->Hkv, c->d, c->k_stride + 1, c->page_size) ||
+      !make_tmap_bshd(&tv, v_pool, c->n_pages, c->page_size, c->Hkv, c->d, c->v_stride + 1, c->page_size))
+    return FM_ERR_CUDA;
+  const int64_t rows = static_cast<int64_t>(t->max_nodes < t->total ? t->max_nodes : t->total) * P.G;
+  return launch_tree_narrow(P, c->d, rows < (1 << 30) ? static_cast<int>(rows) : 1 << 30, tk, tv, grid,
+                            static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

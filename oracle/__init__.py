@@ -15,7 +15,10 @@ What it computes, from the pages and the plain definitions:
 * ``oracle.attention`` - exact scaled-dot-product attention under the mask and
   its gradients, in float64, on the bf16-rounded inputs.
 
-Every function names the passage it follows.  Parity pins live in
+* ``oracle.cache`` - the paged K/V cache: attention of drafted trees over it,
+  appending, accepting, forking, reserving and compacting.
+
+Every function names the passage it follows (the cache has none there).  Parity pins live in
 ``tests/test_oracle_*.py``.
 """
-from . import masks, attention  # noqa: F401
+from . import masks, attention, cache  # noqa: F401
