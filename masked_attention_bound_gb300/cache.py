@@ -137,10 +137,11 @@ def _tree_desc(H, total, max_nodes, q_stride, o_stride) -> FmTreeDesc:
     return D
 
 
-def tree_workspace(q, k_pool, v_pool, table) -> torch.Tensor:
+def tree_workspace(q, k_pool, v_pool, table, max_nodes=None) -> torch.Tensor:
     """Scratch of ``tree_forward`` for a program that keeps its own (one per call in flight)."""
     C = make_cache(k_pool, v_pool, table)
-    D = _tree_desc(q.shape[1], max(q.shape[0], 1), 1, q.stride()[:2], q.stride()[:2])
+    total = max(q.shape[0], 1)
+    D = _tree_desc(q.shape[1], total, max_nodes or total, q.stride()[:2], q.stride()[:2])
     with _on(q, None):
         n = lib().fm_tree_workspace_size(ctypes.byref(C), ctypes.byref(D))
     if n == 0:
@@ -168,7 +169,7 @@ def tree_forward(q, k_pool, v_pool, table, lens, cu, scale, parents=None, max_no
         if lse is None:
             lse = torch.empty(H, total, dtype=torch.float32, device=dev)
         if ws is None:
-            ws = tree_workspace(q, k_pool, v_pool, table)
+            ws = tree_workspace(q, k_pool, v_pool, table, max_nodes)
     _bf16("tree_forward", k_pool, q=q, o=o)
     if o.shape != q.shape or lse.shape != (H, total) or lse.dtype is not torch.float32 \
             or not lse.is_contiguous() or lse.device != dev:

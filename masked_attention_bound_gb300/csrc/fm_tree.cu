@@ -18,7 +18,7 @@ namespace fm {
 // 16 rows fill its M, where a tcgen05.mma would pad them to 128.
 template <int D>
 struct NarrowCfg {
-  static constexpr int R = 16;
+  static constexpr int R = kNarrowRows;
   static constexpr int WARPS = 8;                  // consumers
   static constexpr int THREADS = 32 * (WARPS + 1);
   static constexpr int TILE = kTile * D * 2;       // bytes of a K or V tile
@@ -413,7 +413,7 @@ __global__ void __launch_bounds__(NarrowCfg<D>::THREADS, 1)
                   ll > 0.f || ll != ll ? (mm + __log2f(ll)) * 0.69314718055994530942f : -INFINITY;
           } else {
             const int slot = 2 * blockIdx.x + (u.t0 == 0 ? 1 : 0);
-            const int64_t at = static_cast<int64_t>(slot) * R + r;
+            const int64_t at = static_cast<int64_t>(slot) * P.part_rows + r;
             float4* dst = reinterpret_cast<float4*>(P.part_o + at * D + c0);
 #pragma unroll
             for (int c = 0; c < CPT / 4; ++c)
@@ -457,7 +457,7 @@ __global__ void __launch_bounds__(kJoinThreads)
   for (int r = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5); r < rows;
        r += gridDim.y * (kJoinThreads / 32)) {
     auto at = [&](int x) -> int64_t {
-      return static_cast<int64_t>(x == c ? 2 * c + 1 : 2 * x) * R + r;
+      return static_cast<int64_t>(x == c ? 2 * c + 1 : 2 * x) * P.part_rows + r;
     };
     float mm = -INFINITY;
     for (int x = c + lane; x <= last; x += 32) mm = fmaxf(mm, P.part_ml[at(x)].x);
@@ -501,20 +501,19 @@ __global__ void __launch_bounds__(kJoinThreads)
 }
 
 template <int R, int D>
-static fm_status launch_join(const TreeParams& P, int grid, int max_rows, cudaStream_t s) {
+static fm_status launch_join(const TreeParams& P, int grid, cudaStream_t s) {
   if (grid < 2) return FM_OK;
-  const int rows = max_rows < R ? max_rows : R;
   prof_begin(K_TREE_JOIN, s);
-  const cudaError_t e = launch_dependent(tree_join_kernel<R, D>,
-                                         dim3(grid - 1, ceil_div(rows, kJoinThreads / 32)),
-                                         kJoinThreads, 0, s, P, grid);
+  const cudaError_t e = launch_dependent(
+      tree_join_kernel<R, D>, dim3(grid - 1, ceil_div(P.part_rows, kJoinThreads / 32)), kJoinThreads,
+      0, s, P, grid);
   prof_end(K_TREE_JOIN, s);
   return e == cudaSuccess ? FM_OK : FM_ERR_CUDA;
 }
 
 template <int D>
-static fm_status launch_narrow_d(TreeParams& P, int max_rows, const CUtensorMap& tk,
-                                 const CUtensorMap& tv, int grid, cudaStream_t s) {
+static fm_status launch_narrow(const TreeParams& P, const CUtensorMap& tk, const CUtensorMap& tv,
+                               int grid, cudaStream_t s) {
   using C = NarrowCfg<D>;
   auto kern = tree_narrow_kernel<D>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
@@ -522,14 +521,7 @@ static fm_status launch_narrow_d(TreeParams& P, int max_rows, const CUtensorMap&
   prof_begin(K_TREE, s);
   kern<<<grid, C::THREADS, C::SMEM, s>>>(P, tk, tv);
   prof_end(K_TREE, s);
-  if (cudaGetLastError() != cudaSuccess) return FM_ERR_CUDA;
-  return launch_join<C::R, D>(P, grid, max_rows, s);
-}
-
-fm_status launch_tree_narrow(TreeParams& P, int d, int max_rows, const CUtensorMap& tk,
-                             const CUtensorMap& tv, int grid, cudaStream_t s) {
-  return d == 64 ? launch_narrow_d<64>(P, max_rows, tk, tv, grid, s)
-                 : launch_narrow_d<128>(P, max_rows, tk, tv, grid, s);
+  return cudaGetLastError() == cudaSuccess ? FM_OK : FM_ERR_CUDA;
 }
 
 namespace {
@@ -545,18 +537,21 @@ fm_status check_tree(const fm_cache* c, const fm_tree_desc* t) {
   return FM_OK;
 }
 
-// Workspace: the blocks' records, then their parts (up to two units' rows each).
-constexpr int kMaxUnitRows = 16;
+// Workspace: the blocks' records, then their parts (two each).
 struct TreeWs {
+  int rows;    // of a part: the largest unit's
   size_t rec, ml, o, bytes;
 };
-TreeWs tree_ws(int grid, int d) {
+TreeWs tree_ws(const fm_cache& c, const fm_tree_desc& t, int grid) {
   auto up = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
+  const int64_t rows =
+      static_cast<int64_t>(t.max_nodes < t.total ? t.max_nodes : t.total) * (t.H / c.Hkv);
   TreeWs W;
+  W.rows = rows <= kNarrowRows ? kNarrowRows : (rows >= kWideRows ? kWideRows : (static_cast<int>(rows) + 31) / 32 * 32);
   W.rec = 0;
   W.ml = up(static_cast<size_t>(grid) * sizeof(int4));
-  W.o = W.ml + up(2ull * grid * kMaxUnitRows * sizeof(float2));
-  W.bytes = W.o + 2ull * grid * kMaxUnitRows * d * sizeof(float);
+  W.o = W.ml + up(2ull * grid * W.rows * sizeof(float2));
+  W.bytes = W.o + 2ull * grid * W.rows * c.d * sizeof(float);
   return W;
 }
 
@@ -569,7 +564,7 @@ extern "C" {
 
 size_t fm_tree_workspace_size(const fm_cache* c, const fm_tree_desc* t) {
   if (check_tree(c, t) != FM_OK) return 0;
-  return tree_ws(num_sms(), c->d).bytes;
+  return tree_ws(*c, *t, num_sms()).bytes;
 }
 
 fm_status fm_tree_fwd(const fm_cache* c, const fm_tree_desc* t, const void* q, const void* k_pool,
@@ -585,7 +580,7 @@ fm_status fm_tree_fwd(const fm_cache* c, const fm_tree_desc* t, const void* q, c
   // masked scores are -inf and the largest score is the largest product
   if (!(scale > 0.f && scale < INFINITY)) return FM_ERR_INVALID;
   const int grid = num_sms();
-  const TreeWs W = tree_ws(grid, c->d);
+  const TreeWs W = tree_ws(*c, *t, grid);
   if (!aligned_to(ws, 256) || ws_bytes < W.bytes) return FM_ERR_WORKSPACE;
   char* w = static_cast<char*>(ws);
   TreeParams P{};
@@ -605,6 +600,7 @@ fm_status fm_tree_fwd(const fm_cache* c, const fm_tree_desc* t, const void* q, c
   for (int i = 0; i < 3; ++i) P.v_stride[i] = c->v_stride[i + 1];
   P.table = table; P.lens = lens; P.cu = cu; P.parents = parents;
   P.rec = reinterpret_cast<int4*>(w + W.rec);
+  P.part_rows = W.rows;
   P.part_ml = reinterpret_cast<float2*>(w + W.ml);
   P.part_o = reinterpret_cast<float*>(w + W.o);
   P.status = status;
@@ -616,9 +612,16 @@ fm_status fm_tree_fwd(const fm_cache* c, const fm_tree_desc* t, const void* q, c
   if (!make_tmap_bshd(&tk, k_pool, c->n_pages, c->page_size, c->Hkv, c->d, c->k_stride + 1, c->page_size) ||
       !make_tmap_bshd(&tv, v_pool, c->n_pages, c->page_size, c->Hkv, c->d, c->v_stride + 1, c->page_size))
     return FM_ERR_CUDA;
-  const int64_t rows = static_cast<int64_t>(t->max_nodes < t->total ? t->max_nodes : t->total) * P.G;
-  return launch_tree_narrow(P, c->d, rows < (1 << 30) ? static_cast<int>(rows) : 1 << 30, tk, tv, grid,
-                            static_cast<cudaStream_t>(stream));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool d64 = c->d == 64;
+  if (W.rows <= kNarrowRows) {
+    st = d64 ? launch_narrow<64>(P, tk, tv, grid, s) : launch_narrow<128>(P, tk, tv, grid, s);
+    if (st != FM_OK) return st;
+    return d64 ? launch_join<kNarrowRows, 64>(P, grid, s) : launch_join<kNarrowRows, 128>(P, grid, s);
+  }
+  st = launch_tree_wide(P, c->d, tk, tv, grid, s);
+  if (st != FM_OK) return st;
+  return d64 ? launch_join<kWideRows, 64>(P, grid, s) : launch_join<kWideRows, 128>(P, grid, s);
 }
 
 }  // extern "C"

@@ -31,8 +31,9 @@ struct TreeParams {
   int64_t v_stride[3];           // page, slot, head
   const int32_t *table, *lens, *cu, *parents;
   int4* rec;               // [grid] see Parts
-  float2* part_ml;         // [2 * grid][R] running max (base-2 exponent) and sum
-  float* part_o;           // [2 * grid][R][D]
+  int part_rows;           // rows that a part has room for
+  float2* part_ml;         // [2 * grid][part_rows] running max (base-2 exponent) and sum
+  float* part_o;           // [2 * grid][part_rows][D]
   int* status;
   uint64_t wait_ns;
   int withhold;
@@ -318,6 +319,9 @@ __device__ __forceinline__ uint32_t bf16x2_clean(uint32_t x) {
   return x;
 }
 
+// Row tiles of the two kernels.
+constexpr int kNarrowRows = 16, kWideRows = 256;
+
 // Adds to x what the keys flagged in nf (bit i: key origin + i) and seen
 // (bit i of `seen`) hold in column c, if that is not finite.
 __device__ __forceinline__ float fix_value(const TreeParams& P, const TreePiece& u,
@@ -340,8 +344,20 @@ __device__ __forceinline__ float fix_value(const TreeParams& P, const TreePiece&
   return x;
 }
 
-// The narrow kernel (up to 16 rows a unit, mma.sync) and the join.
-fm_status launch_tree_narrow(TreeParams& P, int d, int max_rows, const CUtensorMap& tk,
-                             const CUtensorMap& tv, int grid, cudaStream_t s);
+// fix_value over columns [c0, c1) of a row that has been written (bf16 or fp32).
+template <typename T>
+__device__ __noinline__ void fix_row(const TreeParams& P, const TreePiece& u, const uint32_t* nf,
+                                     const uint32_t* seen, int c0, int c1, T* row) {
+  for (int c = c0; c < c1; ++c) {
+    const float x = static_cast<float>(row[c]);
+    const float y = fix_value(P, u, nf, seen, c, x);
+    if (!(x == y)) row[c] = static_cast<T>(y);
+  }
+}
+
+// The kernel for units of up to 256 rows (fm_tree_wide.cu) and the join of
+// either kernel's parts (fm_tree.cu).
+fm_status launch_tree_wide(const TreeParams& P, int d, const CUtensorMap& tk, const CUtensorMap& tv,
+                           int grid, cudaStream_t s);
 
 }  // namespace fm

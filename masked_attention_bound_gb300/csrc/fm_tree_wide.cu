@@ -1,0 +1,573 @@
+// Attention over the paged cache for units of up to 256 rows (drafted trees,
+// causal runs, many query heads per K/V head), on the 5th-generation tensor
+// cores.
+//
+// A unit's rows fill one or two 128-row tiles of tcgen05.mma.  The block has
+// two slots, each with its own S/P and O in tensor memory, its own warpgroup
+// of softmax threads (thread = row = TMEM lane) and its own MMA thread, so
+// that one slot's softmax runs while the other's products do:
+//  - up to 128 rows: both slots hold the same rows and take the key tiles
+//    in turn; their O, maximum and sum are merged at the end of the piece.
+//    K and V are read once for all rows; such units are bound by that;
+//  - up to 256 rows: slot s holds rows [128 s, 128 s + 128) and both walk
+//    every tile, so a tile is loaded once for 256 rows; such units are bound
+//    by the softmax and the tensor pipe.
+// Twelve warps: 0-3 / 4-7 softmax of slot 0 / 1, 8 loads K, 10 loads V, 9 /
+// 11 issue the MMAs of slot 0 / 1.  The softmax warps also put Q into shared
+// memory (rows of a unit are nodes times query heads: any group size, one
+// 256-byte row per thread) and clean the V tiles that hold drafted nodes.
+// TMEM: S/P of slot s at [128 s, 128 s + 128), O at [256 + 128 s, .. + D).
+#include "fm_tree.h"
+
+namespace fm {
+
+template <int D>
+struct WideCfg {
+  static constexpr int TILE = kTile * D * 2;
+  static constexpr int SLABS = D / 64;
+  static constexpr int KSTAGES = 2, VSTAGES = 3;
+  static constexpr int OFF_Q = 0;                       // one tile per slot
+  static constexpr int OFF_K = 2 * TILE;
+  static constexpr int OFF_V = OFF_K + KSTAGES * TILE;
+  static constexpr int OFF_ML = OFF_V + VSTAGES * TILE; // float2 [slot][128]
+  static constexpr int OFF_NF = OFF_ML + 2 * 128 * 8;   // [2][8] keys with values not finite
+  static constexpr int OFF_BAR = OFF_NF + 64;
+  static constexpr int NBAR = 22;
+  static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;   // abort flag, TMEM address
+  static constexpr int OFF_SCAN = OFF_MISC + 16;
+  static constexpr int USED = OFF_SCAN + sizeof(TreeScan);
+  // one block per SM: it takes all of the tensor memory
+  static constexpr int SMEM = USED > 120 * 1024 ? USED : 120 * 1024;
+  static constexpr int THREADS = 384;
+  // register split as in the prompt forward: 2 x 128 x 216 + 128 x 72 = 384 x 168
+  static constexpr uint32_t REGS_SOFTMAX = 216, REGS_PRODUCER = 72;
+  static constexpr int MIN_LAUNCH_REGS =
+      (2 * 128 * REGS_SOFTMAX + 128 * REGS_PRODUCER + THREADS - 1) / THREADS;
+};
+
+enum {
+  W_QFULL = 0, W_SFULL = 2, W_PFULL = 4, W_PVDONE = 6, W_OEMPTY = 8, W_KFULL = 10, W_KEMPTY = 12,
+  W_VFULL = 14, W_VEMPTY = 17, W_DRAIN = 20
+};
+
+// How the two slots share a piece.
+struct WideSplit {
+  bool rows;     // slots split the rows (else the key tiles)
+  int n;         // key tiles of the piece
+  // slot s takes part at all
+  __device__ __forceinline__ bool active(int s) const {
+    return s == 0 || rows || n > 1;
+  }
+  __device__ __forceinline__ bool takes(int s, int x) const { return rows || (x & 1) == s; }
+};
+__device__ __forceinline__ WideSplit wide_split(const TreePiece& u) {
+  return WideSplit{u.rows > 128, u.keys > 0 ? u.t1 - u.t0 : 0};
+}
+
+__device__ __forceinline__ void slots_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+
+template <int D>
+__global__ void __launch_bounds__(WideCfg<D>::THREADS, 1)
+    tree_wide_kernel(const __grid_constant__ TreeParams P, const __grid_constant__ CUtensorMap tmK,
+                     const __grid_constant__ CUtensorMap tmV) {
+  using C = WideCfg<D>;
+  constexpr int R = kWideRows;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  if (smem_u32(smem) & 1023u) {
+    if (threadIdx.x == 0 && P.status) atomicOr(P.status, DEV_LAYOUT);
+    return;
+  }
+  const uint32_t sbase = smem_u32(smem);
+  auto bar = [&](int i) { return sbase + C::OFF_BAR + 8u * i; };
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC + 4);
+  uint32_t* nf_all = reinterpret_cast<uint32_t*>(smem + C::OFF_NF);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  constexpr int K_WARP = 8, MMA_WARP = 9, V_WARP = 10;   // 11: slot 1's MMAs
+
+  if (tid == 0) {
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(bar(W_QFULL + s), 4);     // one arrival per softmax warp of the slot
+      mbar_init(bar(W_SFULL + s), 1);
+      mbar_init(bar(W_PFULL + s), 4);
+      mbar_init(bar(W_PVDONE + s), 1);
+      mbar_init(bar(W_OEMPTY + s), 8);    // both slots' warps may read O of either
+    }
+    // a stage is free after two commits: one by each MMA thread, or both by
+    // the one whose slot took the tile
+    for (int i = 0; i < C::KSTAGES; ++i) {
+      mbar_init(bar(W_KFULL + i), 1);
+      mbar_init(bar(W_KEMPTY + i), 2);
+    }
+    for (int i = 0; i < C::VSTAGES; ++i) {
+      mbar_init(bar(W_VFULL + i), 1);
+      mbar_init(bar(W_VEMPTY + i), 2);
+    }
+    mbar_init(bar(W_DRAIN), 2);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (tid < 16) nf_all[tid] = 0;
+  if (warp == MMA_WARP) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  if (warp == K_WARP && lane == 0) tma_prefetch_desc(&tmK);
+  if (warp == V_WARP && lane == 0) tma_prefetch_desc(&tmV);
+  grid_launch_dependents();
+  tc_fence_before();
+  TreeWalk<R> walk;
+  walk.run = tree_run<R, C::THREADS>(P, *reinterpret_cast<TreeScan*>(smem + C::OFF_SCAN));
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = *tmem_slot;
+
+  auto wait = [&](int b, uint32_t parity) -> bool {
+    if (*abort_flag) return false;
+    if (!mbar_wait(bar(b), parity, P.status, P.wait_ns)) {
+      *abort_flag = 1;
+      return false;
+    }
+    return true;
+  };
+  auto wait_all = [&](int b, uint32_t parity) -> bool {
+    const bool ok = wait(b, parity);
+    return __all_sync(0xffffffffu, ok);
+  };
+
+  if (warp >= 8) {
+    regs_decrease<C::REGS_PRODUCER>();
+    if (warp == K_WARP || warp == V_WARP) {
+      // ---------------------------------------------------------- K / V loads
+      const bool isk = warp == K_WARP;
+      const int stages = isk ? C::KSTAGES : C::VSTAGES;
+      const int b_full = isk ? W_KFULL : W_VFULL, b_empty = isk ? W_KEMPTY : W_VEMPTY;
+      const uint32_t buf = sbase + (isk ? C::OFF_K : C::OFF_V);
+      const CUtensorMap* tm = isk ? &tmK : &tmV;
+      uint32_t st = 0, use = 0, issued = 0;    // stage, its uses so far, tiles issued
+      TreePiece u;
+      bool ok = true;
+      while (ok && walk.next(P, u)) {
+        if (u.keys == 0) continue;
+        int page = TileLoad<D>::lane_page(P, u, u.t0, lane);
+        for (int t = u.t0; t < u.t1; ++t) {
+          const int next = t + 1 < u.t1 ? TileLoad<D>::lane_page(P, u, t + 1, lane) : 0;
+          if (use > 0) ok = wait_all(b_empty + st, (use - 1) & 1);
+          if (!ok) break;
+          TileLoad<D>::issue(P, u, t, lane, page, tm, buf + st * C::TILE, bar(b_full + st));
+          ++issued;
+          if (++st == stages) {
+            st = 0;
+            ++use;
+          }
+          page = next;
+        }
+      }
+      // every issued copy has landed before the block may exit
+      if (lane == 0)
+        for (uint32_t x = issued > stages ? issued - stages : 0; x < issued; ++x)
+          mbar_wait(bar(b_full + x % stages), (x / stages) & 1, P.status, P.wait_ns);
+      __syncwarp();
+    } else if (lane == 0) {
+      // ---------------------------------------------------------- MMA issuers
+      const int s = warp == MMA_WARP ? 0 : 1;
+      constexpr uint32_t idS = idesc_bf16(128, 128, false, false);
+      constexpr uint32_t idPV = idesc_bf16(128, D, false, true);
+      const uint32_t dQ = sdesc_lo(sbase + C::OFF_Q + s * C::TILE, 16);
+      const uint32_t dK0 = sdesc_lo(sbase + C::OFF_K, 16);
+      const uint32_t dV0 = sdesc_lo(sbase + C::OFF_V, kTile * 128);
+      const uint32_t tS = tbase + 128 * s, tO = tbase + 256 + 128 * s;
+      uint32_t e0 = 0;          // tiles before this piece
+      uint32_t pieces = 0;      // pieces with keys before this one
+      uint32_t qn = 0, np = 0;  // Q tiles, P tiles of this slot so far
+      bool ok = true;
+      TreePiece u;
+      while (ok && walk.next(P, u)) {
+        const WideSplit w = wide_split(u);
+        if (w.n == 0) continue;
+        if (!w.active(s)) {
+          // a single key tile, which slot 0 takes and releases
+          e0 += w.n;
+          ++pieces;
+          continue;
+        }
+        auto issue_s = [&](uint32_t e) -> bool {
+          const uint32_t st = e % C::KSTAGES;
+          if (!wait(W_KFULL + st, (e / C::KSTAGES) & 1)) return false;
+          tc_fence_after();
+          const uint32_t dK = dK0 + st * (C::TILE >> 4);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = (kk >> 2) * (kTile * 128) + (kk & 3) * 32;
+            mma_ss(tS, sdesc_at(dQ, off), sdesc_at(dK, off), idS, kk > 0 ? 1u : 0u);
+          }
+          mma_commit(bar(W_SFULL + s));
+          mma_commit(bar(W_KEMPTY + st));
+          if (!w.rows) mma_commit(bar(W_KEMPTY + st));
+          return true;
+        };
+        auto issue_pv = [&](uint32_t e, bool first, bool last) -> bool {
+          if (!wait(W_PFULL + s, np & 1)) return false;
+          ++np;
+          // O of the slot is overwritten: the last piece's must have been read
+          if (first && pieces > 0 && !wait(W_OEMPTY + s, (pieces - 1) & 1)) return false;
+          const uint32_t st = e % C::VSTAGES;
+          if (!wait(W_VFULL + st, (e / C::VSTAGES) & 1)) return false;
+          tc_fence_after();
+          const uint32_t dV = dV0 + st * (C::TILE >> 4);
+#pragma unroll
+          for (int kk = 0; kk < kTile / 16; ++kk)
+            mma_ts(tO, tS + kk * 8, sdesc_at(dV, kk * 2048), idPV, (!first || kk > 0) ? 1u : 0u);
+          if (last) mma_commit(bar(W_PVDONE + s));
+          mma_commit(bar(W_VEMPTY + st));
+          if (!w.rows) mma_commit(bar(W_VEMPTY + st));
+          return true;
+        };
+        ok = wait(W_QFULL + s, qn & 1);
+        ++qn;
+        // S of the slot's next tile overwrites P of the last one: MMAs run in
+        // the order in which this thread issues them
+        const int step = w.rows ? 1 : 2, x0 = w.rows ? 0 : s;
+        if (ok) ok = issue_s(e0 + x0);
+        for (int x = x0; ok && x < w.n; x += step) {
+          ok = issue_pv(e0 + x, x == x0, x + step >= w.n);
+          if (ok && x + step < w.n) ok = issue_s(e0 + x + step);
+        }
+        e0 += w.n;
+        ++pieces;
+      }
+      mma_commit(bar(W_DRAIN));
+      mbar_wait(bar(W_DRAIN), 0, P.status, P.wait_ns);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ softmax
+    regs_increase<C::REGS_SOFTMAX>();
+    const int slot = warp >> 2, quarter = warp & 3;
+    const int r = quarter * 32 + lane;                 // row within the slot = TMEM lane
+    const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t tS = tbase + lane_off + 128 * slot;
+    const uint32_t tO = tbase + lane_off + 256 + 128 * slot;
+    float2* ml = reinterpret_cast<float2*>(smem + C::OFF_ML);
+    // A warp whose wait gave up goes on without waiting or touching tensor
+    // memory: the slots' barriers of every piece still find all eight warps.
+    bool ok = true;
+    uint32_t e0 = 0, pieces = 0, j = 0;                // j: tiles of this slot so far
+    uint32_t pd0 = 0, pd1 = 0;                         // pieces in which slot 0 / 1 took part
+    int4 rec = make_int4(-1, 0, 0, 0);
+    TreePiece u;
+    while (walk.next(P, u)) {
+      const WideSplit w = wide_split(u);
+      const int ur = w.rows ? slot * 128 + r : r;      // row of the unit
+      const bool mine = ur < u.rows && (w.rows || slot == 0 || w.n > 0);
+      const int rr = u.row_first + ur;
+      const int node = ur < u.rows ? rr / P.G : 0;
+      const int h = u.hk * P.G + (ur < u.rows ? rr - node * P.G : 0);
+      __nv_bfloat16* orow = P.o + (u.s.row0 + node) * P.o_stride[0] + h * P.o_stride[1];
+      float* lse_out = P.lse + static_cast<int64_t>(h) * P.total + u.s.row0 + node;
+      if (w.n == 0) {                                  // no keys
+        if (mine && (w.rows || slot == 0)) {
+          const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+          for (int c = 0; c < D / 8; ++c) reinterpret_cast<uint4*>(orow)[c] = z;
+          *lse_out = -INFINITY;
+        }
+        continue;
+      }
+      const bool active = w.active(slot);
+      uint32_t* nf = nf_all + 8 * (pieces & 1);
+      if (tid < 8) nf_all[8 * ((pieces + 1) & 1) + tid] = 0;   // the next piece's, read by nobody now
+      // which keys from origin on the row sees: bit i is key origin + i
+      uint32_t seen[8];
+      bool live = mine;
+      if (P.tree) {
+#pragma unroll
+        for (int x = 0; x < 8; ++x) seen[x] = 0;
+        if (mine) tree_ancestors(P, u.s, node, seen);
+        live = (seen[0] | seen[1] | seen[2] | seen[3] | seen[4] | seen[5] | seen[6] | seen[7]) != 0;
+      }
+      const bool warp_live = __any_sync(0xffffffffu, live);
+      float m_used = -INFINITY, l = 0.f;
+      if (active) {
+        // this slot's Q: S of the slot's earlier pieces has been read
+        const uint4* src = reinterpret_cast<const uint4*>(P.q + (u.s.row0 + node) * P.q_stride[0] +
+                                                          h * P.q_stride[1]);
+        uint4 x[D / 8];
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) x[c] = mine ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c)
+          st_shared_v4(sbase + C::OFF_Q + slot * C::TILE + sw128_offset(r, c * 8, 128), x[c].x, x[c].y,
+                       x[c].z, x[c].w);
+        fence_proxy_async_smem();
+        mbar_arrive_warp(bar(W_QFULL + slot));
+        const int part0 = u.origin / kTile;            // tiles from here on are not seen by all
+        int done = 0;
+        for (int x0 = w.rows ? 0 : slot; x0 < w.n; x0 += w.rows ? 1 : 2) {
+          const int t = u.t0 + x0;
+          const bool partial = t >= part0;
+          if (ok) ok = wait_all(W_SFULL + slot, j & 1);
+          tc_fence_after();
+          if (ok && warp_live) {
+            float sv[128];
+            uint32_t* raw = reinterpret_cast<uint32_t*>(sv);
+#pragma unroll
+            for (int y = 0; y < 4; ++y) tmem_ld32(tS + 32 * y, raw + 32 * y);
+            uint32_t vis[4];
+            if (partial) {
+              // the row's 128 visibility bits of this tile
+#pragma unroll
+              for (int y = 0; y < 4; ++y) {
+                const int j0 = t * kTile + 32 * y - u.origin;   // bit 0 is key origin + j0
+                if (P.tree) {
+                  // the 64 bits from word (j0 >> 5) on, ones before bit 0
+                  const int i0 = j0 >> 5;
+                  uint32_t lo = i0 < 0 ? 0xffffffffu : 0u, hi = i0 + 1 < 0 ? 0xffffffffu : 0u;
+#pragma unroll
+                  for (int i = 0; i < 8; ++i) {
+                    lo = i == i0 ? seen[i] : lo;
+                    hi = i == i0 + 1 ? seen[i] : hi;
+                  }
+                  vis[y] = __funnelshift_r(lo, hi, j0 & 31);
+                } else {
+                  const int upto = u.s.base + node - u.origin - j0;   // last visible bit
+                  vis[y] = upto >= 31 ? 0xffffffffu : (upto < 0 ? 0u : (2u << upto) - 1u);
+                }
+              }
+            }
+            tmem_wait_ld();
+            if (partial) {
+#pragma unroll
+              for (int c = 0; c < 128; ++c) sv[c] = ((vis[c >> 5] >> (c & 31)) & 1u) ? sv[c] : -INFINITY;
+            }
+            float mx8[8];
+#pragma unroll
+            for (int y = 0; y < 8; ++y) mx8[y] = fmax3(sv[y], sv[y + 8], sv[y + 16]);
+#pragma unroll
+            for (int c = 24; c < 120; c += 16)
+#pragma unroll
+              for (int y = 0; y < 8; ++y) mx8[y] = fmax3(mx8[y], sv[c + y], sv[c + 8 + y]);
+#pragma unroll
+            for (int y = 0; y < 8; ++y) mx8[y] = fmaxf(mx8[y], sv[120 + y]);
+            const float mx = fmax3(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(mx8[3], mx8[4], mx8[5]),
+                                   fmaxf(mx8[6], mx8[7]));
+            // the reference moves only when the maximum grows by more than
+            // 2^8 (as in the prompt forward): few tiles rescale O
+            const float m_tile = mx * P.scale_log2;
+            const bool grow = m_tile > m_used + 8.f;
+            const float m_new = grow ? m_tile : m_used;
+            const float alpha = grow ? ex2(m_used - m_new) : 1.f;
+            l *= alpha;
+            m_used = m_new;
+            const float m_ref = m_used == -INFINITY ? 0.f : m_used;
+            const uint64_t sc2 = splat2(P.scale_log2), nm2 = splat2(-m_ref);
+            float sum4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int c4 = 0; c4 < 4; ++c4) {
+              uint32_t pk[16];
+#pragma unroll
+              for (int y = 0; y < 16; ++y) {
+                float a0, a1;
+                fma2_bc(a0, a1, sv[c4 * 32 + 2 * y], sv[c4 * 32 + 2 * y + 1], sc2, nm2);
+                const float p0 = ex2(a0), p1 = ex2(a1);
+                if (y & 1) add2_acc(sum4[2], sum4[3], p0, p1);
+                else add2_acc(sum4[0], sum4[1], p0, p1);
+                pk[y] = pack_bf16(p0, p1);   // P in bf16 for the product; the sum keeps 32 bits
+              }
+              tmem_st16(tS + c4 * 16, pk);
+            }
+            if (done > 0 && __any_sync(0xffffffffu, grow)) {
+              uint32_t ro[D];
+#pragma unroll
+              for (int y = 0; y < D / 32; ++y) tmem_ld32(tO + 32 * y, ro + 32 * y);
+              tmem_wait_ld();
+#pragma unroll
+              for (int y = 0; y < D; ++y) ro[y] = __float_as_uint(__uint_as_float(ro[y]) * alpha);
+#pragma unroll
+              for (int y = 0; y < D / 32; ++y) tmem_st32(tO + 32 * y, ro + 32 * y);
+            }
+            l += (sum4[0] + sum4[1]) + (sum4[2] + sum4[3]);
+            tmem_wait_st();
+          }
+          if (partial && ok) {
+            // clean row r of the V tile (see fix_value) before the product
+            const uint32_t e = e0 + x0, st = e % C::VSTAGES;
+            ok = wait_all(W_VFULL + st, (e / C::VSTAGES) & 1);
+            if (ok) {
+              const int key = t * kTile + r, i = key - u.origin;
+              uint8_t* v = smem + C::OFF_V + st * C::TILE + r * 128;
+              bool dirty = false;
+              if (key >= u.keys) {
+#pragma unroll
+                for (int c = 0; c < D / 8; ++c)
+                  *reinterpret_cast<uint4*>(v + (c >> 3) * (kTile * 128) + (c & 7) * 16) =
+                      make_uint4(0u, 0u, 0u, 0u);
+              } else if (i >= 0) {
+#pragma unroll
+                for (int c = 0; c < D / 8; ++c) {
+                  const uint4 y = *reinterpret_cast<uint4*>(v + (c >> 3) * (kTile * 128) + (c & 7) * 16);
+                  dirty |= bf16x2_not_finite(y.x) || bf16x2_not_finite(y.y) || bf16x2_not_finite(y.z) ||
+                           bf16x2_not_finite(y.w);
+                }
+              }
+              if (dirty) {
+                // the flag first: whoever finds the row clean finds the flag
+                atomicOr(nf + (i >> 5), 1u << (i & 31));
+                __threadfence_block();
+                for (int c = 0; c < D / 8; ++c) {
+                  uint4* y = reinterpret_cast<uint4*>(v + (c >> 3) * (kTile * 128) + (c & 7) * 16);
+                  *y = make_uint4(bf16x2_clean(y->x), bf16x2_clean(y->y), bf16x2_clean(y->z),
+                                  bf16x2_clean(y->w));
+                }
+              }
+              fence_proxy_async_smem();
+            }
+          }
+          tc_fence_before();
+          mbar_arrive_warp(bar(W_PFULL + slot));
+          ++j;
+          ++done;
+        }
+      }
+      if (!live) {                // a padding node's row sees nothing, the context included
+        m_used = -INFINITY;
+        l = 0.f;
+      }
+
+      // ---------------------------------------------------------- the piece's end
+      const bool two = !w.rows && w.n > 1;             // O is in both slots
+      int c0 = 0, c1 = D;                              // columns that this thread writes
+      float m_out = m_used, l_out = l, f0 = 1.f, f1 = 0.f;
+      if (!w.rows) {
+        ml[slot * 128 + r] = make_float2(m_used, l);
+        slots_sync();
+        const float2 a = ml[r], b = two ? ml[128 + r] : make_float2(-INFINITY, 0.f);
+        m_out = fmaxf(a.x, b.x);
+        f0 = a.y != 0.f ? ex2(a.x - m_out) : 0.f;
+        f1 = b.y != 0.f ? ex2(b.x - m_out) : 0.f;
+        l_out = (a.y != 0.f ? a.y * f0 : 0.f) + (b.y != 0.f ? b.y * f1 : 0.f);
+        c0 = slot * (D / 2);
+        c1 = c0 + D / 2;
+      }
+      if (ok && (!w.rows || slot == 0)) ok = wait_all(W_PVDONE, pd0 & 1);
+      if (ok && (w.rows ? slot == 1 : two)) ok = wait_all(W_PVDONE + 1, pd1 & 1);
+      pd0 += w.active(0);
+      pd1 += w.active(1);
+      tc_fence_after();
+      const bool whole = u.whole();
+      const bool writes = mine && ok;
+      const float inv = whole ? (l_out > 0.f ? 1.f / l_out : (l_out == 0.f ? 0.f : l_out)) : 1.f;
+      const int slot_part = 2 * blockIdx.x + (u.t0 == 0 ? 1 : 0);
+      const int64_t at = static_cast<int64_t>(slot_part) * P.part_rows + ur;
+      float* prow = P.part_o + at * D;
+      // 32 columns at a time
+#pragma unroll
+      for (int cb = 0; cb < D / 32; ++cb) {
+        if (cb * 32 < c0 || cb * 32 >= c1) continue;
+        float v[32];
+        uint32_t* raw = reinterpret_cast<uint32_t*>(v);
+        if (ok) {
+          tmem_ld32(w.rows ? tO + cb * 32 : tbase + lane_off + 256 + cb * 32, raw);
+          if (two) {
+            uint32_t rb[32];
+            tmem_ld32(tbase + lane_off + 384 + cb * 32, rb);
+            tmem_wait_ld();
+#pragma unroll
+            for (int y = 0; y < 32; ++y)
+              v[y] = (f0 != 0.f ? v[y] * f0 : 0.f) + (f1 != 0.f ? __uint_as_float(rb[y]) * f1 : 0.f);
+          } else {
+            tmem_wait_ld();
+          }
+        }
+        if (writes) {
+#pragma unroll
+          for (int y = 0; y < 32; ++y) v[y] = l_out == 0.f ? 0.f : v[y] * inv;
+          if (whole) {
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+              reinterpret_cast<uint4*>(orow + cb * 32)[y] =
+                  make_uint4(pack_bf16(v[8 * y], v[8 * y + 1]), pack_bf16(v[8 * y + 2], v[8 * y + 3]),
+                             pack_bf16(v[8 * y + 4], v[8 * y + 5]), pack_bf16(v[8 * y + 6], v[8 * y + 7]));
+          } else {
+#pragma unroll
+            for (int y = 0; y < 8; ++y)
+              reinterpret_cast<float4*>(prow + cb * 32)[y] =
+                  make_float4(v[4 * y], v[4 * y + 1], v[4 * y + 2], v[4 * y + 3]);
+          }
+        }
+      }
+      tc_fence_before();
+      if (w.rows) {
+        // two arrivals for each of this slot's warps
+        __syncwarp();
+        if (lane == 0) mbar_arrive_count(bar(W_OEMPTY + slot), 2);
+      } else {
+        mbar_arrive_warp(bar(W_OEMPTY));
+        mbar_arrive_warp(bar(W_OEMPTY + 1));
+      }
+      if (writes) {
+        if (c0 == 0) {
+          if (whole) {
+            const float m_ref = m_out == -INFINITY ? 0.f : m_out;
+            *lse_out = l_out == 0.f ? -INFINITY : (m_ref + __log2f(l_out)) * 0.69314718055994530942f;
+          } else {
+            P.part_ml[at] = make_float2(m_out, l_out);
+          }
+        }
+        uint32_t any = 0;
+#pragma unroll
+        for (int x = 0; x < 8; ++x) any |= nf[x];
+        if (any) {
+          uint32_t see[8];
+#pragma unroll
+          for (int x = 0; x < 8; ++x) {
+            const int upto = u.s.base + node - u.origin - 32 * x;
+            see[x] = P.tree ? seen[x]
+                            : (upto >= 31 ? 0xffffffffu : (upto < 0 ? 0u : (2u << upto) - 1u));
+          }
+          if (whole) fix_row(P, u, nf, see, c0, c1, orow);
+          else fix_row(P, u, nf, see, c0, c1, prow);
+        }
+      }
+      if (!whole) {
+        if (u.t0 == 0) rec = make_int4(u.b, u.hk, u.rt, rec.w);
+        else rec.w = u.t1 == u.tiles ? 1 : 2;
+      }
+      e0 += w.n;
+      ++pieces;
+      slots_sync();               // ml and nf have been read, and S of both slots
+    }
+    if (tid == 0) P.rec[blockIdx.x] = rec;
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == MMA_WARP) {
+    tc_fence_after();
+    tmem_dealloc(tbase, 512);
+  }
+}
+
+template <int D>
+static fm_status launch_wide_d(const TreeParams& P, const CUtensorMap& tk, const CUtensorMap& tv,
+                               int grid, cudaStream_t s) {
+  using C = WideCfg<D>;
+  auto kern = tree_wide_kernel<D>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
+    return FM_ERR_CUDA;
+  // the setmaxnreg split must fit in the registers the block launches with
+  cudaFuncAttributes fa;
+  if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess) return FM_ERR_CUDA;
+  if (fa.numRegs < C::MIN_LAUNCH_REGS) return FM_ERR_UNSUPPORTED;
+  prof_begin(K_TREE, s);
+  kern<<<grid, C::THREADS, C::SMEM, s>>>(P, tk, tv);
+  prof_end(K_TREE, s);
+  return cudaGetLastError() == cudaSuccess ? FM_OK : FM_ERR_CUDA;
+}
+
+fm_status launch_tree_wide(const TreeParams& P, int d, const CUtensorMap& tk, const CUtensorMap& tv,
+                           int grid, cudaStream_t s) {
+  return d == 64 ? launch_wide_d<64>(P, tk, tv, grid, s) : launch_wide_d<128>(P, tk, tv, grid, s);
+}
+
+}  // namespace fm

@@ -238,7 +238,7 @@ def test_equal_inputs_give_equal_bits(nodes):
 @pytest.mark.parametrize("nodes", [1, 24])
 def test_captured_and_replayed_with_growing_lengths(nodes):
     b = Batch(16, [600, 333], [nodes] * 2, 8, 2, 128, 16)
-    ws = fm.tree_workspace(b.q, b.k, b.v, b.table)
+    ws = fm.tree_workspace(b.q, b.k, b.v, b.table, nodes)
     ws.fill_(255)
     o, lse = torch.empty_like(b.q), torch.empty(8, b.q.shape[0], device="cuda")
     lens = b.lens_t.clone()
