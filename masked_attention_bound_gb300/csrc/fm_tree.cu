@@ -10,8 +10,8 @@ namespace fm {
 // ---------------------------------------------------------------- narrow kernel
 // Units of up to 16 rows (one token of up to 16 query heads per K/V head, or
 // a few nodes).  Bound by reading K and V once: 512 bytes per key and head at
-// d = 128 against 8 KFLOP.  A warp loads K and V tiles by TMA through a ring
-// of tiles; eight warps each take 16 keys of every 128-key tile and keep
+// d = 128 against 8 KFLOP.  Two warps load K and V tiles by TMA through
+// rings of tiles; eight warps each take 16 keys of every 128-key tile and keep
 // their own running maximum, sum and O in registers, so no warp waits for
 // another inside a unit.  S and O come from mma.sync (16 x 8 x 16, bf16): its
 // fragments leave P in registers as the A operand of the second product, and
@@ -20,17 +20,18 @@ template <int D>
 struct NarrowCfg {
   static constexpr int R = kNarrowRows;
   static constexpr int WARPS = 8;                  // consumers
-  static constexpr int THREADS = 32 * (WARPS + 1);
+  static constexpr int THREADS = 32 * (WARPS + 2);
   static constexpr int TILE = kTile * D * 2;       // bytes of a K or V tile
-  static constexpr int SLOTS = D == 128 ? 5 : 10;  // ring of tiles: K0 V0 K1 V1 ...
+  static constexpr int KS = D == 128 ? 3 : 5, VS = D == 128 ? 2 : 5;   // rings of tiles
   static constexpr int PITCH = D + 8;              // floats of a row of the merge buffer
-  static constexpr int OFF_MERGE = SLOTS * TILE;
+  static constexpr int OFF_V = KS * TILE;
+  static constexpr int OFF_MERGE = OFF_V + VS * TILE;
   static constexpr int OFF_ML = OFF_MERGE + 4 * R * PITCH * 4;   // [WARPS][R] max, then sum
   static constexpr int OFF_SEEN = OFF_ML + 2 * WARPS * R * 4;    // [R][8] ancestors
   static constexpr int OFF_NF = OFF_SEEN + R * 8 * 4;            // [8] keys with values not finite
   static constexpr int OFF_BAR = OFF_NF + 32;
-  static constexpr int OFF_SCAN = OFF_BAR + (2 * SLOTS + 1) * 8;  // after the barriers: abort flag
-  static constexpr int SMEM = OFF_SCAN + sizeof(TreeScan);
+  static constexpr int OFF_ABORT = OFF_BAR + 2 * (KS + VS) * 8;
+  static constexpr int SMEM = OFF_ABORT + 8;
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
@@ -64,19 +65,19 @@ __global__ void __launch_bounds__(NarrowCfg<D>::THREADS, 1)
   using C = NarrowCfg<D>;
   constexpr int R = C::R;
   extern __shared__ __align__(1024) uint8_t smem[];
-  TreeScan& scan = *reinterpret_cast<TreeScan*>(smem + C::OFF_SCAN);
-  volatile int& abort_flag = *reinterpret_cast<volatile int*>(smem + C::OFF_SCAN - 8);
+  volatile int& abort_flag = *reinterpret_cast<volatile int*>(smem + C::OFF_ABORT);
   if (smem_u32(smem) & 1023u) {
     if (threadIdx.x == 0 && P.status) atomicOr(P.status, DEV_LAYOUT);
     return;
   }
   const uint32_t sbase = smem_u32(smem);
   const uint32_t bar0 = sbase + C::OFF_BAR;
-  auto full = [&](int i) { return bar0 + 8u * i; };
-  auto empty = [&](int i) { return bar0 + 8u * (C::SLOTS + i); };
+  auto full = [&](int i) { return bar0 + 8u * i; };                      // K stages, then V's
+  auto empty = [&](int i) { return bar0 + 8u * (C::KS + C::VS + i); };
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (warp == 2) touch_inputs(P, lane);
   if (tid == 0) {
-    for (int i = 0; i < C::SLOTS; ++i) {
+    for (int i = 0; i < C::KS + C::VS; ++i) {
       mbar_init(full(i), 1);
       mbar_init(empty(i), C::WARPS);
     }
@@ -88,52 +89,59 @@ __global__ void __launch_bounds__(NarrowCfg<D>::THREADS, 1)
     tma_prefetch_desc(&tmV);
   }
   grid_launch_dependents();
+  grid_dependency_wait();
   TreeWalk<R> walk;
-  walk.run = tree_run<R, C::THREADS>(P, scan);   // synchronises the block
+  walk.run = tree_run<R>(P);
   __syncthreads();
 
   // every lane gets the same answer
   auto wait_all = [&](uint32_t bar, uint32_t parity) -> bool {
-    bool ok = !abort_flag;
-    if (ok) ok = mbar_wait(bar, parity, P.status, P.wait_ns);
-    if (!ok) abort_flag = 1;
+    bool ok = mbar_try_wait(bar, parity);
+    if (!ok && !abort_flag) {
+      ok = mbar_wait(bar, parity, P.status, P.wait_ns);
+      if (!ok) abort_flag = 1;
+    }
     return __all_sync(0xffffffffu, ok);
   };
 
-  if (warp == C::WARPS) {
+  if (warp >= C::WARPS) {
     // ------------------------------------------------------------ loads
-    uint32_t i = 0;   // ring position: 2 e for K of the e-th tile, 2 e + 1 for V
+    // one warp for K, one for V
+    const bool isk = warp == C::WARPS;
+    const CUtensorMap* tm = isk ? &tmK : &tmV;
+    const int stages = isk ? C::KS : C::VS, first = isk ? 0 : C::KS;
+    const uint32_t buf = sbase + (isk ? 0 : C::OFF_V);
+    int st = 0, issued = 0;
+    uint32_t use = 0;
     TreePiece u;
     bool ok = true;
     while (ok && walk.next(P, u)) {
       if (u.keys == 0) continue;
       int page = TileLoad<D>::lane_page(P, u, u.t0, lane);
-      for (int t = u.t0; ok && t < u.t1; ++t) {
+      for (int t = u.t0; t < u.t1; ++t) {
         const int next = t + 1 < u.t1 ? TileLoad<D>::lane_page(P, u, t + 1, lane) : 0;
-#pragma unroll
-        for (int kv = 0; kv < 2; ++kv, ++i) {
-          const int slot = i % C::SLOTS;
-          const uint32_t use = i / C::SLOTS;
-          if (use > 0) ok = wait_all(empty(slot), (use - 1) & 1);
-          if (!ok) break;
-          TileLoad<D>::issue(P, u, t, lane, page, kv ? &tmV : &tmK, sbase + slot * C::TILE,
-                             full(slot));
+        if (use > 0) ok = wait_all(empty(first + st), (use - 1) & 1);
+        if (!ok) break;
+        TileLoad<D>::issue(P, u, t, lane, page, tm, buf + st * C::TILE, full(first + st));
+        ++issued;
+        if (++st == stages) {
+          st = 0;
+          ++use;
         }
         page = next;
       }
     }
     // every issued copy has landed before the block may exit
-    __syncwarp();
     if (lane == 0)
-      for (uint32_t x = i > C::SLOTS ? i - C::SLOTS : 0; x < i; ++x)
-        mbar_wait(full(x % C::SLOTS), (x / C::SLOTS) & 1, P.status, P.wait_ns);
+      for (int x = max(issued - stages, 0); x < issued; ++x)
+        mbar_wait(full(first + x % stages), (x / stages) & 1, P.status, P.wait_ns);
     __syncwarp();
   } else {
     // ------------------------------------------------------------ attention
     // A warp whose wait gave up goes on without waiting or computing: the
     // block-wide merges of every piece still find all eight warps.
     bool ok = true;
-    uint32_t i = 0;
+    uint32_t e = 0;                              // tiles so far
     const int g = lane >> 2, tq = lane & 3;      // fragment row and column pair
     uint32_t* seen = reinterpret_cast<uint32_t*>(smem + C::OFF_SEEN);
     uint32_t* nf = reinterpret_cast<uint32_t*>(smem + C::OFF_NF);
@@ -147,7 +155,7 @@ __global__ void __launch_bounds__(NarrowCfg<D>::THREADS, 1)
       // which keys past origin a row sees: bit j is key origin + j
       if (warp == 0) {
         uint32_t w[8];
-        const int node = (u.row_first + min(lane, u.rows - 1)) / P.G;
+        const int node = P.by_G(u.row_first + min(lane, u.rows - 1));
         if (P.tree) {
           if (lane < R && u.s.base >= 0) tree_ancestors(P, u.s, node, w);
         } else {
@@ -168,7 +176,7 @@ __global__ void __launch_bounds__(NarrowCfg<D>::THREADS, 1)
       for (int hh = 0; hh < 2; ++hh) {
         const int r = g + 8 * hh;
         const int rr = u.row_first + r;
-        const int node = rr / P.G;
+        const int node = P.by_G(rr);
         const __nv_bfloat16* src = P.q + (u.s.row0 + node) * P.q_stride[0] +
                                    (u.hk * P.G + rr - node * P.G) * P.q_stride[1] + 2 * tq;
 #pragma unroll
@@ -186,11 +194,11 @@ __global__ void __launch_bounds__(NarrowCfg<D>::THREADS, 1)
         for (int y = 0; y < 4; ++y) acc[x][y] = 0.f;
 
       for (int t = u.t0; u.keys > 0 && t < u.t1; ++t) {
-        const int ks = i % C::SLOTS, vs = (i + 1) % C::SLOTS;
-        const uint32_t kp = (i / C::SLOTS) & 1, vp = ((i + 1) / C::SLOTS) & 1;
-        i += 2;
+        const int ks = e % C::KS, vs = e % C::VS;
+        const uint32_t kp = (e / C::KS) & 1, vp = (e / C::VS) & 1;
+        ++e;
         const int k0 = t * kTile + warp * 16;          // first key of this warp
-        const uint32_t sk = sbase + ks * C::TILE, sv = sbase + vs * C::TILE;
+        const uint32_t sk = sbase + ks * C::TILE, sv = sbase + C::OFF_V + vs * C::TILE;
         const bool mine = k0 < u.keys;                 // any keys at all
         if (ok) ok = wait_all(full(ks), kp);
         float s[2][4];
@@ -267,7 +275,7 @@ __global__ void __launch_bounds__(NarrowCfg<D>::THREADS, 1)
           pf[2] = pack_bf16(p[1][0], p[1][1]);
           pf[3] = pack_bf16(p[1][2], p[1][3]);
         }
-        if (ok) ok = wait_all(full(vs), vp);
+        if (ok) ok = wait_all(full(C::KS + vs), vp);
         if (ok && mine) {
           if (t >= part0 || k0 + 16 > u.keys) {
             // this warp's 16 rows of V: zeros past the unit's keys, and clean
@@ -277,7 +285,7 @@ __global__ void __launch_bounds__(NarrowCfg<D>::THREADS, 1)
             bool dirty = false;
             for (int ch = (lane & 1) * (D / 16); ch < ((lane & 1) + 1) * (D / 16); ++ch) {
               const uint32_t at = (ch >> 3) * (kTile * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4);
-              uint4* ptr = reinterpret_cast<uint4*>(smem + vs * C::TILE + at);
+              uint4* ptr = reinterpret_cast<uint4*>(smem + C::OFF_V + vs * C::TILE + at);
               if (key >= u.keys) {
                 *ptr = make_uint4(0u, 0u, 0u, 0u);
               } else if (j >= 0) {
@@ -309,7 +317,7 @@ __global__ void __launch_bounds__(NarrowCfg<D>::THREADS, 1)
             mma16816(acc[2 * kk + 1], pf, b[2], b[3]);
           }
         }
-        mbar_arrive_warp(empty(vs));
+        mbar_arrive_warp(empty(C::KS + vs));
       }
 
       // ---------------------------------------------------------- merge the eight warps
@@ -395,7 +403,7 @@ __global__ void __launch_bounds__(NarrowCfg<D>::THREADS, 1)
           for (int c = 0; c < CPT; ++c) v[c] = fix_value(P, u, nf, seen + r * 8, c0 + c, v[c]);
         if (r < u.rows) {
           if (u.whole()) {
-            const int rr = u.row_first + r, node = rr / P.G, h = u.hk * P.G + rr - node * P.G;
+            const int rr = u.row_first + r, node = P.by_G(rr), h = u.hk * P.G + rr - node * P.G;
             const float inv = ll > 0.f ? 1.f / ll : 0.f;
             if (ll == 0.f)
 #pragma unroll
@@ -436,41 +444,65 @@ __global__ void __launch_bounds__(NarrowCfg<D>::THREADS, 1)
 // ---------------------------------------------------------------- join
 // A unit that block c starts and does not finish has parts in slot 2 c + 1
 // and in slot 2 x of the blocks x after it up to the one that finishes it
-// (rec.w == 1).  One warp a row: the maximum of the parts' maxima, then their
-// sums and O weighted by 2^(m - maximum), in ascending order.
-constexpr int kJoinThreads = 256;
+// (rec.w == 1).  For each row: the maximum of the parts' maxima, then their
+// sums and O weighted by 2^(m - maximum).  A block's eight warps share a row
+// when it has many parts (one long sequence: 76 parts of two units took 33 us
+// with a warp a row, 512 bytes of each part at a time), each warp taking every
+// eighth, else they take a row each; the order of the sums is fixed either way.
+constexpr int kJoinThreads = 256, kJoinShare = 12;
 
 template <int R, int D>
 __global__ void __launch_bounds__(kJoinThreads)
     tree_join_kernel(const __grid_constant__ TreeParams P, int blocks) {
+  constexpr int NW = kJoinThreads / 32, CPT = D / 32;
+  __shared__ float sums[NW][D + 1];
+  grid_launch_dependents();
   grid_dependency_wait();
-  const int c = blockIdx.x;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  // the unit: opened by the nearest block c at or before this one that is not
+  // in the middle of a unit, and finished by block `last`
+  int c = blockIdx.x;
+  for (int x0 = c;; x0 -= 32) {
+    const int x = x0 - lane;
+    const unsigned opens = __ballot_sync(0xffffffffu, x <= 0 || P.rec[x].w != 2);
+    if (opens) {
+      c = max(x0 - __ffs(opens) + 1, 0);
+      break;
+    }
+  }
   const int4 rec = P.rec[c];
   if (rec.x < 0) return;
-  const TreeSeq s = tree_seq(P, rec.x);
-  const int row_first = rec.z * R;
-  const int rows = static_cast<int>(min(static_cast<int64_t>(R), static_cast<int64_t>(s.n) * P.G - row_first));
   int last = c + 1;
-  while (last < blocks - 1 && P.rec[last].w == 2) ++last;
-  const int lane = threadIdx.x & 31;
-  constexpr int CPT = D / 32;
-  for (int r = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5); r < rows;
-       r += gridDim.y * (kJoinThreads / 32)) {
-    auto at = [&](int x) -> int64_t {
-      return static_cast<int64_t>(x == c ? 2 * c + 1 : 2 * x) * P.part_rows + r;
+  for (int x0 = c + 1;; x0 += 32) {
+    const int x = x0 + lane;
+    const unsigned ends = __ballot_sync(0xffffffffu, x >= blocks || P.rec[x].w != 2);
+    if (ends) {
+      last = min(x0 + __ffs(ends) - 1, blocks - 1);
+      break;
+    }
+  }
+  const TreeSeq s = tree_seq(P, rec.x);
+  const int row_first = rec.z * R, rows = min(R, s.n * P.G - row_first), parts = last - c + 1;
+  const bool share = parts > kJoinShare;
+  // the blocks in the middle of the unit (in [c, last)) take rows of it too
+  const int first = (blockIdx.x - c) * gridDim.y + blockIdx.y;
+  const int step = (last - c) * gridDim.y * (share ? 1 : NW);
+  for (int r = share ? first : first * NW + warp; r < rows; r += step) {
+    auto at = [&](int i) -> int64_t {
+      return static_cast<int64_t>(i == 0 ? 2 * c + 1 : 2 * (c + i)) * P.part_rows + r;
     };
     float mm = -INFINITY;
-    for (int x = c + lane; x <= last; x += 32) mm = fmaxf(mm, P.part_ml[at(x)].x);
+    for (int i = lane; i < parts; i += 32) mm = fmaxf(mm, P.part_ml[at(i)].x);
 #pragma unroll
     for (int o = 16; o; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
     float ll = 0.f, v[CPT];
 #pragma unroll
     for (int i = 0; i < CPT; ++i) v[i] = 0.f;
 #pragma unroll 4
-    for (int x = c; x <= last; ++x) {
-      const float2 p = P.part_ml[at(x)];
+    for (int i = share ? warp : 0; i < parts; i += share ? NW : 1) {
+      const float2 p = P.part_ml[at(i)];
       const float f = ex2(p.x - mm);
-      const float* src = P.part_o + at(x) * D + lane * CPT;
+      const float* src = P.part_o + at(i) * D + lane * CPT;
       float y[CPT];
       if constexpr (CPT == 4) {
         const float4 z = *reinterpret_cast<const float4*>(src);
@@ -482,10 +514,27 @@ __global__ void __launch_bounds__(kJoinThreads)
       if (p.y != 0.f) {                  // 0: the part's keys were not seen
         ll += p.y * f;
 #pragma unroll
-        for (int i = 0; i < CPT; ++i) v[i] += y[i] * f;
+        for (int x = 0; x < CPT; ++x) v[x] += y[x] * f;
       }
     }
-    const int rr = row_first + r, node = rr / P.G, h = rec.y * P.G + rr - node * P.G;
+    if (share) {
+      __syncthreads();                   // the row before has been read
+#pragma unroll
+      for (int x = 0; x < CPT; ++x) sums[warp][lane * CPT + x] = v[x];
+      if (lane == 0) sums[warp][D] = ll;
+      __syncthreads();
+      if (warp > 0) continue;
+      ll = 0.f;
+#pragma unroll
+      for (int x = 0; x < CPT; ++x) v[x] = 0.f;
+#pragma unroll
+      for (int w = 0; w < NW; ++w) {
+        ll += sums[w][D];
+#pragma unroll
+        for (int x = 0; x < CPT; ++x) v[x] += sums[w][lane * CPT + x];
+      }
+    }
+    const int rr = row_first + r, node = P.by_G(rr), h = rec.y * P.G + rr - node * P.G;
     const float inv = ll > 0.f ? 1.f / ll : 0.f;
     uint32_t w[CPT / 2];
 #pragma unroll
@@ -503,6 +552,7 @@ __global__ void __launch_bounds__(kJoinThreads)
 template <int R, int D>
 static fm_status launch_join(const TreeParams& P, int grid, cudaStream_t s) {
   if (grid < 2) return FM_OK;
+  // a block's warps take a row each of the largest unit in two parts
   prof_begin(K_TREE_JOIN, s);
   const cudaError_t e = launch_dependent(
       tree_join_kernel<R, D>, dim3(grid - 1, ceil_div(P.part_rows, kJoinThreads / 32)), kJoinThreads,
@@ -519,9 +569,9 @@ static fm_status launch_narrow(const TreeParams& P, const CUtensorMap& tk, const
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
     return FM_ERR_CUDA;
   prof_begin(K_TREE, s);
-  kern<<<grid, C::THREADS, C::SMEM, s>>>(P, tk, tv);
+  const cudaError_t e = launch_dependent(kern, dim3(grid), C::THREADS, C::SMEM, s, P, tk, tv);
   prof_end(K_TREE, s);
-  return cudaGetLastError() == cudaSuccess ? FM_OK : FM_ERR_CUDA;
+  return e == cudaSuccess ? FM_OK : FM_ERR_CUDA;
 }
 
 namespace {
@@ -582,11 +632,19 @@ fm_status fm_tree_fwd(const fm_cache* c, const fm_tree_desc* t, const void* q, c
   const int grid = num_sms();
   const TreeWs W = tree_ws(*c, *t, grid);
   if (!aligned_to(ws, 256) || ws_bytes < W.bytes) return FM_ERR_WORKSPACE;
+  // the tiles of all units (an upper bound) are counted in 31 bits
+  const double units = static_cast<double>(c->Hkv) *
+                       (static_cast<double>(t->total) * (t->H / c->Hkv) / kNarrowRows + c->B);
+  if (units * (static_cast<double>(c->max_pages) * c->page_size / kTile + 1) >= 2147483647.0)
+    return FM_ERR_UNSUPPORTED;
   char* w = static_cast<char*>(ws);
   TreeParams P{};
   P.B = c->B; P.H = t->H; P.Hkv = c->Hkv; P.G = t->H / c->Hkv;
   P.total = t->total; P.max_nodes = t->max_nodes;
-  P.page_size = c->page_size; P.n_pages = c->n_pages; P.max_pages = c->max_pages;
+  P.page_shift = c->page_size == 16 ? 4 : c->page_size == 32 ? 5 : c->page_size == 64 ? 6 : 7;
+  P.n_pages = c->n_pages; P.max_pages = c->max_pages;
+  P.by_G = FastDiv::of(P.G);
+  P.by_grid = FastDiv::of(grid);
   P.tree = parents != nullptr;
   P.scale_log2 = scale * 1.4426950408889634f;
   P.q = static_cast<const __nv_bfloat16*>(q);

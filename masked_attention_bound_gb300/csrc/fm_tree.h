@@ -18,19 +18,35 @@
 
 namespace fm {
 
+// Division by a number that the host knows, of values below 2^31: one high
+// product, one add and one shift in place of some forty instructions.
+struct FastDiv {
+  uint32_t d, mul, shift;
+  static FastDiv of(uint32_t d) {
+    FastDiv f{d, 0, 0};
+    while ((1ull << f.shift) < d) ++f.shift;
+    f.mul = static_cast<uint32_t>(((1ull << f.shift) - d) * (1ull << 32) / d + 1);
+    return f;
+  }
+  __device__ __forceinline__ int operator()(int n) const {
+    return static_cast<int>((__umulhi(static_cast<uint32_t>(n), mul) + static_cast<uint32_t>(n)) >> shift);
+  }
+};
+
 struct TreeParams {
-  int B, H, Hkv, G, total, max_nodes, page_size, n_pages, max_pages;
+  int B, H, Hkv, G, total, max_nodes, page_shift, n_pages, max_pages;
   int tree;                // 0: chain (no parents)
+  FastDiv by_G, by_grid;
   float scale_log2;        // scale * log2(e)
   const __nv_bfloat16* q;
   int64_t q_stride[2];
   __nv_bfloat16* o;
   int64_t o_stride[2];
   float* lse;
-  const __nv_bfloat16* v_pool;   // for values that are not finite (see fix_row)
+  const __nv_bfloat16* v_pool;   // for values that are not finite (see fix_value)
   int64_t v_stride[3];           // page, slot, head
   const int32_t *table, *lens, *cu, *parents;
-  int4* rec;               // [grid] see Parts
+  int4* rec;               // [grid] what a block leaves for the join, see below
   int part_rows;           // rows that a part has room for
   float2* part_ml;         // [2 * grid][part_rows] running max (base-2 exponent) and sum
   float* part_o;           // [2 * grid][part_rows][D]
@@ -39,11 +55,11 @@ struct TreeParams {
   int withhold;
 };
 
-// What a block leaves for the join: rec.x = the unit it starts and does not
-// finish (a part in slot 2 * block + 1), -1 if none: sequence in .x, K/V head
-// in .y, row tile in .z; rec.w = 0, or 1: its first run finishes a unit that
-// an earlier block started, 2: belongs to one and does not finish it (a part
-// in slot 2 * block).
+// What a block leaves for the join: the unit that it starts and does not
+// finish (its part is in slot 2 * block + 1): sequence in rec.x (-1: none),
+// K/V head in .y, row tile in .z; rec.w = 0, or 1: its first run finishes a
+// unit that an earlier block started, 2: belongs to one and does not finish
+// it (its part is in slot 2 * block).
 
 // Per sequence: packed rows, nodes, context length (-1: out of range).
 struct TreeSeq {
@@ -57,7 +73,7 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeParams& P, int b) {
   s.n = c1 - c0;
   s.base = len - s.n;
   if (c0 < 0 || s.n < 0 || c1 > P.total || s.n > P.max_nodes || len < s.n ||
-      len > P.max_pages * P.page_size) {
+      len > (P.max_pages << P.page_shift)) {
     // the rows that can be written get zeros
     const int lo = max(c0, 0), hi = min(c1, P.total);
     s.row0 = lo;
@@ -67,124 +83,111 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeParams& P, int b) {
   return s;
 }
 
-// Row tiles of a sequence, keys and tiles of one of them.
+// Row tiles of a sequence, keys and tiles of one of them (total * H is at
+// most 2^30: 32 bits hold every row).
 template <int R>
 __device__ __forceinline__ int row_tiles(const TreeParams& P, const TreeSeq& s) {
-  return static_cast<int>((static_cast<int64_t>(s.n) * P.G + R - 1) / R);
+  return (s.n * P.G + R - 1) / R;
 }
 template <int R>
 __device__ __forceinline__ int unit_keys(const TreeParams& P, const TreeSeq& s, int rt) {
   if (s.base < 0) return 0;
-  const int64_t rows = static_cast<int64_t>(s.n) * P.G;
-  const int64_t end = min(rows, static_cast<int64_t>(rt + 1) * R);
-  return s.base + static_cast<int>((end - 1) / P.G) + 1;
+  return s.base + P.by_G(min(s.n * P.G, (rt + 1) * R) - 1) + 1;
 }
 __device__ __forceinline__ int key_tiles(int keys) {
   return keys > 0 ? (keys + kTile - 1) / kTile : 1;
 }
-// Tiles of all units of one K/V head of a sequence.
+// Tiles of all units of one K/V head of a sequence.  (The launch checks that
+// the tiles of all units fit in 31 bits.)
 template <int R>
-__device__ __forceinline__ int64_t seq_tiles(const TreeParams& P, const TreeSeq& s) {
+__device__ __forceinline__ uint32_t seq_tiles(const TreeParams& P, const TreeSeq& s) {
   const int nr = row_tiles<R>(P, s);
-  int64_t w = 0;
+  uint32_t w = 0;
   for (int rt = 0; rt < nr; ++rt) w += key_tiles(unit_keys<R>(P, s, rt));
   return w;
 }
 
-// A place on the line of tiles.
-struct TreePlace {
-  int b, hk, rt, tile;
-};
+// The first touch of a memory page by an SM costs 2 to 3 us (address
+// translation): the small inputs are touched at once, while the block sets up
+// (lens and cu, then the table, then K and V would each wait for it in turn).
+__device__ __forceinline__ void touch_inputs(const TreeParams& P, int lane) {
+  const void* p = lane == 0 ? static_cast<const void*>(P.lens)
+                            : (lane == 1 ? static_cast<const void*>(P.cu)
+                                         : (lane == 2 ? static_cast<const void*>(P.table)
+                                                      : (lane == 3 ? static_cast<const void*>(P.q)
+                                                                   : static_cast<const void*>(P.parents))));
+  if (lane < 4 || (lane == 4 && P.tree)) asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+}
 
-// The run [begin, end) of a block and where it starts; all threads of the
-// block call it.
+// A block's run: the place of its first tile, and its tiles.
 struct TreeRun {
-  int64_t left;       // tiles of the run
-  TreePlace at;
+  int b, hk, rt, tile, left;
+  TreeSeq s;          // sequence b
 };
 
-struct TreeScan {
-  int64_t warp[32];
-  int64_t begin, end;
-  int64_t before;     // tiles before sequence b
-  int b;
-};
-
-template <int R, int NT>
-__device__ __forceinline__ TreeRun tree_run(const TreeParams& P, TreeScan& sh) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  constexpr int NW = NT / 32;
-  int64_t w_first = 0;            // this thread's sequence of the first round
-  auto weight = [&](int b) -> int64_t {
-    if (b >= P.B) return 0;
-    const TreeSeq s = tree_seq(P, b);
+// Every warp of the block finds the run by itself (no shared memory and no
+// barrier: the start of the kernel is on the path of every call).  Lane l
+// adds up the tiles of sequences [l m, l m + m), m = ceil(B / 32); one scan
+// over the lanes, and the lane whose sequences hold the run's first tile
+// looks for it among them.
+template <int R>
+__device__ __forceinline__ TreeRun tree_run(const TreeParams& P) {
+  constexpr unsigned ALL = 0xffffffffu;
+  const int lane = threadIdx.x & 31;
+  const int m = (P.B + 31) >> 5;
+  const int b0 = lane * m, b1 = min(b0 + m, P.B);
+  TreeSeq s{0, 0, 0};
+  uint32_t w = 0;
+#pragma unroll 4
+  for (int b = b0; b < b1; ++b) {
+    s = tree_seq(P, b);
     if (s.base < 0 && blockIdx.x == 0 && P.status) atomicOr(P.status, DEV_CACHE);
-    return seq_tiles<R>(P, s) * P.Hkv;
-  };
-  int64_t sum = 0;
-  for (int b = tid; b < P.B; b += NT) {
-    const int64_t w = weight(b);
-    if (b == tid) w_first = w;
-    sum += w;
+    w += seq_tiles<R>(P, s) * P.Hkv;
   }
+  uint32_t inc = w;
 #pragma unroll
-  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if (lane == 0) sh.warp[warp] = sum;
-  if (tid == 0) sh.b = -1;
-  __syncthreads();
-  int64_t all = 0;
-  for (int i = 0; i < NW; ++i) all += sh.warp[i];
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t y = __shfl_up_sync(ALL, inc, o);
+    if (lane >= o) inc += y;
+  }
+  const uint32_t all = __shfl_sync(ALL, inc, 31);
   // no more blocks than tiles: the runs of the others are empty
-  const int64_t blocks = min(all, static_cast<int64_t>(gridDim.x));
-  const bool idle = blockIdx.x >= blocks;
-  const int64_t begin = idle ? all : all * blockIdx.x / blocks;
-  const int64_t end = idle ? all : all * (blockIdx.x + 1) / blocks;
-  int64_t before = 0;
-  for (int b0 = 0; b0 < P.B; b0 += NT) {
-    __syncthreads();
-    const int b = b0 + tid;
-    const int64_t w = b0 == 0 ? w_first : weight(b);
-    int64_t inc = w;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += y;
+  TreeRun run{0, 0, 0, 0, 0, s};
+  const uint32_t me = blockIdx.x, grid = gridDim.x;
+  if (me >= all) return run;
+  const uint32_t each = all < grid ? 1 : P.by_grid(all);
+  const uint32_t more = all < grid ? 0 : all - each * grid;   // the first blocks take one more
+  const uint32_t begin = each * me + min(me, more);
+  run.left = each + (me < more);
+  const unsigned owner = __ballot_sync(ALL, inc > begin);
+  const int from = __ffs(owner) - 1;
+  if (lane == from) {
+    uint32_t off = begin - (inc - w), per = 0;
+    int b = b0;
+    for (;; ++b) {
+      if (m > 1) s = tree_seq(P, b);
+      per = seq_tiles<R>(P, s);
+      if (off < per * P.Hkv) break;
+      off -= per * P.Hkv;
     }
-    if (lane == 31) sh.warp[warp] = inc;
-    __syncthreads();
-    int64_t pre = before;
-    for (int i = 0; i < NW; ++i) {
-      if (i < warp) pre += sh.warp[i];
-      before += sh.warp[i];
-    }
-    const int64_t lo = pre + inc - w;
-    if (w > 0 && lo <= begin && begin < lo + w) {
-      sh.b = b;
-      sh.before = lo;
-    }
-    if (before > begin) break;
-  }
-  __syncthreads();
-  TreeRun run;
-  run.left = end - begin;
-  run.at = TreePlace{sh.b, 0, 0, 0};
-  if (sh.b < 0) run.left = 0;     // no tiles at all
-  if (run.left > 0) {
-    const TreeSeq s = tree_seq(P, sh.b);
-    const int64_t per = seq_tiles<R>(P, s);
-    int64_t off = begin - sh.before;
-    run.at.hk = static_cast<int>(off / per);
-    off -= run.at.hk * per;
-    int rt = 0;
+    run.b = b;
+    run.hk = off / per;
+    off -= run.hk * per;
     while (true) {
-      const int t = key_tiles(unit_keys<R>(P, s, rt));
+      const uint32_t t = key_tiles(unit_keys<R>(P, s, run.rt));
       if (off < t) break;
       off -= t;
-      ++rt;
+      ++run.rt;
     }
-    run.at.rt = rt;
-    run.at.tile = static_cast<int>(off);
+    run.tile = off;
   }
+  run.b = __shfl_sync(ALL, run.b, from);
+  run.hk = __shfl_sync(ALL, run.hk, from);
+  run.rt = __shfl_sync(ALL, run.rt, from);
+  run.tile = __shfl_sync(ALL, run.tile, from);
+  run.s.row0 = __shfl_sync(ALL, s.row0, from);
+  run.s.n = __shfl_sync(ALL, s.n, from);
+  run.s.base = __shfl_sync(ALL, s.base, from);
   return run;
 }
 
@@ -205,35 +208,31 @@ struct TreeWalk {
   TreeRun run;
   __device__ __forceinline__ bool next(const TreeParams& P, TreePiece& u) {
     if (run.left <= 0) return false;
-    TreePlace& at = run.at;
-    TreeSeq s = tree_seq(P, at.b);
+    TreeSeq& s = run.s;
     // on to the next sequence with rows
-    while (at.hk >= P.Hkv || s.n <= 0) {
-      at.hk = 0;
-      at.rt = 0;
-      at.tile = 0;
-      ++at.b;
-      if (at.b >= P.B) return false;
-      s = tree_seq(P, at.b);
+    while (run.hk >= P.Hkv || s.n <= 0) {
+      run.hk = run.rt = run.tile = 0;
+      if (++run.b >= P.B) return false;
+      s = tree_seq(P, run.b);
     }
-    u.b = at.b;
-    u.hk = at.hk;
-    u.rt = at.rt;
+    u.b = run.b;
+    u.hk = run.hk;
+    u.rt = run.rt;
     u.s = s;
-    u.keys = unit_keys<R>(P, s, at.rt);
+    u.keys = unit_keys<R>(P, s, run.rt);
     u.tiles = key_tiles(u.keys);
-    u.t0 = at.tile;
-    u.t1 = static_cast<int>(min(static_cast<int64_t>(u.tiles), at.tile + run.left));
+    u.t0 = run.tile;
+    u.t1 = min(u.tiles, run.tile + run.left);
     run.left -= u.t1 - u.t0;
-    u.row_first = at.rt * R;
-    u.rows = static_cast<int>(min(static_cast<int64_t>(R), static_cast<int64_t>(s.n) * P.G - u.row_first));
-    u.origin = s.base + (P.tree ? 0 : u.row_first / P.G);
-    at.tile = u.t1;
+    u.row_first = run.rt * R;
+    u.rows = min(R, s.n * P.G - u.row_first);
+    u.origin = s.base + (P.tree ? 0 : P.by_G(u.row_first));
+    run.tile = u.t1;
     if (u.t1 == u.tiles) {
-      at.tile = 0;
-      if (++at.rt >= row_tiles<R>(P, s)) {
-        at.rt = 0;
-        ++at.hk;
+      run.tile = 0;
+      if (++run.rt >= row_tiles<R>(P, s)) {
+        run.rt = 0;
+        ++run.hk;
       }
     }
     return true;
@@ -275,7 +274,7 @@ struct TileLoad {
   // pages of the tile that hold keys of the unit
   __device__ static __forceinline__ int pages(const TreeParams& P, const TreePiece& u, int tile) {
     const int keys = min(u.keys - tile * kTile, kTile);
-    return keys <= 0 ? 0 : (keys + P.page_size - 1) / P.page_size;
+    return keys <= 0 ? 0 : (keys + (1 << P.page_shift) - 1) >> P.page_shift;
   }
   // lane l: page index of the pool for page l / SLABS of the tile, one past
   // the pool (which TMA reads as zeros) if the table's entry is out of range
@@ -284,7 +283,7 @@ struct TileLoad {
     const int j = lane / SLABS;
     if (j >= pages(P, u, tile)) return 0;
     const int pg = P.table[static_cast<int64_t>(u.b) * P.max_pages +
-                           tile * (kTile / P.page_size) + j];
+                           tile * (kTile >> P.page_shift) + j];
     if (pg >= 0 && pg < P.n_pages) return pg;
     if (P.status) atomicOr(P.status, DEV_CACHE);
     return P.n_pages;
@@ -293,11 +292,11 @@ struct TileLoad {
                                                int lane, int page, const CUtensorMap* tm,
                                                uint32_t dst, uint32_t bar) {
     const int n = pages(P, u, tile);
-    if (lane == 0) mbar_arrive_expect_tx(bar, n * P.page_size * D * 2);
+    if (lane == 0) mbar_arrive_expect_tx(bar, (n << P.page_shift) * D * 2);
     __syncwarp();
     const int j = lane / SLABS, slab = lane % SLABS;
     if (j < n)
-      tma_load_4d(dst + slab * (kTile * 128) + j * P.page_size * 128, tm, bar, slab * 64, u.hk, 0,
+      tma_load_4d(dst + slab * (kTile * 128) + (j << P.page_shift) * 128, tm, bar, slab * 64, u.hk, 0,
                   page);
   }
 };
@@ -333,10 +332,10 @@ __device__ __forceinline__ float fix_value(const TreeParams& P, const TreePiece&
       const int i = w * 32 + __ffs(bits) - 1;
       bits &= bits - 1;
       const int pos = u.origin + i;
-      const int pg = P.table[static_cast<int64_t>(u.b) * P.max_pages + pos / P.page_size];
+      const int pg = P.table[static_cast<int64_t>(u.b) * P.max_pages + (pos >> P.page_shift)];
       if (pg < 0 || pg >= P.n_pages) continue;
       const float v = __bfloat162float(P.v_pool[pg * P.v_stride[0] +
-                                                (pos % P.page_size) * P.v_stride[1] +
+                                                (pos & ((1 << P.page_shift) - 1)) * P.v_stride[1] +
                                                 u.hk * P.v_stride[2] + c]);
       if (!isfinite(v)) x += v;
     }

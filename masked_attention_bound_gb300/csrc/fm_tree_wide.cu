@@ -32,10 +32,9 @@ struct WideCfg {
   static constexpr int OFF_ML = OFF_V + VSTAGES * TILE; // float2 [slot][128]
   static constexpr int OFF_NF = OFF_ML + 2 * 128 * 8;   // [2][8] keys with values not finite
   static constexpr int OFF_BAR = OFF_NF + 64;
-  static constexpr int NBAR = 22;
+  static constexpr int NBAR = 24;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;   // abort flag, TMEM address
-  static constexpr int OFF_SCAN = OFF_MISC + 16;
-  static constexpr int USED = OFF_SCAN + sizeof(TreeScan);
+  static constexpr int USED = OFF_MISC + 16;
   // one block per SM: it takes all of the tensor memory
   static constexpr int SMEM = USED > 120 * 1024 ? USED : 120 * 1024;
   static constexpr int THREADS = 384;
@@ -47,7 +46,7 @@ struct WideCfg {
 
 enum {
   W_QFULL = 0, W_SFULL = 2, W_PFULL = 4, W_PVDONE = 6, W_OEMPTY = 8, W_KFULL = 10, W_KEMPTY = 12,
-  W_VFULL = 14, W_VEMPTY = 17, W_DRAIN = 20
+  W_VFULL = 14, W_VEMPTY = 17, W_DRAIN = 20, W_TURN = 21
 };
 
 // How the two slots share a piece.
@@ -62,6 +61,16 @@ struct WideSplit {
 };
 __device__ __forceinline__ WideSplit wide_split(const TreePiece& u) {
   return WideSplit{u.rows > 128, u.keys > 0 ? u.t1 - u.t0 : 0};
+}
+
+// 16 bytes from global to shared memory without a register or a line of L1;
+// `bytes` 0 reads nothing and writes zeros.
+__device__ __forceinline__ void copy_async16(uint32_t dst, uint64_t src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void copy_async_wait() {
+  asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 __device__ __forceinline__ void slots_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
@@ -85,6 +94,7 @@ __global__ void __launch_bounds__(WideCfg<D>::THREADS, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   constexpr int K_WARP = 8, MMA_WARP = 9, V_WARP = 10;   // 11: slot 1's MMAs
 
+  if (warp == 2) touch_inputs(P, lane);
   if (tid == 0) {
     for (int s = 0; s < 2; ++s) {
       mbar_init(bar(W_QFULL + s), 4);     // one arrival per softmax warp of the slot
@@ -92,6 +102,7 @@ __global__ void __launch_bounds__(WideCfg<D>::THREADS, 1)
       mbar_init(bar(W_PFULL + s), 4);
       mbar_init(bar(W_PVDONE + s), 1);
       mbar_init(bar(W_OEMPTY + s), 8);    // both slots' warps may read O of either
+      mbar_init(bar(W_TURN + s), 1);
     }
     // a stage is free after two commits: one by each MMA thread, or both by
     // the one whose slot took the tile
@@ -115,14 +126,16 @@ __global__ void __launch_bounds__(WideCfg<D>::THREADS, 1)
   if (warp == K_WARP && lane == 0) tma_prefetch_desc(&tmK);
   if (warp == V_WARP && lane == 0) tma_prefetch_desc(&tmV);
   grid_launch_dependents();
+  grid_dependency_wait();
   tc_fence_before();
   TreeWalk<R> walk;
-  walk.run = tree_run<R, C::THREADS>(P, *reinterpret_cast<TreeScan*>(smem + C::OFF_SCAN));
+  walk.run = tree_run<R>(P);
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = *tmem_slot;
 
   auto wait = [&](int b, uint32_t parity) -> bool {
+    if (mbar_try_wait(bar(b), parity)) return true;
     if (*abort_flag) return false;
     if (!mbar_wait(bar(b), parity, P.status, P.wait_ns)) {
       *abort_flag = 1;
@@ -180,58 +193,87 @@ __global__ void __launch_bounds__(WideCfg<D>::THREADS, 1)
       uint32_t e0 = 0;          // tiles before this piece
       uint32_t pieces = 0;      // pieces with keys before this one
       uint32_t qn = 0, np = 0;  // Q tiles, P tiles of this slot so far
+      uint32_t turn = 0;        // turns taken
       bool ok = true;
       TreePiece u;
       while (ok && walk.next(P, u)) {
         const WideSplit w = wide_split(u);
         if (w.n == 0) continue;
-        if (!w.active(s)) {
-          // a single key tile, which slot 0 takes and releases
-          e0 += w.n;
-          ++pieces;
-          continue;
-        }
-        auto issue_s = [&](uint32_t e) -> bool {
-          const uint32_t st = e % C::KSTAGES;
-          if (!wait(W_KFULL + st, (e / C::KSTAGES) & 1)) return false;
-          tc_fence_after();
-          const uint32_t dK = dK0 + st * (C::TILE >> 4);
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = (kk >> 2) * (kTile * 128) + (kk & 3) * 32;
-            mma_ss(tS, sdesc_at(dQ, off), sdesc_at(dK, off), idS, kk > 0 ? 1u : 0u);
-          }
-          mma_commit(bar(W_SFULL + s));
-          mma_commit(bar(W_KEMPTY + st));
-          if (!w.rows) mma_commit(bar(W_KEMPTY + st));
-          return true;
+        // The two MMA threads take turns: a turn is one tile's PV and the next
+        // one's S.  Without it the slots fall into step (both wait for the
+        // same K, then both softmaxes run, then both slots' MMAs share the
+        // tensor pipe: 4900 cycles a pair of tiles); with turns one slot's
+        // MMAs run while the other's softmax does.
+        auto my_turn = [&]() -> bool {
+          return s == 0 ? (turn == 0 || wait(W_TURN + 1, (turn - 1) & 1)) : wait(W_TURN, turn & 1);
         };
-        auto issue_pv = [&](uint32_t e, bool first, bool last) -> bool {
-          if (!wait(W_PFULL + s, np & 1)) return false;
-          ++np;
-          // O of the slot is overwritten: the last piece's must have been read
-          if (first && pieces > 0 && !wait(W_OEMPTY + s, (pieces - 1) & 1)) return false;
-          const uint32_t st = e % C::VSTAGES;
-          if (!wait(W_VFULL + st, (e / C::VSTAGES) & 1)) return false;
-          tc_fence_after();
-          const uint32_t dV = dV0 + st * (C::TILE >> 4);
-#pragma unroll
-          for (int kk = 0; kk < kTile / 16; ++kk)
-            mma_ts(tO, tS + kk * 8, sdesc_at(dV, kk * 2048), idPV, (!first || kk > 0) ? 1u : 0u);
-          if (last) mma_commit(bar(W_PVDONE + s));
-          mma_commit(bar(W_VEMPTY + st));
-          if (!w.rows) mma_commit(bar(W_VEMPTY + st));
-          return true;
+        auto end_turn = [&]() {
+          mbar_arrive(bar(W_TURN + s));
+          ++turn;
         };
-        ok = wait(W_QFULL + s, qn & 1);
-        ++qn;
-        // S of the slot's next tile overwrites P of the last one: MMAs run in
-        // the order in which this thread issues them
         const int step = w.rows ? 1 : 2, x0 = w.rows ? 0 : s;
-        if (ok) ok = issue_s(e0 + x0);
-        for (int x = x0; ok && x < w.n; x += step) {
-          ok = issue_pv(e0 + x, x == x0, x + step >= w.n);
-          if (ok && x + step < w.n) ok = issue_s(e0 + x + step);
+        const int turns = (w.rows ? w.n : (w.n + 1) / 2) + 1;   // of either slot
+        const bool active = w.active(s);
+        if (active) {
+          ok = wait(W_QFULL + s, qn & 1);
+          ++qn;
+        }
+        int x = x0;
+        for (int i = 0; ok && i < turns; ++i) {
+          // PV of the slot's tile x - step, then S of its tile x, which
+          // overwrites that P: MMAs run in the order in which a thread issues them
+          const int xp = x - step;
+          const bool pv = i > 0 && xp < w.n, sn = x < w.n;
+          const uint32_t ep = e0 + xp, e = e0 + x;
+          const uint32_t vst = ep % C::VSTAGES, kst = e % C::KSTAGES;
+          // P comes last: what else the turn needs is known by then, and the
+          // product starts as soon as P is there
+          bool kready = false;
+          if (pv) {
+            ok = wait(W_VFULL + vst, (ep / C::VSTAGES) & 1);
+            // O of the slot is overwritten: the last piece's must have been read
+            if (ok && i == 1 && pieces > 0) ok = wait(W_OEMPTY + s, (pieces - 1) & 1);
+            if (ok) ok = my_turn();
+            if (sn) kready = mbar_try_wait(bar(W_KFULL + kst), (e / C::KSTAGES) & 1);
+            if (ok) ok = wait(W_PFULL + s, np & 1);
+            ++np;
+          } else {
+            if (sn) ok = wait(W_KFULL + kst, (e / C::KSTAGES) & 1);
+            kready = true;
+            if (ok) ok = my_turn();
+          }
+          if (!ok) break;
+          tc_fence_after();
+          if (pv) {
+            const uint32_t dV = dV0 + vst * (C::TILE >> 4);
+#pragma unroll
+            for (int kk = 0; kk < kTile / 16; ++kk)
+              mma_ts(tO, tS + kk * 8, sdesc_at(dV, kk * 2048), idPV, (i > 1 || kk > 0) ? 1u : 0u);
+            if (!sn) mma_commit(bar(W_PVDONE + s));
+            mma_commit(bar(W_VEMPTY + vst));
+            if (!w.rows) mma_commit(bar(W_VEMPTY + vst));
+          }
+          bool given = false;
+          if (sn) {
+            if (!kready && !mbar_try_wait(bar(W_KFULL + kst), (e / C::KSTAGES) & 1)) {
+              end_turn();        // K has not landed: the other slot need not wait for it
+              given = true;
+              ok = wait(W_KFULL + kst, (e / C::KSTAGES) & 1);
+              if (!ok) break;
+              tc_fence_after();
+            }
+            const uint32_t dK = dK0 + kst * (C::TILE >> 4);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint32_t off = (kk >> 2) * (kTile * 128) + (kk & 3) * 32;
+              mma_ss(tS, sdesc_at(dQ, off), sdesc_at(dK, off), idS, kk > 0 ? 1u : 0u);
+            }
+            mma_commit(bar(W_SFULL + s));
+            mma_commit(bar(W_KEMPTY + kst));
+            if (!w.rows) mma_commit(bar(W_KEMPTY + kst));
+          }
+          if (!given) end_turn();
+          x += step;
         }
         e0 += w.n;
         ++pieces;
@@ -261,7 +303,7 @@ __global__ void __launch_bounds__(WideCfg<D>::THREADS, 1)
       const int ur = w.rows ? slot * 128 + r : r;      // row of the unit
       const bool mine = ur < u.rows && (w.rows || slot == 0 || w.n > 0);
       const int rr = u.row_first + ur;
-      const int node = ur < u.rows ? rr / P.G : 0;
+      const int node = ur < u.rows ? P.by_G(rr) : 0;
       const int h = u.hk * P.G + (ur < u.rows ? rr - node * P.G : 0);
       __nv_bfloat16* orow = P.o + (u.s.row0 + node) * P.o_stride[0] + h * P.o_stride[1];
       float* lse_out = P.lse + static_cast<int64_t>(h) * P.total + u.s.row0 + node;
@@ -280,28 +322,35 @@ __global__ void __launch_bounds__(WideCfg<D>::THREADS, 1)
       // which keys from origin on the row sees: bit i is key origin + i
       uint32_t seen[8];
       bool live = mine;
+      const int part0 = u.origin / kTile;              // tiles from here on are not seen by all
       if (P.tree) {
 #pragma unroll
         for (int x = 0; x < 8; ++x) seen[x] = 0;
-        if (mine) tree_ancestors(P, u.s, node, seen);
-        live = (seen[0] | seen[1] | seen[2] | seen[3] | seen[4] | seen[5] | seen[6] | seen[7]) != 0;
+        if (mine) live = tree_parent(P, u.s, node) != -2;
+        if (live && u.t1 > part0) tree_ancestors(P, u.s, node, seen);
       }
       const bool warp_live = __any_sync(0xffffffffu, live);
       float m_used = -INFINITY, l = 0.f;
       if (active) {
-        // this slot's Q: S of the slot's earlier pieces has been read
-        const uint4* src = reinterpret_cast<const uint4*>(P.q + (u.s.row0 + node) * P.q_stride[0] +
-                                                          h * P.q_stride[1]);
-        uint4 x[D / 8];
+        // this slot's Q (S of its earlier pieces has been read): a row is
+        // copied by D / 8 lanes, so that a warp's copy covers whole rows, and
+        // asynchronously past L1: the few KB that shared memory leaves of it
+        // hold up plain loads of 64 KB for 7000 cycles
+        const __nv_bfloat16* src =
+            P.q + (u.s.row0 + node) * P.q_stride[0] + static_cast<int64_t>(h) * P.q_stride[1];
+        constexpr int LPR = D / 8, RPI = 32 / LPR;     // lanes a row, rows an instruction
+        const unsigned in_rows = __ballot_sync(0xffffffffu, mine);
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c) x[c] = mine ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-        for (int c = 0; c < D / 8; ++c)
-          st_shared_v4(sbase + C::OFF_Q + slot * C::TILE + sw128_offset(r, c * 8, 128), x[c].x, x[c].y,
-                       x[c].z, x[c].w);
+        for (int i = 0; i < 32 / RPI; ++i) {
+          const int from = i * RPI + lane / LPR;
+          const uint64_t row = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(src), from);
+          copy_async16(sbase + C::OFF_Q + slot * C::TILE +
+                           sw128_offset(quarter * 32 + from, (lane % LPR) * 8, 128),
+                       row + (lane % LPR) * 16, (in_rows >> from) & 1u ? 16 : 0);
+        }
+        copy_async_wait();
         fence_proxy_async_smem();
         mbar_arrive_warp(bar(W_QFULL + slot));
-        const int part0 = u.origin / kTile;            // tiles from here on are not seen by all
         int done = 0;
         for (int x0 = w.rows ? 0 : slot; x0 < w.n; x0 += w.rows ? 1 : 2) {
           const int t = u.t0 + x0;
@@ -460,7 +509,11 @@ __global__ void __launch_bounds__(WideCfg<D>::THREADS, 1)
       const int slot_part = 2 * blockIdx.x + (u.t0 == 0 ? 1 : 0);
       const int64_t at = static_cast<int64_t>(slot_part) * P.part_rows + ur;
       float* prow = P.part_o + at * D;
-      // 32 columns at a time
+      // O by blocks of 32 columns; each passes through the warp's part of the
+      // slot's Q buffer (no longer needed), so that the stores cover whole
+      // runs of a row: 64 bytes (bf16) or 128 bytes (fp32 parts)
+      uint8_t* stage = smem + C::OFF_Q + slot * C::TILE + quarter * 32 * (D * 2);
+      const unsigned out_rows = __ballot_sync(0xffffffffu, writes);
 #pragma unroll
       for (int cb = 0; cb < D / 32; ++cb) {
         if (cb * 32 < c0 || cb * 32 >= c1) continue;
@@ -479,22 +532,42 @@ __global__ void __launch_bounds__(WideCfg<D>::THREADS, 1)
             tmem_wait_ld();
           }
         }
-        if (writes) {
 #pragma unroll
-          for (int y = 0; y < 32; ++y) v[y] = l_out == 0.f ? 0.f : v[y] * inv;
-          if (whole) {
+        for (int y = 0; y < 32; ++y) v[y] = l_out == 0.f ? 0.f : v[y] * inv;
+        // 16-byte words of a row's 32 columns: 4 (bf16) or 8 (fp32), stored
+        // at their number xor the row's
+        if (whole) {
+          uint4* own = reinterpret_cast<uint4*>(stage) + lane * 4;
 #pragma unroll
-            for (int y = 0; y < 4; ++y)
-              reinterpret_cast<uint4*>(orow + cb * 32)[y] =
-                  make_uint4(pack_bf16(v[8 * y], v[8 * y + 1]), pack_bf16(v[8 * y + 2], v[8 * y + 3]),
-                             pack_bf16(v[8 * y + 4], v[8 * y + 5]), pack_bf16(v[8 * y + 6], v[8 * y + 7]));
-          } else {
+          for (int y = 0; y < 4; ++y)
+            own[y ^ ((lane >> 1) & 3)] =
+                make_uint4(pack_bf16(v[8 * y], v[8 * y + 1]), pack_bf16(v[8 * y + 2], v[8 * y + 3]),
+                           pack_bf16(v[8 * y + 4], v[8 * y + 5]), pack_bf16(v[8 * y + 6], v[8 * y + 7]));
+          __syncwarp();
 #pragma unroll
-            for (int y = 0; y < 8; ++y)
-              reinterpret_cast<float4*>(prow + cb * 32)[y] =
-                  make_float4(v[4 * y], v[4 * y + 1], v[4 * y + 2], v[4 * y + 3]);
+          for (int i = 0; i < 4; ++i) {
+            const int row = i * 8 + lane / 4, word = lane % 4;
+            const uint64_t dst = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(orow), row);
+            if ((out_rows >> row) & 1u)
+              reinterpret_cast<uint4*>(dst)[cb * 4 + word] =
+                  reinterpret_cast<const uint4*>(stage)[row * 4 + (word ^ ((row >> 1) & 3))];
+          }
+        } else {
+          uint4* own = reinterpret_cast<uint4*>(stage) + lane * 8;
+#pragma unroll
+          for (int y = 0; y < 8; ++y)
+            own[y ^ (lane & 7)] = make_uint4(raw[4 * y], raw[4 * y + 1], raw[4 * y + 2], raw[4 * y + 3]);
+          __syncwarp();
+          // a part's rows lie one after the other
+          uint4* dst = reinterpret_cast<uint4*>(prow - static_cast<int64_t>(lane) * D) + cb * 8;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int row = i * 4 + lane / 8, word = lane % 8;
+            if ((out_rows >> row) & 1u)
+              dst[row * (D / 4) + word] = reinterpret_cast<const uint4*>(stage)[row * 8 + (word ^ (row & 7))];
           }
         }
+        __syncwarp();
       }
       tc_fence_before();
       if (w.rows) {
@@ -560,9 +633,9 @@ static fm_status launch_wide_d(const TreeParams& P, const CUtensorMap& tk, const
   if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess) return FM_ERR_CUDA;
   if (fa.numRegs < C::MIN_LAUNCH_REGS) return FM_ERR_UNSUPPORTED;
   prof_begin(K_TREE, s);
-  kern<<<grid, C::THREADS, C::SMEM, s>>>(P, tk, tv);
+  const cudaError_t e = launch_dependent(kern, dim3(grid), C::THREADS, C::SMEM, s, P, tk, tv);
   prof_end(K_TREE, s);
-  return cudaGetLastError() == cudaSuccess ? FM_OK : FM_ERR_CUDA;
+  return e == cudaSuccess ? FM_OK : FM_ERR_CUDA;
 }
 
 fm_status launch_tree_wide(const TreeParams& P, int d, const CUtensorMap& tk, const CUtensorMap& tv,
