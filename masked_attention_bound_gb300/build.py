@@ -1,8 +1,10 @@
-"""Build ``libfm.so`` in-tree with nvcc for sm_103a.
+"""Build ``libfm.so`` in-tree with nvcc for sm_103a, and ``_fmcache.so``, the
+Python module of the paged cache's calls.
 
 Each ``csrc/*.cu`` compiles to ``_build/<name>.o`` in parallel, then one
-nvcc link makes the shared library next to this file.  Rebuilds only when a
-source or header is newer than the library.
+nvcc link makes the shared library next to this file.  ``csrc/fm_binding.cpp``
+compiles with the host compiler against torch's headers and links to the
+library.  Rebuilds only when a source or header is newer than its result.
 """
 from __future__ import annotations
 
@@ -18,6 +20,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libfm.so")
+BINDING = os.path.join(CSRC, "fm_binding.cpp")
+MODULE = os.path.join(PKG, "_fmcache.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I" + INCLUDE, "-I" + CSRC]
@@ -39,11 +43,46 @@ def _deps():
         + glob.glob(os.path.join(INCLUDE, "*.h"))
 
 
-def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+def _newer(result, deps) -> bool:
+    if not os.path.exists(result):
         return False
-    t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(f) <= t for f in _deps())
+    t = os.path.getmtime(result)
+    return all(os.path.getmtime(f) <= t for f in deps)
+
+
+def _binding_deps():
+    return [BINDING, os.path.join(INCLUDE, "fm.h")]
+
+
+def up_to_date() -> bool:
+    return _newer(LIB, _deps()) and _newer(MODULE, _binding_deps())
+
+
+def _compile_binding(obj):
+    import sysconfig
+
+    import torch
+    base = os.path.join(os.path.dirname(torch.__file__), "include")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")
+    inc = [base, os.path.join(base, "torch", "csrc", "api", "include"), sysconfig.get_paths()["include"],
+           cuda, INCLUDE]
+    _run(["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+          *(a for i in inc for a in ("-isystem", i)), "-c", BINDING, "-o", obj], "the binding")
+
+
+def _link_binding(obj):
+    import torch
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = MODULE + ".tmp"
+    _run(["g++", "-shared", "-o", tmp, obj, "-L" + PKG, "-l:libfm.so", "-L" + libs, "-lc10", "-lc10_cuda",
+          "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN"], "linking the binding")
+    os.replace(tmp, MODULE)
+
+
+def _run(cmd, what):
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what} failed:\n{r.stdout}\n{r.stderr}")
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -65,8 +104,11 @@ def build(force: bool = False, verbose: bool = False) -> str:
             sys.stderr.write(r.stderr)
         return obj
 
+    binding = os.path.join(BUILD, "fm_binding.o")
     with ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 4)) as ex:
+        made = ex.submit(_compile_binding, binding)
         objs = list(ex.map(compile_one, _sources()))
+        made.result()
     tmp = LIB + ".tmp"
     # no -lcuda: the TMA encoder is fetched through the runtime's driver
     # entry-point query, so the library loads on machines without a driver
@@ -75,6 +117,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    _link_binding(binding)
     return LIB
 
 

@@ -1,5 +1,7 @@
 // Host-side declarations of the paged K/V cache's translation units.
 #pragma once
+#include <atomic>
+
 #include "fm_internal.h"
 
 namespace fm {
@@ -19,6 +21,24 @@ inline bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
   const char* x = static_cast<const char*>(a);
   const char* y = static_cast<const char*>(b);
   return x < y + nb && y < x + na;
+}
+
+// Sets a kernel's shared memory on the current device at its first launch
+// there (two runtime calls, some 1.5 us, that every later launch is spared);
+// min_regs: registers per thread that it must have been compiled with.
+template <typename K>
+inline fm_status prepare_kernel(K* kern, int smem, int min_regs, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return FM_ERR_CUDA;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (done.load(std::memory_order_acquire) & bit) return FM_OK;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    return FM_ERR_CUDA;
+  cudaFuncAttributes fa;
+  if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess) return FM_ERR_CUDA;
+  if (fa.numRegs < min_regs) return FM_ERR_UNSUPPORTED;
+  done.fetch_or(bit, std::memory_order_release);
+  return FM_OK;
 }
 
 // A launch that may start while the kernel before it in the stream still

@@ -566,8 +566,9 @@ static fm_status launch_narrow(const TreeParams& P, const CUtensorMap& tk, const
                                int grid, cudaStream_t s) {
   using C = NarrowCfg<D>;
   auto kern = tree_narrow_kernel<D>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
-    return FM_ERR_CUDA;
+  static std::atomic<uint64_t> ready{0};
+  const fm_status st = prepare_kernel(kern, C::SMEM, 0, ready);
+  if (st != FM_OK) return st;
   prof_begin(K_TREE, s);
   const cudaError_t e = launch_dependent(kern, dim3(grid), C::THREADS, C::SMEM, s, P, tk, tv);
   prof_end(K_TREE, s);

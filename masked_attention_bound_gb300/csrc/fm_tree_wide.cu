@@ -626,12 +626,10 @@ static fm_status launch_wide_d(const TreeParams& P, const CUtensorMap& tk, const
                                int grid, cudaStream_t s) {
   using C = WideCfg<D>;
   auto kern = tree_wide_kernel<D>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
-    return FM_ERR_CUDA;
   // the setmaxnreg split must fit in the registers the block launches with
-  cudaFuncAttributes fa;
-  if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess) return FM_ERR_CUDA;
-  if (fa.numRegs < C::MIN_LAUNCH_REGS) return FM_ERR_UNSUPPORTED;
+  static std::atomic<uint64_t> ready{0};
+  const fm_status st = prepare_kernel(kern, C::SMEM, C::MIN_LAUNCH_REGS, ready);
+  if (st != FM_OK) return st;
   prof_begin(K_TREE, s);
   const cudaError_t e = launch_dependent(kern, dim3(grid), C::THREADS, C::SMEM, s, P, tk, tv);
   prof_end(K_TREE, s);
