@@ -292,7 +292,8 @@ fm_status fm_varlen_bounds(const int32_t* cu_seqlens, int n_seqs, int total, int
  * counterpart there.
  *
  * The cache: K and V pools of n_pages pages of page_size tokens (16, 32, 64
- * or 128) with Hkv heads of d (64 or 128) bf16 elements, for `layers` layers.
+ * or 128; n_pages below 2^23) with Hkv heads of d (64 or 128) bf16 elements, for
+ * `layers` layers.
  * Element (layer, page, slot, head, c) of a pool is at layer*stride[0] +
  * page*stride[1] + slot*stride[2] + head*stride[3] + c (elements; multiples
  * of 8, bases 16-byte aligned).  One page index means the same page in every

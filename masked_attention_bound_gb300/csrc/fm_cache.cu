@@ -38,9 +38,16 @@ namespace {
 struct Pools {
   uint4* p[2];          // K, V
   int64_t layer[2], page[2], slot[2], head[2];
-  int Hkv, chunks;      // heads, vectors per head (d / 8)
-  int row;              // vectors of one token: Hkv * chunks
-  int page_size;
+  int chunk_shift;      // vectors per head (d / 8) as a power of two
+  int row;              // vectors of one token, K or V
+  int page_shift;       // page_size as a power of two
+  FastDiv by_row;
+  bool linear[2];       // a page's tokens lie one after the other without gaps
+  __device__ __forceinline__ int page_size() const { return 1 << page_shift; }
+  // place of vector r of a token: head r >> chunk_shift
+  __device__ __forceinline__ int64_t in_token(int kv, int r) const {
+    return (r >> chunk_shift) * head[kv] + (r & ((1 << chunk_shift) - 1));
+  }
 };
 
 Pools pools_of(const fm_cache& c, void* k, void* v) {
@@ -53,11 +60,12 @@ Pools pools_of(const fm_cache& c, void* k, void* v) {
     P.page[t] = st[t][1] / 8;
     P.slot[t] = st[t][2] / 8;
     P.head[t] = st[t][3] / 8;
+    P.linear[t] = (c.Hkv == 1 || P.head[t] == c.d / 8) && P.slot[t] == c.Hkv * (c.d / 8);
   }
-  P.Hkv = c.Hkv;
-  P.chunks = c.d / 8;
-  P.row = c.Hkv * P.chunks;
-  P.page_size = c.page_size;
+  P.chunk_shift = c.d == 64 ? 3 : 4;
+  P.row = c.Hkv << P.chunk_shift;
+  P.by_row = FastDiv::of(P.row);
+  P.page_shift = page_shift(c.page_size);
   return P;
 }
 
@@ -76,10 +84,10 @@ __device__ __forceinline__ int context_of(const int32_t* lens, const int32_t* cu
 }
 
 // ------------------------------------------------------------------ append
-// Each block takes kAppendTokens consecutive packed tokens; one thread per
-// token finds its sequence (binary search over cu), page and slot, then all
-// threads copy 16-byte vectors, K and V.
-constexpr int kAppendThreads = 256;
+// Each block takes a few consecutive packed tokens.  All threads first load
+// its 16-byte vectors, K and V, which needs no lookup; meanwhile one thread
+// per token finds its sequence (binary search over cu), page and slot.
+constexpr int kAppendThreads = 256, kAppendVecs = 4;
 
 struct AppendArgs {
   const uint4* src[2];
@@ -89,12 +97,39 @@ struct AppendArgs {
   int B, total, max_pages, n_pages, tokens;  // tokens: per block
 };
 
-__global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_constant__ AppendArgs A, const __grid_constant__ Pools P) {
+__global__ void __launch_bounds__(kAppendThreads)
+    append_kernel(const __grid_constant__ AppendArgs A, const __grid_constant__ Pools P) {
   extern __shared__ int64_t where[];   // per token of the block: page << 8 | slot, -1: skip
+  grid_launch_dependents();
+  grid_dependency_wait();
   const int t0 = blockIdx.x * A.tokens;
+  const int per = 2 * P.row;           // vectors of one token, K then V
+  const int all = min(A.tokens, A.total - t0) * per;
+  uint4 x[kAppendVecs];
+  // vector v of the block: token, K or V, vector of the token
+  struct At {
+    int i, kv, r;
+  };
+  auto at = [&](int v) -> At {
+    const int half = P.by_row(v);      // 2 i + kv
+    return At{half >> 1, half & 1, v - half * P.row};
+  };
+  auto load = [&](int v0) {
+#pragma unroll
+    for (int u = 0; u < kAppendVecs; ++u) {
+      const int v = v0 + u * kAppendThreads;
+      if (v < all) {
+        const At w = at(v);
+        const int64_t head = (w.r >> P.chunk_shift) * A.head[w.kv];
+        x[u] = __ldg(A.src[w.kv] + (t0 + w.i) * A.tok[w.kv] + head +
+                     (w.r & ((1 << P.chunk_shift) - 1)));
+      }
+    }
+  };
+  load(threadIdx.x);
   for (int i = threadIdx.x; i < A.tokens; i += blockDim.x) {
     const int t = t0 + i;
-    int64_t at = -1;
+    int64_t to = -1;
     if (t < A.total && t < A.cu[A.B]) {
       int lo = 0, hi = A.B;            // the last b with cu[b] <= t
       while (hi - lo > 1) {
@@ -102,56 +137,47 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
         if (A.cu[mid] <= t) lo = mid; else hi = mid;
       }
       int n;
-      const int base = context_of(A.lens, A.cu, lo, A.total, A.max_pages * P.page_size, n);
+      const int base = context_of(A.lens, A.cu, lo, A.total, A.max_pages << P.page_shift, n);
       const int node = t - A.cu[lo];
       bool ok = base >= 0 && node >= 0 && node < n;
       if (ok) {
         const int pos = base + node;
-        const int pg = A.table[static_cast<int64_t>(lo) * A.max_pages + pos / P.page_size];
+        const int pg = A.table[static_cast<int64_t>(lo) * A.max_pages + (pos >> P.page_shift)];
         ok = pg >= 0 && pg < A.n_pages;
-        at = (static_cast<int64_t>(pg) << 8) | (pos % P.page_size);
+        to = (static_cast<int64_t>(pg) << 8) | (pos & (P.page_size() - 1));
       }
       if (!ok) {
-        at = -1;
+        to = -1;
         flag(A.status, DEV_CACHE);
       }
     }
-    where[i] = at;
+    where[i] = to;
   }
   __syncthreads();
-  const int per = 2 * P.row;           // vectors of one token, K then V
-  const int all = A.tokens * per;
-  constexpr int U = 4;
-  for (int v0 = threadIdx.x; v0 < all; v0 += U * kAppendThreads) {
-    uint4 x[U];
-    uint4* to[U];
+  for (int v0 = threadIdx.x; v0 < all; v0 += kAppendVecs * kAppendThreads) {
+    if (v0 != threadIdx.x) load(v0);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
+    for (int u = 0; u < kAppendVecs; ++u) {
       const int v = v0 + u * kAppendThreads;
-      to[u] = nullptr;
       if (v < all) {
-        const int i = v / per, w = v - i * per;
-        const int kv = w >= P.row, r = w - kv * P.row;
-        const int h = r / P.chunks, ch = r - h * P.chunks;
-        const int64_t at = where[i];
-        if (at >= 0) {
-          x[u] = __ldg(A.src[kv] + (t0 + i) * A.tok[kv] + h * A.head[kv] + ch);
-          to[u] = P.p[kv] + (at >> 8) * P.page[kv] + (at & 255) * P.slot[kv] + h * P.head[kv] + ch;
-        }
+        const At w = at(v);
+        const int64_t to = where[w.i];
+        if (to >= 0)
+          P.p[w.kv][(to >> 8) * P.page[w.kv] + (to & 255) * P.slot[w.kv] + P.in_token(w.kv, w.r)] = x[u];
       }
     }
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (to[u]) *to[u] = x[u];
   }
 }
 
 // ------------------------------------------------------------------ accept
-// One thread per (layer, K or V, 16-byte vector of a token) of a sequence
-// walks the accepted nodes in ascending order.  The node moved i-th comes
-// from a place at or past base + i and goes to base + i, so a thread that
-// loads node i before it stores node i never overwrites a source that it
-// still needs; threads share no bytes.
+// A block moves the accepted nodes of one sequence in one layer; its first
+// warp looks their places up, 32 at a time.  Each thread keeps one 16-byte
+// vector of a token (of K or V) and walks the nodes in ascending order.  The
+// node moved i-th comes from a place at or past base + i and goes to base +
+// i, so a thread that loads node i before it stores node i never overwrites
+// a source that it still needs; threads share no bytes.
+constexpr int kAcceptThreads = 256;
+
 struct AcceptArgs {
   const int32_t *accept, *n_accept, *cu, *table, *lens;
   int32_t *lens_out, *ref;
@@ -159,22 +185,45 @@ struct AcceptArgs {
   int max_accept, max_pages, n_pages;
 };
 
-__global__ void __launch_bounds__(256) accept_kernel(const __grid_constant__ AcceptArgs A, const __grid_constant__ Pools P) {
-  const int b = blockIdx.y, layer = blockIdx.z;
+__global__ void __launch_bounds__(kAcceptThreads)
+    accept_kernel(const __grid_constant__ AcceptArgs A, const __grid_constant__ Pools P) {
+  __shared__ int2 place[32];           // from, to: page << 8 | slot
+  __shared__ int good;
+  grid_launch_dependents();
+  grid_dependency_wait();
+  const int b = blockIdx.y, layer = blockIdx.z, lane = threadIdx.x & 31;
   const int32_t* acc = A.accept + static_cast<int64_t>(b) * A.max_accept;
-  int n;
-  const int base = context_of(A.lens, A.cu, b, 0x7fffffff, A.max_pages * P.page_size, n);
-  const int m = A.n_accept[b];
   const int32_t* row = A.table + static_cast<int64_t>(b) * A.max_pages;
-  bool ok = base >= 0 && m >= 0 && m <= n && m <= A.max_accept;
-  for (int i = 0; ok && i < m; ++i) {
-    const int a = acc[i];
-    ok = a < n && a > (i ? acc[i - 1] : -1);
-    if (ok) {
-      const int ps = row[(base + a) / P.page_size], pd = row[(base + i) / P.page_size];
-      ok = ps >= 0 && ps < A.n_pages && pd >= 0 && pd < A.n_pages;
+  const int m = A.n_accept[b];
+  int n;
+  const int base = context_of(A.lens, A.cu, b, 0x7fffffff, A.max_pages << P.page_shift, n);
+  const bool sized = base >= 0 && m >= 0 && m <= n && m <= A.max_accept;
+  // page << 8 | slot of a position, -1 if its page is out of range
+  auto at = [&](int pos) -> int {
+    const int pg = row[pos >> P.page_shift];
+    return pg >= 0 && pg < A.n_pages ? (pg << 8) | (pos & (P.page_size() - 1)) : -1;
+  };
+  // entry i of the list, valid or not
+  auto look = [&](int i, int2& p) -> bool {
+    const int a = acc[i], before = i ? acc[i - 1] : -1;
+    if (a <= before || a >= n) return false;
+    p = make_int2(at(base + a), at(base + i));
+    return p.x >= 0 && p.y >= 0;
+  };
+  if (threadIdx.x < 32) {
+    bool ok = sized;
+    int2 p = make_int2(0, 0);
+    for (int i = lane; sized && i < m; i += 32) {
+      int2 q;
+      ok = look(i, q) && ok;
+      if (i < 32) p = q;
     }
+    ok = __all_sync(0xffffffffu, ok);
+    place[lane] = p;
+    if (lane == 0) good = ok;
   }
+  __syncthreads();
+  const bool ok = good != 0;
   if (blockIdx.x == 0 && layer == 0) {
     if (threadIdx.x == 0) {
       A.lens_out[b] = ok ? base + m : A.lens[b];
@@ -182,30 +231,40 @@ __global__ void __launch_bounds__(256) accept_kernel(const __grid_constant__ Acc
     }
     // the pages past the new length
     if (ok && A.ref)
-      for (int j = (base + m + P.page_size - 1) / P.page_size + threadIdx.x;
-           j < (base + n + P.page_size - 1) / P.page_size; j += blockDim.x) {
+      for (int j = ((base + m + P.page_size() - 1) >> P.page_shift) + threadIdx.x;
+           j < (base + n + P.page_size() - 1) >> P.page_shift; j += blockDim.x) {
         const int pg = row[j];
         if (pg >= 0 && pg < A.n_pages) atomicSub(A.ref + pg, 1);
         else flag(A.status, DEV_CACHE);
       }
   }
-  const int v = blockIdx.x * blockDim.x + threadIdx.x;
-  if (!ok || v >= 2 * P.row) return;
-  const int kv = v >= P.row, r = v - kv * P.row;
-  const int h = r / P.chunks;
-  uint4* pool = P.p[kv] + layer * P.layer[kv] + h * P.head[kv] + (r - h * P.chunks);
-  auto at = [&](int pos) -> uint4* {
-    return pool + row[pos / P.page_size] * P.page[kv] + (pos % P.page_size) * P.slot[kv];
-  };
+  if (!ok) return;
+  const int v = blockIdx.x * kAcceptThreads + threadIdx.x;
+  const int kv = v >= P.row;
+  uint4* pool = P.p[kv] + layer * P.layer[kv] + P.in_token(kv, v - kv * P.row);
   constexpr int U = 8;
-  for (int i0 = 0; i0 < m; i0 += U) {
-    uint4 x[U];
+  for (int i0 = 0; i0 < m; i0 += 32) {
+    if (i0 > 0) {                      // the next 32 places
+      __syncthreads();
+      int2 q;
+      if (threadIdx.x < 32 && i0 + lane < m && look(i0 + lane, q)) place[lane] = q;
+      __syncthreads();
+    }
+    if (v >= 2 * P.row) continue;
+    const int end = min(m - i0, 32);
+    for (int j0 = 0; j0 < end; j0 += U) {
+      uint4 x[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (i0 + u < m && acc[i0 + u] != i0 + u) x[u] = *at(base + acc[i0 + u]);
+      for (int u = 0; u < U; ++u) {
+        const int2 p = place[(j0 + u) & 31];
+        if (j0 + u < end && p.x != p.y) x[u] = pool[(p.x >> 8) * P.page[kv] + (p.x & 255) * P.slot[kv]];
+      }
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (i0 + u < m && acc[i0 + u] != i0 + u) *at(base + i0 + u) = x[u];
+      for (int u = 0; u < U; ++u) {
+        const int2 p = place[(j0 + u) & 31];
+        if (j0 + u < end && p.x != p.y) pool[(p.y >> 8) * P.page[kv] + (p.y & 255) * P.slot[kv]] = x[u];
+      }
+    }
   }
 }
 
@@ -225,8 +284,16 @@ __device__ __forceinline__ int pages_of(const PageArgs& A, int b, int& len, bool
   return (len + A.page_size - 1) / A.page_size;
 }
 
+__global__ void __launch_bounds__(256) ref_copy_kernel(const int32_t* from, int32_t* to, int n) {
+  grid_launch_dependents();
+  grid_dependency_wait();
+  for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < n; i += gridDim.x * blockDim.x) to[i] = from[i];
+}
+
 // One warp per row: the new row's pages gain a hold, the old row's lose one.
-__global__ void __launch_bounds__(128) fork_kernel(PageArgs A, const int32_t* parent) {
+__global__ void __launch_bounds__(128) fork_kernel(const __grid_constant__ PageArgs A, const int32_t* parent) {
+  grid_launch_dependents();
+  grid_dependency_wait();
   const int b = (blockIdx.x * blockDim.x + threadIdx.x) >> 5, lane = threadIdx.x & 31;
   if (b >= A.B) return;
   int p = parent[b];
@@ -350,11 +417,14 @@ __device__ __forceinline__ void exchange(cg::cluster_group& cl, PlanShared& sh, 
 
 // info (the caller's): free pages after the call, pages asked for.
 __global__ void __cluster_dims__(kPlanBlocks, 1, 1) __launch_bounds__(kPlanThreads, 1)
-    reserve_kernel(PageArgs A, const int32_t* grow, PlanWs W, int32_t* info) {
+    reserve_kernel(const __grid_constant__ PageArgs A, const int32_t* grow,
+                   const __grid_constant__ PlanWs W, int32_t* info) {
   cg::cluster_group cl = cg::this_cluster();
   __shared__ PlanShared sh;
+  __shared__ int3 rows_of[kPlanThreads];   // asked for, pages, first of the taken ones
   const int rank = cl.block_rank();
   grid_launch_dependents();
+  grid_dependency_wait();
   const int rows = (A.B + kPlanBlocks - 1) / kPlanBlocks;
   const int b0 = min(rank * rows, A.B), b1 = min(b0 + rows, A.B);
   const int span = (A.n_pages + kPlanBlocks - 1) / kPlanBlocks;
@@ -426,9 +496,10 @@ __global__ void __cluster_dims__(kPlanBlocks, 1, 1) __launch_bounds__(kPlanThrea
   }
   cl.sync();                             // the list is complete, and ref_out
 
-  // the rows
+  // the rows, 1024 at a time: a thread each for the counts, then a warp each
+  // for the entries
   int first = sh.before[0], released = 0;
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   for (int c0 = b0; c0 < b1; c0 += kPlanThreads) {
     const int b = c0 + threadIdx.x;
     const int word = b < b1 && go ? W.row[b] : 0;
@@ -436,10 +507,10 @@ __global__ void __cluster_dims__(kPlanBlocks, 1, 1) __launch_bounds__(kPlanThrea
     int n;
     const int at = first + block_scan(mine, sh.warp_sums, n);
     first += n;
-    int len = 0, have = 0;
-    bool ok;
     if (b < b1) {
-      have = pages_of(A, b, len, ok);
+      int len;
+      bool ok;
+      const int have = pages_of(A, b, len, ok);
       A.lens_out[b] = go ? len + grow[b] : A.lens[b];
       int32_t* copy = W.copy + 3 * static_cast<int64_t>(b);
       copy[1] = -1;
@@ -450,19 +521,17 @@ __global__ void __cluster_dims__(kPlanBlocks, 1, 1) __launch_bounds__(kPlanThrea
         copy[2] = len % A.page_size;
         released += atomicSub(A.ref_out + old, 1) == 1;
       }
+      rows_of[threadIdx.x] = make_int3(word, have, at);
     }
-    // the table rows, a warp at a time: 32 rows of the warp one after the other
-    for (int i = 0; i < 32; ++i) {
-      const int bi = __shfl_sync(0xffffffffu, b, i);
-      const int wi = __shfl_sync(0xffffffffu, word, i), hi = __shfl_sync(0xffffffffu, have, i);
-      const int ai = __shfl_sync(0xffffffffu, at, i);
-      if (bi >= b1) break;
-      const bool swap = wi >= kReplace;
-      const int32_t* row = A.table + static_cast<int64_t>(bi) * A.max_pages;
-      int32_t* out = A.table_out + static_cast<int64_t>(bi) * A.max_pages;
+    __syncthreads();
+    for (int i = warp; i < min(b1 - c0, kPlanThreads); i += kPlanThreads / 32) {
+      const int3 r = rows_of[i];
+      const int swap = r.x >= kReplace;
+      const int32_t* row = A.table + static_cast<int64_t>(c0 + i) * A.max_pages;
+      int32_t* out = A.table_out + static_cast<int64_t>(c0 + i) * A.max_pages;
       if (A.table_out != A.table)
-        for (int j = lane; j < hi - swap; j += 32) out[j] = row[j];
-      for (int j = lane; j < (wi & ~kReplace) + swap; j += 32) out[hi - swap + j] = W.list[ai + j];
+        for (int j = lane; j < r.y - swap; j += 32) out[j] = row[j];
+      for (int j = lane; j < (r.x & ~kReplace) + swap; j += 32) out[r.y - swap + j] = W.list[r.z + j];
     }
   }
   released = block_sum(released, sh.warp_sums);
@@ -473,11 +542,13 @@ __global__ void __cluster_dims__(kPlanBlocks, 1, 1) __launch_bounds__(kPlanThrea
 
 // info of the workspace: [0] moves, [1] held pages
 __global__ void __cluster_dims__(kPlanBlocks, 1, 1) __launch_bounds__(kPlanThreads, 1)
-    compact_kernel(PageArgs A, PlanWs W, int32_t* n_live_out) {
+    compact_kernel(const __grid_constant__ PageArgs A, const __grid_constant__ PlanWs W,
+                   int32_t* n_live_out) {
   cg::cluster_group cl = cg::this_cluster();
   __shared__ PlanShared sh;
   const int rank = cl.block_rank();
   grid_launch_dependents();
+  grid_dependency_wait();
   const int span = (A.n_pages + kPlanBlocks - 1) / kPlanBlocks;
   const int p0 = min(rank * span, A.n_pages), p1 = min(p0 + span, A.n_pages);
   int live = 0;
@@ -537,13 +608,15 @@ __global__ void __cluster_dims__(kPlanBlocks, 1, 1) __launch_bounds__(kPlanThrea
 
 // ------------------------------------------------------------------ page copies
 // n tokens of one page of one layer, K or V, from page src to page dst, by
-// one block: vectors of 16 bytes, eight in flight per thread.
+// one block: vectors of 16 bytes, eight in flight per thread, neither side
+// kept in L1.
 constexpr int kCopyThreads = 256;
 
 __device__ __forceinline__ void copy_page(const Pools& P, int kv, int layer, int src, int dst, int n) {
   const uint4* from = P.p[kv] + layer * P.layer[kv] + src * P.page[kv];
   uint4* to = P.p[kv] + layer * P.layer[kv] + dst * P.page[kv];
   const int all = n * P.row;
+  const bool linear = P.linear[kv];
   constexpr int U = 8;
   for (int v0 = threadIdx.x; v0 < all; v0 += U * kCopyThreads) {
     uint4 x[U];
@@ -551,22 +624,22 @@ __device__ __forceinline__ void copy_page(const Pools& P, int kv, int layer, int
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int v = v0 + u * kCopyThreads;
-      at[u] = -1;
-      if (v < all) {
-        const int s = v / P.row, r = v - s * P.row;
-        const int h = r / P.chunks;
-        at[u] = s * P.slot[kv] + h * P.head[kv] + (r - h * P.chunks);
-        x[u] = from[at[u]];
+      at[u] = v;
+      if (!linear) {
+        const int s = P.by_row(v);
+        at[u] = s * P.slot[kv] + P.in_token(kv, v - s * P.row);
       }
+      if (v < all) x[u] = __ldcs(from + at[u]);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      if (at[u] >= 0) to[at[u]] = x[u];
+      if (v0 + u * kCopyThreads < all) __stcs(to + at[u], x[u]);
   }
 }
 
 __global__ void __launch_bounds__(kCopyThreads)
     reserve_copy_kernel(const __grid_constant__ Pools P, const int32_t* copy, int B, int layers) {
+  grid_launch_dependents();
   grid_dependency_wait();
   const int64_t items = static_cast<int64_t>(B) * layers * 2;
   for (int64_t i = blockIdx.x; i < items; i += gridDim.x) {
@@ -580,12 +653,13 @@ __global__ void __launch_bounds__(kCopyThreads)
 __global__ void __launch_bounds__(kCopyThreads)
     compact_copy_kernel(const __grid_constant__ Pools P, const __grid_constant__ PageArgs A,
                         const __grid_constant__ PlanWs W, int layers) {
+  grid_launch_dependents();
   grid_dependency_wait();
   const int moves = W.info[0], n_live = W.info[1];
   const int64_t items = static_cast<int64_t>(moves) * layers * 2;
   for (int64_t i = blockIdx.x; i < items; i += gridDim.x) {
     const int k = static_cast<int>(i / (layers * 2)), r = static_cast<int>(i % (layers * 2));
-    copy_page(P, r & 1, r >> 1, W.mover[k], W.list[k], P.page_size);
+    copy_page(P, r & 1, r >> 1, W.mover[k], W.list[k], P.page_size());
   }
   for (int b = blockIdx.x; b < A.B; b += gridDim.x) {
     int len;
@@ -643,16 +717,17 @@ fm_status fm_cache_append(const fm_cache* c, const void* k, const void* v, const
   A.tok[1] = v_stride[0] / 8; A.head[1] = v_stride[1] / 8;
   A.cu = cu; A.table = table; A.lens = lens; A.status = status;
   A.B = c->B; A.total = total; A.max_pages = c->max_pages; A.n_pages = c->n_pages;
-  // about four vectors per thread, and no fewer blocks than tokens allow
-  int tokens = 4 * kAppendThreads / (2 * P.row);
+  // the vectors that a block's threads hold, in more blocks where there are few
+  int tokens = kAppendVecs * kAppendThreads / (2 * P.row);
   if (tokens < 1) tokens = 1;
   while (tokens > 1 && ceil_div(total, tokens) < 2 * num_sms()) tokens = (tokens + 1) / 2;
   A.tokens = tokens;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   prof_begin(K_CACHE_APPEND, s);
-  append_kernel<<<ceil_div(total, tokens), kAppendThreads, tokens * sizeof(int64_t), s>>>(A, P);
+  const cudaError_t e = launch_dependent(append_kernel, dim3(ceil_div(total, tokens)), kAppendThreads,
+                                         tokens * sizeof(int64_t), s, A, P);
   prof_end(K_CACHE_APPEND, s);
-  return done(cudaGetLastError());
+  return done(e);
 }
 
 fm_status fm_cache_accept(const fm_cache* c, const int32_t* accept, int max_accept,
@@ -671,9 +746,11 @@ fm_status fm_cache_accept(const fm_cache* c, const int32_t* accept, int max_acce
                c->n_pages};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   prof_begin(K_CACHE_ACCEPT, s);
-  accept_kernel<<<dim3(ceil_div(2 * P.row, 256), c->B, c->layers), 256, 0, s>>>(A, P);
+  const cudaError_t e =
+      launch_dependent(accept_kernel, dim3(ceil_div(2 * P.row, kAcceptThreads), c->B, c->layers),
+                       kAcceptThreads, 0, s, A, P);
   prof_end(K_CACHE_ACCEPT, s);
-  return done(cudaGetLastError());
+  return done(e);
 }
 
 fm_status fm_pages_fork(const fm_cache* c, const int32_t* parent, const int32_t* table,
@@ -686,13 +763,16 @@ fm_status fm_pages_fork(const fm_cache* c, const int32_t* parent, const int32_t*
              c->max_pages};
   if (table_out == table || lens_out == lens || !outputs_apart(*c, A)) return FM_ERR_INVALID;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (ref_out != ref && cudaMemcpyAsync(ref_out, ref, c->n_pages * 4ull, cudaMemcpyDeviceToDevice,
-                                        s) != cudaSuccess)
-    return FM_ERR_CUDA;
   prof_begin(K_PAGES_FORK, s);
-  fork_kernel<<<ceil_div(c->B, 4), 128, 0, s>>>(A, parent);
+  cudaError_t e = cudaSuccess;
+  if (ref_out != ref) {
+    const int blocks = ceil_div(c->n_pages, 1024);
+    e = launch_dependent(ref_copy_kernel, dim3(blocks < 1024 ? blocks : 1024), 256, 0, s, ref, ref_out,
+                         c->n_pages);
+  }
+  if (e == cudaSuccess) e = launch_dependent(fork_kernel, dim3(ceil_div(c->B, 4)), 128, 0, s, A, parent);
   prof_end(K_PAGES_FORK, s);
-  return done(cudaGetLastError());
+  return done(e);
 }
 
 size_t fm_pages_workspace_size(const fm_cache* c) {
@@ -717,12 +797,12 @@ fm_status fm_pages_reserve(const fm_cache* c, const int32_t* grow, void* k_pool,
   if (ws_bytes < W.bytes) return FM_ERR_WORKSPACE;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   prof_begin(K_PAGES_PLAN, s);
-  reserve_kernel<<<kPlanBlocks, kPlanThreads, 0, s>>>(A, grow, W, info);
+  cudaError_t e = launch_dependent(reserve_kernel, dim3(kPlanBlocks), kPlanThreads, 0, s, A, grow, W, info);
   prof_end(K_PAGES_PLAN, s);
-  if (cudaGetLastError() != cudaSuccess) return FM_ERR_CUDA;
+  if (e != cudaSuccess) return FM_ERR_CUDA;
   const int64_t items = static_cast<int64_t>(c->B) * c->layers * 2;
   prof_begin(K_PAGES_COPY, s);
-  const cudaError_t e =
+  e =
       launch_dependent(reserve_copy_kernel, dim3(items < copy_grid() ? static_cast<int>(items) : copy_grid()),
                        kCopyThreads, 0, s, pools_of(*c, k_pool, v_pool), W.copy, c->B, c->layers);
   prof_end(K_PAGES_COPY, s);
@@ -745,11 +825,11 @@ fm_status fm_pages_compact(const fm_cache* c, void* k_pool, void* v_pool, const 
   if (ws_bytes < W.bytes) return FM_ERR_WORKSPACE;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   prof_begin(K_PAGES_PLAN, s);
-  compact_kernel<<<kPlanBlocks, kPlanThreads, 0, s>>>(A, W, n_live);
+  cudaError_t e = launch_dependent(compact_kernel, dim3(kPlanBlocks), kPlanThreads, 0, s, A, W, n_live);
   prof_end(K_PAGES_PLAN, s);
-  if (cudaGetLastError() != cudaSuccess) return FM_ERR_CUDA;
+  if (e != cudaSuccess) return FM_ERR_CUDA;
   prof_begin(K_PAGES_COPY, s);
-  const cudaError_t e = launch_dependent(compact_copy_kernel, dim3(copy_grid()), kCopyThreads, 0, s,
+  e = launch_dependent(compact_copy_kernel, dim3(copy_grid()), kCopyThreads, 0, s,
                                          pools_of(*c, k_pool, v_pool), A, W, c->layers);
   prof_end(K_PAGES_COPY, s);
   return done(e);

@@ -7,10 +7,14 @@
 namespace fm {
 
 constexpr int kMaxTokenIndex = 1 << 30;   // tokens of a row (32-bit positions)
-constexpr int kMaxPoolPages = 1 << 24;
+constexpr int kMaxPoolPages = (1 << 23) - 1;
 
 // Sizes of `c` that every cache entry point needs; `pools`: its pools' too.
 fm_status check_cache(const fm_cache* c, bool pools);
+
+inline int page_shift(int page_size) {
+  return page_size == 16 ? 4 : page_size == 32 ? 5 : page_size == 64 ? 6 : 7;
+}
 
 inline bool aligned_to(const void* p, uintptr_t n) {
   return p && (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0;
@@ -40,6 +44,21 @@ inline fm_status prepare_kernel(K* kern, int smem, int min_regs, std::atomic<uin
   done.fetch_or(bit, std::memory_order_release);
   return FM_OK;
 }
+
+// Division by a number that the host knows, of values below 2^31: one high
+// product, one add and one shift in place of some forty instructions.
+struct FastDiv {
+  uint32_t d, mul, shift;
+  static FastDiv of(uint32_t d) {
+    FastDiv f{d, 0, 0};
+    while ((1ull << f.shift) < d) ++f.shift;
+    f.mul = static_cast<uint32_t>(((1ull << f.shift) - d) * (1ull << 32) / d + 1);
+    return f;
+  }
+  __device__ __forceinline__ int operator()(int n) const {
+    return static_cast<int>((__umulhi(static_cast<uint32_t>(n), mul) + static_cast<uint32_t>(n)) >> shift);
+  }
+};
 
 // A launch that may start while the kernel before it in the stream still
 // runs (it calls grid_dependency_wait() before it touches memory).

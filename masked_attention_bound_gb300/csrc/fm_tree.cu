@@ -642,7 +642,7 @@ fm_status fm_tree_fwd(const fm_cache* c, const fm_tree_desc* t, const void* q, c
   TreeParams P{};
   P.B = c->B; P.H = t->H; P.Hkv = c->Hkv; P.G = t->H / c->Hkv;
   P.total = t->total; P.max_nodes = t->max_nodes;
-  P.page_shift = c->page_size == 16 ? 4 : c->page_size == 32 ? 5 : c->page_size == 64 ? 6 : 7;
+  P.page_shift = page_shift(c->page_size);
   P.n_pages = c->n_pages; P.max_pages = c->max_pages;
   P.by_G = FastDiv::of(P.G);
   P.by_grid = FastDiv::of(grid);

@@ -18,21 +18,6 @@
 
 namespace fm {
 
-// Division by a number that the host knows, of values below 2^31: one high
-// product, one add and one shift in place of some forty instructions.
-struct FastDiv {
-  uint32_t d, mul, shift;
-  static FastDiv of(uint32_t d) {
-    FastDiv f{d, 0, 0};
-    while ((1ull << f.shift) < d) ++f.shift;
-    f.mul = static_cast<uint32_t>(((1ull << f.shift) - d) * (1ull << 32) / d + 1);
-    return f;
-  }
-  __device__ __forceinline__ int operator()(int n) const {
-    return static_cast<int>((__umulhi(static_cast<uint32_t>(n), mul) + static_cast<uint32_t>(n)) >> shift);
-  }
-};
-
 struct TreeParams {
   int B, H, Hkv, G, total, max_nodes, page_shift, n_pages, max_pages;
   int tree;                // 0: chain (no parents)
