@@ -96,12 +96,7 @@ __global__ void __launch_bounds__(NarrowCfg<D>::THREADS, 1)
 
   // every lane gets the same answer
   auto wait_all = [&](uint32_t bar, uint32_t parity) -> bool {
-    bool ok = mbar_try_wait(bar, parity);
-    if (!ok && !abort_flag) {
-      ok = mbar_wait(bar, parity, P.status, P.wait_ns);
-      if (!ok) abort_flag = 1;
-    }
-    return __all_sync(0xffffffffu, ok);
+    return __all_sync(0xffffffffu, tree_wait(bar, parity, P, &abort_flag));
   };
 
   if (warp >= C::WARPS) {
@@ -118,6 +113,7 @@ __global__ void __launch_bounds__(NarrowCfg<D>::THREADS, 1)
     while (ok && walk.next(P, u)) {
       if (u.keys == 0) continue;
       int page = TileLoad<D>::lane_page(P, u, u.t0, lane);
+#pragma unroll 1
       for (int t = u.t0; t < u.t1; ++t) {
         const int next = t + 1 < u.t1 ? TileLoad<D>::lane_page(P, u, t + 1, lane) : 0;
         if (use > 0) ok = wait_all(empty(first + st), (use - 1) & 1);
@@ -133,6 +129,7 @@ __global__ void __launch_bounds__(NarrowCfg<D>::THREADS, 1)
     }
     // every issued copy has landed before the block may exit
     if (lane == 0)
+#pragma unroll 1
       for (int x = max(issued - stages, 0); x < issued; ++x)
         mbar_wait(full(first + x % stages), (x / stages) & 1, P.status, P.wait_ns);
     __syncwarp();
@@ -157,7 +154,16 @@ __global__ void __launch_bounds__(NarrowCfg<D>::THREADS, 1)
         uint32_t w[8];
         const int node = P.by_G(u.row_first + min(lane, u.rows - 1));
         if (P.tree) {
-          if (lane < R && u.s.base >= 0) tree_ancestors(P, u.s, node, w);
+          // at most 16 rows: lane l knows the parent of node l
+          const int mine = lane < u.s.n && u.s.base >= 0 ? tree_parent(P, u.s, lane) : -1;
+          int a = u.s.base >= 0 ? node : -1;
+#pragma unroll
+          for (int x = 0; x < 8; ++x) w[x] = 0;
+          while (__any_sync(0xffffffffu, a >= 0)) {
+            const int p = __shfl_sync(0xffffffffu, mine, a & 31);
+            if (a >= 0 && p != -2) w[0] |= 1u << a;
+            a = a < 0 || p == -2 ? -1 : p;   // a node drafted after a padding node is a root
+          }
         } else {
           const int upto = u.s.base + node - u.origin;   // 0 .. R - 1
 #pragma unroll
@@ -193,6 +199,7 @@ __global__ void __launch_bounds__(NarrowCfg<D>::THREADS, 1)
 #pragma unroll
         for (int y = 0; y < 4; ++y) acc[x][y] = 0.f;
 
+#pragma unroll 1
       for (int t = u.t0; u.keys > 0 && t < u.t1; ++t) {
         const int ks = e % C::KS, vs = e % C::VS;
         const uint32_t kp = (e / C::KS) & 1, vp = (e / C::VS) & 1;
@@ -283,6 +290,7 @@ __global__ void __launch_bounds__(NarrowCfg<D>::THREADS, 1)
             const int row = warp * 16 + (lane >> 1);
             const int key = k0 + (lane >> 1), j = key - u.origin;
             bool dirty = false;
+#pragma unroll 1
             for (int ch = (lane & 1) * (D / 16); ch < ((lane & 1) + 1) * (D / 16); ++ch) {
               const uint32_t at = (ch >> 3) * (kTile * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4);
               uint4* ptr = reinterpret_cast<uint4*>(smem + C::OFF_V + vs * C::TILE + at);
@@ -395,12 +403,8 @@ __global__ void __launch_bounds__(NarrowCfg<D>::THREADS, 1)
         for (int c = 0; c < CPT; ++c)
           v[c] = (merge[r * C::PITCH + c0 + c] + merge[(R + r) * C::PITCH + c0 + c]) +
                  (merge[(2 * R + r) * C::PITCH + c0 + c] + merge[(3 * R + r) * C::PITCH + c0 + c]);
-        uint32_t any = 0;
-#pragma unroll
-        for (int x = 0; x < 8; ++x) any |= nf[x];
-        if (any && r < u.rows)
-#pragma unroll
-          for (int c = 0; c < CPT; ++c) v[c] = fix_value(P, u, nf, seen + r * 8, c0 + c, v[c]);
+        const uint4 n0 = reinterpret_cast<const uint4*>(nf)[0], n1 = reinterpret_cast<const uint4*>(nf)[1];
+        const bool any = (n0.x | n0.y | n0.z | n0.w | n1.x | n1.y | n1.z | n1.w) != 0;
         if (r < u.rows) {
           if (u.whole()) {
             const int rr = u.row_first + r, node = P.by_G(rr), h = u.hk * P.G + rr - node * P.G;
@@ -416,6 +420,7 @@ __global__ void __launch_bounds__(NarrowCfg<D>::THREADS, 1)
               *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
             else
               *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+            if (any) fix_row(P, u, nf, seen + r * 8, 0, CPT, c0, dst);
             if (c0 == 0)
               P.lse[static_cast<int64_t>(h) * P.total + u.s.row0 + node] =
                   ll > 0.f || ll != ll ? (mm + __log2f(ll)) * 0.69314718055994530942f : -INFINITY;
@@ -426,6 +431,7 @@ __global__ void __launch_bounds__(NarrowCfg<D>::THREADS, 1)
 #pragma unroll
             for (int c = 0; c < CPT / 4; ++c)
               dst[c] = make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+            if (any) fix_row(P, u, nf, seen + r * 8, 0, CPT, c0, P.part_o + at * D + c0);
             if (c0 == 0) P.part_ml[at] = make_float2(mm, ll);
           }
         }
@@ -664,7 +670,7 @@ fm_status fm_tree_fwd(const fm_cache* c, const fm_tree_desc* t, const void* q, c
   P.part_o = reinterpret_cast<float*>(w + W.o);
   P.status = status;
   const TestHooks th = test_hooks();
-  P.wait_ns = th.wait_ns;
+  P.wait_ns = th.wait_ns < 4000000000ull ? static_cast<uint32_t>(th.wait_ns) : 4000000000u;
   P.withhold = th.withhold;
   // one page of one head is a box: page_size rows of 64 columns
   CUtensorMap tk, tv;

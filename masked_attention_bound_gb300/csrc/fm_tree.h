@@ -36,7 +36,7 @@ struct TreeParams {
   float2* part_ml;         // [2 * grid][part_rows] running max (base-2 exponent) and sum
   float* part_o;           // [2 * grid][part_rows][D]
   int* status;
-  uint64_t wait_ns;
+  uint32_t wait_ns;        // limit of every mbarrier wait
   int withhold;
 };
 
@@ -88,6 +88,7 @@ template <int R>
 __device__ __forceinline__ uint32_t seq_tiles(const TreeParams& P, const TreeSeq& s) {
   const int nr = row_tiles<R>(P, s);
   uint32_t w = 0;
+#pragma unroll 1
   for (int rt = 0; rt < nr; ++rt) w += key_tiles(unit_keys<R>(P, s, rt));
   return w;
 }
@@ -123,7 +124,7 @@ __device__ __forceinline__ TreeRun tree_run(const TreeParams& P) {
   const int b0 = lane * m, b1 = min(b0 + m, P.B);
   TreeSeq s{0, 0, 0};
   uint32_t w = 0;
-#pragma unroll 4
+#pragma unroll 1
   for (int b = b0; b < b1; ++b) {
     s = tree_seq(P, b);
     if (s.base < 0 && blockIdx.x == 0 && P.status) atomicOr(P.status, DEV_CACHE);
@@ -149,6 +150,7 @@ __device__ __forceinline__ TreeRun tree_run(const TreeParams& P) {
   if (lane == from) {
     uint32_t off = begin - (inc - w), per = 0;
     int b = b0;
+#pragma unroll 1
     for (;; ++b) {
       if (m > 1) s = tree_seq(P, b);
       per = seq_tiles<R>(P, s);
@@ -158,6 +160,7 @@ __device__ __forceinline__ TreeRun tree_run(const TreeParams& P) {
     run.b = b;
     run.hk = off / per;
     off -= run.hk * per;
+#pragma unroll 1
     while (true) {
       const uint32_t t = key_tiles(unit_keys<R>(P, s, run.rt));
       if (off < t) break;
@@ -195,6 +198,7 @@ struct TreeWalk {
     if (run.left <= 0) return false;
     TreeSeq& s = run.s;
     // on to the next sequence with rows
+#pragma unroll 1
     while (run.hk >= P.Hkv || s.n <= 0) {
       run.hk = run.rt = run.tile = 0;
       if (++run.b >= P.B) return false;
@@ -232,20 +236,48 @@ __device__ __forceinline__ int tree_parent(const TreeParams& P, const TreeSeq& s
   return -1;
 }
 
-// Ancestors of node t and itself as bits [0, 256) of w (all 0 for padding).
-__device__ __forceinline__ void tree_ancestors(const TreeParams& P, const TreeSeq& s, int t,
-                                               uint32_t (&w)[8]) {
+// Ancestors of node t and itself as bits [0, 256) of w (all 0 for padding);
+// parent(a): tree_parent of node a.
+template <typename F>
+__device__ __forceinline__ void tree_ancestors(int t, F parent, uint32_t (&w)[8]) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) w[i] = 0;
-  int a = t;
-  if (tree_parent(P, s, t) == -2) return;
-  while (a >= 0) {
-    const int p = tree_parent(P, s, a);
+#pragma unroll 1
+  for (int a = t; a >= 0;) {
+    const int p = parent(a);
     if (p == -2) break;      // a node drafted after a padding node is a root
 #pragma unroll
     for (int i = 0; i < 8; ++i) w[i] |= (a >> 5) == i ? 1u << (a & 31) : 0u;
     a = p;
   }
+}
+
+// ---------------------------------------------------------------- waits
+// Code that a block runs once costs its instruction fetches, which queue
+// behind the K/V stream in L2: the first version of the wide kernel (149 KB,
+// rare paths unrolled everywhere) spent 21000 cycles on its first masked tile
+// and 10000 on writing O.  So the rare paths are kept small: short waits,
+// loops that are not unrolled.
+__device__ __forceinline__ uint32_t globaltimer_lo() {
+  uint32_t t;
+  asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+  return t;
+}
+// mbar_wait with the limit in 32 bits; false (with the status and the abort
+// flag set) when it runs out, or when another warp's did.
+__device__ __forceinline__ bool tree_wait(uint32_t bar, uint32_t parity, const TreeParams& P,
+                                          volatile int* abort_flag) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint32_t t0 = globaltimer_lo();
+  while (!mbar_try_wait(bar, parity)) {
+    if (*abort_flag) return false;
+    if (globaltimer_lo() - t0 > P.wait_ns) {
+      if (P.status) atomicOr(P.status, DEV_TIMEOUT);
+      *abort_flag = 1;
+      return false;
+    }
+  }
+  return true;
 }
 
 // ---------------------------------------------------------------- K/V loads
@@ -311,8 +343,10 @@ constexpr int kNarrowRows = 16, kWideRows = 256;
 __device__ __forceinline__ float fix_value(const TreeParams& P, const TreePiece& u,
                                            const uint32_t* nf, const uint32_t* seen, int c,
                                            float x) {
+#pragma unroll 1
   for (int w = 0; w < 8; ++w) {
     uint32_t bits = nf[w] & seen[w];
+#pragma unroll 1
     while (bits) {
       const int i = w * 32 + __ffs(bits) - 1;
       bits &= bits - 1;
@@ -328,14 +362,16 @@ __device__ __forceinline__ float fix_value(const TreeParams& P, const TreePiece&
   return x;
 }
 
-// fix_value over columns [c0, c1) of a row that has been written (bf16 or fp32).
+// fix_value over n elements of a row that has been written (bf16 or fp32):
+// row[i] holds column c0 + i.
 template <typename T>
-__device__ __noinline__ void fix_row(const TreeParams& P, const TreePiece& u, const uint32_t* nf,
-                                     const uint32_t* seen, int c0, int c1, T* row) {
-  for (int c = c0; c < c1; ++c) {
-    const float x = static_cast<float>(row[c]);
-    const float y = fix_value(P, u, nf, seen, c, x);
-    if (!(x == y)) row[c] = static_cast<T>(y);
+static __device__ __noinline__ void fix_row(const TreeParams& P, const TreePiece& u, const uint32_t* nf,
+                                            const uint32_t* seen, int i0, int n, int c0, T* row) {
+#pragma unroll 1
+  for (int i = i0; i < n; ++i) {
+    const float x = static_cast<float>(row[i]);
+    const float y = fix_value(P, u, nf, seen, c0 + i, x);
+    if (!(x == y)) row[i] = static_cast<T>(y);
   }
 }
 

@@ -34,7 +34,8 @@ struct WideCfg {
   static constexpr int OFF_BAR = OFF_NF + 64;
   static constexpr int NBAR = 24;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;   // abort flag, TMEM address
-  static constexpr int USED = OFF_MISC + 16;
+  static constexpr int OFF_PAR = OFF_MISC + 16;         // int16 [256] parents of the unit's nodes
+  static constexpr int USED = OFF_PAR + 512;
   // one block per SM: it takes all of the tensor memory
   static constexpr int SMEM = USED > 120 * 1024 ? USED : 120 * 1024;
   static constexpr int THREADS = 384;
@@ -134,18 +135,10 @@ __global__ void __launch_bounds__(WideCfg<D>::THREADS, 1)
   tc_fence_after();
   const uint32_t tbase = *tmem_slot;
 
-  auto wait = [&](int b, uint32_t parity) -> bool {
-    if (mbar_try_wait(bar(b), parity)) return true;
-    if (*abort_flag) return false;
-    if (!mbar_wait(bar(b), parity, P.status, P.wait_ns)) {
-      *abort_flag = 1;
-      return false;
-    }
-    return true;
-  };
+  auto wait = [&](int b, uint32_t parity) -> bool { return tree_wait(bar(b), parity, P, abort_flag); };
+  // every lane gets the same answer
   auto wait_all = [&](int b, uint32_t parity) -> bool {
-    const bool ok = wait(b, parity);
-    return __all_sync(0xffffffffu, ok);
+    return __all_sync(0xffffffffu, wait(b, parity));
   };
 
   if (warp >= 8) {
@@ -163,6 +156,7 @@ __global__ void __launch_bounds__(WideCfg<D>::THREADS, 1)
       while (ok && walk.next(P, u)) {
         if (u.keys == 0) continue;
         int page = TileLoad<D>::lane_page(P, u, u.t0, lane);
+#pragma unroll 1
         for (int t = u.t0; t < u.t1; ++t) {
           const int next = t + 1 < u.t1 ? TileLoad<D>::lane_page(P, u, t + 1, lane) : 0;
           if (use > 0) ok = wait_all(b_empty + st, (use - 1) & 1);
@@ -178,6 +172,7 @@ __global__ void __launch_bounds__(WideCfg<D>::THREADS, 1)
       }
       // every issued copy has landed before the block may exit
       if (lane == 0)
+#pragma unroll 1
         for (uint32_t x = issued > stages ? issued - stages : 0; x < issued; ++x)
           mbar_wait(bar(b_full + x % stages), (x / stages) & 1, P.status, P.wait_ns);
       __syncwarp();
@@ -219,6 +214,7 @@ __global__ void __launch_bounds__(WideCfg<D>::THREADS, 1)
           ++qn;
         }
         int x = x0;
+#pragma unroll 1
         for (int i = 0; ok && i < turns; ++i) {
           // PV of the slot's tile x - step, then S of its tile x, which
           // overwrites that P: MMAs run in the order in which a thread issues them
@@ -327,7 +323,14 @@ __global__ void __launch_bounds__(WideCfg<D>::THREADS, 1)
 #pragma unroll
         for (int x = 0; x < 8; ++x) seen[x] = 0;
         if (mine) live = tree_parent(P, u.s, node) != -2;
-        if (live && u.t1 > part0) tree_ancestors(P, u.s, node, seen);
+        if (u.t1 > part0) {
+          // the walks up the tree read shared memory: a parent from L2 took
+          // 700 cycles a step
+          int16_t* par = reinterpret_cast<int16_t*>(smem + C::OFF_PAR);
+          if (tid < u.s.n) par[tid] = static_cast<int16_t>(tree_parent(P, u.s, tid));
+          slots_sync();
+          if (live) tree_ancestors(node, [&](int a) -> int { return par[a]; }, seen);
+        }
       }
       const bool warp_live = __any_sync(0xffffffffu, live);
       float m_used = -INFINITY, l = 0.f;
@@ -340,7 +343,7 @@ __global__ void __launch_bounds__(WideCfg<D>::THREADS, 1)
             P.q + (u.s.row0 + node) * P.q_stride[0] + static_cast<int64_t>(h) * P.q_stride[1];
         constexpr int LPR = D / 8, RPI = 32 / LPR;     // lanes a row, rows an instruction
         const unsigned in_rows = __ballot_sync(0xffffffffu, mine);
-#pragma unroll
+#pragma unroll 2
         for (int i = 0; i < 32 / RPI; ++i) {
           const int from = i * RPI + lane / LPR;
           const uint64_t row = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(src), from);
@@ -352,22 +355,21 @@ __global__ void __launch_bounds__(WideCfg<D>::THREADS, 1)
         fence_proxy_async_smem();
         mbar_arrive_warp(bar(W_QFULL + slot));
         int done = 0;
+#pragma unroll 1
         for (int x0 = w.rows ? 0 : slot; x0 < w.n; x0 += w.rows ? 1 : 2) {
           const int t = u.t0 + x0;
           const bool partial = t >= part0;
           if (ok) ok = wait_all(W_SFULL + slot, j & 1);
           tc_fence_after();
           if (ok && warp_live) {
-            float sv[128];
-            uint32_t* raw = reinterpret_cast<uint32_t*>(sv);
-#pragma unroll
-            for (int y = 0; y < 4; ++y) tmem_ld32(tS + 32 * y, raw + 32 * y);
-            uint32_t vis[4];
             if (partial) {
-              // the row's 128 visibility bits of this tile
-#pragma unroll
+              // what the row does not see becomes -inf, 32 columns at a time
+              // and back to tensor memory: a few tiles of a unit at most, and
+              // the loop below stays free of it
+#pragma unroll 1
               for (int y = 0; y < 4; ++y) {
                 const int j0 = t * kTile + 32 * y - u.origin;   // bit 0 is key origin + j0
+                uint32_t vis;
                 if (P.tree) {
                   // the 64 bits from word (j0 >> 5) on, ones before bit 0
                   const int i0 = j0 >> 5;
@@ -377,18 +379,25 @@ __global__ void __launch_bounds__(WideCfg<D>::THREADS, 1)
                     lo = i == i0 ? seen[i] : lo;
                     hi = i == i0 + 1 ? seen[i] : hi;
                   }
-                  vis[y] = __funnelshift_r(lo, hi, j0 & 31);
+                  vis = __funnelshift_r(lo, hi, j0 & 31);
                 } else {
                   const int upto = u.s.base + node - u.origin - j0;   // last visible bit
-                  vis[y] = upto >= 31 ? 0xffffffffu : (upto < 0 ? 0u : (2u << upto) - 1u);
+                  vis = upto >= 31 ? 0xffffffffu : (upto < 0 ? 0u : (2u << upto) - 1u);
                 }
-              }
-            }
-            tmem_wait_ld();
-            if (partial) {
+                uint32_t q[32];
+                tmem_ld32(tS + 32 * y, q);
+                tmem_wait_ld();
 #pragma unroll
-              for (int c = 0; c < 128; ++c) sv[c] = ((vis[c >> 5] >> (c & 31)) & 1u) ? sv[c] : -INFINITY;
+                for (int c = 0; c < 32; ++c) q[c] = (vis >> c) & 1u ? q[c] : 0xff800000u;
+                tmem_st32(tS + 32 * y, q);
+              }
+              tmem_wait_st();
             }
+            float sv[128];
+            uint32_t* raw = reinterpret_cast<uint32_t*>(sv);
+#pragma unroll
+            for (int y = 0; y < 4; ++y) tmem_ld32(tS + 32 * y, raw + 32 * y);
+            tmem_wait_ld();
             float mx8[8];
 #pragma unroll
             for (int y = 0; y < 8; ++y) mx8[y] = fmax3(sv[y], sv[y + 8], sv[y + 16]);
@@ -444,17 +453,20 @@ __global__ void __launch_bounds__(WideCfg<D>::THREADS, 1)
             ok = wait_all(W_VFULL + st, (e / C::VSTAGES) & 1);
             if (ok) {
               const int key = t * kTile + r, i = key - u.origin;
+              // 16-byte words of the row, the slabs 16 KB apart; the lanes
+              // start at different words (bank conflicts)
               uint8_t* v = smem + C::OFF_V + st * C::TILE + r * 128;
+              auto word = [&](int c) {
+                return reinterpret_cast<uint4*>(v + (c >> 3) * (kTile * 128) + ((c ^ r) & 7) * 16);
+              };
               bool dirty = false;
               if (key >= u.keys) {
-#pragma unroll
-                for (int c = 0; c < D / 8; ++c)
-                  *reinterpret_cast<uint4*>(v + (c >> 3) * (kTile * 128) + (c & 7) * 16) =
-                      make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll 1
+                for (int c = 0; c < D / 8; ++c) *word(c) = make_uint4(0u, 0u, 0u, 0u);
               } else if (i >= 0) {
-#pragma unroll
+#pragma unroll 4
                 for (int c = 0; c < D / 8; ++c) {
-                  const uint4 y = *reinterpret_cast<uint4*>(v + (c >> 3) * (kTile * 128) + (c & 7) * 16);
+                  const uint4 y = *word(c);
                   dirty |= bf16x2_not_finite(y.x) || bf16x2_not_finite(y.y) || bf16x2_not_finite(y.z) ||
                            bf16x2_not_finite(y.w);
                 }
@@ -463,8 +475,9 @@ __global__ void __launch_bounds__(WideCfg<D>::THREADS, 1)
                 // the flag first: whoever finds the row clean finds the flag
                 atomicOr(nf + (i >> 5), 1u << (i & 31));
                 __threadfence_block();
+#pragma unroll 1
                 for (int c = 0; c < D / 8; ++c) {
-                  uint4* y = reinterpret_cast<uint4*>(v + (c >> 3) * (kTile * 128) + (c & 7) * 16);
+                  uint4* y = word(c);
                   *y = make_uint4(bf16x2_clean(y->x), bf16x2_clean(y->y), bf16x2_clean(y->z),
                                   bf16x2_clean(y->w));
                 }
@@ -514,9 +527,8 @@ __global__ void __launch_bounds__(WideCfg<D>::THREADS, 1)
       // runs of a row: 64 bytes (bf16) or 128 bytes (fp32 parts)
       uint8_t* stage = smem + C::OFF_Q + slot * C::TILE + quarter * 32 * (D * 2);
       const unsigned out_rows = __ballot_sync(0xffffffffu, writes);
-#pragma unroll
-      for (int cb = 0; cb < D / 32; ++cb) {
-        if (cb * 32 < c0 || cb * 32 >= c1) continue;
+#pragma unroll 1
+      for (int cb = c0 / 32; cb < c1 / 32; ++cb) {
         float v[32];
         uint32_t* raw = reinterpret_cast<uint32_t*>(v);
         if (ok) {
@@ -598,8 +610,8 @@ __global__ void __launch_bounds__(WideCfg<D>::THREADS, 1)
             see[x] = P.tree ? seen[x]
                             : (upto >= 31 ? 0xffffffffu : (upto < 0 ? 0u : (2u << upto) - 1u));
           }
-          if (whole) fix_row(P, u, nf, see, c0, c1, orow);
-          else fix_row(P, u, nf, see, c0, c1, prow);
+          if (whole) fix_row(P, u, nf, see, c0, c1, 0, orow);
+          else fix_row(P, u, nf, see, c0, c1, 0, prow);
         }
       }
       if (!whole) {
