@@ -176,16 +176,18 @@ __global__ void __launch_bounds__(WideCfg<D>::THREADS, 1)
         for (uint32_t x = issued > stages ? issued - stages : 0; x < issued; ++x)
           mbar_wait(bar(b_full + x % stages), (x / stages) & 1, P.status, P.wait_ns);
       __syncwarp();
-    } else if (lane == 0) {
+    } else {
       // ---------------------------------------------------------- MMA issuers
-      const int s = warp == MMA_WARP ? 0 : 1;
+      // The whole warp walks and waits, and one elected lane issues: the
+      // descriptors are then uniform, and an MMA costs its issue only.
+      const int s = warp - MMA_WARP >> 1;
       constexpr uint32_t idS = idesc_bf16(128, 128, false, false);
       constexpr uint32_t idPV = idesc_bf16(128, D, false, true);
       const uint32_t dQ = sdesc_lo(sbase + C::OFF_Q + s * C::TILE, 16);
       const uint32_t dK0 = sdesc_lo(sbase + C::OFF_K, 16);
       const uint32_t dV0 = sdesc_lo(sbase + C::OFF_V, kTile * 128);
       const uint32_t tS = tbase + 128 * s, tO = tbase + 256 + 128 * s;
-      uint32_t e0 = 0;          // tiles before this piece
+      uint32_t kst = 0, kph = 0, vst = 0, vph = 0;   // stages and phases of the next tile of the block
       uint32_t pieces = 0;      // pieces with keys before this one
       uint32_t qn = 0, np = 0;  // Q tiles, P tiles of this slot so far
       uint32_t turn = 0;        // turns taken
@@ -194,23 +196,34 @@ __global__ void __launch_bounds__(WideCfg<D>::THREADS, 1)
       while (ok && walk.next(P, u)) {
         const WideSplit w = wide_split(u);
         if (w.n == 0) continue;
-        // The two MMA threads take turns: a turn is one tile's PV and the next
+        // The two MMA warps take turns: a turn is one tile's PV and the next
         // one's S.  Without it the slots fall into step (both wait for the
         // same K, then both softmaxes run, then both slots' MMAs share the
         // tensor pipe: 4900 cycles a pair of tiles); with turns one slot's
         // MMAs run while the other's softmax does.
         auto my_turn = [&]() -> bool {
-          return s == 0 ? (turn == 0 || wait(W_TURN + 1, (turn - 1) & 1)) : wait(W_TURN, turn & 1);
+          return s == 0 ? (turn == 0 || wait_all(W_TURN + 1, (turn - 1) & 1)) : wait_all(W_TURN, turn & 1);
         };
         auto end_turn = [&]() {
-          mbar_arrive(bar(W_TURN + s));
+          if (elect_one()) mbar_arrive(bar(W_TURN + s));
           ++turn;
         };
+        // stages advance by the piece's tiles; the slot's own tiles are every
+        // first or every second one
         const int step = w.rows ? 1 : 2, x0 = w.rows ? 0 : s;
         const int turns = (w.rows ? w.n : (w.n + 1) / 2) + 1;   // of either slot
-        const bool active = w.active(s);
-        if (active) {
-          ok = wait(W_QFULL + s, qn & 1);
+        auto advance = [](uint32_t& st, uint32_t& ph, int by, int stages) {
+          st += by;
+          while (st >= stages) {
+            st -= stages;
+            ph ^= 1;
+          }
+        };
+        uint32_t ks = kst, kp = kph, vs = vst, vp = vph;        // of tiles x (K) and x - step (V)
+        advance(ks, kp, x0, C::KSTAGES);
+        advance(vs, vp, x0, C::VSTAGES);
+        if (w.active(s)) {
+          ok = wait_all(W_QFULL + s, qn & 1);
           ++qn;
         }
         int x = x0;
@@ -218,64 +231,72 @@ __global__ void __launch_bounds__(WideCfg<D>::THREADS, 1)
         for (int i = 0; ok && i < turns; ++i) {
           // PV of the slot's tile x - step, then S of its tile x, which
           // overwrites that P: MMAs run in the order in which a thread issues them
-          const int xp = x - step;
-          const bool pv = i > 0 && xp < w.n, sn = x < w.n;
-          const uint32_t ep = e0 + xp, e = e0 + x;
-          const uint32_t vst = ep % C::VSTAGES, kst = e % C::KSTAGES;
+          const bool pv = i > 0 && x - step < w.n, sn = x < w.n;
           // P comes last: what else the turn needs is known by then, and the
           // product starts as soon as P is there
-          bool kready = false;
+          bool kready = true;
           if (pv) {
-            ok = wait(W_VFULL + vst, (ep / C::VSTAGES) & 1);
+            ok = wait_all(W_VFULL + vs, vp);
             // O of the slot is overwritten: the last piece's must have been read
-            if (ok && i == 1 && pieces > 0) ok = wait(W_OEMPTY + s, (pieces - 1) & 1);
+            if (ok && i == 1 && pieces > 0) ok = wait_all(W_OEMPTY + s, (pieces - 1) & 1);
             if (ok) ok = my_turn();
-            if (sn) kready = mbar_try_wait(bar(W_KFULL + kst), (e / C::KSTAGES) & 1);
-            if (ok) ok = wait(W_PFULL + s, np & 1);
+            if (sn) kready = __all_sync(0xffffffffu, mbar_try_wait(bar(W_KFULL + ks), kp));
+            if (ok) ok = wait_all(W_PFULL + s, np & 1);
             ++np;
           } else {
-            if (sn) ok = wait(W_KFULL + kst, (e / C::KSTAGES) & 1);
-            kready = true;
+            if (sn) ok = wait_all(W_KFULL + ks, kp);
             if (ok) ok = my_turn();
           }
           if (!ok) break;
           tc_fence_after();
           if (pv) {
-            const uint32_t dV = dV0 + vst * (C::TILE >> 4);
+            const uint32_t dV = dV0 + vs * (C::TILE >> 4);
+            if (elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < kTile / 16; ++kk)
-              mma_ts(tO, tS + kk * 8, sdesc_at(dV, kk * 2048), idPV, (i > 1 || kk > 0) ? 1u : 0u);
-            if (!sn) mma_commit(bar(W_PVDONE + s));
-            mma_commit(bar(W_VEMPTY + vst));
-            if (!w.rows) mma_commit(bar(W_VEMPTY + vst));
+              for (int kk = 0; kk < kTile / 16; ++kk)
+                mma_ts(tO, tS + kk * 8, sdesc_at(dV, kk * 2048), idPV, (i > 1 || kk > 0) ? 1u : 0u);
+              if (!sn) mma_commit(bar(W_PVDONE + s));
+              mma_commit(bar(W_VEMPTY + vs));
+              if (!w.rows) mma_commit(bar(W_VEMPTY + vs));
+            }
+            __syncwarp();
+            advance(vs, vp, step, C::VSTAGES);
           }
           bool given = false;
           if (sn) {
-            if (!kready && !mbar_try_wait(bar(W_KFULL + kst), (e / C::KSTAGES) & 1)) {
+            if (!kready) kready = __all_sync(0xffffffffu, mbar_try_wait(bar(W_KFULL + ks), kp));
+            if (!kready) {
               end_turn();        // K has not landed: the other slot need not wait for it
               given = true;
-              ok = wait(W_KFULL + kst, (e / C::KSTAGES) & 1);
+              ok = wait_all(W_KFULL + ks, kp);
               if (!ok) break;
               tc_fence_after();
             }
-            const uint32_t dK = dK0 + kst * (C::TILE >> 4);
+            const uint32_t dK = dK0 + ks * (C::TILE >> 4);
+            if (elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              const uint32_t off = (kk >> 2) * (kTile * 128) + (kk & 3) * 32;
-              mma_ss(tS, sdesc_at(dQ, off), sdesc_at(dK, off), idS, kk > 0 ? 1u : 0u);
+              for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t off = (kk >> 2) * (kTile * 128) + (kk & 3) * 32;
+                mma_ss(tS, sdesc_at(dQ, off), sdesc_at(dK, off), idS, kk > 0 ? 1u : 0u);
+              }
+              mma_commit(bar(W_SFULL + s));
+              mma_commit(bar(W_KEMPTY + ks));
+              if (!w.rows) mma_commit(bar(W_KEMPTY + ks));
             }
-            mma_commit(bar(W_SFULL + s));
-            mma_commit(bar(W_KEMPTY + kst));
-            if (!w.rows) mma_commit(bar(W_KEMPTY + kst));
+            __syncwarp();
+            advance(ks, kp, step, C::KSTAGES);
           }
           if (!given) end_turn();
           x += step;
         }
-        e0 += w.n;
+        advance(kst, kph, w.n % (2 * C::KSTAGES), C::KSTAGES);
+        advance(vst, vph, w.n % (2 * C::VSTAGES), C::VSTAGES);
         ++pieces;
       }
-      mma_commit(bar(W_DRAIN));
-      mbar_wait(bar(W_DRAIN), 0, P.status, P.wait_ns);
+      if (elect_one()) {
+        mma_commit(bar(W_DRAIN));
+        mbar_wait(bar(W_DRAIN), 0, P.status, P.wait_ns);
+      }
     }
     __syncwarp();
   } else {
