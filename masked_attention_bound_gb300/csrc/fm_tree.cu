@@ -75,7 +75,7 @@ __global__ void __launch_bounds__(NarrowCfg<D>::THREADS, 1)
   auto full = [&](int i) { return bar0 + 8u * i; };                      // K stages, then V's
   auto empty = [&](int i) { return bar0 + 8u * (C::KS + C::VS + i); };
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (warp == 2) touch_inputs(P, lane);
+  if (warp == 2) touch_memory<D>(P, lane);
   if (tid == 0) {
     for (int i = 0; i < C::KS + C::VS; ++i) {
       mbar_init(full(i), 1);
@@ -639,10 +639,10 @@ fm_status fm_tree_fwd(const fm_cache* c, const fm_tree_desc* t, const void* q, c
   const int grid = num_sms();
   const TreeWs W = tree_ws(*c, *t, grid);
   if (!aligned_to(ws, 256) || ws_bytes < W.bytes) return FM_ERR_WORKSPACE;
-  // the tiles of all units (an upper bound) are counted in 31 bits
+  // the length of the line of units (an upper bound) is counted in 31 bits
   const double units = static_cast<double>(c->Hkv) *
                        (static_cast<double>(t->total) * (t->H / c->Hkv) / kNarrowRows + c->B);
-  if (units * (static_cast<double>(c->max_pages) * c->page_size / kTile + 1) >= 2147483647.0)
+  if (units * (static_cast<double>(c->max_pages) * c->page_size / kTile + 5) >= 2147483647.0)
     return FM_ERR_UNSUPPORTED;
   char* w = static_cast<char*>(ws);
   TreeParams P{};

@@ -4,9 +4,10 @@
 // tile): up to R rows, row r of a sequence being node r / G of query head hk *
 // G + r % G, so the G query heads that share a K/V head share its loads.  A
 // unit walks the 128-key tiles [0, tiles) of its sequence up to its last
-// node.  All tiles of all units, in order, form one line; each block takes an
-// equal run of it, whatever the lengths, so one long sequence keeps every SM
-// busy and a full batch is balanced.  Where a run ends inside a unit, each
+// node.  All units, in order, form one line on which a unit is as long as its
+// tiles and its fixed cost (writing its rows, fetching the next one's; END
+// tiles); each block takes an equal run of it, whatever the lengths, so one
+// long sequence keeps every SM busy and a full batch is balanced.  Where a run ends inside a unit, each
 // block leaves its unnormalised part (running max, sum, O) in the workspace
 // and tree_join_kernel adds the parts in ascending order.
 #pragma once
@@ -82,30 +83,43 @@ __device__ __forceinline__ int unit_keys(const TreeParams& P, const TreeSeq& s, 
 __device__ __forceinline__ int key_tiles(int keys) {
   return keys > 0 ? (keys + kTile - 1) / kTile : 1;
 }
-// Tiles of all units of one K/V head of a sequence.  (The launch checks that
-// the tiles of all units fit in 31 bits.)
+// A unit's length on the line.  Its fixed cost in tiles, measured: 4 for the
+// wide kernel (a block with a unit's end in its run took 12000 to 14000
+// cycles longer, a tile of 256 rows takes 3600 and one of 128 rows 2800), 1
+// for the narrow one.
 template <int R>
-__device__ __forceinline__ uint32_t seq_tiles(const TreeParams& P, const TreeSeq& s) {
+__device__ __forceinline__ int unit_length(int tiles) {
+  return tiles + (R > 16 ? 4 : 1);
+}
+// Length of all units of one K/V head of a sequence.  (The launch checks that
+// the line's length fits in 31 bits.)
+template <int R>
+__device__ __forceinline__ uint32_t seq_length(const TreeParams& P, const TreeSeq& s) {
   const int nr = row_tiles<R>(P, s);
   uint32_t w = 0;
 #pragma unroll 1
-  for (int rt = 0; rt < nr; ++rt) w += key_tiles(unit_keys<R>(P, s, rt));
+  for (int rt = 0; rt < nr; ++rt) w += unit_length<R>(key_tiles(unit_keys<R>(P, s, rt)));
   return w;
 }
 
 // The first touch of a memory page by an SM costs 2 to 3 us (address
-// translation): the small inputs are touched at once, while the block sets up
-// (lens and cu, then the table, then K and V would each wait for it in turn).
-__device__ __forceinline__ void touch_inputs(const TreeParams& P, int lane) {
-  const void* p = lane == 0 ? static_cast<const void*>(P.lens)
-                            : (lane == 1 ? static_cast<const void*>(P.cu)
-                                         : (lane == 2 ? static_cast<const void*>(P.table)
-                                                      : (lane == 3 ? static_cast<const void*>(P.q)
-                                                                   : static_cast<const void*>(P.parents))));
-  if (lane < 4 || (lane == 4 && P.tree)) asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+// translation, behind the K/V stream): the small inputs and this block's
+// places in the workspace are touched at once, while the block sets up.
+__device__ __forceinline__ void touch(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+template <int D>
+__device__ __forceinline__ void touch_memory(const TreeParams& P, int lane) {
+  const int64_t part = 2 * static_cast<int64_t>(blockIdx.x) * P.part_rows;
+  if (lane == 0) touch(P.lens);
+  if (lane == 1) touch(P.cu);
+  if (lane == 2) touch(P.table);
+  if (lane == 3) touch(P.q);
+  if (lane == 4 && P.tree) touch(P.parents);
+  if (lane == 5) touch(P.part_o + part * D);
+  if (lane == 6) touch(P.part_o + (part + P.part_rows) * D);
+  if (lane == 7) touch(P.part_ml + part);
 }
 
-// A block's run: the place of its first tile, and its tiles.
+// A block's run: the place where it starts, and its length.
 struct TreeRun {
   int b, hk, rt, tile, left;
   TreeSeq s;          // sequence b
@@ -113,9 +127,9 @@ struct TreeRun {
 
 // Every warp of the block finds the run by itself (no shared memory and no
 // barrier: the start of the kernel is on the path of every call).  Lane l
-// adds up the tiles of sequences [l m, l m + m), m = ceil(B / 32); one scan
-// over the lanes, and the lane whose sequences hold the run's first tile
-// looks for it among them.
+// adds up the lengths of sequences [l m, l m + m), m = ceil(B / 32); one scan
+// over the lanes, and the lane whose sequences hold the run's start looks for
+// it among them.
 template <int R>
 __device__ __forceinline__ TreeRun tree_run(const TreeParams& P) {
   constexpr unsigned ALL = 0xffffffffu;
@@ -128,7 +142,7 @@ __device__ __forceinline__ TreeRun tree_run(const TreeParams& P) {
   for (int b = b0; b < b1; ++b) {
     s = tree_seq(P, b);
     if (s.base < 0 && blockIdx.x == 0 && P.status) atomicOr(P.status, DEV_CACHE);
-    w += seq_tiles<R>(P, s) * P.Hkv;
+    w += seq_length<R>(P, s) * P.Hkv;
   }
   uint32_t inc = w;
 #pragma unroll
@@ -137,7 +151,7 @@ __device__ __forceinline__ TreeRun tree_run(const TreeParams& P) {
     if (lane >= o) inc += y;
   }
   const uint32_t all = __shfl_sync(ALL, inc, 31);
-  // no more blocks than tiles: the runs of the others are empty
+  // on a short line the last blocks have nothing
   TreeRun run{0, 0, 0, 0, 0, s};
   const uint32_t me = blockIdx.x, grid = gridDim.x;
   if (me >= all) return run;
@@ -153,7 +167,7 @@ __device__ __forceinline__ TreeRun tree_run(const TreeParams& P) {
 #pragma unroll 1
     for (;; ++b) {
       if (m > 1) s = tree_seq(P, b);
-      per = seq_tiles<R>(P, s);
+      per = seq_length<R>(P, s);
       if (off < per * P.Hkv) break;
       off -= per * P.Hkv;
     }
@@ -162,7 +176,7 @@ __device__ __forceinline__ TreeRun tree_run(const TreeParams& P) {
     off -= run.hk * per;
 #pragma unroll 1
     while (true) {
-      const uint32_t t = key_tiles(unit_keys<R>(P, s, run.rt));
+      const uint32_t t = unit_length<R>(key_tiles(unit_keys<R>(P, s, run.rt)));
       if (off < t) break;
       off -= t;
       ++run.rt;
@@ -195,35 +209,40 @@ template <int R>
 struct TreeWalk {
   TreeRun run;
   __device__ __forceinline__ bool next(const TreeParams& P, TreePiece& u) {
-    if (run.left <= 0) return false;
     TreeSeq& s = run.s;
-    // on to the next sequence with rows
 #pragma unroll 1
-    while (run.hk >= P.Hkv || s.n <= 0) {
-      run.hk = run.rt = run.tile = 0;
-      if (++run.b >= P.B) return false;
-      s = tree_seq(P, run.b);
+    while (true) {
+      if (run.left <= 0) return false;
+      // on to the next sequence with rows
+      if (run.hk >= P.Hkv || s.n <= 0) {
+        run.hk = run.rt = run.tile = 0;
+        if (++run.b >= P.B) return false;
+        s = tree_seq(P, run.b);
+        continue;
+      }
+      u.hk = run.hk;
+      u.rt = run.rt;
+      u.keys = unit_keys<R>(P, s, run.rt);
+      u.tiles = key_tiles(u.keys);
+      u.t0 = run.tile;
+      u.t1 = min(u.tiles, run.tile + run.left);
+      const int end = u.t1 < u.tiles ? u.t1 : unit_length<R>(u.tiles);
+      run.left -= end - run.tile;
+      run.tile = end;
+      if (u.t1 >= u.tiles) {
+        run.tile = 0;
+        if (++run.rt >= row_tiles<R>(P, s)) {
+          run.rt = 0;
+          ++run.hk;
+        }
+      }
+      if (u.t0 < u.tiles) break;       // else the run starts in a unit's fixed cost
     }
     u.b = run.b;
-    u.hk = run.hk;
-    u.rt = run.rt;
     u.s = s;
-    u.keys = unit_keys<R>(P, s, run.rt);
-    u.tiles = key_tiles(u.keys);
-    u.t0 = run.tile;
-    u.t1 = min(u.tiles, run.tile + run.left);
-    run.left -= u.t1 - u.t0;
-    u.row_first = run.rt * R;
+    u.row_first = u.rt * R;
     u.rows = min(R, s.n * P.G - u.row_first);
     u.origin = s.base + (P.tree ? 0 : P.by_G(u.row_first));
-    run.tile = u.t1;
-    if (u.t1 == u.tiles) {
-      run.tile = 0;
-      if (++run.rt >= row_tiles<R>(P, s)) {
-        run.rt = 0;
-        ++run.hk;
-      }
-    }
     return true;
   }
 };

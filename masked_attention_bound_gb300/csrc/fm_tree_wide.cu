@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(WideCfg<D>::THREADS, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   constexpr int K_WARP = 8, MMA_WARP = 9, V_WARP = 10;   // 11: slot 1's MMAs
 
-  if (warp == 2) touch_inputs(P, lane);
+  if (warp == 2) touch_memory<D>(P, lane);
   if (tid == 0) {
     for (int s = 0; s < 2; ++s) {
       mbar_init(bar(W_QFULL + s), 4);     // one arrival per softmax warp of the slot
@@ -278,6 +278,9 @@ __global__ void __launch_bounds__(WideCfg<D>::THREADS, 1)
               for (int kk = 0; kk < D / 16; ++kk) {
                 const uint32_t off = (kk >> 2) * (kTile * 128) + (kk & 3) * 32;
                 mma_ss(tS, sdesc_at(dQ, off), sdesc_at(dK, off), idS, kk > 0 ? 1u : 0u);
+                // the turn passes a little early: the other warp needs some
+                // 250 cycles to notice
+                if (kk == D / 16 - 4 && !given) mbar_arrive(bar(W_TURN + s));
               }
               mma_commit(bar(W_SFULL + s));
               mma_commit(bar(W_KEMPTY + ks));
@@ -285,8 +288,10 @@ __global__ void __launch_bounds__(WideCfg<D>::THREADS, 1)
             }
             __syncwarp();
             advance(ks, kp, step, C::KSTAGES);
+            if (!given) ++turn;
+          } else {
+            end_turn();
           }
-          if (!given) end_turn();
           x += step;
         }
         advance(kst, kph, w.n % (2 * C::KSTAGES), C::KSTAGES);
@@ -334,6 +339,10 @@ __global__ void __launch_bounds__(WideCfg<D>::THREADS, 1)
         continue;
       }
       const bool active = w.active(slot);
+      if (lane == 0 && mine && u.whole()) {   // where the rows will go (see touch_memory)
+        touch(orow);
+        touch(lse_out);
+      }
       uint32_t* nf = nf_all + 8 * (pieces & 1);
       if (tid < 8) nf_all[8 * ((pieces + 1) & 1) + tid] = 0;   // the next piece's, read by nobody now
       // which keys from origin on the row sees: bit i is key origin + i
