@@ -504,25 +504,34 @@ __global__ void __launch_bounds__(kJoinThreads)
     float ll = 0.f, v[CPT];
 #pragma unroll
     for (int i = 0; i < CPT; ++i) v[i] = 0.f;
-#pragma unroll 4
-    for (int i = share ? warp : 0; i < parts; i += share ? NW : 1) {
-      const float2 p = P.part_ml[at(i)];
+    for (int i0 = 0; i0 < parts; i0 += 32) {
+      // lane j: weight of part i0 + j; a sum of 0 says that its keys were not seen
+      const int i = i0 + lane;
+      const float2 p = i < parts ? P.part_ml[at(i)] : make_float2(0.f, 0.f);
       const float f = ex2(p.x - mm);
-      const float* src = P.part_o + at(i) * D + lane * CPT;
-      float y[CPT];
-      if constexpr (CPT == 4) {
-        const float4 z = *reinterpret_cast<const float4*>(src);
-        y[0] = z.x; y[1] = z.y; y[2] = z.z; y[3] = z.w;
-      } else {
-        const float2 z = *reinterpret_cast<const float2*>(src);
-        y[0] = z.x; y[1] = z.y;
-      }
-      if (p.y != 0.f) {                  // 0: the part's keys were not seen
-        ll += p.y * f;
+      const unsigned seen = __ballot_sync(0xffffffffu, p.y != 0.f);
+      const bool own = !share || (lane & (NW - 1)) == warp;
+      ll += p.y != 0.f && own ? p.y * f : 0.f;
+      const int end = min(32, parts - i0);
+#pragma unroll 4
+      for (int j = share ? warp : 0; j < end; j += share ? NW : 1) {
+        const float* src = P.part_o + at(i0 + j) * D + lane * CPT;
+        float y[CPT];
+        if constexpr (CPT == 4) {
+          const float4 z = *reinterpret_cast<const float4*>(src);
+          y[0] = z.x; y[1] = z.y; y[2] = z.z; y[3] = z.w;
+        } else {
+          const float2 z = *reinterpret_cast<const float2*>(src);
+          y[0] = z.x; y[1] = z.y;
+        }
+        const float fj = __shfl_sync(0xffffffffu, f, j);
+        if ((seen >> j) & 1u)
 #pragma unroll
-        for (int x = 0; x < CPT; ++x) v[x] += y[x] * f;
+          for (int x = 0; x < CPT; ++x) v[x] += y[x] * fj;
       }
     }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) ll += __shfl_xor_sync(0xffffffffu, ll, o);
     if (share) {
       __syncthreads();                   // the row before has been read
 #pragma unroll
@@ -557,7 +566,7 @@ __global__ void __launch_bounds__(kJoinThreads)
 
 template <int R, int D>
 static fm_status launch_join(const TreeParams& P, int grid, cudaStream_t s) {
-  if (grid < 2) return FM_OK;
+  if (grid < 2 || P.whole) return FM_OK;
   // a block's warps take a row each of the largest unit in two parts
   prof_begin(K_TREE_JOIN, s);
   const cudaError_t e = launch_dependent(
@@ -653,6 +662,10 @@ fm_status fm_tree_fwd(const fm_cache* c, const fm_tree_desc* t, const void* q, c
   P.by_G = FastDiv::of(P.G);
   P.by_grid = FastDiv::of(grid);
   P.tree = parents != nullptr;
+  // Rows of the table that hold at most four tiles: units are not cut, and the
+  // join (2.5 us after the first kernel) is spared; the tiles that a block then
+  // takes in turn cost 0.4 us each.
+  P.whole = static_cast<int64_t>(c->max_pages) * c->page_size <= 4 * kTile;
   P.scale_log2 = scale * 1.4426950408889634f;
   P.q = static_cast<const __nv_bfloat16*>(q);
   P.o = static_cast<__nv_bfloat16*>(o);

@@ -22,6 +22,7 @@ namespace fm {
 struct TreeParams {
   int B, H, Hkv, G, total, max_nodes, page_shift, n_pages, max_pages;
   int tree;                // 0: chain (no parents)
+  int whole;               // units are not cut: no parts, no join
   FastDiv by_G, by_grid;
   float scale_log2;        // scale * log2(e)
   const __nv_bfloat16* q;
@@ -83,13 +84,13 @@ __device__ __forceinline__ int unit_keys(const TreeParams& P, const TreeSeq& s, 
 __device__ __forceinline__ int key_tiles(int keys) {
   return keys > 0 ? (keys + kTile - 1) / kTile : 1;
 }
-// A unit's length on the line.  Its fixed cost in tiles, measured: 4 for the
-// wide kernel (a block with a unit's end in its run took 12000 to 14000
-// cycles longer, a tile of 256 rows takes 3600 and one of 128 rows 2800), 1
-// for the narrow one.
+// A unit's length on the line.  Its fixed cost in tiles, measured: a block
+// with a unit's end in its run took 12000 (256 rows) to 20000 cycles (128
+// rows) longer, where a tile takes 3100 and 2800; 1 for the narrow kernel.
+// With P.whole a unit is a point of the line and never cut.
 template <int R>
-__device__ __forceinline__ int unit_length(int tiles) {
-  return tiles + (R > 16 ? 4 : 1);
+__device__ __forceinline__ int unit_length(const TreeParams& P, const TreeSeq& s, int rt, int tiles) {
+  return P.whole ? 1 : tiles + (R <= 16 ? 1 : (s.n * P.G - rt * R > 128 ? 4 : 7));
 }
 // Length of all units of one K/V head of a sequence.  (The launch checks that
 // the line's length fits in 31 bits.)
@@ -98,7 +99,7 @@ __device__ __forceinline__ uint32_t seq_length(const TreeParams& P, const TreeSe
   const int nr = row_tiles<R>(P, s);
   uint32_t w = 0;
 #pragma unroll 1
-  for (int rt = 0; rt < nr; ++rt) w += unit_length<R>(key_tiles(unit_keys<R>(P, s, rt)));
+  for (int rt = 0; rt < nr; ++rt) w += unit_length<R>(P, s, rt, key_tiles(unit_keys<R>(P, s, rt)));
   return w;
 }
 
@@ -114,6 +115,7 @@ __device__ __forceinline__ void touch_memory(const TreeParams& P, int lane) {
   if (lane == 2) touch(P.table);
   if (lane == 3) touch(P.q);
   if (lane == 4 && P.tree) touch(P.parents);
+  if (lane >= 5 && P.whole) return;
   if (lane == 5) touch(P.part_o + part * D);
   if (lane == 6) touch(P.part_o + (part + P.part_rows) * D);
   if (lane == 7) touch(P.part_ml + part);
@@ -176,7 +178,7 @@ __device__ __forceinline__ TreeRun tree_run(const TreeParams& P) {
     off -= run.hk * per;
 #pragma unroll 1
     while (true) {
-      const uint32_t t = unit_length<R>(key_tiles(unit_keys<R>(P, s, run.rt)));
+      const uint32_t t = unit_length<R>(P, s, run.rt, key_tiles(unit_keys<R>(P, s, run.rt)));
       if (off < t) break;
       off -= t;
       ++run.rt;
@@ -225,8 +227,8 @@ struct TreeWalk {
       u.keys = unit_keys<R>(P, s, run.rt);
       u.tiles = key_tiles(u.keys);
       u.t0 = run.tile;
-      u.t1 = min(u.tiles, run.tile + run.left);
-      const int end = u.t1 < u.tiles ? u.t1 : unit_length<R>(u.tiles);
+      u.t1 = P.whole ? u.tiles : min(u.tiles, run.tile + run.left);
+      const int end = u.t1 < u.tiles ? u.t1 : unit_length<R>(P, s, run.rt, u.tiles);
       run.left -= end - run.tile;
       run.tile = end;
       if (u.t1 >= u.tiles) {

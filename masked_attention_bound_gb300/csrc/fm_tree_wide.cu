@@ -21,21 +21,27 @@
 
 namespace fm {
 
-template <int D>
+// ROWS: units may have more than 128 rows; without it there is one Q tile,
+// and its room holds another K tile.
+template <int D, bool ROWS>
 struct WideCfg {
   static constexpr int TILE = kTile * D * 2;
-  static constexpr int SLABS = D / 64;
-  static constexpr int KSTAGES = 2, VSTAGES = 3;
-  static constexpr int OFF_Q = 0;                       // one tile per slot
-  static constexpr int OFF_K = 2 * TILE;
+  static constexpr int QTILES = ROWS ? 2 : 1;
+  static constexpr int KSTAGES = ROWS ? 2 : 3, VSTAGES = 3;
+  static constexpr int OFF_Q = 0;                       // one tile, or one per slot
+  static constexpr int OFF_K = QTILES * TILE;
   static constexpr int OFF_V = OFF_K + KSTAGES * TILE;
   static constexpr int OFF_ML = OFF_V + VSTAGES * TILE; // float2 [slot][128]
   static constexpr int OFF_NF = OFF_ML + 2 * 128 * 8;   // [2][8] keys with values not finite
   static constexpr int OFF_BAR = OFF_NF + 64;
-  static constexpr int NBAR = 24;
+  static constexpr int NBAR = 26;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;   // abort flag, TMEM address
   static constexpr int OFF_PAR = OFF_MISC + 16;         // int16 [256] parents of the unit's nodes
-  static constexpr int USED = OFF_PAR + 512;
+  // 4 KB per softmax warp through which O is written: the Q tiles, where they
+  // are large enough (they are not needed any more by then)
+  static constexpr bool STAGE_IN_Q = QTILES * TILE >= 8 * 4096;
+  static constexpr int OFF_STAGE = STAGE_IN_Q ? OFF_Q : (OFF_PAR + 512 + 127) / 128 * 128;
+  static constexpr int USED = STAGE_IN_Q ? OFF_PAR + 512 : OFF_STAGE + 8 * 4096;
   // one block per SM: it takes all of the tensor memory
   static constexpr int SMEM = USED > 120 * 1024 ? USED : 120 * 1024;
   static constexpr int THREADS = 384;
@@ -46,8 +52,8 @@ struct WideCfg {
 };
 
 enum {
-  W_QFULL = 0, W_SFULL = 2, W_PFULL = 4, W_PVDONE = 6, W_OEMPTY = 8, W_KFULL = 10, W_KEMPTY = 12,
-  W_VFULL = 14, W_VEMPTY = 17, W_DRAIN = 20, W_TURN = 21
+  W_QFULL = 0, W_SFULL = 2, W_PFULL = 4, W_PVDONE = 6, W_OEMPTY = 8, W_KFULL = 10, W_KEMPTY = 13,
+  W_VFULL = 16, W_VEMPTY = 19, W_DRAIN = 22, W_TURN = 23
 };
 
 // How the two slots share a piece.
@@ -60,8 +66,9 @@ struct WideSplit {
   }
   __device__ __forceinline__ bool takes(int s, int x) const { return rows || (x & 1) == s; }
 };
+template <bool ROWS>
 __device__ __forceinline__ WideSplit wide_split(const TreePiece& u) {
-  return WideSplit{u.rows > 128, u.keys > 0 ? u.t1 - u.t0 : 0};
+  return WideSplit{ROWS && u.rows > 128, u.keys > 0 ? u.t1 - u.t0 : 0};
 }
 
 // 16 bytes from global to shared memory without a register or a line of L1;
@@ -76,11 +83,11 @@ __device__ __forceinline__ void copy_async_wait() {
 
 __device__ __forceinline__ void slots_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
-template <int D>
-__global__ void __launch_bounds__(WideCfg<D>::THREADS, 1)
+template <int D, bool ROWS>
+__global__ void __launch_bounds__(WideCfg<D, ROWS>::THREADS, 1)
     tree_wide_kernel(const __grid_constant__ TreeParams P, const __grid_constant__ CUtensorMap tmK,
                      const __grid_constant__ CUtensorMap tmV) {
-  using C = WideCfg<D>;
+  using C = WideCfg<D, ROWS>;
   constexpr int R = kWideRows;
   extern __shared__ __align__(1024) uint8_t smem[];
   if (smem_u32(smem) & 1023u) {
@@ -183,7 +190,7 @@ __global__ void __launch_bounds__(WideCfg<D>::THREADS, 1)
       const int s = warp - MMA_WARP >> 1;
       constexpr uint32_t idS = idesc_bf16(128, 128, false, false);
       constexpr uint32_t idPV = idesc_bf16(128, D, false, true);
-      const uint32_t dQ = sdesc_lo(sbase + C::OFF_Q + s * C::TILE, 16);
+      const uint32_t dQ = sdesc_lo(sbase + C::OFF_Q + (ROWS ? s * C::TILE : 0), 16);
       const uint32_t dK0 = sdesc_lo(sbase + C::OFF_K, 16);
       const uint32_t dV0 = sdesc_lo(sbase + C::OFF_V, kTile * 128);
       const uint32_t tS = tbase + 128 * s, tO = tbase + 256 + 128 * s;
@@ -194,7 +201,7 @@ __global__ void __launch_bounds__(WideCfg<D>::THREADS, 1)
       bool ok = true;
       TreePiece u;
       while (ok && walk.next(P, u)) {
-        const WideSplit w = wide_split(u);
+        const WideSplit w = wide_split<ROWS>(u);
         if (w.n == 0) continue;
         // The two MMA warps take turns: a turn is one tile's PV and the next
         // one's S.  Without it the slots fall into step (both wait for the
@@ -222,10 +229,8 @@ __global__ void __launch_bounds__(WideCfg<D>::THREADS, 1)
         uint32_t ks = kst, kp = kph, vs = vst, vp = vph;        // of tiles x (K) and x - step (V)
         advance(ks, kp, x0, C::KSTAGES);
         advance(vs, vp, x0, C::VSTAGES);
-        if (w.active(s)) {
-          ok = wait_all(W_QFULL + s, qn & 1);
-          ++qn;
-        }
+        if (w.active(s)) ok = wait_all(W_QFULL + (ROWS ? s : 0), qn & 1);
+        if (!ROWS || w.active(s)) ++qn;
         int x = x0;
 #pragma unroll 1
         for (int i = 0; ok && i < turns; ++i) {
@@ -321,20 +326,21 @@ __global__ void __launch_bounds__(WideCfg<D>::THREADS, 1)
     int4 rec = make_int4(-1, 0, 0, 0);
     TreePiece u;
     while (walk.next(P, u)) {
-      const WideSplit w = wide_split(u);
+      const WideSplit w = wide_split<ROWS>(u);
       const int ur = w.rows ? slot * 128 + r : r;      // row of the unit
-      const bool mine = ur < u.rows && (w.rows || slot == 0 || w.n > 0);
+      const bool mine = ur < u.rows;
       const int rr = u.row_first + ur;
       const int node = ur < u.rows ? P.by_G(rr) : 0;
       const int h = u.hk * P.G + (ur < u.rows ? rr - node * P.G : 0);
       __nv_bfloat16* orow = P.o + (u.s.row0 + node) * P.o_stride[0] + h * P.o_stride[1];
       float* lse_out = P.lse + static_cast<int64_t>(h) * P.total + u.s.row0 + node;
-      if (w.n == 0) {                                  // no keys
-        if (mine && (w.rows || slot == 0)) {
-          const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-          for (int c = 0; c < D / 8; ++c) reinterpret_cast<uint4*>(orow)[c] = z;
-          *lse_out = -INFINITY;
+      if (w.n == 0) {                                  // no keys: zeros in all its rows
+        const int z = slot * 128 + r, zr = u.row_first + z, zn = P.by_G(zr), zh = u.hk * P.G + zr - zn * P.G;
+        if (z < u.rows) {
+          uint4* dst = reinterpret_cast<uint4*>(P.o + (u.s.row0 + zn) * P.o_stride[0] + zh * P.o_stride[1]);
+#pragma unroll 1
+          for (int c = 0; c < D / 8; ++c) dst[c] = make_uint4(0u, 0u, 0u, 0u);
+          P.lse[static_cast<int64_t>(zh) * P.total + u.s.row0 + zn] = -INFINITY;
         }
         continue;
       }
@@ -364,8 +370,8 @@ __global__ void __launch_bounds__(WideCfg<D>::THREADS, 1)
       }
       const bool warp_live = __any_sync(0xffffffffu, live);
       float m_used = -INFINITY, l = 0.f;
-      if (active) {
-        // this slot's Q (S of its earlier pieces has been read): a row is
+      if (ROWS ? active : slot == 0) {
+        // Q (S of the slots' earlier pieces has been read): a row is
         // copied by D / 8 lanes, so that a warp's copy covers whole rows, and
         // asynchronously past L1: the few KB that shared memory leaves of it
         // hold up plain loads of 64 KB for 7000 cycles
@@ -384,6 +390,8 @@ __global__ void __launch_bounds__(WideCfg<D>::THREADS, 1)
         copy_async_wait();
         fence_proxy_async_smem();
         mbar_arrive_warp(bar(W_QFULL + slot));
+      }
+      if (active) {
         int done = 0;
 #pragma unroll 1
         for (int x0 = w.rows ? 0 : slot; x0 < w.n; x0 += w.rows ? 1 : 2) {
@@ -555,7 +563,7 @@ __global__ void __launch_bounds__(WideCfg<D>::THREADS, 1)
       // O by blocks of 32 columns; each passes through the warp's part of the
       // slot's Q buffer (no longer needed), so that the stores cover whole
       // runs of a row: 64 bytes (bf16) or 128 bytes (fp32 parts)
-      uint8_t* stage = smem + C::OFF_Q + slot * C::TILE + quarter * 32 * (D * 2);
+      uint8_t* stage = smem + C::OFF_STAGE + warp * 4096;
       const unsigned out_rows = __ballot_sync(0xffffffffu, writes);
 #pragma unroll 1
       for (int cb = c0 / 32; cb < c1 / 32; ++cb) {
@@ -663,11 +671,11 @@ __global__ void __launch_bounds__(WideCfg<D>::THREADS, 1)
   }
 }
 
-template <int D>
+template <int D, bool ROWS>
 static fm_status launch_wide_d(const TreeParams& P, const CUtensorMap& tk, const CUtensorMap& tv,
                                int grid, cudaStream_t s) {
-  using C = WideCfg<D>;
-  auto kern = tree_wide_kernel<D>;
+  using C = WideCfg<D, ROWS>;
+  auto kern = tree_wide_kernel<D, ROWS>;
   // the setmaxnreg split must fit in the registers the block launches with
   static std::atomic<uint64_t> ready{0};
   const fm_status st = prepare_kernel(kern, C::SMEM, C::MIN_LAUNCH_REGS, ready);
@@ -680,7 +688,10 @@ static fm_status launch_wide_d(const TreeParams& P, const CUtensorMap& tk, const
 
 fm_status launch_tree_wide(const TreeParams& P, int d, const CUtensorMap& tk, const CUtensorMap& tv,
                            int grid, cudaStream_t s) {
-  return d == 64 ? launch_wide_d<64>(P, tk, tv, grid, s) : launch_wide_d<128>(P, tk, tv, grid, s);
+  const bool rows = P.part_rows > 128;
+  if (d == 64)
+    return rows ? launch_wide_d<64, true>(P, tk, tv, grid, s) : launch_wide_d<64, false>(P, tk, tv, grid, s);
+  return rows ? launch_wide_d<128, true>(P, tk, tv, grid, s) : launch_wide_d<128, false>(P, tk, tv, grid, s);
 }
 
 }  // namespace fm
