@@ -106,6 +106,7 @@ __global__ void __launch_bounds__(NarrowCfg<D>::THREADS, 1)
     const CUtensorMap* tm = isk ? &tmK : &tmV;
     const int stages = isk ? C::KS : C::VS, first = isk ? 0 : C::KS;
     const uint32_t buf = sbase + (isk ? 0 : C::OFF_V);
+    const uint64_t policy = policy_evict_first();
     int st = 0, issued = 0;
     uint32_t use = 0;
     TreePiece u;
@@ -118,7 +119,7 @@ __global__ void __launch_bounds__(NarrowCfg<D>::THREADS, 1)
         const int next = t + 1 < u.t1 ? TileLoad<D>::lane_page(P, u, t + 1, lane) : 0;
         if (use > 0) ok = wait_all(empty(first + st), (use - 1) & 1);
         if (!ok) break;
-        TileLoad<D>::issue(P, u, t, lane, page, tm, buf + st * C::TILE, full(first + st));
+        TileLoad<D>::issue(P, u, t, lane, page, tm, buf + st * C::TILE, full(first + st), policy);
         ++issued;
         if (++st == stages) {
           st = 0;
@@ -454,13 +455,14 @@ __global__ void __launch_bounds__(NarrowCfg<D>::THREADS, 1)
 // sums and O weighted by 2^(m - maximum).  A block's eight warps share a row
 // when it has many parts (one long sequence: 76 parts of two units took 33 us
 // with a warp a row, 512 bytes of each part at a time), each warp taking every
-// eighth, else they take a row each; the order of the sums is fixed either way.
+// eighth, else they take rows of their own; the order of the sums is fixed
+// either way.
 constexpr int kJoinThreads = 256, kJoinShare = 12;
 
 template <int R, int D>
 __global__ void __launch_bounds__(kJoinThreads)
     tree_join_kernel(const __grid_constant__ TreeParams P, int blocks) {
-  constexpr int NW = kJoinThreads / 32, CPT = D / 32;
+  constexpr int NW = kJoinThreads / 32, CPT = D / 32, RPW = R == kNarrowRows ? 2 : 4;
   __shared__ float sums[NW][D + 1];
   grid_launch_dependents();
   grid_dependency_wait();
@@ -491,64 +493,21 @@ __global__ void __launch_bounds__(kJoinThreads)
   const int row_first = rec.z * R, rows = min(R, s.n * P.G - row_first), parts = last - c + 1;
   const bool share = parts > kJoinShare;
   // the blocks in the middle of the unit (in [c, last)) take rows of it too
-  const int first = (blockIdx.x - c) * gridDim.y + blockIdx.y;
-  const int step = (last - c) * gridDim.y * (share ? 1 : NW);
-  for (int r = share ? first : first * NW + warp; r < rows; r += step) {
-    auto at = [&](int i) -> int64_t {
-      return static_cast<int64_t>(i == 0 ? 2 * c + 1 : 2 * (c + i)) * P.part_rows + r;
-    };
-    float mm = -INFINITY;
-    for (int i = lane; i < parts; i += 32) mm = fmaxf(mm, P.part_ml[at(i)].x);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
-    float ll = 0.f, v[CPT];
-#pragma unroll
-    for (int i = 0; i < CPT; ++i) v[i] = 0.f;
-    for (int i0 = 0; i0 < parts; i0 += 32) {
-      // lane j: weight of part i0 + j; a sum of 0 says that its keys were not seen
-      const int i = i0 + lane;
-      const float2 p = i < parts ? P.part_ml[at(i)] : make_float2(0.f, 0.f);
-      const float f = ex2(p.x - mm);
-      const unsigned seen = __ballot_sync(0xffffffffu, p.y != 0.f);
-      const bool own = !share || (lane & (NW - 1)) == warp;
-      ll += p.y != 0.f && own ? p.y * f : 0.f;
-      const int end = min(32, parts - i0);
-#pragma unroll 4
-      for (int j = share ? warp : 0; j < end; j += share ? NW : 1) {
-        const float* src = P.part_o + at(i0 + j) * D + lane * CPT;
-        float y[CPT];
-        if constexpr (CPT == 4) {
-          const float4 z = *reinterpret_cast<const float4*>(src);
-          y[0] = z.x; y[1] = z.y; y[2] = z.z; y[3] = z.w;
-        } else {
-          const float2 z = *reinterpret_cast<const float2*>(src);
-          y[0] = z.x; y[1] = z.y;
-        }
-        const float fj = __shfl_sync(0xffffffffu, f, j);
-        if ((seen >> j) & 1u)
-#pragma unroll
-          for (int x = 0; x < CPT; ++x) v[x] += y[x] * fj;
-      }
+  const int first = (blockIdx.x - c) * gridDim.y + blockIdx.y, step = (last - c) * gridDim.y;
+  auto at = [&](int i, int r) -> int64_t {
+    return static_cast<int64_t>(i == 0 ? 2 * c + 1 : 2 * (c + i)) * P.part_rows + r;
+  };
+  auto load = [&](int i, int r, float (&y)[CPT]) {
+    const float* src = P.part_o + at(i, r) * D + lane * CPT;
+    if constexpr (CPT == 4) {
+      const float4 z = *reinterpret_cast<const float4*>(src);
+      y[0] = z.x; y[1] = z.y; y[2] = z.z; y[3] = z.w;
+    } else {
+      const float2 z = *reinterpret_cast<const float2*>(src);
+      y[0] = z.x; y[1] = z.y;
     }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) ll += __shfl_xor_sync(0xffffffffu, ll, o);
-    if (share) {
-      __syncthreads();                   // the row before has been read
-#pragma unroll
-      for (int x = 0; x < CPT; ++x) sums[warp][lane * CPT + x] = v[x];
-      if (lane == 0) sums[warp][D] = ll;
-      __syncthreads();
-      if (warp > 0) continue;
-      ll = 0.f;
-#pragma unroll
-      for (int x = 0; x < CPT; ++x) v[x] = 0.f;
-#pragma unroll
-      for (int w = 0; w < NW; ++w) {
-        ll += sums[w][D];
-#pragma unroll
-        for (int x = 0; x < CPT; ++x) v[x] += sums[w][lane * CPT + x];
-      }
-    }
+  };
+  auto write = [&](int r, float mm, float ll, const float (&v)[CPT]) {
     const int rr = row_first + r, node = P.by_G(rr), h = rec.y * P.G + rr - node * P.G;
     const float inv = ll > 0.f ? 1.f / ll : 0.f;
     uint32_t w[CPT / 2];
@@ -561,16 +520,102 @@ __global__ void __launch_bounds__(kJoinThreads)
     if (lane == 0)
       P.lse[static_cast<int64_t>(h) * P.total + s.row0 + node] =
           ll > 0.f || ll != ll ? (mm + __log2f(ll)) * 0.69314718055994530942f : -INFINITY;
+  };
+
+  if (!share) {
+    // few parts: a warp joins RPW rows at a time, to have their loads in flight
+    // together (a row a warp left the parts of 150 units at 3 TB/s)
+    for (int r0 = (first * NW + warp) * RPW; r0 < rows; r0 += step * NW * RPW) {
+      float mm[RPW], f[RPW], ll[RPW], v[RPW][CPT];
+      unsigned seen[RPW];
+      // lane i: maximum and sum of part i; a sum of 0 says that its keys were not seen
+      float2 p[RPW];
+#pragma unroll
+      for (int k = 0; k < RPW; ++k)
+        p[k] = lane < parts && r0 + k < rows ? P.part_ml[at(lane, r0 + k)] : make_float2(-INFINITY, 0.f);
+#pragma unroll
+      for (int k = 0; k < RPW; ++k) {
+        mm[k] = p[k].x;
+#pragma unroll
+        for (int o = 8; o; o >>= 1) mm[k] = fmaxf(mm[k], __shfl_xor_sync(0xffffffffu, mm[k], o));
+        mm[k] = __shfl_sync(0xffffffffu, mm[k], 0);
+        f[k] = p[k].y != 0.f ? ex2(p[k].x - mm[k]) : 0.f;
+        seen[k] = __ballot_sync(0xffffffffu, p[k].y != 0.f);
+        ll[k] = p[k].y != 0.f ? p[k].y * f[k] : 0.f;
+#pragma unroll
+        for (int o = 8; o; o >>= 1) ll[k] += __shfl_xor_sync(0xffffffffu, ll[k], o);
+        ll[k] = __shfl_sync(0xffffffffu, ll[k], 0);
+#pragma unroll
+        for (int x = 0; x < CPT; ++x) v[k][x] = 0.f;
+      }
+#pragma unroll 2
+      for (int i = 0; i < parts; ++i) {
+        float y[RPW][CPT];
+#pragma unroll
+        for (int k = 0; k < RPW; ++k)
+          if (r0 + k < rows) load(i, r0 + k, y[k]);
+#pragma unroll
+        for (int k = 0; k < RPW; ++k) {
+          const float w = __shfl_sync(0xffffffffu, f[k], i);
+          if ((seen[k] >> i) & 1u)
+#pragma unroll
+            for (int x = 0; x < CPT; ++x) v[k][x] += y[k][x] * w;
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < RPW; ++k)
+        if (r0 + k < rows) write(r0 + k, mm[k], ll[k], v[k]);
+    }
+    return;
+  }
+
+  // many parts: the block's warps share a row, each taking every eighth part
+  for (int r = first; r < rows; r += step) {
+    float mm = -INFINITY;
+    for (int i = lane; i < parts; i += 32) mm = fmaxf(mm, P.part_ml[at(i, r)].x);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
+    float ll = 0.f, v[CPT];
+#pragma unroll
+    for (int i = 0; i < CPT; ++i) v[i] = 0.f;
+#pragma unroll 4
+    for (int i = warp; i < parts; i += NW) {
+      float y[CPT];
+      load(i, r, y);
+      const float2 p = P.part_ml[at(i, r)];
+      if (p.y != 0.f) {
+        const float f = ex2(p.x - mm);
+        ll += p.y * f;
+#pragma unroll
+        for (int x = 0; x < CPT; ++x) v[x] += y[x] * f;
+      }
+    }
+    __syncthreads();                   // the row before has been read
+#pragma unroll
+    for (int x = 0; x < CPT; ++x) sums[warp][lane * CPT + x] = v[x];
+    if (lane == 0) sums[warp][D] = ll;
+    __syncthreads();
+    if (warp > 0) continue;
+    ll = 0.f;
+#pragma unroll
+    for (int x = 0; x < CPT; ++x) v[x] = 0.f;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+      ll += sums[w][D];
+#pragma unroll
+      for (int x = 0; x < CPT; ++x) v[x] += sums[w][lane * CPT + x];
+    }
+    write(r, mm, ll, v);
   }
 }
 
 template <int R, int D>
 static fm_status launch_join(const TreeParams& P, int grid, cudaStream_t s) {
   if (grid < 2 || P.whole) return FM_OK;
-  // a block's warps take a row each of the largest unit in two parts
+  // the blocks of a unit in two parts take its rows in one go
   prof_begin(K_TREE_JOIN, s);
   const cudaError_t e = launch_dependent(
-      tree_join_kernel<R, D>, dim3(grid - 1, ceil_div(P.part_rows, kJoinThreads / 32)), kJoinThreads,
+      tree_join_kernel<R, D>, dim3(grid - 1, ceil_div(P.part_rows, kJoinThreads / 32 * (R == kNarrowRows ? 2 : 4))), kJoinThreads,
       0, s, P, grid);
   prof_end(K_TREE_JOIN, s);
   return e == cudaSuccess ? FM_OK : FM_ERR_CUDA;

@@ -305,7 +305,10 @@ __device__ __forceinline__ bool tree_wait(uint32_t bar, uint32_t parity, const T
 // One 128-key tile of K or V (a pool's tensor map) into shared memory:
 // page_size rows of 64 columns per copy, the tile's two 64-column slabs 16 KB
 // apart.  Pages past the unit's keys are not loaded.  All 32 lanes call it;
-// `pages`: this lane's page (see tile_pages).
+// `page`: this lane's (lane_page); `policy`: evict first, since a stream of K
+// and V through L2 would push out what the next piece needs, the kernel's
+// own instructions among it (a fetch from DRAM behind the stream took 5000
+// cycles).
 template <int D>
 struct TileLoad {
   static constexpr int SLABS = D / 64;
@@ -328,14 +331,14 @@ struct TileLoad {
   }
   __device__ static __forceinline__ void issue(const TreeParams& P, const TreePiece& u, int tile,
                                                int lane, int page, const CUtensorMap* tm,
-                                               uint32_t dst, uint32_t bar) {
+                                               uint32_t dst, uint32_t bar, uint64_t policy) {
     const int n = pages(P, u, tile);
     if (lane == 0) mbar_arrive_expect_tx(bar, (n << P.page_shift) * D * 2);
     __syncwarp();
     const int j = lane / SLABS, slab = lane % SLABS;
     if (j < n)
-      tma_load_4d(dst + slab * (kTile * 128) + (j << P.page_shift) * 128, tm, bar, slab * 64, u.hk, 0,
-                  page);
+      tma_load_4d_hint(dst + slab * (kTile * 128) + (j << P.page_shift) * 128, tm, bar, slab * 64, u.hk,
+                       0, page, policy);
   }
 };
 

@@ -157,6 +157,7 @@ __global__ void __launch_bounds__(WideCfg<D, ROWS>::THREADS, 1)
       const int b_full = isk ? W_KFULL : W_VFULL, b_empty = isk ? W_KEMPTY : W_VEMPTY;
       const uint32_t buf = sbase + (isk ? C::OFF_K : C::OFF_V);
       const CUtensorMap* tm = isk ? &tmK : &tmV;
+      const uint64_t policy = policy_evict_first();
       uint32_t st = 0, use = 0, issued = 0;    // stage, its uses so far, tiles issued
       TreePiece u;
       bool ok = true;
@@ -168,7 +169,7 @@ __global__ void __launch_bounds__(WideCfg<D, ROWS>::THREADS, 1)
           const int next = t + 1 < u.t1 ? TileLoad<D>::lane_page(P, u, t + 1, lane) : 0;
           if (use > 0) ok = wait_all(b_empty + st, (use - 1) & 1);
           if (!ok) break;
-          TileLoad<D>::issue(P, u, t, lane, page, tm, buf + st * C::TILE, bar(b_full + st));
+          TileLoad<D>::issue(P, u, t, lane, page, tm, buf + st * C::TILE, bar(b_full + st), policy);
           ++issued;
           if (++st == stages) {
             st = 0;
