@@ -90,7 +90,7 @@ __device__ __forceinline__ int key_tiles(int keys) {
 // With P.whole a unit is a point of the line and never cut.
 template <int R>
 __device__ __forceinline__ int unit_length(const TreeParams& P, const TreeSeq& s, int rt, int tiles) {
-  return P.whole ? 1 : tiles + (R <= 16 ? 1 : (s.n * P.G - rt * R > 128 ? 4 : 7));
+  return P.whole ? 1 : tiles + (R <= 16 ? 1 : (s.n * P.G - rt * R > 128 ? 5 : 10));
 }
 // Length of all units of one K/V head of a sequence.  (The launch checks that
 // the line's length fits in 31 bits.)
