@@ -11,27 +11,32 @@ namespace fm {
 // Units of up to 16 rows (one token of up to 16 query heads per K/V head, or
 // a few nodes).  Bound by reading K and V once: 512 bytes per key and head at
 // d = 128 against 8 KFLOP.  Two warps load K and V tiles by TMA through
-// rings of tiles; eight warps each take 16 keys of every 128-key tile and keep
+// rings of tiles; four warps each take 16 keys of every 64-key tile and keep
 // their own running maximum, sum and O in registers, so no warp waits for
 // another inside a unit.  S and O come from mma.sync (16 x 8 x 16, bf16): its
 // fragments leave P in registers as the A operand of the second product, and
 // 16 rows fill its M, where a tcgen05.mma would pad them to 128.
+// Two blocks share an SM: one's fetching of rows, merging and writing at the
+// ends of units runs while the other's tiles stream (one block of twice the
+// size took 56 us for 1024 units of three 128-key tiles).
 template <int D>
 struct NarrowCfg {
-  static constexpr int R = kNarrowRows;
-  static constexpr int WARPS = 8;                  // consumers
+  using Geo = NarrowGeo;
+  static constexpr int R = Geo::R, KT = Geo::KT;
+  static constexpr int WARPS = 4;                  // consumers
   static constexpr int THREADS = 32 * (WARPS + 2);
-  static constexpr int TILE = kTile * D * 2;       // bytes of a K or V tile
+  static constexpr int TILE = KT * D * 2;          // bytes of a K or V tile
   static constexpr int KS = D == 128 ? 3 : 5, VS = D == 128 ? 2 : 5;   // rings of tiles
   static constexpr int PITCH = D + 8;              // floats of a row of the merge buffer
   static constexpr int OFF_V = KS * TILE;
   static constexpr int OFF_MERGE = OFF_V + VS * TILE;
-  static constexpr int OFF_ML = OFF_MERGE + 4 * R * PITCH * 4;   // [WARPS][R] max, then sum
+  static constexpr int OFF_ML = OFF_MERGE + WARPS / 2 * R * PITCH * 4;   // [WARPS][R] max, then sum
   static constexpr int OFF_SEEN = OFF_ML + 2 * WARPS * R * 4;    // [R][8] ancestors
   static constexpr int OFF_NF = OFF_SEEN + R * 8 * 4;            // [8] keys with values not finite
   static constexpr int OFF_BAR = OFF_NF + 32;
   static constexpr int OFF_ABORT = OFF_BAR + 2 * (KS + VS) * 8;
   static constexpr int SMEM = OFF_ABORT + 8;
+  static_assert(2 * (SMEM + 1024) <= 228 * 1024, "two blocks per SM");
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
@@ -59,11 +64,12 @@ __device__ __forceinline__ void named_sync(int id, int threads) {
 }
 
 template <int D>
-__global__ void __launch_bounds__(NarrowCfg<D>::THREADS, 1)
+__global__ void __launch_bounds__(NarrowCfg<D>::THREADS, 2)
     tree_narrow_kernel(const __grid_constant__ TreeParams P, const __grid_constant__ CUtensorMap tmK,
                        const __grid_constant__ CUtensorMap tmV) {
   using C = NarrowCfg<D>;
-  constexpr int R = C::R;
+  using Load = TileLoad<D, C::KT>;
+  constexpr int R = C::R, KT = C::KT;
   extern __shared__ __align__(1024) uint8_t smem[];
   volatile int& abort_flag = *reinterpret_cast<volatile int*>(smem + C::OFF_ABORT);
   if (smem_u32(smem) & 1023u) {
@@ -90,8 +96,8 @@ __global__ void __launch_bounds__(NarrowCfg<D>::THREADS, 1)
   }
   grid_launch_dependents();
   grid_dependency_wait();
-  TreeWalk<R> walk;
-  walk.run = tree_run<R>(P);
+  TreeWalk<typename C::Geo> walk;
+  walk.run = tree_run<typename C::Geo>(P);
   __syncthreads();
 
   // every lane gets the same answer
@@ -113,13 +119,13 @@ __global__ void __launch_bounds__(NarrowCfg<D>::THREADS, 1)
     bool ok = true;
     while (ok && walk.next(P, u)) {
       if (u.keys == 0) continue;
-      int page = TileLoad<D>::lane_page(P, u, u.t0, lane);
+      int page = Load::lane_page(P, u, u.t0, lane);
 #pragma unroll 1
       for (int t = u.t0; t < u.t1; ++t) {
-        const int next = t + 1 < u.t1 ? TileLoad<D>::lane_page(P, u, t + 1, lane) : 0;
+        const int next = t + 1 < u.t1 ? Load::lane_page(P, u, t + 1, lane) : 0;
         if (use > 0) ok = wait_all(empty(first + st), (use - 1) & 1);
         if (!ok) break;
-        TileLoad<D>::issue(P, u, t, lane, page, tm, buf + st * C::TILE, full(first + st), policy);
+        Load::issue(P, u, t, lane, page, tm, buf + st * C::TILE, full(first + st), policy);
         ++issued;
         if (++st == stages) {
           st = 0;
@@ -149,7 +155,7 @@ __global__ void __launch_bounds__(NarrowCfg<D>::THREADS, 1)
     TreePiece u;
     while (walk.next(P, u)) {
       // tiles from this one on hold keys that not every row sees
-      const int part0 = u.origin / kTile;
+      const int part0 = u.origin / KT;
       // which keys past origin a row sees: bit j is key origin + j
       if (warp == 0) {
         uint32_t w[8];
@@ -205,7 +211,7 @@ __global__ void __launch_bounds__(NarrowCfg<D>::THREADS, 1)
         const int ks = e % C::KS, vs = e % C::VS;
         const uint32_t kp = (e / C::KS) & 1, vp = (e / C::VS) & 1;
         ++e;
-        const int k0 = t * kTile + warp * 16;          // first key of this warp
+        const int k0 = t * KT + warp * 16;          // first key of this warp
         const uint32_t sk = sbase + ks * C::TILE, sv = sbase + C::OFF_V + vs * C::TILE;
         const bool mine = k0 < u.keys;                 // any keys at all
         if (ok) ok = wait_all(full(ks), kp);
@@ -223,7 +229,7 @@ __global__ void __launch_bounds__(NarrowCfg<D>::THREADS, 1)
           for (int kk = 0; kk < D / 16; ++kk) {
             uint32_t b[4];
             const int ch = kk * 2 + chunk0;
-            ldsm4(sk + (ch >> 3) * (kTile * 128) + key * 128 + (((ch & 7) ^ (key & 7)) << 4), b);
+            ldsm4(sk + (ch >> 3) * (KT * 128) + key * 128 + (((ch & 7) ^ (key & 7)) << 4), b);
             mma16816(s[0], qf[kk], b[0], b[1]);
             mma16816(s[1], qf[kk], b[2], b[3]);
           }
@@ -293,7 +299,7 @@ __global__ void __launch_bounds__(NarrowCfg<D>::THREADS, 1)
             bool dirty = false;
 #pragma unroll 1
             for (int ch = (lane & 1) * (D / 16); ch < ((lane & 1) + 1) * (D / 16); ++ch) {
-              const uint32_t at = (ch >> 3) * (kTile * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4);
+              const uint32_t at = (ch >> 3) * (KT * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4);
               uint4* ptr = reinterpret_cast<uint4*>(smem + C::OFF_V + vs * C::TILE + at);
               if (key >= u.keys) {
                 *ptr = make_uint4(0u, 0u, 0u, 0u);
@@ -321,7 +327,7 @@ __global__ void __launch_bounds__(NarrowCfg<D>::THREADS, 1)
           for (int kk = 0; kk < D / 16; ++kk) {
             uint32_t b[4];
             const int ch = kk * 2 + chunk0;
-            ldsm4_t(sv + (ch >> 3) * (kTile * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4), b);
+            ldsm4_t(sv + (ch >> 3) * (KT * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4), b);
             mma16816(acc[2 * kk], pf, b[0], b[1]);
             mma16816(acc[2 * kk + 1], pf, b[2], b[3]);
           }
@@ -329,7 +335,7 @@ __global__ void __launch_bounds__(NarrowCfg<D>::THREADS, 1)
         mbar_arrive_warp(empty(C::KS + vs));
       }
 
-      // ---------------------------------------------------------- merge the eight warps
+      // ---------------------------------------------------------- merge the four warps
 #pragma unroll
       for (int hh = 0; hh < 2; ++hh) {
         l[hh] += __shfl_xor_sync(0xffffffffu, l[hh], 1);
@@ -369,14 +375,14 @@ __global__ void __launch_bounds__(NarrowCfg<D>::THREADS, 1)
       auto cell = [&](int w, int x, int hh) {
         return reinterpret_cast<float2*>(merge + (w * R + g + 8 * hh) * C::PITCH + x * 8 + 2 * tq);
       };
-      if (warp >= 4)
+      if (warp >= C::WARPS / 2)
 #pragma unroll
         for (int x = 0; x < D / 8; ++x)
 #pragma unroll
           for (int hh = 0; hh < 2; ++hh)
-            *cell(warp - 4, x, hh) = make_float2(acc[x][2 * hh], acc[x][2 * hh + 1]);
+            *cell(warp - C::WARPS / 2, x, hh) = make_float2(acc[x][2 * hh], acc[x][2 * hh + 1]);
       named_sync(1, 32 * C::WARPS);
-      if (warp < 4)
+      if (warp < C::WARPS / 2)
 #pragma unroll
         for (int x = 0; x < D / 8; ++x)
 #pragma unroll
@@ -388,9 +394,9 @@ __global__ void __launch_bounds__(NarrowCfg<D>::THREADS, 1)
           }
       named_sync(1, 32 * C::WARPS);
       {
-        // 16 threads a row, D / 16 columns each
-        constexpr int CPT = D / 16;
-        const int r = tid >> 4, c0 = (tid & 15) * CPT;
+        // eight threads a row, D / 8 columns each
+        constexpr int TPR = 32 * C::WARPS / R, CPT = D / TPR;
+        const int r = tid / TPR, c0 = (tid % TPR) * CPT;
         float mm = -INFINITY, ll = 0.f;
 #pragma unroll
         for (int w = 0; w < C::WARPS; ++w) mm = fmaxf(mm, ml[w * R + r]);
@@ -402,8 +408,7 @@ __global__ void __launch_bounds__(NarrowCfg<D>::THREADS, 1)
         float v[CPT];
 #pragma unroll
         for (int c = 0; c < CPT; ++c)
-          v[c] = (merge[r * C::PITCH + c0 + c] + merge[(R + r) * C::PITCH + c0 + c]) +
-                 (merge[(2 * R + r) * C::PITCH + c0 + c] + merge[(3 * R + r) * C::PITCH + c0 + c]);
+          v[c] = merge[r * C::PITCH + c0 + c] + merge[(R + r) * C::PITCH + c0 + c];
         const uint4 n0 = reinterpret_cast<const uint4*>(nf)[0], n1 = reinterpret_cast<const uint4*>(nf)[1];
         const bool any = (n0.x | n0.y | n0.z | n0.w | n1.x | n1.y | n1.z | n1.w) != 0;
         if (r < u.rows) {
@@ -417,10 +422,10 @@ __global__ void __launch_bounds__(NarrowCfg<D>::THREADS, 1)
 #pragma unroll
             for (int c = 0; c < CPT / 2; ++c) w[c] = pack_bf16(v[2 * c] * inv, v[2 * c + 1] * inv);
             __nv_bfloat16* dst = P.o + (u.s.row0 + node) * P.o_stride[0] + h * P.o_stride[1] + c0;
-            if constexpr (CPT == 8)
-              *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
-            else
-              *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+#pragma unroll
+            for (int c = 0; c < CPT / 8; ++c)
+              reinterpret_cast<uint4*>(dst)[c] =
+                  make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
             if (any) fix_row(P, u, nf, seen + r * 8, 0, CPT, c0, dst);
             if (c0 == 0)
               P.lse[static_cast<int64_t>(h) * P.total + u.s.row0 + node] =
@@ -462,7 +467,7 @@ constexpr int kJoinThreads = 256, kJoinShare = 12;
 template <int R, int D>
 __global__ void __launch_bounds__(kJoinThreads)
     tree_join_kernel(const __grid_constant__ TreeParams P, int blocks) {
-  constexpr int NW = kJoinThreads / 32, CPT = D / 32, RPW = R == kNarrowRows ? 2 : 4;
+  constexpr int NW = kJoinThreads / 32, CPT = D / 32, RPW = R == NarrowGeo::R ? 2 : 4;
   __shared__ float sums[NW][D + 1];
   grid_launch_dependents();
   grid_dependency_wait();
@@ -615,7 +620,7 @@ static fm_status launch_join(const TreeParams& P, int grid, cudaStream_t s) {
   // the blocks of a unit in two parts take its rows in one go
   prof_begin(K_TREE_JOIN, s);
   const cudaError_t e = launch_dependent(
-      tree_join_kernel<R, D>, dim3(grid - 1, ceil_div(P.part_rows, kJoinThreads / 32 * (R == kNarrowRows ? 2 : 4))), kJoinThreads,
+      tree_join_kernel<R, D>, dim3(grid - 1, ceil_div(P.part_rows, kJoinThreads / 32 * (R == NarrowGeo::R ? 2 : 4))), kJoinThreads,
       0, s, P, grid);
   prof_end(K_TREE_JOIN, s);
   return e == cudaSuccess ? FM_OK : FM_ERR_CUDA;
@@ -651,14 +656,19 @@ fm_status check_tree(const fm_cache* c, const fm_tree_desc* t) {
 // Workspace: the blocks' records, then their parts (two each).
 struct TreeWs {
   int rows;    // of a part: the largest unit's
+  int grid;
   size_t rec, ml, o, bytes;
 };
-TreeWs tree_ws(const fm_cache& c, const fm_tree_desc& t, int grid) {
+TreeWs tree_ws(const fm_cache& c, const fm_tree_desc& t, int sms) {
   auto up = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
   const int64_t rows =
       static_cast<int64_t>(t.max_nodes < t.total ? t.max_nodes : t.total) * (t.H / c.Hkv);
   TreeWs W;
-  W.rows = rows <= kNarrowRows ? kNarrowRows : (rows >= kWideRows ? kWideRows : (static_cast<int>(rows) + 31) / 32 * 32);
+  W.rows = rows <= NarrowGeo::R ? NarrowGeo::R
+           : rows >= WideGeo::R ? WideGeo::R
+                                : (static_cast<int>(rows) + 31) / 32 * 32;
+  W.grid = W.rows > MidGeo::R ? sms : 2 * sms;   // blocks per SM of the kernel for these rows
+  const int grid = W.grid;
   W.rec = 0;
   W.ml = up(static_cast<size_t>(grid) * sizeof(int4));
   W.o = W.ml + up(2ull * grid * W.rows * sizeof(float2));
@@ -690,13 +700,13 @@ fm_status fm_tree_fwd(const fm_cache* c, const fm_tree_desc* t, const void* q, c
   if (!table || !lens || !cu || !lse) return FM_ERR_INVALID;
   // masked scores are -inf and the largest score is the largest product
   if (!(scale > 0.f && scale < INFINITY)) return FM_ERR_INVALID;
-  const int grid = num_sms();
-  const TreeWs W = tree_ws(*c, *t, grid);
+  const TreeWs W = tree_ws(*c, *t, num_sms());
+  const int grid = W.grid;
   if (!aligned_to(ws, 256) || ws_bytes < W.bytes) return FM_ERR_WORKSPACE;
   // the length of the line of units (an upper bound) is counted in 31 bits
   const double units = static_cast<double>(c->Hkv) *
-                       (static_cast<double>(t->total) * (t->H / c->Hkv) / kNarrowRows + c->B);
-  if (units * (static_cast<double>(c->max_pages) * c->page_size / kTile + 5) >= 2147483647.0)
+                       (static_cast<double>(t->total) * (t->H / c->Hkv) / NarrowGeo::R + c->B);
+  if (units * (static_cast<double>(c->max_pages) * c->page_size / MidGeo::KT + 10) >= 2147483647.0)
     return FM_ERR_UNSUPPORTED;
   char* w = static_cast<char*>(ws);
   TreeParams P{};
@@ -707,10 +717,10 @@ fm_status fm_tree_fwd(const fm_cache* c, const fm_tree_desc* t, const void* q, c
   P.by_G = FastDiv::of(P.G);
   P.by_grid = FastDiv::of(grid);
   P.tree = parents != nullptr;
-  // Rows of the table that hold at most four tiles: units are not cut, and the
+  // Rows of the table that hold at most 512 tokens: units are not cut, and the
   // join (2.5 us after the first kernel) is spared; the tiles that a block then
   // takes in turn cost 0.4 us each.
-  P.whole = static_cast<int64_t>(c->max_pages) * c->page_size <= 4 * kTile;
+  P.whole = static_cast<int64_t>(c->max_pages) * c->page_size <= 512;
   P.scale_log2 = scale * 1.4426950408889634f;
   P.q = static_cast<const __nv_bfloat16*>(q);
   P.o = static_cast<__nv_bfloat16*>(o);
@@ -730,21 +740,28 @@ fm_status fm_tree_fwd(const fm_cache* c, const fm_tree_desc* t, const void* q, c
   const TestHooks th = test_hooks();
   P.wait_ns = th.wait_ns < 4000000000ull ? static_cast<uint32_t>(th.wait_ns) : 4000000000u;
   P.withhold = th.withhold;
-  // one page of one head is a box: page_size rows of 64 columns
+  // one page of one head, or a tile's part of it, is a box of 64 columns
+  const int box = W.rows > MidGeo::R ? c->page_size : c->page_size < MidGeo::KT ? c->page_size : MidGeo::KT;
+  P.box_shift = page_shift(box);
   CUtensorMap tk, tv;
-  if (!make_tmap_bshd(&tk, k_pool, c->n_pages, c->page_size, c->Hkv, c->d, c->k_stride + 1, c->page_size) ||
-      !make_tmap_bshd(&tv, v_pool, c->n_pages, c->page_size, c->Hkv, c->d, c->v_stride + 1, c->page_size))
+  if (!make_tmap_bshd(&tk, k_pool, c->n_pages, c->page_size, c->Hkv, c->d, c->k_stride + 1, box) ||
+      !make_tmap_bshd(&tv, v_pool, c->n_pages, c->page_size, c->Hkv, c->d, c->v_stride + 1, box))
     return FM_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool d64 = c->d == 64;
-  if (W.rows <= kNarrowRows) {
+  if (W.rows <= NarrowGeo::R) {
     st = d64 ? launch_narrow<64>(P, tk, tv, grid, s) : launch_narrow<128>(P, tk, tv, grid, s);
     if (st != FM_OK) return st;
-    return d64 ? launch_join<kNarrowRows, 64>(P, grid, s) : launch_join<kNarrowRows, 128>(P, grid, s);
+    return d64 ? launch_join<NarrowGeo::R, 64>(P, grid, s) : launch_join<NarrowGeo::R, 128>(P, grid, s);
+  }
+  if (W.rows <= MidGeo::R) {
+    st = launch_tree_mid(P, c->d, tk, tv, grid, s);
+    if (st != FM_OK) return st;
+    return d64 ? launch_join<MidGeo::R, 64>(P, grid, s) : launch_join<MidGeo::R, 128>(P, grid, s);
   }
   st = launch_tree_wide(P, c->d, tk, tv, grid, s);
   if (st != FM_OK) return st;
-  return d64 ? launch_join<kWideRows, 64>(P, grid, s) : launch_join<kWideRows, 128>(P, grid, s);
+  return d64 ? launch_join<WideGeo::R, 64>(P, grid, s) : launch_join<WideGeo::R, 128>(P, grid, s);
 }
 
 }  // extern "C"

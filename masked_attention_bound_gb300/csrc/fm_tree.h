@@ -3,7 +3,7 @@
 // Work is cut into units and tiles.  A unit is one (sequence, K/V head, row
 // tile): up to R rows, row r of a sequence being node r / G of query head hk *
 // G + r % G, so the G query heads that share a K/V head share its loads.  A
-// unit walks the 128-key tiles [0, tiles) of its sequence up to its last
+// unit walks the 64- or 128-key tiles [0, tiles) of its sequence up to its last
 // node.  All units, in order, form one line on which a unit is as long as its
 // tiles and its fixed cost (writing its rows, fetching the next one's; END
 // tiles); each block takes an equal run of it, whatever the lengths, so one
@@ -21,6 +21,7 @@ namespace fm {
 
 struct TreeParams {
   int B, H, Hkv, G, total, max_nodes, page_shift, n_pages, max_pages;
+  int box_shift;           // log2 of the rows of a TMA box, min(page_size, tile)
   int tree;                // 0: chain (no parents)
   int whole;               // units are not cut: no parts, no join
   FastDiv by_G, by_grid;
@@ -70,36 +71,52 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeParams& P, int b) {
   return s;
 }
 
+// Geometry of the three kernels: rows of a unit, keys of a tile, and a unit's
+// fixed cost in tiles.
+struct NarrowGeo {
+  static constexpr int R = 16, KT = 64;
+  __device__ static __forceinline__ int end(int) { return 2; }
+};
+struct MidGeo {
+  static constexpr int R = 128, KT = 64;
+  __device__ static __forceinline__ int end(int) { return 4; }
+};
+struct WideGeo {
+  static constexpr int R = 256, KT = 128;
+  // a block with a unit's end in its run took 12000 (256 rows) to 20000
+  // cycles (128 rows) longer, where a tile takes 3100 and 2800
+  __device__ static __forceinline__ int end(int rows) { return rows > 128 ? 5 : 10; }
+};
+
 // Row tiles of a sequence, keys and tiles of one of them (total * H is at
 // most 2^30: 32 bits hold every row).
-template <int R>
+template <class Geo>
 __device__ __forceinline__ int row_tiles(const TreeParams& P, const TreeSeq& s) {
-  return (s.n * P.G + R - 1) / R;
+  return (s.n * P.G + Geo::R - 1) / Geo::R;
 }
-template <int R>
+template <class Geo>
 __device__ __forceinline__ int unit_keys(const TreeParams& P, const TreeSeq& s, int rt) {
   if (s.base < 0) return 0;
-  return s.base + P.by_G(min(s.n * P.G, (rt + 1) * R) - 1) + 1;
+  return s.base + P.by_G(min(s.n * P.G, (rt + 1) * Geo::R) - 1) + 1;
 }
+template <class Geo>
 __device__ __forceinline__ int key_tiles(int keys) {
-  return keys > 0 ? (keys + kTile - 1) / kTile : 1;
+  return keys > 0 ? (keys + Geo::KT - 1) / Geo::KT : 1;
 }
-// A unit's length on the line.  Its fixed cost in tiles, measured: a block
-// with a unit's end in its run took 12000 (256 rows) to 20000 cycles (128
-// rows) longer, where a tile takes 3100 and 2800; 1 for the narrow kernel.
-// With P.whole a unit is a point of the line and never cut.
-template <int R>
+// A unit's length on the line.  With P.whole a unit is a point of the line and
+// never cut.
+template <class Geo>
 __device__ __forceinline__ int unit_length(const TreeParams& P, const TreeSeq& s, int rt, int tiles) {
-  return P.whole ? 1 : tiles + (R <= 16 ? 1 : (s.n * P.G - rt * R > 128 ? 5 : 10));
+  return P.whole ? 1 : tiles + Geo::end(s.n * P.G - rt * Geo::R);
 }
 // Length of all units of one K/V head of a sequence.  (The launch checks that
 // the line's length fits in 31 bits.)
-template <int R>
+template <class Geo>
 __device__ __forceinline__ uint32_t seq_length(const TreeParams& P, const TreeSeq& s) {
-  const int nr = row_tiles<R>(P, s);
+  const int nr = row_tiles<Geo>(P, s);
   uint32_t w = 0;
 #pragma unroll 1
-  for (int rt = 0; rt < nr; ++rt) w += unit_length<R>(P, s, rt, key_tiles(unit_keys<R>(P, s, rt)));
+  for (int rt = 0; rt < nr; ++rt) w += unit_length<Geo>(P, s, rt, key_tiles<Geo>(unit_keys<Geo>(P, s, rt)));
   return w;
 }
 
@@ -132,7 +149,7 @@ struct TreeRun {
 // adds up the lengths of sequences [l m, l m + m), m = ceil(B / 32); one scan
 // over the lanes, and the lane whose sequences hold the run's start looks for
 // it among them.
-template <int R>
+template <class Geo>
 __device__ __forceinline__ TreeRun tree_run(const TreeParams& P) {
   constexpr unsigned ALL = 0xffffffffu;
   const int lane = threadIdx.x & 31;
@@ -144,7 +161,7 @@ __device__ __forceinline__ TreeRun tree_run(const TreeParams& P) {
   for (int b = b0; b < b1; ++b) {
     s = tree_seq(P, b);
     if (s.base < 0 && blockIdx.x == 0 && P.status) atomicOr(P.status, DEV_CACHE);
-    w += seq_length<R>(P, s) * P.Hkv;
+    w += seq_length<Geo>(P, s) * P.Hkv;
   }
   uint32_t inc = w;
 #pragma unroll
@@ -169,7 +186,7 @@ __device__ __forceinline__ TreeRun tree_run(const TreeParams& P) {
 #pragma unroll 1
     for (;; ++b) {
       if (m > 1) s = tree_seq(P, b);
-      per = seq_length<R>(P, s);
+      per = seq_length<Geo>(P, s);
       if (off < per * P.Hkv) break;
       off -= per * P.Hkv;
     }
@@ -178,7 +195,7 @@ __device__ __forceinline__ TreeRun tree_run(const TreeParams& P) {
     off -= run.hk * per;
 #pragma unroll 1
     while (true) {
-      const uint32_t t = unit_length<R>(P, s, run.rt, key_tiles(unit_keys<R>(P, s, run.rt)));
+      const uint32_t t = unit_length<Geo>(P, s, run.rt, key_tiles<Geo>(unit_keys<Geo>(P, s, run.rt)));
       if (off < t) break;
       off -= t;
       ++run.rt;
@@ -207,7 +224,7 @@ struct TreePiece {
 };
 
 // Every role of a block walks its run piece by piece in the same order.
-template <int R>
+template <class Geo>
 struct TreeWalk {
   TreeRun run;
   __device__ __forceinline__ bool next(const TreeParams& P, TreePiece& u) {
@@ -224,16 +241,16 @@ struct TreeWalk {
       }
       u.hk = run.hk;
       u.rt = run.rt;
-      u.keys = unit_keys<R>(P, s, run.rt);
-      u.tiles = key_tiles(u.keys);
+      u.keys = unit_keys<Geo>(P, s, run.rt);
+      u.tiles = key_tiles<Geo>(u.keys);
       u.t0 = run.tile;
       u.t1 = P.whole ? u.tiles : min(u.tiles, run.tile + run.left);
-      const int end = u.t1 < u.tiles ? u.t1 : unit_length<R>(P, s, run.rt, u.tiles);
+      const int end = u.t1 < u.tiles ? u.t1 : unit_length<Geo>(P, s, run.rt, u.tiles);
       run.left -= end - run.tile;
       run.tile = end;
       if (u.t1 >= u.tiles) {
         run.tile = 0;
-        if (++run.rt >= row_tiles<R>(P, s)) {
+        if (++run.rt >= row_tiles<Geo>(P, s)) {
           run.rt = 0;
           ++run.hk;
         }
@@ -242,8 +259,8 @@ struct TreeWalk {
     }
     u.b = run.b;
     u.s = s;
-    u.row_first = u.rt * R;
-    u.rows = min(R, s.n * P.G - u.row_first);
+    u.row_first = u.rt * Geo::R;
+    u.rows = min(Geo::R, s.n * P.G - u.row_first);
     u.origin = s.base + (P.tree ? 0 : P.by_G(u.row_first));
     return true;
   }
@@ -302,29 +319,29 @@ __device__ __forceinline__ bool tree_wait(uint32_t bar, uint32_t parity, const T
 }
 
 // ---------------------------------------------------------------- K/V loads
-// One 128-key tile of K or V (a pool's tensor map) into shared memory:
-// page_size rows of 64 columns per copy, the tile's two 64-column slabs 16 KB
-// apart.  Pages past the unit's keys are not loaded.  All 32 lanes call it;
-// `page`: this lane's (lane_page); `policy`: evict first, since a stream of K
-// and V through L2 would push out what the next piece needs, the kernel's
-// own instructions among it (a fetch from DRAM behind the stream took 5000
-// cycles).
-template <int D>
+// One KT-key tile of K or V (a pool's tensor map) into shared memory: boxes of
+// min(page_size, KT) rows of 64 columns, the tile's two 64-column slabs KT *
+// 128 bytes apart.  Boxes past the unit's keys are not loaded.  All 32 lanes
+// call it; `page`: this lane's (lane_page); `policy`: evict first, since a
+// stream of K and V through L2 would push out what the next piece needs, the
+// kernel's own instructions among it (a fetch from DRAM behind the stream took
+// 5000 cycles).
+template <int D, int KT>
 struct TileLoad {
   static constexpr int SLABS = D / 64;
-  // pages of the tile that hold keys of the unit
-  __device__ static __forceinline__ int pages(const TreeParams& P, const TreePiece& u, int tile) {
-    const int keys = min(u.keys - tile * kTile, kTile);
-    return keys <= 0 ? 0 : (keys + (1 << P.page_shift) - 1) >> P.page_shift;
+  // boxes of the tile that hold keys of the unit
+  __device__ static __forceinline__ int boxes(const TreeParams& P, const TreePiece& u, int tile) {
+    const int keys = min(u.keys - tile * KT, KT);
+    return keys <= 0 ? 0 : (keys + (1 << P.box_shift) - 1) >> P.box_shift;
   }
-  // lane l: page index of the pool for page l / SLABS of the tile, one past
+  // lane l: page of the pool that holds box l / SLABS of the tile, one past
   // the pool (which TMA reads as zeros) if the table's entry is out of range
   __device__ static __forceinline__ int lane_page(const TreeParams& P, const TreePiece& u, int tile,
                                                   int lane) {
     const int j = lane / SLABS;
-    if (j >= pages(P, u, tile)) return 0;
+    if (j >= boxes(P, u, tile)) return 0;
     const int pg = P.table[static_cast<int64_t>(u.b) * P.max_pages +
-                           tile * (kTile >> P.page_shift) + j];
+                           ((tile * KT + (j << P.box_shift)) >> P.page_shift)];
     if (pg >= 0 && pg < P.n_pages) return pg;
     if (P.status) atomicOr(P.status, DEV_CACHE);
     return P.n_pages;
@@ -332,13 +349,13 @@ struct TileLoad {
   __device__ static __forceinline__ void issue(const TreeParams& P, const TreePiece& u, int tile,
                                                int lane, int page, const CUtensorMap* tm,
                                                uint32_t dst, uint32_t bar, uint64_t policy) {
-    const int n = pages(P, u, tile);
-    if (lane == 0) mbar_arrive_expect_tx(bar, (n << P.page_shift) * D * 2);
+    const int n = boxes(P, u, tile);
+    if (lane == 0) mbar_arrive_expect_tx(bar, (n << P.box_shift) * D * 2);
     __syncwarp();
     const int j = lane / SLABS, slab = lane % SLABS;
     if (j < n)
-      tma_load_4d_hint(dst + slab * (kTile * 128) + (j << P.page_shift) * 128, tm, bar, slab * 64, u.hk,
-                       0, page, policy);
+      tma_load_4d_hint(dst + slab * (KT * 128) + (j << P.box_shift) * 128, tm, bar, slab * 64, u.hk,
+                       (tile * KT + (j << P.box_shift)) & ((1 << P.page_shift) - 1), page, policy);
   }
 };
 
@@ -358,9 +375,6 @@ __device__ __forceinline__ uint32_t bf16x2_clean(uint32_t x) {
   if ((x & 0x7f800000u) == 0x7f800000u) x &= 0xffffu;
   return x;
 }
-
-// Row tiles of the two kernels.
-constexpr int kNarrowRows = 16, kWideRows = 256;
 
 // Adds to x what the keys flagged in nf (bit i: key origin + i) and seen
 // (bit i of `seen`) hold in column c, if that is not finite.
@@ -399,8 +413,10 @@ static __device__ __noinline__ void fix_row(const TreeParams& P, const TreePiece
   }
 }
 
-// The kernel for units of up to 256 rows (fm_tree_wide.cu) and the join of
-// either kernel's parts (fm_tree.cu).
+// The kernels for units of up to 128 and 256 rows (fm_tree_wide.cu); the one
+// for up to 16 rows and the join of their parts are in fm_tree.cu.
+fm_status launch_tree_mid(const TreeParams& P, int d, const CUtensorMap& tk, const CUtensorMap& tv,
+                          int grid, cudaStream_t s);
 fm_status launch_tree_wide(const TreeParams& P, int d, const CUtensorMap& tk, const CUtensorMap& tv,
                            int grid, cudaStream_t s);
 

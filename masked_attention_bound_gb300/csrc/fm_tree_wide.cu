@@ -1,74 +1,86 @@
-// Attention over the paged cache for units of up to 256 rows (drafted trees,
-// causal runs, many query heads per K/V head), on the 5th-generation tensor
-// cores.
+// Attention over the paged cache for units of up to 128 or 256 rows (drafted
+// trees, causal runs, many query heads per K/V head), on the 5th-generation
+// tensor cores.
 //
-// A unit's rows fill one or two 128-row tiles of tcgen05.mma.  The block has
-// two slots, each with its own S/P and O in tensor memory, its own warpgroup
-// of softmax threads (thread = row = TMEM lane) and its own MMA thread, so
-// that one slot's softmax runs while the other's products do:
-//  - up to 128 rows: both slots hold the same rows and take the key tiles
-//    in turn; their O, maximum and sum are merged at the end of the piece.
-//    K and V are read once for all rows; such units are bound by that;
-//  - up to 256 rows: slot s holds rows [128 s, 128 s + 128) and both walk
+// A unit's rows fill one or two 128-row tiles of tcgen05.mma.  A slot is an
+// S/P and an O in tensor memory, a warpgroup of softmax threads (thread = row
+// = TMEM lane) and an MMA warp.
+//
+// SLOTS = 1 (up to 128 rows, bound by reading K and V): 64-key tiles and two
+// blocks per SM, so that one's fetching and writing at the ends of units run
+// while the other's tiles stream.  S has two buffers: S of a tile is computed
+// while the softmax of the one before runs, and its PV while that of the next.
+//
+// SLOTS = 2 (some unit has more than 128 rows): 128-key tiles, one block per
+// SM, one slot's softmax running while the other's products do:
+//  - more than 128 rows: slot s holds rows [128 s, 128 s + 128) and both walk
 //    every tile, so a tile is loaded once for 256 rows; such units are bound
-//    by the softmax and the tensor pipe.
-// Twelve warps: 0-3 / 4-7 softmax of slot 0 / 1, 8 loads K, 10 loads V, 9 /
-// 11 issue the MMAs of slot 0 / 1.  The softmax warps also put Q into shared
-// memory (rows of a unit are nodes times query heads: any group size, one
-// 256-byte row per thread) and clean the V tiles that hold drafted nodes.
-// TMEM: S/P of slot s at [128 s, 128 s + 128), O at [256 + 128 s, .. + D).
+//    by the softmax and the tensor pipe;
+//  - up to 128 rows: both slots hold the same rows and take the key tiles in
+//    turn; their O, maximum and sum are merged at the end of the piece.
+//
+// Warps: 4 per slot for the softmax, then one that loads K, slot 0's MMAs, one
+// that loads V, slot 1's MMAs.  The softmax warps also put Q into shared
+// memory (rows of a unit are nodes times query heads: any group size) and
+// clean the V tiles that hold drafted nodes.
+// TMEM: S/P of slot s at column 128 s (SLOTS = 1: of every second tile at
+// column 64), the O's after the S's.
+#include <type_traits>
+
 #include "fm_tree.h"
 
 namespace fm {
 
-// ROWS: units may have more than 128 rows; without it there is one Q tile,
-// and its room holds another K tile.
-template <int D, bool ROWS>
+template <int D, int SLOTS_>
 struct WideCfg {
-  static constexpr int TILE = kTile * D * 2;
-  static constexpr int QTILES = ROWS ? 2 : 1;
-  static constexpr int KSTAGES = ROWS ? 2 : 3, VSTAGES = 3;
-  static constexpr int OFF_Q = 0;                       // one tile, or one per slot
-  static constexpr int OFF_K = QTILES * TILE;
+  static constexpr int SLOTS = SLOTS_;
+  using Geo = std::conditional_t<SLOTS == 2, WideGeo, MidGeo>;
+  static constexpr int KT = Geo::KT;
+  static constexpr int TILE = KT * D * 2;               // bytes of a K or V tile
+  static constexpr int QTILE = 128 * D * 2;             // of a slot's Q
+  static constexpr int KSTAGES = D == 64 ? 4 : 2, VSTAGES = D == 64 ? 5 : 3;
+  static constexpr int SM_WARPS = 4 * SLOTS;            // softmax
+  static constexpr int THREADS = 32 * (SM_WARPS + 4);
+  static constexpr int BLOCKS = SLOTS == 2 ? 1 : 2;     // per SM
+  static constexpr int OFF_Q = 0;
+  static constexpr int OFF_K = SLOTS * QTILE;
   static constexpr int OFF_V = OFF_K + KSTAGES * TILE;
-  static constexpr int OFF_ML = OFF_V + VSTAGES * TILE; // float2 [slot][128]
-  static constexpr int OFF_NF = OFF_ML + 2 * 128 * 8;   // [2][8] keys with values not finite
+  static constexpr int OFF_ML = OFF_V + VSTAGES * TILE; // SLOTS 2: float2 [slot][128]
+  static constexpr int OFF_NF = OFF_ML + (SLOTS == 2 ? 2 * 128 * 8 : 0);   // [2][8] keys with values not finite
   static constexpr int OFF_BAR = OFF_NF + 64;
-  static constexpr int NBAR = 26;
+  static constexpr int NBAR = 33;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;   // abort flag, TMEM address
   static constexpr int OFF_PAR = OFF_MISC + 16;         // int16 [256] parents of the unit's nodes
-  // 4 KB per softmax warp through which O is written: the Q tiles, where they
-  // are large enough (they are not needed any more by then)
-  static constexpr bool STAGE_IN_Q = QTILES * TILE >= 8 * 4096;
-  static constexpr int OFF_STAGE = STAGE_IN_Q ? OFF_Q : (OFF_PAR + 512 + 127) / 128 * 128;
-  static constexpr int USED = STAGE_IN_Q ? OFF_PAR + 512 : OFF_STAGE + 8 * 4096;
-  // one block per SM: it takes all of the tensor memory
-  static constexpr int SMEM = USED > 120 * 1024 ? USED : 120 * 1024;
-  static constexpr int THREADS = 384;
-  // register split as in the prompt forward: 2 x 128 x 216 + 128 x 72 = 384 x 168
-  static constexpr uint32_t REGS_SOFTMAX = 216, REGS_PRODUCER = 72;
+  static constexpr int USED = OFF_PAR + 512;
+  static constexpr int SMEM = USED;
+  static_assert(BLOCKS * (SMEM + 1024) <= 228 * 1024, "blocks per SM");
+  // O is written through 4 KB per softmax warp, in the Q tiles: they are not
+  // needed any more by then
+  static_assert(SM_WARPS * 4096 <= SLOTS * QTILE, "room for the output's staging");
+  static constexpr uint32_t T_COLS = 256 * SLOTS, T_O = 128 * SLOTS;
+  // register split: the softmax warpgroups' and the others' budgets add up to
+  // what the block is launched with (384 x 168, 256 x 128)
+  static constexpr uint32_t REGS_SOFTMAX = SLOTS == 2 ? 216 : 184, REGS_PRODUCER = 72;
   static constexpr int MIN_LAUNCH_REGS =
-      (2 * 128 * REGS_SOFTMAX + 128 * REGS_PRODUCER + THREADS - 1) / THREADS;
+      (32 * SM_WARPS * REGS_SOFTMAX + 128 * REGS_PRODUCER + THREADS - 1) / THREADS;
 };
 
 enum {
-  W_QFULL = 0, W_SFULL = 2, W_PFULL = 4, W_PVDONE = 6, W_OEMPTY = 8, W_KFULL = 10, W_KEMPTY = 13,
-  W_VFULL = 16, W_VEMPTY = 19, W_DRAIN = 22, W_TURN = 23
+  W_QFULL = 0, W_SFULL = 2, W_PFULL = 4, W_PVDONE = 6, W_OEMPTY = 8, W_KFULL = 10, W_KEMPTY = 15,
+  W_VFULL = 20, W_VEMPTY = 25, W_DRAIN = 30, W_TURN = 31,
+  W_PVTILE = W_PVDONE + 1   // SLOTS 1: the PV of each tile (the SFULL and PFULL are its two buffers')
 };
 
-// How the two slots share a piece.
+// How the slots share a piece.
 struct WideSplit {
   bool rows;     // slots split the rows (else the key tiles)
   int n;         // key tiles of the piece
   // slot s takes part at all
-  __device__ __forceinline__ bool active(int s) const {
-    return s == 0 || rows || n > 1;
-  }
-  __device__ __forceinline__ bool takes(int s, int x) const { return rows || (x & 1) == s; }
+  __device__ __forceinline__ bool active(int s) const { return s == 0 || rows || n > 1; }
 };
-template <bool ROWS>
+template <int SLOTS>
 __device__ __forceinline__ WideSplit wide_split(const TreePiece& u) {
-  return WideSplit{ROWS && u.rows > 128, u.keys > 0 ? u.t1 - u.t0 : 0};
+  return WideSplit{SLOTS == 1 || u.rows > 128, u.keys > 0 ? u.t1 - u.t0 : 0};
 }
 
 // 16 bytes from global to shared memory without a register or a line of L1;
@@ -81,14 +93,19 @@ __device__ __forceinline__ void copy_async_wait() {
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-__device__ __forceinline__ void slots_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+// All softmax warps.
+template <int SLOTS>
+__device__ __forceinline__ void slots_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(128 * SLOTS) : "memory");
+}
 
-template <int D, bool ROWS>
-__global__ void __launch_bounds__(WideCfg<D, ROWS>::THREADS, 1)
+template <int D, int SLOTS>
+__global__ void __launch_bounds__(WideCfg<D, SLOTS>::THREADS, WideCfg<D, SLOTS>::BLOCKS)
     tree_wide_kernel(const __grid_constant__ TreeParams P, const __grid_constant__ CUtensorMap tmK,
                      const __grid_constant__ CUtensorMap tmV) {
-  using C = WideCfg<D, ROWS>;
-  constexpr int R = kWideRows;
+  using C = WideCfg<D, SLOTS>;
+  using Load = TileLoad<D, C::KT>;
+  constexpr int KT = C::KT;
   extern __shared__ __align__(1024) uint8_t smem[];
   if (smem_u32(smem) & 1023u) {
     if (threadIdx.x == 0 && P.status) atomicOr(P.status, DEV_LAYOUT);
@@ -100,7 +117,7 @@ __global__ void __launch_bounds__(WideCfg<D, ROWS>::THREADS, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC + 4);
   uint32_t* nf_all = reinterpret_cast<uint32_t*>(smem + C::OFF_NF);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  constexpr int K_WARP = 8, MMA_WARP = 9, V_WARP = 10;   // 11: slot 1's MMAs
+  constexpr int K_WARP = C::SM_WARPS, MMA_WARP = K_WARP + 1, V_WARP = K_WARP + 2, MMA_WARP_B = K_WARP + 3;
 
   if (warp == 2) touch_memory<D>(P, lane);
   if (tid == 0) {
@@ -109,26 +126,26 @@ __global__ void __launch_bounds__(WideCfg<D, ROWS>::THREADS, 1)
       mbar_init(bar(W_SFULL + s), 1);
       mbar_init(bar(W_PFULL + s), 4);
       mbar_init(bar(W_PVDONE + s), 1);
-      mbar_init(bar(W_OEMPTY + s), 8);    // both slots' warps may read O of either
+      mbar_init(bar(W_OEMPTY + s), C::SM_WARPS);   // every slot's warps may read O of either
       mbar_init(bar(W_TURN + s), 1);
     }
-    // a stage is free after two commits: one by each MMA thread, or both by
-    // the one whose slot took the tile
+    // a stage is free after a commit per slot: one by each MMA warp, or both
+    // by the one whose slot took the tile
     for (int i = 0; i < C::KSTAGES; ++i) {
       mbar_init(bar(W_KFULL + i), 1);
-      mbar_init(bar(W_KEMPTY + i), 2);
+      mbar_init(bar(W_KEMPTY + i), SLOTS);
     }
     for (int i = 0; i < C::VSTAGES; ++i) {
       mbar_init(bar(W_VFULL + i), 1);
-      mbar_init(bar(W_VEMPTY + i), 2);
+      mbar_init(bar(W_VEMPTY + i), SLOTS);
     }
-    mbar_init(bar(W_DRAIN), 2);
+    mbar_init(bar(W_DRAIN), SLOTS);
     *abort_flag = 0;
     fence_barrier_init();
   }
   if (tid < 16) nf_all[tid] = 0;
   if (warp == MMA_WARP) {
-    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_alloc(smem_u32(tmem_slot), C::T_COLS);
     tmem_relinquish();
   }
   if (warp == K_WARP && lane == 0) tma_prefetch_desc(&tmK);
@@ -136,8 +153,8 @@ __global__ void __launch_bounds__(WideCfg<D, ROWS>::THREADS, 1)
   grid_launch_dependents();
   grid_dependency_wait();
   tc_fence_before();
-  TreeWalk<R> walk;
-  walk.run = tree_run<R>(P);
+  TreeWalk<typename C::Geo> walk;
+  walk.run = tree_run<typename C::Geo>(P);
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = *tmem_slot;
@@ -148,7 +165,7 @@ __global__ void __launch_bounds__(WideCfg<D, ROWS>::THREADS, 1)
     return __all_sync(0xffffffffu, wait(b, parity));
   };
 
-  if (warp >= 8) {
+  if (warp >= C::SM_WARPS) {
     regs_decrease<C::REGS_PRODUCER>();
     if (warp == K_WARP || warp == V_WARP) {
       // ---------------------------------------------------------- K / V loads
@@ -163,13 +180,13 @@ __global__ void __launch_bounds__(WideCfg<D, ROWS>::THREADS, 1)
       bool ok = true;
       while (ok && walk.next(P, u)) {
         if (u.keys == 0) continue;
-        int page = TileLoad<D>::lane_page(P, u, u.t0, lane);
+        int page = Load::lane_page(P, u, u.t0, lane);
 #pragma unroll 1
         for (int t = u.t0; t < u.t1; ++t) {
-          const int next = t + 1 < u.t1 ? TileLoad<D>::lane_page(P, u, t + 1, lane) : 0;
+          const int next = t + 1 < u.t1 ? Load::lane_page(P, u, t + 1, lane) : 0;
           if (use > 0) ok = wait_all(b_empty + st, (use - 1) & 1);
           if (!ok) break;
-          TileLoad<D>::issue(P, u, t, lane, page, tm, buf + st * C::TILE, bar(b_full + st), policy);
+          Load::issue(P, u, t, lane, page, tm, buf + st * C::TILE, bar(b_full + st), policy);
           ++issued;
           if (++st == stages) {
             st = 0;
@@ -184,17 +201,17 @@ __global__ void __launch_bounds__(WideCfg<D, ROWS>::THREADS, 1)
         for (uint32_t x = issued > stages ? issued - stages : 0; x < issued; ++x)
           mbar_wait(bar(b_full + x % stages), (x / stages) & 1, P.status, P.wait_ns);
       __syncwarp();
-    } else {
+    } else if (warp == MMA_WARP || (SLOTS == 2 && warp == MMA_WARP_B)) {
       // ---------------------------------------------------------- MMA issuers
       // The whole warp walks and waits, and one elected lane issues: the
       // descriptors are then uniform, and an MMA costs its issue only.
-      const int s = warp - MMA_WARP >> 1;
-      constexpr uint32_t idS = idesc_bf16(128, 128, false, false);
+      const int s = warp == MMA_WARP ? 0 : 1;
+      constexpr uint32_t idS = idesc_bf16(128, KT, false, false);
       constexpr uint32_t idPV = idesc_bf16(128, D, false, true);
-      const uint32_t dQ = sdesc_lo(sbase + C::OFF_Q + (ROWS ? s * C::TILE : 0), 16);
+      const uint32_t dQ = sdesc_lo(sbase + C::OFF_Q + s * C::QTILE, 16);
       const uint32_t dK0 = sdesc_lo(sbase + C::OFF_K, 16);
-      const uint32_t dV0 = sdesc_lo(sbase + C::OFF_V, kTile * 128);
-      const uint32_t tS = tbase + 128 * s, tO = tbase + 256 + 128 * s;
+      const uint32_t dV0 = sdesc_lo(sbase + C::OFF_V, KT * 128);
+      const uint32_t tS = tbase + 128 * s, tO = tbase + C::T_O + 128 * s;
       uint32_t kst = 0, kph = 0, vst = 0, vph = 0;   // stages and phases of the next tile of the block
       uint32_t pieces = 0;      // pieces with keys before this one
       uint32_t qn = 0, np = 0;  // Q tiles, P tiles of this slot so far
@@ -202,7 +219,7 @@ __global__ void __launch_bounds__(WideCfg<D, ROWS>::THREADS, 1)
       bool ok = true;
       TreePiece u;
       while (ok && walk.next(P, u)) {
-        const WideSplit w = wide_split<ROWS>(u);
+        const WideSplit w = wide_split<SLOTS>(u);
         if (w.n == 0) continue;
         // The two MMA warps take turns: a turn is one tile's PV and the next
         // one's S.  Without it the slots fall into step (both wait for the
@@ -210,10 +227,11 @@ __global__ void __launch_bounds__(WideCfg<D, ROWS>::THREADS, 1)
         // tensor pipe: 4900 cycles a pair of tiles); with turns one slot's
         // MMAs run while the other's softmax does.
         auto my_turn = [&]() -> bool {
+          if constexpr (SLOTS == 1) return true;
           return s == 0 ? (turn == 0 || wait_all(W_TURN + 1, (turn - 1) & 1)) : wait_all(W_TURN, turn & 1);
         };
         auto end_turn = [&]() {
-          if (elect_one()) mbar_arrive(bar(W_TURN + s));
+          if (SLOTS == 2 && elect_one()) mbar_arrive(bar(W_TURN + s));
           ++turn;
         };
         // stages advance by the piece's tiles; the slot's own tiles are every
@@ -230,8 +248,58 @@ __global__ void __launch_bounds__(WideCfg<D, ROWS>::THREADS, 1)
         uint32_t ks = kst, kp = kph, vs = vst, vp = vph;        // of tiles x (K) and x - step (V)
         advance(ks, kp, x0, C::KSTAGES);
         advance(vs, vp, x0, C::VSTAGES);
-        if (w.active(s)) ok = wait_all(W_QFULL + (ROWS ? s : 0), qn & 1);
-        if (!ROWS || w.active(s)) ++qn;
+        if (w.active(s)) {
+          ok = wait_all(W_QFULL + s, qn & 1);
+          ++qn;
+        }
+        if constexpr (SLOTS == 1) {
+          // S of tile x + 1 overwrites P of tile x - 1, whose PV this warp has
+          // issued before; then PV of tile x
+          auto issue_s = [&](uint32_t tile) {
+            const uint32_t dK = dK0 + ks * (C::TILE >> 4);
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk)
+                mma_ss(tS + 64 * (tile & 1), sdesc_at(dQ, (kk >> 2) * (128 * 128) + (kk & 3) * 32),
+                       sdesc_at(dK, (kk >> 2) * (KT * 128) + (kk & 3) * 32), idS, kk > 0 ? 1u : 0u);
+              mma_commit(bar(W_SFULL + (tile & 1)));
+              mma_commit(bar(W_KEMPTY + ks));
+            }
+            __syncwarp();
+            advance(ks, kp, 1, C::KSTAGES);
+          };
+          if (ok) ok = wait_all(W_KFULL + ks, kp);
+          if (ok) issue_s(np);
+#pragma unroll 1
+          for (int x = 0; ok && x < w.n; ++x, ++np) {
+            if (x + 1 < w.n) {
+              ok = wait_all(W_KFULL + ks, kp);
+              if (!ok) break;
+              issue_s(np + 1);
+            }
+            ok = wait_all(W_VFULL + vs, vp);
+            // O is overwritten: the last piece's must have been read
+            if (ok && x == 0 && pieces > 0) ok = wait_all(W_OEMPTY, (pieces - 1) & 1);
+            if (ok) ok = wait_all(W_PFULL + (np & 1), (np >> 1) & 1);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t dV = dV0 + vs * (C::TILE >> 4), tP = tS + 64 * (np & 1);
+            if (elect_one()) {
+#pragma unroll
+              for (int kk = 0; kk < KT / 16; ++kk)
+                mma_ts(tO, tP + kk * 8, sdesc_at(dV, kk * 2048), idPV, (x > 0 || kk > 0) ? 1u : 0u);
+              mma_commit(bar(W_PVTILE));
+              if (x + 1 == w.n) mma_commit(bar(W_PVDONE));
+              mma_commit(bar(W_VEMPTY + vs));
+            }
+            __syncwarp();
+            advance(vs, vp, 1, C::VSTAGES);
+          }
+          kst = ks; kph = kp; vst = vs; vph = vp;
+          ++pieces;
+          continue;
+        }
         int x = x0;
 #pragma unroll 1
         for (int i = 0; ok && i < turns; ++i) {
@@ -259,7 +327,7 @@ __global__ void __launch_bounds__(WideCfg<D, ROWS>::THREADS, 1)
             const uint32_t dV = dV0 + vs * (C::TILE >> 4);
             if (elect_one()) {
 #pragma unroll
-              for (int kk = 0; kk < kTile / 16; ++kk)
+              for (int kk = 0; kk < KT / 16; ++kk)
                 mma_ts(tO, tS + kk * 8, sdesc_at(dV, kk * 2048), idPV, (i > 1 || kk > 0) ? 1u : 0u);
               if (!sn) mma_commit(bar(W_PVDONE + s));
               mma_commit(bar(W_VEMPTY + vs));
@@ -282,11 +350,11 @@ __global__ void __launch_bounds__(WideCfg<D, ROWS>::THREADS, 1)
             if (elect_one()) {
 #pragma unroll
               for (int kk = 0; kk < D / 16; ++kk) {
-                const uint32_t off = (kk >> 2) * (kTile * 128) + (kk & 3) * 32;
-                mma_ss(tS, sdesc_at(dQ, off), sdesc_at(dK, off), idS, kk > 0 ? 1u : 0u);
+                mma_ss(tS, sdesc_at(dQ, (kk >> 2) * (128 * 128) + (kk & 3) * 32),
+                       sdesc_at(dK, (kk >> 2) * (KT * 128) + (kk & 3) * 32), idS, kk > 0 ? 1u : 0u);
                 // the turn passes a little early: the other warp needs some
                 // 250 cycles to notice
-                if (kk == D / 16 - 4 && !given) mbar_arrive(bar(W_TURN + s));
+                if (SLOTS == 2 && kk == D / 16 - 4 && !given) mbar_arrive(bar(W_TURN + s));
               }
               mma_commit(bar(W_SFULL + s));
               mma_commit(bar(W_KEMPTY + ks));
@@ -317,7 +385,7 @@ __global__ void __launch_bounds__(WideCfg<D, ROWS>::THREADS, 1)
     const int r = quarter * 32 + lane;                 // row within the slot = TMEM lane
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t tS = tbase + lane_off + 128 * slot;
-    const uint32_t tO = tbase + lane_off + 256 + 128 * slot;
+    const uint32_t tO = tbase + lane_off + C::T_O + 128 * slot;
     float2* ml = reinterpret_cast<float2*>(smem + C::OFF_ML);
     // A warp whose wait gave up goes on without waiting or touching tensor
     // memory: the slots' barriers of every piece still find all eight warps.
@@ -327,7 +395,7 @@ __global__ void __launch_bounds__(WideCfg<D, ROWS>::THREADS, 1)
     int4 rec = make_int4(-1, 0, 0, 0);
     TreePiece u;
     while (walk.next(P, u)) {
-      const WideSplit w = wide_split<ROWS>(u);
+      const WideSplit w = wide_split<SLOTS>(u);
       const int ur = w.rows ? slot * 128 + r : r;      // row of the unit
       const bool mine = ur < u.rows;
       const int rr = u.row_first + ur;
@@ -355,7 +423,7 @@ __global__ void __launch_bounds__(WideCfg<D, ROWS>::THREADS, 1)
       // which keys from origin on the row sees: bit i is key origin + i
       uint32_t seen[8];
       bool live = mine;
-      const int part0 = u.origin / kTile;              // tiles from here on are not seen by all
+      const int part0 = u.origin / KT;              // tiles from here on are not seen by all
       if (P.tree) {
 #pragma unroll
         for (int x = 0; x < 8; ++x) seen[x] = 0;
@@ -364,14 +432,14 @@ __global__ void __launch_bounds__(WideCfg<D, ROWS>::THREADS, 1)
           // the walks up the tree read shared memory: a parent from L2 took
           // 700 cycles a step
           int16_t* par = reinterpret_cast<int16_t*>(smem + C::OFF_PAR);
-          if (tid < u.s.n) par[tid] = static_cast<int16_t>(tree_parent(P, u.s, tid));
-          slots_sync();
+          for (int i = tid; i < u.s.n; i += 128 * SLOTS) par[i] = static_cast<int16_t>(tree_parent(P, u.s, i));
+          slots_sync<SLOTS>();
           if (live) tree_ancestors(node, [&](int a) -> int { return par[a]; }, seen);
         }
       }
       const bool warp_live = __any_sync(0xffffffffu, live);
       float m_used = -INFINITY, l = 0.f;
-      if (ROWS ? active : slot == 0) {
+      if (active) {
         // Q (S of the slots' earlier pieces has been read): a row is
         // copied by D / 8 lanes, so that a warp's copy covers whole rows, and
         // asynchronously past L1: the few KB that shared memory leaves of it
@@ -384,21 +452,22 @@ __global__ void __launch_bounds__(WideCfg<D, ROWS>::THREADS, 1)
         for (int i = 0; i < 32 / RPI; ++i) {
           const int from = i * RPI + lane / LPR;
           const uint64_t row = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(src), from);
-          copy_async16(sbase + C::OFF_Q + slot * C::TILE +
+          copy_async16(sbase + C::OFF_Q + slot * C::QTILE +
                            sw128_offset(quarter * 32 + from, (lane % LPR) * 8, 128),
                        row + (lane % LPR) * 16, (in_rows >> from) & 1u ? 16 : 0);
         }
         copy_async_wait();
         fence_proxy_async_smem();
         mbar_arrive_warp(bar(W_QFULL + slot));
-      }
-      if (active) {
         int done = 0;
 #pragma unroll 1
         for (int x0 = w.rows ? 0 : slot; x0 < w.n; x0 += w.rows ? 1 : 2) {
           const int t = u.t0 + x0;
           const bool partial = t >= part0;
-          if (ok) ok = wait_all(W_SFULL + slot, j & 1);
+          // SLOTS 1: the buffers alternate
+          const int buf = SLOTS == 1 ? j & 1 : slot;
+          const uint32_t tSj = SLOTS == 1 ? tS + 64 * (j & 1) : tS;
+          if (ok) ok = wait_all(W_SFULL + buf, SLOTS == 1 ? (j >> 1) & 1 : j & 1);
           tc_fence_after();
           if (ok && warp_live) {
             if (partial) {
@@ -406,8 +475,8 @@ __global__ void __launch_bounds__(WideCfg<D, ROWS>::THREADS, 1)
               // and back to tensor memory: a few tiles of a unit at most, and
               // the loop below stays free of it
 #pragma unroll 1
-              for (int y = 0; y < 4; ++y) {
-                const int j0 = t * kTile + 32 * y - u.origin;   // bit 0 is key origin + j0
+              for (int y = 0; y < KT / 32; ++y) {
+                const int j0 = t * KT + 32 * y - u.origin;   // bit 0 is key origin + j0
                 uint32_t vis;
                 if (P.tree) {
                   // the 64 bits from word (j0 >> 5) on, ones before bit 0
@@ -424,28 +493,28 @@ __global__ void __launch_bounds__(WideCfg<D, ROWS>::THREADS, 1)
                   vis = upto >= 31 ? 0xffffffffu : (upto < 0 ? 0u : (2u << upto) - 1u);
                 }
                 uint32_t q[32];
-                tmem_ld32(tS + 32 * y, q);
+                tmem_ld32(tSj + 32 * y, q);
                 tmem_wait_ld();
 #pragma unroll
                 for (int c = 0; c < 32; ++c) q[c] = (vis >> c) & 1u ? q[c] : 0xff800000u;
-                tmem_st32(tS + 32 * y, q);
+                tmem_st32(tSj + 32 * y, q);
               }
               tmem_wait_st();
             }
-            float sv[128];
+            float sv[KT];
             uint32_t* raw = reinterpret_cast<uint32_t*>(sv);
 #pragma unroll
-            for (int y = 0; y < 4; ++y) tmem_ld32(tS + 32 * y, raw + 32 * y);
+            for (int y = 0; y < KT / 32; ++y) tmem_ld32(tSj + 32 * y, raw + 32 * y);
             tmem_wait_ld();
             float mx8[8];
 #pragma unroll
             for (int y = 0; y < 8; ++y) mx8[y] = fmax3(sv[y], sv[y + 8], sv[y + 16]);
 #pragma unroll
-            for (int c = 24; c < 120; c += 16)
+            for (int c = 24; c < KT - 8; c += 16)
 #pragma unroll
               for (int y = 0; y < 8; ++y) mx8[y] = fmax3(mx8[y], sv[c + y], sv[c + 8 + y]);
 #pragma unroll
-            for (int y = 0; y < 8; ++y) mx8[y] = fmaxf(mx8[y], sv[120 + y]);
+            for (int y = 0; y < 8; ++y) mx8[y] = fmaxf(mx8[y], sv[KT - 8 + y]);
             const float mx = fmax3(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(mx8[3], mx8[4], mx8[5]),
                                    fmaxf(mx8[6], mx8[7]));
             // the reference moves only when the maximum grows by more than
@@ -460,7 +529,7 @@ __global__ void __launch_bounds__(WideCfg<D, ROWS>::THREADS, 1)
             const uint64_t sc2 = splat2(P.scale_log2), nm2 = splat2(-m_ref);
             float sum4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int c4 = 0; c4 < 4; ++c4) {
+            for (int c4 = 0; c4 < KT / 32; ++c4) {
               uint32_t pk[16];
 #pragma unroll
               for (int y = 0; y < 16; ++y) {
@@ -471,9 +540,15 @@ __global__ void __launch_bounds__(WideCfg<D, ROWS>::THREADS, 1)
                 else add2_acc(sum4[0], sum4[1], p0, p1);
                 pk[y] = pack_bf16(p0, p1);   // P in bf16 for the product; the sum keeps 32 bits
               }
-              tmem_st16(tS + c4 * 16, pk);
+              tmem_st16(tSj + c4 * 16, pk);
             }
             if (done > 0 && __any_sync(0xffffffffu, grow)) {
+              // O holds the PVs of the earlier tiles; with two S buffers the
+              // last one may still run
+              if (SLOTS == 1) {
+                ok = wait_all(W_PVTILE, (j - 1) & 1);
+                tc_fence_after();
+              }
               uint32_t ro[D];
 #pragma unroll
               for (int y = 0; y < D / 32; ++y) tmem_ld32(tO + 32 * y, ro + 32 * y);
@@ -491,15 +566,17 @@ __global__ void __launch_bounds__(WideCfg<D, ROWS>::THREADS, 1)
             const uint32_t e = e0 + x0, st = e % C::VSTAGES;
             ok = wait_all(W_VFULL + st, (e / C::VSTAGES) & 1);
             if (ok) {
-              const int key = t * kTile + r, i = key - u.origin;
+              const int key = t * KT + r, i = key - u.origin;
               // 16-byte words of the row, the slabs 16 KB apart; the lanes
               // start at different words (bank conflicts)
               uint8_t* v = smem + C::OFF_V + st * C::TILE + r * 128;
               auto word = [&](int c) {
-                return reinterpret_cast<uint4*>(v + (c >> 3) * (kTile * 128) + ((c ^ r) & 7) * 16);
+                return reinterpret_cast<uint4*>(v + (c >> 3) * (KT * 128) + ((c ^ r) & 7) * 16);
               };
               bool dirty = false;
-              if (key >= u.keys) {
+              if (r >= KT) {
+                // the tile has no row for this thread
+              } else if (key >= u.keys) {
 #pragma unroll 1
                 for (int c = 0; c < D / 8; ++c) *word(c) = make_uint4(0u, 0u, 0u, 0u);
               } else if (i >= 0) {
@@ -525,7 +602,7 @@ __global__ void __launch_bounds__(WideCfg<D, ROWS>::THREADS, 1)
             }
           }
           tc_fence_before();
-          mbar_arrive_warp(bar(W_PFULL + slot));
+          mbar_arrive_warp(bar(W_PFULL + buf));
           ++j;
           ++done;
         }
@@ -541,7 +618,7 @@ __global__ void __launch_bounds__(WideCfg<D, ROWS>::THREADS, 1)
       float m_out = m_used, l_out = l, f0 = 1.f, f1 = 0.f;
       if (!w.rows) {
         ml[slot * 128 + r] = make_float2(m_used, l);
-        slots_sync();
+        slots_sync<SLOTS>();
         const float2 a = ml[r], b = two ? ml[128 + r] : make_float2(-INFINITY, 0.f);
         m_out = fmaxf(a.x, b.x);
         f0 = a.y != 0.f ? ex2(a.x - m_out) : 0.f;
@@ -564,17 +641,17 @@ __global__ void __launch_bounds__(WideCfg<D, ROWS>::THREADS, 1)
       // O by blocks of 32 columns; each passes through the warp's part of the
       // slot's Q buffer (no longer needed), so that the stores cover whole
       // runs of a row: 64 bytes (bf16) or 128 bytes (fp32 parts)
-      uint8_t* stage = smem + C::OFF_STAGE + warp * 4096;
+      uint8_t* stage = smem + C::OFF_Q + warp * 4096;
       const unsigned out_rows = __ballot_sync(0xffffffffu, writes);
 #pragma unroll 1
       for (int cb = c0 / 32; cb < c1 / 32; ++cb) {
         float v[32];
         uint32_t* raw = reinterpret_cast<uint32_t*>(v);
         if (ok) {
-          tmem_ld32(w.rows ? tO + cb * 32 : tbase + lane_off + 256 + cb * 32, raw);
+          tmem_ld32(w.rows ? tO + cb * 32 : tbase + lane_off + C::T_O + cb * 32, raw);
           if (two) {
             uint32_t rb[32];
-            tmem_ld32(tbase + lane_off + 384 + cb * 32, rb);
+            tmem_ld32(tbase + lane_off + C::T_O + 128 + cb * 32, rb);
             tmem_wait_ld();
 #pragma unroll
             for (int y = 0; y < 32; ++y)
@@ -622,9 +699,9 @@ __global__ void __launch_bounds__(WideCfg<D, ROWS>::THREADS, 1)
       }
       tc_fence_before();
       if (w.rows) {
-        // two arrivals for each of this slot's warps
+        // for each of this slot's warps, and those of the other
         __syncwarp();
-        if (lane == 0) mbar_arrive_count(bar(W_OEMPTY + slot), 2);
+        if (lane == 0) mbar_arrive_count(bar(W_OEMPTY + slot), SLOTS);
       } else {
         mbar_arrive_warp(bar(W_OEMPTY));
         mbar_arrive_warp(bar(W_OEMPTY + 1));
@@ -659,7 +736,7 @@ __global__ void __launch_bounds__(WideCfg<D, ROWS>::THREADS, 1)
       }
       e0 += w.n;
       ++pieces;
-      slots_sync();               // ml and nf have been read, and S of both slots
+      slots_sync<SLOTS>();        // ml and nf have been read, and S of both slots
     }
     if (tid == 0) P.rec[blockIdx.x] = rec;
   }
@@ -668,15 +745,15 @@ __global__ void __launch_bounds__(WideCfg<D, ROWS>::THREADS, 1)
   __syncthreads();
   if (warp == MMA_WARP) {
     tc_fence_after();
-    tmem_dealloc(tbase, 512);
+    tmem_dealloc(tbase, C::T_COLS);
   }
 }
 
-template <int D, bool ROWS>
+template <int D, int SLOTS>
 static fm_status launch_wide_d(const TreeParams& P, const CUtensorMap& tk, const CUtensorMap& tv,
                                int grid, cudaStream_t s) {
-  using C = WideCfg<D, ROWS>;
-  auto kern = tree_wide_kernel<D, ROWS>;
+  using C = WideCfg<D, SLOTS>;
+  auto kern = tree_wide_kernel<D, SLOTS>;
   // the setmaxnreg split must fit in the registers the block launches with
   static std::atomic<uint64_t> ready{0};
   const fm_status st = prepare_kernel(kern, C::SMEM, C::MIN_LAUNCH_REGS, ready);
@@ -687,12 +764,14 @@ static fm_status launch_wide_d(const TreeParams& P, const CUtensorMap& tk, const
   return e == cudaSuccess ? FM_OK : FM_ERR_CUDA;
 }
 
+fm_status launch_tree_mid(const TreeParams& P, int d, const CUtensorMap& tk, const CUtensorMap& tv,
+                          int grid, cudaStream_t s) {
+  return d == 64 ? launch_wide_d<64, 1>(P, tk, tv, grid, s) : launch_wide_d<128, 1>(P, tk, tv, grid, s);
+}
+
 fm_status launch_tree_wide(const TreeParams& P, int d, const CUtensorMap& tk, const CUtensorMap& tv,
                            int grid, cudaStream_t s) {
-  const bool rows = P.part_rows > 128;
-  if (d == 64)
-    return rows ? launch_wide_d<64, true>(P, tk, tv, grid, s) : launch_wide_d<64, false>(P, tk, tv, grid, s);
-  return rows ? launch_wide_d<128, true>(P, tk, tv, grid, s) : launch_wide_d<128, false>(P, tk, tv, grid, s);
+  return d == 64 ? launch_wide_d<64, 2>(P, tk, tv, grid, s) : launch_wide_d<128, 2>(P, tk, tv, grid, s);
 }
 
 }  // namespace fm
