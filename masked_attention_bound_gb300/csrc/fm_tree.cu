@@ -457,53 +457,56 @@ __global__ void __launch_bounds__(NarrowCfg<D>::THREADS, 2)
 // A unit that block c starts and does not finish has parts in slot 2 c + 1
 // and in slot 2 x of the blocks x after it up to the one that finishes it
 // (rec.w == 1).  For each row: the maximum of the parts' maxima, then their
-// sums and O weighted by 2^(m - maximum).  A block's eight warps share a row
-// when it has many parts (one long sequence: 76 parts of two units took 33 us
-// with a warp a row, 512 bytes of each part at a time), each warp taking every
-// eighth, else they take rows of their own; the order of the sums is fixed
-// either way.
-constexpr int kJoinThreads = 256, kJoinShare = 12;
+// sums and O weighted by 2^(m - maximum).  The blocks of a unit (one column of
+// the grid for every block that it runs through but the last) share its rows;
+// where there are more warps than rows, 2, 4 or 8 warps share a row, each
+// taking every second, fourth or eighth part (76 parts of two units took 33 us
+// with a warp a row).  The order of the sums depends on the cuts only.
+constexpr int kJoinThreads = 256, kMaxJoin = 4096;   // blocks of the first kernel
 
 template <int R, int D>
 __global__ void __launch_bounds__(kJoinThreads)
     tree_join_kernel(const __grid_constant__ TreeParams P, int blocks) {
   constexpr int NW = kJoinThreads / 32, CPT = D / 32, RPW = R == NarrowGeo::R ? 2 : 4;
-  __shared__ float sums[NW][D + 1];
+  __shared__ float sums[NW][D + 2];
+  __shared__ unsigned middle[kMaxJoin / 32];
   grid_launch_dependents();
   grid_dependency_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  // the unit: opened by the nearest block c at or before this one that is not
-  // in the middle of a unit, and finished by block `last`
-  int c = blockIdx.x;
-  for (int x0 = c;; x0 -= 32) {
-    const int x = x0 - lane;
-    const unsigned opens = __ballot_sync(0xffffffffu, x <= 0 || P.rec[x].w != 2);
-    if (opens) {
-      c = max(x0 - __ffs(opens) + 1, 0);
-      break;
-    }
+  // bit x: block x is in the middle of a unit
+#pragma unroll 1
+  for (int i = warp; i * 32 < blocks; i += NW) {
+    const int x = i * 32 + lane;
+    const unsigned mid = __ballot_sync(0xffffffffu, x < blocks && P.rec[x].w == 2);
+    if (lane == 0) middle[i] = mid;
   }
+  __syncthreads();
+  // the unit: opened by the nearest block c at or before this one that is not
+  // in the middle of one, and finished by the next such block
+  int c = blockIdx.x, last = blockIdx.x + 1;
+#pragma unroll 1
+  while (c > 0 && ((middle[c >> 5] >> (c & 31)) & 1u)) {
+    const unsigned below = ~middle[c >> 5] & ((1u << (c & 31)) - 1u);
+    c = below ? (c & ~31) + 31 - __clz(below) : (c & ~31) - 1;
+  }
+#pragma unroll 1
+  while (last < blocks - 1 && ((middle[last >> 5] >> (last & 31)) & 1u)) {
+    const unsigned above = ~middle[last >> 5] & ~((2u << (last & 31)) - 1u);
+    last = above ? (last & ~31) + __ffs(above) - 1 : (last & ~31) + 32;
+  }
+  last = min(last, blocks - 1);
   const int4 rec = P.rec[c];
   if (rec.x < 0) return;
-  int last = c + 1;
-  for (int x0 = c + 1;; x0 += 32) {
-    const int x = x0 + lane;
-    const unsigned ends = __ballot_sync(0xffffffffu, x >= blocks || P.rec[x].w != 2);
-    if (ends) {
-      last = min(x0 + __ffs(ends) - 1, blocks - 1);
-      break;
-    }
-  }
   const TreeSeq s = tree_seq(P, rec.x);
   const int row_first = rec.z * R, rows = min(R, s.n * P.G - row_first), parts = last - c + 1;
-  const bool share = parts > kJoinShare;
   // the blocks in the middle of the unit (in [c, last)) take rows of it too
-  const int first = (blockIdx.x - c) * gridDim.y + blockIdx.y, step = (last - c) * gridDim.y;
-  auto at = [&](int i, int r) -> int64_t {
-    return static_cast<int64_t>(i == 0 ? 2 * c + 1 : 2 * (c + i)) * P.part_rows + r;
-  };
+  const int first = blockIdx.y * (last - c) + blockIdx.x - c, step = (last - c) * gridDim.y;
+  // part i of the unit is in slot 2 (c + i), the first in slot 2 c + 1
+  const float* po = P.part_o + static_cast<int64_t>(2 * c) * P.part_rows * D + lane * CPT;
+  const float2* pm = P.part_ml + 2 * c * P.part_rows;
+  auto at = [&](int i, int r) -> int { return (i ? 2 * i : 1) * P.part_rows + r; };
   auto load = [&](int i, int r, float (&y)[CPT]) {
-    const float* src = P.part_o + at(i, r) * D + lane * CPT;
+    const float* src = po + at(i, r) * D;
     if constexpr (CPT == 4) {
       const float4 z = *reinterpret_cast<const float4*>(src);
       y[0] = z.x; y[1] = z.y; y[2] = z.z; y[3] = z.w;
@@ -527,33 +530,38 @@ __global__ void __launch_bounds__(kJoinThreads)
           ll > 0.f || ll != ll ? (mm + __log2f(ll)) * 0.69314718055994530942f : -INFINITY;
   };
 
-  if (!share) {
-    // few parts: a warp joins RPW rows at a time, to have their loads in flight
-    // together (a row a warp left the parts of 150 units at 3 TB/s)
+  // warps per row
+  int wpr = 1;
+#pragma unroll 1
+  while (wpr < NW && 2 * wpr <= parts && rows * 2 * wpr <= (last - c) * static_cast<int>(gridDim.y) * NW)
+    wpr *= 2;
+  if (wpr == 1) {
+    // a warp joins RPW rows at a time, to have their loads in flight together
+    // (one row at a time left the parts of 150 units at 3 TB/s)
+#pragma unroll 1
     for (int r0 = (first * NW + warp) * RPW; r0 < rows; r0 += step * NW * RPW) {
       float mm[RPW], f[RPW], ll[RPW], v[RPW][CPT];
       unsigned seen[RPW];
-      // lane i: maximum and sum of part i; a sum of 0 says that its keys were not seen
+      // lane i: maximum and sum of part i (there are eight at most: with more,
+      // the warps outnumber the rows); a sum of 0 says that its keys were not seen
       float2 p[RPW];
 #pragma unroll
       for (int k = 0; k < RPW; ++k)
-        p[k] = lane < parts && r0 + k < rows ? P.part_ml[at(lane, r0 + k)] : make_float2(-INFINITY, 0.f);
+        p[k] = lane < parts && r0 + k < rows ? pm[at(lane, r0 + k)] : make_float2(-INFINITY, 0.f);
 #pragma unroll
       for (int k = 0; k < RPW; ++k) {
         mm[k] = p[k].x;
 #pragma unroll
-        for (int o = 8; o; o >>= 1) mm[k] = fmaxf(mm[k], __shfl_xor_sync(0xffffffffu, mm[k], o));
-        mm[k] = __shfl_sync(0xffffffffu, mm[k], 0);
+        for (int o = 16; o; o >>= 1) mm[k] = fmaxf(mm[k], __shfl_xor_sync(0xffffffffu, mm[k], o));
         f[k] = p[k].y != 0.f ? ex2(p[k].x - mm[k]) : 0.f;
         seen[k] = __ballot_sync(0xffffffffu, p[k].y != 0.f);
         ll[k] = p[k].y != 0.f ? p[k].y * f[k] : 0.f;
 #pragma unroll
-        for (int o = 8; o; o >>= 1) ll[k] += __shfl_xor_sync(0xffffffffu, ll[k], o);
-        ll[k] = __shfl_sync(0xffffffffu, ll[k], 0);
+        for (int o = 16; o; o >>= 1) ll[k] += __shfl_xor_sync(0xffffffffu, ll[k], o);
 #pragma unroll
         for (int x = 0; x < CPT; ++x) v[k][x] = 0.f;
       }
-#pragma unroll 2
+#pragma unroll 1
       for (int i = 0; i < parts; ++i) {
         float y[RPW][CPT];
 #pragma unroll
@@ -574,49 +582,78 @@ __global__ void __launch_bounds__(kJoinThreads)
     return;
   }
 
-  // many parts: the block's warps share a row, each taking every eighth part
-  for (int r = first; r < rows; r += step) {
-    float mm = -INFINITY;
-    for (int i = lane; i < parts; i += 32) mm = fmaxf(mm, P.part_ml[at(i, r)].x);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
-    float ll = 0.f, v[CPT];
+  const int team = warp / wpr, sub = warp % wpr, teams = NW / wpr;
+#pragma unroll 1
+  for (int r0 = first * teams; r0 < rows; r0 += step * teams) {
+    const int r = r0 + team;
+    float mm = -INFINITY, ll = 0.f, v[CPT];
 #pragma unroll
     for (int i = 0; i < CPT; ++i) v[i] = 0.f;
-#pragma unroll 4
-    for (int i = warp; i < parts; i += NW) {
-      float y[CPT];
-      load(i, r, y);
-      const float2 p = P.part_ml[at(i, r)];
-      if (p.y != 0.f) {
-        const float f = ex2(p.x - mm);
-        ll += p.y * f;
+    if (r < rows) {
+#pragma unroll 1
+      for (int i0 = sub; i0 < parts; i0 += 32 * wpr) {
+        // lane j: maximum and sum of part i0 + j * wpr; a sum of 0 says that
+        // its keys were not seen
+        const int mine = i0 + lane * wpr;
+        const float2 p = mine < parts ? pm[at(mine, r)] : make_float2(-INFINITY, 0.f);
+        float m = p.x;
 #pragma unroll
-        for (int x = 0; x < CPT; ++x) v[x] += y[x] * f;
+        for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        m = fmaxf(m, mm);
+        const float old = mm == -INFINITY ? (ll == 0.f ? 0.f : 1.f) : ex2(mm - m);
+        mm = m;
+        const float f = p.y != 0.f ? ex2(p.x - m) : 0.f;
+        const unsigned seen = __ballot_sync(0xffffffffu, p.y != 0.f);
+        float l = p.y != 0.f ? p.y * f : 0.f;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+        ll = ll * old + l;
+#pragma unroll
+        for (int x = 0; x < CPT; ++x) v[x] *= old;
+        const int n = min(32, (parts - i0 + wpr - 1) / wpr);
+#pragma unroll 4
+        for (int j = 0; j < n; ++j) {
+          float y[CPT];
+          load(i0 + j * wpr, r, y);
+          const float w = __shfl_sync(0xffffffffu, f, j);
+          if ((seen >> j) & 1u)
+#pragma unroll
+            for (int x = 0; x < CPT; ++x) v[x] += y[x] * w;
+        }
       }
     }
-    __syncthreads();                   // the row before has been read
+    __syncthreads();                   // the rows before have been read
 #pragma unroll
     for (int x = 0; x < CPT; ++x) sums[warp][lane * CPT + x] = v[x];
-    if (lane == 0) sums[warp][D] = ll;
+    if (lane == 0) {
+      sums[warp][D] = ll;
+      sums[warp][D + 1] = mm;
+    }
     __syncthreads();
-    if (warp > 0) continue;
-    ll = 0.f;
+    if (sub > 0 || r >= rows) continue;
+    float top = mm;
+#pragma unroll 1
+    for (int w = 1; w < wpr; ++w) top = fmaxf(top, sums[warp + w][D + 1]);
+    float total = 0.f;
 #pragma unroll
     for (int x = 0; x < CPT; ++x) v[x] = 0.f;
+#pragma unroll 1
+    for (int w = 0; w < wpr; ++w) {
+      const float* from = sums[warp + w];
+      if (from[D] == 0.f) continue;    // nothing seen
+      const float f = ex2(from[D + 1] - top);
+      total += from[D] * f;
 #pragma unroll
-    for (int w = 0; w < NW; ++w) {
-      ll += sums[w][D];
-#pragma unroll
-      for (int x = 0; x < CPT; ++x) v[x] += sums[w][lane * CPT + x];
+      for (int x = 0; x < CPT; ++x) v[x] += from[lane * CPT + x] * f;
     }
-    write(r, mm, ll, v);
+    write(r, top, total, v);
   }
 }
 
 template <int R, int D>
 static fm_status launch_join(const TreeParams& P, int grid, cudaStream_t s) {
   if (grid < 2 || P.whole) return FM_OK;
+  if (grid > kMaxJoin) return FM_ERR_UNSUPPORTED;
   // the blocks of a unit in two parts take its rows in one go
   prof_begin(K_TREE_JOIN, s);
   const cudaError_t e = launch_dependent(

@@ -71,18 +71,19 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeParams& P, int b) {
   return s;
 }
 
-// Geometry of the three kernels: rows of a unit, keys of a tile, and a unit's
-// fixed cost in tiles.
+// Geometry of the three kernels: rows of a unit, keys of a tile, a unit's
+// fixed cost in tiles, and the shortest run of a block in tiles (a part of
+// 128 rows is as many bytes as two 64-key tiles, written and read again).
 struct NarrowGeo {
-  static constexpr int R = 16, KT = 64;
+  static constexpr int R = 16, KT = 64, LEAST = 2;
   __device__ static __forceinline__ int end(int) { return 2; }
 };
 struct MidGeo {
-  static constexpr int R = 128, KT = 64;
-  __device__ static __forceinline__ int end(int) { return 4; }
+  static constexpr int R = 128, KT = 64, LEAST = 4;
+  __device__ static __forceinline__ int end(int) { return 8; }
 };
 struct WideGeo {
-  static constexpr int R = 256, KT = 128;
+  static constexpr int R = 256, KT = 128, LEAST = 2;
   // a block with a unit's end in its run took 12000 (256 rows) to 20000
   // cycles (128 rows) longer, where a tile takes 3100 and 2800
   __device__ static __forceinline__ int end(int rows) { return rows > 128 ? 5 : 10; }
@@ -170,14 +171,16 @@ __device__ __forceinline__ TreeRun tree_run(const TreeParams& P) {
     if (lane >= o) inc += y;
   }
   const uint32_t all = __shfl_sync(ALL, inc, 31);
-  // on a short line the last blocks have nothing
   TreeRun run{0, 0, 0, 0, 0, s};
-  const uint32_t me = blockIdx.x, grid = gridDim.x;
-  if (me >= all) return run;
-  const uint32_t each = all < grid ? 1 : P.by_grid(all);
-  const uint32_t more = all < grid ? 0 : all - each * grid;   // the first blocks take one more
+  const uint32_t me = blockIdx.x, grid = gridDim.x, least = P.whole ? 1 : Geo::LEAST;
+  uint32_t each = P.by_grid(all), more = all - each * grid;   // the first blocks take one more
+  if (each < least) {                  // on a short line the last blocks have nothing
+    each = least;
+    more = 0;
+  }
   const uint32_t begin = each * me + min(me, more);
-  run.left = each + (me < more);
+  if (begin >= all) return run;
+  run.left = min(each + (me < more), all - begin);
   const unsigned owner = __ballot_sync(ALL, inc > begin);
   const int from = __ffs(owner) - 1;
   if (lane == from) {
