@@ -691,7 +691,9 @@ fm_status check_tree(const fm_cache* c, const fm_tree_desc* t) {
 }
 
 // Workspace: the blocks' records, then their parts (two each).
+enum TreeKind { NARROW, MID, WIDE };
 struct TreeWs {
+  TreeKind kind;
   int rows;    // of a part: the largest unit's
   int grid;
   size_t rec, ml, o, bytes;
@@ -704,7 +706,11 @@ TreeWs tree_ws(const fm_cache& c, const fm_tree_desc& t, int sms) {
   W.rows = rows <= NarrowGeo::R ? NarrowGeo::R
            : rows >= WideGeo::R ? WideGeo::R
                                 : (static_cast<int>(rows) + 31) / 32 * 32;
-  W.grid = W.rows > MidGeo::R ? sms : 2 * sms;   // blocks per SM of the kernel for these rows
+  // The kernel: with d = 64, tiles of 128 rows side by side beat pairs of them
+  // (64 sequences of 1000 tokens with 150 rows: 70 us against 81)
+  W.kind = W.rows <= NarrowGeo::R ? NARROW : (W.rows <= MidGeo::R || c.d == 64 ? MID : WIDE);
+  if (W.kind == MID && W.rows > MidGeo::R) W.rows = MidGeo::R;   // of a part
+  W.grid = W.kind == WIDE ? sms : 2 * sms;       // by the kernel's blocks per SM
   const int grid = W.grid;
   W.rec = 0;
   W.ml = up(static_cast<size_t>(grid) * sizeof(int4));
@@ -754,10 +760,12 @@ fm_status fm_tree_fwd(const fm_cache* c, const fm_tree_desc* t, const void* q, c
   P.by_G = FastDiv::of(P.G);
   P.by_grid = FastDiv::of(grid);
   P.tree = parents != nullptr;
-  // Rows of the table that hold at most 512 tokens: units are not cut, and the
-  // join (2.5 us after the first kernel) is spared; the tiles that a block then
-  // takes in turn cost 0.4 us each.
-  P.whole = static_cast<int64_t>(c->max_pages) * c->page_size <= 512;
+  // Units are not cut, and the join (3 us after the first kernel) is spared,
+  // where the rows of the table hold at most 512 tokens (eight tiles in turn
+  // cost a block 4 us), as long as there is a block for each unit: 1024 units
+  // of 480 keys took 48 us whole and 43 us cut and joined.
+  const int64_t tokens = static_cast<int64_t>(c->max_pages) * c->page_size;
+  P.whole = tokens <= 256 || (tokens <= 512 && static_cast<int64_t>(c->B) * c->Hkv <= grid);
   P.scale_log2 = scale * 1.4426950408889634f;
   P.q = static_cast<const __nv_bfloat16*>(q);
   P.o = static_cast<__nv_bfloat16*>(o);
@@ -778,7 +786,7 @@ fm_status fm_tree_fwd(const fm_cache* c, const fm_tree_desc* t, const void* q, c
   P.wait_ns = th.wait_ns < 4000000000ull ? static_cast<uint32_t>(th.wait_ns) : 4000000000u;
   P.withhold = th.withhold;
   // one page of one head, or a tile's part of it, is a box of 64 columns
-  const int box = W.rows > MidGeo::R ? c->page_size : c->page_size < MidGeo::KT ? c->page_size : MidGeo::KT;
+  const int box = W.kind == WIDE || c->page_size < MidGeo::KT ? c->page_size : MidGeo::KT;
   P.box_shift = page_shift(box);
   CUtensorMap tk, tv;
   if (!make_tmap_bshd(&tk, k_pool, c->n_pages, c->page_size, c->Hkv, c->d, c->k_stride + 1, box) ||
@@ -786,12 +794,12 @@ fm_status fm_tree_fwd(const fm_cache* c, const fm_tree_desc* t, const void* q, c
     return FM_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool d64 = c->d == 64;
-  if (W.rows <= NarrowGeo::R) {
+  if (W.kind == NARROW) {
     st = d64 ? launch_narrow<64>(P, tk, tv, grid, s) : launch_narrow<128>(P, tk, tv, grid, s);
     if (st != FM_OK) return st;
     return d64 ? launch_join<NarrowGeo::R, 64>(P, grid, s) : launch_join<NarrowGeo::R, 128>(P, grid, s);
   }
-  if (W.rows <= MidGeo::R) {
+  if (W.kind == MID) {
     st = launch_tree_mid(P, c->d, tk, tv, grid, s);
     if (st != FM_OK) return st;
     return d64 ? launch_join<MidGeo::R, 64>(P, grid, s) : launch_join<MidGeo::R, 128>(P, grid, s);
