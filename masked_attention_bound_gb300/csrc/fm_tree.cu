@@ -96,8 +96,7 @@ __global__ void __launch_bounds__(NarrowCfg<D>::THREADS, 2)
   }
   grid_launch_dependents();
   grid_dependency_wait();
-  TreeWalk<typename C::Geo> walk;
-  walk.run = tree_run<typename C::Geo>(P);
+  TreeWalk<typename C::Geo> u(tree_run<typename C::Geo>(P));
   __syncthreads();
 
   // every lane gets the same answer
@@ -115,9 +114,8 @@ __global__ void __launch_bounds__(NarrowCfg<D>::THREADS, 2)
     const uint64_t policy = policy_evict_first();
     int st = 0, issued = 0;
     uint32_t use = 0;
-    TreePiece u;
     bool ok = true;
-    while (ok && walk.next(P, u)) {
+    while (ok && u.next(P)) {
       if (u.keys == 0) continue;
       int page = Load::lane_page(P, u, u.t0, lane);
 #pragma unroll 1
@@ -151,9 +149,8 @@ __global__ void __launch_bounds__(NarrowCfg<D>::THREADS, 2)
     uint32_t* nf = reinterpret_cast<uint32_t*>(smem + C::OFF_NF);
     float* merge = reinterpret_cast<float*>(smem + C::OFF_MERGE);
     float* ml = reinterpret_cast<float*>(smem + C::OFF_ML);
-    int4 rec = make_int4(-1, 0, 0, 0);
-    TreePiece u;
-    while (walk.next(P, u)) {
+    if (tid == 0) P.rec[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    while (u.next(P)) {
       // tiles from this one on hold keys that not every row sees
       const int part0 = u.origin / KT;
       // which keys past origin a row sees: bit j is key origin + j
@@ -426,7 +423,9 @@ __global__ void __launch_bounds__(NarrowCfg<D>::THREADS, 2)
             for (int c = 0; c < CPT / 8; ++c)
               reinterpret_cast<uint4*>(dst)[c] =
                   make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
-            if (any) fix_row(P, u, nf, seen + r * 8, 0, CPT, c0, dst);
+            if (any)
+              fix_row(P, u.b, u.hk, u.origin, nf, reinterpret_cast<const uint4*>(seen)[2 * r],
+                      reinterpret_cast<const uint4*>(seen)[2 * r + 1], c0, CPT, dst);
             if (c0 == 0)
               P.lse[static_cast<int64_t>(h) * P.total + u.s.row0 + node] =
                   ll > 0.f || ll != ll ? (mm + __log2f(ll)) * 0.69314718055994530942f : -INFINITY;
@@ -437,18 +436,16 @@ __global__ void __launch_bounds__(NarrowCfg<D>::THREADS, 2)
 #pragma unroll
             for (int c = 0; c < CPT / 4; ++c)
               dst[c] = make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
-            if (any) fix_row(P, u, nf, seen + r * 8, 0, CPT, c0, P.part_o + at * D + c0);
+            if (any)
+              fix_row(P, u.b, u.hk, u.origin, nf, reinterpret_cast<const uint4*>(seen)[2 * r],
+                      reinterpret_cast<const uint4*>(seen)[2 * r + 1], c0, CPT, P.part_o + at * D + c0);
             if (c0 == 0) P.part_ml[at] = make_float2(mm, ll);
           }
         }
       }
-      if (!u.whole()) {
-        if (u.t0 == 0) rec = make_int4(u.b, u.hk, u.rt, rec.w);
-        else rec.w = u.t1 == u.tiles ? 1 : 2;
-      }
+      if (tid == 0) leave_record(P, u);
       named_sync(1, 32 * C::WARPS);     // ml, merge, seen and nf have been read
     }
-    if (tid == 0) P.rec[blockIdx.x] = rec;
   }
   __syncthreads();
 }
@@ -765,7 +762,7 @@ fm_status fm_tree_fwd(const fm_cache* c, const fm_tree_desc* t, const void* q, c
   // cost a block 4 us), as long as there is a block for each unit: 1024 units
   // of 480 keys took 48 us whole and 43 us cut and joined.
   const int64_t tokens = static_cast<int64_t>(c->max_pages) * c->page_size;
-  P.whole = tokens <= 256 || (tokens <= 512 && static_cast<int64_t>(c->B) * c->Hkv <= grid);
+  P.whole = tokens <= 320 || (tokens <= 512 && static_cast<int64_t>(c->B) * c->Hkv <= grid);
   P.scale_log2 = scale * 1.4426950408889634f;
   P.q = static_cast<const __nv_bfloat16*>(q);
   P.o = static_cast<__nv_bfloat16*>(o);

@@ -31,7 +31,7 @@ struct TreeParams {
   __nv_bfloat16* o;
   int64_t o_stride[2];
   float* lse;
-  const __nv_bfloat16* v_pool;   // for values that are not finite (see fix_value)
+  const __nv_bfloat16* v_pool;   // for values that are not finite (see fix_row)
   int64_t v_stride[3];           // page, slot, head
   const int32_t *table, *lens, *cu, *parents;
   int4* rec;               // [grid] what a block leaves for the join, see below
@@ -226,48 +226,67 @@ struct TreePiece {
   __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == tiles; }
 };
 
-// Every role of a block walks its run piece by piece in the same order.
+// Every role of a block walks its run piece by piece in the same order.  The
+// walk is the piece: each field is held once.
 template <class Geo>
-struct TreeWalk {
-  TreeRun run;
-  __device__ __forceinline__ bool next(const TreeParams& P, TreePiece& u) {
-    TreeSeq& s = run.s;
+struct TreeWalk : TreePiece {
+  int left;            // of the run, in units of the line
+  int next_tile;       // where the next piece starts; -1: at the next unit
+  __device__ __forceinline__ explicit TreeWalk(const TreeRun& run) {
+    b = run.b;
+    hk = run.hk;
+    rt = run.rt;
+    s = run.s;
+    left = run.left;
+    next_tile = run.tile;
+  }
+  __device__ __forceinline__ bool next(const TreeParams& P) {
 #pragma unroll 1
     while (true) {
-      if (run.left <= 0) return false;
-      // on to the next sequence with rows
-      if (run.hk >= P.Hkv || s.n <= 0) {
-        run.hk = run.rt = run.tile = 0;
-        if (++run.b >= P.B) return false;
-        s = tree_seq(P, run.b);
-        continue;
-      }
-      u.hk = run.hk;
-      u.rt = run.rt;
-      u.keys = unit_keys<Geo>(P, s, run.rt);
-      u.tiles = key_tiles<Geo>(u.keys);
-      u.t0 = run.tile;
-      u.t1 = P.whole ? u.tiles : min(u.tiles, run.tile + run.left);
-      const int end = u.t1 < u.tiles ? u.t1 : unit_length<Geo>(P, s, run.rt, u.tiles);
-      run.left -= end - run.tile;
-      run.tile = end;
-      if (u.t1 >= u.tiles) {
-        run.tile = 0;
-        if (++run.rt >= row_tiles<Geo>(P, s)) {
-          run.rt = 0;
-          ++run.hk;
+      if (left <= 0) return false;
+      if (next_tile < 0) {
+        next_tile = 0;
+        if (++rt >= row_tiles<Geo>(P, s)) {
+          rt = 0;
+          ++hk;
         }
       }
-      if (u.t0 < u.tiles) break;       // else the run starts in a unit's fixed cost
+      // on to the next sequence with rows
+      if (hk >= P.Hkv || s.n <= 0) {
+        hk = rt = next_tile = 0;
+        if (++b >= P.B) return false;
+        s = tree_seq(P, b);
+        continue;
+      }
+      keys = unit_keys<Geo>(P, s, rt);
+      tiles = key_tiles<Geo>(keys);
+      t0 = next_tile;
+      t1 = P.whole ? tiles : min(tiles, t0 + left);
+      const bool ends = t1 >= tiles;
+      left -= (ends ? unit_length<Geo>(P, s, rt, tiles) : t1) - t0;
+      next_tile = ends ? -1 : t1;
+      if (t0 < tiles) break;           // else the run starts in a unit's fixed cost
     }
-    u.b = run.b;
-    u.s = s;
-    u.row_first = u.rt * Geo::R;
-    u.rows = min(Geo::R, s.n * P.G - u.row_first);
-    u.origin = s.base + (P.tree ? 0 : P.by_G(u.row_first));
+    row_first = rt * Geo::R;
+    rows = min(Geo::R, s.n * P.G - row_first);
+    origin = s.base + (P.tree ? 0 : P.by_G(row_first));
     return true;
   }
 };
+
+// A piece's share of the block's record (its first thread's; the block starts
+// with {-1, 0, 0, 0}).
+__device__ __forceinline__ void leave_record(const TreeParams& P, const TreePiece& u) {
+  if (u.whole()) return;
+  int* rec = reinterpret_cast<int*>(P.rec + blockIdx.x);
+  if (u.t0 == 0) {
+    rec[0] = u.b;
+    rec[1] = u.hk;
+    rec[2] = u.rt;
+  } else {
+    rec[3] = u.t1 == u.tiles ? 1 : 2;
+  }
+}
 
 // Parent of node t of sequence s as the kernels use it: -1 a root, -2 padding.
 __device__ __forceinline__ int tree_parent(const TreeParams& P, const TreeSeq& s, int t) {
@@ -367,7 +386,7 @@ struct TileLoad {
 // infinity of V is not 0.  Keys at or past `origin` (drafted nodes, which not
 // every row sees) are therefore cleaned: their elements that are not finite
 // become 0 in shared memory, a bit per key remembers it, and the epilogue
-// applies them to the rows that do see the key (fix_value).  A weight of the
+// applies them to the rows that do see the key (fix_row).  A weight of the
 // softmax is positive, so the sum over visible keys has +-inf where one of
 // them has, and NaN where one has NaN or both infinities meet.
 __device__ __forceinline__ bool bf16x2_not_finite(uint32_t x) {
@@ -379,39 +398,36 @@ __device__ __forceinline__ uint32_t bf16x2_clean(uint32_t x) {
   return x;
 }
 
-// Adds to x what the keys flagged in nf (bit i: key origin + i) and seen
-// (bit i of `seen`) hold in column c, if that is not finite.
-__device__ __forceinline__ float fix_value(const TreeParams& P, const TreePiece& u,
-                                           const uint32_t* nf, const uint32_t* seen, int c,
-                                           float x) {
-#pragma unroll 1
-  for (int w = 0; w < 8; ++w) {
-    uint32_t bits = nf[w] & seen[w];
-#pragma unroll 1
-    while (bits) {
-      const int i = w * 32 + __ffs(bits) - 1;
-      bits &= bits - 1;
-      const int pos = u.origin + i;
-      const int pg = P.table[static_cast<int64_t>(u.b) * P.max_pages + (pos >> P.page_shift)];
-      if (pg < 0 || pg >= P.n_pages) continue;
-      const float v = __bfloat162float(P.v_pool[pg * P.v_stride[0] +
-                                                (pos & ((1 << P.page_shift) - 1)) * P.v_stride[1] +
-                                                u.hk * P.v_stride[2] + c]);
-      if (!isfinite(v)) x += v;
-    }
-  }
-  return x;
-}
-
-// fix_value over n elements of a row that has been written (bf16 or fp32):
-// row[i] holds column c0 + i.
+// Adds to elements [0, n) of a row that has been written (bf16 or fp32, row[i]
+// is column c0 + i) what the keys flagged in nf (bit i: key origin + i) and
+// seen (bit i of s0, s1) hold there, where that is not finite.  Arguments by
+// value: what has its address taken lives in local memory, and the little L1
+// that shared memory leaves does not hold it.
 template <typename T>
-static __device__ __noinline__ void fix_row(const TreeParams& P, const TreePiece& u, const uint32_t* nf,
-                                            const uint32_t* seen, int i0, int n, int c0, T* row) {
+static __device__ __noinline__ void fix_row(const TreeParams& P, int b, int hk, int origin,
+                                            const uint32_t* nf, uint4 s0, uint4 s1, int c0, int n,
+                                            T* row) {
 #pragma unroll 1
-  for (int i = i0; i < n; ++i) {
+  for (int i = 0; i < n; ++i) {
     const float x = static_cast<float>(row[i]);
-    const float y = fix_value(P, u, nf, seen, c0 + i, x);
+    float y = x;
+#pragma unroll 1
+    for (int w = 0; w < 8; ++w) {
+      const uint4 s = w < 4 ? s0 : s1;
+      const uint32_t seen = (w & 3) == 0 ? s.x : (w & 3) == 1 ? s.y : (w & 3) == 2 ? s.z : s.w;
+      uint32_t bits = nf[w] & seen;
+#pragma unroll 1
+      while (bits) {
+        const int pos = origin + w * 32 + __ffs(bits) - 1;
+        bits &= bits - 1;
+        const int pg = P.table[static_cast<int64_t>(b) * P.max_pages + (pos >> P.page_shift)];
+        if (pg < 0 || pg >= P.n_pages) continue;
+        const float v = __bfloat162float(P.v_pool[pg * P.v_stride[0] +
+                                                  (pos & ((1 << P.page_shift) - 1)) * P.v_stride[1] +
+                                                  hk * P.v_stride[2] + c0 + i]);
+        if (!isfinite(v)) y += v;
+      }
+    }
     if (!(x == y)) row[i] = static_cast<T>(y);
   }
 }

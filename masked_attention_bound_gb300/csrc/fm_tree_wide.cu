@@ -153,8 +153,7 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS>::THREADS, WideCfg<D, SLOTS>:
   grid_launch_dependents();
   grid_dependency_wait();
   tc_fence_before();
-  TreeWalk<typename C::Geo> walk;
-  walk.run = tree_run<typename C::Geo>(P);
+  TreeWalk<typename C::Geo> u(tree_run<typename C::Geo>(P));
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = *tmem_slot;
@@ -176,9 +175,8 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS>::THREADS, WideCfg<D, SLOTS>:
       const CUtensorMap* tm = isk ? &tmK : &tmV;
       const uint64_t policy = policy_evict_first();
       uint32_t st = 0, use = 0, issued = 0;    // stage, its uses so far, tiles issued
-      TreePiece u;
       bool ok = true;
-      while (ok && walk.next(P, u)) {
+      while (ok && u.next(P)) {
         if (u.keys == 0) continue;
         int page = Load::lane_page(P, u, u.t0, lane);
 #pragma unroll 1
@@ -217,8 +215,7 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS>::THREADS, WideCfg<D, SLOTS>:
       uint32_t qn = 0, np = 0;  // Q tiles, P tiles of this slot so far
       uint32_t turn = 0;        // turns taken
       bool ok = true;
-      TreePiece u;
-      while (ok && walk.next(P, u)) {
+      while (ok && u.next(P)) {
         const WideSplit w = wide_split<SLOTS>(u);
         if (w.n == 0) continue;
         // The two MMA warps take turns: a turn is one tile's PV and the next
@@ -392,17 +389,16 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS>::THREADS, WideCfg<D, SLOTS>:
     bool ok = true;
     uint32_t e0 = 0, pieces = 0, j = 0;                // j: tiles of this slot so far
     uint32_t pd0 = 0, pd1 = 0;                         // pieces in which slot 0 / 1 took part
-    int4 rec = make_int4(-1, 0, 0, 0);
-    TreePiece u;
-    while (walk.next(P, u)) {
+    if (tid == 0) P.rec[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    while (u.next(P)) {
       const WideSplit w = wide_split<SLOTS>(u);
       const int ur = w.rows ? slot * 128 + r : r;      // row of the unit
       const bool mine = ur < u.rows;
       const int rr = u.row_first + ur;
       const int node = ur < u.rows ? P.by_G(rr) : 0;
       const int h = u.hk * P.G + (ur < u.rows ? rr - node * P.G : 0);
-      __nv_bfloat16* orow = P.o + (u.s.row0 + node) * P.o_stride[0] + h * P.o_stride[1];
-      float* lse_out = P.lse + static_cast<int64_t>(h) * P.total + u.s.row0 + node;
+      auto out_row = [&]() { return P.o + (u.s.row0 + node) * P.o_stride[0] + h * P.o_stride[1]; };
+      auto out_lse = [&]() { return P.lse + static_cast<int64_t>(h) * P.total + u.s.row0 + node; };
       if (w.n == 0) {                                  // no keys: zeros in all its rows
         const int z = slot * 128 + r, zr = u.row_first + z, zn = P.by_G(zr), zh = u.hk * P.G + zr - zn * P.G;
         if (z < u.rows) {
@@ -415,18 +411,14 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS>::THREADS, WideCfg<D, SLOTS>:
       }
       const bool active = w.active(slot);
       if (lane == 0 && mine && u.whole()) {   // where the rows will go (see touch_memory)
-        touch(orow);
-        touch(lse_out);
+        touch(out_row());
+        touch(out_lse());
       }
       uint32_t* nf = nf_all + 8 * (pieces & 1);
       if (tid < 8) nf_all[8 * ((pieces + 1) & 1) + tid] = 0;   // the next piece's, read by nobody now
-      // which keys from origin on the row sees: bit i is key origin + i
-      uint32_t seen[8];
+      const int part0 = u.origin / KT;                 // tiles from here on are not seen by all
       bool live = mine;
-      const int part0 = u.origin / KT;              // tiles from here on are not seen by all
       if (P.tree) {
-#pragma unroll
-        for (int x = 0; x < 8; ++x) seen[x] = 0;
         if (mine) live = tree_parent(P, u.s, node) != -2;
         if (u.t1 > part0) {
           // the walks up the tree read shared memory: a parent from L2 took
@@ -434,9 +426,23 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS>::THREADS, WideCfg<D, SLOTS>:
           int16_t* par = reinterpret_cast<int16_t*>(smem + C::OFF_PAR);
           for (int i = tid; i < u.s.n; i += 128 * SLOTS) par[i] = static_cast<int16_t>(tree_parent(P, u.s, i));
           slots_sync<SLOTS>();
-          if (live) tree_ancestors(node, [&](int a) -> int { return par[a]; }, seen);
         }
       }
+      // which keys from origin on the row sees: bit i is key origin + i.
+      // Found again for each of the unit's few tiles that need it, which
+      // leaves eight registers to the loop.
+      auto row_sees = [&](uint32_t (&seen)[8]) {
+        if (P.tree) {
+          const int16_t* par = reinterpret_cast<const int16_t*>(smem + C::OFF_PAR);
+          tree_ancestors(live ? node : -1, [&](int a) -> int { return par[a]; }, seen);
+        } else {
+          const int upto = u.s.base + node - u.origin;   // last visible bit
+#pragma unroll
+          for (int x = 0; x < 8; ++x)
+            seen[x] = upto >= 32 * x + 31 ? 0xffffffffu
+                                          : (upto < 32 * x ? 0u : (2u << (upto - 32 * x)) - 1u);
+        }
+      };
       const bool warp_live = __any_sync(0xffffffffu, live);
       float m_used = -INFINITY, l = 0.f;
       if (active) {
@@ -474,24 +480,20 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS>::THREADS, WideCfg<D, SLOTS>:
               // what the row does not see becomes -inf, 32 columns at a time
               // and back to tensor memory: a few tiles of a unit at most, and
               // the loop below stays free of it
+              uint32_t seen[8];
+              row_sees(seen);
 #pragma unroll 1
               for (int y = 0; y < KT / 32; ++y) {
-                const int j0 = t * KT + 32 * y - u.origin;   // bit 0 is key origin + j0
-                uint32_t vis;
-                if (P.tree) {
-                  // the 64 bits from word (j0 >> 5) on, ones before bit 0
-                  const int i0 = j0 >> 5;
-                  uint32_t lo = i0 < 0 ? 0xffffffffu : 0u, hi = i0 + 1 < 0 ? 0xffffffffu : 0u;
+                const int j0 = t * KT + 32 * y - u.origin;      // bit 0 is key origin + j0
+                // the 64 bits from word (j0 >> 5) on, ones before bit 0
+                const int i0 = j0 >> 5;
+                uint32_t lo = i0 < 0 ? 0xffffffffu : 0u, hi = i0 + 1 < 0 ? 0xffffffffu : 0u;
 #pragma unroll
-                  for (int i = 0; i < 8; ++i) {
-                    lo = i == i0 ? seen[i] : lo;
-                    hi = i == i0 + 1 ? seen[i] : hi;
-                  }
-                  vis = __funnelshift_r(lo, hi, j0 & 31);
-                } else {
-                  const int upto = u.s.base + node - u.origin - j0;   // last visible bit
-                  vis = upto >= 31 ? 0xffffffffu : (upto < 0 ? 0u : (2u << upto) - 1u);
+                for (int i = 0; i < 8; ++i) {
+                  lo = i == i0 ? seen[i] : lo;
+                  hi = i == i0 + 1 ? seen[i] : hi;
                 }
+                const uint32_t vis = __funnelshift_r(lo, hi, j0 & 31);
                 uint32_t q[32];
                 tmem_ld32(tSj + 32 * y, q);
                 tmem_wait_ld();
@@ -549,14 +551,15 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS>::THREADS, WideCfg<D, SLOTS>:
                 ok = wait_all(W_PVTILE, (j - 1) & 1);
                 tc_fence_after();
               }
-              uint32_t ro[D];
+#pragma unroll 1
+              for (int y = 0; y < D / 32; ++y) {
+                uint32_t ro[32];
+                tmem_ld32(tO + 32 * y, ro);
+                tmem_wait_ld();
 #pragma unroll
-              for (int y = 0; y < D / 32; ++y) tmem_ld32(tO + 32 * y, ro + 32 * y);
-              tmem_wait_ld();
-#pragma unroll
-              for (int y = 0; y < D; ++y) ro[y] = __float_as_uint(__uint_as_float(ro[y]) * alpha);
-#pragma unroll
-              for (int y = 0; y < D / 32; ++y) tmem_st32(tO + 32 * y, ro + 32 * y);
+                for (int z = 0; z < 32; ++z) ro[z] = __float_as_uint(__uint_as_float(ro[z]) * alpha);
+                tmem_st32(tO + 32 * y, ro);
+              }
             }
             l += (sum4[0] + sum4[1]) + (sum4[2] + sum4[3]);
             tmem_wait_st();
@@ -637,7 +640,8 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS>::THREADS, WideCfg<D, SLOTS>:
       const float inv = whole ? (l_out > 0.f ? 1.f / l_out : (l_out == 0.f ? 0.f : l_out)) : 1.f;
       const int slot_part = 2 * blockIdx.x + (u.t0 == 0 ? 1 : 0);
       const int64_t at = static_cast<int64_t>(slot_part) * P.part_rows + ur;
-      float* prow = P.part_o + at * D;
+      float* const prow = P.part_o + at * D;
+      __nv_bfloat16* const orow = out_row();
       // O by blocks of 32 columns; each passes through the warp's part of the
       // slot's Q buffer (no longer needed), so that the stores cover whole
       // runs of a row: 64 bytes (bf16) or 128 bytes (fp32 parts)
@@ -710,7 +714,7 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS>::THREADS, WideCfg<D, SLOTS>:
         if (c0 == 0) {
           if (whole) {
             const float m_ref = m_out == -INFINITY ? 0.f : m_out;
-            *lse_out = l_out == 0.f ? -INFINITY : (m_ref + __log2f(l_out)) * 0.69314718055994530942f;
+            *out_lse() = l_out == 0.f ? -INFINITY : (m_ref + __log2f(l_out)) * 0.69314718055994530942f;
           } else {
             P.part_ml[at] = make_float2(m_out, l_out);
           }
@@ -719,26 +723,19 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS>::THREADS, WideCfg<D, SLOTS>:
 #pragma unroll
         for (int x = 0; x < 8; ++x) any |= nf[x];
         if (any) {
-          uint32_t see[8];
-#pragma unroll
-          for (int x = 0; x < 8; ++x) {
-            const int upto = u.s.base + node - u.origin - 32 * x;
-            see[x] = P.tree ? seen[x]
-                            : (upto >= 31 ? 0xffffffffu : (upto < 0 ? 0u : (2u << upto) - 1u));
-          }
-          if (whole) fix_row(P, u, nf, see, c0, c1, 0, orow);
-          else fix_row(P, u, nf, see, c0, c1, 0, prow);
+          uint32_t seen[8];
+          row_sees(seen);
+          const uint4 s0 = make_uint4(seen[0], seen[1], seen[2], seen[3]);
+          const uint4 s1 = make_uint4(seen[4], seen[5], seen[6], seen[7]);
+          if (whole) fix_row(P, u.b, u.hk, u.origin, nf, s0, s1, c0, c1 - c0, orow + c0);
+          else fix_row(P, u.b, u.hk, u.origin, nf, s0, s1, c0, c1 - c0, prow + c0);
         }
       }
-      if (!whole) {
-        if (u.t0 == 0) rec = make_int4(u.b, u.hk, u.rt, rec.w);
-        else rec.w = u.t1 == u.tiles ? 1 : 2;
-      }
+      if (tid == 0) leave_record(P, u);
       e0 += w.n;
       ++pieces;
       slots_sync<SLOTS>();        // ml and nf have been read, and S of both slots
     }
-    if (tid == 0) P.rec[blockIdx.x] = rec;
   }
 
   tc_fence_before();
