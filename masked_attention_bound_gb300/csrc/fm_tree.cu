@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(NarrowCfg<D>::THREADS, 2)
           }
         }
         mbar_arrive_warp(empty(ks));
-        uint32_t pf[4];
+        uint32_t pf[4], pl[4];
         if (ok && mine) {
           if (t >= part0 || k0 + 16 > u.keys) {
             // keys past origin: only what the row sees
@@ -279,12 +279,18 @@ __global__ void __launch_bounds__(NarrowCfg<D>::THREADS, 2)
               p[x][y] = ex2(fmaf(s[x][y], P.scale_log2, -ref[y >> 1]));
               l[y >> 1] += p[x][y];
             }
-          // P rounded to bf16 for the second product, as in the other
-          // forwards (the sum l keeps its 32 bits)
-          pf[0] = pack_bf16(p[0][0], p[0][1]);
-          pf[1] = pack_bf16(p[0][2], p[0][3]);
-          pf[2] = pack_bf16(p[1][0], p[1][1]);
-          pf[3] = pack_bf16(p[1][2], p[1][3]);
+          // P as the sum of two bf16 numbers (16 bits of mantissa): with one,
+          // its rounding is as large an error of O as the rounding of the
+          // output, and the tensor cores have the time here
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) {
+              const uint32_t hi = pack_bf16(p[x][2 * hh], p[x][2 * hh + 1]);
+              pf[2 * x + hh] = hi;
+              pl[2 * x + hh] = pack_bf16(p[x][2 * hh] - __uint_as_float(hi << 16),
+                                         p[x][2 * hh + 1] - __uint_as_float(hi & 0xffff0000u));
+            }
         }
         if (ok) ok = wait_all(full(C::KS + vs), vp);
         if (ok && mine) {
@@ -327,6 +333,8 @@ __global__ void __launch_bounds__(NarrowCfg<D>::THREADS, 2)
             ldsm4_t(sv + (ch >> 3) * (KT * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4), b);
             mma16816(acc[2 * kk], pf, b[0], b[1]);
             mma16816(acc[2 * kk + 1], pf, b[2], b[3]);
+            mma16816(acc[2 * kk], pl, b[0], b[1]);
+            mma16816(acc[2 * kk + 1], pl, b[2], b[3]);
           }
         }
         mbar_arrive_warp(empty(C::KS + vs));
