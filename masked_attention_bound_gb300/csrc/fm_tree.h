@@ -392,6 +392,12 @@ struct TileLoad {
 __device__ __forceinline__ bool bf16x2_not_finite(uint32_t x) {
   return (x & 0x7f80u) == 0x7f80u || (x & 0x7f800000u) == 0x7f800000u;
 }
+// x * 0 + sum of both halves.
+__device__ __forceinline__ uint32_t bf16x2_times_zero(uint32_t x, uint32_t sum) {
+  uint32_t y;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(y) : "r"(x), "r"(0u), "r"(sum));
+  return y;
+}
 __device__ __forceinline__ uint32_t bf16x2_clean(uint32_t x) {
   if ((x & 0x7f80u) == 0x7f80u) x &= 0xffff0000u;
   if ((x & 0x7f800000u) == 0x7f800000u) x &= 0xffffu;

@@ -389,6 +389,7 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS>::THREADS, WideCfg<D, SLOTS>:
     bool ok = true;
     uint32_t e0 = 0, pieces = 0, j = 0;                // j: tiles of this slot so far
     uint32_t pd0 = 0, pd1 = 0;                         // pieces in which slot 0 / 1 took part
+    int par_of = -1;                                   // the sequence whose parents are in shared memory
     if (tid == 0) P.rec[blockIdx.x] = make_int4(-1, 0, 0, 0);
     while (u.next(P)) {
       const WideSplit w = wide_split<SLOTS>(u);
@@ -414,19 +415,26 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS>::THREADS, WideCfg<D, SLOTS>:
         touch(out_row());
         touch(out_lse());
       }
+      // the next unit's Q, if it is this sequence's next head: to L2
+      if (mine && u.next_tile < 0 && u.left > 0 && u.hk + 1 < P.Hkv)
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c)
+          touch(P.q + (u.s.row0 + node) * P.q_stride[0] + (h + P.G) * P.q_stride[1] + c * 64);
       uint32_t* nf = nf_all + 8 * (pieces & 1);
       if (tid < 8) nf_all[8 * ((pieces + 1) & 1) + tid] = 0;   // the next piece's, read by nobody now
       const int part0 = u.origin / KT;                 // tiles from here on are not seen by all
       bool live = mine;
       if (P.tree) {
-        if (mine) live = tree_parent(P, u.s, node) != -2;
-        if (u.t1 > part0) {
-          // the walks up the tree read shared memory: a parent from L2 took
-          // 700 cycles a step
-          int16_t* par = reinterpret_cast<int16_t*>(smem + C::OFF_PAR);
+        // the sequence's parents, in shared memory for all its units: from L2
+        // a step up the tree took 700 cycles
+        int16_t* par = reinterpret_cast<int16_t*>(smem + C::OFF_PAR);
+        if (par_of != u.b) {
+#pragma unroll 1
           for (int i = tid; i < u.s.n; i += 128 * SLOTS) par[i] = static_cast<int16_t>(tree_parent(P, u.s, i));
           slots_sync<SLOTS>();
+          par_of = u.b;
         }
+        if (mine) live = par[node] != -2;
       }
       // which keys from origin on the row sees: bit i is key origin + i.
       // Found again for each of the unit's few tiles that need it, which
@@ -485,6 +493,7 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS>::THREADS, WideCfg<D, SLOTS>:
 #pragma unroll 1
               for (int y = 0; y < KT / 32; ++y) {
                 const int j0 = t * KT + 32 * y - u.origin;      // bit 0 is key origin + j0
+                if (j0 <= -32) continue;                        // seen by all
                 // the 64 bits from word (j0 >> 5) on, ones before bit 0
                 const int i0 = j0 >> 5;
                 uint32_t lo = i0 < 0 ? 0xffffffffu : 0u, hi = i0 + 1 < 0 ? 0xffffffffu : 0u;
@@ -583,12 +592,16 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS>::THREADS, WideCfg<D, SLOTS>:
 #pragma unroll 1
                 for (int c = 0; c < D / 8; ++c) *word(c) = make_uint4(0u, 0u, 0u, 0u);
               } else if (i >= 0) {
+                uint32_t zero = 0;             // 0, or NaN once a value was not finite
 #pragma unroll 4
                 for (int c = 0; c < D / 8; ++c) {
                   const uint4 y = *word(c);
-                  dirty |= bf16x2_not_finite(y.x) || bf16x2_not_finite(y.y) || bf16x2_not_finite(y.z) ||
-                           bf16x2_not_finite(y.w);
+                  zero = bf16x2_times_zero(y.x, zero);
+                  zero = bf16x2_times_zero(y.y, zero);
+                  zero = bf16x2_times_zero(y.z, zero);
+                  zero = bf16x2_times_zero(y.w, zero);
                 }
+                dirty = bf16x2_not_finite(zero);
               }
               if (dirty) {
                 // the flag first: whoever finds the row clean finds the flag
