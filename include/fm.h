@@ -306,7 +306,8 @@ fm_status fm_varlen_bounds(const int32_t* cu_seqlens, int n_seqs, int total, int
  *   cu [B + 1]            rows of a packed batch of new tokens: cu[0] = 0,
  *                         sequence b's are [cu[b], cu[b+1]), cu[B] <= total;
  *                         packed rows past cu[B] are neither read nor written
- * Tokens with index above 2^30 are not supported.
+ * Rows of more than 2^30 tokens, B * max_pages above 2^31 - 1 and more than
+ * 65535 K/V heads are not supported.
  *
  * `status`: a device int32 owned by the caller, or null.  What the kernels
  * find wrong is or-ed into it and never cleared by the library; it is read
@@ -352,8 +353,8 @@ fm_status fm_cache_append(const fm_cache* cache, const void* k, const void* v,
  * has no part in its result, whatever its K and V hold (NaN and infinities
  * included).  Rows that see no key get O = 0 and LSE = -inf.
  * q, o: bf16, element (token, head, c) at token*stride[0] + head*stride[1] +
- * c; lse: fp32 [H][total].  scale: positive and finite.  max_nodes: an upper bound of n over the batch.
- * Sequences with lens or cu out of range or more than max_nodes nodes get
+ * c; lse: fp32 [H][total].  scale: positive, and scale * log2(e) a normal
+ * finite number.  max_nodes: an upper bound of n over the batch.  Sequences with lens or cu out of range or more than max_nodes nodes get
  * O = 0, LSE = -inf on those of their rows that lie in [0, total); keys on
  * a page that is out of range read as 0, and a parent that is out of range
  * counts as -1 (FM_ERR_CACHE).  The result of a call
@@ -468,7 +469,8 @@ fm_status fm_measure_exp2_rate(double* per_second, void* stream);
  * their first "P ready" arrival in each CTA), 2 fm_bwd's dK/dV pass (the
  * compute warps skip their first "P ready" arrival in each CTA), 3 fm_bwd's
  * dQ pass (the compute warps skip their first "dS ready" arrival in each
- * CTA).  For tests of the unwind
+ * CTA), 8 fm_tree_fwd (the compute warps skip their first "stage free" or
+ * "P ready" arrival in each CTA).  For tests of the unwind
  * path only; calls that overlap a change of these settings see either value.
  * FM_ERR_INVALID for other withhold values. */
 fm_status fm_test_hooks(uint64_t wait_limit_ns, int withhold_release);

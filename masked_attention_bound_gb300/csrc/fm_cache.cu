@@ -23,9 +23,11 @@ fm_status check_cache(const fm_cache* c, bool pools) {
   if (c->n_pages > kMaxPoolPages ||
       static_cast<int64_t>(c->max_pages) * c->page_size > kMaxTokenIndex)
     return FM_ERR_UNSUPPORTED;
+  // sums of pages over the rows are counted in 31 bits
+  if (static_cast<int64_t>(c->B) * c->max_pages > 0x7fffffff) return FM_ERR_UNSUPPORTED;
   if (!pools) return FM_OK;
   if (c->Hkv < 1 || c->layers < 1) return FM_ERR_INVALID;
-  if (c->d != 64 && c->d != 128) return FM_ERR_UNSUPPORTED;
+  if ((c->d != 64 && c->d != 128) || c->Hkv > kMaxHeads) return FM_ERR_UNSUPPORTED;
   for (const int64_t* st : {c->k_stride, c->v_stride})
     for (int i = 0; i < 4; ++i)
       if (st[i] <= 0 || st[i] % 8 != 0 || st[i] >= (int64_t(1) << 36)) return FM_ERR_INVALID;
@@ -79,7 +81,7 @@ __device__ __forceinline__ int context_of(const int32_t* lens, const int32_t* cu
                                           int max_tokens, int& n) {
   const int c0 = cu[b], c1 = cu[b + 1], len = lens[b];
   n = c1 - c0;
-  if (c0 < 0 || n < 0 || c1 > total || len > max_tokens || len < n) return -1;
+  if (c0 < 0 || c1 < c0 || c1 > total || len > max_tokens || len < n) return -1;
   return len - n;
 }
 

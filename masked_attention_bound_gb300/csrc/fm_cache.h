@@ -8,6 +8,7 @@ namespace fm {
 
 constexpr int kMaxTokenIndex = 1 << 30;   // tokens of a row (32-bit positions)
 constexpr int kMaxPoolPages = (1 << 23) - 1;
+constexpr int kMaxHeads = 65535;
 
 // Sizes of `c` that every cache entry point needs; `pools`: its pools' too.
 fm_status check_cache(const fm_cache* c, bool pools);

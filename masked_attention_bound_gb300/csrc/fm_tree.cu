@@ -1,6 +1,7 @@
 // Attention of drafted trees and single tokens over the paged cache: the
 // entry point, the kernel for units of up to 16 rows, and the join of units
 // that several blocks worked on.
+#include <cfloat>
 #include <cmath>
 
 #include "fm_tree.h"
@@ -231,7 +232,9 @@ __global__ void __launch_bounds__(NarrowCfg<D>::THREADS, 2)
             mma16816(s[1], qf[kk], b[2], b[3]);
           }
         }
-        mbar_arrive_warp(empty(ks));
+        // (a test of the wait limit withholds the first one: the K loader's
+        // wait for the stage then runs out)
+        if (!(P.withhold == 8 && e == 1)) mbar_arrive_warp(empty(ks));
         uint32_t pf[4], pl[4];
         if (ok && mine) {
           if (t >= part0 || k0 + 16 > u.keys) {
@@ -746,8 +749,10 @@ fm_status fm_tree_fwd(const fm_cache* c, const fm_tree_desc* t, const void* q, c
   if (!aligned_to(q, 16) || !aligned_to(k_pool, 16) || !aligned_to(v_pool, 16) || !aligned_to(o, 16))
     return FM_ERR_INVALID;
   if (!table || !lens || !cu || !lse) return FM_ERR_INVALID;
-  // masked scores are -inf and the largest score is the largest product
-  if (!(scale > 0.f && scale < INFINITY)) return FM_ERR_INVALID;
+  // masked scores are -inf, the largest score is the largest product, and a
+  // masked score times the scale is -inf again
+  const float scale_log2 = scale * 1.4426950408889634f;
+  if (!(scale_log2 >= FLT_MIN && scale_log2 < INFINITY)) return FM_ERR_INVALID;
   const TreeWs W = tree_ws(*c, *t, num_sms());
   const int grid = W.grid;
   if (!aligned_to(ws, 256) || ws_bytes < W.bytes) return FM_ERR_WORKSPACE;
@@ -771,7 +776,7 @@ fm_status fm_tree_fwd(const fm_cache* c, const fm_tree_desc* t, const void* q, c
   // of 480 keys took 48 us whole and 43 us cut and joined.
   const int64_t tokens = static_cast<int64_t>(c->max_pages) * c->page_size;
   P.whole = tokens <= 320 || (tokens <= 512 && static_cast<int64_t>(c->B) * c->Hkv <= grid);
-  P.scale_log2 = scale * 1.4426950408889634f;
+  P.scale_log2 = scale_log2;
   P.q = static_cast<const __nv_bfloat16*>(q);
   P.o = static_cast<__nv_bfloat16*>(o);
   for (int i = 0; i < 2; ++i) {
@@ -809,9 +814,8 @@ fm_status fm_tree_fwd(const fm_cache* c, const fm_tree_desc* t, const void* q, c
     if (st != FM_OK) return st;
     return d64 ? launch_join<MidGeo::R, 64>(P, grid, s) : launch_join<MidGeo::R, 128>(P, grid, s);
   }
-  st = launch_tree_wide(P, c->d, tk, tv, grid, s);
-  if (st != FM_OK) return st;
-  return d64 ? launch_join<WideGeo::R, 64>(P, grid, s) : launch_join<WideGeo::R, 128>(P, grid, s);
+  st = launch_tree_wide(P, tk, tv, grid, s);
+  return st != FM_OK ? st : launch_join<WideGeo::R, 128>(P, grid, s);
 }
 
 }  // extern "C"

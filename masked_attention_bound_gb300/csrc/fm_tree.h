@@ -40,7 +40,7 @@ struct TreeParams {
   float* part_o;           // [2 * grid][part_rows][D]
   int* status;
   uint32_t wait_ns;        // limit of every mbarrier wait
-  int withhold;
+  int withhold;            // test hook: 8 = the consumers skip their first arrival, see fm_test_hooks
 };
 
 // What a block leaves for the join: the unit that it starts and does not
@@ -60,10 +60,10 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeParams& P, int b) {
   s.row0 = c0;
   s.n = c1 - c0;
   s.base = len - s.n;
-  if (c0 < 0 || s.n < 0 || c1 > P.total || s.n > P.max_nodes || len < s.n ||
+  if (c0 < 0 || c1 < c0 || c1 > P.total || s.n > P.max_nodes || len < s.n ||
       len > (P.max_pages << P.page_shift)) {
     // the rows that can be written get zeros
-    const int lo = max(c0, 0), hi = min(c1, P.total);
+    const int lo = min(max(c0, 0), P.total), hi = min(max(c1, 0), P.total);
     s.row0 = lo;
     s.n = max(hi - lo, 0);
     s.base = -1;
@@ -442,7 +442,7 @@ static __device__ __noinline__ void fix_row(const TreeParams& P, int b, int hk, 
 // for up to 16 rows and the join of their parts are in fm_tree.cu.
 fm_status launch_tree_mid(const TreeParams& P, int d, const CUtensorMap& tk, const CUtensorMap& tv,
                           int grid, cudaStream_t s);
-fm_status launch_tree_wide(const TreeParams& P, int d, const CUtensorMap& tk, const CUtensorMap& tv,
-                           int grid, cudaStream_t s);
+fm_status launch_tree_wide(const TreeParams& P, const CUtensorMap& tk, const CUtensorMap& tv, int grid,
+                           cudaStream_t s);   // d = 128
 
 }  // namespace fm

@@ -34,6 +34,7 @@ namespace fm {
 template <int D, int SLOTS_>
 struct WideCfg {
   static constexpr int SLOTS = SLOTS_;
+  static_assert(D == 128 || SLOTS == 1, "d = 64 runs with tiles of 128 rows side by side");
   using Geo = std::conditional_t<SLOTS == 2, WideGeo, MidGeo>;
   static constexpr int KT = Geo::KT;
   static constexpr int TILE = KT * D * 2;               // bytes of a K or V tile
@@ -618,7 +619,9 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS>::THREADS, WideCfg<D, SLOTS>:
             }
           }
           tc_fence_before();
-          mbar_arrive_warp(bar(W_PFULL + buf));
+          // (a test of the wait limit withholds the first one of slot 0: its
+          // MMA warp's wait then runs out)
+          if (!(P.withhold == 8 && slot == 0 && j == 0)) mbar_arrive_warp(bar(W_PFULL + buf));
           ++j;
           ++done;
         }
@@ -779,9 +782,9 @@ fm_status launch_tree_mid(const TreeParams& P, int d, const CUtensorMap& tk, con
   return d == 64 ? launch_wide_d<64, 1>(P, tk, tv, grid, s) : launch_wide_d<128, 1>(P, tk, tv, grid, s);
 }
 
-fm_status launch_tree_wide(const TreeParams& P, int d, const CUtensorMap& tk, const CUtensorMap& tv,
-                           int grid, cudaStream_t s) {
-  return d == 64 ? launch_wide_d<64, 2>(P, tk, tv, grid, s) : launch_wide_d<128, 2>(P, tk, tv, grid, s);
+fm_status launch_tree_wide(const TreeParams& P, const CUtensorMap& tk, const CUtensorMap& tv, int grid,
+                           cudaStream_t s) {
+  return launch_wide_d<128, 2>(P, tk, tv, grid, s);
 }
 
 }  // namespace fm

@@ -51,7 +51,7 @@ def _tree(L, C, D, q=0, parents=8, scale=0.1, ws=9, ws_bytes=1 << 30, **null):
 BAD_CACHE = [("B", 0, INVALID), ("Hkv", 0, INVALID), ("d", 96, UNSUPPORTED), ("page_size", 8, UNSUPPORTED),
              ("page_size", 48, UNSUPPORTED), ("page_size", 256, UNSUPPORTED), ("n_pages", 0, INVALID),
              ("n_pages", (1 << 24) + 1, UNSUPPORTED), ("max_pages", 0, INVALID),
-             ("max_pages", (1 << 26) + 1, UNSUPPORTED), ("layers", 0, INVALID)]
+             ("max_pages", (1 << 26) + 1, UNSUPPORTED), ("layers", 0, INVALID), ("B", 1 << 30, UNSUPPORTED), ("Hkv", 1 << 16, UNSUPPORTED)]
 
 
 @pytest.mark.parametrize("field,value,code", BAD_CACHE)
@@ -98,7 +98,7 @@ def test_unaligned_tensors(L, i):
     assert _tree(L, _cache(), _desc(), **{f"a{i}": ctypes.c_void_p((1 << 28) + 8)}) == INVALID
 
 
-@pytest.mark.parametrize("scale", [0.0, -1.0, float("nan"), float("inf")])
+@pytest.mark.parametrize("scale", [0.0, -1.0, float("nan"), float("inf"), 1e-39, 3e38])
 def test_bad_scales(L, scale):
     assert _tree(L, _cache(), _desc(), scale=scale) == INVALID
 

@@ -291,3 +291,87 @@ def test_excess_sees_a_wrong_row():
     with pytest.raises(AssertionError):
         b.check(o, lse)
     assert o_excess(o.float().cpu().numpy(), o.float().cpu().numpy(), 0 * o.float().cpu().numpy()).max() <= 0
+
+
+@pytest.mark.parametrize("nodes,d", [(1, 128), (1, 64), (16, 128), (16, 64), (50, 128)])
+def test_a_wait_that_runs_out_is_reported_then_the_next_call_is_clean(nodes, d):
+    """A hook withholds one release in each block (see fm_test_hooks): its wait runs out after 20 ms, and
+    the call ends by itself with the status set; one for each kernel."""
+    b = Batch(20, [2100] * 8, [nodes] * 8, 32, 8, d, 16, "random")
+    ws = fm.tree_workspace(b.q, b.k, b.v, b.table, nodes)
+    ws.zero_()
+    assert fm.lib().fm_test_hooks(20_000_000, 8) == _abi.FM_OK
+    try:
+        _, _, code = run(b, max_nodes=nodes, ws=ws)
+    finally:
+        assert fm.lib().fm_test_hooks(0, 0) == _abi.FM_OK
+    assert code == _abi.FM_ERR_TIMEOUT, _abi.status_string(code)
+    o, lse, code = run(b, max_nodes=nodes, ws=ws)
+    assert code == 0
+    b.check(o, lse, rows=10)
+
+
+@pytest.mark.parametrize("nodes", [1, 24, 70])
+def test_two_calls_at_once(nodes):
+    """Two streams, a workspace each (the default), the kernels in flight together."""
+    b = Batch(21, [6000, 900, 3000], [nodes] * 3, 8, 2, 128, 16, "random")
+    want = run(b)[:2]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    outs = []
+    for i in range(30):
+        outs.append(fm.tree_forward(b.q, b.k, b.v, b.table, b.lens_t, b.cu, b.scale, parents=b.parents,
+                                    max_nodes=nodes, stream=streams[i % 2]))
+    torch.cuda.synchronize()
+    for got in outs:
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_two_graphs_share_a_workspace():
+    b = Batch(22, [3000, 700], [20, 20], 8, 2, 128, 16, "random")
+    ws = fm.tree_workspace(b.q, b.k, b.v, b.table, 20)
+    want = run(b)[:2]
+    graphs, outs = [], []
+    lens = [b.lens_t, b.lens_t.clone()]
+    for i in range(2):
+        outs.append((torch.empty_like(b.q), torch.empty_like(want[1])))
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            fm.tree_forward(b.q, b.k, b.v, b.table, lens[i], b.cu, b.scale, parents=b.parents, max_nodes=20,
+                            o=outs[i][0], lse=outs[i][1], ws=ws)
+        graphs.append(g)
+    lens[1].sub_(100)
+    second = fm.tree_forward(b.q, b.k, b.v, b.table, lens[1], b.cu, b.scale, parents=b.parents, max_nodes=20)
+    for _ in range(20):
+        for g in graphs:
+            g.replay()
+    torch.cuda.synchronize()
+    for got, ref in zip(outs, (want, second)):
+        assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
+
+
+@pytest.mark.parametrize("nodes,longest", [(1, 60), (1, 1500), (5, 400), (30, 700)])
+def test_many_sequences(nodes, longest):
+    """More sequences than a warp has lanes, of mixed lengths, some without nodes."""
+    n = [nodes if i % 7 else 0 for i in range(333)]
+    lens = [max(m, 1 + (i * 7919) % longest) for i, m in enumerate(n)]
+    b = Batch(23, lens, n, 4, 2, 64, 16, None if nodes == 1 else "random")
+    o, lse, code = run(b)
+    assert code == 0
+    b.check(o, lse, rows=3)
+
+
+@pytest.mark.parametrize("nodes,kind", [(1, None), (24, "random")])
+def test_offsets_at_the_ends_of_32_bits_are_reported_and_stay_in_bounds(nodes, kind):
+    b = Batch(24, [100, 50, 200, 90], [nodes] * 4, 4, 2, 64, 16, kind)
+    top, low = 2 ** 31 - 1, -2 ** 31
+    for cu in ([0, top, low, top, low], [top, low, 0, top, 4 * nodes], [low, low, top, top, top],
+               [0, nodes, top, low, 4 * nodes]):
+        b.cu.copy_(ints(cu))
+        around = torch.full((b.q.shape[0] + 64, 4, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        fm.tree_forward(b.q, b.k, b.v, b.table, b.lens_t, b.cu, b.scale, parents=b.parents, max_nodes=nodes,
+                        o=around[32:-32], status=status)
+        torch.cuda.synchronize()
+        assert fm.device_status(status) == _abi.FM_ERR_CACHE
+        assert (around[:32] == 7).all() and (around[-32:] == 7).all()
