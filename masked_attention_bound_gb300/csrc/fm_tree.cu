@@ -541,7 +541,8 @@ __global__ void __launch_bounds__(kJoinThreads)
   // warps per row
   int wpr = 1;
 #pragma unroll 1
-  while (wpr < NW && 2 * wpr <= parts && rows * 2 * wpr <= (last - c) * static_cast<int>(gridDim.y) * NW)
+  while (wpr < NW && 2 * wpr <= parts &&
+         (parts > 32 * wpr || rows * 2 * wpr <= (last - c) * static_cast<int>(gridDim.y) * NW))
     wpr *= 2;
   if (wpr == 1) {
     // a warp joins RPW rows at a time, to have their loads in flight together
@@ -550,12 +551,20 @@ __global__ void __launch_bounds__(kJoinThreads)
     for (int r0 = (first * NW + warp) * RPW; r0 < rows; r0 += step * NW * RPW) {
       float mm[RPW], f[RPW], ll[RPW], v[RPW][CPT];
       unsigned seen[RPW];
-      // lane i: maximum and sum of part i (there are eight at most: with more,
-      // the warps outnumber the rows); a sum of 0 says that its keys were not seen
+      // lane i: maximum and sum of part i; a sum of 0 says that its keys were
+      // not seen
       float2 p[RPW];
 #pragma unroll
       for (int k = 0; k < RPW; ++k)
         p[k] = lane < parts && r0 + k < rows ? pm[at(lane, r0 + k)] : make_float2(-INFINITY, 0.f);
+      // and, at the same time, the first two parts' rows (there are two at least)
+      float y0[RPW][CPT], y1[RPW][CPT];
+#pragma unroll
+      for (int k = 0; k < RPW; ++k)
+        if (r0 + k < rows) {
+          load(0, r0 + k, y0[k]);
+          load(1, r0 + k, y1[k]);
+        }
 #pragma unroll
       for (int k = 0; k < RPW; ++k) {
         mm[k] = p[k].x;
@@ -569,12 +578,7 @@ __global__ void __launch_bounds__(kJoinThreads)
 #pragma unroll
         for (int x = 0; x < CPT; ++x) v[k][x] = 0.f;
       }
-#pragma unroll 1
-      for (int i = 0; i < parts; ++i) {
-        float y[RPW][CPT];
-#pragma unroll
-        for (int k = 0; k < RPW; ++k)
-          if (r0 + k < rows) load(i, r0 + k, y[k]);
+      auto add = [&](int i, const float (&y)[RPW][CPT]) {
 #pragma unroll
         for (int k = 0; k < RPW; ++k) {
           const float w = __shfl_sync(0xffffffffu, f[k], i);
@@ -582,6 +586,15 @@ __global__ void __launch_bounds__(kJoinThreads)
 #pragma unroll
             for (int x = 0; x < CPT; ++x) v[k][x] += y[k][x] * w;
         }
+      };
+      add(0, y0);
+      add(1, y1);
+#pragma unroll 1
+      for (int i = 2; i < parts; ++i) {
+#pragma unroll
+        for (int k = 0; k < RPW; ++k)
+          if (r0 + k < rows) load(i, r0 + k, y0[k]);
+        add(i, y0);
       }
 #pragma unroll
       for (int k = 0; k < RPW; ++k)
@@ -662,10 +675,18 @@ template <int R, int D>
 static fm_status launch_join(const TreeParams& P, int grid, cudaStream_t s) {
   if (grid < 2 || P.whole) return FM_OK;
   if (grid > kMaxJoin) return FM_ERR_UNSUPPORTED;
-  // the blocks of a unit in two parts take its rows in one go
+  // Columns of the grid, for as many units as there can be: one group of rows
+  // a warp, or a warp a row where units are in 32 parts or more, which then
+  // take eight warps a row.  (Columns for units of two parts throughout left
+  // 3 us more between the kernel and the end of the join of two units of 131072
+  // keys: their blocks start in turn.)
+  const int64_t units = P.B * P.Hkv * ((static_cast<int64_t>(P.max_nodes) * P.G + R - 1) / R);
+  const int64_t rows = (units < grid ? units : grid) * P.part_rows;
+  const int64_t per_block = units * 32 <= grid ? 1 : kJoinThreads / 32 * (R == NarrowGeo::R ? 2 : 4);
+  const int y = static_cast<int>((rows + grid * per_block - 1) / (grid * per_block));
   prof_begin(K_TREE_JOIN, s);
   const cudaError_t e = launch_dependent(
-      tree_join_kernel<R, D>, dim3(grid - 1, ceil_div(P.part_rows, kJoinThreads / 32 * (R == NarrowGeo::R ? 2 : 4))), kJoinThreads,
+      tree_join_kernel<R, D>, dim3(grid - 1, y), kJoinThreads,
       0, s, P, grid);
   prof_end(K_TREE_JOIN, s);
   return e == cudaSuccess ? FM_OK : FM_ERR_CUDA;
