@@ -286,18 +286,9 @@ __device__ __forceinline__ int pages_of(const PageArgs& A, int b, int& len, bool
   return (len + A.page_size - 1) / A.page_size;
 }
 
-__global__ void __launch_bounds__(256) ref_copy_kernel(const int32_t* from, int32_t* to, int n) {
-  grid_launch_dependents();
-  grid_dependency_wait();
-  for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < n; i += gridDim.x * blockDim.x) to[i] = from[i];
-}
-
 // One warp per row: the new row's pages gain a hold, the old row's lose one.
-__global__ void __launch_bounds__(128) fork_kernel(const __grid_constant__ PageArgs A, const int32_t* parent) {
-  grid_launch_dependents();
-  grid_dependency_wait();
-  const int b = (blockIdx.x * blockDim.x + threadIdx.x) >> 5, lane = threadIdx.x & 31;
-  if (b >= A.B) return;
+__device__ __forceinline__ void fork_row(const PageArgs& A, const int32_t* parent, int b) {
+  const int lane = threadIdx.x & 31;
   int p = parent[b];
   bool ok = p >= -1 && p < A.B;
   if (!ok) p = -1;
@@ -324,13 +315,44 @@ __global__ void __launch_bounds__(128) fork_kernel(const __grid_constant__ PageA
   if (!ok) flag(A.status, DEV_CACHE);
 }
 
+// ref_out has the old counts already: it is ref itself, or ref_copy_kernel ran.
+__global__ void __launch_bounds__(128) fork_kernel(const __grid_constant__ PageArgs A, const int32_t* parent) {
+  grid_launch_dependents();
+  grid_dependency_wait();
+  const int b = (blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+  if (b < A.B) fork_row(A, parent, b);
+}
+// Both by one block, for few pages and rows.
+__global__ void __launch_bounds__(1024)
+    fork_copy_kernel(const __grid_constant__ PageArgs A, const int32_t* parent) {
+  grid_launch_dependents();
+  grid_dependency_wait();
+#pragma unroll 4
+  for (int i = threadIdx.x; i < A.n_pages; i += 1024) A.ref_out[i] = A.ref[i];
+  __syncthreads();
+  for (int b = threadIdx.x >> 5; b < A.B; b += 32) fork_row(A, parent, b);
+}
+__global__ void __launch_bounds__(256) ref_copy_kernel(const int32_t* from, int32_t* to, int n) {
+  grid_launch_dependents();
+  grid_dependency_wait();
+  for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < n; i += gridDim.x * blockDim.x) to[i] = from[i];
+}
+
 // ------------------------------------------------------------------ page plans
 // Reserve and compact rank the pages of the pool by prefix sums of the
-// reference counts.  One cluster of eight blocks does it in a single launch:
-// each block owns an eighth of the pages (and of the rows), the blocks
-// exchange their sums through distributed shared memory, and the cluster
-// barrier separates the passes.
-constexpr int kPlanBlocks = 8, kPlanThreads = 1024;
+// reference counts.  One cluster of N blocks does it in a single launch: each
+// block owns an N-th of the pages (and of the rows), the blocks exchange their
+// sums through distributed shared memory, and the cluster barrier separates
+// the passes.  N is 8, or 1 where a block has few pages and rows to a thread:
+// its barriers are cheaper.
+constexpr int kPlanThreads = 1024;
+
+template <int N>
+__device__ __forceinline__ void plan_sync(cg::cluster_group& cl) {
+  if constexpr (N == 1) __syncthreads();
+  else cl.sync();
+}
+
 
 // Regions of the pages workspace (int32 words).
 struct PlanWs {
@@ -402,11 +424,12 @@ struct PlanShared {
 };
 
 // Exchange: sums over the blocks before this one, and over all, of `said`.
+template <int N>
 __device__ __forceinline__ void exchange(cg::cluster_group& cl, PlanShared& sh, int n) {
-  cl.sync();
+  plan_sync<N>(cl);
   if (threadIdx.x < n) {
     int before = 0, all = 0;
-    for (int r = 0; r < kPlanBlocks; ++r) {
+    for (int r = 0; r < N; ++r) {
       const int x = *cl.map_shared_rank(&sh.said[threadIdx.x], r);
       if (r < static_cast<int>(cl.block_rank())) before += x;
       all += x;
@@ -414,11 +437,12 @@ __device__ __forceinline__ void exchange(cg::cluster_group& cl, PlanShared& sh, 
     sh.before[threadIdx.x] = before;
     sh.all[threadIdx.x] = all;
   }
-  cl.sync();                             // nobody's numbers change before all have read them
+  plan_sync<N>(cl);                      // nobody's numbers change before all have read them
 }
 
 // info (the caller's): free pages after the call, pages asked for.
-__global__ void __cluster_dims__(kPlanBlocks, 1, 1) __launch_bounds__(kPlanThreads, 1)
+template <int N>
+__global__ void __cluster_dims__(N, 1, 1) __launch_bounds__(kPlanThreads, 1)
     reserve_kernel(const __grid_constant__ PageArgs A, const int32_t* grow,
                    const __grid_constant__ PlanWs W, int32_t* info) {
   cg::cluster_group cl = cg::this_cluster();
@@ -427,9 +451,9 @@ __global__ void __cluster_dims__(kPlanBlocks, 1, 1) __launch_bounds__(kPlanThrea
   const int rank = cl.block_rank();
   grid_launch_dependents();
   grid_dependency_wait();
-  const int rows = (A.B + kPlanBlocks - 1) / kPlanBlocks;
+  const int rows = (A.B + N - 1) / N;
   const int b0 = min(rank * rows, A.B), b1 = min(b0 + rows, A.B);
-  const int span = (A.n_pages + kPlanBlocks - 1) / kPlanBlocks;
+  const int span = (A.n_pages + N - 1) / N;
   const int p0 = min(rank * span, A.n_pages), p1 = min(p0 + span, A.n_pages);
   constexpr int kReplace = 1 << 30;
 
@@ -470,7 +494,7 @@ __global__ void __cluster_dims__(kPlanBlocks, 1, 1) __launch_bounds__(kPlanThrea
     sh.said[1] = free_pages;
     sh.said[2] = bad;
   }
-  exchange(cl, sh, 3);
+  exchange<N>(cl, sh, 3);
   const int total = sh.all[0], n_free = sh.all[1];
   const bool refused = sh.all[2] != 0;
   const bool full = total > n_free;
@@ -496,7 +520,7 @@ __global__ void __cluster_dims__(kPlanBlocks, 1, 1) __launch_bounds__(kPlanThrea
     if (refused) flag(A.status, DEV_CACHE);
     if (full) flag(A.status, DEV_PAGES);
   }
-  cl.sync();                             // the list is complete, and ref_out
+  plan_sync<N>(cl);                      // the list is complete, and ref_out
 
   // the rows, 1024 at a time: a thread each for the counts, then a warp each
   // for the entries
@@ -538,12 +562,13 @@ __global__ void __cluster_dims__(kPlanBlocks, 1, 1) __launch_bounds__(kPlanThrea
   }
   released = block_sum(released, sh.warp_sums);
   if (threadIdx.x == 0) sh.said[0] = released;
-  exchange(cl, sh, 1);
+  exchange<N>(cl, sh, 1);
   if (rank == 0 && threadIdx.x == 0) info[0] = n_free - (go ? total : 0) + sh.all[0];
 }
 
 // info of the workspace: [0] moves, [1] held pages
-__global__ void __cluster_dims__(kPlanBlocks, 1, 1) __launch_bounds__(kPlanThreads, 1)
+template <int N>
+__global__ void __cluster_dims__(N, 1, 1) __launch_bounds__(kPlanThreads, 1)
     compact_kernel(const __grid_constant__ PageArgs A, const __grid_constant__ PlanWs W,
                    int32_t* n_live_out) {
   cg::cluster_group cl = cg::this_cluster();
@@ -551,14 +576,14 @@ __global__ void __cluster_dims__(kPlanBlocks, 1, 1) __launch_bounds__(kPlanThrea
   const int rank = cl.block_rank();
   grid_launch_dependents();
   grid_dependency_wait();
-  const int span = (A.n_pages + kPlanBlocks - 1) / kPlanBlocks;
+  const int span = (A.n_pages + N - 1) / N;
   const int p0 = min(rank * span, A.n_pages), p1 = min(p0 + span, A.n_pages);
   int live = 0;
 #pragma unroll 4
   for (int p = p0 + threadIdx.x; p < p1; p += kPlanThreads) live += A.ref[p] != 0;
   live = block_sum(live, sh.warp_sums);
   if (threadIdx.x == 0) sh.said[0] = live;
-  exchange(cl, sh, 1);
+  exchange<N>(cl, sh, 1);
   const int n_live = sh.all[0];
 
   int holes = 0, movers = 0;
@@ -574,7 +599,7 @@ __global__ void __cluster_dims__(kPlanBlocks, 1, 1) __launch_bounds__(kPlanThrea
     sh.said[0] = holes;
     sh.said[1] = movers;
   }
-  exchange(cl, sh, 2);
+  exchange<N>(cl, sh, 2);
   const int moves = sh.all[1];           // as many holes as movers
   int h0 = sh.before[0], m0 = sh.before[1];
   for (int p = p0; p < p1; p += kPlanThreads) {
@@ -599,8 +624,8 @@ __global__ void __cluster_dims__(kPlanBlocks, 1, 1) __launch_bounds__(kPlanThrea
     W.info[1] = n_live;
     *n_live_out = n_live;
   }
-  cl.sync();
-  for (int k = rank * kPlanThreads + threadIdx.x; k < moves; k += kPlanBlocks * kPlanThreads) {
+  plan_sync<N>(cl);
+  for (int k = rank * kPlanThreads + threadIdx.x; k < moves; k += N * kPlanThreads) {
     const int src = W.mover[k], dst = W.list[k];
     W.to[src] = dst;
     A.ref_out[dst] = A.ref[src];
@@ -690,6 +715,12 @@ bool outputs_apart(const fm_cache& c, const PageArgs& A) {
   return true;
 }
 
+// Few enough pages (four a thread) and rows (two a warp) that the page
+// bookkeeping is faster by one block: a fork and a reserve of 8 rows took 9.0
+// us so and 12.6 by clusters, of 64 rows 12.5 and 13.2, of 128 rows 17.6 and
+// 14.6; a compaction of 250 pages 6.3 and 8.6.
+bool few_pages(const fm_cache& c) { return c.n_pages <= 4096 && c.B <= 64; }
+
 int copy_grid() { return num_sms() * 8; }
 
 }  // namespace
@@ -767,6 +798,11 @@ fm_status fm_pages_fork(const fm_cache* c, const int32_t* parent, const int32_t*
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   prof_begin(K_PAGES_FORK, s);
   cudaError_t e = cudaSuccess;
+  if (ref_out != ref && few_pages(*c)) {
+    e = launch_dependent(fork_copy_kernel, dim3(1), 1024, 0, s, A, parent);
+    prof_end(K_PAGES_FORK, s);
+    return done(e);
+  }
   if (ref_out != ref) {
     const int blocks = ceil_div(c->n_pages, 1024);
     e = launch_dependent(ref_copy_kernel, dim3(blocks < 1024 ? blocks : 1024), 256, 0, s, ref, ref_out,
@@ -799,7 +835,9 @@ fm_status fm_pages_reserve(const fm_cache* c, const int32_t* grow, void* k_pool,
   if (ws_bytes < W.bytes) return FM_ERR_WORKSPACE;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   prof_begin(K_PAGES_PLAN, s);
-  cudaError_t e = launch_dependent(reserve_kernel, dim3(kPlanBlocks), kPlanThreads, 0, s, A, grow, W, info);
+  cudaError_t e = few_pages(*c)
+                      ? launch_dependent(reserve_kernel<1>, dim3(1), kPlanThreads, 0, s, A, grow, W, info)
+                      : launch_dependent(reserve_kernel<8>, dim3(8), kPlanThreads, 0, s, A, grow, W, info);
   prof_end(K_PAGES_PLAN, s);
   if (e != cudaSuccess) return FM_ERR_CUDA;
   const int64_t items = static_cast<int64_t>(c->B) * c->layers * 2;
@@ -827,7 +865,9 @@ fm_status fm_pages_compact(const fm_cache* c, void* k_pool, void* v_pool, const 
   if (ws_bytes < W.bytes) return FM_ERR_WORKSPACE;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   prof_begin(K_PAGES_PLAN, s);
-  cudaError_t e = launch_dependent(compact_kernel, dim3(kPlanBlocks), kPlanThreads, 0, s, A, W, n_live);
+  cudaError_t e = few_pages(*c)
+                      ? launch_dependent(compact_kernel<1>, dim3(1), kPlanThreads, 0, s, A, W, n_live)
+                      : launch_dependent(compact_kernel<8>, dim3(8), kPlanThreads, 0, s, A, W, n_live);
   prof_end(K_PAGES_PLAN, s);
   if (e != cudaSuccess) return FM_ERR_CUDA;
   prof_begin(K_PAGES_COPY, s);

@@ -234,6 +234,20 @@ def test_many_pages_and_rows():
     assert all(flat[b, :len(r)].tolist() == r for b, r in enumerate(rows2))
 
 
+@pytest.mark.parametrize("B,n_pages", [(1, 4), (40, 4096), (64, 700), (65, 700), (300, 9000)])
+def test_fork_with_counts_of_its_own(B, n_pages):
+    p = Pool(12, B, n_pages, L=1, Hkv=1, max_pages=4)
+    p.reserve([int(x) for x in p.rng.integers(0, 50, B)])
+    before = p.ref_t.clone()
+    parent = [int(x) for x in p.rng.integers(-1, B, B)]
+    want = oc.fork(parent, p.rows, p.lens, p.ref)
+    out = torch.full_like(p.ref_t, -9)
+    t, ln, rf = fm.pages_fork(ints(parent), 16, p.table, p.lens_t, p.ref_t, ref_out=out)
+    assert rf.data_ptr() == out.data_ptr() and out.tolist() == want[2]
+    assert ln.tolist() == want[1] and torch.equal(p.ref_t, before)
+    assert all(t[b, :len(r)].tolist() == r for b, r in enumerate(want[0]))
+
+
 def test_fork_reports_bad_rows():
     p = Pool(9, 3, 20)
     p.reserve([20, 20, 20])
