@@ -26,10 +26,11 @@ inline EncodeTiledFn encode_fn() {
 }
 
 // 4-D view (head_dim, head, seq, batch) of a BSHD tensor; one box is
-// `box_rows` sequence rows x 64 head-dim elements of one (batch, head), laid
-// out in shared memory with the 128-byte swizzle.  Rows past the end read 0.
+// `box_rows` sequence rows x `box_heads` heads (a row's heads next to each
+// other) x 64 head-dim elements of one batch entry, laid out in shared memory
+// with the 128-byte swizzle.  Rows past the end read 0.
 inline bool make_tmap_bshd(CUtensorMap* m, const void* base, int B, int S, int H, int D,
-                           const int64_t* stride, int box_rows) {
+                           const int64_t* stride, int box_rows, int box_heads = 1) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
   cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(H),
@@ -37,7 +38,7 @@ inline bool make_tmap_bshd(CUtensorMap* m, const void* base, int B, int S, int H
   cuuint64_t strides[3] = {static_cast<cuuint64_t>(stride[2]) * 2,
                            static_cast<cuuint64_t>(stride[1]) * 2,
                            static_cast<cuuint64_t>(stride[0]) * 2};
-  cuuint32_t box[4] = {64, 1, static_cast<cuuint32_t>(box_rows), 1};
+  cuuint32_t box[4] = {64, static_cast<cuuint32_t>(box_heads), static_cast<cuuint32_t>(box_rows), 1};
   cuuint32_t es[4] = {1, 1, 1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box,
             es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,

@@ -823,6 +823,13 @@ fm_status fm_tree_fwd(const fm_cache* c, const fm_tree_desc* t, const void* q, c
   if (!make_tmap_bshd(&tk, k_pool, c->n_pages, c->page_size, c->Hkv, c->d, c->k_stride + 1, box) ||
       !make_tmap_bshd(&tv, v_pool, c->n_pages, c->page_size, c->Hkv, c->d, c->v_stride + 1, box))
     return FM_ERR_CUDA;
+  // Q of 128 rows of a unit: the G heads of 128 / G nodes
+  CUtensorMap tq = tk;
+  P.q_tma = W.kind == WIDE && 128 % P.G == 0;
+  if (P.q_tma) {
+    const int64_t st[3] = {8, t->q_stride[0], t->q_stride[1]};
+    if (!make_tmap_bshd(&tq, q, 1, t->total, t->H, c->d, st, 128 / P.G, P.G)) return FM_ERR_CUDA;
+  }
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool d64 = c->d == 64;
   if (W.kind == NARROW) {
@@ -831,11 +838,11 @@ fm_status fm_tree_fwd(const fm_cache* c, const fm_tree_desc* t, const void* q, c
     return d64 ? launch_join<NarrowGeo::R, 64>(P, grid, s) : launch_join<NarrowGeo::R, 128>(P, grid, s);
   }
   if (W.kind == MID) {
-    st = launch_tree_mid(P, c->d, tk, tv, grid, s);
+    st = launch_tree_mid(P, c->d, tq, tk, tv, grid, s);
     if (st != FM_OK) return st;
     return d64 ? launch_join<MidGeo::R, 64>(P, grid, s) : launch_join<MidGeo::R, 128>(P, grid, s);
   }
-  st = launch_tree_wide(P, tk, tv, grid, s);
+  st = launch_tree_wide(P, tq, tk, tv, grid, s);
   return st != FM_OK ? st : launch_join<WideGeo::R, 128>(P, grid, s);
 }
 

@@ -23,6 +23,7 @@ struct TreeParams {
   int B, H, Hkv, G, total, max_nodes, page_shift, n_pages, max_pages;
   int box_shift;           // log2 of the rows of a TMA box, min(page_size, tile)
   int tree;                // 0: chain (no parents)
+  int q_tma;               // the wide kernel loads Q by TMA: G divides 128
   int whole;               // units are not cut: no parts, no join
   FastDiv by_G, by_grid;
   float scale_log2;        // scale * log2(e)
@@ -440,9 +441,9 @@ static __device__ __noinline__ void fix_row(const TreeParams& P, int b, int hk, 
 
 // The kernels for units of up to 128 and 256 rows (fm_tree_wide.cu); the one
 // for up to 16 rows and the join of their parts are in fm_tree.cu.
-fm_status launch_tree_mid(const TreeParams& P, int d, const CUtensorMap& tk, const CUtensorMap& tv,
-                          int grid, cudaStream_t s);
-fm_status launch_tree_wide(const TreeParams& P, const CUtensorMap& tk, const CUtensorMap& tv, int grid,
-                           cudaStream_t s);   // d = 128
+fm_status launch_tree_mid(const TreeParams& P, int d, const CUtensorMap& tq, const CUtensorMap& tk,
+                          const CUtensorMap& tv, int grid, cudaStream_t s);
+fm_status launch_tree_wide(const TreeParams& P, const CUtensorMap& tq, const CUtensorMap& tk,
+                           const CUtensorMap& tv, int grid, cudaStream_t s);   // d = 128
 
 }  // namespace fm

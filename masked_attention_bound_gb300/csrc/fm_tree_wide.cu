@@ -49,7 +49,7 @@ struct WideCfg {
   static constexpr int OFF_ML = OFF_V + VSTAGES * TILE; // SLOTS 2: float2 [slot][128]
   static constexpr int OFF_NF = OFF_ML + (SLOTS == 2 ? 2 * 128 * 8 : 0);   // [2][8] keys with values not finite
   static constexpr int OFF_BAR = OFF_NF + 64;
-  static constexpr int NBAR = 33;
+  static constexpr int NBAR = 34;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;   // abort flag, TMEM address
   static constexpr int OFF_PAR = OFF_MISC + 16;         // int16 [256] parents of the unit's nodes
   static constexpr int USED = OFF_PAR + 512;
@@ -68,7 +68,7 @@ struct WideCfg {
 
 enum {
   W_QFULL = 0, W_SFULL = 2, W_PFULL = 4, W_PVDONE = 6, W_OEMPTY = 8, W_KFULL = 10, W_KEMPTY = 15,
-  W_VFULL = 20, W_VEMPTY = 25, W_DRAIN = 30, W_TURN = 31,
+  W_VFULL = 20, W_VEMPTY = 25, W_DRAIN = 30, W_TURN = 31, W_QEMPTY = 33,
   W_PVTILE = W_PVDONE + 1   // SLOTS 1: the PV of each tile (the SFULL and PFULL are its two buffers')
 };
 
@@ -102,8 +102,8 @@ __device__ __forceinline__ void slots_sync() {
 
 template <int D, int SLOTS>
 __global__ void __launch_bounds__(WideCfg<D, SLOTS>::THREADS, WideCfg<D, SLOTS>::BLOCKS)
-    tree_wide_kernel(const __grid_constant__ TreeParams P, const __grid_constant__ CUtensorMap tmK,
-                     const __grid_constant__ CUtensorMap tmV) {
+    tree_wide_kernel(const __grid_constant__ TreeParams P, const __grid_constant__ CUtensorMap tmQ,
+                     const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV) {
   using C = WideCfg<D, SLOTS>;
   using Load = TileLoad<D, C::KT>;
   constexpr int KT = C::KT;
@@ -120,10 +120,16 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS>::THREADS, WideCfg<D, SLOTS>:
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   constexpr int K_WARP = C::SM_WARPS, MMA_WARP = K_WARP + 1, V_WARP = K_WARP + 2, MMA_WARP_B = K_WARP + 3;
 
+  // Q by TMA as soon as the piece before has left its tiles, while the softmax
+  // warps find out what their rows see: 512 units of 544 keys took 76 us so
+  // and 82 us with these warps' copies.  (With two blocks per SM the other
+  // block has the time: 50 us by their copies, 53 by TMA.)
+  const bool q_tma = SLOTS == 2 && P.q_tma;
+
   if (warp == 2) touch_memory<D>(P, lane);
   if (tid == 0) {
     for (int s = 0; s < 2; ++s) {
-      mbar_init(bar(W_QFULL + s), 4);     // one arrival per softmax warp of the slot
+      mbar_init(bar(W_QFULL + s), q_tma ? 1 : 4);   // else one arrival per softmax warp of the slot
       mbar_init(bar(W_SFULL + s), 1);
       mbar_init(bar(W_PFULL + s), 4);
       mbar_init(bar(W_PVDONE + s), 1);
@@ -141,6 +147,7 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS>::THREADS, WideCfg<D, SLOTS>:
       mbar_init(bar(W_VEMPTY + i), SLOTS);
     }
     mbar_init(bar(W_DRAIN), SLOTS);
+    mbar_init(bar(W_QEMPTY), C::SM_WARPS);
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -151,6 +158,7 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS>::THREADS, WideCfg<D, SLOTS>:
   }
   if (warp == K_WARP && lane == 0) tma_prefetch_desc(&tmK);
   if (warp == V_WARP && lane == 0) tma_prefetch_desc(&tmV);
+  if (q_tma && warp == MMA_WARP && lane == 0) tma_prefetch_desc(&tmQ);
   grid_launch_dependents();
   grid_dependency_wait();
   tc_fence_before();
@@ -247,6 +255,20 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS>::THREADS, WideCfg<D, SLOTS>:
         advance(ks, kp, x0, C::KSTAGES);
         advance(vs, vp, x0, C::VSTAGES);
         if (w.active(s)) {
+          if (q_tma) {
+            // the rows of the piece before have left through the Q tiles
+            if (pieces > 0) ok = wait_all(W_QEMPTY, (pieces - 1) & 1);
+            if (!ok) break;
+            if (elect_one()) {
+              const int node0 = u.s.row0 + P.by_G(u.row_first + (w.rows ? 128 * s : 0));
+              mbar_arrive_expect_tx(bar(W_QFULL + s), C::QTILE);
+#pragma unroll
+              for (int c = 0; c < D / 64; ++c)
+                tma_load_4d(sbase + C::OFF_Q + s * C::QTILE + c * (128 * 128), &tmQ, bar(W_QFULL + s), c * 64,
+                            u.hk * P.G, node0, 0);
+            }
+            __syncwarp();
+          }
           ok = wait_all(W_QFULL + s, qn & 1);
           ++qn;
         }
@@ -371,6 +393,7 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS>::THREADS, WideCfg<D, SLOTS>:
         ++pieces;
       }
       if (elect_one()) {
+        if (q_tma && qn > 0) mbar_wait(bar(W_QFULL + s), (qn - 1) & 1, P.status, P.wait_ns);   // the last Q has landed
         mma_commit(bar(W_DRAIN));
         mbar_wait(bar(W_DRAIN), 0, P.status, P.wait_ns);
       }
@@ -412,15 +435,6 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS>::THREADS, WideCfg<D, SLOTS>:
         continue;
       }
       const bool active = w.active(slot);
-      if (lane == 0 && mine && u.whole()) {   // where the rows will go (see touch_memory)
-        touch(out_row());
-        touch(out_lse());
-      }
-      // the next unit's Q, if it is this sequence's next head: to L2
-      if (mine && u.next_tile < 0 && u.left > 0 && u.hk + 1 < P.Hkv)
-#pragma unroll
-        for (int c = 0; c < D / 64; ++c)
-          touch(P.q + (u.s.row0 + node) * P.q_stride[0] + (h + P.G) * P.q_stride[1] + c * 64);
       uint32_t* nf = nf_all + 8 * (pieces & 1);
       if (tid < 8) nf_all[8 * ((pieces + 1) & 1) + tid] = 0;   // the next piece's, read by nobody now
       const int part0 = u.origin / KT;                 // tiles from here on are not seen by all
@@ -455,25 +469,28 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS>::THREADS, WideCfg<D, SLOTS>:
       const bool warp_live = __any_sync(0xffffffffu, live);
       float m_used = -INFINITY, l = 0.f;
       if (active) {
-        // Q (S of the slots' earlier pieces has been read): a row is
-        // copied by D / 8 lanes, so that a warp's copy covers whole rows, and
-        // asynchronously past L1: the few KB that shared memory leaves of it
-        // hold up plain loads of 64 KB for 7000 cycles
-        const __nv_bfloat16* src =
-            P.q + (u.s.row0 + node) * P.q_stride[0] + static_cast<int64_t>(h) * P.q_stride[1];
-        constexpr int LPR = D / 8, RPI = 32 / LPR;     // lanes a row, rows an instruction
-        const unsigned in_rows = __ballot_sync(0xffffffffu, mine);
+        // Q, where the MMA warps do not fetch it (S of the slots' earlier
+        // pieces has been read): a row is copied by D / 8 lanes, so that a
+        // warp's copy covers whole rows, and asynchronously past L1: the few
+        // KB that shared memory leaves of it hold up plain loads of 64 KB for
+        // 7000 cycles
+        if (!q_tma) {
+          const __nv_bfloat16* src =
+              P.q + (u.s.row0 + node) * P.q_stride[0] + static_cast<int64_t>(h) * P.q_stride[1];
+          constexpr int LPR = D / 8, RPI = 32 / LPR;     // lanes a row, rows an instruction
+          const unsigned in_rows = __ballot_sync(0xffffffffu, mine);
 #pragma unroll 2
-        for (int i = 0; i < 32 / RPI; ++i) {
-          const int from = i * RPI + lane / LPR;
-          const uint64_t row = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(src), from);
-          copy_async16(sbase + C::OFF_Q + slot * C::QTILE +
-                           sw128_offset(quarter * 32 + from, (lane % LPR) * 8, 128),
-                       row + (lane % LPR) * 16, (in_rows >> from) & 1u ? 16 : 0);
+          for (int i = 0; i < 32 / RPI; ++i) {
+            const int from = i * RPI + lane / LPR;
+            const uint64_t row = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(src), from);
+            copy_async16(sbase + C::OFF_Q + slot * C::QTILE +
+                             sw128_offset(quarter * 32 + from, (lane % LPR) * 8, 128),
+                         row + (lane % LPR) * 16, (in_rows >> from) & 1u ? 16 : 0);
+          }
+          copy_async_wait();
+          fence_proxy_async_smem();
+          mbar_arrive_warp(bar(W_QFULL + slot));
         }
-        copy_async_wait();
-        fence_proxy_async_smem();
-        mbar_arrive_warp(bar(W_QFULL + slot));
         int done = 0;
 #pragma unroll 1
         for (int x0 = w.rows ? 0 : slot; x0 < w.n; x0 += w.rows ? 1 : 2) {
@@ -717,6 +734,10 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS>::THREADS, WideCfg<D, SLOTS>:
         }
         __syncwarp();
       }
+      if (q_tma) {
+        fence_proxy_async_smem();
+        mbar_arrive_warp(bar(W_QEMPTY));
+      }
       tc_fence_before();
       if (w.rows) {
         // for each of this slot's warps, and those of the other
@@ -763,8 +784,8 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS>::THREADS, WideCfg<D, SLOTS>:
 }
 
 template <int D, int SLOTS>
-static fm_status launch_wide_d(const TreeParams& P, const CUtensorMap& tk, const CUtensorMap& tv,
-                               int grid, cudaStream_t s) {
+static fm_status launch_wide_d(const TreeParams& P, const CUtensorMap& tq, const CUtensorMap& tk,
+                               const CUtensorMap& tv, int grid, cudaStream_t s) {
   using C = WideCfg<D, SLOTS>;
   auto kern = tree_wide_kernel<D, SLOTS>;
   // the setmaxnreg split must fit in the registers the block launches with
@@ -772,19 +793,19 @@ static fm_status launch_wide_d(const TreeParams& P, const CUtensorMap& tk, const
   const fm_status st = prepare_kernel(kern, C::SMEM, C::MIN_LAUNCH_REGS, ready);
   if (st != FM_OK) return st;
   prof_begin(K_TREE, s);
-  const cudaError_t e = launch_dependent(kern, dim3(grid), C::THREADS, C::SMEM, s, P, tk, tv);
+  const cudaError_t e = launch_dependent(kern, dim3(grid), C::THREADS, C::SMEM, s, P, tq, tk, tv);
   prof_end(K_TREE, s);
   return e == cudaSuccess ? FM_OK : FM_ERR_CUDA;
 }
 
-fm_status launch_tree_mid(const TreeParams& P, int d, const CUtensorMap& tk, const CUtensorMap& tv,
-                          int grid, cudaStream_t s) {
-  return d == 64 ? launch_wide_d<64, 1>(P, tk, tv, grid, s) : launch_wide_d<128, 1>(P, tk, tv, grid, s);
+fm_status launch_tree_mid(const TreeParams& P, int d, const CUtensorMap& tq, const CUtensorMap& tk,
+                          const CUtensorMap& tv, int grid, cudaStream_t s) {
+  return d == 64 ? launch_wide_d<64, 1>(P, tq, tk, tv, grid, s) : launch_wide_d<128, 1>(P, tq, tk, tv, grid, s);
 }
 
-fm_status launch_tree_wide(const TreeParams& P, const CUtensorMap& tk, const CUtensorMap& tv, int grid,
-                           cudaStream_t s) {
-  return launch_wide_d<128, 2>(P, tk, tv, grid, s);
+fm_status launch_tree_wide(const TreeParams& P, const CUtensorMap& tq, const CUtensorMap& tk,
+                           const CUtensorMap& tv, int grid, cudaStream_t s) {
+  return launch_wide_d<128, 2>(P, tq, tk, tv, grid, s);
 }
 
 }  // namespace fm
