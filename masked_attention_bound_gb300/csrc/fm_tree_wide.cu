@@ -20,9 +20,10 @@
 //    turn; their O, maximum and sum are merged at the end of the piece.
 //
 // Warps: 4 per slot for the softmax, then one that loads K, slot 0's MMAs, one
-// that loads V, slot 1's MMAs.  The softmax warps also put Q into shared
-// memory (rows of a unit are nodes times query heads: any group size) and
-// clean the V tiles that hold drafted nodes.
+// that loads V, slot 1's MMAs.  Rows of a unit are nodes times query heads: Q
+// comes by TMA (SLOTS = 2, a group size that divides 128) or by the softmax
+// warps' copies.  The softmax warps also clean the V tiles that hold drafted
+// nodes.
 // TMEM: S/P of slot s at column 128 s (SLOTS = 1: of every second tile at
 // column 64), the O's after the S's.
 #include <type_traits>
