@@ -15,6 +15,8 @@ A step of a model that drafts trees:
     o, lse = tree_forward(q, k[layer], v[layer], table, lens, cu, scale, parents=parents)
     lens = cache_accept(accept, n_accept, cu, k, v, table, lens, ref=ref)  # after verification
 
+These are operators of inference: no gradient flows through them.
+
 Calls are enqueued on ``stream`` (default: the current stream of the tensors'
 device), allocate there what the caller leaves out, and do not synchronise.
 Arguments that the host can check raise ValueError or FMError; what the
