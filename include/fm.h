@@ -305,7 +305,8 @@ fm_status fm_varlen_bounds(const int32_t* cu_seqlens, int n_seqs, int total, int
  *   ref [n_pages]         rows that hold the page; 0: the page is free
  *   cu [B + 1]            rows of a packed batch of new tokens: cu[0] = 0,
  *                         sequence b's are [cu[b], cu[b+1]), cu[B] <= total;
- *                         packed rows past cu[B] are neither read nor written
+ *                         packed rows past cu[B] have no part in a result and are
+ *                         not written
  * Rows of more than 2^30 tokens, B * max_pages above 2^31 - 1 and more than
  * 65535 K/V heads are not supported.
  *

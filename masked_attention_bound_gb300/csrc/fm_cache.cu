@@ -87,8 +87,10 @@ __device__ __forceinline__ int context_of(const int32_t* lens, const int32_t* cu
 
 // ------------------------------------------------------------------ append
 // Each block takes a few consecutive packed tokens.  All threads first load
-// its 16-byte vectors, K and V, which needs no lookup; meanwhile one thread
-// per token finds its sequence (binary search over cu), page and slot.
+// its 16-byte vectors, K and V, which needs no lookup; meanwhile a warp (or, of
+// more than eight tokens a block, a thread) per token finds its sequence (a
+// search over cu), page and slot.  128 single tokens took 3.2 us by threads and
+// 2.6 by warps, 20000 tokens of 512 bytes 4.2 by threads and 6.9 by warps.
 constexpr int kAppendThreads = 256, kAppendVecs = 4;
 
 struct AppendArgs {
@@ -129,31 +131,45 @@ __global__ void __launch_bounds__(kAppendThreads)
     }
   };
   load(threadIdx.x);
-  for (int i = threadIdx.x; i < A.tokens; i += blockDim.x) {
-    const int t = t0 + i;
-    int64_t to = -1;
-    if (t < A.total && t < A.cu[A.B]) {
-      int lo = 0, hi = A.B;            // the last b with cu[b] <= t
+  // token t of sequence b, the last one with cu[b] <= t: page << 8 | slot
+  auto place = [&](int t, int b) -> int64_t {
+    int n;
+    const int base = context_of(A.lens, A.cu, b, A.total, A.max_pages << P.page_shift, n);
+    const int node = t - A.cu[b], pos = base + node;
+    if (base >= 0 && node >= 0 && node < n) {
+      const int pg = A.table[static_cast<int64_t>(b) * A.max_pages + (pos >> P.page_shift)];
+      if (pg >= 0 && pg < A.n_pages) return (static_cast<int64_t>(pg) << 8) | (pos & (P.page_size() - 1));
+    }
+    flag(A.status, DEV_CACHE);
+    return -1;
+  };
+  const int behind = A.cu[A.B];          // tokens from here on belong to no sequence
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (A.tokens <= kAppendThreads / 32) {
+    // a warp per token: 32 of the offsets a step
+    const int t = t0 + warp;
+    if (warp < A.tokens && t < A.total) {
+      int lo = 0;
+      for (int n = A.B; n > 1;) {
+        const int step = (n + 31) >> 5;
+        const unsigned below = __ballot_sync(0xffffffffu, lane * step < n && A.cu[lo + lane * step] <= t);
+        const int k = 31 - __clz(below | 1u);
+        lo += k * step;
+        n = min(step, n - k * step);
+      }
+      const int64_t to = t < behind ? place(t, lo) : -1;
+      if (lane == 0) where[warp] = to;
+    }
+  } else {
+    for (int i = threadIdx.x; i < A.tokens; i += kAppendThreads) {
+      const int t = t0 + i;
+      int lo = 0, hi = A.B;
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (A.cu[mid] <= t) lo = mid; else hi = mid;
       }
-      int n;
-      const int base = context_of(A.lens, A.cu, lo, A.total, A.max_pages << P.page_shift, n);
-      const int node = t - A.cu[lo];
-      bool ok = base >= 0 && node >= 0 && node < n;
-      if (ok) {
-        const int pos = base + node;
-        const int pg = A.table[static_cast<int64_t>(lo) * A.max_pages + (pos >> P.page_shift)];
-        ok = pg >= 0 && pg < A.n_pages;
-        to = (static_cast<int64_t>(pg) << 8) | (pos & (P.page_size() - 1));
-      }
-      if (!ok) {
-        to = -1;
-        flag(A.status, DEV_CACHE);
-      }
+      where[i] = t < A.total && t < behind ? place(t, lo) : -1;
     }
-    where[i] = to;
   }
   __syncthreads();
   for (int v0 = threadIdx.x; v0 < all; v0 += kAppendVecs * kAppendThreads) {

@@ -43,6 +43,21 @@ def test_append(page, Hkv, d, nodes):
     assert np.array_equal(_bits(b.k), want[0]) and np.array_equal(_bits(b.v), want[1])
 
 
+@pytest.mark.parametrize("B", [31, 33, 1025, 2500])
+@pytest.mark.parametrize("Hkv,d", [(1, 64), (8, 128)])
+def test_append_to_many_sequences(B, Hkv, d):
+    """The search for a token's sequence: none, one or some new tokens each, in runs."""
+    nodes = [(0, 1, 0, 0, 3, 1, 1)[(i * i) % 7] for i in range(B)]
+    lens = [n + i % 20 for i, n in enumerate(nodes)]
+    b = Batch(13, lens, nodes, Hkv, Hkv, d, 16)
+    k, v = _pools(14, sum(nodes), Hkv, d)
+    want = [oc.append(_bits(x), b.cu_np, _bits(p), b.table_np, lens) for x, p in ((k, b.k), (v, b.v))]
+    st = _status()
+    fm.cache_append(k, v, b.cu, b.k, b.v, b.table, b.lens_t, status=st)
+    assert fm.device_status(st) == 0
+    assert np.array_equal(_bits(b.k), want[0]) and np.array_equal(_bits(b.v), want[1])
+
+
 def test_append_skips_what_is_out_of_range():
     b = Batch(3, [20, 20, 20], [2, 2, 2], 2, 2, 64, 16)
     k, v = _pools(4, 6, 2, 64)
