@@ -193,8 +193,11 @@ __global__ void __launch_bounds__(kAppendThreads)
 // vector of a token (of K or V) and walks the nodes in ascending order.  The
 // node moved i-th comes from a place at or past base + i and goes to base +
 // i, so a thread that loads node i before it stores node i never overwrites
-// a source that it still needs; threads share no bytes.
-constexpr int kAcceptThreads = 256;
+// a source that it still needs; threads share no bytes.  Bound by the latency
+// of the lookups, so what counts is how many blocks an SM holds: 64 trees of 8
+// accepted nodes in 16 layers took 5.7 us with 4 nodes in flight a thread and
+// 40 registers, 7.8 us with 8 and 72.
+constexpr int kAcceptThreads = 128;
 
 struct AcceptArgs {
   const int32_t *accept, *n_accept, *cu, *table, *lens;
@@ -203,7 +206,7 @@ struct AcceptArgs {
   int max_accept, max_pages, n_pages;
 };
 
-__global__ void __launch_bounds__(kAcceptThreads)
+__global__ void __launch_bounds__(kAcceptThreads, 12)
     accept_kernel(const __grid_constant__ AcceptArgs A, const __grid_constant__ Pools P) {
   __shared__ int2 place[32];           // from, to: page << 8 | slot
   __shared__ int good;
@@ -260,7 +263,7 @@ __global__ void __launch_bounds__(kAcceptThreads)
   const int v = blockIdx.x * kAcceptThreads + threadIdx.x;
   const int kv = v >= P.row;
   uint4* pool = P.p[kv] + layer * P.layer[kv] + P.in_token(kv, v - kv * P.row);
-  constexpr int U = 8;
+  constexpr int U = 4;
   for (int i0 = 0; i0 < m; i0 += 32) {
     if (i0 > 0) {                      // the next 32 places
       __syncthreads();
@@ -651,16 +654,19 @@ __global__ void __cluster_dims__(N, 1, 1) __launch_bounds__(kPlanThreads, 1)
 
 // ------------------------------------------------------------------ page copies
 // n tokens of one page of one layer, K or V, from page src to page dst, by
-// one block: vectors of 16 bytes, eight in flight per thread, neither side
-// kept in L1.
-constexpr int kCopyThreads = 256;
+// one block: vectors of 16 bytes, four in flight per thread, neither side
+// kept in L1.  Small pages (4 KB of K or V at 16 tokens of 2 heads of 64) are
+// bound by the latency of finding them, large ones by HBM: 256 sequences of
+// 8000 tokens, half of the pages free, took 335 us by blocks of 128 threads and
+// 622 by blocks of 256 with eight in flight, and 64 KB pages 254 and 255.
+constexpr int kCopyThreads = 128;
 
 __device__ __forceinline__ void copy_page(const Pools& P, int kv, int layer, int src, int dst, int n) {
   const uint4* from = P.p[kv] + layer * P.layer[kv] + src * P.page[kv];
   uint4* to = P.p[kv] + layer * P.layer[kv] + dst * P.page[kv];
   const int all = n * P.row;
   const bool linear = P.linear[kv];
-  constexpr int U = 8;
+  constexpr int U = 4;
   for (int v0 = threadIdx.x; v0 < all; v0 += U * kCopyThreads) {
     uint4 x[U];
     int64_t at[U];
@@ -737,7 +743,7 @@ bool outputs_apart(const fm_cache& c, const PageArgs& A) {
 // 14.6; a compaction of 250 pages 6.3 and 8.6.
 bool few_pages(const fm_cache& c) { return c.n_pages <= 4096 && c.B <= 64; }
 
-int copy_grid() { return num_sms() * 8; }
+int copy_grid() { return num_sms() * 16; }
 
 }  // namespace
 }  // namespace fm
