@@ -429,18 +429,29 @@ __device__ __forceinline__ int block_scan(int x, int* warp_sums, int& total) {
   return before + inc - x;
 }
 
-__device__ __forceinline__ int block_sum(int x, int* warp_sums) {
-  int total;
-  block_scan(x, warp_sums, total);
-  return total;
-}
-
 // What the blocks of a plan tell each other.
 struct PlanShared {
   int warp_sums[32];
   int said[4];       // this block's numbers, read by the others
   int before[4], all[4];
+  int parts[3][32];  // see block_sums
 };
+
+// Sums of n values per thread over the block (kPlanThreads), into sh.said.
+template <int n>
+__device__ __forceinline__ void block_sums(const int (&x)[n], PlanShared& sh) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int i = 0; i < n; ++i) {
+    const int s = __reduce_add_sync(0xffffffffu, x[i]);
+    if (lane == 0) sh.parts[i][warp] = s;
+  }
+  __syncthreads();
+  if (warp < n) {
+    const int s = __reduce_add_sync(0xffffffffu, sh.parts[warp][lane]);
+    if (lane == 0) sh.said[warp] = s;
+  }
+}
 
 // Exchange: sums over the blocks before this one, and over all, of `said`.
 template <int N>
@@ -505,14 +516,7 @@ __global__ void __cluster_dims__(N, 1, 1) __launch_bounds__(kPlanThreads, 1)
     free_pages += r == 0;
     bad |= r < 0;
   }
-  asked = block_sum(asked, sh.warp_sums);
-  free_pages = block_sum(free_pages, sh.warp_sums);
-  bad = block_sum(bad, sh.warp_sums);
-  if (threadIdx.x == 0) {
-    sh.said[0] = asked;
-    sh.said[1] = free_pages;
-    sh.said[2] = bad;
-  }
+  block_sums<3>({asked, free_pages, bad}, sh);
   exchange<N>(cl, sh, 3);
   const int total = sh.all[0], n_free = sh.all[1];
   const bool refused = sh.all[2] != 0;
@@ -579,8 +583,7 @@ __global__ void __cluster_dims__(N, 1, 1) __launch_bounds__(kPlanThreads, 1)
       for (int j = lane; j < (r.x & ~kReplace) + swap; j += 32) out[r.y - swap + j] = W.list[r.z + j];
     }
   }
-  released = block_sum(released, sh.warp_sums);
-  if (threadIdx.x == 0) sh.said[0] = released;
+  block_sums<1>({released}, sh);
   exchange<N>(cl, sh, 1);
   if (rank == 0 && threadIdx.x == 0) info[0] = n_free - (go ? total : 0) + sh.all[0];
 }
@@ -600,8 +603,7 @@ __global__ void __cluster_dims__(N, 1, 1) __launch_bounds__(kPlanThreads, 1)
   int live = 0;
 #pragma unroll 4
   for (int p = p0 + threadIdx.x; p < p1; p += kPlanThreads) live += A.ref[p] != 0;
-  live = block_sum(live, sh.warp_sums);
-  if (threadIdx.x == 0) sh.said[0] = live;
+  block_sums<1>({live}, sh);
   exchange<N>(cl, sh, 1);
   const int n_live = sh.all[0];
 
@@ -612,12 +614,7 @@ __global__ void __cluster_dims__(N, 1, 1) __launch_bounds__(kPlanThreads, 1)
     holes += !held && p < n_live;
     movers += held && p >= n_live;
   }
-  holes = block_sum(holes, sh.warp_sums);
-  movers = block_sum(movers, sh.warp_sums);
-  if (threadIdx.x == 0) {
-    sh.said[0] = holes;
-    sh.said[1] = movers;
-  }
+  block_sums<2>({holes, movers}, sh);
   exchange<N>(cl, sh, 2);
   const int moves = sh.all[1];           // as many holes as movers
   int h0 = sh.before[0], m0 = sh.before[1];
