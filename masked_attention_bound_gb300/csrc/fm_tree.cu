@@ -792,11 +792,12 @@ fm_status fm_tree_fwd(const fm_cache* c, const fm_tree_desc* t, const void* q, c
   P.by_grid = FastDiv::of(grid);
   P.tree = parents != nullptr;
   // Units are not cut, and the join (3 us after the first kernel) is spared,
-  // where the rows of the table hold at most 512 tokens (eight tiles in turn
-  // cost a block 4 us), as long as there is a block for each unit: 1024 units
-  // of 480 keys took 48 us whole and 43 us cut and joined.
+  // where the rows of the table hold at most 320 tokens (512 units of 100 keys
+  // 14.7 us, cut 19.5; 4096 of 250 keys 116, cut 113), or at most 512 as long as
+  // no block has more than two units (512 units of 64 rows and 400 keys 31.3 us,
+  // cut 36.4; 1024 units of 480 keys 48, cut 43).
   const int64_t tokens = static_cast<int64_t>(c->max_pages) * c->page_size;
-  P.whole = tokens <= 320 || (tokens <= 512 && static_cast<int64_t>(c->B) * c->Hkv <= grid);
+  P.whole = tokens <= 320 || (tokens <= 512 && static_cast<int64_t>(c->B) * c->Hkv <= 2 * grid);
   P.scale_log2 = scale_log2;
   P.q = static_cast<const __nv_bfloat16*>(q);
   P.o = static_cast<__nv_bfloat16*>(o);
