@@ -30,11 +30,11 @@ struct NarrowCfg {
   static constexpr int KS = D == 128 ? 3 : 5, VS = D == 128 ? 2 : 5;   // rings of tiles
   static constexpr int PITCH = D + 8;              // floats of a row of the merge buffer
   static constexpr int OFF_V = KS * TILE;
-  static constexpr int OFF_MERGE = OFF_V + VS * TILE;
-  static constexpr int OFF_ML = OFF_MERGE + WARPS / 2 * R * PITCH * 4;   // [WARPS][R] max, then sum
-  static constexpr int OFF_SEEN = OFF_ML + 2 * WARPS * R * 4;    // [R][8] ancestors
-  static constexpr int OFF_NF = OFF_SEEN + R * 8 * 4;            // [8] keys with values not finite
-  static constexpr int OFF_BAR = OFF_NF + 32;
+  static constexpr int OFF_MERGE = OFF_V + VS * TILE;            // [WARPS][R / 2][PITCH]
+  static constexpr int OFF_ML = OFF_MERGE + WARPS * R / 2 * PITCH * 4;   // float2 [R][WARPS] max and sum
+  static constexpr int OFF_SEEN = OFF_ML + WARPS * R * 8;        // [R] see bits
+  static constexpr int OFF_NF = OFF_SEEN + R * 4;                // [2][8] keys with values not finite
+  static constexpr int OFF_BAR = OFF_NF + 64;
   static constexpr int OFF_ABORT = OFF_BAR + 2 * (KS + VS) * 8;
   static constexpr int SMEM = OFF_ABORT + 8;
   static_assert(2 * (SMEM + 1024) <= 228 * 1024, "two blocks per SM");
@@ -91,6 +91,7 @@ __global__ void __launch_bounds__(NarrowCfg<D>::THREADS, 2)
     abort_flag = 0;
     fence_barrier_init();
   }
+  if (tid < 16) reinterpret_cast<uint32_t*>(smem + C::OFF_NF)[tid] = 0;
   if (warp == C::WARPS && lane == 0) {
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
@@ -147,40 +148,17 @@ __global__ void __launch_bounds__(NarrowCfg<D>::THREADS, 2)
     uint32_t e = 0;                              // tiles so far
     const int g = lane >> 2, tq = lane & 3;      // fragment row and column pair
     uint32_t* seen = reinterpret_cast<uint32_t*>(smem + C::OFF_SEEN);
-    uint32_t* nf = reinterpret_cast<uint32_t*>(smem + C::OFF_NF);
+    uint32_t* nf_all = reinterpret_cast<uint32_t*>(smem + C::OFF_NF);
     float* merge = reinterpret_cast<float*>(smem + C::OFF_MERGE);
-    float* ml = reinterpret_cast<float*>(smem + C::OFF_ML);
+    float2* ml = reinterpret_cast<float2*>(smem + C::OFF_ML);
+    uint32_t pieces = 0;
     if (tid == 0) P.rec[blockIdx.x] = make_int4(-1, 0, 0, 0);
-    while (u.next(P)) {
+    for (; u.next(P); ++pieces) {
       // tiles from this one on hold keys that not every row sees
       const int part0 = u.origin / KT;
-      // which keys past origin a row sees: bit j is key origin + j
-      if (warp == 0) {
-        uint32_t w[8];
-        const int node = P.by_G(u.row_first + min(lane, u.rows - 1));
-        if (P.tree) {
-          // at most 16 rows: lane l knows the parent of node l
-          const int mine = lane < u.s.n && u.s.base >= 0 ? tree_parent(P, u.s, lane) : -1;
-          int a = u.s.base >= 0 ? node : -1;
-#pragma unroll
-          for (int x = 0; x < 8; ++x) w[x] = 0;
-          while (__any_sync(0xffffffffu, a >= 0)) {
-            const int p = __shfl_sync(0xffffffffu, mine, a & 31);
-            if (a >= 0 && p != -2) w[0] |= 1u << a;
-            a = a < 0 || p == -2 ? -1 : p;   // a node drafted after a padding node is a root
-          }
-        } else {
-          const int upto = u.s.base + node - u.origin;   // 0 .. R - 1
-#pragma unroll
-          for (int x = 0; x < 8; ++x)
-            w[x] = upto >= 32 * x + 31 ? 0xffffffffu
-                                       : (upto < 32 * x ? 0u : (2u << (upto - 32 * x)) - 1u);
-        }
-        if (lane < R && u.s.base >= 0)
-#pragma unroll
-          for (int x = 0; x < 8; ++x) seen[lane * 8 + x] = w[x];
-        if (lane < 8) nf[lane] = 0;
-      }
+      // the next piece's flags, read by nobody now
+      uint32_t* nf = nf_all + 8 * (pieces & 1);
+      if (tid == 0) nf_all[8 * ((pieces + 1) & 1)] = 0;
       // Q of rows g and g + 8 as A fragments, straight from memory
       uint32_t qf[D / 16][4];
 #pragma unroll
@@ -196,7 +174,26 @@ __global__ void __launch_bounds__(NarrowCfg<D>::THREADS, 2)
           qf[kk][hh + 2] = r < u.rows ? *reinterpret_cast<const uint32_t*>(src + kk * 16 + 8) : 0u;
         }
       }
-      named_sync(1, 32 * C::WARPS);     // seen, nf
+      // which keys from origin on row lane & 15 sees: bit i is key origin + i
+      // (16 rows are of 16 nodes at most)
+      uint32_t bits = 0;
+      {
+        const int node = P.by_G(u.row_first + min(lane & 15, u.rows - 1));
+        if (P.tree) {
+          // lane l knows the parent of node l
+          const int mine = lane < u.s.n && u.s.base >= 0 ? tree_parent(P, u.s, lane) : -1;
+          int a = u.s.base >= 0 ? node : -1;
+          while (__any_sync(0xffffffffu, a >= 0)) {
+            const int p = __shfl_sync(0xffffffffu, mine, a & 31);
+            if (a >= 0 && p != -2) bits |= 1u << a;
+            a = a < 0 || p == -2 ? -1 : p;   // a node drafted after a padding node is a root
+          }
+        } else {
+          bits = (2u << (u.s.base + node - u.origin)) - 1u;
+        }
+      }
+      if (tid < R) seen[tid] = bits;    // for values that are not finite
+      const uint32_t bits_of[2] = {__shfl_sync(0xffffffffu, bits, g), __shfl_sync(0xffffffffu, bits, g + 8)};
       float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
       float acc[D / 8][4];
 #pragma unroll
@@ -238,16 +235,20 @@ __global__ void __launch_bounds__(NarrowCfg<D>::THREADS, 2)
         uint32_t pf[4], pl[4];
         if (ok && mine) {
           if (t >= part0 || k0 + 16 > u.keys) {
-            // keys past origin: only what the row sees
+            // keys past origin: only what the row sees; bit i of vis is key k0 + i
+            const int j0 = k0 - u.origin;
 #pragma unroll
-            for (int x = 0; x < 2; ++x)
+            for (int hh = 0; hh < 2; ++hh) {
+              const uint32_t vis = j0 >= 16 ? 0u
+                                   : j0 >= 0 ? bits_of[hh] >> j0
+                                   : j0 > -16 ? bits_of[hh] << -j0 | ((1u << -j0) - 1u)
+                                              : 0xffffu;
 #pragma unroll
-              for (int y = 0; y < 4; ++y) {
-                const int key = k0 + x * 8 + 2 * tq + (y & 1), r = g + 8 * (y >> 1);
-                const int j = key - u.origin;
-                const bool vis = key < u.keys && (j < 0 || ((seen[r * 8 + (j >> 5)] >> (j & 31)) & 1u));
-                if (!vis) s[x][y] = -INFINITY;
-              }
+              for (int x = 0; x < 2; ++x)
+#pragma unroll
+                for (int y = 0; y < 2; ++y)
+                  if (!((vis >> (x * 8 + 2 * tq + y)) & 1u)) s[x][2 * hh + y] = -INFINITY;
+            }
           }
           bool grow = false;
           float alpha[2], ref[2];
@@ -302,27 +303,35 @@ __global__ void __launch_bounds__(NarrowCfg<D>::THREADS, 2)
             // where not every row sees the key
             const int row = warp * 16 + (lane >> 1);
             const int key = k0 + (lane >> 1), j = key - u.origin;
+            auto word = [&](int c) {
+              const int ch = (lane & 1) * (D / 16) + c;
+              return reinterpret_cast<uint4*>(smem + C::OFF_V + vs * C::TILE + (ch >> 3) * (KT * 128) +
+                                              row * 128 + (((ch & 7) ^ (row & 7)) << 4));
+            };
             bool dirty = false;
+            if (key >= u.keys) {
+#pragma unroll
+              for (int c = 0; c < D / 16; ++c) *word(c) = make_uint4(0u, 0u, 0u, 0u);
+            } else if (j >= 0) {
+              uint32_t zero = 0;               // 0, or NaN once a value was not finite
+#pragma unroll
+              for (int c = 0; c < D / 16; ++c) {
+                const uint4 x = *word(c);
+                zero = bf16x2_times_zero(x.x, zero);
+                zero = bf16x2_times_zero(x.y, zero);
+                zero = bf16x2_times_zero(x.z, zero);
+                zero = bf16x2_times_zero(x.w, zero);
+              }
+              dirty = bf16x2_not_finite(zero);
+            }
+            if (dirty) {
+              atomicOr(nf, 1u << j);
 #pragma unroll 1
-            for (int ch = (lane & 1) * (D / 16); ch < ((lane & 1) + 1) * (D / 16); ++ch) {
-              const uint32_t at = (ch >> 3) * (KT * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4);
-              uint4* ptr = reinterpret_cast<uint4*>(smem + C::OFF_V + vs * C::TILE + at);
-              if (key >= u.keys) {
-                *ptr = make_uint4(0u, 0u, 0u, 0u);
-              } else if (j >= 0) {
-                uint4 x = *ptr;
-                if (bf16x2_not_finite(x.x) || bf16x2_not_finite(x.y) || bf16x2_not_finite(x.z) ||
-                    bf16x2_not_finite(x.w)) {
-                  dirty = true;
-                  x.x = bf16x2_clean(x.x);
-                  x.y = bf16x2_clean(x.y);
-                  x.z = bf16x2_clean(x.z);
-                  x.w = bf16x2_clean(x.w);
-                  *ptr = x;
-                }
+              for (int c = 0; c < D / 16; ++c) {
+                uint4* x = word(c);
+                *x = make_uint4(bf16x2_clean(x->x), bf16x2_clean(x->y), bf16x2_clean(x->z), bf16x2_clean(x->w));
               }
             }
-            if (dirty) atomicOr(nf + (j >> 5), 1u << (j & 31));
             fence_proxy_async_smem();   // before the next copy into this slot
             __syncwarp();
           }
@@ -344,113 +353,67 @@ __global__ void __launch_bounds__(NarrowCfg<D>::THREADS, 2)
       }
 
       // ---------------------------------------------------------- merge the four warps
+      // Each warp's maxima, sums and O as they are to shared memory, eight rows
+      // at a time; then a thread adds four columns of a row.
 #pragma unroll
       for (int hh = 0; hh < 2; ++hh) {
         l[hh] += __shfl_xor_sync(0xffffffffu, l[hh], 1);
         l[hh] += __shfl_xor_sync(0xffffffffu, l[hh], 2);
-        if (P.tree) {
-          // a padding node's row sees nothing, the context included
-          const uint4* w = reinterpret_cast<const uint4*>(seen + (g + 8 * hh) * 8);
-          const uint4 a = w[0], b = w[1];
-          if ((a.x | a.y | a.z | a.w | b.x | b.y | b.z | b.w) == 0) {
-            m[hh] = -INFINITY;
-            l[hh] = 0.f;
-          }
-        }
-        if (tq == 0) {
-          ml[warp * R + g + 8 * hh] = m[hh];
-          ml[(C::WARPS + warp) * R + g + 8 * hh] = l[hh];
-        }
+        // a padding node's row sees nothing, the context included
+        const bool dead = P.tree && bits_of[hh] == 0;
+        if (tq == 0)
+          ml[(g + 8 * hh) * C::WARPS + warp] =
+              dead ? make_float2(-INFINITY, 0.f) : make_float2(m[hh], l[hh]);
       }
-      named_sync(1, 32 * C::WARPS);
-#pragma unroll
-      for (int hh = 0; hh < 2; ++hh) {
-        float mm = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < C::WARPS; ++w) mm = fmaxf(mm, ml[w * R + g + 8 * hh]);
-        const float f = ex2(m[hh] - mm);
-        if (l[hh] == 0.f) {           // nothing seen: all zeros, also where V was not finite
-#pragma unroll
-          for (int x = 0; x < D / 8; ++x) acc[x][2 * hh] = acc[x][2 * hh + 1] = 0.f;
-        } else {
-#pragma unroll
-          for (int x = 0; x < D / 8; ++x) {
-            acc[x][2 * hh] *= f;
-            acc[x][2 * hh + 1] *= f;
-          }
-        }
-      }
-      auto cell = [&](int w, int x, int hh) {
-        return reinterpret_cast<float2*>(merge + (w * R + g + 8 * hh) * C::PITCH + x * 8 + 2 * tq);
-      };
-      if (warp >= C::WARPS / 2)
+#pragma unroll 1
+      for (int r0 = 0; r0 < u.rows; r0 += 8) {
+        if (r0 > 0) named_sync(1, 32 * C::WARPS);       // the first eight rows have been read
 #pragma unroll
         for (int x = 0; x < D / 8; ++x)
+          *reinterpret_cast<float2*>(merge + (warp * 8 + g) * C::PITCH + x * 8 + 2 * tq) =
+              r0 ? make_float2(acc[x][2], acc[x][3]) : make_float2(acc[x][0], acc[x][1]);
+        named_sync(1, 32 * C::WARPS);
+        const bool any = *nf != 0;
+#pragma unroll 1
+        for (int i = tid; i < min(u.rows - r0, 8) * (D / 4); i += 32 * C::WARPS) {
+          const int rl = i / (D / 4), c = i % (D / 4) * 4, r = r0 + rl;
+          float2 w[C::WARPS];
+          float mm = -INFINITY, ll = 0.f;
 #pragma unroll
-          for (int hh = 0; hh < 2; ++hh)
-            *cell(warp - C::WARPS / 2, x, hh) = make_float2(acc[x][2 * hh], acc[x][2 * hh + 1]);
-      named_sync(1, 32 * C::WARPS);
-      if (warp < C::WARPS / 2)
-#pragma unroll
-        for (int x = 0; x < D / 8; ++x)
-#pragma unroll
-          for (int hh = 0; hh < 2; ++hh) {
-            float2 y = *cell(warp, x, hh);
-            y.x += acc[x][2 * hh];
-            y.y += acc[x][2 * hh + 1];
-            *cell(warp, x, hh) = y;
+          for (int k = 0; k < C::WARPS; ++k) {
+            w[k] = ml[r * C::WARPS + k];
+            mm = fmaxf(mm, w[k].x);
           }
-      named_sync(1, 32 * C::WARPS);
-      {
-        // eight threads a row, D / 8 columns each
-        constexpr int TPR = 32 * C::WARPS / R, CPT = D / TPR;
-        const int r = tid / TPR, c0 = (tid % TPR) * CPT;
-        float mm = -INFINITY, ll = 0.f;
+          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int w = 0; w < C::WARPS; ++w) mm = fmaxf(mm, ml[w * R + r]);
-#pragma unroll
-        for (int w = 0; w < C::WARPS; ++w) {
-          const float lw = ml[(C::WARPS + w) * R + r];   // 0: that warp's keys were not seen
-          if (lw != 0.f) ll += lw * ex2(ml[w * R + r] - mm);
-        }
-        float v[CPT];
-#pragma unroll
-        for (int c = 0; c < CPT; ++c)
-          v[c] = merge[r * C::PITCH + c0 + c] + merge[(R + r) * C::PITCH + c0 + c];
-        const uint4 n0 = reinterpret_cast<const uint4*>(nf)[0], n1 = reinterpret_cast<const uint4*>(nf)[1];
-        const bool any = (n0.x | n0.y | n0.z | n0.w | n1.x | n1.y | n1.z | n1.w) != 0;
-        if (r < u.rows) {
+          for (int k = 0; k < C::WARPS; ++k) {
+            const float4 y = *reinterpret_cast<const float4*>(merge + (k * 8 + rl) * C::PITCH + c);
+            if (w[k].y != 0.f) {        // 0: that warp's keys were not seen
+              const float f = ex2(w[k].x - mm);
+              ll += w[k].y * f;
+              v.x += y.x * f;
+              v.y += y.y * f;
+              v.z += y.z * f;
+              v.w += y.w * f;
+            }
+          }
+          const uint4 none = make_uint4(0u, 0u, 0u, 0u);
           if (u.whole()) {
             const int rr = u.row_first + r, node = P.by_G(rr), h = u.hk * P.G + rr - node * P.G;
-            const float inv = ll > 0.f ? 1.f / ll : 0.f;
-            if (ll == 0.f)
-#pragma unroll
-              for (int c = 0; c < CPT; ++c) v[c] = 0.f;
-            uint32_t w[CPT / 2];
-#pragma unroll
-            for (int c = 0; c < CPT / 2; ++c) w[c] = pack_bf16(v[2 * c] * inv, v[2 * c + 1] * inv);
-            __nv_bfloat16* dst = P.o + (u.s.row0 + node) * P.o_stride[0] + h * P.o_stride[1] + c0;
-#pragma unroll
-            for (int c = 0; c < CPT / 8; ++c)
-              reinterpret_cast<uint4*>(dst)[c] =
-                  make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
-            if (any)
-              fix_row(P, u.b, u.hk, u.origin, nf, reinterpret_cast<const uint4*>(seen)[2 * r],
-                      reinterpret_cast<const uint4*>(seen)[2 * r + 1], c0, CPT, dst);
-            if (c0 == 0)
+            const float inv = ll > 0.f ? 1.f / ll : ll;     // 0 or NaN as it is
+            __nv_bfloat16* dst = P.o + (u.s.row0 + node) * P.o_stride[0] + h * P.o_stride[1] + c;
+            *reinterpret_cast<uint2*>(dst) =
+                make_uint2(pack_bf16(v.x * inv, v.y * inv), pack_bf16(v.z * inv, v.w * inv));
+            if (any) fix_row(P, u.b, u.hk, u.origin, nf, make_uint4(seen[r], 0u, 0u, 0u), none, c, 4, dst);
+            if (c == 0)
               P.lse[static_cast<int64_t>(h) * P.total + u.s.row0 + node] =
                   ll > 0.f || ll != ll ? (mm + __log2f(ll)) * 0.69314718055994530942f : -INFINITY;
           } else {
-            const int slot = 2 * blockIdx.x + (u.t0 == 0 ? 1 : 0);
-            const int64_t at = static_cast<int64_t>(slot) * P.part_rows + r;
-            float4* dst = reinterpret_cast<float4*>(P.part_o + at * D + c0);
-#pragma unroll
-            for (int c = 0; c < CPT / 4; ++c)
-              dst[c] = make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
-            if (any)
-              fix_row(P, u.b, u.hk, u.origin, nf, reinterpret_cast<const uint4*>(seen)[2 * r],
-                      reinterpret_cast<const uint4*>(seen)[2 * r + 1], c0, CPT, P.part_o + at * D + c0);
-            if (c0 == 0) P.part_ml[at] = make_float2(mm, ll);
+            const int64_t at = static_cast<int64_t>(2 * blockIdx.x + (u.t0 == 0 ? 1 : 0)) * P.part_rows + r;
+            float* dst = P.part_o + at * D + c;
+            *reinterpret_cast<float4*>(dst) = v;
+            if (any) fix_row(P, u.b, u.hk, u.origin, nf, make_uint4(seen[r], 0u, 0u, 0u), none, c, 4, dst);
+            if (c == 0) P.part_ml[at] = make_float2(mm, ll);
           }
         }
       }
