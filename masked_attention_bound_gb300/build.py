@@ -75,7 +75,7 @@ def _link_binding(obj):
     libs = os.path.join(os.path.dirname(torch.__file__), "lib")
     tmp = MODULE + ".tmp"
     _run(["g++", "-shared", "-o", tmp, obj, "-L" + PKG, "-l:libfm.so", "-L" + libs, "-lc10", "-lc10_cuda",
-          "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN"], "linking the binding")
+          "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python", "-Wl,-rpath,$ORIGIN"], "linking the binding")
     os.replace(tmp, MODULE)
 
 

@@ -7,7 +7,7 @@
 // device.
 #include <Python.h>
 
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -95,8 +95,10 @@ struct Call {
     return static_cast<int32_t*>(t.data_ptr());
   }
 
+  // straight from the allocator: by way of the dispatcher a call that makes
+  // three took 8.8 us of host time, and takes 7.0 so
   at::Tensor empty(at::IntArrayRef shape, at::ScalarType type) const {
-    return at::empty(shape, at::TensorOptions().dtype(type).device(device));
+    return at::Tensor(at::detail::empty_cuda(shape, type, device, std::nullopt));
   }
   // `o`, or a new int32 tensor
   at::Tensor out(const char* name, PyObject* o, Shape shape) const {
