@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(NarrowCfg<D>::THREADS, 2)
   } else {
     // ------------------------------------------------------------ attention
     // A warp whose wait gave up goes on without waiting or computing: the
-    // block-wide merges of every piece still find all eight warps.
+    // block-wide merges of every piece still find all four warps.
     bool ok = true;
     uint32_t e = 0;                              // tiles so far
     const int g = lane >> 2, tq = lane & 3;      // fragment row and column pair
