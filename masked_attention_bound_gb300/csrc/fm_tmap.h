@@ -30,7 +30,8 @@ inline EncodeTiledFn encode_fn() {
 // other) x 64 head-dim elements of one batch entry, laid out in shared memory
 // with the 128-byte swizzle.  Rows past the end read 0.
 inline bool make_tmap_bshd(CUtensorMap* m, const void* base, int B, int S, int H, int D,
-                           const int64_t* stride, int box_rows, int box_heads = 1) {
+                           const int64_t* stride, int box_rows, int box_heads = 1,
+                           CUtensorMapL2promotion promotion = CU_TENSOR_MAP_L2_PROMOTION_L2_256B) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
   cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(H),
@@ -42,7 +43,7 @@ inline bool make_tmap_bshd(CUtensorMap* m, const void* base, int B, int S, int H
   cuuint32_t es[4] = {1, 1, 1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box,
             es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+            promotion, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // e4m3 codes (one byte each): BSHD with head_dim 128 contiguous, one box =
