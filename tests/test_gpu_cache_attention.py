@@ -375,3 +375,22 @@ def test_offsets_at_the_ends_of_32_bits_are_reported_and_stay_in_bounds(nodes, k
         torch.cuda.synchronize()
         assert fm.device_status(status) == _abi.FM_ERR_CACHE
         assert (around[:32] == 7).all() and (around[-32:] == 7).all()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("H,Hkv,nodes", [(128, 1, 1), (256, 2, 3), (300, 1, 2), (512, 1, 1), (129, 1, 5)])
+def test_groups_of_many_heads(H, Hkv, nodes, d):
+    """A node's heads fill row tiles, or pass over their ends."""
+    b = Batch(25, [700, nodes, 130], [nodes] * 3, H, Hkv, d, 32, "random")
+    o, lse, code = run(b)
+    assert code == 0
+    b.check(o, lse)
+
+
+def test_in_inference_mode_and_with_allocated_outputs():
+    b = Batch(26, [700, 40], [9, 3], 8, 2, 128, 16, "random")
+    want = run(b)[:2]
+    with torch.inference_mode():
+        o, lse = fm.tree_forward(b.q, b.k, b.v, b.table, b.lens_t, b.cu, b.scale, parents=b.parents, max_nodes=9)
+    assert not o.requires_grad and o.device == b.q.device
+    assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
