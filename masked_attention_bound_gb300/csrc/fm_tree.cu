@@ -698,9 +698,13 @@ TreeWs tree_ws(const fm_cache& c, const fm_tree_desc& t, int sms) {
   W.rows = rows <= NarrowGeo::R ? NarrowGeo::R
            : rows >= WideGeo::R ? WideGeo::R
                                 : (static_cast<int>(rows) + 31) / 32 * 32;
-  // The kernel: with d = 64, tiles of 128 rows side by side beat pairs of them
-  // (64 sequences of 1000 tokens with 150 rows: 70 us against 81)
-  W.kind = W.rows <= NarrowGeo::R ? NARROW : (W.rows <= MidGeo::R || c.d == 64 ? MID : WIDE);
+  // The kernel: tiles of 128 rows side by side beat pairs of them with d = 64
+  // (64 sequences of 1000 tokens with 150 rows: 70 us against 81), and where
+  // the rows of the table hold at most 640 tokens, so that a unit's ends are
+  // most of it (512 units of 256 rows and 164 keys: 46 us against 56, 544 keys
+  // 75 and 76, 1064 keys 103 and 92)
+  const bool pairs = c.d == 128 && static_cast<int64_t>(c.max_pages) * c.page_size > 640;
+  W.kind = W.rows <= NarrowGeo::R ? NARROW : (W.rows <= MidGeo::R || !pairs ? MID : WIDE);
   if (W.kind == MID && W.rows > MidGeo::R) W.rows = MidGeo::R;   // of a part
   W.grid = W.kind == WIDE ? sms : 2 * sms;       // by the kernel's blocks per SM
   const int grid = W.grid;

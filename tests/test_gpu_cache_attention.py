@@ -394,3 +394,35 @@ def test_in_inference_mode_and_with_allocated_outputs():
         o, lse = fm.tree_forward(b.q, b.k, b.v, b.table, b.lens_t, b.cu, b.scale, parents=b.parents, max_nodes=9)
     assert not o.requires_grad and o.device == b.q.device
     assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+
+
+@pytest.mark.parametrize("H,Hkv", [(8, 2), (10, 2), (8, 8)])
+@pytest.mark.parametrize("bad", [float("nan"), float("-inf")])
+def test_values_not_finite_beside_a_long_context(H, Hkv, bad):
+    """As above, with a table that holds more tokens and units of more than 128 rows or of few."""
+    nodes, ctx, node = 40, 900, 33
+    b = Batch(27, [nodes + ctx], [nodes], H, Hkv, 128, 16, "beams")
+    clean, clean_lse, _ = run(b)
+    p = ctx + node
+    b.v[b.table_np[0, p // 16], p % 16, :, 64] = bad
+    o, lse, code = run(b)
+    assert code == 0 and torch.equal(lse, clean_lse)
+    for t in range(nodes):
+        a = t
+        while a > node:
+            a = b.parents_np[0][a]
+        want = clean[t].clone()
+        if a == node:
+            want[:, 64] = bad
+        assert torch.equal(o[t].nan_to_num(nan=123.0), want.nan_to_num(nan=123.0)), t
+
+
+@pytest.mark.parametrize("kind", [None, "padded", "random"])
+@pytest.mark.parametrize("H,Hkv", [(8, 2), (6, 2), (5, 1)])
+def test_trees_beside_a_long_context(kind, H, Hkv):
+    nodes = [1, 64, 33, 0, 50, 64]
+    lens = [1, 64, 700, 100, 1500, 900]
+    b = Batch(28, lens, nodes, H, Hkv, 128, 16, kind)
+    o, lse, code = run(b)
+    assert code == 0
+    b.check(o, lse)
