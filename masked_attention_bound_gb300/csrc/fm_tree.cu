@@ -692,8 +692,7 @@ struct TreeWs {
 };
 TreeWs tree_ws(const fm_cache& c, const fm_tree_desc& t, int sms) {
   auto up = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
-  const int64_t rows =
-      static_cast<int64_t>(t.max_nodes < t.total ? t.max_nodes : t.total) * (t.H / c.Hkv);
+  const int64_t nodes = t.max_nodes < t.total ? t.max_nodes : t.total, rows = nodes * (t.H / c.Hkv);
   TreeWs W;
   W.rows = rows <= NarrowGeo::R ? NarrowGeo::R
            : rows >= WideGeo::R ? WideGeo::R
@@ -703,8 +702,18 @@ TreeWs tree_ws(const fm_cache& c, const fm_tree_desc& t, int sms) {
   // the rows of the table hold at most 640 tokens, so that a unit's ends are
   // most of it (512 units of 256 rows and 164 keys: 46 us against 56, 544 keys
   // 75 and 76, 1064 keys 103 and 92)
-  const bool pairs = c.d == 128 && static_cast<int64_t>(c.max_pages) * c.page_size > 640;
-  W.kind = W.rows <= NarrowGeo::R ? NARROW : (W.rows <= MidGeo::R || !pairs ? MID : WIDE);
+  const int64_t tokens = static_cast<int64_t>(c.max_pages) * c.page_size;
+  const bool pairs = c.d == 128 && tokens > 640;
+  // More rows than 16 on the kernel for 16, which reads K and V again for each
+  // 16 but starts sooner, where it is little: one tree of 8 nodes of 4 heads
+  // over 2000 tokens took 12.3 us so and 18.4 by 128 rows, 16 over 250 11.4
+  // and 12.4, 32 over 250 18.4 and 13.5, 8 over 2000 23.8 and 22.4.  (Up to 16
+  // nodes: what a row sees is held in 16 bits.  Not where units of up to 512
+  // tokens are left whole: 13.8 and 12.7 over 450.)
+  const int64_t units = static_cast<int64_t>(c.B) * c.Hkv * ((rows + NarrowGeo::R - 1) / NarrowGeo::R);
+  const bool little = nodes <= 16 && units <= 2 * sms && units * tokens <= 80000 && (tokens <= 320 || tokens > 512);
+  W.kind = W.rows <= NarrowGeo::R || little ? NARROW : (W.rows <= MidGeo::R || !pairs ? MID : WIDE);
+  if (W.kind == NARROW) W.rows = NarrowGeo::R;
   if (W.kind == MID && W.rows > MidGeo::R) W.rows = MidGeo::R;   // of a part
   W.grid = W.kind == WIDE ? sms : 2 * sms;       // by the kernel's blocks per SM
   const int grid = W.grid;

@@ -426,3 +426,29 @@ def test_trees_beside_a_long_context(kind, H, Hkv):
     o, lse, code = run(b)
     assert code == 0
     b.check(o, lse)
+
+
+@pytest.mark.parametrize("kind", [None, "chain", "padded", "random"])
+@pytest.mark.parametrize("H,Hkv,d,lens", [(8, 1, 128, [260, 16, 100]), (14, 2, 64, [16, 31, 290]),
+                                          (5, 1, 128, [1500, 700, 16]), (64, 2, 64, [200, 16, 20])])
+def test_few_nodes_of_many_heads(kind, H, Hkv, d, lens):
+    """Up to 16 nodes whose rows are several units of 16, NaN in a place that not all see."""
+    b = Batch(29, lens, [16, 7, 12], H, Hkv, d, 16, kind)
+    o, lse, code = run(b)
+    assert code == 0
+    b.check(o, lse)
+    node, base = 5, lens[0] - 16
+    p = base + node
+    b.v[b.table_np[0, p // 16], p % 16, :, 3] = float("nan")
+    o2, lse2, code = run(b)
+    assert code == 0 and torch.equal(lse2, lse)
+    for t in range(16):
+        see = t >= node if kind is None else False
+        a = t
+        while kind is not None and a >= 0 and b.parents_np[0][a] != -2:
+            see |= a == node
+            a = b.parents_np[0][a]
+        want = o[t].clone()
+        if see:
+            want[:, 3] = float("nan")
+        assert torch.equal(o2[t].nan_to_num(nan=123.0), want.nan_to_num(nan=123.0)), t
