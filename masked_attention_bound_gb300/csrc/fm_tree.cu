@@ -285,15 +285,24 @@ __global__ void __launch_bounds__(NarrowCfg<D>::THREADS, 2)
             }
           // P as the sum of two bf16 numbers (16 bits of mantissa): with one,
           // its rounding is as large an error of O as the rounding of the
-          // output, and the tensor cores have the time here
+          // output, and the tensor cores have the time here.  Both are
+          // positive wherever P is, so that an infinity of V in the context
+          // stays one: the first is P cut off, never rounded up, and the
+          // second at least the smallest bf16 number.
 #pragma unroll
           for (int x = 0; x < 2; ++x)
 #pragma unroll
             for (int hh = 0; hh < 2; ++hh) {
-              const uint32_t hi = pack_bf16(p[x][2 * hh], p[x][2 * hh + 1]);
-              pf[2 * x + hh] = hi;
-              pl[2 * x + hh] = pack_bf16(p[x][2 * hh] - __uint_as_float(hi << 16),
-                                         p[x][2 * hh + 1] - __uint_as_float(hi & 0xffff0000u));
+              float lo[2];
+#pragma unroll
+              for (int y = 0; y < 2; ++y) {
+                const float w = p[x][2 * hh + y];
+                const float cut = __uint_as_float(__float_as_uint(w) & 0xffff0000u);
+                lo[y] = fminf(w, fmaxf(w - cut, __uint_as_float(0x00010000u)));
+              }
+              pf[2 * x + hh] =
+                  __byte_perm(__float_as_uint(p[x][2 * hh]), __float_as_uint(p[x][2 * hh + 1]), 0x7632);
+              pl[2 * x + hh] = pack_bf16(lo[0], lo[1]);
             }
         }
         if (ok) ok = wait_all(full(C::KS + vs), vp);

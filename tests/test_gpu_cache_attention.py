@@ -452,3 +452,50 @@ def test_few_nodes_of_many_heads(kind, H, Hkv, d, lens):
         if see:
             want[:, 3] = float("nan")
         assert torch.equal(o2[t].nan_to_num(nan=123.0), want.nan_to_num(nan=123.0)), t
+
+
+# kernels: 16 rows; several units of 16 rows; 128 rows; 256 rows (with a sequence of up to 128, whose
+# key tiles two slots take in turn)
+KERNELS = [(64, [1, 1], 8, 2, 300, 16), (128, [1, 1], 5, 1, 300, 16), (128, [12, 3], 2, 2, 300, 16),
+           (64, [12, 5], 8, 2, 100, 16), (128, [12, 16], 12, 2, 100, 32), (64, [20, 7], 8, 2, 300, 16),
+           (128, [20, 32], 8, 2, 300, 64), (128, [20, 60], 8, 2, 900, 16), (128, [200, 33], 4, 1, 700, 16)]
+
+
+@pytest.mark.parametrize("kind", [None, "random"])
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf")])
+@pytest.mark.parametrize("d,nodes,H,Hkv,ctx,page", KERNELS)
+def test_infinities_in_the_context_reach_every_row(d, nodes, H, Hkv, ctx, page, bad, kind):
+    """Whatever the weight's last bits, the infinity's sign stays; a context of one key too."""
+    b = Batch(30, [1 + nodes[0], ctx + nodes[1]], nodes, H, Hkv, d, page, kind)
+    clean, clean_lse, _ = run(b)
+    cols = [1, min(ctx, d - 1)]           # a key each, spread over the context; the last column stays finite
+    for seq, m in enumerate(cols):
+        for c in range(m):
+            p = c * ((1, ctx)[seq] // m)
+            b.v[b.table_np[seq, p // page], p % page, :, c] = bad
+    o, lse, code = run(b)
+    assert code == 0 and torch.equal(lse, clean_lse)
+    for seq, m in enumerate(cols):
+        rows = slice(b.cu_np[seq], b.cu_np[seq + 1])
+        assert (o[rows, :, :m] == bad).all(), (seq, int((o[rows, :, :m] != bad).sum()))
+        assert torch.equal(o[rows, :, m:], clean[rows, :, m:])
+
+
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf")])
+@pytest.mark.parametrize("d,nodes,H,Hkv,ctx,page", KERNELS)
+def test_infinities_under_small_weights(d, nodes, H, Hkv, ctx, page, bad):
+    """Weights down to 2^-125 of the largest one (the smallest normal number is 2^-126)."""
+    b = Batch(31, [ctx + n for n in nodes], nodes, H, Hkv, d, page)
+    b.scale = 1.0
+    b.q.zero_()
+    b.q[:, :, 0] = 1.0
+    b.k.zero_()
+    for seq in range(2):
+        for c, x in enumerate((0.0, -1.0, -20.25, -40.5, -76.0, -80.0, -83.0, -85.5, -86.5)):
+            p = 3 + c
+            b.k[b.table_np[seq, p // page], p % page, :, 0] = x
+            b.v[b.table_np[seq, p // page], p % page, :, c] = bad
+    o, lse, code = run(b)
+    assert code == 0 and lse.isfinite().all()
+    assert (o[:, :, :9] == bad).all(), [(o[:, :, c] != bad).any().item() for c in range(9)]
+    assert o[:, :, 9:].isfinite().all()
