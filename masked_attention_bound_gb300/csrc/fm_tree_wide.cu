@@ -658,8 +658,10 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS>::THREADS, WideCfg<D, SLOTS>:
         slots_sync<SLOTS>();
         const float2 a = ml[r], b = two ? ml[128 + r] : make_float2(-INFINITY, 0.f);
         m_out = fmaxf(a.x, b.x);
-        f0 = a.y != 0.f ? ex2(a.x - m_out) : 0.f;
-        f1 = b.y != 0.f ? ex2(b.x - m_out) : 0.f;
+        // negative: that slot's keys were not seen.  A weight of 0 is no such
+        // sign: a NaN under it counts
+        f0 = a.y != 0.f ? ex2(a.x - m_out) : -1.f;
+        f1 = b.y != 0.f ? ex2(b.x - m_out) : -1.f;
         l_out = (a.y != 0.f ? a.y * f0 : 0.f) + (b.y != 0.f ? b.y * f1 : 0.f);
         c0 = slot * (D / 2);
         c1 = c0 + D / 2;
@@ -693,7 +695,7 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS>::THREADS, WideCfg<D, SLOTS>:
             tmem_wait_ld();
 #pragma unroll
             for (int y = 0; y < 32; ++y)
-              v[y] = (f0 != 0.f ? v[y] * f0 : 0.f) + (f1 != 0.f ? __uint_as_float(rb[y]) * f1 : 0.f);
+              v[y] = (f0 < 0.f ? 0.f : v[y] * f0) + (f1 < 0.f ? 0.f : __uint_as_float(rb[y]) * f1);
           } else {
             tmem_wait_ld();
           }

@@ -499,3 +499,21 @@ def test_infinities_under_small_weights(d, nodes, H, Hkv, ctx, page, bad):
     assert code == 0 and lse.isfinite().all()
     assert (o[:, :, :9] == bad).all(), [(o[:, :, c] != bad).any().item() for c in range(9)]
     assert o[:, :, 9:].isfinite().all()
+
+
+@pytest.mark.parametrize("d,nodes,H,Hkv,ctx,page", KERNELS)
+def test_nan_under_a_weight_of_zero_reaches_every_row(d, nodes, H, Hkv, ctx, page):
+    """Context keys whose weight underflows to 0 (scores 200 below the others') are visible all the same."""
+    ctx = max(ctx, 256)
+    b = Batch(32, [ctx + n for n in nodes], nodes, H, Hkv, d, page)
+    b.scale = 1.0
+    b.q.zero_()
+    b.q[:, :, 0] = 1.0
+    b.k.zero_()
+    for seq in range(2):
+        for p in range(128, 256):
+            b.k[b.table_np[seq, p // page], p % page, :, 0] = -200.0
+        b.v[b.table_np[seq, 130 // page], 130 % page, :, 9] = float("nan")
+    o, lse, code = run(b)
+    assert code == 0 and lse.isfinite().all()
+    assert o[:, :, 9].isnan().all() and o[:, :, 10:].isfinite().all()
