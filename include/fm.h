@@ -362,7 +362,8 @@ fm_status fm_cache_append(const fm_cache* cache, const void* k, const void* v,
  * does not depend on the order in which its parts run: equal inputs give
  * equal bits on the same GPU.  `ws`: fm_tree_workspace_size() bytes, 256-byte
  * aligned, scratch of this call only; calls that may overlap on the GPU need
- * one each. */
+ * one each.  A workspace serves every call of up to the max_nodes and total
+ * that it was sized for, with the same heads and d and any page table. */
 #define FM_TREE_MAX_NODES 256
 typedef struct {
   int H;          /* query heads, a multiple of Hkv */

@@ -89,7 +89,8 @@ def cache_append(k, v, cu, k_pool, v_pool, table, lens, status=None, stream=None
 
 
 def tree_workspace(q, k_pool, v_pool, table, max_nodes=None) -> torch.Tensor:
-    """Scratch of ``tree_forward`` for a program that keeps its own (one per call in flight)."""
+    """Scratch of ``tree_forward`` for a program that keeps its own (one per call in flight).  It
+    serves every call of up to ``max_nodes`` and q's tokens, with the same heads and any table."""
     C = make_cache(k_pool, v_pool, table)
     D = FmTreeDesc()
     total = max(q.shape[0], 1)

@@ -699,8 +699,14 @@ struct TreeWs {
   int grid;
   size_t rec, ml, o, bytes;
 };
-TreeWs tree_ws(const fm_cache& c, const fm_tree_desc& t, int sms) {
+void tree_ws_places(TreeWs& W, int d) {
   auto up = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
+  W.rec = 0;
+  W.ml = up(static_cast<size_t>(W.grid) * sizeof(int4));
+  W.o = W.ml + up(2ull * W.grid * W.rows * sizeof(float2));
+  W.bytes = W.o + 2ull * W.grid * W.rows * d * sizeof(float);
+}
+TreeWs tree_ws(const fm_cache& c, const fm_tree_desc& t, int sms) {
   const int64_t nodes = t.max_nodes < t.total ? t.max_nodes : t.total, rows = nodes * (t.H / c.Hkv);
   TreeWs W;
   W.rows = rows <= NarrowGeo::R ? NarrowGeo::R
@@ -725,12 +731,22 @@ TreeWs tree_ws(const fm_cache& c, const fm_tree_desc& t, int sms) {
   if (W.kind == NARROW) W.rows = NarrowGeo::R;
   if (W.kind == MID && W.rows > MidGeo::R) W.rows = MidGeo::R;   // of a part
   W.grid = W.kind == WIDE ? sms : 2 * sms;       // by the kernel's blocks per SM
-  const int grid = W.grid;
-  W.rec = 0;
-  W.ml = up(static_cast<size_t>(grid) * sizeof(int4));
-  W.o = W.ml + up(2ull * grid * W.rows * sizeof(float2));
-  W.bytes = W.o + 2ull * grid * W.rows * c.d * sizeof(float);
+  tree_ws_places(W, c.d);
   return W;
+}
+
+// Bytes that suffice for every call of up to these nodes and tokens, whatever
+// kernel the other sizes choose: a part for each of two blocks per SM, of the
+// rows of a unit, at most 128.  (The kernel for 256 rows has half the blocks.)
+size_t tree_ws_bound(const fm_cache& c, const fm_tree_desc& t, int sms) {
+  const int64_t nodes = t.max_nodes < t.total ? t.max_nodes : t.total, rows = nodes * (t.H / c.Hkv);
+  TreeWs W;
+  W.rows = rows <= NarrowGeo::R ? NarrowGeo::R
+           : rows >= MidGeo::R  ? MidGeo::R
+                                : (static_cast<int>(rows) + 31) / 32 * 32;
+  W.grid = 2 * sms;
+  tree_ws_places(W, c.d);
+  return W.bytes;
 }
 
 }  // namespace
@@ -742,7 +758,7 @@ extern "C" {
 
 size_t fm_tree_workspace_size(const fm_cache* c, const fm_tree_desc* t) {
   if (check_tree(c, t) != FM_OK) return 0;
-  return tree_ws(*c, *t, num_sms()).bytes;
+  return tree_ws_bound(*c, *t, num_sms());
 }
 
 fm_status fm_tree_fwd(const fm_cache* c, const fm_tree_desc* t, const void* q, const void* k_pool,

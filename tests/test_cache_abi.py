@@ -1,5 +1,6 @@
 """Refusals of the paged-cache entry points, on the host and without a GPU."""
 import ctypes
+import itertools
 
 import pytest
 import torch
@@ -164,3 +165,21 @@ def test_binding_refuses_cpu_tensors_and_wrong_shapes():
 def test_status_names(L):
     for c in (_abi.FM_ERR_CACHE, _abi.FM_ERR_PAGES):
         assert len(_abi.status_string(c)) > 5 and _abi.STATUS_NAMES[c].startswith("FM_ERR")
+
+
+def test_a_workspace_of_the_attention_serves_every_smaller_description(L):
+    """No kernel that fewer nodes, tokens or a narrower table choose needs more than the size given for
+    more of them."""
+    for d, G, B in itertools.product((64, 128), (1, 3, 4, 8, 40, 300), (1, 2, 40, 1000)):
+        need = {}
+        for width, total, nodes in itertools.product((4, 20, 41, 200), (1, 4, 20, 128, 129, 600),
+                                                     (1, 2, 3, 4, 5, 16, 17, 31, 32, 33, 40, 63, 64, 65, 128, 200, 256)):
+            C = _cache(d=d, B=B, max_pages=width)
+            D = _desc(H=2 * G, total=total, max_nodes=nodes)
+            need[width, total, nodes] = L.fm_tree_workspace_size(ctypes.byref(C), ctypes.byref(D))
+        assert min(need.values()) > 0
+        for size, n in need.items():
+            for axis in range(3):        # the next smaller value of one axis
+                less = max((x for x in need if all(x[a] == size[a] or a == axis for a in range(3))
+                            and x[axis] < size[axis]), key=lambda x: x[axis], default=size)
+                assert need[less] <= n, (d, G, B, less, size)

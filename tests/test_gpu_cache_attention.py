@@ -517,3 +517,16 @@ def test_nan_under_a_weight_of_zero_reaches_every_row(d, nodes, H, Hkv, ctx, pag
     o, lse, code = run(b)
     assert code == 0 and lse.isfinite().all()
     assert o[:, :, 9].isnan().all() and o[:, :, 10:].isfinite().all()
+
+
+@pytest.mark.parametrize("d,G", [(128, 4), (64, 4), (128, 1)])
+def test_a_workspace_for_the_largest_step_serves_smaller_ones(d, G):
+    """One workspace, sized once for 60 nodes, through every kernel that fewer nodes take."""
+    b = Batch(33, [900, 700], [60, 60], 2 * G, 2, d, 16)
+    ws = fm.tree_workspace(b.q, b.k, b.v, b.table, 60)
+    for nodes in (60, 40, 33, 32, 31, 17, 16, 5, 4, 1):
+        c = Batch(33, [900, 700], [nodes, nodes], 2 * G, 2, d, 16)
+        ws.fill_(255)
+        o, lse, code = run(c, ws=ws)
+        assert code == 0
+        c.check(o, lse, rows=3)
