@@ -224,6 +224,8 @@ __global__ void __launch_bounds__(kAcceptThreads, 12)
     const int pg = row[pos >> P.page_shift];
     return pg >= 0 && pg < A.n_pages ? (pg << 8) | (pos & (P.page_size() - 1)) : -1;
   };
+  // the first page past the context and x more tokens
+  auto first_free = [&](int x) { return (base + x + P.page_size() - 1) >> P.page_shift; };
   // entry i of the list, valid or not
   auto look = [&](int i, int2& p) -> bool {
     const int a = acc[i], before = i ? acc[i - 1] : -1;
@@ -239,6 +241,11 @@ __global__ void __launch_bounds__(kAcceptThreads, 12)
       ok = look(i, q) && ok;
       if (i < 32) p = q;
     }
+    // the pages past the new length, which the first block of the sequence
+    // lets go of: looked at by all, since one that is out of range leaves the
+    // whole sequence as it is
+    if (sized && A.ref)
+      for (int j = first_free(m) + lane; j < first_free(n); j += 32) ok = at(j << P.page_shift) >= 0 && ok;
     ok = __all_sync(0xffffffffu, ok);
     place[lane] = p;
     if (lane == 0) good = ok;
@@ -250,14 +257,8 @@ __global__ void __launch_bounds__(kAcceptThreads, 12)
       A.lens_out[b] = ok ? base + m : A.lens[b];
       if (!ok) flag(A.status, DEV_CACHE);
     }
-    // the pages past the new length
     if (ok && A.ref)
-      for (int j = ((base + m + P.page_size() - 1) >> P.page_shift) + threadIdx.x;
-           j < (base + n + P.page_size() - 1) >> P.page_shift; j += blockDim.x) {
-        const int pg = row[j];
-        if (pg >= 0 && pg < A.n_pages) atomicSub(A.ref + pg, 1);
-        else flag(A.status, DEV_CACHE);
-      }
+      for (int j = first_free(m) + threadIdx.x; j < first_free(n); j += blockDim.x) atomicSub(A.ref + row[j], 1);
   }
   if (!ok) return;
   const int v = blockIdx.x * kAcceptThreads + threadIdx.x;

@@ -400,3 +400,21 @@ def test_drafting_and_verifying_equals_decoding_token_by_token(H, Hkv, d, page):
             for i, pool in enumerate((k, v)):
                 got = oc.gather(pool[layer].float().cpu().numpy(), rows, n)
                 assert np.array_equal(got, np.stack(plain[layer][b][i]))
+
+
+@pytest.mark.parametrize("value", [-1, 1 << 23, "pages"])
+@pytest.mark.parametrize("at", [2, 3, 4])
+def test_accept_leaves_a_sequence_with_a_bad_page_to_release(at, value):
+    """A page past the new length that is out of range: nothing of the sequence is moved or released."""
+    b = Batch(14, [20 + 50, 25], [50, 5], 2, 2, 64, 16)
+    k, v = _pools(15, 3, b.k.shape[0], 16, 2, 64)
+    ref = torch.full((b.k.shape[0],), 3, dtype=torch.int32, device="cuda")
+    b.table[0, at] = b.k.shape[0] if value == "pages" else value
+    arr = np.zeros((2, 3))
+    arr[0], arr[1, :2] = [1, 4, 8], [2, 4]       # row 0: tokens 21, 24 and 28, all in good pages
+    want, lens = oc.accept([[], [2, 4]], b.cu_np, _bits(k), b.table_np, [70, 25])
+    st = _status()
+    out = fm.cache_accept(ints(arr), ints([3, 2]), b.cu, k, v, b.table, b.lens_t, ref=ref, status=st)
+    assert fm.device_status(st) == _abi.FM_ERR_CACHE
+    assert out.tolist() == [70, lens[1]] and np.array_equal(_bits(k), want)
+    assert ref.tolist() == [3] * b.k.shape[0]
