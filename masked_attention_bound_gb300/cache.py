@@ -71,6 +71,8 @@ def make_cache(k_pool, v_pool, table) -> FmCache:
             raise ValueError("pools must be bf16 CUDA tensors on the page table's device")
         if t.stride(-1) != 1:
             raise ValueError("head_dim must be the contiguous dimension")
+    if max(*k_pool.shape, *table.shape) >= 1 << 31:
+        raise ValueError("pools and page tables have fewer than 2^31 layers, pages, rows and entries of a row")
     C = FmCache()
     C.B, C.max_pages = table.shape
     C.layers = k_pool.shape[0] if k_pool.dim() == 5 else 1

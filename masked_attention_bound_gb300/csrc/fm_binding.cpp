@@ -141,6 +141,8 @@ struct Cache {
                                      "without layers, and the page table [B][max_pages]");
     for (int64_t i = 0; i < dim; ++i)
       if (kp.size(i) > INT32_MAX) refuse(call.where, "pools of more than 2^31 pages");
+    if (tb.size(0) > INT32_MAX || tb.size(1) > INT32_MAX)
+      refuse(call.where, "a page table of more than 2^31 rows or entries of a row");
     const int f = dim == 5;
     c.layers = f ? static_cast<int>(kp.size(0)) : 1;
     c.n_pages = static_cast<int>(kp.size(f));
@@ -277,8 +279,10 @@ PyObject* fork(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const at::Tensor& ref = tensor(call.where, "ref", a[4]);
   const long long page = PyLong_AsLongLong(a[1]);
   if (page == -1 && PyErr_Occurred()) throw Raised();
-  if (table.dim() != 2 || ref.dim() != 1 || ref.size(0) > INT32_MAX || page < 1 || page > INT32_MAX)
+  if (table.dim() != 2 || ref.dim() != 1 || page < 1 || page > INT32_MAX)
     refuse(call.where, "table must be [B][max_pages], ref [pages] and page_size positive");
+  if (table.size(0) > INT32_MAX || table.size(1) > INT32_MAX || ref.size(0) > INT32_MAX)
+    refuse(call.where, "more than 2^31 rows, entries of a row or pages");
   const int64_t B = table.size(0), m = table.size(1), P = ref.size(0);
   fm_cache c{};
   c.B = static_cast<int>(B);

@@ -418,3 +418,17 @@ def test_accept_leaves_a_sequence_with_a_bad_page_to_release(at, value):
     assert fm.device_status(st) == _abi.FM_ERR_CACHE
     assert out.tolist() == [70, lens[1]] and np.array_equal(_bits(k), want)
     assert ref.tolist() == [3] * b.k.shape[0]
+
+
+def test_tables_of_more_rows_than_32_bits_are_refused():
+    table = torch.empty((1 << 32) + 2, 1, dtype=torch.int32, device="cuda")
+    k, v = _pools(16, 4, 16, 1, 64)
+    two, ref = ints([0, 0]), ints([1, 0, 0, 0])
+    with pytest.raises(ValueError):
+        fm.pages_fork(two, 16, table, two, ref, table_out=torch.empty_like(table), lens_out=ints([0, 0]))
+    with pytest.raises(ValueError):
+        fm.pages_reserve(two, k, v, table, two, ref)
+    with pytest.raises(ValueError):
+        fm.cache_append(k[0, :2], v[0, :2], ints([0, 1, 2]), k, v, table, ints([1, 1]))
+    with pytest.raises(ValueError):
+        fm.make_cache(k, v, table)
