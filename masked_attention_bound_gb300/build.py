@@ -4,7 +4,8 @@ Python module of the paged cache's calls.
 Each ``csrc/*.cu`` compiles to ``_build/<name>.o`` in parallel, then one
 nvcc link makes the shared library next to this file.  ``csrc/fm_binding.cpp``
 compiles with the host compiler against torch's headers and links to the
-library.  Rebuilds only when a source or header is newer than its result.
+library.  Rebuilds only when a source or header is newer than its result, and the
+module also when it was built against another torch.
 """
 from __future__ import annotations
 
@@ -54,8 +55,32 @@ def _binding_deps():
     return [BINDING, os.path.join(INCLUDE, "fm.h")]
 
 
+def _torch_version():
+    try:
+        import torch
+    except ImportError:
+        return None
+    return torch.__version__
+
+
+def _binding_stamp():
+    """The file that holds the torch version that the module was built against."""
+    return os.path.join(BUILD, "fm_binding.torch")
+
+
+def _lib_up_to_date() -> bool:
+    return _newer(LIB, _deps())
+
+
+def _binding_up_to_date() -> bool:
+    if not _newer(MODULE, _binding_deps()) or not os.path.exists(_binding_stamp()):
+        return False
+    with open(_binding_stamp()) as f:
+        return f.read() == _torch_version()
+
+
 def up_to_date() -> bool:
-    return _newer(LIB, _deps()) and _newer(MODULE, _binding_deps())
+    return _lib_up_to_date() and _binding_up_to_date()
 
 
 def _compile_binding(obj):
@@ -77,6 +102,8 @@ def _link_binding(obj):
     _run(["g++", "-shared", "-o", tmp, obj, "-L" + PKG, "-l:libfm.so", "-L" + libs, "-lc10", "-lc10_cuda",
           "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python", "-Wl,-rpath,$ORIGIN"], "linking the binding")
     os.replace(tmp, MODULE)
+    with open(_binding_stamp(), "w") as f:
+        f.write(torch.__version__)
 
 
 def _run(cmd, what):
@@ -85,11 +112,7 @@ def _run(cmd, what):
         raise RuntimeError(f"{what} failed:\n{r.stdout}\n{r.stderr}")
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile and link; returns the path of the shared library."""
-    if not force and up_to_date():
-        return LIB
-    os.makedirs(BUILD, exist_ok=True)
+def _build_lib(ex, verbose):
     nvcc = _nvcc()
 
     def compile_one(src):
@@ -104,20 +127,31 @@ def build(force: bool = False, verbose: bool = False) -> str:
             sys.stderr.write(r.stderr)
         return obj
 
-    binding = os.path.join(BUILD, "fm_binding.o")
-    with ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 4)) as ex:
-        made = ex.submit(_compile_binding, binding)
-        objs = list(ex.map(compile_one, _sources()))
-        made.result()
+    objs = list(ex.map(compile_one, _sources()))
     tmp = LIB + ".tmp"
     # no -lcuda: the TMA encoder is fetched through the runtime's driver
     # entry-point query, so the library loads on machines without a driver
-    cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    _run([nvcc, *ARCH, "-shared", "-o", tmp, *objs], "linking the library")
     os.replace(tmp, LIB)
-    _link_binding(binding)
+
+
+def build(force: bool = False, verbose: bool = False) -> str:
+    """Compile and link what is not up to date; returns the path of the shared library.
+
+    The library comes first and needs nvcc only.  Where the Python module cannot be
+    built (no g++, Python.h or torch headers), the call raises after the library is in
+    place."""
+    if not force and up_to_date():
+        return LIB
+    os.makedirs(BUILD, exist_ok=True)
+    binding = os.path.join(BUILD, "fm_binding.o")
+    with ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 4)) as ex:
+        made = ex.submit(_compile_binding, binding) if force or not _binding_up_to_date() else None
+        if force or not _lib_up_to_date():
+            _build_lib(ex, verbose)
+        if made:
+            made.result()
+            _link_binding(binding)
     return LIB
 
 
