@@ -56,9 +56,9 @@ struct WideCfg {
   static constexpr int USED = OFF_PAR + 512;
   static constexpr int SMEM = USED;
   static_assert(BLOCKS * (SMEM + 1024) <= 228 * 1024, "blocks per SM");
-  // O is written through 4 KB per softmax warp, in the Q tiles: they are not
-  // needed any more by then
-  static_assert(SM_WARPS * 4096 <= SLOTS * QTILE, "room for the output's staging");
+  // O is written through 4 KB per softmax warp, in its slot's Q tile: that
+  // slot's S have all been read by then
+  static_assert(4 * 4096 <= QTILE, "room for the output's staging");
   static constexpr uint32_t T_COLS = 256 * SLOTS, T_O = 128 * SLOTS;
   // register split: the softmax warpgroups' and the others' budgets add up to
   // what the block is launched with (384 x 168, 256 x 128)
@@ -681,7 +681,7 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS>::THREADS, WideCfg<D, SLOTS>:
       // O by blocks of 32 columns; each passes through the warp's part of the
       // slot's Q buffer (no longer needed), so that the stores cover whole
       // runs of a row: 64 bytes (bf16) or 128 bytes (fp32 parts)
-      uint8_t* stage = smem + C::OFF_Q + warp * 4096;
+      uint8_t* stage = smem + C::OFF_Q + slot * C::QTILE + quarter * 4096;
       const unsigned out_rows = __ballot_sync(0xffffffffu, writes);
 #pragma unroll 1
       for (int cb = c0 / 32; cb < c1 / 32; ++cb) {
