@@ -725,7 +725,7 @@ __global__ void __launch_bounds__(kCopyThreads)
 
 fm_status done(cudaError_t e) { return e == cudaSuccess ? FM_OK : FM_ERR_CUDA; }
 
-// Each output is its input itself or does not overlap it (or any other input).
+// Each output is its input itself or does not overlap it.
 bool outputs_apart(const fm_cache& c, const PageArgs& A) {
   const size_t nt = static_cast<size_t>(c.B) * c.max_pages * 4, nl = static_cast<size_t>(c.B) * 4,
                nr = static_cast<size_t>(c.n_pages) * 4;

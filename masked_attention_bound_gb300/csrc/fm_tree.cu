@@ -794,9 +794,14 @@ fm_status fm_tree_fwd(const fm_cache* c, const fm_tree_desc* t, const void* q, c
   P.tree = parents != nullptr;
   // Units are not cut, and the join (3 us after the first kernel) is spared,
   // where the rows of the table hold at most 320 tokens (512 units of 100 keys
-  // 14.7 us, cut 19.5; 4096 of 250 keys 116, cut 113), or at most 512 as long as
-  // no block has more than two units (512 units of 64 rows and 400 keys 31.3 us,
-  // cut 36.4; 1024 units of 480 keys 48, cut 43).
+  // 11.7 us, cut 15.0; 4096 of 250 keys 116, cut 113), or at most 512 as long as
+  // no block has more than two pairs of a sequence and a K/V head (512 units of
+  // 64 rows and 400 keys 31.3 us, cut 36.4; 1024 units of 480 keys 48, cut 43).
+  // Row tiles are not counted: causal runs of 480 tokens of 32 heads over 8,
+  // 15 units a pair, took 28.6, 88 and 284 us for 4, 16 and 64 of them left
+  // whole, and 35, 89 and 290 cut.  What the host knows of the lengths is the
+  // table's width: one token of 256 keys takes 6.7 us with a table of 272
+  // tokens a row and 7.9 with one of 1024 or more.
   const int64_t tokens = static_cast<int64_t>(c->max_pages) * c->page_size;
   P.whole = tokens <= 320 || (tokens <= 512 && static_cast<int64_t>(c->B) * c->Hkv <= 2 * grid);
   P.scale_log2 = scale_log2;

@@ -24,6 +24,16 @@
 // comes by TMA (SLOTS = 2, a group size that divides 128) or by the softmax
 // warps' copies.  The softmax warps also clean the V tiles that hold drafted
 // nodes.
+//
+// P is rounded to bf16, the type of V, for its product (the operands of
+// tcgen05.mma have one type), as in the prompt forward; its sum, the maximum, S
+// and O are fp32.  That is at most 2^-8 of a weight, and O is off by 0.0023 of
+// its norm against float64 where an fp32 computation rounded once is off by
+// 0.0017.  P as two bf16 numbers, as in the kernel for 16 rows, would bring
+// 0.0017 and cost a second product: 64 sequences of 1000 tokens with 64 rows
+// took 55.7 us so and 50.7 with one number, with d = 64 and 150 rows 74.7 and
+// 64.5.
+//
 // TMEM: S/P of slot s at column 128 s (SLOTS = 1: of every second tile at
 // column 64), the O's after the S's.
 #include <type_traits>
@@ -593,13 +603,13 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS>::THREADS, WideCfg<D, SLOTS>:
             tmem_wait_st();
           }
           if (partial && ok) {
-            // clean row r of the V tile (see fix_value) before the product
+            // clean row r of the V tile (see fix_row) before the product
             const uint32_t e = e0 + x0, st = e % C::VSTAGES;
             ok = wait_all(W_VFULL + st, (e / C::VSTAGES) & 1);
             if (ok) {
               const int key = t * KT + r, i = key - u.origin;
-              // 16-byte words of the row, the slabs 16 KB apart; the lanes
-              // start at different words (bank conflicts)
+              // 16-byte words of the row, the slabs KT * 128 bytes apart; the
+              // lanes start at different words (bank conflicts)
               uint8_t* v = smem + C::OFF_V + st * C::TILE + r * 128;
               auto word = [&](int c) {
                 return reinterpret_cast<uint4*>(v + (c >> 3) * (KT * 128) + ((c ^ r) & 7) * 16);
