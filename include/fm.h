@@ -352,7 +352,9 @@ fm_status fm_cache_append(const fm_cache* cache, const void* k, const void* v,
  * O = softmax(scale * q k^T) v over the visible keys, exactly as fm_fwd, with
  * query head h reading K/V head h / (H / Hkv); a key that a row does not see
  * has no part in its result, whatever its K and V hold (NaN and infinities
- * included).  Rows that see no key get O = 0 and LSE = -inf.
+ * included).  An infinity of V that it does see gives that infinity (NaN under
+ * a weight of less than some 2^-126 of the largest, which fp32 does not hold).
+ * Rows that see no key get O = 0 and LSE = -inf.
  * q, o: bf16, element (token, head, c) at token*stride[0] + head*stride[1] +
  * c; lse: fp32 [H][total].  scale: positive, and scale * log2(e) a normal
  * finite number.  max_nodes: an upper bound of n over the batch.  Sequences with lens or cu out of range or more than max_nodes nodes get
