@@ -435,6 +435,92 @@ fm_status fm_pages_compact(const fm_cache* cache, void* k_pool, void* v_pool, co
                            int32_t* ref_out, int32_t* n_live, void* ws, size_t ws_bytes,
                            int32_t* status, void* stream);
 
+/* ------------------------------------------------------- position rotation
+ * fm_cache_append with the rotation of keys (and queries) by their position
+ * on the way, to pools of bf16 or of e4m3 codes (below).
+ *
+ * Pair i < rot / 2 of a head's first `rot` elements, (x[i], x[i + rot / 2]) or
+ * with `interleaved` (x[2 i], x[2 i + 1]), turns by the angle p * freqs[i]: (a,
+ * b) becomes (a cos - b sin, b cos + a sin).  The other elements stay.  p is
+ * positions[row], or with positions NULL the token's place in its sequence
+ * (lens[b] - (cu[b+1] - cu[b]) + i).  A drafted node, whose place is not its
+ * depth, gets context + depth, which is its place once it is accepted.
+ *   rot: 0 (no rotation: freqs and positions are not read) or a multiple of
+ *     16 up to d; freqs: device float [rot / 2], radians per position; one
+ *     that is not finite makes its pairs NaN.
+ *   positions: device int32 [total], any values, or NULL.
+ *   H: query heads, a multiple of Hkv, or 0: no queries.  q, q_out: bf16,
+ *     element (token, head, c) at token*stride[0] + head*stride[1] + c, q_out
+ *     may be q with the same strides and may not overlap it otherwise.
+ * Angles are exact to 2^-34 of a turn at any position below 2^30.  Sequences
+ * with lens or cu out of range are skipped, their rows of q_out with them; a
+ * token whose page is out of range is not cached (FM_ERR_CACHE). */
+typedef struct {
+  int rot, interleaved;
+  const float* freqs;
+  const int32_t* positions;
+  int H;
+  const void* q;
+  void* q_out;
+  int64_t q_stride[2], o_stride[2];  /* token, head */
+} fm_rotary;
+/* k_scale, v_scale: NULL with pools of bf16. */
+fm_status fm_cache_append_rotary(const fm_cache* cache, const fm_rotary* rotary, const void* k,
+                                 const void* v, const int64_t* k_stride, const int64_t* v_stride,
+                                 const int32_t* cu, int total, void* k_pool, void* v_pool,
+                                 float* k_scale, float* v_scale, const int32_t* table,
+                                 const int32_t* lens, int32_t* status, void* stream);
+
+/* ---------------------------------------------------------- cache of 8 bits
+ * The same cache with pools of e4m3 codes, one byte an element, and a scale
+ * for each block of FM_SCALE_BLOCK tokens of a head: the value is code *
+ * scale.  The pools' strides are in elements and multiples of 16.  k_scale,
+ * v_scale: device float [layers][n_pages][Hkv][page_size / FM_SCALE_BLOCK],
+ * contiguous (a layer's own for the calls of one layer).  They need no
+ * initial values.  A scale is read as the nearest number in [2^-60, 2^60]
+ * (NaN as 2^-60).
+ *
+ * fm_cache_append_rotary: a block whose first token is new gets the least
+ * power of two (in that range) under which its new tokens' largest finite
+ * value is 448 or less; a block that has tokens keeps at least the scale that
+ * it had, and where that grows its codes are rounded to the new one.  Values
+ * go to the nearest code (ties to even), those past 448 times the scale,
+ * infinities among them, to the largest; NaN stays NaN.  The keys are rounded
+ * once, after their rotation.
+ *
+ * fm_tree_fwd_fp8: as fm_tree_fwd (workspace, masks, split and order
+ * included), over the values that the codes stand for.  A NaN code reaches
+ * the rows that see its key, and no other.
+ *
+ * fm_cache_accept_fp8: as fm_cache_accept.  A block that accepted nodes come to
+ * gets the largest of its own scale and those of the blocks that they come
+ * from, and its codes are rounded to that one where it is larger than theirs.
+ *
+ * fm_pages_reserve_fp8, fm_pages_compact_fp8: as fm_pages_reserve and
+ * fm_pages_compact; a page's scales move with its codes.  (fm_pages_fork
+ * touches no pool and serves both.) */
+#define FM_SCALE_BLOCK 16
+fm_status fm_tree_fwd_fp8(const fm_cache* cache, const fm_tree_desc* desc, const void* q,
+                          const void* k_pool, const void* v_pool, const float* k_scale,
+                          const float* v_scale, const int32_t* table, const int32_t* lens,
+                          const int32_t* cu, const int32_t* parents, float scale, void* o, float* lse,
+                          void* ws, size_t ws_bytes, int32_t* status, void* stream);
+fm_status fm_cache_accept_fp8(const fm_cache* cache, const int32_t* accept, int max_accept,
+                              const int32_t* n_accept, const int32_t* cu, void* k_pool, void* v_pool,
+                              float* k_scale, float* v_scale, const int32_t* table,
+                              const int32_t* lens, int32_t* lens_out, int32_t* ref, int32_t* status,
+                              void* stream);
+fm_status fm_pages_reserve_fp8(const fm_cache* cache, const int32_t* grow, void* k_pool, void* v_pool,
+                               float* k_scale, float* v_scale, const int32_t* table,
+                               const int32_t* lens, const int32_t* ref, int32_t* table_out,
+                               int32_t* lens_out, int32_t* ref_out, int32_t* info, void* ws,
+                               size_t ws_bytes, int32_t* status, void* stream);
+fm_status fm_pages_compact_fp8(const fm_cache* cache, void* k_pool, void* v_pool, float* k_scale,
+                               float* v_scale, const int32_t* table, const int32_t* lens,
+                               const int32_t* ref, int32_t* table_out, int32_t* ref_out,
+                               int32_t* n_live, void* ws, size_t ws_bytes, int32_t* status,
+                               void* stream);
+
 /* Kernel timing, for benchmarks.  While enabled, every kernel the library
  * launches is bracketed by a pair of CUDA events recorded on its own stream
  * (event objects are created on first use and reused; no device memory is
@@ -445,8 +531,8 @@ fm_status fm_pages_compact(const fm_cache* cache, void* k_pool, void* v_pool, co
  * 3 localize, 4 forward, 5 backward preprocess, 6 backward dK/dV, 7 backward
  * dQ, 8 partial-tile visibility masks, 9 FP8 quantisation, 10 FP8 forward,
  * 11 cache append, 12 tree attention, 13 its joining of split rows, 14 cache
- * accept, 15 page fork, 16 page plan (reserve and compact), 17 page copies;
- * fm_kernel_name(id) names them.  At most 65536 launches are recorded per
+ * accept, 15 page fork, 16 page plan (reserve and compact), 17 page copies,
+ * 18 append with rotation; fm_kernel_name(id) names them.  At most 65536 launches are recorded per
  * read; later launches are counted but not timed. */
 fm_status fm_profile_enable(int on);
 fm_status fm_profile_read(double* total_ms, int* launches, int n);

@@ -13,9 +13,10 @@ aligned storage such as torch's own allocations, take the kernels' faster
 LTS, LTE, UTS, UTE; key j is hidden from query row i iff LTS[j] <= i < LTE[j]
 or UTS[j] <= i < UTE[j].
 
-For serving, ``cache.py`` has the paged K/V cache: appending tokens, attention
-of single tokens, causal runs and drafted trees over it, and its pages'
-bookkeeping.
+For serving, ``cache.py`` has the paged K/V cache, of bf16 or of e4m3 codes with
+scales: appending tokens (with keys and queries rotated by position on the
+way), attention of single tokens, causal runs and drafted trees over it, and
+its pages' bookkeeping.
 """
 from __future__ import annotations
 
@@ -25,12 +26,13 @@ from typing import NamedTuple
 import torch
 
 from ._abi import FMError, FmDesc, FmWsLayout, check, lib  # noqa: F401
-from .cache import (cache_accept, cache_append, make_cache, pages_compact,  # noqa: F401
-                    pages_fork, pages_reserve, pages_workspace, tree_forward, tree_workspace)
+from .cache import (cache_accept, cache_append, cache_append_rotary, cache_scales,  # noqa: F401
+                    make_cache, pages_compact, pages_fork, pages_reserve, pages_workspace,
+                    tree_forward, tree_workspace)
 
 __all__ = ["FMError", "make_desc", "workspace_size", "workspace_layout", "workspace", "plan",
            "forward", "backward", "localize", "device_status", "lib", "profile_enable",
-           "profile_read", "make_cache", "cache_append", "tree_forward", "tree_workspace",
+           "profile_read", "make_cache", "cache_scales", "cache_append", "cache_append_rotary", "tree_forward", "tree_workspace",
            "cache_accept", "pages_fork", "pages_reserve", "pages_compact", "pages_workspace"]
 
 

@@ -46,6 +46,13 @@ class FmTreeDesc(ctypes.Structure):
                 ("q_stride", ctypes.c_int64 * 2), ("o_stride", ctypes.c_int64 * 2)]
 
 
+class FmRotary(ctypes.Structure):
+    _fields_ = [("rot", ctypes.c_int), ("interleaved", ctypes.c_int), ("freqs", ctypes.c_void_p),
+                ("positions", ctypes.c_void_p), ("H", ctypes.c_int), ("q", ctypes.c_void_p),
+                ("q_out", ctypes.c_void_p), ("q_stride", ctypes.c_int64 * 2),
+                ("o_stride", ctypes.c_int64 * 2)]
+
+
 class FMError(RuntimeError):
     """A non-OK status returned by the library."""
 
@@ -98,6 +105,17 @@ SIGNATURES = {
                                         I32P, I32P, I32P, P, ctypes.c_size_t, P, P]),
     "fm_pages_compact": (ctypes.c_int, [ctypes.POINTER(FmCache), P, P, I32P, I32P, I32P, I32P, I32P,
                                         I32P, P, ctypes.c_size_t, P, P]),
+    "fm_cache_append_rotary": (ctypes.c_int, [ctypes.POINTER(FmCache), ctypes.POINTER(FmRotary), P, P, P,
+                                              P, I32P, ctypes.c_int, P, P, P, P, I32P, I32P, P, P]),
+    "fm_tree_fwd_fp8": (ctypes.c_int, [ctypes.POINTER(FmCache), ctypes.POINTER(FmTreeDesc), P, P, P, P, P,
+                                       I32P, I32P, I32P, I32P, ctypes.c_float, P, P, P, ctypes.c_size_t,
+                                       P, P]),
+    "fm_cache_accept_fp8": (ctypes.c_int, [ctypes.POINTER(FmCache), I32P, ctypes.c_int, I32P, I32P, P, P,
+                                           P, P, I32P, I32P, I32P, I32P, P, P]),
+    "fm_pages_reserve_fp8": (ctypes.c_int, [ctypes.POINTER(FmCache), I32P, P, P, P, P, I32P, I32P, I32P,
+                                            I32P, I32P, I32P, I32P, P, ctypes.c_size_t, P, P]),
+    "fm_pages_compact_fp8": (ctypes.c_int, [ctypes.POINTER(FmCache), P, P, P, P, I32P, I32P, I32P, I32P,
+                                            I32P, I32P, P, ctypes.c_size_t, P, P]),
     "fm_device_status": (ctypes.c_int, [P, P]),
     "fm_test_hooks": (ctypes.c_int, [ctypes.c_uint64, ctypes.c_int]),
     "fm_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -108,7 +126,7 @@ SIGNATURES = {
     "fm_measure_exp2_rate": (ctypes.c_int, [P, P]),
 }
 
-KERNEL_IDS = 18
+KERNEL_IDS = 19
 
 
 def lib():

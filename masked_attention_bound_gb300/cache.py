@@ -1,9 +1,15 @@
 """The paged K/V cache: the ``fm_cache_*``, ``fm_tree_*`` and ``fm_pages_*``
 entry points of ``include/fm.h`` on torch tensors.
 
-Pools are bf16 CUDA tensors [pages][page_size][Hkv][d] of one layer, or
+Pools are CUDA tensors [pages][page_size][Hkv][d] of one layer, or
 [layers][pages][page_size][Hkv][d]; page_size is 16, 32, 64 or 128, d 64 or
-128, d is contiguous and the other strides are multiples of 8 elements.
+128, d is contiguous.  They hold bf16, with the other strides multiples of 8
+elements, or e4m3 codes (torch.float8_e4m3fn, strides multiples of 16).  A
+cache of codes comes with ``k_scale`` and ``v_scale``, contiguous fp32 tensors
+[pages][Hkv][page_size / 16] (with the layers in front where the pools have
+them; ``cache_scales`` makes them): a value is its code times the scale of its
+block of 16 tokens and head.  It takes half the bytes, and attention over it,
+bound by reading them, about half the time.
 ``table`` [B][max_pages], ``lens`` [B], ``ref`` [pages], ``cu`` [B + 1],
 ``parents`` [total] and the other index arrays are contiguous int32 tensors on
 the pools' device.
@@ -11,7 +17,9 @@ the pools' device.
 A step of a model that drafts trees:
 
     pages_reserve(n, k, v, table, lens, ref)          # room for n[b] nodes each
-    cache_append(k_new, v_new, cu, k[layer], v[layer], table, lens)     # per layer
+    cache_append(k_new, v_new, cu, k[layer], v[layer], table, lens)     # per layer, or with
+    q = cache_append_rotary(q, k_new, v_new, cu, freqs, k[layer], v[layer], table, lens,
+                            positions=context_and_depth)                # rotated by position
     o, lse = tree_forward(q, k[layer], v[layer], table, lens, cu, scale, parents=parents,
                           max_nodes=64)               # no sequence has more
     lens = cache_accept(accept, n_accept, cu, k, v, table, lens, ref=ref)  # after verification
@@ -36,6 +44,8 @@ import torch
 
 from ._abi import FmCache, FmTreeDesc, lib
 
+SCALE_BLOCK = 16          # tokens of a head that share a scale in a cache of codes
+
 _module = None
 
 
@@ -56,7 +66,7 @@ def _call(name, stream, *args):
     m = _module or _load()
     if stream is None:
         return getattr(m, name)(*args)
-    if stream.device != args[0].device:
+    if stream.device != next(a.device for a in args if isinstance(a, torch.Tensor)):
         raise ValueError("stream must belong to the tensors' device")
     with torch.cuda.stream(stream):        # memory that the call allocates belongs to it too
         return getattr(m, name)(*args)
@@ -68,8 +78,8 @@ def make_cache(k_pool, v_pool, table) -> FmCache:
         raise ValueError("pools must have one shape, [layers][pages][page_size][Hkv][d] or "
                          "[pages][page_size][Hkv][d], and the page table two dimensions")
     for t in (k_pool, v_pool):
-        if t.dtype is not torch.bfloat16 or not t.is_cuda or t.device != table.device:
-            raise ValueError("pools must be bf16 CUDA tensors on the page table's device")
+        if t.dtype not in (torch.bfloat16, torch.float8_e4m3fn) or not t.is_cuda or t.device != table.device:
+            raise ValueError("pools must be bf16 or float8_e4m3fn CUDA tensors on the page table's device")
         if t.stride(-1) != 1:
             raise ValueError("head_dim must be the contiguous dimension")
     if max(*k_pool.shape, *table.shape) >= 1 << 31:
@@ -80,15 +90,40 @@ def make_cache(k_pool, v_pool, table) -> FmCache:
     C.n_pages, C.page_size, C.Hkv, C.d = k_pool.shape[-4:]
     for to, t in ((C.k_stride, k_pool), (C.v_stride, v_pool)):
         # a dimension of one element is never stepped along
-        s = [8 if n == 1 else x for n, x in zip(t.shape[:-1], t.stride()[:-1])]
-        to[:] = s if t.dim() == 5 else [8, *s]
+        s = [16 if n == 1 else x for n, x in zip(t.shape[:-1], t.stride()[:-1])]
+        to[:] = s if t.dim() == 5 else [16, *s]
     return C
 
 
-def cache_append(k, v, cu, k_pool, v_pool, table, lens, status=None, stream=None):
+def cache_scales(pool) -> torch.Tensor:
+    """Scales of a pool of e4m3 codes, one for each block of 16 tokens of a head, all 1.
+    (Appending gives a block its scale; the initial values have no part in a result.)"""
+    if pool.dim() not in (4, 5) or pool.shape[-3] % SCALE_BLOCK:
+        raise ValueError("a pool has the shape [layers][pages][page_size][Hkv][d] or [pages][page_size][Hkv][d]")
+    *front, page_size, heads, _ = pool.shape
+    return torch.ones(*front, heads, page_size // SCALE_BLOCK, dtype=torch.float32, device=pool.device)
+
+
+def cache_append(k, v, cu, k_pool, v_pool, table, lens, status=None, stream=None, k_scale=None,
+                 v_scale=None):
     """Write new tokens' K and V ([total][Hkv][d], packed by ``cu``) to one layer's
-    pools: sequence b's are its last cu[b + 1] - cu[b] of lens[b] cached tokens."""
-    _call("append", stream, k, v, cu, k_pool, v_pool, table, lens, status)
+    pools: sequence b's are its last cu[b + 1] - cu[b] of lens[b] cached tokens.  With pools of
+    codes (``k_scale``, ``v_scale``) a block that begins with a new token gets the least power of
+    two as its scale that brings its largest value to 448 or less; one that has tokens keeps at
+    least its scale, and its codes are rounded again where that grows."""
+    _call("append", stream, k, v, cu, k_pool, v_pool, table, lens, k_scale, v_scale, status)
+
+
+def cache_append_rotary(q, k, v, cu, freqs, k_pool, v_pool, table, lens, positions=None,
+                        interleaved=False, q_out=None, k_scale=None, v_scale=None, status=None,
+                        stream=None):
+    """``cache_append`` with keys and queries rotated by their position on the way: element pair i
+    of a head's first 2 n, n = len(freqs) (a multiple of 8), turns by position * freqs[i] radians.  Pairs
+    are (x[i], x[i + n]), or neighbours with ``interleaved``.  ``positions`` [total]: by default
+    a token's place in its sequence; a drafted node has context + depth.  Returns the rotated queries
+    [total][H][d] (``q_out``, which may be ``q``), or None where ``q`` is None."""
+    return _call("append_rotary", stream, q, k, v, cu, freqs, k_pool, v_pool, table, lens, positions,
+                 interleaved, q_out, k_scale, v_scale, status)
 
 
 def tree_workspace(q, k_pool, v_pool, table, max_nodes=None) -> torch.Tensor:
@@ -107,7 +142,7 @@ def tree_workspace(q, k_pool, v_pool, table, max_nodes=None) -> torch.Tensor:
 
 
 def tree_forward(q, k_pool, v_pool, table, lens, cu, scale, parents=None, max_nodes=None, o=None,
-                 lse=None, ws=None, status=None, stream=None):
+                 lse=None, ws=None, status=None, stream=None, k_scale=None, v_scale=None):
     """Attention of packed query tokens over one layer's cache: O [total][H][d] bf16 and
     LSE [H][total] fp32.  Sequence b's cu[b + 1] - cu[b] query tokens are the last of its
     lens[b] cached tokens.  ``parents`` [total]: the drafted tree (the node's parent within
@@ -118,16 +153,17 @@ def tree_forward(q, k_pool, v_pool, table, lens, cu, scale, parents=None, max_no
     per K/V head: 31 us with 1, 60 with the default, which plans for 128 tokens a sequence; over
     up to 8192 tokens 481 and 493)."""
     return _call("tree", stream, q, k_pool, v_pool, table, lens, cu, scale, parents, max_nodes, o, lse,
-                 ws, status)
+                 ws, k_scale, v_scale, status)
 
 
 def cache_accept(accept, n_accept, cu, k_pool, v_pool, table, lens, lens_out=None, ref=None,
-                 status=None, stream=None):
+                 status=None, stream=None, k_scale=None, v_scale=None):
     """Keep the accepted nodes of each sequence's tree: node accept[b][i] (ascending, the first
     n_accept[b] count) moves to the i-th place after the context, in all layers.  With ``ref``
     the pages past a row's new length lose its hold.  Returns the new lengths (``lens_out``,
     which may not be ``lens``)."""
-    return _call("accept", stream, accept, n_accept, cu, k_pool, v_pool, table, lens, lens_out, ref, status)
+    return _call("accept", stream, accept, n_accept, cu, k_pool, v_pool, table, lens, lens_out, ref, k_scale,
+                 v_scale, status)
 
 
 def pages_fork(parent, page_size, table, lens, ref, table_out=None, lens_out=None, ref_out=None,
@@ -148,17 +184,18 @@ def pages_workspace(k_pool, v_pool, table) -> torch.Tensor:
 
 
 def pages_reserve(grow, k_pool, v_pool, table, lens, ref, table_out=None, lens_out=None,
-                  ref_out=None, info=None, ws=None, status=None, stream=None):
+                  ref_out=None, info=None, ws=None, status=None, stream=None, k_scale=None, v_scale=None):
     """Room for grow[b] more tokens of every row, in place by default: free pages in ascending
     order, and a copy of a shared last page that the row will write.  All or nothing.  Returns
     ``info``: int32 [2], free pages after the call and pages asked for (more than were free:
     nothing was done)."""
     return _call("reserve", stream, grow, k_pool, v_pool, table, lens, ref, table_out, lens_out, ref_out,
-                 info, ws, status)
+                 info, ws, k_scale, v_scale, status)
 
 
 def pages_compact(k_pool, v_pool, table, lens, ref, table_out=None, ref_out=None, n_live=None,
-                  ws=None, status=None, stream=None):
+                  ws=None, status=None, stream=None, k_scale=None, v_scale=None):
     """Move the held pages to the front of the pool, [0, n_live), in place by default.  Returns
     ``n_live``: int32 [1]."""
-    return _call("compact", stream, k_pool, v_pool, table, lens, ref, table_out, ref_out, n_live, ws, status)
+    return _call("compact", stream, k_pool, v_pool, table, lens, ref, table_out, ref_out, n_live, ws, k_scale,
+                 v_scale, status)

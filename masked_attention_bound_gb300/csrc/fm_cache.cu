@@ -40,11 +40,14 @@ namespace {
 struct Pools {
   uint4* p[2];          // K, V
   int64_t layer[2], page[2], slot[2], head[2];
-  int chunk_shift;      // vectors per head (d / 8) as a power of two
+  int chunk_shift;      // vectors per head (d / 8, of codes d / 16) as a power of two
   int row;              // vectors of one token, K or V
   int page_shift;       // page_size as a power of two
   FastDiv by_row;
   bool linear[2];       // a page's tokens lie one after the other without gaps
+  float* scale[2];      // of a cache of codes, [layers][pages][Hkv][blocks of a page]; null: bf16
+  int64_t scale_layer;  // scales of a layer
+  int scale_page, block_shift;   // of a page; log2 of its blocks
   __device__ __forceinline__ int page_size() const { return 1 << page_shift; }
   // place of vector r of a token: head r >> chunk_shift
   __device__ __forceinline__ int64_t in_token(int kv, int r) const {
@@ -52,19 +55,26 @@ struct Pools {
   }
 };
 
-Pools pools_of(const fm_cache& c, void* k, void* v) {
+// k_scale, v_scale: of a cache of e4m3 codes
+Pools pools_of(const fm_cache& c, void* k, void* v, float* k_scale = nullptr, float* v_scale = nullptr) {
   Pools P;
+  const int unit = k_scale ? 16 : 8;     // elements of a vector
+  P.scale[0] = k_scale;
+  P.scale[1] = v_scale;
+  P.block_shift = page_shift(c.page_size) - 4;
+  P.scale_page = c.Hkv << P.block_shift;
+  P.scale_layer = static_cast<int64_t>(c.n_pages) * P.scale_page;
   P.p[0] = static_cast<uint4*>(k);
   P.p[1] = static_cast<uint4*>(v);
   const int64_t* st[2] = {c.k_stride, c.v_stride};
   for (int t = 0; t < 2; ++t) {
-    P.layer[t] = st[t][0] / 8;
-    P.page[t] = st[t][1] / 8;
-    P.slot[t] = st[t][2] / 8;
-    P.head[t] = st[t][3] / 8;
-    P.linear[t] = (c.Hkv == 1 || P.head[t] == c.d / 8) && P.slot[t] == c.Hkv * (c.d / 8);
+    P.layer[t] = st[t][0] / unit;
+    P.page[t] = st[t][1] / unit;
+    P.slot[t] = st[t][2] / unit;
+    P.head[t] = st[t][3] / unit;
+    P.linear[t] = (c.Hkv == 1 || P.head[t] == c.d / unit) && P.slot[t] == c.Hkv * (c.d / unit);
   }
-  P.chunk_shift = c.d == 64 ? 3 : 4;
+  P.chunk_shift = (c.d == 64 ? 3 : 4) - (k_scale ? 1 : 0);
   P.row = c.Hkv << P.chunk_shift;
   P.by_row = FastDiv::of(P.row);
   P.page_shift = page_shift(c.page_size);
@@ -682,6 +692,13 @@ __device__ __forceinline__ void copy_page(const Pools& P, int kv, int layer, int
     for (int u = 0; u < U; ++u)
       if (v0 + u * kCopyThreads < all) __stcs(to + at[u], x[u]);
   }
+  if (P.scale[kv]) {
+    // the scales of the blocks that hold these tokens
+    float* s = P.scale[kv] + layer * P.scale_layer;
+    for (int i = threadIdx.x; i < P.scale_page; i += kCopyThreads)
+      if ((i & ((1 << P.block_shift) - 1)) * 16 < n)
+        s[static_cast<int64_t>(dst) * P.scale_page + i] = s[static_cast<int64_t>(src) * P.scale_page + i];
+  }
 }
 
 __global__ void __launch_bounds__(kCopyThreads)
@@ -742,6 +759,66 @@ bool outputs_apart(const fm_cache& c, const PageArgs& A) {
 bool few_pages(const fm_cache& c) { return c.n_pages <= 4096 && c.B <= 64; }
 
 int copy_grid() { return num_sms() * 16; }
+
+// k_scale, v_scale: of a cache of e4m3 codes; both null with a cache of bf16.
+fm_status reserve_pages(const fm_cache* c, const int32_t* grow, void* k_pool, void* v_pool, float* k_scale,
+                        float* v_scale, const int32_t* table, const int32_t* lens, const int32_t* ref,
+                        int32_t* table_out, int32_t* lens_out, int32_t* ref_out, int32_t* info, void* ws,
+                        size_t ws_bytes, int32_t* status, void* stream) {
+  fm_status st = check_cache(c, true);
+  if (st != FM_OK) return st;
+  if (!grow || !table || !lens || !ref || !table_out || !lens_out || !ref_out || !info)
+    return FM_ERR_INVALID;
+  if (!aligned_to(k_pool, 16) || !aligned_to(v_pool, 16)) return FM_ERR_INVALID;
+  PageArgs A{table, lens, ref, table_out, lens_out, ref_out, status, c->B, c->page_size, c->n_pages,
+             c->max_pages};
+  if (!outputs_apart(*c, A)) return FM_ERR_INVALID;
+  if (!aligned_to(ws, 256)) return FM_ERR_WORKSPACE;
+  const PlanWs W = plan_ws(*c, ws);
+  if (ws_bytes < W.bytes) return FM_ERR_WORKSPACE;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  prof_begin(K_PAGES_PLAN, s);
+  cudaError_t e = few_pages(*c)
+                      ? launch_dependent(reserve_kernel<1>, dim3(1), kPlanThreads, 0, s, A, grow, W, info)
+                      : launch_dependent(reserve_kernel<8>, dim3(8), kPlanThreads, 0, s, A, grow, W, info);
+  prof_end(K_PAGES_PLAN, s);
+  if (e != cudaSuccess) return FM_ERR_CUDA;
+  const int64_t items = static_cast<int64_t>(c->B) * c->layers * 2;
+  prof_begin(K_PAGES_COPY, s);
+  e =
+      launch_dependent(reserve_copy_kernel, dim3(items < copy_grid() ? static_cast<int>(items) : copy_grid()),
+                       kCopyThreads, 0, s, pools_of(*c, k_pool, v_pool, k_scale, v_scale), W.copy, c->B, c->layers);
+  prof_end(K_PAGES_COPY, s);
+  return done(e);
+}
+
+fm_status compact_pages(const fm_cache* c, void* k_pool, void* v_pool, float* k_scale, float* v_scale,
+                        const int32_t* table, const int32_t* lens, const int32_t* ref, int32_t* table_out,
+                        int32_t* ref_out, int32_t* n_live, void* ws, size_t ws_bytes, int32_t* status,
+                        void* stream) {
+  fm_status st = check_cache(c, true);
+  if (st != FM_OK) return st;
+  if (!table || !lens || !ref || !table_out || !ref_out || !n_live) return FM_ERR_INVALID;
+  if (!aligned_to(k_pool, 16) || !aligned_to(v_pool, 16)) return FM_ERR_INVALID;
+  PageArgs A{table, lens, ref, table_out, nullptr, ref_out, status, c->B, c->page_size, c->n_pages,
+             c->max_pages};
+  if (!outputs_apart(*c, A)) return FM_ERR_INVALID;
+  if (!aligned_to(ws, 256)) return FM_ERR_WORKSPACE;
+  const PlanWs W = plan_ws(*c, ws);
+  if (ws_bytes < W.bytes) return FM_ERR_WORKSPACE;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  prof_begin(K_PAGES_PLAN, s);
+  cudaError_t e = few_pages(*c)
+                      ? launch_dependent(compact_kernel<1>, dim3(1), kPlanThreads, 0, s, A, W, n_live)
+                      : launch_dependent(compact_kernel<8>, dim3(8), kPlanThreads, 0, s, A, W, n_live);
+  prof_end(K_PAGES_PLAN, s);
+  if (e != cudaSuccess) return FM_ERR_CUDA;
+  prof_begin(K_PAGES_COPY, s);
+  e = launch_dependent(compact_copy_kernel, dim3(copy_grid()), kCopyThreads, 0, s,
+                                         pools_of(*c, k_pool, v_pool, k_scale, v_scale), A, W, c->layers);
+  prof_end(K_PAGES_COPY, s);
+  return done(e);
+}
 
 }  // namespace
 }  // namespace fm
@@ -842,59 +919,36 @@ fm_status fm_pages_reserve(const fm_cache* c, const int32_t* grow, void* k_pool,
                            const int32_t* table, const int32_t* lens, const int32_t* ref,
                            int32_t* table_out, int32_t* lens_out, int32_t* ref_out, int32_t* info,
                            void* ws, size_t ws_bytes, int32_t* status, void* stream) {
-  fm_status st = check_cache(c, true);
+  return reserve_pages(c, grow, k_pool, v_pool, nullptr, nullptr, table, lens, ref, table_out, lens_out,
+                       ref_out, info, ws, ws_bytes, status, stream);
+}
+
+fm_status fm_pages_reserve_fp8(const fm_cache* c, const int32_t* grow, void* k_pool, void* v_pool,
+                               float* k_scale, float* v_scale, const int32_t* table, const int32_t* lens,
+                               const int32_t* ref, int32_t* table_out, int32_t* lens_out, int32_t* ref_out,
+                               int32_t* info, void* ws, size_t ws_bytes, int32_t* status, void* stream) {
+  const fm_status st = check_cache8(c, k_pool, v_pool, k_scale, v_scale);
   if (st != FM_OK) return st;
-  if (!grow || !table || !lens || !ref || !table_out || !lens_out || !ref_out || !info)
-    return FM_ERR_INVALID;
-  if (!aligned_to(k_pool, 16) || !aligned_to(v_pool, 16)) return FM_ERR_INVALID;
-  PageArgs A{table, lens, ref, table_out, lens_out, ref_out, status, c->B, c->page_size, c->n_pages,
-             c->max_pages};
-  if (!outputs_apart(*c, A)) return FM_ERR_INVALID;
-  if (!aligned_to(ws, 256)) return FM_ERR_WORKSPACE;
-  const PlanWs W = plan_ws(*c, ws);
-  if (ws_bytes < W.bytes) return FM_ERR_WORKSPACE;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  prof_begin(K_PAGES_PLAN, s);
-  cudaError_t e = few_pages(*c)
-                      ? launch_dependent(reserve_kernel<1>, dim3(1), kPlanThreads, 0, s, A, grow, W, info)
-                      : launch_dependent(reserve_kernel<8>, dim3(8), kPlanThreads, 0, s, A, grow, W, info);
-  prof_end(K_PAGES_PLAN, s);
-  if (e != cudaSuccess) return FM_ERR_CUDA;
-  const int64_t items = static_cast<int64_t>(c->B) * c->layers * 2;
-  prof_begin(K_PAGES_COPY, s);
-  e =
-      launch_dependent(reserve_copy_kernel, dim3(items < copy_grid() ? static_cast<int>(items) : copy_grid()),
-                       kCopyThreads, 0, s, pools_of(*c, k_pool, v_pool), W.copy, c->B, c->layers);
-  prof_end(K_PAGES_COPY, s);
-  return done(e);
+  return reserve_pages(c, grow, k_pool, v_pool, k_scale, v_scale, table, lens, ref, table_out, lens_out,
+                       ref_out, info, ws, ws_bytes, status, stream);
 }
 
 fm_status fm_pages_compact(const fm_cache* c, void* k_pool, void* v_pool, const int32_t* table,
                            const int32_t* lens, const int32_t* ref, int32_t* table_out,
                            int32_t* ref_out, int32_t* n_live, void* ws, size_t ws_bytes,
                            int32_t* status, void* stream) {
-  fm_status st = check_cache(c, true);
+  return compact_pages(c, k_pool, v_pool, nullptr, nullptr, table, lens, ref, table_out, ref_out, n_live, ws,
+                       ws_bytes, status, stream);
+}
+
+fm_status fm_pages_compact_fp8(const fm_cache* c, void* k_pool, void* v_pool, float* k_scale,
+                               float* v_scale, const int32_t* table, const int32_t* lens,
+                               const int32_t* ref, int32_t* table_out, int32_t* ref_out, int32_t* n_live,
+                               void* ws, size_t ws_bytes, int32_t* status, void* stream) {
+  const fm_status st = check_cache8(c, k_pool, v_pool, k_scale, v_scale);
   if (st != FM_OK) return st;
-  if (!table || !lens || !ref || !table_out || !ref_out || !n_live) return FM_ERR_INVALID;
-  if (!aligned_to(k_pool, 16) || !aligned_to(v_pool, 16)) return FM_ERR_INVALID;
-  PageArgs A{table, lens, ref, table_out, nullptr, ref_out, status, c->B, c->page_size, c->n_pages,
-             c->max_pages};
-  if (!outputs_apart(*c, A)) return FM_ERR_INVALID;
-  if (!aligned_to(ws, 256)) return FM_ERR_WORKSPACE;
-  const PlanWs W = plan_ws(*c, ws);
-  if (ws_bytes < W.bytes) return FM_ERR_WORKSPACE;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  prof_begin(K_PAGES_PLAN, s);
-  cudaError_t e = few_pages(*c)
-                      ? launch_dependent(compact_kernel<1>, dim3(1), kPlanThreads, 0, s, A, W, n_live)
-                      : launch_dependent(compact_kernel<8>, dim3(8), kPlanThreads, 0, s, A, W, n_live);
-  prof_end(K_PAGES_PLAN, s);
-  if (e != cudaSuccess) return FM_ERR_CUDA;
-  prof_begin(K_PAGES_COPY, s);
-  e = launch_dependent(compact_copy_kernel, dim3(copy_grid()), kCopyThreads, 0, s,
-                                         pools_of(*c, k_pool, v_pool), A, W, c->layers);
-  prof_end(K_PAGES_COPY, s);
-  return done(e);
+  return compact_pages(c, k_pool, v_pool, k_scale, v_scale, table, lens, ref, table_out, ref_out, n_live, ws,
+                       ws_bytes, status, stream);
 }
 
 }  // extern "C"

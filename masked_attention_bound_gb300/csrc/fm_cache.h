@@ -12,6 +12,9 @@ constexpr int kMaxHeads = 65535;
 
 // Sizes of `c` that every cache entry point needs; `pools`: its pools' too.
 fm_status check_cache(const fm_cache* c, bool pools);
+// The same of a cache of e4m3 codes, and its pools and scales.
+fm_status check_cache8(const fm_cache* c, const void* k_pool, const void* v_pool, const void* k_scale,
+                       const void* v_scale);
 
 inline int page_shift(int page_size) {
   return page_size == 16 ? 4 : page_size == 32 ? 5 : page_size == 64 ? 6 : 7;

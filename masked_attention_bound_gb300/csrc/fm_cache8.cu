@@ -1,0 +1,574 @@
+// Appending with the position rotation, to a cache of bf16 or of e4m3 codes,
+// and keeping the accepted nodes of a tree in a cache of e4m3 codes.
+//
+// A cache of codes holds, for every 16 tokens of a head (a block), 16 * d
+// codes and one scale; a value is code * scale.
+#include <cuda_bf16.h>
+
+#include "fm_cache.h"
+#include "fm_fp8.cuh"
+
+namespace fm {
+namespace {
+
+__device__ __forceinline__ void flag(int* status, int bit) {
+  if (status) atomicOr(status, bit);
+}
+
+// Context length of packed sequence b (tokens before its new ones), or -1 if
+// its lens or cu entries are out of range; n: its new tokens.
+__device__ __forceinline__ int context_of(const int32_t* lens, const int32_t* cu, int b, int total,
+                                          int max_tokens, int& n) {
+  const int c0 = cu[b], c1 = cu[b + 1], len = lens[b];
+  n = c1 - c0;
+  if (c0 < 0 || c1 < c0 || c1 > total || len > max_tokens || len < n) return -1;
+  return len - n;
+}
+
+// K or V: its new tokens, its pool (16-byte vectors' units: elements) and scales.
+struct Side {
+  const __nv_bfloat16* src;
+  int64_t tok, head;                     // of src, in elements
+  void* pool;
+  int64_t page, slot, phead;             // of the pool, in elements
+  float* scale;                          // null: the pool holds bf16
+};
+
+// ------------------------------------------------------------------ angles
+// The angle of position p at frequency f (radians a position) is p f mod 2
+// pi.  It is kept as a 64-bit fraction of a turn: f / 2 pi is rounded to 64
+// bits once, and the product with p wraps around like the angle does, exactly
+// (2^30 positions on, 2^-34 of a turn is left).  cos and sin come from their
+// Taylor series on an eighth of a turn to either side of a quarter's multiple,
+// each as a sum of two floats, the first of 16 bits: its product with a bf16
+// number is exact, so a rotated value has two roundings to 24 bits.
+struct Turn {
+  float c1, c2, s1, s2;                  // cos = c1 + c2, sin = s1 + s2
+};
+
+__device__ __forceinline__ uint64_t turn_step(float f) {
+  constexpr double kHi = 0.15915494309189535, kLo = -9.839338337591243e-18;   // 1 / 2 pi
+  const double t = f * kHi, low = fma(static_cast<double>(f), kHi, -t) + f * kLo;
+  return static_cast<uint64_t>((t - floor(t)) * 0x1p64) + static_cast<uint64_t>(static_cast<int64_t>(low * 0x1p64));
+}
+
+__device__ __forceinline__ Turn turn_of(int64_t pos, uint64_t step) {
+  const uint64_t x = static_cast<uint64_t>(pos) * step + (1ull << 61);
+  const int quarter = static_cast<int>(x >> 62);
+  const int64_t r = static_cast<int64_t>(x & ((1ull << 62) - 1)) - (1ll << 61);   // of 2^64: +- 1/8
+  // angle th + tl from the first 24 bits and the next 24
+  constexpr float k1 = 9.36267597e-08f, k2 = -2.60540187e-15f;                    // 2 pi / 2^26
+  const float a = static_cast<float>(static_cast<int>(r >> 38));
+  const float b = static_cast<float>(static_cast<int>((r >> 14) & 0xffffff)) * 0x1p-24f;
+  const float u = a * k1, v = b * k1, uv = u + v, low = (u - uv) + v + fmaf(a, k1, -u) + a * k2;
+  const float th = uv + low, tl = (uv - th) + low;
+  const float zz = th * th, zt = fmaf(th, th, -zz) + 2.f * th * tl, z = zz + zt, zl = (zz - z) + zt;
+  // cos = 1 - z / 2 + z^2 / 24 - ...
+  float y = fmaf(z, 2.08767559e-9f, -2.755732e-7f);
+  y = fmaf(z, y, 2.48015876e-5f);
+  y = fmaf(z, y, -1.38888892e-3f);
+  y = fmaf(z, y, 4.16666679e-2f) * z * z;
+  const float ch = fmaf(-0.5f, z, 1.f);
+  const float cl = fmaf(-0.5f, z, 1.f - ch) + fmaf(-0.5f, zl, y);
+  // sin = t - t z / 6 + t z^2 / 120 - ...
+  y = fmaf(z, -2.50521079e-8f, 2.75573188e-6f);
+  y = fmaf(z, y, -1.98412701e-4f);
+  y = fmaf(z, y, 8.33333377e-3f) * z * z;
+  constexpr float k6 = -0.166666672f, k6l = 4.96705373e-9f;                        // -1/6
+  const float m = z * k6, ml = fmaf(z, k6, -m) + fmaf(z, k6l, zl * k6);
+  const float p = th * m, pl = fmaf(th, m, -p);
+  const float sh = th + p;
+  const float sl = (th - sh) + p + pl + fmaf(th, ml + y, tl * fmaf(-0.5f, z, 1.f));
+  auto head = [](float v) { return __uint_as_float(__float_as_uint(v) & 0xffffff00u); };
+  float c1 = head(ch), s1 = head(sh);
+  float c2 = (ch - c1) + cl, s2 = (sh - s1) + sl;
+  if (quarter & 1) {
+    const float t1 = c1, t2 = c2;
+    c1 = -s1; c2 = -s2;
+    s1 = t1; s2 = t2;
+  }
+  if (quarter & 2) {
+    c1 = -c1; c2 = -c2;
+    s1 = -s1; s2 = -s2;
+  }
+  return Turn{c1, c2, s1, s2};
+}
+
+__device__ __forceinline__ void turn_pair(float& a, float& b, const Turn& t) {
+  const float x = fmaf(a, t.c1, fmaf(-b, t.s1, fmaf(a, t.c2, -b * t.s2)));
+  b = fmaf(a, t.s1, fmaf(b, t.c1, fmaf(a, t.s2, b * t.c2)));
+  a = x;
+}
+
+// ------------------------------------------------------------------ append
+// The unit of work is a block: 16 tokens of the cache that share a scale, all
+// heads.  Sequence b's blocks are numbered from cu[b] / 16 + 2 b on, which
+// leaves each sequence room enough wherever its first token lies in a block;
+// a thread block finds its sequence by a search over cu.  The angles' table is
+// made once for all heads.  With n new tokens in the block, n d / 16 threads
+// each take 16 elements (two vectors of 8) of a token, for one head after
+// another.
+//
+// Codes: a warp has a head's new tokens of the block in registers, so that the
+// largest value is known before any is rounded, and K and V are read once.
+constexpr int kRotThreads = 256;
+
+struct RotArgs {
+  Side kv[2];
+  const __nv_bfloat16* q;
+  __nv_bfloat16* q_out;
+  int64_t q_stride[2], o_stride[2];
+  const float* freqs;
+  const int32_t *positions, *cu, *table, *lens;
+  int* status;
+  int B, total, max_pages, n_pages, page_shift;
+  int Hkv, G;                // G: query heads per K/V head (0: no queries)
+  int nrot;                  // rot / 16
+  int inter;
+};
+
+struct Vec2 {
+  uint4 a, b;
+};
+
+__device__ __forceinline__ void unpack8(const uint4& x, float* f) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(w[i] << 16);
+    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ uint4 pack8(const float* f) {
+  return make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
+}
+
+template <int D, bool CODES>
+__global__ void __launch_bounds__(kRotThreads)
+    append_rotary_kernel(const __grid_constant__ RotArgs A) {
+  constexpr int CH = D / 16;               // chunks of 16 elements of a head
+  __shared__ float4 turns[16][8][CH];      // [token][element of the chunk's eight angles][chunk]
+  grid_launch_dependents();
+  grid_dependency_wait();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int max_tokens = A.max_pages << A.page_shift;
+  if (blockIdx.x == 0 && blockIdx.y == 0) {
+    for (int b = tid; b < A.B; b += kRotThreads) {
+      int n;
+      if (context_of(A.lens, A.cu, b, A.total, max_tokens, n) < 0) flag(A.status, DEV_CACHE);
+    }
+  }
+  // the last sequence whose first block is at or before this one
+  const int me = blockIdx.x;
+  int lo = 0;
+  for (int n = A.B; n > 1;) {
+    const int step = (n + 31) >> 5;
+    const int b = lo + lane * step;
+    const unsigned below = __ballot_sync(0xffffffffu, lane * step < n && (A.cu[b] >> 4) + 2 * b <= me);
+    const int k = 31 - __clz(below | 1u);
+    lo += k * step;
+    n = min(step, n - k * step);
+  }
+  int n_new;
+  const int base = context_of(A.lens, A.cu, lo, A.total, max_tokens, n_new);
+  const int at = me - ((A.cu[lo] >> 4) + 2 * lo);
+  if (base < 0 || at < 0 || at > (n_new >> 4) + 1) return;
+  const int block = (base >> kScaleShift) + at;              // of the sequence
+  const int p0 = max(base, block << kScaleShift);            // its new tokens' places
+  const int n = min(base + n_new, (block + 1) << kScaleShift) - p0;
+  if (n <= 0) return;
+  const int t0 = A.cu[lo] + p0 - base;                       // their packed rows
+  const int first = p0 & (kScaleBlock - 1);
+  const int pg = A.table[static_cast<int64_t>(lo) * A.max_pages + (p0 >> A.page_shift)];
+  const bool in = pg >= 0 && pg < A.n_pages;
+  if (!in && tid == 0) flag(A.status, DEV_CACHE);
+  const int slot0 = p0 & ((1 << A.page_shift) - 1);
+
+  // the angles
+  if (A.nrot > 0) {
+    const int half = 8 * A.nrot, row = half <= 8 ? 8 : half <= 16 ? 16 : half <= 32 ? 32 : 64;
+    const int p = tid & (row - 1);
+    if (p < half) {
+      const float f = A.freqs[p];
+      const float poison = f - f;          // NaN where f is not finite
+      const uint64_t step = turn_step(f);
+      for (int i = tid / row; i < n; i += kRotThreads / row) {
+        const Turn t = turn_of(A.positions ? A.positions[t0 + i] : p0 + i, step);
+        turns[i][p & 7][p >> 3] = make_float4(t.c1 + poison, t.c2, t.s1 + poison, t.s2);
+      }
+    }
+    __syncthreads();
+  }
+
+  // the two vectors of chunk c, and its rotation
+  const int nrot = A.nrot;
+  const bool inter = A.inter != 0;
+  auto vec_a = [&](int c) { return inter ? 2 * c : c < nrot ? c : 2 * c; };
+  auto vec_b = [&](int c) { return inter ? 2 * c + 1 : c < nrot ? c + nrot : 2 * c + 1; };
+  auto turn_chunk = [&](float (&f)[16], int i, int c) {
+    if (c >= nrot) return;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float4 w = turns[i][e][c];
+      const Turn t{w.x, w.y, w.z, w.w};
+      if (inter) turn_pair(f[2 * e], f[2 * e + 1], t);
+      else turn_pair(f[e], f[8 + e], t);
+    }
+  };
+
+  // queries, and with a cache of bf16 K and V: heads [h0, h1) of this block
+  {
+    const int per = n * CH;
+    const int sub = tid / per, subs = kRotThreads / per;
+    const int w = tid - sub * per, i = w / CH, c = w % CH;
+    const int va = vec_a(c) * 8, vb = vec_b(c) * 8;
+    const int nq = A.G, heads = nq + (CODES ? 0 : 2);        // of one K/V head
+    if (sub < subs) {
+      const int jobs = heads * ((A.Hkv - static_cast<int>(blockIdx.y) + gridDim.y - 1) / gridDim.y);
+      for (int j = sub; j < jobs; j += subs) {
+        const int hk = blockIdx.y + j / heads * gridDim.y, x = j % heads;
+        const __nv_bfloat16* src;
+        __nv_bfloat16* dst;
+        bool rotates = true, writes = true;
+        if (x < nq) {
+          const int h = hk * nq + x;
+          src = A.q + (t0 + i) * A.q_stride[0] + h * A.q_stride[1];
+          dst = A.q_out + (t0 + i) * A.o_stride[0] + h * A.o_stride[1];
+        } else {
+          const Side& S = A.kv[x - nq];
+          rotates = x == nq;
+          writes = in;
+          src = S.src + (t0 + i) * S.tok + hk * S.head;
+          dst = static_cast<__nv_bfloat16*>(S.pool) + pg * S.page + (slot0 + i) * S.slot + hk * S.phead;
+        }
+        if (!writes) continue;
+        uint4 a = *reinterpret_cast<const uint4*>(src + va), b = *reinterpret_cast<const uint4*>(src + vb);
+        if (rotates && c < nrot) {
+          float f[16];
+          unpack8(a, f);
+          unpack8(b, f + 8);
+          turn_chunk(f, i, c);
+          a = pack8(f);
+          b = pack8(f + 8);
+        }
+        *reinterpret_cast<uint4*>(dst + va) = a;
+        *reinterpret_cast<uint4*>(dst + vb) = b;
+      }
+    }
+  }
+
+  if constexpr (CODES) {
+    if (!in) return;
+    constexpr int ROWS = 32 / CH, PASSES = 16 / ROWS;        // tokens of a pass of the warp
+    const int r = lane / CH, c = lane % CH;
+    const int va = vec_a(c) * 8, vb = vec_b(c) * 8;
+    const int heads = (A.Hkv - static_cast<int>(blockIdx.y) + gridDim.y - 1) / gridDim.y;
+    for (int j = warp; j < 2 * heads; j += kRotThreads / 32) {
+      const int hk = blockIdx.y + (j >> 1) * gridDim.y;
+      const Side& S = A.kv[j & 1];
+      const bool rotates = (j & 1) == 0;
+      const __nv_bfloat16* src = S.src + (t0 + r) * S.tok + hk * S.head;
+      const int nb = 1 << (A.page_shift - kScaleShift);
+      float* sp = S.scale + (static_cast<int64_t>(pg) * A.Hkv + hk) * nb + (slot0 >> kScaleShift);
+      uint8_t* pool = static_cast<uint8_t*>(S.pool) + pg * S.page + hk * S.phead +
+                      static_cast<int64_t>(slot0 - first) * S.slot;      // the block's first token
+      Vec2 x[PASSES];
+#pragma unroll
+      for (int k = 0; k < PASSES; ++k)
+        if (k * ROWS + r < n) {
+          x[k].a = *reinterpret_cast<const uint4*>(src + k * ROWS * S.tok + va);
+          x[k].b = *reinterpret_cast<const uint4*>(src + k * ROWS * S.tok + vb);
+        }
+      const float raw = *sp;
+      float f[PASSES][16];
+      uint32_t top = 0;
+#pragma unroll
+      for (int k = 0; k < PASSES; ++k)
+        if (k * ROWS + r < n) {
+          unpack8(x[k].a, f[k]);
+          unpack8(x[k].b, f[k] + 8);
+          if (rotates) turn_chunk(f[k], k * ROWS + r, c);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const uint32_t y = __float_as_uint(f[k][e]) & 0x7fffffffu;
+            top = max(top, y < 0x7f800000u ? y : 0u);        // the finite ones
+          }
+        }
+      top = __reduce_max_sync(0xffffffffu, top);
+      float s = scale_for(__uint_as_float(top));
+      if (first > 0) {
+        // tokens of the block keep their values: all 16 places, the new
+        // ones are written below
+        const float old = clamp_scale(raw);
+        s = fmaxf(s, old);
+        if (s > old) {
+          for (int row = r; row < kScaleBlock; row += ROWS) {
+            uint4* at16 = reinterpret_cast<uint4*>(pool + row * S.slot + c * 16);
+            if (row < first || row >= first + n) *at16 = rescale_e4m3x16(*at16, old / s);
+          }
+        }
+      }
+      if (lane == 0 && s != raw) *sp = s;
+      const float inv = 1.f / s;           // exact: a power of two, or the caller's own
+#pragma unroll
+      for (int k = 0; k < PASSES; ++k)
+        if (k * ROWS + r < n) {
+          float* g = f[k];
+          uint8_t* dst = pool + (first + k * ROWS + r) * S.slot;
+#pragma unroll
+          for (int e = 0; e < 16; ++e) g[e] *= inv;
+          *reinterpret_cast<uint2*>(dst + va) =
+              make_uint2(pack_e4m3x4(g[0], g[1], g[2], g[3]), pack_e4m3x4(g[4], g[5], g[6], g[7]));
+          *reinterpret_cast<uint2*>(dst + vb) =
+              make_uint2(pack_e4m3x4(g[8], g[9], g[10], g[11]), pack_e4m3x4(g[12], g[13], g[14], g[15]));
+        }
+    }
+  }
+}
+
+// ------------------------------------------------------------------ accept
+// A warp keeps the accepted nodes of one sequence, layer and head, K or V: it
+// walks the blocks that they go to in ascending order.  Into a block D go
+// at most 16 tokens, from D itself or from later blocks; all are loaded before
+// one is stored, so a block may be overwritten once it has been done.  D's new
+// scale is the largest of its own and those of the blocks that its tokens come
+// from: no value grows out of range, and where the scales are equal (most
+// trees lie in a few blocks written together) the codes are copied as they
+// are.
+constexpr int kAccept8Warps = 4;
+
+struct Accept8Args {
+  Side kv[2];                  // without sources
+  int64_t layer[2];            // of the pools, in elements
+  int64_t scale_layer;
+  const int32_t *accept, *n_accept, *cu, *table, *lens;
+  int32_t *lens_out, *ref;
+  int* status;
+  int max_accept, max_pages, n_pages, page_shift, Hkv;
+};
+
+template <int D>
+__global__ void __launch_bounds__(kAccept8Warps * 32)
+    accept8_kernel(const __grid_constant__ Accept8Args A) {
+  __shared__ int place[32];            // by place within two blocks: source (page << 8 | slot), -1: none
+  __shared__ int good;
+  grid_launch_dependents();
+  grid_dependency_wait();
+  const int b = blockIdx.y, layer = blockIdx.z, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int32_t* acc = A.accept + static_cast<int64_t>(b) * A.max_accept;
+  const int32_t* row = A.table + static_cast<int64_t>(b) * A.max_pages;
+  const int m = A.n_accept[b], page = 1 << A.page_shift;
+  int n;
+  const int base = context_of(A.lens, A.cu, b, 0x7fffffff, A.max_pages << A.page_shift, n);
+  const bool sized = base >= 0 && m >= 0 && m <= n && m <= A.max_accept;
+  // page << 8 | slot of a position, -1 if its page is out of range
+  auto at = [&](int pos) -> int {
+    const int pg = row[pos >> A.page_shift];
+    return pg >= 0 && pg < A.n_pages ? (pg << 8) | (pos & (page - 1)) : -1;
+  };
+  auto first_free = [&](int x) { return (base + x + page - 1) >> A.page_shift; };
+  // source of entry i, -1: the entry is not valid
+  auto look = [&](int i) -> int {
+    const int a = acc[i], before = i ? acc[i - 1] : -1;
+    if (a <= before || a >= n || at(base + i) < 0) return -1;
+    return at(base + a);
+  };
+  const int skew = base & (kScaleBlock - 1);   // entry i goes to place skew + i of the first block on
+  if (threadIdx.x < 32) {
+    bool ok = sized;
+    place[lane] = -1;
+    __syncwarp();
+    for (int i = lane; sized && i < m; i += 32) {
+      const int from = look(i);
+      ok = from >= 0 && ok;
+      if (skew + i < 32) place[skew + i] = from;
+    }
+    // the pages past the new length, as in the accept of a bf16 cache
+    if (sized && A.ref)
+      for (int j = first_free(m) + lane; j < first_free(n); j += 32) ok = at(j << A.page_shift) >= 0 && ok;
+    ok = __all_sync(0xffffffffu, ok);
+    if (lane == 0) good = ok;
+  }
+  __syncthreads();
+  const bool ok = good != 0;
+  if (blockIdx.x == 0 && layer == 0) {
+    if (threadIdx.x == 0) {
+      A.lens_out[b] = ok ? base + m : A.lens[b];
+      if (!ok) flag(A.status, DEV_CACHE);
+    }
+    if (ok && A.ref)
+      for (int j = first_free(m) + threadIdx.x; j < first_free(n); j += blockDim.x) atomicSub(A.ref + row[j], 1);
+  }
+  if (!ok || m == 0) return;
+  const int unit = blockIdx.x * kAccept8Warps + warp, hk = unit >> 1;
+  const Side& S = A.kv[unit & 1];
+  const bool mine = hk < A.Hkv;
+  uint8_t* pool = static_cast<uint8_t*>(S.pool) + layer * A.layer[unit & 1] + hk * S.phead;
+  float* scales = S.scale + layer * A.scale_layer;
+  const int nb_shift = A.page_shift - kScaleShift;
+  auto scale_at = [&](int where) -> float* {
+    return scales + (((static_cast<int64_t>(where >> 8) * A.Hkv + hk) << nb_shift) + ((where & 255) >> kScaleShift));
+  };
+  auto codes_at = [&](int where) -> uint8_t* {
+    return pool + (where >> 8) * S.page + static_cast<int64_t>(where & 255) * S.slot;
+  };
+  constexpr int LPR = D / 16, ROWS = 32 / LPR, PASSES = 16 / ROWS;
+  const int r = lane / LPR, c = lane % LPR;
+  for (int d0 = 0; d0 < skew + m; d0 += kScaleBlock) {       // destination blocks
+    if (d0 >= 32 && (d0 & 31) == 0) {                        // the next two blocks' places
+      __syncthreads();
+      if (threadIdx.x < 32) place[lane] = d0 + lane < skew + m ? look(d0 + lane - skew) : -1;
+      __syncthreads();
+    }
+    if (!mine) continue;
+    const int* from = place + (d0 & 31);
+    const int to = at(base - skew + d0);                     // its first token
+    // scales: lane t < 16 of token t's source, lane 16 the block's own
+    const int src = lane < 16 ? from[lane] : -1;
+    const float own_raw = *scale_at(to), old = clamp_scale(own_raw);
+    const float mine_s = src >= 0 ? clamp_scale(*scale_at(src)) : old;
+    const float s = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(mine_s, old))));
+    uint4 x[PASSES];
+    bool write[PASSES];
+#pragma unroll
+    for (int k = 0; k < PASSES; ++k) {
+      const int t = k * ROWS + r;
+      const int w = from[t], here = to + t, f = w >= 0 ? w : here;
+      const float have = __shfl_sync(0xffffffffu, mine_s, t);
+      write[k] = f != here || have != s;
+      if (write[k]) {
+        x[k] = *reinterpret_cast<const uint4*>(codes_at(f) + c * 16);
+        if (have != s) x[k] = rescale_e4m3x16(x[k], have / s);
+      }
+    }
+    __syncwarp();                                            // all loads before the stores
+#pragma unroll
+    for (int k = 0; k < PASSES; ++k)
+      if (write[k]) *reinterpret_cast<uint4*>(codes_at(to + k * ROWS + r) + c * 16) = x[k];
+    if (lane == 0 && s != own_raw) *scale_at(to) = s;
+    __syncwarp();
+  }
+}
+
+fm_status done(cudaError_t e) { return e == cudaSuccess ? FM_OK : FM_ERR_CUDA; }
+
+Side side_of(const fm_cache& c, int which, void* pool, float* scale) {
+  const int64_t* st = which ? c.v_stride : c.k_stride;
+  Side S{};
+  S.pool = pool;
+  S.page = st[1];
+  S.slot = st[2];
+  S.phead = st[3];
+  S.scale = scale;
+  return S;
+}
+
+bool stride_ok(const int64_t* s, int n, int unit) {
+  for (int i = 0; i < n; ++i)
+    if (s[i] <= 0 || s[i] % unit != 0 || s[i] >= (int64_t(1) << 36)) return false;
+  return true;
+}
+
+}  // namespace
+
+fm_status check_cache8(const fm_cache* c, const void* k_pool, const void* v_pool, const void* k_scale,
+                       const void* v_scale) {
+  const fm_status st = check_cache(c, true);
+  if (st != FM_OK) return st;
+  if (!stride_ok(c->k_stride, 4, 16) || !stride_ok(c->v_stride, 4, 16)) return FM_ERR_INVALID;
+  if (!aligned_to(k_pool, 16) || !aligned_to(v_pool, 16) || !aligned_to(k_scale, 4) || !aligned_to(v_scale, 4))
+    return FM_ERR_INVALID;
+  return FM_OK;
+}
+
+}  // namespace fm
+
+using namespace fm;
+
+extern "C" {
+
+fm_status fm_cache_append_rotary(const fm_cache* c, const fm_rotary* t, const void* k, const void* v,
+                                 const int64_t* k_stride, const int64_t* v_stride, const int32_t* cu,
+                                 int total, void* k_pool, void* v_pool, float* k_scale, float* v_scale,
+                                 const int32_t* table, const int32_t* lens, int32_t* status,
+                                 void* stream) {
+  const bool codes = k_scale || v_scale;
+  fm_status st = codes ? check_cache8(c, k_pool, v_pool, k_scale, v_scale) : check_cache(c, true);
+  if (st != FM_OK) return st;
+  if (!t || !k_stride || !v_stride || !cu || !table || !lens || total < 1) return FM_ERR_INVALID;
+  if (!aligned_to(k, 16) || !aligned_to(v, 16) || !aligned_to(k_pool, 16) || !aligned_to(v_pool, 16))
+    return FM_ERR_INVALID;
+  if (!stride_ok(k_stride, 2, 8) || !stride_ok(v_stride, 2, 8)) return FM_ERR_INVALID;
+  if (t->rot < 0 || t->rot > c->d || t->rot % 16 != 0 || (t->rot > 0 && !aligned_to(t->freqs, 4)))
+    return FM_ERR_INVALID;
+  if (t->H < 0 || t->H % c->Hkv != 0) return FM_ERR_INVALID;
+  if (t->H > 0 && (!aligned_to(t->q, 16) || !aligned_to(t->q_out, 16) || !stride_ok(t->q_stride, 2, 8) ||
+                   !stride_ok(t->o_stride, 2, 8)))
+    return FM_ERR_INVALID;
+  if (static_cast<int64_t>(total) * (t->H > c->Hkv ? t->H : c->Hkv) > kMaxTokenIndex) return FM_ERR_UNSUPPORTED;
+  const int64_t blocks = total / kScaleBlock + 2 * static_cast<int64_t>(c->B);
+  if (blocks > 0x7fffffff) return FM_ERR_UNSUPPORTED;
+  RotArgs A{};
+  A.kv[0] = side_of(*c, 0, k_pool, k_scale);
+  A.kv[1] = side_of(*c, 1, v_pool, v_scale);
+  A.kv[0].src = static_cast<const __nv_bfloat16*>(k);
+  A.kv[1].src = static_cast<const __nv_bfloat16*>(v);
+  A.kv[0].tok = k_stride[0]; A.kv[0].head = k_stride[1];
+  A.kv[1].tok = v_stride[0]; A.kv[1].head = v_stride[1];
+  A.q = static_cast<const __nv_bfloat16*>(t->q);
+  A.q_out = static_cast<__nv_bfloat16*>(t->q_out);
+  for (int i = 0; i < 2; ++i) {
+    A.q_stride[i] = t->q_stride[i];
+    A.o_stride[i] = t->o_stride[i];
+  }
+  A.freqs = t->freqs;
+  A.positions = t->positions;
+  A.cu = cu; A.table = table; A.lens = lens; A.status = status;
+  A.B = c->B; A.total = total; A.max_pages = c->max_pages; A.n_pages = c->n_pages;
+  A.page_shift = page_shift(c->page_size);
+  A.Hkv = c->Hkv; A.G = t->H / c->Hkv;
+  A.nrot = t->rot / 16;
+  A.inter = t->interleaved != 0;
+  // few blocks: the heads are spread over more of them
+  int64_t y = (4 * static_cast<int64_t>(num_sms()) + blocks - 1) / blocks;
+  if (y > c->Hkv) y = c->Hkv;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(y));
+  prof_begin(K_CACHE_APPEND_ROTARY, s);
+  auto go = [&](auto kern) { return launch_dependent(kern, grid, kRotThreads, 0, s, A); };
+  const cudaError_t e = c->d == 64 ? (codes ? go(append_rotary_kernel<64, true>) : go(append_rotary_kernel<64, false>))
+                                   : (codes ? go(append_rotary_kernel<128, true>) : go(append_rotary_kernel<128, false>));
+  prof_end(K_CACHE_APPEND_ROTARY, s);
+  return done(e);
+}
+
+fm_status fm_cache_accept_fp8(const fm_cache* c, const int32_t* accept, int max_accept,
+                              const int32_t* n_accept, const int32_t* cu, void* k_pool, void* v_pool,
+                              float* k_scale, float* v_scale, const int32_t* table, const int32_t* lens,
+                              int32_t* lens_out, int32_t* ref, int32_t* status, void* stream) {
+  const fm_status st = check_cache8(c, k_pool, v_pool, k_scale, v_scale);
+  if (st != FM_OK) return st;
+  if (!accept || max_accept < 1 || !n_accept || !cu || !table || !lens || !lens_out) return FM_ERR_INVALID;
+  if (overlaps(lens, c->B * 4ull, lens_out, c->B * 4ull)) return FM_ERR_INVALID;
+  if (c->B > 65535 || c->layers > 65535) return FM_ERR_UNSUPPORTED;
+  Accept8Args A{};
+  A.kv[0] = side_of(*c, 0, k_pool, k_scale);
+  A.kv[1] = side_of(*c, 1, v_pool, v_scale);
+  A.layer[0] = c->k_stride[0];
+  A.layer[1] = c->v_stride[0];
+  A.scale_layer = static_cast<int64_t>(c->n_pages) * c->Hkv * (c->page_size / kScaleBlock);
+  A.accept = accept; A.n_accept = n_accept; A.cu = cu; A.table = table; A.lens = lens;
+  A.lens_out = lens_out; A.ref = ref; A.status = status;
+  A.max_accept = max_accept; A.max_pages = c->max_pages; A.n_pages = c->n_pages;
+  A.page_shift = page_shift(c->page_size);
+  A.Hkv = c->Hkv;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const dim3 grid(ceil_div(2 * c->Hkv, kAccept8Warps), c->B, c->layers);
+  prof_begin(K_CACHE_ACCEPT, s);
+  const cudaError_t e = c->d == 64 ? launch_dependent(accept8_kernel<64>, grid, kAccept8Warps * 32, 0, s, A)
+                                   : launch_dependent(accept8_kernel<128>, grid, kAccept8Warps * 32, 0, s, A);
+  prof_end(K_CACHE_ACCEPT, s);
+  return done(e);
+}
+
+}  // extern "C"

@@ -130,7 +130,8 @@ const char* fm_kernel_name(int id) {
                                        "bwd_kv_kernel", "bwd_dq_kernel", "tile_mask_kernel",
                                        "quant_kernel", "fwd_fp8_kernel", "append_kernel",
                                        "tree_kernel", "tree_join_kernel", "accept_kernel",
-                                       "fork_kernel", "page_plan_kernel", "page_copy_kernel"};
+                                       "fork_kernel", "page_plan_kernel", "page_copy_kernel",
+                                       "append_rotary_kernel"};
   return (id >= 0 && id < K_COUNT) ? names[id] : "unknown";
 }
 

@@ -4,7 +4,7 @@
 #include <cfloat>
 #include <cmath>
 
-#include "fm_tree.h"
+#include "fm_tree8.cuh"
 
 namespace fm {
 
@@ -664,6 +664,15 @@ static fm_status launch_join(const TreeParams& P, int grid, cudaStream_t s) {
   return e == cudaSuccess ? FM_OK : FM_ERR_CUDA;
 }
 
+fm_status launch_tree_join(const TreeParams& P, int d, int rows, int grid, cudaStream_t s) {
+  const bool d64 = d == 64;
+  if (rows == NarrowGeo::R)
+    return d64 ? launch_join<NarrowGeo::R, 64>(P, grid, s) : launch_join<NarrowGeo::R, 128>(P, grid, s);
+  if (rows == MidGeo::R)
+    return d64 ? launch_join<MidGeo::R, 64>(P, grid, s) : launch_join<MidGeo::R, 128>(P, grid, s);
+  return launch_join<WideGeo::R, 128>(P, grid, s);
+}
+
 template <int D>
 static fm_status launch_narrow(const TreeParams& P, const CUtensorMap& tk, const CUtensorMap& tv,
                                int grid, cudaStream_t s) {
@@ -749,22 +758,23 @@ size_t tree_ws_bound(const fm_cache& c, const fm_tree_desc& t, int sms) {
   return W.bytes;
 }
 
-}  // namespace
-}  // namespace fm
-
-using namespace fm;
-
-extern "C" {
-
-size_t fm_tree_workspace_size(const fm_cache* c, const fm_tree_desc* t) {
-  if (check_tree(c, t) != FM_OK) return 0;
-  return tree_ws_bound(*c, *t, num_sms());
+// The same for a cache of e4m3 codes.
+TreeWs tree_ws8(const fm_cache& c, const fm_tree_desc&, int sms) {
+  TreeWs W;
+  W.kind = NARROW;
+  W.rows = NarrowGeo::R;
+  W.grid = 2 * sms;
+  tree_ws_places(W, c.d);
+  return W;
 }
 
-fm_status fm_tree_fwd(const fm_cache* c, const fm_tree_desc* t, const void* q, const void* k_pool,
-                      const void* v_pool, const int32_t* table, const int32_t* lens,
-                      const int32_t* cu, const int32_t* parents, float scale, void* o, float* lse,
-                      void* ws, size_t ws_bytes, int32_t* status, void* stream) {
+// k_scale, v_scale: of a cache of e4m3 codes; both null with a cache of bf16.
+fm_status tree_fwd(const fm_cache* c, const fm_tree_desc* t, const void* q, const void* k_pool,
+                   const void* v_pool, const float* k_scale, const float* v_scale,
+                   const int32_t* table, const int32_t* lens, const int32_t* cu, const int32_t* parents,
+                   float scale, void* o, float* lse, void* ws, size_t ws_bytes, int32_t* status,
+                   void* stream) {
+  const bool codes = k_scale != nullptr;
   fm_status st = check_tree(c, t);
   if (st != FM_OK) return st;
   if (parents && t->max_nodes > FM_TREE_MAX_NODES) return FM_ERR_UNSUPPORTED;
@@ -775,7 +785,7 @@ fm_status fm_tree_fwd(const fm_cache* c, const fm_tree_desc* t, const void* q, c
   // masked score times the scale is -inf again
   const float scale_log2 = scale * 1.4426950408889634f;
   if (!(scale_log2 >= FLT_MIN && scale_log2 < INFINITY)) return FM_ERR_INVALID;
-  const TreeWs W = tree_ws(*c, *t, num_sms());
+  const TreeWs W = codes ? tree_ws8(*c, *t, num_sms()) : tree_ws(*c, *t, num_sms());
   const int grid = W.grid;
   if (!aligned_to(ws, 256) || ws_bytes < W.bytes) return FM_ERR_WORKSPACE;
   // the length of the line of units (an upper bound) is counted in 31 bits
@@ -823,6 +833,19 @@ fm_status fm_tree_fwd(const fm_cache* c, const fm_tree_desc* t, const void* q, c
   const TestHooks th = test_hooks();
   P.wait_ns = th.wait_ns < 4000000000ull ? static_cast<uint32_t>(th.wait_ns) : 4000000000u;
   P.withhold = th.withhold;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (codes) {
+    const int box = c->page_size;          // a page is a tile at most
+    P.box_shift = page_shift(box);
+    Tree8Params A{P, k_scale, v_scale, static_cast<const uint8_t*>(v_pool)};
+    CUtensorMap tk, tv;
+    if (!make_tmap_pool8(&tk, k_pool, c->n_pages, c->page_size, c->Hkv, c->d, c->k_stride + 1, box) ||
+        !make_tmap_pool8(&tv, v_pool, c->n_pages, c->page_size, c->Hkv, c->d, c->v_stride + 1, box))
+      return FM_ERR_CUDA;
+    const int64_t rows = static_cast<int64_t>(t->max_nodes < t->total ? t->max_nodes : t->total) * P.G;
+    st = launch_tree8_narrow(A, c->d, rows < NarrowGeo::R ? static_cast<int>(rows) : NarrowGeo::R, tk, tv, grid, s);
+    return st != FM_OK ? st : launch_tree_join(P, c->d, NarrowGeo::R, grid, s);
+  }
   // one page of one head, or a tile's part of it, is a box of 64 columns
   const int box = W.kind == WIDE || c->page_size < MidGeo::KT ? c->page_size : MidGeo::KT;
   P.box_shift = page_shift(box);
@@ -843,20 +866,42 @@ fm_status fm_tree_fwd(const fm_cache* c, const fm_tree_desc* t, const void* q, c
     const int64_t st[3] = {8, t->q_stride[0], t->q_stride[1]};
     if (!make_tmap_bshd(&tq, q, 1, t->total, t->H, c->d, st, 128 / P.G, P.G)) return FM_ERR_CUDA;
   }
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const bool d64 = c->d == 64;
-  if (W.kind == NARROW) {
-    st = d64 ? launch_narrow<64>(P, tk, tv, grid, s) : launch_narrow<128>(P, tk, tv, grid, s);
-    if (st != FM_OK) return st;
-    return d64 ? launch_join<NarrowGeo::R, 64>(P, grid, s) : launch_join<NarrowGeo::R, 128>(P, grid, s);
-  }
-  if (W.kind == MID) {
-    st = launch_tree_mid(P, c->d, tq, tk, tv, grid, s);
-    if (st != FM_OK) return st;
-    return d64 ? launch_join<MidGeo::R, 64>(P, grid, s) : launch_join<MidGeo::R, 128>(P, grid, s);
-  }
-  st = launch_tree_wide(P, tq, tk, tv, grid, s);
-  return st != FM_OK ? st : launch_join<WideGeo::R, 128>(P, grid, s);
+  if (W.kind == NARROW) st = c->d == 64 ? launch_narrow<64>(P, tk, tv, grid, s) : launch_narrow<128>(P, tk, tv, grid, s);
+  else if (W.kind == MID) st = launch_tree_mid(P, c->d, tq, tk, tv, grid, s);
+  else st = launch_tree_wide(P, tq, tk, tv, grid, s);
+  if (st != FM_OK) return st;
+  return launch_tree_join(P, c->d, W.kind == NARROW ? NarrowGeo::R : W.kind == MID ? MidGeo::R : WideGeo::R, grid, s);
+}
+
+}  // namespace
+}  // namespace fm
+
+using namespace fm;
+
+extern "C" {
+
+size_t fm_tree_workspace_size(const fm_cache* c, const fm_tree_desc* t) {
+  if (check_tree(c, t) != FM_OK) return 0;
+  return tree_ws_bound(*c, *t, num_sms());
+}
+
+fm_status fm_tree_fwd(const fm_cache* c, const fm_tree_desc* t, const void* q, const void* k_pool,
+                      const void* v_pool, const int32_t* table, const int32_t* lens,
+                      const int32_t* cu, const int32_t* parents, float scale, void* o, float* lse,
+                      void* ws, size_t ws_bytes, int32_t* status, void* stream) {
+  return tree_fwd(c, t, q, k_pool, v_pool, nullptr, nullptr, table, lens, cu, parents, scale, o, lse, ws,
+                  ws_bytes, status, stream);
+}
+
+fm_status fm_tree_fwd_fp8(const fm_cache* c, const fm_tree_desc* t, const void* q, const void* k_pool,
+                          const void* v_pool, const float* k_scale, const float* v_scale,
+                          const int32_t* table, const int32_t* lens, const int32_t* cu,
+                          const int32_t* parents, float scale, void* o, float* lse, void* ws,
+                          size_t ws_bytes, int32_t* status, void* stream) {
+  const fm_status st = check_cache8(c, k_pool, v_pool, k_scale, v_scale);
+  if (st != FM_OK) return st;
+  return tree_fwd(c, t, q, k_pool, v_pool, k_scale, v_scale, table, lens, cu, parents, scale, o, lse, ws,
+                  ws_bytes, status, stream);
 }
 
 }  // extern "C"

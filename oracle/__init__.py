@@ -16,9 +16,11 @@ What it computes, from the pages and the plain definitions:
   its gradients, in float64, on the bf16-rounded inputs.
 
 * ``oracle.cache`` - the paged K/V cache: attention of drafted trees over it,
-  appending, accepting, forking, reserving and compacting.
+  appending, accepting, forking, reserving and compacting;
+* ``oracle.cache8`` - the cache held in e4m3 codes with scales, and the
+  rotation by position.
 
 Every function names the passage it follows (the cache has none there).  Parity pins live in
 ``tests/test_oracle_*.py``.
 """
-from . import masks, attention, cache  # noqa: F401
+from . import masks, attention, cache, cache8  # noqa: F401
