@@ -338,11 +338,18 @@ __device__ __forceinline__ uint32_t sdesc_lo(uint32_t saddr, uint32_t lbo) {
 __device__ __forceinline__ uint64_t sdesc_at(uint32_t lo, uint32_t bytes) {
   return (static_cast<uint64_t>(kSdescHi) << 32) | (lo + (bytes >> 4));
 }
-// Instruction descriptor, kind::f16 with bf16 A/B and fp32 accumulation.
 // Instruction descriptor of a kind::f8f6f4 MMA with e4m3 A and B (format
 // code 0 in both fields) and an f32 accumulator; both operands K-major.
 __host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N) {
   return (1u << 4)                                  // D format: f32
+         | (static_cast<uint32_t>(N >> 3) << 17)    // N / 8
+         | (static_cast<uint32_t>(M >> 4) << 24);   // M / 16
+}
+// Instruction descriptors, kind::f16 with f16 or bf16 A/B and fp32 accumulation.
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool a_mn_major, bool b_mn_major) {
+  return (1u << 4)                                  // D format: f32
+         | ((a_mn_major ? 1u : 0u) << 15)           // A major-ness
+         | ((b_mn_major ? 1u : 0u) << 16)           // B major-ness
          | (static_cast<uint32_t>(N >> 3) << 17)    // N / 8
          | (static_cast<uint32_t>(M >> 4) << 24);   // M / 16
 }

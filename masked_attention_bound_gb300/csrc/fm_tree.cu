@@ -759,10 +759,11 @@ size_t tree_ws_bound(const fm_cache& c, const fm_tree_desc& t, int sms) {
 }
 
 // The same for a cache of e4m3 codes.
-TreeWs tree_ws8(const fm_cache& c, const fm_tree_desc&, int sms) {
+TreeWs tree_ws8(const fm_cache& c, const fm_tree_desc& t, int sms) {
+  const int64_t nodes = t.max_nodes < t.total ? t.max_nodes : t.total, rows = nodes * (t.H / c.Hkv);
   TreeWs W;
-  W.kind = NARROW;
-  W.rows = NarrowGeo::R;
+  W.kind = rows <= NarrowGeo::R ? NARROW : MID;
+  W.rows = W.kind == NARROW ? NarrowGeo::R : rows >= MidGeo::R ? MidGeo::R : (static_cast<int>(rows) + 31) / 32 * 32;
   W.grid = 2 * sms;
   tree_ws_places(W, c.d);
   return W;
@@ -835,13 +836,18 @@ fm_status tree_fwd(const fm_cache* c, const fm_tree_desc* t, const void* q, cons
   P.withhold = th.withhold;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (codes) {
-    const int box = c->page_size;          // a page is a tile at most
+    // a page, or a tile's part of it
+    const int box = W.kind == MID && c->page_size > MidGeo::KT ? MidGeo::KT : c->page_size;
     P.box_shift = page_shift(box);
     Tree8Params A{P, k_scale, v_scale, static_cast<const uint8_t*>(v_pool)};
     CUtensorMap tk, tv;
     if (!make_tmap_pool8(&tk, k_pool, c->n_pages, c->page_size, c->Hkv, c->d, c->k_stride + 1, box) ||
         !make_tmap_pool8(&tv, v_pool, c->n_pages, c->page_size, c->Hkv, c->d, c->v_stride + 1, box))
       return FM_ERR_CUDA;
+    if (W.kind == MID) {
+      st = launch_tree8_mid(A, c->d, tk, tv, grid, s);
+      return st != FM_OK ? st : launch_tree_join(P, c->d, MidGeo::R, grid, s);
+    }
     const int64_t rows = static_cast<int64_t>(t->max_nodes < t->total ? t->max_nodes : t->total) * P.G;
     st = launch_tree8_narrow(A, c->d, rows < NarrowGeo::R ? static_cast<int>(rows) : NarrowGeo::R, tk, tv, grid, s);
     return st != FM_OK ? st : launch_tree_join(P, c->d, NarrowGeo::R, grid, s);

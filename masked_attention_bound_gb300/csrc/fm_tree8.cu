@@ -143,8 +143,9 @@ __global__ void __launch_bounds__(Narrow8Cfg<D, NT>::THREADS, 2)
         const int next = t + 1 < u.t1 ? Load::lane_page(P, u, t + 1, lane) : 0;
         if (use > 0) ok = wait_all(empty(first + st), (use - 1) & 1);
         if (!ok) break;
-        Load::issue(P, u, t, lane, page, tm, scales, buf + st * C::TILE,
-                    sbase + C::OFF_SCALE + (first + st) * C::BLOCKS * 4, full(first + st), policy);
+        Load::issue(P, u, t, lane, page, tm, buf + st * C::TILE, full(first + st), policy);
+        Load::copy_scales(P, u, t, lane, page, scales, sbase + C::OFF_SCALE + (first + st) * C::BLOCKS * 4);
+        Load::landed(full(first + st), lane);
         ++issued;
         if (++st == stages) {
           st = 0;
@@ -205,12 +206,11 @@ __global__ void __launch_bounds__(Narrow8Cfg<D, NT>::THREADS, 2)
         for (int i = 0; i < D / 8; ++i) top = max(top, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const int up = top ? min(13 - (static_cast<int>(top >> 7) - 127), 126) : 0;
-        const float mul = __int_as_float((up + 127) << 23);
+        const int up = row_shift(top);
+        const float mul = pow2(up);
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i)
-          qf[nt][i >> 1][i & 1] = pack_f16(__uint_as_float(w[i] << 16) * mul, __uint_as_float(w[i] & 0xffff0000u) * mul);
-        const float undo = __int_as_float((127 - up) << 23) * P.scale_log2;
+        for (int i = 0; i < D / 8; ++i) qf[nt][i >> 1][i & 1] = f16x2_of_bf16x2(w[i], mul);
+        const float undo = pow2(-up) * P.scale_log2;
         back[nt][0] = __shfl_sync(0xffffffffu, undo, 8 * tq);
         back[nt][1] = __shfl_sync(0xffffffffu, undo, 8 * tq + 4);
       }
@@ -266,7 +266,7 @@ __global__ void __launch_bounds__(Narrow8Cfg<D, NT>::THREADS, 2)
           for (int x = 0; x < 2; ++x) {
             if (x >= nblk) break;
             const int r0 = (warp + 4 * x) * 16 + g;
-            fk[x] = clamp_scale(scale_ring[ks * C::BLOCKS + warp + 4 * x]);
+            fk[x] = scale_ring[ks * C::BLOCKS + warp + 4 * x];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -292,13 +292,11 @@ __global__ void __launch_bounds__(Narrow8Cfg<D, NT>::THREADS, 2)
         if (ok) ok = wait_all(full(C::KS + vs), vp);
         uint32_t pf[2][NT][2];
         if (ok && nblk > 0) {
-          float lv[2], wl[2];                    // log2 of V's scales, and what undoes P's
+          float4 f[2];
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             if (x >= nblk) break;
-            const float c = clamp_scale(scale_ring[(C::KS + vs) * C::BLOCKS + warp + 4 * x]);
-            lv[x] = __log2f(c);
-            wl[x] = kPUndo * ex2(-lv[x]);
+            f[x] = block_factors(fk[x], scale_ring[(C::KS + vs) * C::BLOCKS + warp + 4 * x]);
           }
           // z = x + log2 sv, in place
 #pragma unroll
@@ -308,7 +306,7 @@ __global__ void __launch_bounds__(Narrow8Cfg<D, NT>::THREADS, 2)
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
               for (int y = 0; y < 4; ++y)
-                s[x][nt][y] = fmaf(s[x][nt][y], fminf(back[nt][y & 1] * fk[x], 0x1.fffffep127f), lv[x]);
+                s[x][nt][y] = fmaf(s[x][nt][y], fminf(back[nt][y & 1] * f[x].x, 0x1.fffffep127f), f[x].y);
           }
           if (t >= part0 || (t + 1) * KT > u.keys) {
             // keys past origin: only what the row sees
@@ -366,8 +364,8 @@ __global__ void __launch_bounds__(Narrow8Cfg<D, NT>::THREADS, 2)
               float p[4];
 #pragma unroll
               for (int y = 0; y < 4; ++y) p[y] = ex2(s[x][nt][y] - ref[nt][y & 1]);
-              l[nt][0] = fmaf(p[0] + p[2], wl[x], l[nt][0]);
-              l[nt][1] = fmaf(p[1] + p[3], wl[x], l[nt][1]);
+              l[nt][0] = fmaf(p[0] + p[2], f[x].z, l[nt][0]);
+              l[nt][1] = fmaf(p[1] + p[3], f[x].z, l[nt][1]);
               pf[x][nt][0] = transpose8(pack_f16(p[0], p[1]));
               pf[x][nt][1] = transpose8(pack_f16(p[2], p[3]));
             }
@@ -504,7 +502,9 @@ __global__ void __launch_bounds__(Narrow8Cfg<D, NT>::THREADS, 2)
             __nv_bfloat16* dst = P.o + (u.s.row0 + node) * P.o_stride[0] + h * P.o_stride[1] + c;
             *reinterpret_cast<uint2*>(dst) =
                 make_uint2(pack_bf16(v.x * inv, v.y * inv), pack_bf16(v.z * inv, v.w * inv));
-            if (any) fix_row8(A, u.b, u.hk, u.origin, nf, seen + r * 8, c, 4, dst);
+            if (any)
+              fix_row8(A, u.b, u.hk, u.origin, nf, *reinterpret_cast<const uint4*>(seen + r * 8),
+                       *reinterpret_cast<const uint4*>(seen + r * 8 + 4), c, 4, dst);
             if (c == 0)
               P.lse[static_cast<int64_t>(h) * P.total + u.s.row0 + node] =
                   ll > 0.f || ll != ll ? (mm + __log2f(ll)) * 0.69314718055994530942f : -INFINITY;
@@ -512,7 +512,9 @@ __global__ void __launch_bounds__(Narrow8Cfg<D, NT>::THREADS, 2)
             const int64_t at = static_cast<int64_t>(2 * blockIdx.x + (u.t0 == 0 ? 1 : 0)) * P.part_rows + r;
             float* dst = P.part_o + at * D + c;
             *reinterpret_cast<float4*>(dst) = v;
-            if (any) fix_row8(A, u.b, u.hk, u.origin, nf, seen + r * 8, c, 4, dst);
+            if (any)
+              fix_row8(A, u.b, u.hk, u.origin, nf, *reinterpret_cast<const uint4*>(seen + r * 8),
+                       *reinterpret_cast<const uint4*>(seen + r * 8 + 4), c, 4, dst);
             if (c == 0) P.part_ml[at] = make_float2(mm, ll);
           }
         }

@@ -34,12 +34,12 @@ constexpr float kPOffset = 7.f, kPUndo = 0x1p-7f;
 // One KT-key tile of codes of K or V into shared memory by TMA: boxes of
 // min(page_size, KT) rows of D bytes, swizzled by 16-byte words as wide as
 // the row (word16), and the scales of its KT / 16 blocks by asynchronous
-// copies.  A stage's barrier counts 1 + KT / 16 arrivals.  Boxes past the
-// unit's keys are not loaded, their blocks' scales are 0 (read as the least).
+// copies.  Boxes past the unit's keys are not loaded, their blocks' scales are
+// 0 (read as the least).
 template <int D, int KT>
 struct TileLoad8 {
   static constexpr int BLOCKS = KT / kScaleBlock;
-  static constexpr int ARRIVALS = 1 + BLOCKS;
+  static constexpr int ARRIVALS = 1 + BLOCKS;    // of a barrier for codes and scales
   // the lanes' pages: lane l has box l's, as TileLoad's
   __device__ static __forceinline__ int boxes(const TreeParams& P, const TreePiece& u, int tile) {
     const int keys = min(u.keys - tile * KT, KT);
@@ -52,36 +52,94 @@ struct TileLoad8 {
     if (P.status) atomicOr(P.status, DEV_CACHE);
     return P.n_pages;
   }
-  __device__ static __forceinline__ void issue(const TreeParams& P, const TreePiece& u, int tile, int lane,
-                                               int page, const CUtensorMap* tm, const float* scales,
-                                               uint32_t dst, uint32_t dst_scales, uint32_t bar, uint64_t policy) {
+  __device__ static __forceinline__ void issue(const TreeParams& P, const TreePiece& u, int tile, int lane, int page,
+                                               const CUtensorMap* tm, uint32_t dst, uint32_t bar, uint64_t policy) {
     const int n = boxes(P, u, tile);
     if (lane == 0) mbar_arrive_expect_tx(bar, (n << P.box_shift) * D);
     __syncwarp();
-    const int in_page = (1 << P.page_shift) - 1;
     if (lane < n)
-      tma_load_4d_hint(dst + (lane << P.box_shift) * D, tm, bar, 0, u.hk, (tile * KT + (lane << P.box_shift)) & in_page,
-                       page, policy);
+      tma_load_4d_hint(dst + (lane << P.box_shift) * D, tm, bar, 0, u.hk,
+                       (tile * KT + (lane << P.box_shift)) & ((1 << P.page_shift) - 1), page, policy);
+  }
+  // The tile's scales, block i's to dst + 4 i; landed() makes the barrier wait
+  // for all of them that were copied before.
+  __device__ static __forceinline__ void copy_scales(const TreeParams& P, const TreePiece& u, int tile, int lane,
+                                                     int page, const float* scales, uint32_t dst) {
     // block i of the tile lies in box i * 16 >> box_shift
     const int key = tile * KT + lane * kScaleBlock;
     const int pg = __shfl_sync(0xffffffffu, page, (lane * kScaleBlock) >> P.box_shift);
     if (lane < BLOCKS) {
       const bool there = pg < P.n_pages;
       const float* src = there ? scales + (((static_cast<int64_t>(pg) * P.Hkv + u.hk) << (P.page_shift - kScaleShift)) +
-                                           ((key & in_page) >> kScaleShift))
+                                           ((key & ((1 << P.page_shift) - 1)) >> kScaleShift))
                                : scales;
-      asm volatile(
-          "cp.async.ca.shared.global [%0], [%1], 4, %2;\n\t"
-          "cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%3];" ::"r"(dst_scales + lane * 4),
-          "l"(src), "r"(there ? 4 : 0), "r"(bar)
-          : "memory");
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst + lane * 4), "l"(src), "r"(there ? 4 : 0)
+                   : "memory");
     }
+  }
+  __device__ static __forceinline__ void landed(uint32_t bar, int lane) {
+    if (lane < BLOCKS) asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
   }
   // place of the 16-byte word c of row r of the tile
   __device__ static __forceinline__ uint32_t word16(int r, int c) {
     return D == 128 ? r * 128 + ((c ^ (r & 7)) << 4) : r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
   }
+  // A tile of codes at src to a tile of f16 at dst (slabs of 64 columns, KT *
+  // 128 bytes apart, with the 128-byte swizzle), by a warp: 8 rows of 4 words
+  // an instruction.  The rows of a group of eight lanes differ by 4 (d = 64:
+  // by 1), and of the two halves of a word a lane of the second row stores the
+  // second one first, so that loads and stores touch every bank once.
+  __device__ static __forceinline__ void to_f16(uint32_t src, uint32_t dst, int lane) {
+    const int w = lane & 3;
+    const int row0 = D == 128 ? 4 * ((lane >> 2) & 1) + (lane >> 3) : lane >> 2;
+    const int swap = D == 128 ? (lane >> 2) & 1 : 0;
+    constexpr int SLABS = D / 64, U = 4;
+#pragma unroll 1
+    for (int i0 = 0; i0 < KT / 8 * SLABS; i0 += U) {
+      uint4 x[U];
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        const int i = i0 + k, slab = i % SLABS, row = i / SLABS * 8 + row0;
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(x[k].x), "=r"(x[k].y), "=r"(x[k].z), "=r"(x[k].w)
+                     : "r"(src + word16(row, slab * 4 + w))
+                     : "memory");
+      }
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        const int i = i0 + k, slab = i % SLABS, row = i / SLABS * 8 + row0;
+        const uint32_t a[4] = {f16x2_of_e4m3x2(x[k].x), f16x2_of_e4m3x2(x[k].x >> 16), f16x2_of_e4m3x2(x[k].y),
+                               f16x2_of_e4m3x2(x[k].y >> 16)};
+        const uint32_t b[4] = {f16x2_of_e4m3x2(x[k].z), f16x2_of_e4m3x2(x[k].z >> 16), f16x2_of_e4m3x2(x[k].w),
+                               f16x2_of_e4m3x2(x[k].w >> 16)};
+        const uint32_t to = dst + slab * (KT * 128) + row * 128;
+        const int c = (2 * w) ^ (row & 7);
+        st_shared_v4(to + ((c ^ swap) << 4), swap ? b[0] : a[0], swap ? b[1] : a[1], swap ? b[2] : a[2],
+                     swap ? b[3] : a[3]);
+        st_shared_v4(to + ((c ^ 1 ^ swap) << 4), swap ? a[0] : b[0], swap ? a[1] : b[1], swap ? a[2] : b[2],
+                     swap ? a[3] : b[3]);
+      }
+    }
+  }
 };
+
+// What a tile's blocks bring to the softmax: sk, log2 sv, and what the sum of
+// the weights takes of P.
+__device__ __forceinline__ float4 block_factors(float sk, float sv) {
+  const float lv = __log2f(clamp_scale(sv));
+  return make_float4(clamp_scale(sk), lv, kPUndo * ex2(-lv), 0.f);
+}
+
+// The power of two that brings a row's largest element to [2^13, 2^14), top
+// being its bf16 bits without the sign (0: a row of zeros).
+__device__ __forceinline__ int row_shift(uint32_t top) {
+  return top ? min(13 - (static_cast<int>(top >> 7) - 127), 126) : 0;
+}
+__device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
+// Two bf16 times a factor, as f16.
+__device__ __forceinline__ uint32_t f16x2_of_bf16x2(uint32_t x, float mul) {
+  return pack_f16(__uint_as_float(x << 16) * mul, __uint_as_float(x & 0xffff0000u) * mul);
+}
 
 // ---------------------------------------------------------------- NaN of V
 // As fix_row of a bf16 cache: keys at or past `origin` are cleaned of NaN (the
@@ -89,11 +147,12 @@ struct TileLoad8 {
 // a key get it here.
 template <typename T>
 static __device__ __noinline__ void fix_row8(const Tree8Params& A, int b, int hk, int origin, const uint32_t* nf,
-                                             const uint32_t* seen, int c0, int n, T* row) {
+                                             uint4 s0, uint4 s1, int c0, int n, T* row) {
   const TreeParams& P = A.P;
 #pragma unroll 1
   for (int w = 0; w < 8; ++w) {
-    uint32_t bits = nf[w] & seen[w];
+    const uint4 s = w < 4 ? s0 : s1;
+    uint32_t bits = nf[w] & ((w & 3) == 0 ? s.x : (w & 3) == 1 ? s.y : (w & 3) == 2 ? s.z : s.w);
 #pragma unroll 1
     while (bits) {
       const int pos = origin + w * 32 + __ffs(bits) - 1;
@@ -109,6 +168,8 @@ static __device__ __noinline__ void fix_row8(const Tree8Params& A, int b, int hk
   }
 }
 
+fm_status launch_tree8_mid(const Tree8Params& A, int d, const CUtensorMap& tk, const CUtensorMap& tv, int grid,
+                           cudaStream_t s);        // up to 128 rows
 fm_status launch_tree8_narrow(const Tree8Params& A, int d, int rows, const CUtensorMap& tk, const CUtensorMap& tv,
                               int grid, cudaStream_t s);
 // Joins the parts that the first kernel left (fm_tree.cu); rows: of its units.

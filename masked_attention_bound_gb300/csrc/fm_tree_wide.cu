@@ -34,38 +34,61 @@
 // took 55.7 us so and 50.7 with one number, with d = 64 and 150 rows 74.7 and
 // 64.5.
 //
+// CODES: the cache holds e4m3 codes.  The loading warps bring tiles of codes
+// to stages of their own and turn them into f16 tiles, one in front of the
+// MMAs, laid out as the bf16 tiles are; the warp that loads K also works out
+// what each block's scales bring to the softmax.  See fm_tree8.cuh for the
+// arithmetic.  A tile of 64 keys takes a warp some 450 instructions, less than
+// its softmax.
+//
 // TMEM: S/P of slot s at column 128 s (SLOTS = 1: of every second tile at
 // column 64), the O's after the S's.
 #include <type_traits>
 
-#include "fm_tree.h"
+#include "fm_tree8.cuh"
 
 namespace fm {
 
-template <int D, int SLOTS_>
+template <int D, int SLOTS_, bool CODES_>
 struct WideCfg {
   static constexpr int SLOTS = SLOTS_;
+  static constexpr bool CODES = CODES_;
   static_assert(D == 128 || SLOTS == 1, "d = 64 runs with tiles of 128 rows side by side");
   using Geo = std::conditional_t<SLOTS == 2, WideGeo, MidGeo>;
   static constexpr int KT = Geo::KT;
   static constexpr int TILE = KT * D * 2;               // bytes of a K or V tile
   static constexpr int QTILE = 128 * D * 2;             // of a slot's Q
-  static constexpr int KSTAGES = D == 64 ? 4 : 2, VSTAGES = D == 64 ? 5 : 3;
+  static constexpr int KSTAGES = CODES ? (D == 64 ? 2 : 1) : D == 64 ? 4 : 2;
+  static constexpr int VSTAGES = CODES ? (D == 64 ? 2 : 1) : D == 64 ? 5 : 3;
+  // Barriers that tell that a V tile is there.  Two for a single stage: S of a
+  // tile may come while the V tile before is not there yet, and a wait tells a
+  // phase from the one before only.  (The V tile two before has been multiplied
+  // by then.)
+  static constexpr int VFULLS = VSTAGES == 1 ? 2 : VSTAGES;
+  static_assert(VFULLS == VSTAGES || SLOTS_ == 1, "the pairs' MMA warps wait by stage");
+  // stages of codes
+  static constexpr int CTILE = KT * D, KCODES = !CODES ? 0 : D == 64 ? 4 : 3, VCODES = !CODES ? 0 : D == 64 ? 4 : 2;
+  static constexpr int BLOCKS = KT / kScaleBlock;
   static constexpr int SM_WARPS = 4 * SLOTS;            // softmax
   static constexpr int THREADS = 32 * (SM_WARPS + 4);
-  static constexpr int BLOCKS = SLOTS == 2 ? 1 : 2;     // per SM
+  static constexpr int BLOCKS_PER_SM = SLOTS == 2 ? 1 : 2;
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_K = SLOTS * QTILE;
   static constexpr int OFF_V = OFF_K + KSTAGES * TILE;
-  static constexpr int OFF_ML = OFF_V + VSTAGES * TILE; // SLOTS 2: float2 [slot][128]
+  static constexpr int OFF_KC = OFF_V + VSTAGES * TILE;  // codes of K, then of V
+  static constexpr int OFF_VC = OFF_KC + KCODES * CTILE;
+  static constexpr int OFF_FACT = OFF_VC + VCODES * CTILE;                   // float4 [4][BLOCKS], see block_factors
+  static constexpr int OFF_SCALE = OFF_FACT + (CODES ? 4 * BLOCKS * 16 : 0); // float [KCODES][2][BLOCKS]
+  static constexpr int OFF_ML = OFF_SCALE + KCODES * 2 * BLOCKS * 4;         // SLOTS 2: float2 [slot][128]
   static constexpr int OFF_NF = OFF_ML + (SLOTS == 2 ? 2 * 128 * 8 : 0);   // [2][8] keys with values not finite
   static constexpr int OFF_BAR = OFF_NF + 64;
-  static constexpr int NBAR = 34;
+  static constexpr int NBAR = CODES ? 46 : 34;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;   // abort flag, TMEM address
   static constexpr int OFF_PAR = OFF_MISC + 16;         // int16 [256] parents of the unit's nodes
   static constexpr int USED = OFF_PAR + 512;
   static constexpr int SMEM = USED;
-  static_assert(BLOCKS * (SMEM + 1024) <= 228 * 1024, "blocks per SM");
+  static_assert(BLOCKS_PER_SM * (SMEM + 1024) <= 228 * 1024, "blocks per SM");
+  static_assert(KCODES <= 4 && VCODES <= 4, "barriers of the stages of codes");
   // O is written through 4 KB per softmax warp, in its slot's Q tile: that
   // slot's S have all been read by then
   static_assert(4 * 4096 <= QTILE, "room for the output's staging");
@@ -80,6 +103,7 @@ struct WideCfg {
 enum {
   W_QFULL = 0, W_SFULL = 2, W_PFULL = 4, W_PVDONE = 6, W_OEMPTY = 8, W_KFULL = 10, W_KEMPTY = 15,
   W_VFULL = 20, W_VEMPTY = 25, W_DRAIN = 30, W_TURN = 31, W_QEMPTY = 33,
+  W_KCODES = 34, W_VCODES = 38, W_FACT = 42,   // CODES: copies of codes; a tile's factors (4 sets)
   W_PVTILE = W_PVDONE + 1   // SLOTS 1: the PV of each tile (the SFULL and PFULL are its two buffers')
 };
 
@@ -111,13 +135,47 @@ __device__ __forceinline__ void slots_sync() {
   asm volatile("bar.sync 1, %0;" ::"n"(128 * SLOTS) : "memory");
 }
 
-template <int D, int SLOTS>
-__global__ void __launch_bounds__(WideCfg<D, SLOTS>::THREADS, WideCfg<D, SLOTS>::BLOCKS)
-    tree_wide_kernel(const __grid_constant__ TreeParams P, const __grid_constant__ CUtensorMap tmQ,
+template <bool CODES>
+using WideParams = std::conditional_t<CODES, Tree8Params, TreeParams>;
+__device__ __forceinline__ const TreeParams& tree_params(const TreeParams& A) { return A; }
+__device__ __forceinline__ const TreeParams& tree_params(const Tree8Params& A) { return A.P; }
+
+// Two f16 or bf16 that are not finite, for the cleaning of V.
+template <bool CODES>
+struct VClean {
+  static __device__ __forceinline__ uint32_t times_zero(uint32_t x, uint32_t sum) {
+    if constexpr (CODES) {
+      uint32_t y;
+      asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(y) : "r"(x), "r"(0u), "r"(sum));
+      return y;
+    } else {
+      return bf16x2_times_zero(x, sum);
+    }
+  }
+  static __device__ __forceinline__ bool found(uint32_t zero) {
+    if constexpr (CODES) return (zero & 0x7c00u) == 0x7c00u || (zero & 0x7c000000u) == 0x7c000000u;
+    else return bf16x2_not_finite(zero);
+  }
+  static __device__ __forceinline__ uint32_t clean(uint32_t x) {
+    if constexpr (CODES) {
+      if ((x & 0x7c00u) == 0x7c00u) x &= 0xffff0000u;
+      if ((x & 0x7c000000u) == 0x7c000000u) x &= 0xffffu;
+      return x;
+    } else {
+      return bf16x2_clean(x);
+    }
+  }
+};
+
+template <int D, int SLOTS, bool CODES>
+__global__ void __launch_bounds__(WideCfg<D, SLOTS, CODES>::THREADS, WideCfg<D, SLOTS, CODES>::BLOCKS_PER_SM)
+    tree_wide_kernel(const __grid_constant__ WideParams<CODES> A, const __grid_constant__ CUtensorMap tmQ,
                      const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV) {
-  using C = WideCfg<D, SLOTS>;
-  using Load = TileLoad<D, C::KT>;
+  using C = WideCfg<D, SLOTS, CODES>;
+  using Load = std::conditional_t<CODES, TileLoad8<D, C::KT>, TileLoad<D, C::KT>>;
+  using V16 = VClean<CODES>;
   constexpr int KT = C::KT;
+  const TreeParams& P = tree_params(A);
   extern __shared__ __align__(1024) uint8_t smem[];
   if (smem_u32(smem) & 1023u) {
     if (threadIdx.x == 0 && P.status) atomicOr(P.status, DEV_LAYOUT);
@@ -135,7 +193,7 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS>::THREADS, WideCfg<D, SLOTS>:
   // warps find out what their rows see: 512 units of 544 keys took 76 us so
   // and 82 us with these warps' copies.  (With two blocks per SM the other
   // block has the time: 50 us by their copies, 53 by TMA.)
-  const bool q_tma = SLOTS == 2 && P.q_tma;
+  const bool q_tma = SLOTS == 2 && !CODES && P.q_tma;
 
   if (warp == 2) touch_memory<D>(P, lane);
   if (tid == 0) {
@@ -153,9 +211,12 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS>::THREADS, WideCfg<D, SLOTS>:
       mbar_init(bar(W_KFULL + i), 1);
       mbar_init(bar(W_KEMPTY + i), SLOTS);
     }
-    for (int i = 0; i < C::VSTAGES; ++i) {
-      mbar_init(bar(W_VFULL + i), 1);
-      mbar_init(bar(W_VEMPTY + i), SLOTS);
+    for (int i = 0; i < C::VFULLS; ++i) mbar_init(bar(W_VFULL + i), 1);
+    for (int i = 0; i < C::VSTAGES; ++i) mbar_init(bar(W_VEMPTY + i), SLOTS);
+    if constexpr (CODES) {
+      for (int i = 0; i < C::KCODES; ++i) mbar_init(bar(W_KCODES + i), Load::ARRIVALS);
+      for (int i = 0; i < C::VCODES; ++i) mbar_init(bar(W_VCODES + i), 1);
+      for (int i = 0; i < 4; ++i) mbar_init(bar(W_FACT + i), 1);
     }
     mbar_init(bar(W_DRAIN), SLOTS);
     mbar_init(bar(W_QEMPTY), C::SM_WARPS);
@@ -186,46 +247,124 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS>::THREADS, WideCfg<D, SLOTS>:
 
   if (warp >= C::SM_WARPS) {
     regs_decrease<C::REGS_PRODUCER>();
-    if (warp == K_WARP || warp == V_WARP) {
-      // ---------------------------------------------------------- K / V loads
-      const bool isk = warp == K_WARP;
-      const int stages = isk ? C::KSTAGES : C::VSTAGES;
-      const int b_full = isk ? W_KFULL : W_VFULL, b_empty = isk ? W_KEMPTY : W_VEMPTY;
-      const uint32_t buf = sbase + (isk ? C::OFF_K : C::OFF_V);
-      const CUtensorMap* tm = isk ? &tmK : &tmV;
-      const uint64_t policy = policy_evict_first();
-      uint32_t st = 0, use = 0, issued = 0;    // stage, its uses so far, tiles issued
-      bool ok = true;
-      while (ok && u.next(P)) {
-        if (u.keys == 0) continue;
-        int page = Load::lane_page(P, u, u.t0, lane);
-#pragma unroll 1
-        for (int t = u.t0; t < u.t1; ++t) {
-          const int next = t + 1 < u.t1 ? Load::lane_page(P, u, t + 1, lane) : 0;
-          if (use > 0) ok = wait_all(b_empty + st, (use - 1) & 1);
-          if (!ok) break;
-          Load::issue(P, u, t, lane, page, tm, buf + st * C::TILE, bar(b_full + st), policy);
-          ++issued;
-          if (++st == stages) {
-            st = 0;
-            ++use;
+    if (CODES && (warp == K_WARP || warp == V_WARP)) {
+      // ---------------------------------------------------------- K / V loads, to f16
+      if constexpr (CODES) {
+        const bool isk = warp == K_WARP;
+        const uint32_t copies = isk ? C::KCODES : C::VCODES, stages = isk ? C::KSTAGES : C::VSTAGES;
+        const int b_codes = isk ? W_KCODES : W_VCODES;
+        const int b_full = isk ? W_KFULL : W_VFULL, b_empty = isk ? W_KEMPTY : W_VEMPTY;
+        const uint32_t codes = sbase + (isk ? C::OFF_KC : C::OFF_VC), buf = sbase + (isk ? C::OFF_K : C::OFF_V);
+        const float* scales = reinterpret_cast<const float*>(smem + C::OFF_SCALE);
+        float4* fact = reinterpret_cast<float4*>(smem + C::OFF_FACT);
+        const CUtensorMap* tm = isk ? &tmK : &tmV;
+        const uint64_t policy = policy_evict_first();
+        uint32_t issued = 0, done = 0;           // tiles: copies begun, turned into f16
+        uint32_t ist = 0, dst = 0, dph = 0, fst = 0, fuse = 0;   // their stages
+        bool ok = true, more = true;
+        int t = 0, t1 = 0, page = 0;
+        // the next tile to copy, and its boxes' pages
+        auto step = [&](bool first) {
+          if (!first && ++t < t1) {
+            page = Load::lane_page(P, u, t, lane);
+            return;
           }
-          page = next;
+          do more = u.next(P);
+          while (more && u.keys == 0);
+          if (!more) return;
+          t = u.t0;
+          t1 = u.t1;
+          page = Load::lane_page(P, u, t, lane);
+        };
+        step(true);
+        while (true) {
+          // a stage is free once its codes have been turned into f16
+          while (more && issued - done < copies) {
+            Load::issue(P, u, t, lane, page, tm, codes + ist * C::CTILE, bar(b_codes + ist), policy);
+            if (isk) {
+              const uint32_t to = sbase + C::OFF_SCALE + ist * (2 * C::BLOCKS * 4);
+              Load::copy_scales(P, u, t, lane, page, A.k_scale, to);
+              Load::copy_scales(P, u, t, lane, page, A.v_scale, to + C::BLOCKS * 4);
+              Load::landed(bar(b_codes + ist), lane);
+            }
+            ++issued;
+            if (++ist == copies) ist = 0;
+            step(false);
+          }
+          if (done == issued) break;
+          ok = wait_all(b_codes + dst, dph);
+          if (ok && fuse > 0) ok = wait_all(b_empty + fst, (fuse - 1) & 1);
+          if (!ok) break;
+          if (isk) {
+            // the softmax of the tile four before has read its factors: its P
+            // came before the S that freed this stage
+            if (lane < C::BLOCKS)
+              fact[(done & 3) * C::BLOCKS + lane] = block_factors(scales[dst * 2 * C::BLOCKS + lane],
+                                                                  scales[(dst * 2 + 1) * C::BLOCKS + lane]);
+            mbar_arrive_warp(bar(W_FACT + (done & 3)));
+          }
+          Load::to_f16(codes + dst * C::CTILE, buf + fst * C::TILE, lane);
+          fence_proxy_async_smem();
+          mbar_arrive_warp(bar(b_full + (isk ? fst : done % C::VFULLS)));
+          ++done;
+          if (++dst == copies) {
+            dst = 0;
+            dph ^= 1;
+          }
+          if (++fst == stages) {
+            fst = 0;
+            ++fuse;
+          }
         }
-      }
-      // every issued copy has landed before the block may exit
-      if (lane == 0)
+        // every issued copy has landed before the block may exit
+        if (lane == 0)
 #pragma unroll 1
-        for (uint32_t x = issued > stages ? issued - stages : 0; x < issued; ++x)
-          mbar_wait(bar(b_full + x % stages), (x / stages) & 1, P.status, P.wait_ns);
-      __syncwarp();
+          for (uint32_t x = done; x < issued; ++x)
+            mbar_wait(bar(b_codes + x % copies), (x / copies) & 1, P.status, P.wait_ns);
+        __syncwarp();
+      }
+    } else if (warp == K_WARP || warp == V_WARP) {
+      // ---------------------------------------------------------- K / V loads
+      if constexpr (!CODES) {
+        const bool isk = warp == K_WARP;
+        const int stages = isk ? C::KSTAGES : C::VSTAGES;
+        const int b_full = isk ? W_KFULL : W_VFULL, b_empty = isk ? W_KEMPTY : W_VEMPTY;
+        const uint32_t buf = sbase + (isk ? C::OFF_K : C::OFF_V);
+        const CUtensorMap* tm = isk ? &tmK : &tmV;
+        const uint64_t policy = policy_evict_first();
+        uint32_t st = 0, use = 0, issued = 0;    // stage, its uses so far, tiles issued
+        bool ok = true;
+        while (ok && u.next(P)) {
+          if (u.keys == 0) continue;
+          int page = Load::lane_page(P, u, u.t0, lane);
+#pragma unroll 1
+          for (int t = u.t0; t < u.t1; ++t) {
+            const int next = t + 1 < u.t1 ? Load::lane_page(P, u, t + 1, lane) : 0;
+            if (use > 0) ok = wait_all(b_empty + st, (use - 1) & 1);
+            if (!ok) break;
+            Load::issue(P, u, t, lane, page, tm, buf + st * C::TILE, bar(b_full + st), policy);
+            ++issued;
+            if (++st == stages) {
+              st = 0;
+              ++use;
+            }
+            page = next;
+          }
+        }
+        // every issued copy has landed before the block may exit
+        if (lane == 0)
+#pragma unroll 1
+          for (uint32_t x = issued > stages ? issued - stages : 0; x < issued; ++x)
+            mbar_wait(bar(b_full + x % stages), (x / stages) & 1, P.status, P.wait_ns);
+        __syncwarp();
+      }
     } else if (warp == MMA_WARP || (SLOTS == 2 && warp == MMA_WARP_B)) {
       // ---------------------------------------------------------- MMA issuers
       // The whole warp walks and waits, and one elected lane issues: the
       // descriptors are then uniform, and an MMA costs its issue only.
       const int s = warp == MMA_WARP ? 0 : 1;
-      constexpr uint32_t idS = idesc_bf16(128, KT, false, false);
-      constexpr uint32_t idPV = idesc_bf16(128, D, false, true);
+      constexpr uint32_t idS = CODES ? idesc_f16(128, KT, false, false) : idesc_bf16(128, KT, false, false);
+      constexpr uint32_t idPV = CODES ? idesc_f16(128, D, false, true) : idesc_bf16(128, D, false, true);
       const uint32_t dQ = sdesc_lo(sbase + C::OFF_Q + s * C::QTILE, 16);
       const uint32_t dK0 = sdesc_lo(sbase + C::OFF_K, 16);
       const uint32_t dV0 = sdesc_lo(sbase + C::OFF_V, KT * 128);
@@ -309,7 +448,7 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS>::THREADS, WideCfg<D, SLOTS>:
               if (!ok) break;
               issue_s(np + 1);
             }
-            ok = wait_all(W_VFULL + vs, vp);
+            ok = wait_all(W_VFULL + np % C::VFULLS, (np / C::VFULLS) & 1);
             // O is overwritten: the last piece's must have been read
             if (ok && x == 0 && pieces > 0) ok = wait_all(W_OEMPTY, (pieces - 1) & 1);
             if (ok) ok = wait_all(W_PFULL + (np & 1), (np >> 1) & 1);
@@ -479,6 +618,7 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS>::THREADS, WideCfg<D, SLOTS>:
       };
       const bool warp_live = __any_sync(0xffffffffu, live);
       float m_used = -INFINITY, l = 0.f;
+      [[maybe_unused]] float back = 0.f;               // CODES: the scale, and what undoes the row's shift
       if (active) {
         // Q, where the MMA warps do not fetch it (S of the slots' earlier
         // pieces has been read): a row is copied by D / 8 lanes, so that a
@@ -490,15 +630,40 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS>::THREADS, WideCfg<D, SLOTS>:
               P.q + (u.s.row0 + node) * P.q_stride[0] + static_cast<int64_t>(h) * P.q_stride[1];
           constexpr int LPR = D / 8, RPI = 32 / LPR;     // lanes a row, rows an instruction
           const unsigned in_rows = __ballot_sync(0xffffffffu, mine);
+          if constexpr (CODES) {
+            // to f16, a power of two per row; lane l keeps what undoes row l's
+#pragma unroll 4
+            for (int i = 0; i < 32 / RPI; ++i) {
+              const int from = i * RPI + lane / LPR;
+              const uint64_t row = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(src), from);
+              uint4 x = make_uint4(0u, 0u, 0u, 0u);
+              if ((in_rows >> from) & 1u) x = *reinterpret_cast<const uint4*>(row + (lane % LPR) * 16);
+              const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+              uint32_t top = 0;
+#pragma unroll
+              for (int y = 0; y < 4; ++y) top = max(top, max(w[y] & 0x7fffu, (w[y] >> 16) & 0x7fffu));
+#pragma unroll
+              for (int o = 1; o < LPR; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+              const int up = row_shift(top);
+              const float mul = pow2(up);
+              st_shared_v4(sbase + C::OFF_Q + slot * C::QTILE +
+                               sw128_offset(quarter * 32 + from, (lane % LPR) * 8, 128),
+                           f16x2_of_bf16x2(w[0], mul), f16x2_of_bf16x2(w[1], mul), f16x2_of_bf16x2(w[2], mul),
+                           f16x2_of_bf16x2(w[3], mul));
+              const int of = __shfl_sync(0xffffffffu, up, (lane % RPI) * LPR);
+              if (lane / RPI == i) back = pow2(-of) * P.scale_log2;
+            }
+          } else {
 #pragma unroll 2
-          for (int i = 0; i < 32 / RPI; ++i) {
-            const int from = i * RPI + lane / LPR;
-            const uint64_t row = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(src), from);
-            copy_async16(sbase + C::OFF_Q + slot * C::QTILE +
-                             sw128_offset(quarter * 32 + from, (lane % LPR) * 8, 128),
-                         row + (lane % LPR) * 16, (in_rows >> from) & 1u ? 16 : 0);
+            for (int i = 0; i < 32 / RPI; ++i) {
+              const int from = i * RPI + lane / LPR;
+              const uint64_t row = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(src), from);
+              copy_async16(sbase + C::OFF_Q + slot * C::QTILE +
+                               sw128_offset(quarter * 32 + from, (lane % LPR) * 8, 128),
+                           row + (lane % LPR) * 16, (in_rows >> from) & 1u ? 16 : 0);
+            }
+            copy_async_wait();
           }
-          copy_async_wait();
           fence_proxy_async_smem();
           mbar_arrive_warp(bar(W_QFULL + slot));
         }
@@ -546,41 +711,85 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS>::THREADS, WideCfg<D, SLOTS>:
 #pragma unroll
             for (int y = 0; y < KT / 32; ++y) tmem_ld32(tSj + 32 * y, raw + 32 * y);
             tmem_wait_ld();
-            float mx8[8];
+            float m_tile;
+            [[maybe_unused]] const float4* fact =
+                reinterpret_cast<const float4*>(smem + C::OFF_FACT) + ((e0 + x0) & 3) * C::BLOCKS;
+            // CODES: of a block's scores to x + log2 sv (the factor is kept
+            // finite: a score of 0 stays 0)
+            [[maybe_unused]] auto factor = [&](int b) { return fminf(back * fact[b].x, 0x1.fffffep127f); };
+            if constexpr (CODES) {
+              if (ok) ok = wait_all(W_FACT + ((e0 + x0) & 3), ((e0 + x0) >> 2) & 1);
+              m_tile = -INFINITY;
 #pragma unroll
-            for (int y = 0; y < 8; ++y) mx8[y] = fmax3(sv[y], sv[y + 8], sv[y + 16]);
+              for (int b = 0; b < C::BLOCKS; ++b) {
+                const float* s = sv + 16 * b;
+                float a[4];
 #pragma unroll
-            for (int c = 24; c < KT - 8; c += 16)
+                for (int y = 0; y < 4; ++y) a[y] = fmax3(s[y], s[y + 4], s[y + 8]);
 #pragma unroll
-              for (int y = 0; y < 8; ++y) mx8[y] = fmax3(mx8[y], sv[c + y], sv[c + 8 + y]);
+                for (int y = 0; y < 4; ++y) a[y] = fmaxf(a[y], s[y + 12]);
+                m_tile = fmaxf(m_tile, fmaf(fmax3(a[0], a[1], fmaxf(a[2], a[3])), factor(b), fact[b].y));
+              }
+            } else {
+              float mx8[8];
 #pragma unroll
-            for (int y = 0; y < 8; ++y) mx8[y] = fmaxf(mx8[y], sv[KT - 8 + y]);
-            const float mx = fmax3(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(mx8[3], mx8[4], mx8[5]),
-                                   fmaxf(mx8[6], mx8[7]));
+              for (int y = 0; y < 8; ++y) mx8[y] = fmax3(sv[y], sv[y + 8], sv[y + 16]);
+#pragma unroll
+              for (int c = 24; c < KT - 8; c += 16)
+#pragma unroll
+                for (int y = 0; y < 8; ++y) mx8[y] = fmax3(mx8[y], sv[c + y], sv[c + 8 + y]);
+#pragma unroll
+              for (int y = 0; y < 8; ++y) mx8[y] = fmaxf(mx8[y], sv[KT - 8 + y]);
+              const float mx = fmax3(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(mx8[3], mx8[4], mx8[5]),
+                                     fmaxf(mx8[6], mx8[7]));
+              m_tile = mx * P.scale_log2;
+            }
             // the reference moves only when the maximum grows by more than
             // 2^8 (as in the prompt forward): few tiles rescale O
-            const float m_tile = mx * P.scale_log2;
             const bool grow = m_tile > m_used + 8.f;
             const float m_new = grow ? m_tile : m_used;
             const float alpha = grow ? ex2(m_used - m_new) : 1.f;
             l *= alpha;
             m_used = m_new;
             const float m_ref = m_used == -INFINITY ? 0.f : m_used;
-            const uint64_t sc2 = splat2(P.scale_log2), nm2 = splat2(-m_ref);
             float sum4[4] = {0.f, 0.f, 0.f, 0.f};
+            if constexpr (CODES) {
 #pragma unroll
-            for (int c4 = 0; c4 < KT / 32; ++c4) {
-              uint32_t pk[16];
+              for (int c4 = 0; c4 < KT / 32; ++c4) {
+                uint32_t pk[16];
 #pragma unroll
-              for (int y = 0; y < 16; ++y) {
-                float a0, a1;
-                fma2_bc(a0, a1, sv[c4 * 32 + 2 * y], sv[c4 * 32 + 2 * y + 1], sc2, nm2);
-                const float p0 = ex2(a0), p1 = ex2(a1);
-                if (y & 1) add2_acc(sum4[2], sum4[3], p0, p1);
-                else add2_acc(sum4[0], sum4[1], p0, p1);
-                pk[y] = pack_bf16(p0, p1);   // P in bf16 for the product; the sum keeps 32 bits
+                for (int b = 2 * c4; b < 2 * c4 + 2; ++b) {
+                  const float4 f = fact[b];
+                  const uint64_t sc2 = splat2(factor(b)), nm2 = splat2(f.y - m_ref + kPOffset);
+                  float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+                  for (int y = 0; y < 8; ++y) {
+                    float a0, a1;
+                    fma2_bc(a0, a1, sv[b * 16 + 2 * y], sv[b * 16 + 2 * y + 1], sc2, nm2);
+                    const float p0 = ex2(a0), p1 = ex2(a1);
+                    add2_acc(s0, s1, p0, p1);
+                    pk[(b & 1) * 8 + y] = pack_f16(p0, p1);
+                  }
+                  sum4[b & 1] = fmaf(s0 + s1, f.z, sum4[b & 1]);
+                }
+                tmem_st16(tSj + c4 * 16, pk);
               }
-              tmem_st16(tSj + c4 * 16, pk);
+            } else {
+              const uint64_t sc2 = splat2(P.scale_log2), nm2 = splat2(-m_ref);
+#pragma unroll
+              for (int c4 = 0; c4 < KT / 32; ++c4) {
+                uint32_t pk[16];
+#pragma unroll
+                for (int y = 0; y < 16; ++y) {
+                  float a0, a1;
+                  fma2_bc(a0, a1, sv[c4 * 32 + 2 * y], sv[c4 * 32 + 2 * y + 1], sc2, nm2);
+                  const float p0 = ex2(a0), p1 = ex2(a1);
+                  if (y & 1) add2_acc(sum4[2], sum4[3], p0, p1);
+                  else add2_acc(sum4[0], sum4[1], p0, p1);
+                  pk[y] = pack_bf16(p0, p1);   // P in bf16 for the product; the sum keeps 32 bits
+                }
+                tmem_st16(tSj + c4 * 16, pk);
+              }
             }
             if (done > 0 && __any_sync(0xffffffffu, grow)) {
               // O holds the PVs of the earlier tiles; with two S buffers the
@@ -605,7 +814,7 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS>::THREADS, WideCfg<D, SLOTS>:
           if (partial && ok) {
             // clean row r of the V tile (see fix_row) before the product
             const uint32_t e = e0 + x0, st = e % C::VSTAGES;
-            ok = wait_all(W_VFULL + st, (e / C::VSTAGES) & 1);
+            ok = wait_all(W_VFULL + e % C::VFULLS, (e / C::VFULLS) & 1);
             if (ok) {
               const int key = t * KT + r, i = key - u.origin;
               // 16-byte words of the row, the slabs KT * 128 bytes apart; the
@@ -625,12 +834,12 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS>::THREADS, WideCfg<D, SLOTS>:
 #pragma unroll 4
                 for (int c = 0; c < D / 8; ++c) {
                   const uint4 y = *word(c);
-                  zero = bf16x2_times_zero(y.x, zero);
-                  zero = bf16x2_times_zero(y.y, zero);
-                  zero = bf16x2_times_zero(y.z, zero);
-                  zero = bf16x2_times_zero(y.w, zero);
+                  zero = V16::times_zero(y.x, zero);
+                  zero = V16::times_zero(y.y, zero);
+                  zero = V16::times_zero(y.z, zero);
+                  zero = V16::times_zero(y.w, zero);
                 }
-                dirty = bf16x2_not_finite(zero);
+                dirty = V16::found(zero);
               }
               if (dirty) {
                 // the flag first: whoever finds the row clean finds the flag
@@ -639,8 +848,8 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS>::THREADS, WideCfg<D, SLOTS>:
 #pragma unroll 1
                 for (int c = 0; c < D / 8; ++c) {
                   uint4* y = word(c);
-                  *y = make_uint4(bf16x2_clean(y->x), bf16x2_clean(y->y), bf16x2_clean(y->z),
-                                  bf16x2_clean(y->w));
+                  *y = make_uint4(V16::clean(y->x), V16::clean(y->y), V16::clean(y->z),
+                                  V16::clean(y->w));
                 }
               }
               fence_proxy_async_smem();
@@ -683,7 +892,8 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS>::THREADS, WideCfg<D, SLOTS>:
       tc_fence_after();
       const bool whole = u.whole();
       const bool writes = mine && ok;
-      const float inv = whole ? (l_out > 0.f ? 1.f / l_out : (l_out == 0.f ? 0.f : l_out)) : 1.f;
+      constexpr float undo = CODES ? kPUndo : 1.f;     // P's offset
+      const float inv = whole ? (l_out > 0.f ? undo / l_out : (l_out == 0.f ? 0.f : l_out)) : undo;
       const int slot_part = 2 * blockIdx.x + (u.t0 == 0 ? 1 : 0);
       const int64_t at = static_cast<int64_t>(slot_part) * P.part_rows + ur;
       float* const prow = P.part_o + at * D;
@@ -777,8 +987,13 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS>::THREADS, WideCfg<D, SLOTS>:
           row_sees(seen);
           const uint4 s0 = make_uint4(seen[0], seen[1], seen[2], seen[3]);
           const uint4 s1 = make_uint4(seen[4], seen[5], seen[6], seen[7]);
-          if (whole) fix_row(P, u.b, u.hk, u.origin, nf, s0, s1, c0, c1 - c0, orow + c0);
-          else fix_row(P, u.b, u.hk, u.origin, nf, s0, s1, c0, c1 - c0, prow + c0);
+          if constexpr (CODES) {
+            if (whole) fix_row8(A, u.b, u.hk, u.origin, nf, s0, s1, c0, c1 - c0, orow + c0);
+            else fix_row8(A, u.b, u.hk, u.origin, nf, s0, s1, c0, c1 - c0, prow + c0);
+          } else {
+            if (whole) fix_row(P, u.b, u.hk, u.origin, nf, s0, s1, c0, c1 - c0, orow + c0);
+            else fix_row(P, u.b, u.hk, u.origin, nf, s0, s1, c0, c1 - c0, prow + c0);
+          }
         }
       }
       if (tid == 0) leave_record(P, u);
@@ -796,11 +1011,11 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS>::THREADS, WideCfg<D, SLOTS>:
   }
 }
 
-template <int D, int SLOTS>
-static fm_status launch_wide_d(const TreeParams& P, const CUtensorMap& tq, const CUtensorMap& tk,
+template <int D, int SLOTS, bool CODES>
+static fm_status launch_wide_d(const WideParams<CODES>& P, const CUtensorMap& tq, const CUtensorMap& tk,
                                const CUtensorMap& tv, int grid, cudaStream_t s) {
-  using C = WideCfg<D, SLOTS>;
-  auto kern = tree_wide_kernel<D, SLOTS>;
+  using C = WideCfg<D, SLOTS, CODES>;
+  auto kern = tree_wide_kernel<D, SLOTS, CODES>;
   // the setmaxnreg split must fit in the registers the block launches with
   static std::atomic<uint64_t> ready{0};
   const fm_status st = prepare_kernel(kern, C::SMEM, C::MIN_LAUNCH_REGS, ready);
@@ -813,12 +1028,19 @@ static fm_status launch_wide_d(const TreeParams& P, const CUtensorMap& tq, const
 
 fm_status launch_tree_mid(const TreeParams& P, int d, const CUtensorMap& tq, const CUtensorMap& tk,
                           const CUtensorMap& tv, int grid, cudaStream_t s) {
-  return d == 64 ? launch_wide_d<64, 1>(P, tq, tk, tv, grid, s) : launch_wide_d<128, 1>(P, tq, tk, tv, grid, s);
+  return d == 64 ? launch_wide_d<64, 1, false>(P, tq, tk, tv, grid, s)
+                 : launch_wide_d<128, 1, false>(P, tq, tk, tv, grid, s);
 }
 
 fm_status launch_tree_wide(const TreeParams& P, const CUtensorMap& tq, const CUtensorMap& tk,
                            const CUtensorMap& tv, int grid, cudaStream_t s) {
-  return launch_wide_d<128, 2>(P, tq, tk, tv, grid, s);
+  return launch_wide_d<128, 2, false>(P, tq, tk, tv, grid, s);
+}
+
+fm_status launch_tree8_mid(const Tree8Params& A, int d, const CUtensorMap& tk, const CUtensorMap& tv, int grid,
+                           cudaStream_t s) {
+  return d == 64 ? launch_wide_d<64, 1, true>(A, tk, tk, tv, grid, s)
+                 : launch_wide_d<128, 1, true>(A, tk, tk, tv, grid, s);
 }
 
 }  // namespace fm
