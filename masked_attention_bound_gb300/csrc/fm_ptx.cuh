@@ -338,6 +338,12 @@ __device__ __forceinline__ uint32_t sdesc_lo(uint32_t saddr, uint32_t lbo) {
 __device__ __forceinline__ uint64_t sdesc_at(uint32_t lo, uint32_t bytes) {
   return (static_cast<uint64_t>(kSdescHi) << 32) | (lo + (bytes >> 4));
 }
+// The same for a K-major tile of rows of 64 bytes with the 64-byte swizzle
+// (e4m3, d = 64): sbo = 512.
+constexpr uint32_t kSdescHi64 = (512u >> 4) | (1u << 14) | (4u << 29);
+__device__ __forceinline__ uint64_t sdesc64_at(uint32_t lo, uint32_t bytes) {
+  return (static_cast<uint64_t>(kSdescHi64) << 32) | (lo + (bytes >> 4));
+}
 // Instruction descriptor of a kind::f8f6f4 MMA with e4m3 A and B (format
 // code 0 in both fields) and an f32 accumulator; both operands K-major.
 __host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N) {

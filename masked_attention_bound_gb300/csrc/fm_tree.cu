@@ -702,6 +702,7 @@ fm_status check_tree(const fm_cache* c, const fm_tree_desc* t) {
 
 // Workspace: the blocks' records, then their parts (two each).
 enum TreeKind { NARROW, MID, WIDE };
+int unit_rows(TreeKind k) { return k == NARROW ? NarrowGeo::R : k == MID ? MidGeo::R : WideGeo::R; }
 struct TreeWs {
   TreeKind kind;
   int rows;    // of a part: the largest unit's
@@ -762,9 +763,13 @@ size_t tree_ws_bound(const fm_cache& c, const fm_tree_desc& t, int sms) {
 TreeWs tree_ws8(const fm_cache& c, const fm_tree_desc& t, int sms) {
   const int64_t nodes = t.max_nodes < t.total ? t.max_nodes : t.total, rows = nodes * (t.H / c.Hkv);
   TreeWs W;
-  W.kind = rows <= NarrowGeo::R ? NARROW : MID;
-  W.rows = W.kind == NARROW ? NarrowGeo::R : rows >= MidGeo::R ? MidGeo::R : (static_cast<int>(rows) + 31) / 32 * 32;
-  W.grid = 2 * sms;
+  const int64_t tokens = static_cast<int64_t>(c.max_pages) * c.page_size;
+  W.kind = rows <= NarrowGeo::R ? NARROW : rows <= MidGeo::R || c.d == 64 || tokens <= 640 ? MID : WIDE;
+  W.rows = W.kind == NARROW ? NarrowGeo::R
+           : W.kind == WIDE ? (rows >= WideGeo::R ? WideGeo::R : (static_cast<int>(rows) + 31) / 32 * 32)
+           : rows >= MidGeo::R ? MidGeo::R
+                               : (static_cast<int>(rows) + 31) / 32 * 32;
+  W.grid = W.kind == WIDE ? sms : 2 * sms;
   tree_ws_places(W, c.d);
   return W;
 }
@@ -844,13 +849,11 @@ fm_status tree_fwd(const fm_cache* c, const fm_tree_desc* t, const void* q, cons
     if (!make_tmap_pool8(&tk, k_pool, c->n_pages, c->page_size, c->Hkv, c->d, c->k_stride + 1, box) ||
         !make_tmap_pool8(&tv, v_pool, c->n_pages, c->page_size, c->Hkv, c->d, c->v_stride + 1, box))
       return FM_ERR_CUDA;
-    if (W.kind == MID) {
-      st = launch_tree8_mid(A, c->d, tk, tv, grid, s);
-      return st != FM_OK ? st : launch_tree_join(P, c->d, MidGeo::R, grid, s);
-    }
     const int64_t rows = static_cast<int64_t>(t->max_nodes < t->total ? t->max_nodes : t->total) * P.G;
-    st = launch_tree8_narrow(A, c->d, rows < NarrowGeo::R ? static_cast<int>(rows) : NarrowGeo::R, tk, tv, grid, s);
-    return st != FM_OK ? st : launch_tree_join(P, c->d, NarrowGeo::R, grid, s);
+    if (W.kind == MID) st = launch_tree8_mid(A, c->d, tk, tv, grid, s);
+    else if (W.kind == WIDE) st = launch_tree8_wide(A, tk, tv, grid, s);
+    else st = launch_tree8_narrow(A, c->d, static_cast<int>(rows), tk, tv, grid, s);
+    return st != FM_OK ? st : launch_tree_join(P, c->d, unit_rows(W.kind), grid, s);
   }
   // one page of one head, or a tile's part of it, is a box of 64 columns
   const int box = W.kind == WIDE || c->page_size < MidGeo::KT ? c->page_size : MidGeo::KT;
@@ -876,7 +879,7 @@ fm_status tree_fwd(const fm_cache* c, const fm_tree_desc* t, const void* q, cons
   else if (W.kind == MID) st = launch_tree_mid(P, c->d, tq, tk, tv, grid, s);
   else st = launch_tree_wide(P, tq, tk, tv, grid, s);
   if (st != FM_OK) return st;
-  return launch_tree_join(P, c->d, W.kind == NARROW ? NarrowGeo::R : W.kind == MID ? MidGeo::R : WideGeo::R, grid, s);
+  return launch_tree_join(P, c->d, unit_rows(W.kind), grid, s);
 }
 
 }  // namespace

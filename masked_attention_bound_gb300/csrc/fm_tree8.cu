@@ -306,7 +306,7 @@ __global__ void __launch_bounds__(Narrow8Cfg<D, NT>::THREADS, 2)
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
               for (int y = 0; y < 4; ++y)
-                s[x][nt][y] = fmaf(s[x][nt][y], fminf(back[nt][y & 1] * f[x].x, 0x1.fffffep127f), f[x].y);
+                s[x][nt][y] = fmaf(s[x][nt][y], finite(back[nt][y & 1] * f[x].x), f[x].y);
           }
           if (t >= part0 || (t + 1) * KT > u.keys) {
             // keys past origin: only what the row sees

@@ -8,10 +8,16 @@
 // multiplied by its scale, and neither are K's: a factor per block and row
 // goes into the exponent's multiply-add.
 //
-// The products' operands are f16, which holds every code exactly.  Q is
-// multiplied by a power of two per row that brings its largest element to
-// 2^13 at least: every element within 2^-27 of that one then has all its bits
-// in f16, and what is below is off by 2^-38 of it at most.  P is offset by
+// The codes are exact operands: as they are for tcgen05.mma's S = Q K^T, as
+// f16 otherwise.  Q is multiplied by a power of two per row.  For the kernel of
+// few rows that brings its largest element to 2^13 at least, and it becomes
+// f16: every element within 2^-27 of the largest has all its bits, and what is
+// below is off by 2^-38 of it at most.  For tcgen05, whose operands have one
+// width, Q is the sum of two e4m3 numbers, the nearest one and the rest, with
+// the largest element at 2^7 or more: 4 and 4 of its 8 bits, exactly for
+// elements within 2^-9 of the largest, off by 2^-17 of it below.  (Two products
+// at the 8-bit rate take as long as one of f16, and K needs no conversion: with
+// f16 tiles of K too, 16 trees of 64 nodes took 373 us.)  P is f16 and offset by
 // 2^7 (R moves when the maximum has grown by more than 2^8), so that f16 holds
 // it with 11 bits down to 2^-21 of the largest and with an error of 2^-32 of
 // that below; its rounding, 2^-11 at most of a weight, is an eighth of the
@@ -136,6 +142,22 @@ __device__ __forceinline__ int row_shift(uint32_t top) {
   return top ? min(13 - (static_cast<int>(top >> 7) - 127), 126) : 0;
 }
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
+// Eight bf16 times a factor, as two parts of e4m3 whose sum they are: `hi` the
+// nearest code, `lo` the rest.
+__device__ __forceinline__ void split_e4m3(const uint32_t (&w)[4], float mul, uint2& hi, uint2& lo) {
+  uint32_t h[4], l[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float a = __uint_as_float(w[i] << 16) * mul, b = __uint_as_float(w[i] & 0xffff0000u) * mul;
+    h[i] = pack_e4m3x2(a, b);
+    const float2 r = float2_of_f16x2(f16x2_of_e4m3x2(h[i]));
+    l[i] = pack_e4m3x2(a - r.x, b - r.y);
+  }
+  hi = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
+  lo = make_uint2(l[0] | l[1] << 16, l[2] | l[3] << 16);
+}
+// A factor kept finite, so that a score of 0 stays 0 (NaN stays NaN).
+__device__ __forceinline__ float finite(float x) { return x > 0x1.fffffep127f ? 0x1.fffffep127f : x; }
 // Two bf16 times a factor, as f16.
 __device__ __forceinline__ uint32_t f16x2_of_bf16x2(uint32_t x, float mul) {
   return pack_f16(__uint_as_float(x << 16) * mul, __uint_as_float(x & 0xffff0000u) * mul);
@@ -170,6 +192,8 @@ static __device__ __noinline__ void fix_row8(const Tree8Params& A, int b, int hk
 
 fm_status launch_tree8_mid(const Tree8Params& A, int d, const CUtensorMap& tk, const CUtensorMap& tv, int grid,
                            cudaStream_t s);        // up to 128 rows
+fm_status launch_tree8_wide(const Tree8Params& A, const CUtensorMap& tk, const CUtensorMap& tv, int grid,
+                            cudaStream_t s);       // d = 128
 fm_status launch_tree8_narrow(const Tree8Params& A, int d, int rows, const CUtensorMap& tk, const CUtensorMap& tv,
                               int grid, cudaStream_t s);
 // Joins the parts that the first kernel left (fm_tree.cu); rows: of its units.

@@ -34,12 +34,11 @@
 // took 55.7 us so and 50.7 with one number, with d = 64 and 150 rows 74.7 and
 // 64.5.
 //
-// CODES: the cache holds e4m3 codes.  The loading warps bring tiles of codes
-// to stages of their own and turn them into f16 tiles, one in front of the
-// MMAs, laid out as the bf16 tiles are; the warp that loads K also works out
-// what each block's scales bring to the softmax.  See fm_tree8.cuh for the
-// arithmetic.  A tile of 64 keys takes a warp some 450 instructions, less than
-// its softmax.
+// CODES: the cache holds e4m3 codes (see fm_tree8.cuh for the arithmetic).  S
+// multiplies K's codes as they are.  The warp that loads V brings its codes to
+// stages of their own and turns them into f16 tiles in front of the MMAs, laid
+// out as the bf16 tiles are; it also works out what each block's scales bring to
+// the softmax.  A warp turns a tile of 64 x 128 codes in 910 cycles alone.
 //
 // TMEM: S/P of slot s at column 128 s (SLOTS = 1: of every second tile at
 // column 64), the O's after the S's.
@@ -56,39 +55,32 @@ struct WideCfg {
   static_assert(D == 128 || SLOTS == 1, "d = 64 runs with tiles of 128 rows side by side");
   using Geo = std::conditional_t<SLOTS == 2, WideGeo, MidGeo>;
   static constexpr int KT = Geo::KT;
-  static constexpr int TILE = KT * D * 2;               // bytes of a K or V tile
-  static constexpr int QTILE = 128 * D * 2;             // of a slot's Q
-  static constexpr int KSTAGES = CODES ? (D == 64 ? 2 : 1) : D == 64 ? 4 : 2;
-  static constexpr int VSTAGES = CODES ? (D == 64 ? 2 : 1) : D == 64 ? 5 : 3;
-  // Barriers that tell that a V tile is there.  Two for a single stage: S of a
-  // tile may come while the V tile before is not there yet, and a wait tells a
-  // phase from the one before only.  (The V tile two before has been multiplied
-  // by then.)
-  static constexpr int VFULLS = VSTAGES == 1 ? 2 : VSTAGES;
-  static_assert(VFULLS == VSTAGES || SLOTS_ == 1, "the pairs' MMA warps wait by stage");
-  // stages of codes
-  static constexpr int CTILE = KT * D, KCODES = !CODES ? 0 : D == 64 ? 4 : 3, VCODES = !CODES ? 0 : D == 64 ? 4 : 2;
+  static constexpr int TILE = KT * D * 2;               // bytes of a V tile in front of the MMAs
+  static constexpr int KTILE = CODES ? KT * D : TILE;   // of a K tile
+  static constexpr int QTILE = 128 * D * 2;             // of a slot's Q (CODES: two parts of one byte)
+  static constexpr int KSTAGES = CODES ? (D == 64 ? 5 : 3) : D == 64 ? 4 : 2;
+  static constexpr int VSTAGES = CODES ? 2 : D == 64 ? 5 : 3;
+  static constexpr int VCODES = !CODES ? 0 : D == 64 ? 4 : 2;   // stages of V's codes
   static constexpr int BLOCKS = KT / kScaleBlock;
   static constexpr int SM_WARPS = 4 * SLOTS;            // softmax
   static constexpr int THREADS = 32 * (SM_WARPS + 4);
   static constexpr int BLOCKS_PER_SM = SLOTS == 2 ? 1 : 2;
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_K = SLOTS * QTILE;
-  static constexpr int OFF_V = OFF_K + KSTAGES * TILE;
-  static constexpr int OFF_KC = OFF_V + VSTAGES * TILE;  // codes of K, then of V
-  static constexpr int OFF_VC = OFF_KC + KCODES * CTILE;
-  static constexpr int OFF_FACT = OFF_VC + VCODES * CTILE;                   // float4 [4][BLOCKS], see block_factors
-  static constexpr int OFF_SCALE = OFF_FACT + (CODES ? 4 * BLOCKS * 16 : 0); // float [KCODES][2][BLOCKS]
-  static constexpr int OFF_ML = OFF_SCALE + KCODES * 2 * BLOCKS * 4;         // SLOTS 2: float2 [slot][128]
+  static constexpr int OFF_V = OFF_K + KSTAGES * KTILE;
+  static constexpr int OFF_VC = OFF_V + VSTAGES * TILE;                      // V's codes
+  static constexpr int OFF_FACT = OFF_VC + VCODES * KTILE;                   // float4 [4][BLOCKS], see block_factors
+  static constexpr int OFF_SCALE = OFF_FACT + (CODES ? 4 * BLOCKS * 16 : 0); // float [VCODES][K, V][BLOCKS]
+  static constexpr int OFF_ML = OFF_SCALE + VCODES * 2 * BLOCKS * 4;         // SLOTS 2: float2 [slot][128]
   static constexpr int OFF_NF = OFF_ML + (SLOTS == 2 ? 2 * 128 * 8 : 0);   // [2][8] keys with values not finite
   static constexpr int OFF_BAR = OFF_NF + 64;
-  static constexpr int NBAR = CODES ? 46 : 34;
+  static constexpr int NBAR = CODES ? 42 : 34;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;   // abort flag, TMEM address
   static constexpr int OFF_PAR = OFF_MISC + 16;         // int16 [256] parents of the unit's nodes
   static constexpr int USED = OFF_PAR + 512;
   static constexpr int SMEM = USED;
   static_assert(BLOCKS_PER_SM * (SMEM + 1024) <= 228 * 1024, "blocks per SM");
-  static_assert(KCODES <= 4 && VCODES <= 4, "barriers of the stages of codes");
+  static_assert(KSTAGES <= 5 && VSTAGES <= 5 && VCODES <= 4, "barriers of the stages");
   // O is written through 4 KB per softmax warp, in its slot's Q tile: that
   // slot's S have all been read by then
   static_assert(4 * 4096 <= QTILE, "room for the output's staging");
@@ -103,7 +95,7 @@ struct WideCfg {
 enum {
   W_QFULL = 0, W_SFULL = 2, W_PFULL = 4, W_PVDONE = 6, W_OEMPTY = 8, W_KFULL = 10, W_KEMPTY = 15,
   W_VFULL = 20, W_VEMPTY = 25, W_DRAIN = 30, W_TURN = 31, W_QEMPTY = 33,
-  W_KCODES = 34, W_VCODES = 38, W_FACT = 42,   // CODES: copies of codes; a tile's factors (4 sets)
+  W_VCODES = 34, W_FACT = 38,   // CODES: copies of V's codes; a tile's factors (4 sets)
   W_PVTILE = W_PVDONE + 1   // SLOTS 1: the PV of each tile (the SFULL and PFULL are its two buffers')
 };
 
@@ -211,11 +203,12 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS, CODES>::THREADS, WideCfg<D, 
       mbar_init(bar(W_KFULL + i), 1);
       mbar_init(bar(W_KEMPTY + i), SLOTS);
     }
-    for (int i = 0; i < C::VFULLS; ++i) mbar_init(bar(W_VFULL + i), 1);
-    for (int i = 0; i < C::VSTAGES; ++i) mbar_init(bar(W_VEMPTY + i), SLOTS);
+    for (int i = 0; i < C::VSTAGES; ++i) {
+      mbar_init(bar(W_VFULL + i), 1);
+      mbar_init(bar(W_VEMPTY + i), SLOTS);
+    }
     if constexpr (CODES) {
-      for (int i = 0; i < C::KCODES; ++i) mbar_init(bar(W_KCODES + i), Load::ARRIVALS);
-      for (int i = 0; i < C::VCODES; ++i) mbar_init(bar(W_VCODES + i), 1);
+      for (int i = 0; i < C::VCODES; ++i) mbar_init(bar(W_VCODES + i), Load::ARRIVALS);
       for (int i = 0; i < 4; ++i) mbar_init(bar(W_FACT + i), 1);
     }
     mbar_init(bar(W_DRAIN), SLOTS);
@@ -247,17 +240,12 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS, CODES>::THREADS, WideCfg<D, 
 
   if (warp >= C::SM_WARPS) {
     regs_decrease<C::REGS_PRODUCER>();
-    if (CODES && (warp == K_WARP || warp == V_WARP)) {
-      // ---------------------------------------------------------- K / V loads, to f16
+    if (CODES && warp == V_WARP) {
+      // ---------------------------------------------------------- V loads, to f16
       if constexpr (CODES) {
-        const bool isk = warp == K_WARP;
-        const uint32_t copies = isk ? C::KCODES : C::VCODES, stages = isk ? C::KSTAGES : C::VSTAGES;
-        const int b_codes = isk ? W_KCODES : W_VCODES;
-        const int b_full = isk ? W_KFULL : W_VFULL, b_empty = isk ? W_KEMPTY : W_VEMPTY;
-        const uint32_t codes = sbase + (isk ? C::OFF_KC : C::OFF_VC), buf = sbase + (isk ? C::OFF_K : C::OFF_V);
+        const uint32_t codes = sbase + C::OFF_VC, buf = sbase + C::OFF_V;
         const float* scales = reinterpret_cast<const float*>(smem + C::OFF_SCALE);
         float4* fact = reinterpret_cast<float4*>(smem + C::OFF_FACT);
-        const CUtensorMap* tm = isk ? &tmK : &tmV;
         const uint64_t policy = policy_evict_first();
         uint32_t issued = 0, done = 0;           // tiles: copies begun, turned into f16
         uint32_t ist = 0, dst = 0, dph = 0, fst = 0, fuse = 0;   // their stages
@@ -279,39 +267,37 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS, CODES>::THREADS, WideCfg<D, 
         step(true);
         while (true) {
           // a stage is free once its codes have been turned into f16
-          while (more && issued - done < copies) {
-            Load::issue(P, u, t, lane, page, tm, codes + ist * C::CTILE, bar(b_codes + ist), policy);
-            if (isk) {
-              const uint32_t to = sbase + C::OFF_SCALE + ist * (2 * C::BLOCKS * 4);
-              Load::copy_scales(P, u, t, lane, page, A.k_scale, to);
-              Load::copy_scales(P, u, t, lane, page, A.v_scale, to + C::BLOCKS * 4);
-              Load::landed(bar(b_codes + ist), lane);
-            }
+          while (more && issued - done < C::VCODES) {
+            const uint32_t to = sbase + C::OFF_SCALE + ist * (2 * C::BLOCKS * 4);
+            Load::issue(P, u, t, lane, page, &tmV, codes + ist * C::KTILE, bar(W_VCODES + ist), policy);
+            Load::copy_scales(P, u, t, lane, page, A.k_scale, to);
+            Load::copy_scales(P, u, t, lane, page, A.v_scale, to + C::BLOCKS * 4);
+            Load::landed(bar(W_VCODES + ist), lane);
             ++issued;
-            if (++ist == copies) ist = 0;
+            if (++ist == C::VCODES) ist = 0;
             step(false);
           }
           if (done == issued) break;
-          ok = wait_all(b_codes + dst, dph);
-          if (ok && fuse > 0) ok = wait_all(b_empty + fst, (fuse - 1) & 1);
+          ok = wait_all(W_VCODES + dst, dph);
           if (!ok) break;
-          if (isk) {
-            // the softmax of the tile four before has read its factors: its P
-            // came before the S that freed this stage
-            if (lane < C::BLOCKS)
-              fact[(done & 3) * C::BLOCKS + lane] = block_factors(scales[dst * 2 * C::BLOCKS + lane],
-                                                                  scales[(dst * 2 + 1) * C::BLOCKS + lane]);
-            mbar_arrive_warp(bar(W_FACT + (done & 3)));
-          }
-          Load::to_f16(codes + dst * C::CTILE, buf + fst * C::TILE, lane);
+          // The softmax of the tile four before has read its factors: its P
+          // came before the PV of the tile three before, for which the last
+          // wait of the turn before was.
+          if (lane < C::BLOCKS)
+            fact[(done & 3) * C::BLOCKS + lane] = block_factors(scales[dst * 2 * C::BLOCKS + lane],
+                                                                scales[(dst * 2 + 1) * C::BLOCKS + lane]);
+          mbar_arrive_warp(bar(W_FACT + (done & 3)));
+          if (fuse > 0) ok = wait_all(W_VEMPTY + fst, (fuse - 1) & 1);
+          if (!ok) break;
+          Load::to_f16(codes + dst * C::KTILE, buf + fst * C::TILE, lane);
           fence_proxy_async_smem();
-          mbar_arrive_warp(bar(b_full + (isk ? fst : done % C::VFULLS)));
+          mbar_arrive_warp(bar(W_VFULL + fst));
           ++done;
-          if (++dst == copies) {
+          if (++dst == C::VCODES) {
             dst = 0;
             dph ^= 1;
           }
-          if (++fst == stages) {
+          if (++fst == C::VSTAGES) {
             fst = 0;
             ++fuse;
           }
@@ -320,55 +306,67 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS, CODES>::THREADS, WideCfg<D, 
         if (lane == 0)
 #pragma unroll 1
           for (uint32_t x = done; x < issued; ++x)
-            mbar_wait(bar(b_codes + x % copies), (x / copies) & 1, P.status, P.wait_ns);
+            mbar_wait(bar(W_VCODES + x % C::VCODES), (x / C::VCODES) & 1, P.status, P.wait_ns);
         __syncwarp();
       }
     } else if (warp == K_WARP || warp == V_WARP) {
       // ---------------------------------------------------------- K / V loads
-      if constexpr (!CODES) {
-        const bool isk = warp == K_WARP;
-        const int stages = isk ? C::KSTAGES : C::VSTAGES;
-        const int b_full = isk ? W_KFULL : W_VFULL, b_empty = isk ? W_KEMPTY : W_VEMPTY;
-        const uint32_t buf = sbase + (isk ? C::OFF_K : C::OFF_V);
-        const CUtensorMap* tm = isk ? &tmK : &tmV;
-        const uint64_t policy = policy_evict_first();
-        uint32_t st = 0, use = 0, issued = 0;    // stage, its uses so far, tiles issued
-        bool ok = true;
-        while (ok && u.next(P)) {
-          if (u.keys == 0) continue;
-          int page = Load::lane_page(P, u, u.t0, lane);
+      const bool isk = warp == K_WARP;
+      const int stages = isk ? C::KSTAGES : C::VSTAGES;
+      const int b_full = isk ? W_KFULL : W_VFULL, b_empty = isk ? W_KEMPTY : W_VEMPTY;
+      const uint32_t buf = sbase + (isk ? C::OFF_K : C::OFF_V);
+      const CUtensorMap* tm = isk ? &tmK : &tmV;
+      const uint64_t policy = policy_evict_first();
+      uint32_t st = 0, use = 0, issued = 0;    // stage, its uses so far, tiles issued
+      bool ok = true;
+      while (ok && u.next(P)) {
+        if (u.keys == 0) continue;
+        int page = Load::lane_page(P, u, u.t0, lane);
 #pragma unroll 1
-          for (int t = u.t0; t < u.t1; ++t) {
-            const int next = t + 1 < u.t1 ? Load::lane_page(P, u, t + 1, lane) : 0;
-            if (use > 0) ok = wait_all(b_empty + st, (use - 1) & 1);
-            if (!ok) break;
-            Load::issue(P, u, t, lane, page, tm, buf + st * C::TILE, bar(b_full + st), policy);
-            ++issued;
-            if (++st == stages) {
-              st = 0;
-              ++use;
-            }
-            page = next;
+        for (int t = u.t0; t < u.t1; ++t) {
+          const int next = t + 1 < u.t1 ? Load::lane_page(P, u, t + 1, lane) : 0;
+          if (use > 0) ok = wait_all(b_empty + st, (use - 1) & 1);
+          if (!ok) break;
+          Load::issue(P, u, t, lane, page, tm, buf + st * (isk ? C::KTILE : C::TILE), bar(b_full + st), policy);
+          ++issued;
+          if (++st == stages) {
+            st = 0;
+            ++use;
           }
+          page = next;
         }
-        // every issued copy has landed before the block may exit
-        if (lane == 0)
-#pragma unroll 1
-          for (uint32_t x = issued > stages ? issued - stages : 0; x < issued; ++x)
-            mbar_wait(bar(b_full + x % stages), (x / stages) & 1, P.status, P.wait_ns);
-        __syncwarp();
       }
+      // every issued copy has landed before the block may exit
+      if (lane == 0)
+#pragma unroll 1
+        for (uint32_t x = issued > stages ? issued - stages : 0; x < issued; ++x)
+          mbar_wait(bar(b_full + x % stages), (x / stages) & 1, P.status, P.wait_ns);
+      __syncwarp();
     } else if (warp == MMA_WARP || (SLOTS == 2 && warp == MMA_WARP_B)) {
       // ---------------------------------------------------------- MMA issuers
       // The whole warp walks and waits, and one elected lane issues: the
       // descriptors are then uniform, and an MMA costs its issue only.
       const int s = warp == MMA_WARP ? 0 : 1;
-      constexpr uint32_t idS = CODES ? idesc_f16(128, KT, false, false) : idesc_bf16(128, KT, false, false);
+      constexpr uint32_t idS = CODES ? idesc_e4m3(128, KT) : idesc_bf16(128, KT, false, false);
       constexpr uint32_t idPV = CODES ? idesc_f16(128, D, false, true) : idesc_bf16(128, D, false, true);
       const uint32_t dQ = sdesc_lo(sbase + C::OFF_Q + s * C::QTILE, 16);
       const uint32_t dK0 = sdesc_lo(sbase + C::OFF_K, 16);
       const uint32_t dV0 = sdesc_lo(sbase + C::OFF_V, KT * 128);
       const uint32_t tS = tbase + 128 * s, tO = tbase + C::T_O + 128 * s;
+      // Step i of SSTEPS of S (CODES: of Q's first part, then of its second)
+      constexpr int SSTEPS = D / 16;
+      auto s_step = [&](uint32_t to, uint32_t dK, int i) {
+        if constexpr (CODES) {
+          const int part = i / (D / 32), kk = i % (D / 32);
+          if constexpr (D == 128)
+            mma_ss_f8(to, sdesc_at(dQ, part * (128 * D) + kk * 32), sdesc_at(dK, kk * 32), idS, i > 0 ? 1u : 0u);
+          else
+            mma_ss_f8(to, sdesc64_at(dQ, part * (128 * D) + kk * 32), sdesc64_at(dK, kk * 32), idS, i > 0 ? 1u : 0u);
+        } else {
+          mma_ss(to, sdesc_at(dQ, (i >> 2) * (128 * 128) + (i & 3) * 32),
+                 sdesc_at(dK, (i >> 2) * (KT * 128) + (i & 3) * 32), idS, i > 0 ? 1u : 0u);
+        }
+      };
       uint32_t kst = 0, kph = 0, vst = 0, vph = 0;   // stages and phases of the next tile of the block
       uint32_t pieces = 0;      // pieces with keys before this one
       uint32_t qn = 0, np = 0;  // Q tiles, P tiles of this slot so far
@@ -426,13 +424,11 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS, CODES>::THREADS, WideCfg<D, 
           // S of tile x + 1 overwrites P of tile x - 1, whose PV this warp has
           // issued before; then PV of tile x
           auto issue_s = [&](uint32_t tile) {
-            const uint32_t dK = dK0 + ks * (C::TILE >> 4);
+            const uint32_t dK = dK0 + ks * (C::KTILE >> 4);
             tc_fence_after();
             if (elect_one()) {
 #pragma unroll
-              for (int kk = 0; kk < D / 16; ++kk)
-                mma_ss(tS + 64 * (tile & 1), sdesc_at(dQ, (kk >> 2) * (128 * 128) + (kk & 3) * 32),
-                       sdesc_at(dK, (kk >> 2) * (KT * 128) + (kk & 3) * 32), idS, kk > 0 ? 1u : 0u);
+              for (int kk = 0; kk < SSTEPS; ++kk) s_step(tS + 64 * (tile & 1), dK, kk);
               mma_commit(bar(W_SFULL + (tile & 1)));
               mma_commit(bar(W_KEMPTY + ks));
             }
@@ -448,7 +444,7 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS, CODES>::THREADS, WideCfg<D, 
               if (!ok) break;
               issue_s(np + 1);
             }
-            ok = wait_all(W_VFULL + np % C::VFULLS, (np / C::VFULLS) & 1);
+            ok = wait_all(W_VFULL + vs, vp);
             // O is overwritten: the last piece's must have been read
             if (ok && x == 0 && pieces > 0) ok = wait_all(W_OEMPTY, (pieces - 1) & 1);
             if (ok) ok = wait_all(W_PFULL + (np & 1), (np >> 1) & 1);
@@ -516,15 +512,14 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS, CODES>::THREADS, WideCfg<D, 
               if (!ok) break;
               tc_fence_after();
             }
-            const uint32_t dK = dK0 + ks * (C::TILE >> 4);
+            const uint32_t dK = dK0 + ks * (C::KTILE >> 4);
             if (elect_one()) {
 #pragma unroll
-              for (int kk = 0; kk < D / 16; ++kk) {
-                mma_ss(tS, sdesc_at(dQ, (kk >> 2) * (128 * 128) + (kk & 3) * 32),
-                       sdesc_at(dK, (kk >> 2) * (KT * 128) + (kk & 3) * 32), idS, kk > 0 ? 1u : 0u);
+              for (int kk = 0; kk < SSTEPS; ++kk) {
+                s_step(tS, dK, kk);
                 // the turn passes a little early: the other warp needs some
                 // 250 cycles to notice
-                if (SLOTS == 2 && kk == D / 16 - 4 && !given) mbar_arrive(bar(W_TURN + s));
+                if (SLOTS == 2 && kk == SSTEPS - 4 && !given) mbar_arrive(bar(W_TURN + s));
               }
               mma_commit(bar(W_SFULL + s));
               mma_commit(bar(W_KEMPTY + ks));
@@ -631,7 +626,7 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS, CODES>::THREADS, WideCfg<D, 
           constexpr int LPR = D / 8, RPI = 32 / LPR;     // lanes a row, rows an instruction
           const unsigned in_rows = __ballot_sync(0xffffffffu, mine);
           if constexpr (CODES) {
-            // to f16, a power of two per row; lane l keeps what undoes row l's
+            // to two parts, a power of two per row; lane l keeps what undoes row l's
 #pragma unroll 4
             for (int i = 0; i < 32 / RPI; ++i) {
               const int from = i * RPI + lane / LPR;
@@ -644,14 +639,17 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS, CODES>::THREADS, WideCfg<D, 
               for (int y = 0; y < 4; ++y) top = max(top, max(w[y] & 0x7fffu, (w[y] >> 16) & 0x7fffu));
 #pragma unroll
               for (int o = 1; o < LPR; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-              const int up = row_shift(top);
-              const float mul = pow2(up);
-              st_shared_v4(sbase + C::OFF_Q + slot * C::QTILE +
-                               sw128_offset(quarter * 32 + from, (lane % LPR) * 8, 128),
-                           f16x2_of_bf16x2(w[0], mul), f16x2_of_bf16x2(w[1], mul), f16x2_of_bf16x2(w[2], mul),
-                           f16x2_of_bf16x2(w[3], mul));
-              const int of = __shfl_sync(0xffffffffu, up, (lane % RPI) * LPR);
-              if (lane / RPI == i) back = pow2(-of) * P.scale_log2;
+              const int up = row_shift(top) - 6;       // the largest at [2^7, 2^8)
+              uint2 hi, lo;
+              split_e4m3(w, pow2(up), hi, lo);
+              uint8_t* to = smem + C::OFF_Q + slot * C::QTILE + Load::word16(quarter * 32 + from, (lane % LPR) >> 1) +
+                            (lane & 1) * 8;
+              *reinterpret_cast<uint2*>(to) = hi;
+              *reinterpret_cast<uint2*>(to + 128 * D) = lo;
+              // (an infinity has no code: its row becomes NaN, as its scores are)
+              const float undo = top < 0x7f80u ? pow2(-up) * P.scale_log2 : __int_as_float(0x7fc00000);
+              const float of = __shfl_sync(0xffffffffu, undo, (lane % RPI) * LPR);
+              if (lane / RPI == i) back = of;
             }
           } else {
 #pragma unroll 2
@@ -716,7 +714,7 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS, CODES>::THREADS, WideCfg<D, 
                 reinterpret_cast<const float4*>(smem + C::OFF_FACT) + ((e0 + x0) & 3) * C::BLOCKS;
             // CODES: of a block's scores to x + log2 sv (the factor is kept
             // finite: a score of 0 stays 0)
-            [[maybe_unused]] auto factor = [&](int b) { return fminf(back * fact[b].x, 0x1.fffffep127f); };
+            [[maybe_unused]] auto factor = [&](int b) { return finite(back * fact[b].x); };
             if constexpr (CODES) {
               if (ok) ok = wait_all(W_FACT + ((e0 + x0) & 3), ((e0 + x0) >> 2) & 1);
               m_tile = -INFINITY;
@@ -814,7 +812,7 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS, CODES>::THREADS, WideCfg<D, 
           if (partial && ok) {
             // clean row r of the V tile (see fix_row) before the product
             const uint32_t e = e0 + x0, st = e % C::VSTAGES;
-            ok = wait_all(W_VFULL + e % C::VFULLS, (e / C::VFULLS) & 1);
+            ok = wait_all(W_VFULL + st, (e / C::VSTAGES) & 1);
             if (ok) {
               const int key = t * KT + r, i = key - u.origin;
               // 16-byte words of the row, the slabs KT * 128 bytes apart; the
@@ -1035,6 +1033,11 @@ fm_status launch_tree_mid(const TreeParams& P, int d, const CUtensorMap& tq, con
 fm_status launch_tree_wide(const TreeParams& P, const CUtensorMap& tq, const CUtensorMap& tk,
                            const CUtensorMap& tv, int grid, cudaStream_t s) {
   return launch_wide_d<128, 2, false>(P, tq, tk, tv, grid, s);
+}
+
+fm_status launch_tree8_wide(const Tree8Params& A, const CUtensorMap& tk, const CUtensorMap& tv, int grid,
+                            cudaStream_t s) {
+  return launch_wide_d<128, 2, true>(A, tk, tk, tv, grid, s);
 }
 
 fm_status launch_tree8_mid(const Tree8Params& A, int d, const CUtensorMap& tk, const CUtensorMap& tv, int grid,
