@@ -90,41 +90,39 @@ struct TileLoad8 {
   __device__ static __forceinline__ uint32_t word16(int r, int c) {
     return D == 128 ? r * 128 + ((c ^ (r & 7)) << 4) : r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
   }
-  // A tile of codes at src to a tile of f16 at dst (slabs of 64 columns, KT *
-  // 128 bytes apart, with the 128-byte swizzle), by a warp: 8 rows of 4 words
-  // an instruction.  The rows of a group of eight lanes differ by 4 (d = 64:
-  // by 1), and of the two halves of a word a lane of the second row stores the
-  // second one first, so that loads and stores touch every bank once.
-  __device__ static __forceinline__ void to_f16(uint32_t src, uint32_t dst, int lane) {
+  // Rows [r0, r0 + ROWS) of a tile of codes at src to a tile of f16 at dst
+  // (slabs of 64 columns, KT * 128 bytes apart, with the 128-byte swizzle), by a
+  // warp: 8 rows of 4 words an instruction.  The rows of a group of eight lanes
+  // differ by 4 (d = 64: by 1), and of the two halves of a word a lane of the
+  // second row stores the second one first, so that loads and stores touch every
+  // bank once.  `clean`(row, word): called for each word of 16 codes.
+  template <int ROWS, typename F>
+  __device__ static __forceinline__ void to_f16(uint32_t src, uint32_t dst, int r0, int lane, F clean) {
     const int w = lane & 3;
-    const int row0 = D == 128 ? 4 * ((lane >> 2) & 1) + (lane >> 3) : lane >> 2;
-    const int swap = D == 128 ? (lane >> 2) & 1 : 0;
-    constexpr int SLABS = D / 64, U = 4;
-#pragma unroll 1
-    for (int i0 = 0; i0 < KT / 8 * SLABS; i0 += U) {
-      uint4 x[U];
+    const int row0 = r0 + (D == 128 ? 4 * ((lane >> 2) & 1) + (lane >> 3) : lane >> 2);
+    const bool swap = D == 128 && ((lane >> 2) & 1);
+    constexpr int SLABS = D / 64, N = ROWS / 8 * SLABS;
+    uint4 x[N];
 #pragma unroll
-      for (int k = 0; k < U; ++k) {
-        const int i = i0 + k, slab = i % SLABS, row = i / SLABS * 8 + row0;
-        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(x[k].x), "=r"(x[k].y), "=r"(x[k].z), "=r"(x[k].w)
-                     : "r"(src + word16(row, slab * 4 + w))
-                     : "memory");
-      }
+    for (int i = 0; i < N; ++i)
+      asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(x[i].x), "=r"(x[i].y), "=r"(x[i].z), "=r"(x[i].w)
+                   : "r"(src + word16(row0 + i / SLABS * 8, i % SLABS * 4 + w))
+                   : "memory");
 #pragma unroll
-      for (int k = 0; k < U; ++k) {
-        const int i = i0 + k, slab = i % SLABS, row = i / SLABS * 8 + row0;
-        const uint32_t a[4] = {f16x2_of_e4m3x2(x[k].x), f16x2_of_e4m3x2(x[k].x >> 16), f16x2_of_e4m3x2(x[k].y),
-                               f16x2_of_e4m3x2(x[k].y >> 16)};
-        const uint32_t b[4] = {f16x2_of_e4m3x2(x[k].z), f16x2_of_e4m3x2(x[k].z >> 16), f16x2_of_e4m3x2(x[k].w),
-                               f16x2_of_e4m3x2(x[k].w >> 16)};
-        const uint32_t to = dst + slab * (KT * 128) + row * 128;
-        const int c = (2 * w) ^ (row & 7);
-        st_shared_v4(to + ((c ^ swap) << 4), swap ? b[0] : a[0], swap ? b[1] : a[1], swap ? b[2] : a[2],
-                     swap ? b[3] : a[3]);
-        st_shared_v4(to + ((c ^ 1 ^ swap) << 4), swap ? a[0] : b[0], swap ? a[1] : b[1], swap ? a[2] : b[2],
-                     swap ? a[3] : b[3]);
-      }
+    for (int i = 0; i < N; ++i) {
+      const int slab = i % SLABS, row = row0 + i / SLABS * 8;
+      clean(row, x[i]);
+      const uint32_t a[4] = {f16x2_of_e4m3x2(x[i].x), f16x2_of_e4m3x2(x[i].x >> 16), f16x2_of_e4m3x2(x[i].y),
+                             f16x2_of_e4m3x2(x[i].y >> 16)};
+      const uint32_t b[4] = {f16x2_of_e4m3x2(x[i].z), f16x2_of_e4m3x2(x[i].z >> 16), f16x2_of_e4m3x2(x[i].w),
+                             f16x2_of_e4m3x2(x[i].w >> 16)};
+      const uint32_t to = dst + slab * (KT * 128) + row * 128;
+      const int c = (2 * w) ^ (row & 7);
+      st_shared_v4(to + ((c ^ swap) << 4), swap ? b[0] : a[0], swap ? b[1] : a[1], swap ? b[2] : a[2],
+                   swap ? b[3] : a[3]);
+      st_shared_v4(to + ((c ^ 1 ^ swap) << 4), swap ? a[0] : b[0], swap ? a[1] : b[1], swap ? a[2] : b[2],
+                   swap ? a[3] : b[3]);
     }
   }
 };

@@ -35,10 +35,11 @@
 // 64.5.
 //
 // CODES: the cache holds e4m3 codes (see fm_tree8.cuh for the arithmetic).  S
-// multiplies K's codes as they are.  The warp that loads V brings its codes to
-// stages of their own and turns them into f16 tiles in front of the MMAs, laid
-// out as the bf16 tiles are; it also works out what each block's scales bring to
-// the softmax.  A warp turns a tile of 64 x 128 codes in 910 cycles alone.
+// multiplies K's codes as they are.  V's go to stages of their own, and the
+// softmax warps turn them into f16 tiles in front of the MMAs, laid out as the
+// bf16 tiles are, 16 rows a warp, while S of the tile is multiplied.  (A warp of
+// its own for that took 910 cycles for 64 x 128 codes alone, and among the
+// softmax warps longer than their work: 16 trees of 64 nodes 286 us.)
 //
 // TMEM: S/P of slot s at column 128 s (SLOTS = 1: of every second tile at
 // column 64), the O's after the S's.
@@ -69,8 +70,9 @@ struct WideCfg {
   static constexpr int OFF_K = SLOTS * QTILE;
   static constexpr int OFF_V = OFF_K + KSTAGES * KTILE;
   static constexpr int OFF_VC = OFF_V + VSTAGES * TILE;                      // V's codes
-  static constexpr int OFF_FACT = OFF_VC + VCODES * KTILE;                   // float4 [4][BLOCKS], see block_factors
-  static constexpr int OFF_SCALE = OFF_FACT + (CODES ? 4 * BLOCKS * 16 : 0); // float [VCODES][K, V][BLOCKS]
+  // of each softmax warp, a tile's float4 [BLOCKS] (see block_factors)
+  static constexpr int OFF_FACT = OFF_VC + VCODES * KTILE;
+  static constexpr int OFF_SCALE = OFF_FACT + (CODES ? 4 * SLOTS * BLOCKS * 16 : 0);   // float [VCODES][K, V][BLOCKS]
   static constexpr int OFF_ML = OFF_SCALE + VCODES * 2 * BLOCKS * 4;         // SLOTS 2: float2 [slot][128]
   static constexpr int OFF_NF = OFF_ML + (SLOTS == 2 ? 2 * 128 * 8 : 0);   // [2][8] keys with values not finite
   static constexpr int OFF_BAR = OFF_NF + 64;
@@ -95,7 +97,7 @@ struct WideCfg {
 enum {
   W_QFULL = 0, W_SFULL = 2, W_PFULL = 4, W_PVDONE = 6, W_OEMPTY = 8, W_KFULL = 10, W_KEMPTY = 15,
   W_VFULL = 20, W_VEMPTY = 25, W_DRAIN = 30, W_TURN = 31, W_QEMPTY = 33,
-  W_VCODES = 34, W_FACT = 38,   // CODES: copies of V's codes; a tile's factors (4 sets)
+  W_VCODES = 34, W_VCEMPTY = 38,   // CODES: stages of V's codes
   W_PVTILE = W_PVDONE + 1   // SLOTS 1: the PV of each tile (the SFULL and PFULL are its two buffers')
 };
 
@@ -132,40 +134,12 @@ using WideParams = std::conditional_t<CODES, Tree8Params, TreeParams>;
 __device__ __forceinline__ const TreeParams& tree_params(const TreeParams& A) { return A; }
 __device__ __forceinline__ const TreeParams& tree_params(const Tree8Params& A) { return A.P; }
 
-// Two f16 or bf16 that are not finite, for the cleaning of V.
-template <bool CODES>
-struct VClean {
-  static __device__ __forceinline__ uint32_t times_zero(uint32_t x, uint32_t sum) {
-    if constexpr (CODES) {
-      uint32_t y;
-      asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(y) : "r"(x), "r"(0u), "r"(sum));
-      return y;
-    } else {
-      return bf16x2_times_zero(x, sum);
-    }
-  }
-  static __device__ __forceinline__ bool found(uint32_t zero) {
-    if constexpr (CODES) return (zero & 0x7c00u) == 0x7c00u || (zero & 0x7c000000u) == 0x7c000000u;
-    else return bf16x2_not_finite(zero);
-  }
-  static __device__ __forceinline__ uint32_t clean(uint32_t x) {
-    if constexpr (CODES) {
-      if ((x & 0x7c00u) == 0x7c00u) x &= 0xffff0000u;
-      if ((x & 0x7c000000u) == 0x7c000000u) x &= 0xffffu;
-      return x;
-    } else {
-      return bf16x2_clean(x);
-    }
-  }
-};
-
 template <int D, int SLOTS, bool CODES>
 __global__ void __launch_bounds__(WideCfg<D, SLOTS, CODES>::THREADS, WideCfg<D, SLOTS, CODES>::BLOCKS_PER_SM)
     tree_wide_kernel(const __grid_constant__ WideParams<CODES> A, const __grid_constant__ CUtensorMap tmQ,
                      const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV) {
   using C = WideCfg<D, SLOTS, CODES>;
   using Load = std::conditional_t<CODES, TileLoad8<D, C::KT>, TileLoad<D, C::KT>>;
-  using V16 = VClean<CODES>;
   constexpr int KT = C::KT;
   const TreeParams& P = tree_params(A);
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -204,12 +178,14 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS, CODES>::THREADS, WideCfg<D, 
       mbar_init(bar(W_KEMPTY + i), SLOTS);
     }
     for (int i = 0; i < C::VSTAGES; ++i) {
-      mbar_init(bar(W_VFULL + i), 1);
+      mbar_init(bar(W_VFULL + i), CODES ? C::SM_WARPS : 1);   // CODES: the softmax warps make the tile
       mbar_init(bar(W_VEMPTY + i), SLOTS);
     }
     if constexpr (CODES) {
-      for (int i = 0; i < C::VCODES; ++i) mbar_init(bar(W_VCODES + i), Load::ARRIVALS);
-      for (int i = 0; i < 4; ++i) mbar_init(bar(W_FACT + i), 1);
+      for (int i = 0; i < C::VCODES; ++i) {
+        mbar_init(bar(W_VCODES + i), Load::ARRIVALS);
+        mbar_init(bar(W_VCEMPTY + i), C::SM_WARPS);
+      }
     }
     mbar_init(bar(W_DRAIN), SLOTS);
     mbar_init(bar(W_QEMPTY), C::SM_WARPS);
@@ -240,81 +216,13 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS, CODES>::THREADS, WideCfg<D, 
 
   if (warp >= C::SM_WARPS) {
     regs_decrease<C::REGS_PRODUCER>();
-    if (CODES && warp == V_WARP) {
-      // ---------------------------------------------------------- V loads, to f16
-      if constexpr (CODES) {
-        const uint32_t codes = sbase + C::OFF_VC, buf = sbase + C::OFF_V;
-        const float* scales = reinterpret_cast<const float*>(smem + C::OFF_SCALE);
-        float4* fact = reinterpret_cast<float4*>(smem + C::OFF_FACT);
-        const uint64_t policy = policy_evict_first();
-        uint32_t issued = 0, done = 0;           // tiles: copies begun, turned into f16
-        uint32_t ist = 0, dst = 0, dph = 0, fst = 0, fuse = 0;   // their stages
-        bool ok = true, more = true;
-        int t = 0, t1 = 0, page = 0;
-        // the next tile to copy, and its boxes' pages
-        auto step = [&](bool first) {
-          if (!first && ++t < t1) {
-            page = Load::lane_page(P, u, t, lane);
-            return;
-          }
-          do more = u.next(P);
-          while (more && u.keys == 0);
-          if (!more) return;
-          t = u.t0;
-          t1 = u.t1;
-          page = Load::lane_page(P, u, t, lane);
-        };
-        step(true);
-        while (true) {
-          // a stage is free once its codes have been turned into f16
-          while (more && issued - done < C::VCODES) {
-            const uint32_t to = sbase + C::OFF_SCALE + ist * (2 * C::BLOCKS * 4);
-            Load::issue(P, u, t, lane, page, &tmV, codes + ist * C::KTILE, bar(W_VCODES + ist), policy);
-            Load::copy_scales(P, u, t, lane, page, A.k_scale, to);
-            Load::copy_scales(P, u, t, lane, page, A.v_scale, to + C::BLOCKS * 4);
-            Load::landed(bar(W_VCODES + ist), lane);
-            ++issued;
-            if (++ist == C::VCODES) ist = 0;
-            step(false);
-          }
-          if (done == issued) break;
-          ok = wait_all(W_VCODES + dst, dph);
-          if (!ok) break;
-          // The softmax of the tile four before has read its factors: its P
-          // came before the PV of the tile three before, for which the last
-          // wait of the turn before was.
-          if (lane < C::BLOCKS)
-            fact[(done & 3) * C::BLOCKS + lane] = block_factors(scales[dst * 2 * C::BLOCKS + lane],
-                                                                scales[(dst * 2 + 1) * C::BLOCKS + lane]);
-          mbar_arrive_warp(bar(W_FACT + (done & 3)));
-          if (fuse > 0) ok = wait_all(W_VEMPTY + fst, (fuse - 1) & 1);
-          if (!ok) break;
-          Load::to_f16(codes + dst * C::KTILE, buf + fst * C::TILE, lane);
-          fence_proxy_async_smem();
-          mbar_arrive_warp(bar(W_VFULL + fst));
-          ++done;
-          if (++dst == C::VCODES) {
-            dst = 0;
-            dph ^= 1;
-          }
-          if (++fst == C::VSTAGES) {
-            fst = 0;
-            ++fuse;
-          }
-        }
-        // every issued copy has landed before the block may exit
-        if (lane == 0)
-#pragma unroll 1
-          for (uint32_t x = done; x < issued; ++x)
-            mbar_wait(bar(W_VCODES + x % C::VCODES), (x / C::VCODES) & 1, P.status, P.wait_ns);
-        __syncwarp();
-      }
-    } else if (warp == K_WARP || warp == V_WARP) {
+    if (warp == K_WARP || warp == V_WARP) {
       // ---------------------------------------------------------- K / V loads
       const bool isk = warp == K_WARP;
-      const int stages = isk ? C::KSTAGES : C::VSTAGES;
-      const int b_full = isk ? W_KFULL : W_VFULL, b_empty = isk ? W_KEMPTY : W_VEMPTY;
-      const uint32_t buf = sbase + (isk ? C::OFF_K : C::OFF_V);
+      const int stages = isk ? C::KSTAGES : CODES ? C::VCODES : C::VSTAGES;
+      const int b_full = isk ? W_KFULL : CODES ? W_VCODES : W_VFULL;
+      const int b_empty = isk ? W_KEMPTY : CODES ? W_VCEMPTY : W_VEMPTY;
+      const uint32_t buf = sbase + (isk ? C::OFF_K : CODES ? C::OFF_VC : C::OFF_V);
       const CUtensorMap* tm = isk ? &tmK : &tmV;
       const uint64_t policy = policy_evict_first();
       uint32_t st = 0, use = 0, issued = 0;    // stage, its uses so far, tiles issued
@@ -327,7 +235,15 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS, CODES>::THREADS, WideCfg<D, 
           const int next = t + 1 < u.t1 ? Load::lane_page(P, u, t + 1, lane) : 0;
           if (use > 0) ok = wait_all(b_empty + st, (use - 1) & 1);
           if (!ok) break;
-          Load::issue(P, u, t, lane, page, tm, buf + st * (isk ? C::KTILE : C::TILE), bar(b_full + st), policy);
+          Load::issue(P, u, t, lane, page, tm, buf + st * C::KTILE, bar(b_full + st), policy);
+          if constexpr (CODES) {
+            if (!isk) {                          // and the scales of both
+              const uint32_t to = sbase + C::OFF_SCALE + st * (2 * C::BLOCKS * 4);
+              Load::copy_scales(P, u, t, lane, page, A.k_scale, to);
+              Load::copy_scales(P, u, t, lane, page, A.v_scale, to + C::BLOCKS * 4);
+              Load::landed(bar(b_full + st), lane);
+            }
+          }
           ++issued;
           if (++st == stages) {
             st = 0;
@@ -670,6 +586,47 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS, CODES>::THREADS, WideCfg<D, 
         for (int x0 = w.rows ? 0 : slot; x0 < w.n; x0 += w.rows ? 1 : 2) {
           const int t = u.t0 + x0;
           const bool partial = t >= part0;
+          if constexpr (CODES) {
+            // This warp's rows of the V tile, from codes to f16 (and clean of
+            // what not every row sees, see fix_row8), and the tile's factors.
+            // Here they cost little: S of the tile is still being multiplied.
+            const uint32_t e = e0 + x0, cs = e % C::VCODES, st = e % C::VSTAGES;
+            if (ok) ok = wait_all(W_VCODES + cs, (e / C::VCODES) & 1);
+            if (ok && e >= C::VSTAGES) ok = wait_all(W_VEMPTY + st, (e / C::VSTAGES - 1) & 1);
+            if (ok) {
+              const float* scales = reinterpret_cast<const float*>(smem + C::OFF_SCALE) + cs * 2 * C::BLOCKS;
+              if (lane < C::BLOCKS)
+                reinterpret_cast<float4*>(smem + C::OFF_FACT)[warp * C::BLOCKS + lane] =
+                    block_factors(scales[lane], scales[C::BLOCKS + lane]);
+              const uint32_t from = sbase + C::OFF_VC + cs * C::KTILE, to = sbase + C::OFF_V + st * C::TILE;
+              auto part = [&](int r0) {
+                if (partial) {
+                  Load::template to_f16<16>(from, to, r0, lane, [&](int row, uint4& y) {
+                    const int key = t * KT + row, i = key - u.origin;
+                    if (key >= u.keys) {
+                      y = make_uint4(0u, 0u, 0u, 0u);
+                    } else if (i >= 0) {
+                      const uint4 nan = make_uint4(e4m3x4_nan(y.x), e4m3x4_nan(y.y), e4m3x4_nan(y.z), e4m3x4_nan(y.w));
+                      if (nan.x | nan.y | nan.z | nan.w) {
+                        atomicOr(nf + (i >> 5), 1u << (i & 31));
+                        y = make_uint4(y.x & ~nan.x, y.y & ~nan.y, y.z & ~nan.z, y.w & ~nan.w);
+                      }
+                    }
+                  });
+                } else {
+                  Load::template to_f16<16>(from, to, r0, lane, [](int, uint4&) {});
+                }
+              };
+              part((w.rows ? warp : quarter) * 16);
+              if (!w.rows) part((quarter + 4) * 16);   // the other slot has tiles of its own
+              fence_proxy_async_smem();
+            }
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive_count(bar(W_VFULL + st), w.rows ? 1 : 2);
+              mbar_arrive_count(bar(W_VCEMPTY + cs), w.rows ? 1 : 2);
+            }
+          }
           // SLOTS 1: the buffers alternate
           const int buf = SLOTS == 1 ? j & 1 : slot;
           const uint32_t tSj = SLOTS == 1 ? tS + 64 * (j & 1) : tS;
@@ -711,12 +668,11 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS, CODES>::THREADS, WideCfg<D, 
             tmem_wait_ld();
             float m_tile;
             [[maybe_unused]] const float4* fact =
-                reinterpret_cast<const float4*>(smem + C::OFF_FACT) + ((e0 + x0) & 3) * C::BLOCKS;
+                reinterpret_cast<const float4*>(smem + C::OFF_FACT) + warp * C::BLOCKS;
             // CODES: of a block's scores to x + log2 sv (the factor is kept
             // finite: a score of 0 stays 0)
             [[maybe_unused]] auto factor = [&](int b) { return finite(back * fact[b].x); };
             if constexpr (CODES) {
-              if (ok) ok = wait_all(W_FACT + ((e0 + x0) & 3), ((e0 + x0) >> 2) & 1);
               m_tile = -INFINITY;
 #pragma unroll
               for (int b = 0; b < C::BLOCKS; ++b) {
@@ -809,7 +765,7 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS, CODES>::THREADS, WideCfg<D, 
             l += (sum4[0] + sum4[1]) + (sum4[2] + sum4[3]);
             tmem_wait_st();
           }
-          if (partial && ok) {
+          if (!CODES && partial && ok) {
             // clean row r of the V tile (see fix_row) before the product
             const uint32_t e = e0 + x0, st = e % C::VSTAGES;
             ok = wait_all(W_VFULL + st, (e / C::VSTAGES) & 1);
@@ -832,12 +788,12 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS, CODES>::THREADS, WideCfg<D, 
 #pragma unroll 4
                 for (int c = 0; c < D / 8; ++c) {
                   const uint4 y = *word(c);
-                  zero = V16::times_zero(y.x, zero);
-                  zero = V16::times_zero(y.y, zero);
-                  zero = V16::times_zero(y.z, zero);
-                  zero = V16::times_zero(y.w, zero);
+                  zero = bf16x2_times_zero(y.x, zero);
+                  zero = bf16x2_times_zero(y.y, zero);
+                  zero = bf16x2_times_zero(y.z, zero);
+                  zero = bf16x2_times_zero(y.w, zero);
                 }
-                dirty = V16::found(zero);
+                dirty = bf16x2_not_finite(zero);
               }
               if (dirty) {
                 // the flag first: whoever finds the row clean finds the flag
@@ -846,8 +802,8 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS, CODES>::THREADS, WideCfg<D, 
 #pragma unroll 1
                 for (int c = 0; c < D / 8; ++c) {
                   uint4* y = word(c);
-                  *y = make_uint4(V16::clean(y->x), V16::clean(y->y), V16::clean(y->z),
-                                  V16::clean(y->w));
+                  *y = make_uint4(bf16x2_clean(y->x), bf16x2_clean(y->y), bf16x2_clean(y->z),
+                                  bf16x2_clean(y->w));
                 }
               }
               fence_proxy_async_smem();
