@@ -89,7 +89,9 @@ struct WideCfg {
   static constexpr uint32_t T_COLS = 256 * SLOTS, T_O = 128 * SLOTS;
   // register split: the softmax warpgroups' and the others' budgets add up to
   // what the block is launched with (384 x 168, 256 x 128)
-  static constexpr uint32_t REGS_SOFTMAX = SLOTS == 2 ? 216 : 184, REGS_PRODUCER = 72;
+  // (CODES holds half of a row of S at a time, see below)
+  static constexpr uint32_t REGS_SOFTMAX = CODES ? (SLOTS == 2 ? 184 : 152) : SLOTS == 2 ? 216 : 184;
+  static constexpr uint32_t REGS_PRODUCER = CODES ? (SLOTS == 2 ? 136 : 104) : 72;
   static constexpr int MIN_LAUNCH_REGS =
       (32 * SM_WARPS * REGS_SOFTMAX + 128 * REGS_PRODUCER + THREADS - 1) / THREADS;
 };
@@ -661,30 +663,41 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS, CODES>::THREADS, WideCfg<D, 
               }
               tmem_wait_st();
             }
-            float sv[KT];
+            // CODES: a row of S is loaded by halves, the second one twice (for
+            // its maximum and for P): a whole row of 128 spilled registers in
+            // the loop, and the little L1 that shared memory leaves made their
+            // loads wait for L2
+            constexpr int HALF = CODES ? KT / 2 : KT;
+            float sv[HALF];
             uint32_t* raw = reinterpret_cast<uint32_t*>(sv);
+            auto load = [&](int c0) {
 #pragma unroll
-            for (int y = 0; y < KT / 32; ++y) tmem_ld32(tSj + 32 * y, raw + 32 * y);
-            tmem_wait_ld();
-            float m_tile;
+              for (int y = 0; y < HALF / 32; ++y) tmem_ld32(tSj + c0 + 32 * y, raw + 32 * y);
+              tmem_wait_ld();
+            };
             [[maybe_unused]] const float4* fact =
                 reinterpret_cast<const float4*>(smem + C::OFF_FACT) + warp * C::BLOCKS;
-            // CODES: of a block's scores to x + log2 sv (the factor is kept
-            // finite: a score of 0 stays 0)
-            [[maybe_unused]] auto factor = [&](int b) { return finite(back * fact[b].x); };
+            // of a block's scores to x + log2 sv
+            [[maybe_unused]] auto factor = [&](float4 f) { return finite(back * f.x); };
+            float m_tile = -INFINITY;
             if constexpr (CODES) {
-              m_tile = -INFINITY;
 #pragma unroll
-              for (int b = 0; b < C::BLOCKS; ++b) {
-                const float* s = sv + 16 * b;
-                float a[4];
+              for (int c0 = HALF; c0 >= 0; c0 -= HALF) {
+                load(c0);
 #pragma unroll
-                for (int y = 0; y < 4; ++y) a[y] = fmax3(s[y], s[y + 4], s[y + 8]);
+                for (int b = 0; b < HALF / 16; ++b) {
+                  const float* s = sv + 16 * b;
+                  const float4 f = fact[c0 / 16 + b];
+                  float a[4];
 #pragma unroll
-                for (int y = 0; y < 4; ++y) a[y] = fmaxf(a[y], s[y + 12]);
-                m_tile = fmaxf(m_tile, fmaf(fmax3(a[0], a[1], fmaxf(a[2], a[3])), factor(b), fact[b].y));
+                  for (int y = 0; y < 4; ++y) a[y] = fmax3(s[y], s[y + 4], s[y + 8]);
+#pragma unroll
+                  for (int y = 0; y < 4; ++y) a[y] = fmaxf(a[y], s[y + 12]);
+                  m_tile = fmaxf(m_tile, fmaf(fmax3(a[0], a[1], fmaxf(a[2], a[3])), factor(f), f.y));
+                }
               }
             } else {
+              load(0);
               float mx8[8];
 #pragma unroll
               for (int y = 0; y < 8; ++y) mx8[y] = fmax3(sv[y], sv[y + 8], sv[y + 16]);
@@ -709,12 +722,13 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS, CODES>::THREADS, WideCfg<D, 
             float sum4[4] = {0.f, 0.f, 0.f, 0.f};
             if constexpr (CODES) {
 #pragma unroll
-              for (int c4 = 0; c4 < KT / 32; ++c4) {
-                uint32_t pk[16];
+              for (int c0 = 0; c0 < KT; c0 += HALF) {
+                if (c0 > 0) load(c0);
 #pragma unroll
-                for (int b = 2 * c4; b < 2 * c4 + 2; ++b) {
-                  const float4 f = fact[b];
-                  const uint64_t sc2 = splat2(factor(b)), nm2 = splat2(f.y - m_ref + kPOffset);
+                for (int b = 0; b < HALF / 16; ++b) {
+                  const float4 f = fact[c0 / 16 + b];
+                  const uint64_t sc2 = splat2(factor(f)), nm2 = splat2(f.y - m_ref + kPOffset);
+                  uint32_t pk[8];
                   float s0 = 0.f, s1 = 0.f;
 #pragma unroll
                   for (int y = 0; y < 8; ++y) {
@@ -722,11 +736,11 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS, CODES>::THREADS, WideCfg<D, 
                     fma2_bc(a0, a1, sv[b * 16 + 2 * y], sv[b * 16 + 2 * y + 1], sc2, nm2);
                     const float p0 = ex2(a0), p1 = ex2(a1);
                     add2_acc(s0, s1, p0, p1);
-                    pk[(b & 1) * 8 + y] = pack_f16(p0, p1);
+                    pk[y] = pack_f16(p0, p1);
                   }
-                  sum4[b & 1] = fmaf(s0 + s1, f.z, sum4[b & 1]);
+                  sum4[b & 3] = fmaf(s0 + s1, f.z, sum4[b & 3]);
+                  tmem_st8(tSj + (c0 / 16 + b) * 8, pk);
                 }
-                tmem_st16(tSj + c4 * 16, pk);
               }
             } else {
               const uint64_t sc2 = splat2(P.scale_log2), nm2 = splat2(-m_ref);
