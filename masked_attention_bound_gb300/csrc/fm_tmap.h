@@ -64,20 +64,20 @@ inline bool make_tmap_bshd8(CUtensorMap* m, const void* base, int B, int S, int 
 }
 
 // A pool of e4m3 codes: 4-D view (head_dim, head, slot, page), one box =
-// `box_rows` slots x the whole head, swizzled as wide as its row (128 or 64
-// bytes).  Pages past the end read 0.
+// `box_rows` slots x `box_cols` elements of a head (64 or 128), swizzled as wide
+// as its row.  Pages past the end read 0.
 inline bool make_tmap_pool8(CUtensorMap* m, const void* base, int pages, int page_size, int H, int D,
-                            const int64_t* stride, int box_rows) {
+                            const int64_t* stride, int box_rows, int box_cols) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
   cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(H),
                         static_cast<cuuint64_t>(page_size), static_cast<cuuint64_t>(pages)};
   cuuint64_t strides[3] = {static_cast<cuuint64_t>(stride[2]), static_cast<cuuint64_t>(stride[1]),
                            static_cast<cuuint64_t>(stride[0])};
-  cuuint32_t box[4] = {static_cast<cuuint32_t>(D), 1, static_cast<cuuint32_t>(box_rows), 1};
+  cuuint32_t box[4] = {static_cast<cuuint32_t>(box_cols), 1, static_cast<cuuint32_t>(box_rows), 1};
   cuuint32_t es[4] = {1, 1, 1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base), dims, strides, box, es,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, box_cols == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

@@ -846,8 +846,10 @@ fm_status tree_fwd(const fm_cache* c, const fm_tree_desc* t, const void* q, cons
     P.box_shift = page_shift(box);
     Tree8Params A{P, k_scale, v_scale, static_cast<const uint8_t*>(v_pool)};
     CUtensorMap tk, tv;
-    if (!make_tmap_pool8(&tk, k_pool, c->n_pages, c->page_size, c->Hkv, c->d, c->k_stride + 1, box) ||
-        !make_tmap_pool8(&tv, v_pool, c->n_pages, c->page_size, c->Hkv, c->d, c->v_stride + 1, box))
+    // (tcgen05's V: 64 columns a box, see VTile8)
+    if (!make_tmap_pool8(&tk, k_pool, c->n_pages, c->page_size, c->Hkv, c->d, c->k_stride + 1, box, c->d) ||
+        !make_tmap_pool8(&tv, v_pool, c->n_pages, c->page_size, c->Hkv, c->d, c->v_stride + 1, box,
+                         W.kind == NARROW ? c->d : 64))
       return FM_ERR_CUDA;
     const int64_t rows = static_cast<int64_t>(t->max_nodes < t->total ? t->max_nodes : t->total) * P.G;
     if (W.kind == MID) st = launch_tree8_mid(A, c->d, tk, tv, grid, s);

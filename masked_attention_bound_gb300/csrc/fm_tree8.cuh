@@ -90,39 +90,47 @@ struct TileLoad8 {
   __device__ static __forceinline__ uint32_t word16(int r, int c) {
     return D == 128 ? r * 128 + ((c ^ (r & 7)) << 4) : r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
   }
-  // Rows [r0, r0 + ROWS) of a tile of codes at src to a tile of f16 at dst
-  // (slabs of 64 columns, KT * 128 bytes apart, with the 128-byte swizzle), by a
-  // warp: 8 rows of 4 words an instruction.  The rows of a group of eight lanes
-  // differ by 4 (d = 64: by 1), and of the two halves of a word a lane of the
-  // second row stores the second one first, so that loads and stores touch every
-  // bank once.  `clean`(row, word): called for each word of 16 codes.
-  template <int ROWS, typename F>
+};
+
+// V for tcgen05: a tile of codes as slabs of 64 columns, KT rows of 64 bytes
+// with the 64-byte swizzle (a box each), and rows [r0, r0 + 16) of it at src to a
+// tile of f16 at dst (slabs of 64 columns of KT * 128 bytes with the 128-byte
+// swizzle), by a warp: 8 rows of 4 words of 16 codes an instruction, which are
+// loaded and stored without bank conflicts.  `clean`(row, word): called for each
+// word.
+template <int D, int KT>
+struct VTile8 {
+  static constexpr int SLABS = D / 64;
+  __device__ static __forceinline__ void issue(const TreeParams& P, const TreePiece& u, int tile, int lane, int page,
+                                               const CUtensorMap* tm, uint32_t dst, uint32_t bar, uint64_t policy) {
+    const int n = TileLoad8<D, KT>::boxes(P, u, tile);
+    if (lane == 0) mbar_arrive_expect_tx(bar, (n << P.box_shift) * D);
+    __syncwarp();
+    const int j = lane / SLABS, slab = lane % SLABS, pg = __shfl_sync(0xffffffffu, page, j);
+    if (j < n)
+      tma_load_4d_hint(dst + slab * (KT * 64) + (j << P.box_shift) * 64, tm, bar, slab * 64, u.hk,
+                       (tile * KT + (j << P.box_shift)) & ((1 << P.page_shift) - 1), pg, policy);
+  }
+  template <typename F>
   __device__ static __forceinline__ void to_f16(uint32_t src, uint32_t dst, int r0, int lane, F clean) {
-    const int w = lane & 3;
-    const int row0 = r0 + (D == 128 ? 4 * ((lane >> 2) & 1) + (lane >> 3) : lane >> 2);
-    const bool swap = D == 128 && ((lane >> 2) & 1);
-    constexpr int SLABS = D / 64, N = ROWS / 8 * SLABS;
-    uint4 x[N];
+    const int w = lane & 3, row0 = r0 + (lane >> 2);   // and row0 + 8: the same place of the swizzles
+    const uint32_t from = src + row0 * 64 + ((w ^ ((row0 >> 1) & 3)) << 4);
+    const uint32_t to = dst + row0 * 128, c = ((2 * w) ^ (row0 & 7)) << 4;
+    uint4 x[2 * SLABS];
 #pragma unroll
-    for (int i = 0; i < N; ++i)
+    for (int i = 0; i < 2 * SLABS; ++i)
       asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                    : "=r"(x[i].x), "=r"(x[i].y), "=r"(x[i].z), "=r"(x[i].w)
-                   : "r"(src + word16(row0 + i / SLABS * 8, i % SLABS * 4 + w))
+                   : "r"(from + (i >> 1) * (KT * 64) + (i & 1) * 512)
                    : "memory");
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int slab = i % SLABS, row = row0 + i / SLABS * 8;
-      clean(row, x[i]);
-      const uint32_t a[4] = {f16x2_of_e4m3x2(x[i].x), f16x2_of_e4m3x2(x[i].x >> 16), f16x2_of_e4m3x2(x[i].y),
-                             f16x2_of_e4m3x2(x[i].y >> 16)};
-      const uint32_t b[4] = {f16x2_of_e4m3x2(x[i].z), f16x2_of_e4m3x2(x[i].z >> 16), f16x2_of_e4m3x2(x[i].w),
-                             f16x2_of_e4m3x2(x[i].w >> 16)};
-      const uint32_t to = dst + slab * (KT * 128) + row * 128;
-      const int c = (2 * w) ^ (row & 7);
-      st_shared_v4(to + ((c ^ swap) << 4), swap ? b[0] : a[0], swap ? b[1] : a[1], swap ? b[2] : a[2],
-                   swap ? b[3] : a[3]);
-      st_shared_v4(to + ((c ^ 1 ^ swap) << 4), swap ? a[0] : b[0], swap ? a[1] : b[1], swap ? a[2] : b[2],
-                   swap ? a[3] : b[3]);
+    for (int i = 0; i < 2 * SLABS; ++i) {
+      clean(row0 + (i & 1) * 8, x[i]);
+      const uint32_t at = to + (i >> 1) * (KT * 128) + (i & 1) * 1024;
+      st_shared_v4(at + c, f16x2_of_e4m3x2(x[i].x), f16x2_of_e4m3x2(x[i].x >> 16), f16x2_of_e4m3x2(x[i].y),
+                   f16x2_of_e4m3x2(x[i].y >> 16));
+      st_shared_v4(at + (c ^ 16), f16x2_of_e4m3x2(x[i].z), f16x2_of_e4m3x2(x[i].z >> 16), f16x2_of_e4m3x2(x[i].w),
+                   f16x2_of_e4m3x2(x[i].w >> 16));
     }
   }
 };

@@ -35,11 +35,8 @@
 // 64.5.
 //
 // CODES: the cache holds e4m3 codes (see fm_tree8.cuh for the arithmetic).  S
-// multiplies K's codes as they are.  V's go to stages of their own, and the
-// softmax warps turn them into f16 tiles in front of the MMAs, laid out as the
-// bf16 tiles are, 16 rows a warp, while S of the tile is multiplied.  (A warp of
-// its own for that took 910 cycles for 64 x 128 codes alone, and among the
-// softmax warps longer than their work: 16 trees of 64 nodes 286 us.)
+// multiplies K's codes as they are.  V's go to stages of their own and become f16
+// tiles in front of the MMAs, laid out as the bf16 tiles are.
 //
 // TMEM: S/P of slot s at column 128 s (SLOTS = 1: of every second tile at
 // column 64), the O's after the S's.
@@ -53,6 +50,7 @@ template <int D, int SLOTS_, bool CODES_>
 struct WideCfg {
   static constexpr int SLOTS = SLOTS_;
   static constexpr bool CODES = CODES_;
+  static constexpr int DIM = D;
   static_assert(D == 128 || SLOTS == 1, "d = 64 runs with tiles of 128 rows side by side");
   using Geo = std::conditional_t<SLOTS == 2, WideGeo, MidGeo>;
   static constexpr int KT = Geo::KT;
@@ -64,18 +62,25 @@ struct WideCfg {
   static constexpr int VCODES = !CODES ? 0 : D == 64 ? 4 : 2;   // stages of V's codes
   static constexpr int BLOCKS = KT / kScaleBlock;
   static constexpr int SM_WARPS = 4 * SLOTS;            // softmax
+  // CODES: who turns V's codes into f16.  SLOTS = 1: two warps, in the places of
+  // the V loader (K's loads both) and of a second slot's MMAs.  SLOTS = 2: the
+  // softmax warps, a share each, while S of the tile is multiplied.
+  static constexpr bool CONVERTERS = CODES && SLOTS == 1;
+  static constexpr int CV_WARPS = !CODES ? 0 : CONVERTERS ? 2 : SM_WARPS;
+  // Sets of a tile's factors: by stage, or by warp where the softmax warps find
+  // them (one that waits for the other slot's keeps step with it: 228 us).
+  static constexpr int FACTS = CONVERTERS ? VSTAGES : SM_WARPS;
   static constexpr int THREADS = 32 * (SM_WARPS + 4);
   static constexpr int BLOCKS_PER_SM = SLOTS == 2 ? 1 : 2;
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_K = SLOTS * QTILE;
   static constexpr int OFF_V = OFF_K + KSTAGES * KTILE;
   static constexpr int OFF_VC = OFF_V + VSTAGES * TILE;                      // V's codes
-  // of each softmax warp, a tile's float4 [BLOCKS] (see block_factors)
-  static constexpr int OFF_FACT = OFF_VC + VCODES * KTILE;
-  static constexpr int OFF_SCALE = OFF_FACT + (CODES ? 4 * SLOTS * BLOCKS * 16 : 0);   // float [VCODES][K, V][BLOCKS]
+  static constexpr int OFF_FACT = OFF_VC + VCODES * KTILE;        // CODES: [FACTS][BLOCKS] of float4, then of float
+  static constexpr int OFF_SCALE = OFF_FACT + (CODES ? FACTS * BLOCKS * 20 : 0);     // float [VCODES][K, V][BLOCKS]
   static constexpr int OFF_ML = OFF_SCALE + VCODES * 2 * BLOCKS * 4;         // SLOTS 2: float2 [slot][128]
-  static constexpr int OFF_NF = OFF_ML + (SLOTS == 2 ? 2 * 128 * 8 : 0);   // [2][8] keys with values not finite
-  static constexpr int OFF_BAR = OFF_NF + 64;
+  static constexpr int OFF_NF = OFF_ML + (SLOTS == 2 ? 2 * 128 * 8 : 0);   // [4][8] keys with values not finite
+  static constexpr int OFF_BAR = OFF_NF + 128;
   static constexpr int NBAR = CODES ? 42 : 34;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;   // abort flag, TMEM address
   static constexpr int OFF_PAR = OFF_MISC + 16;         // int16 [256] parents of the unit's nodes
@@ -89,7 +94,6 @@ struct WideCfg {
   static constexpr uint32_t T_COLS = 256 * SLOTS, T_O = 128 * SLOTS;
   // register split: the softmax warpgroups' and the others' budgets add up to
   // what the block is launched with (384 x 168, 256 x 128)
-  // (CODES holds half of a row of S at a time, see below)
   static constexpr uint32_t REGS_SOFTMAX = CODES ? (SLOTS == 2 ? 184 : 152) : SLOTS == 2 ? 216 : 184;
   static constexpr uint32_t REGS_PRODUCER = CODES ? (SLOTS == 2 ? 136 : 104) : 72;
   static constexpr int MIN_LAUNCH_REGS =
@@ -136,6 +140,63 @@ using WideParams = std::conditional_t<CODES, Tree8Params, TreeParams>;
 __device__ __forceinline__ const TreeParams& tree_params(const TreeParams& A) { return A; }
 __device__ __forceinline__ const TreeParams& tree_params(const Tree8Params& A) { return A.P; }
 
+// CODES: rows [part * rows, (part + 1) * rows) of V tile `e` of the block, clean
+// of what not every row sees (see fix_row8), and what the scales of its blocks
+// bring to the softmax; `count` arrivals.  (The stage's last PV has ended, so the
+// softmax of that tile has read its factors.)
+template <typename C, typename W>
+__device__ __forceinline__ bool convert_v(const TreeParams& P, const TreePiece& u, int t, uint32_t e, int part,
+                                          int rows, int count, int lane, const uint8_t* smem, uint32_t sbase,
+                                          uint32_t* nf, W wait_all) {
+  using V = VTile8<C::DIM, C::KT>;
+  const uint32_t cs = e % C::VCODES, st = e % C::VSTAGES;
+  bool ok = wait_all(W_VCODES + cs, (e / C::VCODES) & 1);
+  if (ok && e >= C::VSTAGES) ok = wait_all(W_VEMPTY + st, (e / C::VSTAGES - 1) & 1);
+  if (!ok) return false;
+  const float* scales = reinterpret_cast<const float*>(smem + C::OFF_SCALE) + cs * 2 * C::BLOCKS;
+  const int set = C::CONVERTERS ? st : threadIdx.x >> 5;
+  const int b = (C::CONVERTERS ? part * (rows / kScaleBlock) : 0) + lane;
+  if (lane < (C::CONVERTERS ? rows / kScaleBlock : C::BLOCKS)) {
+    const float4 f = block_factors(scales[b], scales[C::BLOCKS + b]);
+    // in pairs, as the packed arithmetic takes them
+    asm volatile("st.shared.v4.f32 [%0], {%1, %1, %2, %2};" ::"r"(sbase + C::OFF_FACT + (set * C::BLOCKS + b) * 16),
+                 "f"(f.x), "f"(f.y)
+                 : "memory");
+    asm volatile("st.shared.f32 [%0], %1;" ::"r"(sbase + C::OFF_FACT + C::FACTS * C::BLOCKS * 16 +
+                                                 (set * C::BLOCKS + b) * 4),
+                 "f"(f.z)
+                 : "memory");
+  }
+  const uint32_t from = sbase + C::OFF_VC + cs * C::KTILE, to = sbase + C::OFF_V + st * C::TILE;
+  const bool partial = t >= u.origin / C::KT;
+#pragma unroll 1
+  for (int r0 = part * rows; r0 < (part + 1) * rows; r0 += 16) {
+    if (partial) {
+      V::to_f16(from, to, r0, lane, [&](int row, uint4& y) {
+        const int key = t * C::KT + row, i = key - u.origin;
+        if (key >= u.keys) {
+          y = make_uint4(0u, 0u, 0u, 0u);
+        } else if (i >= 0) {
+          const uint4 nan = make_uint4(e4m3x4_nan(y.x), e4m3x4_nan(y.y), e4m3x4_nan(y.z), e4m3x4_nan(y.w));
+          if (nan.x | nan.y | nan.z | nan.w) {
+            atomicOr(nf + (i >> 5), 1u << (i & 31));
+            y = make_uint4(y.x & ~nan.x, y.y & ~nan.y, y.z & ~nan.z, y.w & ~nan.w);
+          }
+        }
+      });
+    } else {
+      V::to_f16(from, to, r0, lane, [](int, uint4&) {});
+    }
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) {
+    mbar_arrive_count(sbase + C::OFF_BAR + 8u * (W_VCEMPTY + cs), count);
+    mbar_arrive_count(sbase + C::OFF_BAR + 8u * (W_VFULL + st), count);
+  }
+  return true;
+}
+
 template <int D, int SLOTS, bool CODES>
 __global__ void __launch_bounds__(WideCfg<D, SLOTS, CODES>::THREADS, WideCfg<D, SLOTS, CODES>::BLOCKS_PER_SM)
     tree_wide_kernel(const __grid_constant__ WideParams<CODES> A, const __grid_constant__ CUtensorMap tmQ,
@@ -180,13 +241,13 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS, CODES>::THREADS, WideCfg<D, 
       mbar_init(bar(W_KEMPTY + i), SLOTS);
     }
     for (int i = 0; i < C::VSTAGES; ++i) {
-      mbar_init(bar(W_VFULL + i), CODES ? C::SM_WARPS : 1);   // CODES: the softmax warps make the tile
+      mbar_init(bar(W_VFULL + i), CODES ? C::CV_WARPS : 1);
       mbar_init(bar(W_VEMPTY + i), SLOTS);
     }
     if constexpr (CODES) {
       for (int i = 0; i < C::VCODES; ++i) {
         mbar_init(bar(W_VCODES + i), Load::ARRIVALS);
-        mbar_init(bar(W_VCEMPTY + i), C::SM_WARPS);
+        mbar_init(bar(W_VCEMPTY + i), C::CV_WARPS);
       }
     }
     mbar_init(bar(W_DRAIN), SLOTS);
@@ -194,7 +255,7 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS, CODES>::THREADS, WideCfg<D, 
     *abort_flag = 0;
     fence_barrier_init();
   }
-  if (tid < 16) nf_all[tid] = 0;
+  if (tid < 32) nf_all[tid] = 0;
   if (warp == MMA_WARP) {
     tmem_alloc(smem_u32(tmem_slot), C::T_COLS);
     tmem_relinquish();
@@ -218,9 +279,20 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS, CODES>::THREADS, WideCfg<D, 
 
   if (warp >= C::SM_WARPS) {
     regs_decrease<C::REGS_PRODUCER>();
-    if (warp == K_WARP || warp == V_WARP) {
+    if (warp == K_WARP || (warp == V_WARP && !C::CONVERTERS)) {
       // ---------------------------------------------------------- K / V loads
       const bool isk = warp == K_WARP;
+      constexpr bool BOTH = C::CONVERTERS;             // K's warp loads V too
+      uint32_t vst = 0, vuse = 0;
+      auto load_v_codes = [&](const TreePiece& u, int t, int page, uint32_t st, uint64_t policy) {
+        if constexpr (CODES) {                         // and the scales of both
+          const uint32_t to = sbase + C::OFF_SCALE + st * (2 * C::BLOCKS * 4);
+          VTile8<D, KT>::issue(P, u, t, lane, page, &tmV, sbase + C::OFF_VC + st * C::KTILE, bar(W_VCODES + st), policy);
+          Load::copy_scales(P, u, t, lane, page, A.k_scale, to);
+          Load::copy_scales(P, u, t, lane, page, A.v_scale, to + C::BLOCKS * 4);
+          Load::landed(bar(W_VCODES + st), lane);
+        }
+      };
       const int stages = isk ? C::KSTAGES : CODES ? C::VCODES : C::VSTAGES;
       const int b_full = isk ? W_KFULL : CODES ? W_VCODES : W_VFULL;
       const int b_empty = isk ? W_KEMPTY : CODES ? W_VCEMPTY : W_VEMPTY;
@@ -237,13 +309,14 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS, CODES>::THREADS, WideCfg<D, 
           const int next = t + 1 < u.t1 ? Load::lane_page(P, u, t + 1, lane) : 0;
           if (use > 0) ok = wait_all(b_empty + st, (use - 1) & 1);
           if (!ok) break;
-          Load::issue(P, u, t, lane, page, tm, buf + st * C::KTILE, bar(b_full + st), policy);
-          if constexpr (CODES) {
-            if (!isk) {                          // and the scales of both
-              const uint32_t to = sbase + C::OFF_SCALE + st * (2 * C::BLOCKS * 4);
-              Load::copy_scales(P, u, t, lane, page, A.k_scale, to);
-              Load::copy_scales(P, u, t, lane, page, A.v_scale, to + C::BLOCKS * 4);
-              Load::landed(bar(b_full + st), lane);
+          if (CODES && !isk) load_v_codes(u, t, page, st, policy);
+          else Load::issue(P, u, t, lane, page, tm, buf + st * C::KTILE, bar(b_full + st), policy);
+          if constexpr (BOTH) {
+            if (vuse > 0) ok = wait_all(W_VCEMPTY + vst, (vuse - 1) & 1);
+            if (ok) load_v_codes(u, t, page, vst, policy);
+            if (ok && ++vst == C::VCODES) {
+              vst = 0;
+              ++vuse;
             }
           }
           ++issued;
@@ -251,6 +324,7 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS, CODES>::THREADS, WideCfg<D, 
             st = 0;
             ++use;
           }
+          if (!ok) break;
           page = next;
         }
       }
@@ -259,6 +333,13 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS, CODES>::THREADS, WideCfg<D, 
 #pragma unroll 1
         for (uint32_t x = issued > stages ? issued - stages : 0; x < issued; ++x)
           mbar_wait(bar(b_full + x % stages), (x / stages) & 1, P.status, P.wait_ns);
+      if constexpr (BOTH) {
+        const uint32_t vs = vuse * C::VCODES + vst;
+        if (lane == 0)
+#pragma unroll 1
+          for (uint32_t x = vs > C::VCODES ? vs - C::VCODES : 0; x < vs; ++x)
+            mbar_wait(bar(W_VCODES + x % C::VCODES), (x / C::VCODES) & 1, P.status, P.wait_ns);
+      }
       __syncwarp();
     } else if (warp == MMA_WARP || (SLOTS == 2 && warp == MMA_WARP_B)) {
       // ---------------------------------------------------------- MMA issuers
@@ -460,6 +541,20 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS, CODES>::THREADS, WideCfg<D, 
         mma_commit(bar(W_DRAIN));
         mbar_wait(bar(W_DRAIN), 0, P.status, P.wait_ns);
       }
+    } else if (C::CONVERTERS) {
+      // ---------------------------------------------------------- V's codes to f16
+      if constexpr (C::CONVERTERS) {
+        uint32_t e = 0, pieces = 0;
+        bool ok = true;
+        while (ok && u.next(P)) {
+          if (u.keys == 0) continue;
+#pragma unroll 1
+          for (int t = u.t0; ok && t < u.t1; ++t, ++e)
+            ok = convert_v<C>(P, u, t, e, warp == V_WARP ? 0 : 1, KT / 2, 1, lane, smem, sbase,
+                              nf_all + 8 * (pieces % 4), wait_all);
+          ++pieces;
+        }
+      }
     }
     __syncwarp();
   } else {
@@ -498,8 +593,12 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS, CODES>::THREADS, WideCfg<D, 
         continue;
       }
       const bool active = w.active(slot);
-      uint32_t* nf = nf_all + 8 * (pieces & 1);
-      if (tid < 8) nf_all[8 * ((pieces + 1) & 1) + tid] = 0;   // the next piece's, read by nobody now
+      // This piece's flags, and the next piece's, read by nobody now, cleared.
+      // (CODES: the warps that set them may be two tiles ahead, and so two
+      // pieces: the one after the next's.)
+      constexpr int AHEAD = CODES ? 2 : 1;
+      uint32_t* nf = nf_all + 8 * (pieces % (2 * AHEAD));
+      if (tid < 8) nf_all[8 * ((pieces + AHEAD) % (2 * AHEAD)) + tid] = 0;
       const int part0 = u.origin / KT;                 // tiles from here on are not seen by all
       bool live = mine;
       if (P.tree) {
@@ -588,50 +687,19 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS, CODES>::THREADS, WideCfg<D, 
         for (int x0 = w.rows ? 0 : slot; x0 < w.n; x0 += w.rows ? 1 : 2) {
           const int t = u.t0 + x0;
           const bool partial = t >= part0;
-          if constexpr (CODES) {
-            // This warp's rows of the V tile, from codes to f16 (and clean of
-            // what not every row sees, see fix_row8), and the tile's factors.
-            // Here they cost little: S of the tile is still being multiplied.
-            const uint32_t e = e0 + x0, cs = e % C::VCODES, st = e % C::VSTAGES;
-            if (ok) ok = wait_all(W_VCODES + cs, (e / C::VCODES) & 1);
-            if (ok && e >= C::VSTAGES) ok = wait_all(W_VEMPTY + st, (e / C::VSTAGES - 1) & 1);
-            if (ok) {
-              const float* scales = reinterpret_cast<const float*>(smem + C::OFF_SCALE) + cs * 2 * C::BLOCKS;
-              if (lane < C::BLOCKS)
-                reinterpret_cast<float4*>(smem + C::OFF_FACT)[warp * C::BLOCKS + lane] =
-                    block_factors(scales[lane], scales[C::BLOCKS + lane]);
-              const uint32_t from = sbase + C::OFF_VC + cs * C::KTILE, to = sbase + C::OFF_V + st * C::TILE;
-              auto part = [&](int r0) {
-                if (partial) {
-                  Load::template to_f16<16>(from, to, r0, lane, [&](int row, uint4& y) {
-                    const int key = t * KT + row, i = key - u.origin;
-                    if (key >= u.keys) {
-                      y = make_uint4(0u, 0u, 0u, 0u);
-                    } else if (i >= 0) {
-                      const uint4 nan = make_uint4(e4m3x4_nan(y.x), e4m3x4_nan(y.y), e4m3x4_nan(y.z), e4m3x4_nan(y.w));
-                      if (nan.x | nan.y | nan.z | nan.w) {
-                        atomicOr(nf + (i >> 5), 1u << (i & 31));
-                        y = make_uint4(y.x & ~nan.x, y.y & ~nan.y, y.z & ~nan.z, y.w & ~nan.w);
-                      }
-                    }
-                  });
-                } else {
-                  Load::template to_f16<16>(from, to, r0, lane, [](int, uint4&) {});
-                }
-              };
-              part((w.rows ? warp : quarter) * 16);
-              if (!w.rows) part((quarter + 4) * 16);   // the other slot has tiles of its own
-              fence_proxy_async_smem();
-            }
-            __syncwarp();
-            if (lane == 0) {
-              mbar_arrive_count(bar(W_VFULL + st), w.rows ? 1 : 2);
-              mbar_arrive_count(bar(W_VCEMPTY + cs), w.rows ? 1 : 2);
-            }
-          }
           // SLOTS 1: the buffers alternate
           const int buf = SLOTS == 1 ? j & 1 : slot;
           const uint32_t tSj = SLOTS == 1 ? tS + 64 * (j & 1) : tS;
+          const uint32_t vt = e0 + x0;
+          if constexpr (CODES && !C::CONVERTERS) {
+            // this warp's rows of the V tile (both halves of the slot's rows where
+            // the other slot has tiles of its own)
+            if (ok)
+              ok = w.rows ? convert_v<C>(P, u, t, vt, warp, KT / 8, 1, lane, smem, sbase, nf, wait_all)
+                          : convert_v<C>(P, u, t, vt, quarter, KT / 4, 2, lane, smem, sbase, nf, wait_all);
+          }
+          // the tile's factors (the V tile comes with them), mostly there before S
+          if (C::CONVERTERS && ok) ok = wait_all(W_VFULL + vt % C::VSTAGES, (vt / C::VSTAGES) & 1);
           if (ok) ok = wait_all(W_SFULL + buf, SLOTS == 1 ? (j >> 1) & 1 : j & 1);
           tc_fence_after();
           if (ok && warp_live) {
@@ -663,41 +731,86 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS, CODES>::THREADS, WideCfg<D, 
               }
               tmem_wait_st();
             }
-            // CODES: a row of S is loaded by halves, the second one twice (for
-            // its maximum and for P): a whole row of 128 spilled registers in
-            // the loop, and the little L1 that shared memory leaves made their
-            // loads wait for L2
-            constexpr int HALF = CODES ? KT / 2 : KT;
-            float sv[HALF];
-            uint32_t* raw = reinterpret_cast<uint32_t*>(sv);
-            auto load = [&](int c0) {
-#pragma unroll
-              for (int y = 0; y < HALF / 32; ++y) tmem_ld32(tSj + c0 + 32 * y, raw + 32 * y);
-              tmem_wait_ld();
-            };
-            [[maybe_unused]] const float4* fact =
-                reinterpret_cast<const float4*>(smem + C::OFF_FACT) + warp * C::BLOCKS;
-            // of a block's scores to x + log2 sv
-            [[maybe_unused]] auto factor = [&](float4 f) { return finite(back * f.x); };
-            float m_tile = -INFINITY;
+            float alpha = 1.f;                       // what the earlier tiles' O takes
+            float sum4[4] = {0.f, 0.f, 0.f, 0.f};
             if constexpr (CODES) {
+              // A row of S by halves: the second one for its maximum, the first
+              // one, which then becomes P, and the second one again.  (A whole row
+              // of 128 spilled registers in the loop, and the little L1 that shared
+              // memory leaves made their loads wait for L2.  32 columns at a time in
+              // one pass, with what had been done scaled where the maximum grew,
+              // took more instructions, which is what bounds a tile: 259 us.)
+              constexpr int HALF = KT / 2, HB = HALF / kScaleBlock;
+              float sv[HALF];
+              auto load = [&](int c0) {
+#pragma unroll
+                for (int y = 0; y < HALF / 32; ++y)
+                  tmem_ld32(tSj + c0 + 32 * y, reinterpret_cast<uint32_t*>(sv) + 32 * y);
+                tmem_wait_ld();
+              };
+              // block b's factor and log2 sv, twice each, and what the sum takes of P
+              const uint32_t set = C::CONVERTERS ? vt % C::VSTAGES : warp;
+              const uint32_t facts = sbase + C::OFF_FACT + set * (C::BLOCKS * 16);
+              const uint32_t takes = sbase + C::OFF_FACT + (C::FACTS * 16 + set * 4) * C::BLOCKS;
+              auto factors = [&](int b, uint64_t& k, uint64_t& v) {
+                asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(k), "=l"(v) : "r"(facts + b * 16));
+              };
+              const uint64_t back2 = splat2(back);
+              float m_tile = -INFINITY;
 #pragma unroll
               for (int c0 = HALF; c0 >= 0; c0 -= HALF) {
                 load(c0);
 #pragma unroll
-                for (int b = 0; b < HALF / 16; ++b) {
+                for (int b = 0; b < HB; ++b) {
                   const float* s = sv + 16 * b;
-                  const float4 f = fact[c0 / 16 + b];
+                  uint64_t k, v;
+                  factors(c0 / 16 + b, k, v);
                   float a[4];
 #pragma unroll
                   for (int y = 0; y < 4; ++y) a[y] = fmax3(s[y], s[y + 4], s[y + 8]);
+                  const float top = fmax3(fmax3(a[0], s[12], a[1]), fmax3(s[13], a[2], s[14]), fmaxf(a[3], s[15]));
+                  m_tile = fmaxf(m_tile, fmaf(top, __uint_as_float(static_cast<uint32_t>(k)) * back,
+                                              __uint_as_float(static_cast<uint32_t>(v))));
+                }
+              }
+              // the reference moves only when the maximum grows by more than
+              // 2^8 (as in the prompt forward): few tiles rescale O
+              const bool grow = m_tile > m_used + 8.f;
+              const float m_new = grow ? m_tile : m_used;
+              alpha = grow ? ex2(m_used - m_new) : 1.f;
+              l *= alpha;
+              m_used = m_new;
+              const uint64_t shift2 = splat2(kPOffset - (m_used == -INFINITY ? 0.f : m_used));
 #pragma unroll
-                  for (int y = 0; y < 4; ++y) a[y] = fmaxf(a[y], s[y + 12]);
-                  m_tile = fmaxf(m_tile, fmaf(fmax3(a[0], a[1], fmaxf(a[2], a[3])), factor(f), f.y));
+              for (int c0 = 0; c0 < KT; c0 += HALF) {
+                if (c0 > 0) load(c0);
+#pragma unroll
+                for (int b = 0; b < HB; ++b) {
+                  uint64_t k, v;
+                  float take;
+                  factors(c0 / 16 + b, k, v);
+                  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(take) : "r"(takes + (c0 / 16 + b) * 4));
+                  const uint64_t sc2 = mul2(k, back2), nm2 = add2(v, shift2);
+                  uint32_t pk[8];
+                  float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+                  for (int y = 0; y < 8; ++y) {
+                    float a0, a1;
+                    fma2_bc(a0, a1, sv[b * 16 + 2 * y], sv[b * 16 + 2 * y + 1], sc2, nm2);
+                    const float p0 = ex2(a0), p1 = ex2(a1);
+                    add2_acc(s0, s1, p0, p1);
+                    pk[y] = pack_f16(p0, p1);
+                  }
+                  sum4[b & 3] = fmaf(s0 + s1, take, sum4[b & 3]);
+                  tmem_st8(tSj + (c0 / 16 + b) * 8, pk);
                 }
               }
             } else {
-              load(0);
+              float sv[KT];
+              uint32_t* raw = reinterpret_cast<uint32_t*>(sv);
+#pragma unroll
+              for (int y = 0; y < KT / 32; ++y) tmem_ld32(tSj + 32 * y, raw + 32 * y);
+              tmem_wait_ld();
               float mx8[8];
 #pragma unroll
               for (int y = 0; y < 8; ++y) mx8[y] = fmax3(sv[y], sv[y + 8], sv[y + 16]);
@@ -709,40 +822,15 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS, CODES>::THREADS, WideCfg<D, 
               for (int y = 0; y < 8; ++y) mx8[y] = fmaxf(mx8[y], sv[KT - 8 + y]);
               const float mx = fmax3(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(mx8[3], mx8[4], mx8[5]),
                                      fmaxf(mx8[6], mx8[7]));
-              m_tile = mx * P.scale_log2;
-            }
-            // the reference moves only when the maximum grows by more than
-            // 2^8 (as in the prompt forward): few tiles rescale O
-            const bool grow = m_tile > m_used + 8.f;
-            const float m_new = grow ? m_tile : m_used;
-            const float alpha = grow ? ex2(m_used - m_new) : 1.f;
-            l *= alpha;
-            m_used = m_new;
-            const float m_ref = m_used == -INFINITY ? 0.f : m_used;
-            float sum4[4] = {0.f, 0.f, 0.f, 0.f};
-            if constexpr (CODES) {
-#pragma unroll
-              for (int c0 = 0; c0 < KT; c0 += HALF) {
-                if (c0 > 0) load(c0);
-#pragma unroll
-                for (int b = 0; b < HALF / 16; ++b) {
-                  const float4 f = fact[c0 / 16 + b];
-                  const uint64_t sc2 = splat2(factor(f)), nm2 = splat2(f.y - m_ref + kPOffset);
-                  uint32_t pk[8];
-                  float s0 = 0.f, s1 = 0.f;
-#pragma unroll
-                  for (int y = 0; y < 8; ++y) {
-                    float a0, a1;
-                    fma2_bc(a0, a1, sv[b * 16 + 2 * y], sv[b * 16 + 2 * y + 1], sc2, nm2);
-                    const float p0 = ex2(a0), p1 = ex2(a1);
-                    add2_acc(s0, s1, p0, p1);
-                    pk[y] = pack_f16(p0, p1);
-                  }
-                  sum4[b & 3] = fmaf(s0 + s1, f.z, sum4[b & 3]);
-                  tmem_st8(tSj + (c0 / 16 + b) * 8, pk);
-                }
-              }
-            } else {
+              // the reference moves only when the maximum grows by more than
+              // 2^8 (as in the prompt forward): few tiles rescale O
+              const float m_tile = mx * P.scale_log2;
+              const bool grow = m_tile > m_used + 8.f;
+              const float m_new = grow ? m_tile : m_used;
+              alpha = grow ? ex2(m_used - m_new) : 1.f;
+              l *= alpha;
+              m_used = m_new;
+              const float m_ref = m_used == -INFINITY ? 0.f : m_used;
               const uint64_t sc2 = splat2(P.scale_log2), nm2 = splat2(-m_ref);
 #pragma unroll
               for (int c4 = 0; c4 < KT / 32; ++c4) {
@@ -759,7 +847,7 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS, CODES>::THREADS, WideCfg<D, 
                 tmem_st16(tSj + c4 * 16, pk);
               }
             }
-            if (done > 0 && __any_sync(0xffffffffu, grow)) {
+            if (done > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
               // O holds the PVs of the earlier tiles; with two S buffers the
               // last one may still run
               if (SLOTS == 1) {
