@@ -643,14 +643,20 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS, CODES>::THREADS, WideCfg<D, 
           constexpr int LPR = D / 8, RPI = 32 / LPR;     // lanes a row, rows an instruction
           const unsigned in_rows = __ballot_sync(0xffffffffu, mine);
           if constexpr (CODES) {
-            // to two parts, a power of two per row; lane l keeps what undoes row l's
-#pragma unroll 4
+            // to two parts, a power of two per row; lane l keeps what undoes row
+            // l's.  All loads first: behind the stream of K and V each takes some
+            // 3000 cycles (four at a time 13000 of a unit's 20000 for its ends).
+            uint4 x[32 / RPI];
+#pragma unroll
             for (int i = 0; i < 32 / RPI; ++i) {
               const int from = i * RPI + lane / LPR;
               const uint64_t row = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(src), from);
-              uint4 x = make_uint4(0u, 0u, 0u, 0u);
-              if ((in_rows >> from) & 1u) x = *reinterpret_cast<const uint4*>(row + (lane % LPR) * 16);
-              const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+              x[i] = make_uint4(0u, 0u, 0u, 0u);
+              if ((in_rows >> from) & 1u) x[i] = *reinterpret_cast<const uint4*>(row + (lane % LPR) * 16);
+            }
+#pragma unroll
+            for (int i = 0; i < 32 / RPI; ++i) {
+              const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
               uint32_t top = 0;
 #pragma unroll
               for (int y = 0; y < 4; ++y) top = max(top, max(w[y] & 0x7fffu, (w[y] >> 16) & 0x7fffu));
@@ -659,8 +665,8 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS, CODES>::THREADS, WideCfg<D, 
               const int up = row_shift(top) - 6;       // the largest at [2^7, 2^8)
               uint2 hi, lo;
               split_e4m3(w, pow2(up), hi, lo);
-              uint8_t* to = smem + C::OFF_Q + slot * C::QTILE + Load::word16(quarter * 32 + from, (lane % LPR) >> 1) +
-                            (lane & 1) * 8;
+              uint8_t* to = smem + C::OFF_Q + slot * C::QTILE +
+                            Load::word16(quarter * 32 + i * RPI + lane / LPR, (lane % LPR) >> 1) + (lane & 1) * 8;
               *reinterpret_cast<uint2*>(to) = hi;
               *reinterpret_cast<uint2*>(to + 128 * D) = lo;
               // (an infinity has no code: its row becomes NaN, as its scores are)
