@@ -842,7 +842,7 @@ fm_status tree_fwd(const fm_cache* c, const fm_tree_desc* t, const void* q, cons
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (codes) {
     // a page, or a tile's part of it
-    const int box = W.kind == MID && c->page_size > MidGeo::KT ? MidGeo::KT : c->page_size;
+    const int box = W.kind != NARROW && c->page_size > MidGeo::KT ? MidGeo::KT : c->page_size;
     P.box_shift = page_shift(box);
     Tree8Params A{P, k_scale, v_scale, static_cast<const uint8_t*>(v_pool)};
     CUtensorMap tk, tv;

@@ -91,6 +91,11 @@ struct WideGeo {
   __device__ static __forceinline__ int end(int rows) { return rows > 128 ? 5 : 10; }
 };
 
+struct Wide8Geo {
+  static constexpr int R = 256, KT = 64, LEAST = 4;
+  __device__ static __forceinline__ int end(int) { return 10; }
+};
+
 // Row tiles of a sequence, keys and tiles of one of them (total * H is at
 // most 2^30: 32 bits hold every row).
 template <class Geo>

@@ -52,36 +52,40 @@ struct WideCfg {
   static constexpr bool CODES = CODES_;
   static constexpr int DIM = D;
   static_assert(D == 128 || SLOTS == 1, "d = 64 runs with tiles of 128 rows side by side");
-  using Geo = std::conditional_t<SLOTS == 2, WideGeo, MidGeo>;
+  // Two S buffers of 64 columns a slot: S of a tile is computed while the
+  // softmax of the one before runs, and slots do not take turns.
+  static constexpr bool BUFS = SLOTS == 1 || CODES;
+  using Geo = std::conditional_t<SLOTS == 1, MidGeo, std::conditional_t<CODES, Wide8Geo, WideGeo>>;
   static constexpr int KT = Geo::KT;
   static constexpr int TILE = KT * D * 2;               // bytes of a V tile in front of the MMAs
   static constexpr int KTILE = CODES ? KT * D : TILE;   // of a K tile
   static constexpr int QTILE = 128 * D * 2;             // of a slot's Q (CODES: two parts of one byte)
-  static constexpr int KSTAGES = CODES ? (D == 64 ? 5 : 3) : D == 64 ? 4 : 2;
-  static constexpr int VSTAGES = CODES ? 2 : D == 64 ? 5 : 3;
-  static constexpr int VCODES = !CODES ? 0 : D == 64 ? 4 : 2;   // stages of V's codes
+  static constexpr int KSTAGES = CODES ? (D == 64 || SLOTS == 2 ? 5 : 3) : D == 64 ? 4 : 2;
+  static constexpr int VSTAGES = CODES ? (SLOTS == 2 ? 3 : 2) : D == 64 ? 5 : 3;
+  static constexpr int VCODES = !CODES ? 0 : D == 64 || SLOTS == 2 ? 4 : 2;   // stages of V's codes
   static constexpr int BLOCKS = KT / kScaleBlock;
   static constexpr int SM_WARPS = 4 * SLOTS;            // softmax
-  // CODES: who turns V's codes into f16.  SLOTS = 1: two warps, in the places of
-  // the V loader (K's loads both) and of a second slot's MMAs.  SLOTS = 2: the
-  // softmax warps, a share each, while S of the tile is multiplied.
-  static constexpr bool CONVERTERS = CODES && SLOTS == 1;
-  static constexpr int CV_WARPS = !CODES ? 0 : CONVERTERS ? 2 : SM_WARPS;
-  // Sets of a tile's factors: by stage, or by warp where the softmax warps find
-  // them (one that waits for the other slot's keeps step with it: 228 us).
-  static constexpr int FACTS = CONVERTERS ? VSTAGES : SM_WARPS;
-  static constexpr int THREADS = 32 * (SM_WARPS + 4);
+  // CODES: warps that turn V's codes into f16: a warpgroup of their own, or with
+  // SLOTS = 1, where registers are short, the places of the V loader (K's loads
+  // both) and of a second slot's MMAs.
+  static constexpr int CV_WARPS = !CODES ? 0 : SLOTS == 2 ? 4 : 2;
+  static constexpr int THREADS = 32 * (SM_WARPS + 4 + (SLOTS == 2 ? CV_WARPS : 0));
+  static constexpr bool LOADS_BOTH = CODES && SLOTS == 1;
+  // S of a tile is issued once its V tile and factors are there, which saves the
+  // softmax a wait.  (Not with V's two stages of SLOTS = 1: 32 nodes over 131072
+  // keys 37.8 us so and 34.5 us with that wait.)
+  static constexpr bool V_FIRST = CODES && SLOTS == 2;
   static constexpr int BLOCKS_PER_SM = SLOTS == 2 ? 1 : 2;
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_K = SLOTS * QTILE;
   static constexpr int OFF_V = OFF_K + KSTAGES * KTILE;
   static constexpr int OFF_VC = OFF_V + VSTAGES * TILE;                      // V's codes
-  static constexpr int OFF_FACT = OFF_VC + VCODES * KTILE;        // CODES: [FACTS][BLOCKS] of float4, then of float
-  static constexpr int OFF_SCALE = OFF_FACT + (CODES ? FACTS * BLOCKS * 20 : 0);     // float [VCODES][K, V][BLOCKS]
-  static constexpr int OFF_ML = OFF_SCALE + VCODES * 2 * BLOCKS * 4;         // SLOTS 2: float2 [slot][128]
-  static constexpr int OFF_NF = OFF_ML + (SLOTS == 2 ? 2 * 128 * 8 : 0);   // [4][8] keys with values not finite
+  static constexpr int OFF_FACT = OFF_VC + VCODES * KTILE;        // CODES: [VSTAGES][BLOCKS] of float4, then of float
+  static constexpr int OFF_SCALE = OFF_FACT + (CODES ? VSTAGES * BLOCKS * 20 : 0);     // float [VCODES][K, V][BLOCKS]
+  static constexpr int OFF_ML = OFF_SCALE + VCODES * 2 * BLOCKS * 4;         // BUFS false: float2 [slot][128]
+  static constexpr int OFF_NF = OFF_ML + (BUFS ? 0 : 2 * 128 * 8);   // [4][8] keys with values not finite
   static constexpr int OFF_BAR = OFF_NF + 128;
-  static constexpr int NBAR = CODES ? 42 : 34;
+  static constexpr int NBAR = CODES ? 48 : 34;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;   // abort flag, TMEM address
   static constexpr int OFF_PAR = OFF_MISC + 16;         // int16 [256] parents of the unit's nodes
   static constexpr int USED = OFF_PAR + 512;
@@ -93,18 +97,20 @@ struct WideCfg {
   static_assert(4 * 4096 <= QTILE, "room for the output's staging");
   static constexpr uint32_t T_COLS = 256 * SLOTS, T_O = 128 * SLOTS;
   // register split: the softmax warpgroups' and the others' budgets add up to
-  // what the block is launched with (384 x 168, 256 x 128)
-  static constexpr uint32_t REGS_SOFTMAX = CODES ? (SLOTS == 2 ? 184 : 152) : SLOTS == 2 ? 216 : 184;
-  static constexpr uint32_t REGS_PRODUCER = CODES ? (SLOTS == 2 ? 136 : 104) : 72;
+  // what the block is launched with (384 x 168, 256 x 128; CODES: 512 x 128)
+  static constexpr uint32_t REGS_SOFTMAX = CODES ? 152 : SLOTS == 2 ? 216 : 184;
+  static constexpr uint32_t REGS_PRODUCER = CODES ? 104 : 72;
   static constexpr int MIN_LAUNCH_REGS =
-      (32 * SM_WARPS * REGS_SOFTMAX + 128 * REGS_PRODUCER + THREADS - 1) / THREADS;
+      (32 * SM_WARPS * REGS_SOFTMAX + (THREADS - 32 * SM_WARPS) * REGS_PRODUCER + THREADS - 1) / THREADS;
 };
 
 enum {
   W_QFULL = 0, W_SFULL = 2, W_PFULL = 4, W_PVDONE = 6, W_OEMPTY = 8, W_KFULL = 10, W_KEMPTY = 15,
   W_VFULL = 20, W_VEMPTY = 25, W_DRAIN = 30, W_TURN = 31, W_QEMPTY = 33,
   W_VCODES = 34, W_VCEMPTY = 38,   // CODES: stages of V's codes
-  W_PVTILE = W_PVDONE + 1   // SLOTS 1: the PV of each tile (the SFULL and PFULL are its two buffers')
+  W_PVTILE = W_PVDONE + 1,  // SLOTS 1: the PV of each tile (the SFULL and PFULL are its two buffers')
+  // BUFS of two slots: the second slot's SFULL and PFULL, the slots' PVTILE
+  W_SFULL_B = 42, W_PFULL_B = 44, W_PVTILE_2 = 46
 };
 
 // How the slots share a piece.
@@ -114,9 +120,9 @@ struct WideSplit {
   // slot s takes part at all
   __device__ __forceinline__ bool active(int s) const { return s == 0 || rows || n > 1; }
 };
-template <int SLOTS>
+template <bool BUFS>
 __device__ __forceinline__ WideSplit wide_split(const TreePiece& u) {
-  return WideSplit{SLOTS == 1 || u.rows > 128, u.keys > 0 ? u.t1 - u.t0 : 0};
+  return WideSplit{BUFS || u.rows > 128, u.keys > 0 ? u.t1 - u.t0 : 0};
 }
 
 // 16 bytes from global to shared memory without a register or a line of L1;
@@ -142,11 +148,11 @@ __device__ __forceinline__ const TreeParams& tree_params(const Tree8Params& A) {
 
 // CODES: rows [part * rows, (part + 1) * rows) of V tile `e` of the block, clean
 // of what not every row sees (see fix_row8), and what the scales of its blocks
-// bring to the softmax; `count` arrivals.  (The stage's last PV has ended, so the
-// softmax of that tile has read its factors.)
+// bring to the softmax.  (The stage's last PV has ended, so the softmax of that
+// tile has read its factors.)
 template <typename C, typename W>
 __device__ __forceinline__ bool convert_v(const TreeParams& P, const TreePiece& u, int t, uint32_t e, int part,
-                                          int rows, int count, int lane, const uint8_t* smem, uint32_t sbase,
+                                          int rows, int lane, const uint8_t* smem, uint32_t sbase,
                                           uint32_t* nf, W wait_all) {
   using V = VTile8<C::DIM, C::KT>;
   const uint32_t cs = e % C::VCODES, st = e % C::VSTAGES;
@@ -154,16 +160,15 @@ __device__ __forceinline__ bool convert_v(const TreeParams& P, const TreePiece& 
   if (ok && e >= C::VSTAGES) ok = wait_all(W_VEMPTY + st, (e / C::VSTAGES - 1) & 1);
   if (!ok) return false;
   const float* scales = reinterpret_cast<const float*>(smem + C::OFF_SCALE) + cs * 2 * C::BLOCKS;
-  const int set = C::CONVERTERS ? st : threadIdx.x >> 5;
-  const int b = (C::CONVERTERS ? part * (rows / kScaleBlock) : 0) + lane;
-  if (lane < (C::CONVERTERS ? rows / kScaleBlock : C::BLOCKS)) {
+  const int b = part * (rows / kScaleBlock) + lane;
+  if (lane < rows / kScaleBlock) {
     const float4 f = block_factors(scales[b], scales[C::BLOCKS + b]);
     // in pairs, as the packed arithmetic takes them
-    asm volatile("st.shared.v4.f32 [%0], {%1, %1, %2, %2};" ::"r"(sbase + C::OFF_FACT + (set * C::BLOCKS + b) * 16),
+    asm volatile("st.shared.v4.f32 [%0], {%1, %1, %2, %2};" ::"r"(sbase + C::OFF_FACT + (st * C::BLOCKS + b) * 16),
                  "f"(f.x), "f"(f.y)
                  : "memory");
-    asm volatile("st.shared.f32 [%0], %1;" ::"r"(sbase + C::OFF_FACT + C::FACTS * C::BLOCKS * 16 +
-                                                 (set * C::BLOCKS + b) * 4),
+    asm volatile("st.shared.f32 [%0], %1;" ::"r"(sbase + C::OFF_FACT + C::VSTAGES * C::BLOCKS * 16 +
+                                                 (st * C::BLOCKS + b) * 4),
                  "f"(f.z)
                  : "memory");
   }
@@ -189,11 +194,8 @@ __device__ __forceinline__ bool convert_v(const TreeParams& P, const TreePiece& 
     }
   }
   fence_proxy_async_smem();
-  __syncwarp();
-  if (lane == 0) {
-    mbar_arrive_count(sbase + C::OFF_BAR + 8u * (W_VCEMPTY + cs), count);
-    mbar_arrive_count(sbase + C::OFF_BAR + 8u * (W_VFULL + st), count);
-  }
+  mbar_arrive_warp(sbase + C::OFF_BAR + 8u * (W_VCEMPTY + cs));
+  if (lane == 0) mbar_arrive(sbase + C::OFF_BAR + 8u * (W_VFULL + st));
   return true;
 }
 
@@ -228,7 +230,7 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS, CODES>::THREADS, WideCfg<D, 
   if (tid == 0) {
     for (int s = 0; s < 2; ++s) {
       mbar_init(bar(W_QFULL + s), q_tma ? 1 : 4);   // else one arrival per softmax warp of the slot
-      mbar_init(bar(W_SFULL + s), 1);
+      mbar_init(bar(W_SFULL + s), C::V_FIRST ? 2 : 1);
       mbar_init(bar(W_PFULL + s), 4);
       mbar_init(bar(W_PVDONE + s), 1);
       mbar_init(bar(W_OEMPTY + s), C::SM_WARPS);   // every slot's warps may read O of either
@@ -248,6 +250,11 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS, CODES>::THREADS, WideCfg<D, 
       for (int i = 0; i < C::VCODES; ++i) {
         mbar_init(bar(W_VCODES + i), Load::ARRIVALS);
         mbar_init(bar(W_VCEMPTY + i), C::CV_WARPS);
+      }
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(bar(W_SFULL_B + i), 2);
+        mbar_init(bar(W_PFULL_B + i), 4);
+        mbar_init(bar(W_PVTILE_2 + i), 1);
       }
     }
     mbar_init(bar(W_DRAIN), SLOTS);
@@ -271,6 +278,10 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS, CODES>::THREADS, WideCfg<D, 
   tc_fence_after();
   const uint32_t tbase = *tmem_slot;
 
+  // BUFS: the barriers of a slot's buffer
+  auto s_full = [](int slot, int buf) { return (SLOTS == 2 && slot ? W_SFULL_B : W_SFULL) + buf; };
+  auto p_full = [](int slot, int buf) { return (SLOTS == 2 && slot ? W_PFULL_B : W_PFULL) + buf; };
+  auto pv_tile = [](int slot) { return SLOTS == 2 ? W_PVTILE_2 + slot : static_cast<int>(W_PVTILE); };
   auto wait = [&](int b, uint32_t parity) -> bool { return tree_wait(bar(b), parity, P, abort_flag); };
   // every lane gets the same answer
   auto wait_all = [&](int b, uint32_t parity) -> bool {
@@ -279,10 +290,10 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS, CODES>::THREADS, WideCfg<D, 
 
   if (warp >= C::SM_WARPS) {
     regs_decrease<C::REGS_PRODUCER>();
-    if (warp == K_WARP || (warp == V_WARP && !C::CONVERTERS)) {
+    if (warp == K_WARP || (warp == V_WARP && !C::LOADS_BOTH)) {
       // ---------------------------------------------------------- K / V loads
       const bool isk = warp == K_WARP;
-      constexpr bool BOTH = C::CONVERTERS;             // K's warp loads V too
+      constexpr bool BOTH = C::LOADS_BOTH;
       uint32_t vst = 0, vuse = 0;
       auto load_v_codes = [&](const TreePiece& u, int t, int page, uint32_t st, uint64_t policy) {
         if constexpr (CODES) {                         // and the scales of both
@@ -372,7 +383,7 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS, CODES>::THREADS, WideCfg<D, 
       uint32_t turn = 0;        // turns taken
       bool ok = true;
       while (ok && u.next(P)) {
-        const WideSplit w = wide_split<SLOTS>(u);
+        const WideSplit w = wide_split<C::BUFS>(u);
         if (w.n == 0) continue;
         // The two MMA warps take turns: a turn is one tile's PV and the next
         // one's S.  Without it the slots fall into step (both wait for the
@@ -419,34 +430,39 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS, CODES>::THREADS, WideCfg<D, 
           ok = wait_all(W_QFULL + s, qn & 1);
           ++qn;
         }
-        if constexpr (SLOTS == 1) {
+        if constexpr (C::BUFS) {
           // S of tile x + 1 overwrites P of tile x - 1, whose PV this warp has
-          // issued before; then PV of tile x
-          auto issue_s = [&](uint32_t tile) {
+          // issued before; then PV of tile x.  (Two slots have a warp each: one
+          // for both spent 2700 cycles a tile on its waits and issues, 291 us.)
+          uint32_t fs = vst, fp = vph;             // V's stage of the next S
+          auto issue_s = [&](uint32_t tile) -> bool {
+            if (!wait_all(W_KFULL + ks, kp)) return false;
+            if constexpr (C::V_FIRST) {
+              if (!wait_all(W_VFULL + fs, fp)) return false;
+              advance(fs, fp, 1, C::VSTAGES);
+            }
             const uint32_t dK = dK0 + ks * (C::KTILE >> 4);
             tc_fence_after();
             if (elect_one()) {
 #pragma unroll
               for (int kk = 0; kk < SSTEPS; ++kk) s_step(tS + 64 * (tile & 1), dK, kk);
-              mma_commit(bar(W_SFULL + (tile & 1)));
+              mma_commit(bar(s_full(s, tile & 1)));
               mma_commit(bar(W_KEMPTY + ks));
+              // (what this thread knows of the factors goes on with its own arrival)
+              if constexpr (C::V_FIRST) mbar_arrive(bar(s_full(s, tile & 1)));
             }
             __syncwarp();
             advance(ks, kp, 1, C::KSTAGES);
+            return true;
           };
-          if (ok) ok = wait_all(W_KFULL + ks, kp);
-          if (ok) issue_s(np);
+          if (ok) ok = issue_s(np);
 #pragma unroll 1
           for (int x = 0; ok && x < w.n; ++x, ++np) {
-            if (x + 1 < w.n) {
-              ok = wait_all(W_KFULL + ks, kp);
-              if (!ok) break;
-              issue_s(np + 1);
-            }
-            ok = wait_all(W_VFULL + vs, vp);
+            if (x + 1 < w.n) ok = issue_s(np + 1);
+            if (ok && !C::V_FIRST) ok = wait_all(W_VFULL + vs, vp);
             // O is overwritten: the last piece's must have been read
-            if (ok && x == 0 && pieces > 0) ok = wait_all(W_OEMPTY, (pieces - 1) & 1);
-            if (ok) ok = wait_all(W_PFULL + (np & 1), (np >> 1) & 1);
+            if (ok && x == 0 && pieces > 0) ok = wait_all(W_OEMPTY + s, (pieces - 1) & 1);
+            if (ok) ok = wait_all(p_full(s, np & 1), (np >> 1) & 1);
             if (!ok) break;
             tc_fence_after();
             const uint32_t dV = dV0 + vs * (C::TILE >> 4), tP = tS + 64 * (np & 1);
@@ -454,8 +470,8 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS, CODES>::THREADS, WideCfg<D, 
 #pragma unroll
               for (int kk = 0; kk < KT / 16; ++kk)
                 mma_ts(tO, tP + kk * 8, sdesc_at(dV, kk * 2048), idPV, (x > 0 || kk > 0) ? 1u : 0u);
-              mma_commit(bar(W_PVTILE));
-              if (x + 1 == w.n) mma_commit(bar(W_PVDONE));
+              mma_commit(bar(pv_tile(s)));
+              if (x + 1 == w.n) mma_commit(bar(W_PVDONE + s));
               mma_commit(bar(W_VEMPTY + vs));
             }
             __syncwarp();
@@ -541,17 +557,18 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS, CODES>::THREADS, WideCfg<D, 
         mma_commit(bar(W_DRAIN));
         mbar_wait(bar(W_DRAIN), 0, P.status, P.wait_ns);
       }
-    } else if (C::CONVERTERS) {
+    } else if (CODES) {
       // ---------------------------------------------------------- V's codes to f16
-      if constexpr (C::CONVERTERS) {
+      if constexpr (CODES) {
+        const int part = SLOTS == 2 ? warp - (K_WARP + 4) : warp == V_WARP ? 0 : 1;
         uint32_t e = 0, pieces = 0;
         bool ok = true;
         while (ok && u.next(P)) {
           if (u.keys == 0) continue;
 #pragma unroll 1
           for (int t = u.t0; ok && t < u.t1; ++t, ++e)
-            ok = convert_v<C>(P, u, t, e, warp == V_WARP ? 0 : 1, KT / 2, 1, lane, smem, sbase,
-                              nf_all + 8 * (pieces % 4), wait_all);
+            ok = convert_v<C>(P, u, t, e, part, KT / C::CV_WARPS, lane, smem, sbase, nf_all + 8 * (pieces % 4),
+                              wait_all);
           ++pieces;
         }
       }
@@ -574,7 +591,7 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS, CODES>::THREADS, WideCfg<D, 
     int par_of = -1;                                   // the sequence whose parents are in shared memory
     if (tid == 0) P.rec[blockIdx.x] = make_int4(-1, 0, 0, 0);
     while (u.next(P)) {
-      const WideSplit w = wide_split<SLOTS>(u);
+      const WideSplit w = wide_split<C::BUFS>(u);
       const int ur = w.rows ? slot * 128 + r : r;      // row of the unit
       const bool mine = ur < u.rows;
       const int rr = u.row_first + ur;
@@ -594,11 +611,12 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS, CODES>::THREADS, WideCfg<D, 
       }
       const bool active = w.active(slot);
       // This piece's flags, and the next piece's, read by nobody now, cleared.
-      // (CODES: the warps that set them may be two tiles ahead, and so two
-      // pieces: the one after the next's.)
-      constexpr int AHEAD = CODES ? 2 : 1;
-      uint32_t* nf = nf_all + 8 * (pieces % (2 * AHEAD));
-      if (tid < 8) nf_all[8 * ((pieces + AHEAD) % (2 * AHEAD)) + tid] = 0;
+      // (CODES: the warps that set them may be as many tiles ahead as V has
+      // stages, and so as many pieces.)
+      constexpr int AHEAD = CODES ? C::VSTAGES : 1, SETS = CODES ? 4 : 2;
+      static_assert(AHEAD < SETS, "sets of flags");
+      uint32_t* nf = nf_all + 8 * (pieces % SETS);
+      if (tid < 8) nf_all[8 * ((pieces + AHEAD) % SETS) + tid] = 0;
       const int part0 = u.origin / KT;                 // tiles from here on are not seen by all
       bool live = mine;
       if (P.tree) {
@@ -693,20 +711,13 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS, CODES>::THREADS, WideCfg<D, 
         for (int x0 = w.rows ? 0 : slot; x0 < w.n; x0 += w.rows ? 1 : 2) {
           const int t = u.t0 + x0;
           const bool partial = t >= part0;
-          // SLOTS 1: the buffers alternate
-          const int buf = SLOTS == 1 ? j & 1 : slot;
-          const uint32_t tSj = SLOTS == 1 ? tS + 64 * (j & 1) : tS;
+          // BUFS: they alternate
+          const int b_s = C::BUFS ? s_full(slot, j & 1) : W_SFULL + slot, b_p = C::BUFS ? p_full(slot, j & 1) : W_PFULL + slot;
+          const uint32_t tSj = C::BUFS ? tS + 64 * (j & 1) : tS;
           const uint32_t vt = e0 + x0;
-          if constexpr (CODES && !C::CONVERTERS) {
-            // this warp's rows of the V tile (both halves of the slot's rows where
-            // the other slot has tiles of its own)
-            if (ok)
-              ok = w.rows ? convert_v<C>(P, u, t, vt, warp, KT / 8, 1, lane, smem, sbase, nf, wait_all)
-                          : convert_v<C>(P, u, t, vt, quarter, KT / 4, 2, lane, smem, sbase, nf, wait_all);
-          }
-          // the tile's factors (the V tile comes with them), mostly there before S
-          if (C::CONVERTERS && ok) ok = wait_all(W_VFULL + vt % C::VSTAGES, (vt / C::VSTAGES) & 1);
-          if (ok) ok = wait_all(W_SFULL + buf, SLOTS == 1 ? (j >> 1) & 1 : j & 1);
+          // the tile's factors
+          if (CODES && !C::V_FIRST && ok) ok = wait_all(W_VFULL + vt % C::VSTAGES, (vt / C::VSTAGES) & 1);
+          if (ok) ok = wait_all(b_s, C::BUFS ? (j >> 1) & 1 : j & 1);
           tc_fence_after();
           if (ok && warp_live) {
             if (partial) {
@@ -740,44 +751,37 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS, CODES>::THREADS, WideCfg<D, 
             float alpha = 1.f;                       // what the earlier tiles' O takes
             float sum4[4] = {0.f, 0.f, 0.f, 0.f};
             if constexpr (CODES) {
-              // A row of S by halves: the second one for its maximum, the first
-              // one, which then becomes P, and the second one again.  (A whole row
-              // of 128 spilled registers in the loop, and the little L1 that shared
-              // memory leaves made their loads wait for L2.  32 columns at a time in
-              // one pass, with what had been done scaled where the maximum grew,
-              // took more instructions, which is what bounds a tile: 259 us.)
-              constexpr int HALF = KT / 2, HB = HALF / kScaleBlock;
-              float sv[HALF];
-              auto load = [&](int c0) {
+              // (In tiles of 128 keys with one S a slot, as the bf16 pairs, a row of
+              // S spilled registers in this loop or was loaded twice, and its
+              // softmax and its MMAs came one after the other: 198 us.  32 columns
+              // at a time in one pass, with what had been done scaled where the
+              // maximum grew: 259 us.)
+              float sv[KT];
 #pragma unroll
-                for (int y = 0; y < HALF / 32; ++y)
-                  tmem_ld32(tSj + c0 + 32 * y, reinterpret_cast<uint32_t*>(sv) + 32 * y);
-                tmem_wait_ld();
-              };
+              for (int y = 0; y < KT / 32; ++y) tmem_ld32(tSj + 32 * y, reinterpret_cast<uint32_t*>(sv) + 32 * y);
+              tmem_wait_ld();
               // block b's factor and log2 sv, twice each, and what the sum takes of P
-              const uint32_t set = C::CONVERTERS ? vt % C::VSTAGES : warp;
-              const uint32_t facts = sbase + C::OFF_FACT + set * (C::BLOCKS * 16);
-              const uint32_t takes = sbase + C::OFF_FACT + (C::FACTS * 16 + set * 4) * C::BLOCKS;
+              uint32_t facts = sbase + C::OFF_FACT + vt % C::VSTAGES * (C::BLOCKS * 16);
+              uint32_t takes = sbase + C::OFF_FACT + (C::VSTAGES * 16 + vt % C::VSTAGES * 4) * C::BLOCKS;
+              // (the addresses only from here on, after the wait for S: the loads
+              // themselves may be moved)
+              asm volatile("" : "+r"(facts), "+r"(takes)::"memory");
               auto factors = [&](int b, uint64_t& k, uint64_t& v) {
-                asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(k), "=l"(v) : "r"(facts + b * 16));
+                asm("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(k), "=l"(v) : "r"(facts + b * 16));
               };
               const uint64_t back2 = splat2(back);
               float m_tile = -INFINITY;
 #pragma unroll
-              for (int c0 = HALF; c0 >= 0; c0 -= HALF) {
-                load(c0);
+              for (int b = 0; b < C::BLOCKS; ++b) {
+                const float* s = sv + 16 * b;
+                uint64_t k, v;
+                factors(b, k, v);
+                float a[4];
 #pragma unroll
-                for (int b = 0; b < HB; ++b) {
-                  const float* s = sv + 16 * b;
-                  uint64_t k, v;
-                  factors(c0 / 16 + b, k, v);
-                  float a[4];
-#pragma unroll
-                  for (int y = 0; y < 4; ++y) a[y] = fmax3(s[y], s[y + 4], s[y + 8]);
-                  const float top = fmax3(fmax3(a[0], s[12], a[1]), fmax3(s[13], a[2], s[14]), fmaxf(a[3], s[15]));
-                  m_tile = fmaxf(m_tile, fmaf(top, __uint_as_float(static_cast<uint32_t>(k)) * back,
-                                              __uint_as_float(static_cast<uint32_t>(v))));
-                }
+                for (int y = 0; y < 4; ++y) a[y] = fmax3(s[y], s[y + 4], s[y + 8]);
+                const float top = fmax3(fmax3(a[0], s[12], a[1]), fmax3(s[13], a[2], s[14]), fmaxf(a[3], s[15]));
+                m_tile = fmaxf(m_tile, fmaf(top, __uint_as_float(static_cast<uint32_t>(k)) * back,
+                                            __uint_as_float(static_cast<uint32_t>(v))));
               }
               // the reference moves only when the maximum grows by more than
               // 2^8 (as in the prompt forward): few tiles rescale O
@@ -788,28 +792,24 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS, CODES>::THREADS, WideCfg<D, 
               m_used = m_new;
               const uint64_t shift2 = splat2(kPOffset - (m_used == -INFINITY ? 0.f : m_used));
 #pragma unroll
-              for (int c0 = 0; c0 < KT; c0 += HALF) {
-                if (c0 > 0) load(c0);
+              for (int b = 0; b < C::BLOCKS; ++b) {
+                uint64_t k, v;
+                float take;
+                factors(b, k, v);
+                asm("ld.shared.f32 %0, [%1];" : "=f"(take) : "r"(takes + b * 4));
+                const uint64_t sc2 = mul2(k, back2), nm2 = add2(v, shift2);
+                uint32_t pk[8];
+                float s0 = 0.f, s1 = 0.f;
 #pragma unroll
-                for (int b = 0; b < HB; ++b) {
-                  uint64_t k, v;
-                  float take;
-                  factors(c0 / 16 + b, k, v);
-                  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(take) : "r"(takes + (c0 / 16 + b) * 4));
-                  const uint64_t sc2 = mul2(k, back2), nm2 = add2(v, shift2);
-                  uint32_t pk[8];
-                  float s0 = 0.f, s1 = 0.f;
-#pragma unroll
-                  for (int y = 0; y < 8; ++y) {
-                    float a0, a1;
-                    fma2_bc(a0, a1, sv[b * 16 + 2 * y], sv[b * 16 + 2 * y + 1], sc2, nm2);
-                    const float p0 = ex2(a0), p1 = ex2(a1);
-                    add2_acc(s0, s1, p0, p1);
-                    pk[y] = pack_f16(p0, p1);
-                  }
-                  sum4[b & 3] = fmaf(s0 + s1, take, sum4[b & 3]);
-                  tmem_st8(tSj + (c0 / 16 + b) * 8, pk);
+                for (int y = 0; y < 8; ++y) {
+                  float a0, a1;
+                  fma2_bc(a0, a1, sv[b * 16 + 2 * y], sv[b * 16 + 2 * y + 1], sc2, nm2);
+                  const float p0 = ex2(a0), p1 = ex2(a1);
+                  add2_acc(s0, s1, p0, p1);
+                  pk[y] = pack_f16(p0, p1);
                 }
+                sum4[b & 3] = fmaf(s0 + s1, take, sum4[b & 3]);
+                tmem_st8(tSj + b * 8, pk);
               }
             } else {
               float sv[KT];
@@ -856,8 +856,8 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS, CODES>::THREADS, WideCfg<D, 
             if (done > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
               // O holds the PVs of the earlier tiles; with two S buffers the
               // last one may still run
-              if (SLOTS == 1) {
-                ok = wait_all(W_PVTILE, (j - 1) & 1);
+              if (C::BUFS) {
+                ok = wait_all(pv_tile(slot), (j - 1) & 1);
                 tc_fence_after();
               }
 #pragma unroll 1
@@ -920,7 +920,7 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS, CODES>::THREADS, WideCfg<D, 
           tc_fence_before();
           // (a test of the wait limit withholds the first one of slot 0: its
           // MMA warp's wait then runs out)
-          if (!(P.withhold == 8 && slot == 0 && j == 0)) mbar_arrive_warp(bar(W_PFULL + buf));
+          if (!(P.withhold == 8 && slot == 0 && j == 0)) mbar_arrive_warp(bar(b_p));
           ++j;
           ++done;
         }
@@ -931,10 +931,10 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS, CODES>::THREADS, WideCfg<D, 
       }
 
       // ---------------------------------------------------------- the piece's end
-      const bool two = !w.rows && w.n > 1;             // O is in both slots
+      const bool two = !C::BUFS && !w.rows && w.n > 1; // O is in both slots
       int c0 = 0, c1 = D;                              // columns that this thread writes
       float m_out = m_used, l_out = l, f0 = 1.f, f1 = 0.f;
-      if (!w.rows) {
+      if (!C::BUFS && !w.rows) {
         ml[slot * 128 + r] = make_float2(m_used, l);
         slots_sync<SLOTS>();
         const float2 a = ml[r], b = two ? ml[128 + r] : make_float2(-INFINITY, 0.f);
