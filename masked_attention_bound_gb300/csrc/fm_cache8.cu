@@ -40,10 +40,9 @@ struct Side {
 // bits once, and the product with p wraps around like the angle does, exactly
 // (2^30 positions on, 2^-34 of a turn is left).  cos and sin come from their
 // Taylor series on an eighth of a turn to either side of a quarter's multiple,
-// each as a sum of two floats, the first of 16 bits: its product with a bf16
-// number is exact, so a rotated value has two roundings to 24 bits.
+// as sums of two floats (off by 2^-27), and are rounded to one float each.
 struct Turn {
-  float c1, c2, s1, s2;                  // cos = c1 + c2, sin = s1 + s2
+  float c, s;
 };
 
 __device__ __forceinline__ uint64_t turn_step(float f) {
@@ -79,24 +78,18 @@ __device__ __forceinline__ Turn turn_of(int64_t pos, uint64_t step) {
   const float p = th * m, pl = fmaf(th, m, -p);
   const float sh = th + p;
   const float sl = (th - sh) + p + pl + fmaf(th, ml + y, tl * fmaf(-0.5f, z, 1.f));
-  auto head = [](float v) { return __uint_as_float(__float_as_uint(v) & 0xffffff00u); };
-  float c1 = head(ch), s1 = head(sh);
-  float c2 = (ch - c1) + cl, s2 = (sh - s1) + sl;
+  float c = ch + cl, s = sh + sl;
   if (quarter & 1) {
-    const float t1 = c1, t2 = c2;
-    c1 = -s1; c2 = -s2;
-    s1 = t1; s2 = t2;
+    const float y = c;
+    c = -s;
+    s = y;
   }
-  if (quarter & 2) {
-    c1 = -c1; c2 = -c2;
-    s1 = -s1; s2 = -s2;
-  }
-  return Turn{c1, c2, s1, s2};
+  return quarter & 2 ? Turn{-c, -s} : Turn{c, s};
 }
 
 __device__ __forceinline__ void turn_pair(float& a, float& b, const Turn& t) {
-  const float x = fmaf(a, t.c1, fmaf(-b, t.s1, fmaf(a, t.c2, -b * t.s2)));
-  b = fmaf(a, t.s1, fmaf(b, t.c1, fmaf(a, t.s2, b * t.c2)));
+  const float x = fmaf(a, t.c, -b * t.s);
+  b = fmaf(b, t.c, a * t.s);
   a = x;
 }
 
@@ -104,13 +97,16 @@ __device__ __forceinline__ void turn_pair(float& a, float& b, const Turn& t) {
 // The unit of work is a block: 16 tokens of the cache that share a scale, all
 // heads.  Sequence b's blocks are numbered from cu[b] / 16 + 2 b on, which
 // leaves each sequence room enough wherever its first token lies in a block;
-// a thread block finds its sequence by a search over cu.  The angles' table is
-// made once for all heads.  With n new tokens in the block, n d / 16 threads
-// each take 16 elements (two vectors of 8) of a token, for one head after
-// another.
-//
-// Codes: a warp has a head's new tokens of the block in registers, so that the
-// largest value is known before any is rounded, and K and V are read once.
+// a thread block finds its sequence by a search over cu.  With n new tokens in
+// the block, a group of n d / 16 threads (rounded up to a power of two) holds a
+// head's new tokens, 16 elements (two vectors of 8) a thread, so that a block's
+// largest value is known before any is rounded and K and V are read once.  The
+// groups take the heads of q, K and V in turn, each with the next one's loads
+// under way; a thread has the same token and elements throughout, and so its
+// eight angles in registers.
+// Bound by HBM for prompts, by the latency of the lookups for single tokens.  (A
+// warp for all of a head's 16 tokens needed 159 registers: one thread block per
+// SM, 174 us for 16K tokens of 32 + 2 * 8 heads to codes.)
 constexpr int kRotThreads = 256;
 
 struct RotArgs {
@@ -127,10 +123,6 @@ struct RotArgs {
   int inter;
 };
 
-struct Vec2 {
-  uint4 a, b;
-};
-
 __device__ __forceinline__ void unpack8(const uint4& x, float* f) {
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
@@ -144,10 +136,11 @@ __device__ __forceinline__ uint4 pack8(const float* f) {
 }
 
 template <int D, bool CODES>
-__global__ void __launch_bounds__(kRotThreads)
+__global__ void __launch_bounds__(kRotThreads, 3)
     append_rotary_kernel(const __grid_constant__ RotArgs A) {
   constexpr int CH = D / 16;               // chunks of 16 elements of a head
-  __shared__ float4 turns[16][8][CH];      // [token][element of the chunk's eight angles][chunk]
+  __shared__ Turn turns[16][8][CH];        // [token][element of the chunk's eight angles][chunk]
+  __shared__ uint32_t tops[2][kRotThreads / 32];
   grid_launch_dependents();
   grid_dependency_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -184,145 +177,142 @@ __global__ void __launch_bounds__(kRotThreads)
   if (!in && tid == 0) flag(A.status, DEV_CACHE);
   const int slot0 = p0 & ((1 << A.page_shift) - 1);
 
+  // groups of threads: token i and chunk c of one head after another
+  int size_shift = CH == 8 ? 3 : 2;
+  while ((1 << size_shift) < n * CH) ++size_shift;
+  const int size = 1 << size_shift, group = tid >> size_shift, member = tid & (size - 1);
+  const int i = member / CH, c = member % CH;
+  const bool active = i < n;
+  const int nrot = A.nrot;
+  const bool inter = A.inter != 0, turned = c < nrot;
+  // the chunk's two vectors
+  const int va = 8 * (inter || !turned ? 2 * c : c), vb = inter || !turned ? va + 8 : va + 8 * nrot;
+  // this block's heads of K, V and q: K and V of head hk, then its G queries
+  const int nq = A.G, per = nq + 2;
+  const int y = blockIdx.y, ny = gridDim.y;
+  const int jobs = per * ((A.Hkv - y + ny - 1) / ny), step = kRotThreads >> size_shift;
+  struct Job {
+    int hk, x;               // K/V head; 0: K, 1: V, 2 + g: query head g of it
+  };
+  auto job = [&](int j) { return Job{y + j / per * ny, j % per}; };
+  auto load = [&](int j, uint4& a, uint4& b) {
+    const Job w = job(j);
+    const __nv_bfloat16* src = w.x < 2 ? A.kv[w.x].src + (t0 + i) * A.kv[w.x].tok + w.hk * A.kv[w.x].head
+                                       : A.q + (t0 + i) * A.q_stride[0] + (w.hk * nq + w.x - 2) * A.q_stride[1];
+    a = *reinterpret_cast<const uint4*>(src + va);
+    b = *reinterpret_cast<const uint4*>(src + vb);
+  };
+  uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a;
+  if (active && group < jobs) load(group, a, b);
+
   // the angles
-  if (A.nrot > 0) {
-    const int half = 8 * A.nrot, row = half <= 8 ? 8 : half <= 16 ? 16 : half <= 32 ? 32 : 64;
+  if (nrot > 0) {
+    const int half = 8 * nrot, row = half <= 8 ? 8 : half <= 16 ? 16 : half <= 32 ? 32 : 64;
     const int p = tid & (row - 1);
     if (p < half) {
       const float f = A.freqs[p];
       const float poison = f - f;          // NaN where f is not finite
-      const uint64_t step = turn_step(f);
-      for (int i = tid / row; i < n; i += kRotThreads / row) {
-        const Turn t = turn_of(A.positions ? A.positions[t0 + i] : p0 + i, step);
-        turns[i][p & 7][p >> 3] = make_float4(t.c1 + poison, t.c2, t.s1 + poison, t.s2);
+      const uint64_t turn = turn_step(f);
+      for (int k = tid / row; k < n; k += kRotThreads / row) {
+        const Turn w = turn_of(A.positions ? A.positions[t0 + k] : p0 + k, turn);
+        turns[k][p & 7][p >> 3] = Turn{w.c + poison, w.s + poison};
       }
     }
     __syncthreads();
   }
-
-  // the two vectors of chunk c, and its rotation
-  const int nrot = A.nrot;
-  const bool inter = A.inter != 0;
-  auto vec_a = [&](int c) { return inter ? 2 * c : c < nrot ? c : 2 * c; };
-  auto vec_b = [&](int c) { return inter ? 2 * c + 1 : c < nrot ? c + nrot : 2 * c + 1; };
-  auto turn_chunk = [&](float (&f)[16], int i, int c) {
-    if (c >= nrot) return;
+  Turn w[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float4 w = turns[i][e][c];
-      const Turn t{w.x, w.y, w.z, w.w};
-      if (inter) turn_pair(f[2 * e], f[2 * e + 1], t);
-      else turn_pair(f[e], f[8 + e], t);
-    }
-  };
+  for (int e = 0; e < 8; ++e) w[e] = active && turned ? turns[i][e][c] : Turn{0.f, 0.f};
 
-  // queries, and with a cache of bf16 K and V: heads [h0, h1) of this block
-  {
-    const int per = n * CH;
-    const int sub = tid / per, subs = kRotThreads / per;
-    const int w = tid - sub * per, i = w / CH, c = w % CH;
-    const int va = vec_a(c) * 8, vb = vec_b(c) * 8;
-    const int nq = A.G, heads = nq + (CODES ? 0 : 2);        // of one K/V head
-    if (sub < subs) {
-      const int jobs = heads * ((A.Hkv - static_cast<int>(blockIdx.y) + gridDim.y - 1) / gridDim.y);
-      for (int j = sub; j < jobs; j += subs) {
-        const int hk = blockIdx.y + j / heads * gridDim.y, x = j % heads;
-        const __nv_bfloat16* src;
-        __nv_bfloat16* dst;
-        bool rotates = true, writes = true;
-        if (x < nq) {
-          const int h = hk * nq + x;
-          src = A.q + (t0 + i) * A.q_stride[0] + h * A.q_stride[1];
-          dst = A.q_out + (t0 + i) * A.o_stride[0] + h * A.o_stride[1];
-        } else {
-          const Side& S = A.kv[x - nq];
-          rotates = x == nq;
-          writes = in;
-          src = S.src + (t0 + i) * S.tok + hk * S.head;
-          dst = static_cast<__nv_bfloat16*>(S.pool) + pg * S.page + (slot0 + i) * S.slot + hk * S.phead;
-        }
-        if (!writes) continue;
-        uint4 a = *reinterpret_cast<const uint4*>(src + va), b = *reinterpret_cast<const uint4*>(src + vb);
-        if (rotates && c < nrot) {
-          float f[16];
-          unpack8(a, f);
-          unpack8(b, f + 8);
-          turn_chunk(f, i, c);
-          a = pack8(f);
-          b = pack8(f + 8);
-        }
+  int which = 0;             // of tops: a group's threads are one barrier apart at most
+#pragma unroll 1
+  for (int j = group; j < jobs; j += step) {
+    uint4 a1 = a, b1 = b;
+    if (active && j + step < jobs) load(j + step, a1, b1);
+    const Job k = job(j);
+    float f[16];
+    const bool rotates = turned && k.x != 1;
+    if (rotates || (CODES && k.x < 2)) {
+      unpack8(a, f);
+      unpack8(b, f + 8);
+    }
+    if (rotates) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        if (inter) turn_pair(f[2 * e], f[2 * e + 1], w[e]);
+        else turn_pair(f[e], f[8 + e], w[e]);
+      }
+    }
+    if (!CODES || k.x >= 2) {
+      if (rotates) {
+        a = pack8(f);
+        b = pack8(f + 8);
+      }
+      __nv_bfloat16* dst =
+          k.x < 2 ? static_cast<__nv_bfloat16*>(A.kv[k.x].pool) + pg * A.kv[k.x].page + (slot0 + i) * A.kv[k.x].slot +
+                        k.hk * A.kv[k.x].phead
+                  : A.q_out + (t0 + i) * A.o_stride[0] + (k.hk * nq + k.x - 2) * A.o_stride[1];
+      if (active && (k.x >= 2 || in)) {
         *reinterpret_cast<uint4*>(dst + va) = a;
         *reinterpret_cast<uint4*>(dst + vb) = b;
       }
-    }
-  }
-
-  if constexpr (CODES) {
-    if (!in) return;
-    constexpr int ROWS = 32 / CH, PASSES = 16 / ROWS;        // tokens of a pass of the warp
-    const int r = lane / CH, c = lane % CH;
-    const int va = vec_a(c) * 8, vb = vec_b(c) * 8;
-    const int heads = (A.Hkv - static_cast<int>(blockIdx.y) + gridDim.y - 1) / gridDim.y;
-    for (int j = warp; j < 2 * heads; j += kRotThreads / 32) {
-      const int hk = blockIdx.y + (j >> 1) * gridDim.y;
-      const Side& S = A.kv[j & 1];
-      const bool rotates = (j & 1) == 0;
-      const __nv_bfloat16* src = S.src + (t0 + r) * S.tok + hk * S.head;
-      const int nb = 1 << (A.page_shift - kScaleShift);
-      float* sp = S.scale + (static_cast<int64_t>(pg) * A.Hkv + hk) * nb + (slot0 >> kScaleShift);
-      uint8_t* pool = static_cast<uint8_t*>(S.pool) + pg * S.page + hk * S.phead +
-                      static_cast<int64_t>(slot0 - first) * S.slot;      // the block's first token
-      Vec2 x[PASSES];
-#pragma unroll
-      for (int k = 0; k < PASSES; ++k)
-        if (k * ROWS + r < n) {
-          x[k].a = *reinterpret_cast<const uint4*>(src + k * ROWS * S.tok + va);
-          x[k].b = *reinterpret_cast<const uint4*>(src + k * ROWS * S.tok + vb);
-        }
-      const float raw = *sp;
-      float f[PASSES][16];
+    } else {
+      const Side& S = A.kv[k.x];
+      float* sp = S.scale + ((static_cast<int64_t>(pg) * A.Hkv + k.hk) << (A.page_shift - kScaleShift)) +
+                  (slot0 >> kScaleShift);
+      // (only where the block has tokens is its scale read)
+      const float raw = in && first > 0 ? *sp : 0.f;
       uint32_t top = 0;
+      if (active) {
 #pragma unroll
-      for (int k = 0; k < PASSES; ++k)
-        if (k * ROWS + r < n) {
-          unpack8(x[k].a, f[k]);
-          unpack8(x[k].b, f[k] + 8);
-          if (rotates) turn_chunk(f[k], k * ROWS + r, c);
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const uint32_t y = __float_as_uint(f[k][e]) & 0x7fffffffu;
-            top = max(top, y < 0x7f800000u ? y : 0u);        // the finite ones
-          }
+        for (int e = 0; e < 16; ++e) {
+          const uint32_t z = __float_as_uint(f[e]) & 0x7fffffffu;
+          top = max(top, z < 0x7f800000u ? z : 0u);          // the finite ones
         }
-      top = __reduce_max_sync(0xffffffffu, top);
+      }
+      // over the group
+      if (size >= 32) {
+        top = __reduce_max_sync(0xffffffffu, top);
+        if (size > 32) {
+          which ^= 1;
+          if (lane == 0) tops[which][warp] = top;
+          asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(size) : "memory");
+          const int w0 = group << (size_shift - 5);
+          for (int o = 0; o < size / 32; ++o) top = max(top, tops[which][w0 + o]);
+        }
+      } else {
+        const unsigned peers = ((1u << size) - 1u) << (lane & ~(size - 1));
+        for (int o = 1; o < size; o <<= 1) top = max(top, __shfl_xor_sync(peers, top, o));
+      }
       float s = scale_for(__uint_as_float(top));
+      uint8_t* pool = static_cast<uint8_t*>(S.pool) + pg * S.page + k.hk * S.phead +
+                      static_cast<int64_t>(slot0 - first) * S.slot;      // the block's first token
       if (first > 0) {
-        // tokens of the block keep their values: all 16 places, the new
-        // ones are written below
+        // tokens of the block keep their values: all 16 places but the new
+        // ones, which are written below
         const float old = clamp_scale(raw);
         s = fmaxf(s, old);
-        if (s > old) {
-          for (int row = r; row < kScaleBlock; row += ROWS) {
+        if (in && s > old) {
+          for (int row = i; row < kScaleBlock; row += size / CH) {
             uint4* at16 = reinterpret_cast<uint4*>(pool + row * S.slot + c * 16);
             if (row < first || row >= first + n) *at16 = rescale_e4m3x16(*at16, old / s);
           }
         }
       }
-      if (lane == 0 && s != raw) *sp = s;
-      const float inv = 1.f / s;           // exact: a power of two, or the caller's own
+      if (in && active) {
+        if (member == 0) *sp = s;
+        const float inv = 1.f / s;         // exact: a power of two, or the caller's own
+        uint8_t* dst = pool + (first + i) * S.slot;
 #pragma unroll
-      for (int k = 0; k < PASSES; ++k)
-        if (k * ROWS + r < n) {
-          float* g = f[k];
-          uint8_t* dst = pool + (first + k * ROWS + r) * S.slot;
-#pragma unroll
-          for (int e = 0; e < 16; ++e) g[e] *= inv;
-          *reinterpret_cast<uint2*>(dst + va) =
-              make_uint2(pack_e4m3x4(g[0], g[1], g[2], g[3]), pack_e4m3x4(g[4], g[5], g[6], g[7]));
-          *reinterpret_cast<uint2*>(dst + vb) =
-              make_uint2(pack_e4m3x4(g[8], g[9], g[10], g[11]), pack_e4m3x4(g[12], g[13], g[14], g[15]));
-        }
+        for (int e = 0; e < 16; ++e) f[e] *= inv;
+        *reinterpret_cast<uint2*>(dst + va) =
+            make_uint2(pack_e4m3x4(f[0], f[1], f[2], f[3]), pack_e4m3x4(f[4], f[5], f[6], f[7]));
+        *reinterpret_cast<uint2*>(dst + vb) =
+            make_uint2(pack_e4m3x4(f[8], f[9], f[10], f[11]), pack_e4m3x4(f[12], f[13], f[14], f[15]));
+      }
     }
+    a = a1;
+    b = b1;
   }
 }
 
