@@ -136,7 +136,7 @@ __device__ __forceinline__ uint4 pack8(const float* f) {
 }
 
 template <int D, bool CODES>
-__global__ void __launch_bounds__(kRotThreads, 3)
+__global__ void __launch_bounds__(kRotThreads, CODES ? 3 : 4)
     append_rotary_kernel(const __grid_constant__ RotArgs A) {
   constexpr int CH = D / 16;               // chunks of 16 elements of a head
   __shared__ Turn turns[16][8][CH];        // [token][element of the chunk's eight angles][chunk]
@@ -190,20 +190,38 @@ __global__ void __launch_bounds__(kRotThreads, 3)
   // this block's heads of K, V and q: K and V of head hk, then its G queries
   const int nq = A.G, per = nq + 2;
   const int y = blockIdx.y, ny = gridDim.y;
-  const int jobs = per * ((A.Hkv - y + ny - 1) / ny), step = kRotThreads >> size_shift;
+  const int step = kRotThreads >> size_shift;
   struct Job {
     int hk, x;               // K/V head; 0: K, 1: V, 2 + g: query head g of it
   };
-  auto job = [&](int j) { return Job{y + j / per * ny, j % per}; };
-  auto load = [&](int j, uint4& a, uint4& b) {
-    const Job w = job(j);
-    const __nv_bfloat16* src = w.x < 2 ? A.kv[w.x].src + (t0 + i) * A.kv[w.x].tok + w.hk * A.kv[w.x].head
-                                       : A.q + (t0 + i) * A.q_stride[0] + (w.hk * nq + w.x - 2) * A.q_stride[1];
+  const int step_hk = step / per * ny, step_x = step % per;
+  auto next = [&](Job k) {
+    k.hk += step_hk;
+    k.x += step_x;
+    if (k.x >= per) {
+      k.x -= per;
+      k.hk += ny;
+    }
+    return k;
+  };
+  const Job j0{y + group / per * ny, group % per};
+  auto load = [&](Job k, uint4& a, uint4& b) {
+    if (!active || k.hk >= A.Hkv) return;
+    const __nv_bfloat16* src = k.x < 2 ? A.kv[k.x].src + (t0 + i) * A.kv[k.x].tok + k.hk * A.kv[k.x].head
+                                       : A.q + (t0 + i) * A.q_stride[0] + (k.hk * nq + k.x - 2) * A.q_stride[1];
     a = *reinterpret_cast<const uint4*>(src + va);
     b = *reinterpret_cast<const uint4*>(src + vb);
   };
-  uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a;
-  if (active && group < jobs) load(group, a, b);
+  // the next AHEAD heads' elements
+  constexpr int AHEAD = CODES ? 1 : 2;
+  uint4 a[AHEAD + 1], b[AHEAD + 1];
+  Job ahead = j0;
+#pragma unroll
+  for (int k = 0; k < AHEAD; ++k) {
+    a[k] = b[k] = make_uint4(0u, 0u, 0u, 0u);
+    load(ahead, a[k], b[k]);
+    ahead = next(ahead);
+  }
 
   // the angles
   if (nrot > 0) {
@@ -226,15 +244,13 @@ __global__ void __launch_bounds__(kRotThreads, 3)
 
   int which = 0;             // of tops: a group's threads are one barrier apart at most
 #pragma unroll 1
-  for (int j = group; j < jobs; j += step) {
-    uint4 a1 = a, b1 = b;
-    if (active && j + step < jobs) load(j + step, a1, b1);
-    const Job k = job(j);
+  for (Job k = j0; k.hk < A.Hkv; k = next(k), ahead = next(ahead)) {
+    load(ahead, a[AHEAD], b[AHEAD]);
     float f[16];
     const bool rotates = turned && k.x != 1;
     if (rotates || (CODES && k.x < 2)) {
-      unpack8(a, f);
-      unpack8(b, f + 8);
+      unpack8(a[0], f);
+      unpack8(b[0], f + 8);
     }
     if (rotates) {
 #pragma unroll
@@ -245,16 +261,16 @@ __global__ void __launch_bounds__(kRotThreads, 3)
     }
     if (!CODES || k.x >= 2) {
       if (rotates) {
-        a = pack8(f);
-        b = pack8(f + 8);
+        a[0] = pack8(f);
+        b[0] = pack8(f + 8);
       }
       __nv_bfloat16* dst =
           k.x < 2 ? static_cast<__nv_bfloat16*>(A.kv[k.x].pool) + pg * A.kv[k.x].page + (slot0 + i) * A.kv[k.x].slot +
                         k.hk * A.kv[k.x].phead
                   : A.q_out + (t0 + i) * A.o_stride[0] + (k.hk * nq + k.x - 2) * A.o_stride[1];
       if (active && (k.x >= 2 || in)) {
-        *reinterpret_cast<uint4*>(dst + va) = a;
-        *reinterpret_cast<uint4*>(dst + vb) = b;
+        *reinterpret_cast<uint4*>(dst + va) = a[0];
+        *reinterpret_cast<uint4*>(dst + vb) = b[0];
       }
     } else {
       const Side& S = A.kv[k.x];
@@ -311,13 +327,16 @@ __global__ void __launch_bounds__(kRotThreads, 3)
             make_uint2(pack_e4m3x4(f[8], f[9], f[10], f[11]), pack_e4m3x4(f[12], f[13], f[14], f[15]));
       }
     }
-    a = a1;
-    b = b1;
+#pragma unroll
+    for (int x = 0; x < AHEAD; ++x) {
+      a[x] = a[x + 1];
+      b[x] = b[x + 1];
+    }
   }
 }
 
 // ------------------------------------------------------------------ accept
-// A warp keeps the accepted nodes of one sequence, layer and head, K or V: it
+// A warp keeps the accepted nodes of one sequence, head and run of layers, K or V: it
 // walks the blocks that they go to in ascending order.  Into a block D go
 // at most 16 tokens, from D itself or from later blocks; all are loaded before
 // one is stored, so a block may be overwritten once it has been done.  D's new
@@ -335,16 +354,18 @@ struct Accept8Args {
   int32_t *lens_out, *ref;
   int* status;
   int max_accept, max_pages, n_pages, page_shift, Hkv;
+  int layers, per_block;       // layers of a thread block
 };
 
 template <int D>
-__global__ void __launch_bounds__(kAccept8Warps * 32)
+__global__ void __launch_bounds__(kAccept8Warps * 32, 8)
     accept8_kernel(const __grid_constant__ Accept8Args A) {
   __shared__ int place[32];            // by place within two blocks: source (page << 8 | slot), -1: none
+  __shared__ int dest[2];              // the two blocks' own first tokens
   __shared__ int good;
   grid_launch_dependents();
   grid_dependency_wait();
-  const int b = blockIdx.y, layer = blockIdx.z, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int b = blockIdx.y, layer0 = blockIdx.z * A.per_block, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int32_t* acc = A.accept + static_cast<int64_t>(b) * A.max_accept;
   const int32_t* row = A.table + static_cast<int64_t>(b) * A.max_pages;
   const int m = A.n_accept[b], page = 1 << A.page_shift;
@@ -371,7 +392,10 @@ __global__ void __launch_bounds__(kAccept8Warps * 32)
     for (int i = lane; sized && i < m; i += 32) {
       const int from = look(i);
       ok = from >= 0 && ok;
-      if (skew + i < 32) place[skew + i] = from;
+      if (skew + i < 32) {
+        place[skew + i] = from;
+        if (i == 0 || skew + i == 16) dest[(skew + i) >> 4] = at(base + i) & ~(kScaleBlock - 1);
+      }
     }
     // the pages past the new length, as in the accept of a bf16 cache
     if (sized && A.ref)
@@ -381,7 +405,7 @@ __global__ void __launch_bounds__(kAccept8Warps * 32)
   }
   __syncthreads();
   const bool ok = good != 0;
-  if (blockIdx.x == 0 && layer == 0) {
+  if (blockIdx.x == 0 && layer0 == 0) {
     if (threadIdx.x == 0) {
       A.lens_out[b] = ok ? base + m : A.lens[b];
       if (!ok) flag(A.status, DEV_CACHE);
@@ -393,50 +417,60 @@ __global__ void __launch_bounds__(kAccept8Warps * 32)
   const int unit = blockIdx.x * kAccept8Warps + warp, hk = unit >> 1;
   const Side& S = A.kv[unit & 1];
   const bool mine = hk < A.Hkv;
-  uint8_t* pool = static_cast<uint8_t*>(S.pool) + layer * A.layer[unit & 1] + hk * S.phead;
-  float* scales = S.scale + layer * A.scale_layer;
   const int nb_shift = A.page_shift - kScaleShift;
-  auto scale_at = [&](int where) -> float* {
-    return scales + (((static_cast<int64_t>(where >> 8) * A.Hkv + hk) << nb_shift) + ((where & 255) >> kScaleShift));
-  };
-  auto codes_at = [&](int where) -> uint8_t* {
-    return pool + (where >> 8) * S.page + static_cast<int64_t>(where & 255) * S.slot;
-  };
   constexpr int LPR = D / 16, ROWS = 32 / LPR, PASSES = 16 / ROWS;
   const int r = lane / LPR, c = lane % LPR;
+  const int layer1 = min(layer0 + A.per_block, A.layers);
   for (int d0 = 0; d0 < skew + m; d0 += kScaleBlock) {       // destination blocks
     if (d0 >= 32 && (d0 & 31) == 0) {                        // the next two blocks' places
       __syncthreads();
-      if (threadIdx.x < 32) place[lane] = d0 + lane < skew + m ? look(d0 + lane - skew) : -1;
+      if (threadIdx.x < 32) {
+        const int i = d0 + lane - skew;
+        place[lane] = i < m ? look(i) : -1;
+        if ((lane & 15) == 0 && i < m) dest[lane >> 4] = at(base + i);
+      }
       __syncthreads();
     }
     if (!mine) continue;
     const int* from = place + (d0 & 31);
-    const int to = at(base - skew + d0);                     // its first token
-    // scales: lane t < 16 of token t's source, lane 16 the block's own
+    const int to = dest[(d0 >> 4) & 1];
     const int src = lane < 16 ? from[lane] : -1;
-    const float own_raw = *scale_at(to), old = clamp_scale(own_raw);
-    const float mine_s = src >= 0 ? clamp_scale(*scale_at(src)) : old;
-    const float s = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(mine_s, old))));
-    uint4 x[PASSES];
-    bool write[PASSES];
+#pragma unroll 1
+    for (int layer = layer0; layer < layer1; ++layer) {
+      float* scales = S.scale + layer * A.scale_layer;
+      auto scale_at = [&](int where) -> float* {
+        return scales + (((static_cast<int64_t>(where >> 8) * A.Hkv + hk) << nb_shift) + ((where & 255) >> kScaleShift));
+      };
+      uint8_t* pool = static_cast<uint8_t*>(S.pool) + layer * A.layer[unit & 1] + hk * S.phead + c * 16;
+      auto codes_at = [&](int where) -> uint4* {
+        return reinterpret_cast<uint4*>(pool + (where >> 8) * S.page + static_cast<int64_t>(where & 255) * S.slot);
+      };
+      // the codes that move, and at the same time the scales: lane t < 16 that of
+      // token t's source, the others the block's own
+      uint4 x[PASSES];
 #pragma unroll
-    for (int k = 0; k < PASSES; ++k) {
-      const int t = k * ROWS + r;
-      const int w = from[t], here = to + t, f = w >= 0 ? w : here;
-      const float have = __shfl_sync(0xffffffffu, mine_s, t);
-      write[k] = f != here || have != s;
-      if (write[k]) {
-        x[k] = *reinterpret_cast<const uint4*>(codes_at(f) + c * 16);
-        if (have != s) x[k] = rescale_e4m3x16(x[k], have / s);
+      for (int k = 0; k < PASSES; ++k) {
+        const int t = k * ROWS + r, w = from[t];
+        if (w >= 0 && w != to + t) x[k] = *codes_at(w);
       }
-    }
-    __syncwarp();                                            // all loads before the stores
+      const float own_raw = *scale_at(to), old = clamp_scale(own_raw);
+      const float mine_s = src >= 0 ? clamp_scale(*scale_at(src)) : old;
+      const float s = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(mine_s, old))));
+      __syncwarp();                                          // all loads before the stores
 #pragma unroll
-    for (int k = 0; k < PASSES; ++k)
-      if (write[k]) *reinterpret_cast<uint4*>(codes_at(to + k * ROWS + r) + c * 16) = x[k];
-    if (lane == 0 && s != own_raw) *scale_at(to) = s;
-    __syncwarp();
+      for (int k = 0; k < PASSES; ++k) {
+        const int t = k * ROWS + r, w = from[t];
+        const float have = __shfl_sync(0xffffffffu, mine_s, t);
+        const bool moves = w >= 0 && w != to + t;
+        if (!moves && have == s) continue;
+        uint4* here = codes_at(to + t);
+        uint4 y = moves ? x[k] : *here;
+        if (have != s) y = rescale_e4m3x16(y, have / s);
+        *here = y;
+      }
+      if (lane == 0 && s != own_raw) *scale_at(to) = s;
+      __syncwarp();
+    }
   }
 }
 
@@ -552,8 +586,16 @@ fm_status fm_cache_accept_fp8(const fm_cache* c, const int32_t* accept, int max_
   A.max_accept = max_accept; A.max_pages = c->max_pages; A.n_pages = c->n_pages;
   A.page_shift = page_shift(c->page_size);
   A.Hkv = c->Hkv;
+  A.layers = c->layers;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const dim3 grid(ceil_div(2 * c->Hkv, kAccept8Warps), c->B, c->layers);
+  // as many layers a thread block, whose lookups are the same for all, as leave
+  // some two rounds of them (64 trees of 8 accepted nodes in 16 layers of 8 heads:
+  // 9.3 us so, 9.7 us by a layer each, 14.5 us by eight.  Most of that is blocks
+  // whose scale grows and which are written again, 4 KB of traffic each.)
+  const int x = ceil_div(2 * c->Hkv, kAccept8Warps);
+  const int64_t blocks = static_cast<int64_t>(x) * c->B * c->layers, round = 16ll * num_sms();
+  A.per_block = static_cast<int>((blocks + round - 1) / round < c->layers ? (blocks + round - 1) / round : c->layers);
+  const dim3 grid(x, c->B, ceil_div(c->layers, A.per_block));
   prof_begin(K_CACHE_ACCEPT, s);
   const cudaError_t e = c->d == 64 ? launch_dependent(accept8_kernel<64>, grid, kAccept8Warps * 32, 0, s, A)
                                    : launch_dependent(accept8_kernel<128>, grid, kAccept8Warps * 32, 0, s, A);
