@@ -82,7 +82,7 @@ __global__ void __launch_bounds__(NarrowCfg<D>::THREADS, 2)
   auto full = [&](int i) { return bar0 + 8u * i; };                      // K stages, then V's
   auto empty = [&](int i) { return bar0 + 8u * (C::KS + C::VS + i); };
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (warp == 2) touch_memory<D>(P, lane);
+  if (warp == 2) touch_memory<D>(P, lane, blockIdx.x);
   if (tid == 0) {
     for (int i = 0; i < C::KS + C::VS; ++i) {
       mbar_init(full(i), 1);
@@ -98,7 +98,7 @@ __global__ void __launch_bounds__(NarrowCfg<D>::THREADS, 2)
   }
   grid_launch_dependents();
   grid_dependency_wait();
-  TreeWalk<typename C::Geo> u(tree_run<typename C::Geo>(P));
+  TreeWalk<typename C::Geo> u(tree_run<typename C::Geo>(P, blockIdx.x));
   __syncthreads();
 
   // every lane gets the same answer
@@ -426,7 +426,7 @@ __global__ void __launch_bounds__(NarrowCfg<D>::THREADS, 2)
           }
         }
       }
-      if (tid == 0) leave_record(P, u);
+      if (tid == 0) leave_record(P, u, blockIdx.x);
       named_sync(1, 32 * C::WARPS);     // ml, merge, seen and nf have been read
     }
   }

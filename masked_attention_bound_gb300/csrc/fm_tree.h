@@ -72,18 +72,22 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeParams& P, int b) {
   return s;
 }
 
-// Geometry of the three kernels: rows of a unit, keys of a tile, a unit's
-// fixed cost in tiles, and the shortest run of a block in tiles (a part of
-// 128 rows is as many bytes as two 64-key tiles, written and read again).
+// Geometry of the kernels: rows of a unit, keys of a tile, a unit's fixed cost
+// in tiles, and the shortest run of a block in tiles (a part of 128 rows is as
+// many bytes as two 64-key tiles, written and read again).  HEADS_FIRST: the
+// order of the units on the line, heads outside of sequences.
 struct NarrowGeo {
+  static constexpr bool HEADS_FIRST = false;
   static constexpr int R = 16, KT = 64, LEAST = 2;
   __device__ static __forceinline__ int end(int) { return 2; }
 };
 struct MidGeo {
+  static constexpr bool HEADS_FIRST = false;
   static constexpr int R = 128, KT = 64, LEAST = 4;
   __device__ static __forceinline__ int end(int) { return 8; }
 };
 struct WideGeo {
+  static constexpr bool HEADS_FIRST = false;
   static constexpr int R = 256, KT = 128, LEAST = 2;
   // a block with a unit's end in its run took 12000 (256 rows) to 20000
   // cycles (128 rows) longer, where a tile takes 3100 and 2800; with Q by TMA
@@ -92,6 +96,7 @@ struct WideGeo {
 };
 
 struct Wide8Geo {
+  static constexpr bool HEADS_FIRST = false;
   static constexpr int R = 256, KT = 64, LEAST = 4;
   __device__ static __forceinline__ int end(int) { return 10; }
 };
@@ -133,8 +138,8 @@ __device__ __forceinline__ uint32_t seq_length(const TreeParams& P, const TreeSe
 // places in the workspace are touched at once, while the block sets up.
 __device__ __forceinline__ void touch(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 template <int D>
-__device__ __forceinline__ void touch_memory(const TreeParams& P, int lane) {
-  const int64_t part = 2 * static_cast<int64_t>(blockIdx.x) * P.part_rows;
+__device__ __forceinline__ void touch_memory(const TreeParams& P, int lane, int block) {
+  const int64_t part = 2 * static_cast<int64_t>(block) * P.part_rows;
   if (lane == 0) touch(P.lens);
   if (lane == 1) touch(P.cu);
   if (lane == 2) touch(P.table);
@@ -158,7 +163,7 @@ struct TreeRun {
 // over the lanes, and the lane whose sequences hold the run's start looks for
 // it among them.
 template <class Geo>
-__device__ __forceinline__ TreeRun tree_run(const TreeParams& P) {
+__device__ __forceinline__ TreeRun tree_run(const TreeParams& P, int block) {
   constexpr unsigned ALL = 0xffffffffu;
   const int lane = threadIdx.x & 31;
   const int m = (P.B + 31) >> 5;
@@ -168,8 +173,8 @@ __device__ __forceinline__ TreeRun tree_run(const TreeParams& P) {
 #pragma unroll 1
   for (int b = b0; b < b1; ++b) {
     s = tree_seq(P, b);
-    if (s.base < 0 && blockIdx.x == 0 && P.status) atomicOr(P.status, DEV_CACHE);
-    w += seq_length<Geo>(P, s) * P.Hkv;
+    if (s.base < 0 && block == 0 && P.status) atomicOr(P.status, DEV_CACHE);
+    w += seq_length<Geo>(P, s) * (Geo::HEADS_FIRST ? 1 : P.Hkv);
   }
   uint32_t inc = w;
 #pragma unroll
@@ -177,17 +182,22 @@ __device__ __forceinline__ TreeRun tree_run(const TreeParams& P) {
     const uint32_t y = __shfl_up_sync(ALL, inc, o);
     if (lane >= o) inc += y;
   }
-  const uint32_t all = __shfl_sync(ALL, inc, 31);
+  const uint32_t once = __shfl_sync(ALL, inc, 31);           // HEADS_FIRST: of one head
+  const uint32_t all = Geo::HEADS_FIRST ? once * P.Hkv : once;
   TreeRun run{0, 0, 0, 0, 0, s};
-  const uint32_t me = blockIdx.x, grid = gridDim.x, least = P.whole ? 1 : Geo::LEAST;
+  const uint32_t me = block, grid = gridDim.x, least = P.whole ? 1 : Geo::LEAST;
   uint32_t each = P.by_grid(all), more = all - each * grid;   // the first blocks take one more
   if (each < least) {                  // on a short line the last blocks have nothing
     each = least;
     more = 0;
   }
-  const uint32_t begin = each * me + min(me, more);
+  uint32_t begin = each * me + min(me, more);
   if (begin >= all) return run;
   run.left = min(each + (me < more), all - begin);
+  if (Geo::HEADS_FIRST) {
+    run.hk = begin / once;
+    begin -= run.hk * once;
+  }
   const unsigned owner = __ballot_sync(ALL, inc > begin);
   const int from = __ffs(owner) - 1;
   if (lane == from) {
@@ -197,12 +207,15 @@ __device__ __forceinline__ TreeRun tree_run(const TreeParams& P) {
     for (;; ++b) {
       if (m > 1) s = tree_seq(P, b);
       per = seq_length<Geo>(P, s);
-      if (off < per * P.Hkv) break;
-      off -= per * P.Hkv;
+      const uint32_t span = Geo::HEADS_FIRST ? per : per * P.Hkv;
+      if (off < span) break;
+      off -= span;
     }
     run.b = b;
-    run.hk = off / per;
-    off -= run.hk * per;
+    if (!Geo::HEADS_FIRST) {
+      run.hk = off / per;
+      off -= run.hk * per;
+    }
 #pragma unroll 1
     while (true) {
       const uint32_t t = unit_length<Geo>(P, s, run.rt, key_tiles<Geo>(unit_keys<Geo>(P, s, run.rt)));
@@ -255,11 +268,22 @@ struct TreeWalk : TreePiece {
         next_tile = 0;
         if (++rt >= row_tiles<Geo>(P, s)) {
           rt = 0;
-          ++hk;
+          if (Geo::HEADS_FIRST) s.n = 0;         // on to the next sequence
+          else ++hk;
         }
       }
       // on to the next sequence with rows
-      if (hk >= P.Hkv || s.n <= 0) {
+      if (Geo::HEADS_FIRST) {
+        if (s.n <= 0) {
+          rt = next_tile = 0;
+          if (++b >= P.B) {
+            b = 0;
+            if (++hk >= P.Hkv) return false;
+          }
+          s = tree_seq(P, b);
+          continue;
+        }
+      } else if (hk >= P.Hkv || s.n <= 0) {
         hk = rt = next_tile = 0;
         if (++b >= P.B) return false;
         s = tree_seq(P, b);
@@ -283,9 +307,9 @@ struct TreeWalk : TreePiece {
 
 // A piece's share of the block's record (its first thread's; the block starts
 // with {-1, 0, 0, 0}).
-__device__ __forceinline__ void leave_record(const TreeParams& P, const TreePiece& u) {
+__device__ __forceinline__ void leave_record(const TreeParams& P, const TreePiece& u, int block) {
   if (u.whole()) return;
-  int* rec = reinterpret_cast<int*>(P.rec + blockIdx.x);
+  int* rec = reinterpret_cast<int*>(P.rec + block);
   if (u.t0 == 0) {
     rec[0] = u.b;
     rec[1] = u.hk;

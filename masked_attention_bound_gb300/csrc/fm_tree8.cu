@@ -20,7 +20,12 @@
 
 namespace fm {
 
+// HEADS_FIRST: with the blocks numbered as below, the heads of a sequence are
+// read at about the same time.  A token's codes of a head are 128 bytes (64),
+// and the next heads' follow: fetched alone, 128 at a time, they came at 5.8
+// TB/s.
 struct Narrow8Geo {
+  static constexpr bool HEADS_FIRST = true;
   static constexpr int R = 16, KT = 128, LEAST = 2;
   __device__ static __forceinline__ int end(int) { return 2; }
 };
@@ -99,7 +104,13 @@ __global__ void __launch_bounds__(Narrow8Cfg<D, NT>::THREADS, 2)
   auto full = [&](int i) { return bar0 + 8u * i; };                      // K stages, then V's
   auto empty = [&](int i) { return bar0 + 8u * (C::KS + C::VS + i); };
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (warp == 2) touch_memory<D>(P, lane);
+  // Blocks next to each other have one head each of the same stretch: the line
+  // is cut into as many runs as blocks, and block x has run x / Hkv of head x %
+  // Hkv (where the heads divide the blocks).
+  int block = blockIdx.x;
+  if (P.Hkv > 1 && gridDim.x % P.Hkv == 0)
+    block = blockIdx.x % P.Hkv * (gridDim.x / P.Hkv) + blockIdx.x / P.Hkv;
+  if (warp == 2) touch_memory<D>(P, lane, block);
   if (tid == 0) {
     for (int i = 0; i < C::KS + C::VS; ++i) {
       mbar_init(full(i), Load::ARRIVALS);
@@ -115,7 +126,7 @@ __global__ void __launch_bounds__(Narrow8Cfg<D, NT>::THREADS, 2)
   }
   grid_launch_dependents();
   grid_dependency_wait();
-  TreeWalk<typename C::Geo> u(tree_run<typename C::Geo>(P));
+  TreeWalk<typename C::Geo> u(tree_run<typename C::Geo>(P, block));
   __syncthreads();
 
   // every lane gets the same answer
@@ -175,7 +186,7 @@ __global__ void __launch_bounds__(Narrow8Cfg<D, NT>::THREADS, 2)
     const float* scale_ring = reinterpret_cast<const float*>(smem + C::OFF_SCALE);
     uint32_t pieces = 0;
     int par_of = -1;                             // the sequence whose parents are in shared memory
-    if (tid == 0) P.rec[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    if (tid == 0) P.rec[block] = make_int4(-1, 0, 0, 0);
     for (; u.next(P); ++pieces) {
       // tiles from this one on hold keys that not every row sees
       const int part0 = u.origin / KT;
@@ -255,53 +266,67 @@ __global__ void __launch_bounds__(Narrow8Cfg<D, NT>::THREADS, 2)
         const uint32_t kp = (e / C::KS) & 1, vp = (e / C::VS) & 1;
         ++e;
         const uint32_t sk = sbase + ks * C::TILE, sv = sbase + C::OFF_V + vs * C::TILE;
-        // this warp's blocks: warp and warp + 4 of the tile
-        const int left = u.keys - t * KT - warp * 16;
-        const int nblk = left <= 0 ? 0 : left <= 64 ? 1 : 2;
+        // This warp's blocks: warp and warp + 4 of the tile, both always (what is
+        // past the unit's keys is masked, in its last tile only): without
+        // branches between them their loads and products overlap.
         if (ok) ok = wait_all(full(ks), kp);
         float s[2][NT][4];
         float fk[2];
         if (ok) {
+          // two accumulators a block and row group: a product waits for the one
+          // before into the same
+          float s2[2][NT][4];
+          uint4 ka[2][D / 64], kb[2][D / 64];
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            if (x >= nblk) break;
             const int r0 = (warp + 4 * x) * 16 + g;
             fk[x] = scale_ring[ks * C::BLOCKS + warp + 4 * x];
 #pragma unroll
+            for (int w = 0; w < D / 64; ++w) {
+              ka[x][w] = lds128(sk + Load::word16(r0, tq * (D / 64) + w));
+              kb[x][w] = lds128(sk + Load::word16(r0 + 8, tq * (D / 64) + w));
+            }
+#pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-              for (int y = 0; y < 4; ++y) s[x][nt][y] = 0.f;
-#pragma unroll
-            for (int w = 0; w < D / 64; ++w) {
-              const uint4 a = lds128(sk + Load::word16(r0, tq * (D / 64) + w));
-              const uint4 b = lds128(sk + Load::word16(r0 + 8, tq * (D / 64) + w));
-              const uint32_t wa[4] = {a.x, a.y, a.z, a.w}, wb[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const uint32_t f[4] = {f16x2_of_e4m3x2(wa[i]), f16x2_of_e4m3x2(wb[i]), f16x2_of_e4m3x2(wa[i] >> 16),
-                                       f16x2_of_e4m3x2(wb[i] >> 16)};
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) mma_f16(s[x][nt], f, qf[nt][4 * w + i][0], qf[nt][4 * w + i][1]);
-              }
-            }
+              for (int y = 0; y < 4; ++y) s[x][nt][y] = s2[x][nt][y] = 0.f;
           }
+#pragma unroll
+          for (int w = 0; w < D / 64; ++w)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {
+                const uint4 &a = ka[x][w], &b = kb[x][w];
+                const uint32_t wa = i == 0 ? a.x : i == 1 ? a.y : i == 2 ? a.z : a.w;
+                const uint32_t wb = i == 0 ? b.x : i == 1 ? b.y : i == 2 ? b.z : b.w;
+                const uint32_t f[4] = {f16x2_of_e4m3x2(wa), f16x2_of_e4m3x2(wb), f16x2_of_e4m3x2(wa >> 16),
+                                       f16x2_of_e4m3x2(wb >> 16)};
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+                  mma_f16(i & 1 ? s2[x][nt] : s[x][nt], f, qf[nt][4 * w + i][0], qf[nt][4 * w + i][1]);
+              }
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int y = 0; y < 4; ++y) s[x][nt][y] += s2[x][nt][y];
         }
         // (a test of the wait limit withholds the first one: the K loader's
         // wait for the stage then runs out)
         if (!(P.withhold == 8 && e == 1)) mbar_arrive_warp(empty(ks));
         if (ok) ok = wait_all(full(C::KS + vs), vp);
         uint32_t pf[2][NT][2];
-        if (ok && nblk > 0) {
+        if (ok) {
           float4 f[2];
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            if (x >= nblk) break;
             f[x] = block_factors(fk[x], scale_ring[(C::KS + vs) * C::BLOCKS + warp + 4 * x]);
           }
           // z = x + log2 sv, in place
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            if (x >= nblk) break;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -312,8 +337,7 @@ __global__ void __launch_bounds__(Narrow8Cfg<D, NT>::THREADS, 2)
             // keys past origin: only what the row sees
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-              if (x >= nblk) break;
-              const int key0 = t * KT + (warp + 4 * x) * 16 + g;
+                const int key0 = t * KT + (warp + 4 * x) * 16 + g;
 #pragma unroll
               for (int y = 0; y < 4; ++y) {
                 const int key = key0 + 8 * (y >> 1), j = key - u.origin;
@@ -332,8 +356,7 @@ __global__ void __launch_bounds__(Narrow8Cfg<D, NT>::THREADS, 2)
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
-              float mx = fmaxf(s[0][nt][y], s[0][nt][y + 2]);
-              if (nblk > 1) mx = fmaxf(mx, fmaxf(s[1][nt][y], s[1][nt][y + 2]));
+              float mx = fmaxf(fmaxf(s[0][nt][y], s[0][nt][y + 2]), fmaxf(s[1][nt][y], s[1][nt][y + 2]));
               mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
               mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
               mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
@@ -358,7 +381,6 @@ __global__ void __launch_bounds__(Narrow8Cfg<D, NT>::THREADS, 2)
           }
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            if (x >= nblk) break;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               float p[4];
@@ -374,7 +396,7 @@ __global__ void __launch_bounds__(Narrow8Cfg<D, NT>::THREADS, 2)
             // this warp's rows of V: zeros past the unit's keys, and clean
             // where not every row sees the key
 #pragma unroll 1
-            for (int x = 0; x < nblk; ++x) {
+            for (int x = 0; x < 2; ++x) {
               const int row = (warp + 4 * x) * 16 + (lane >> 1);
               const int key = t * KT + row, j = key - u.origin;
               auto word = [&](int c) {
@@ -407,7 +429,6 @@ __global__ void __launch_bounds__(Narrow8Cfg<D, NT>::THREADS, 2)
           }
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            if (x >= nblk) break;
             // matrices: keys 0-7 bytes 0-15, keys 8-15 bytes 0-15, keys 0-7
             // bytes 16-31, keys 8-15 bytes 16-31
             const int row = (warp + 4 * x) * 16 + (lane & 15);
@@ -509,7 +530,7 @@ __global__ void __launch_bounds__(Narrow8Cfg<D, NT>::THREADS, 2)
               P.lse[static_cast<int64_t>(h) * P.total + u.s.row0 + node] =
                   ll > 0.f || ll != ll ? (mm + __log2f(ll)) * 0.69314718055994530942f : -INFINITY;
           } else {
-            const int64_t at = static_cast<int64_t>(2 * blockIdx.x + (u.t0 == 0 ? 1 : 0)) * P.part_rows + r;
+            const int64_t at = static_cast<int64_t>(2 * block + (u.t0 == 0 ? 1 : 0)) * P.part_rows + r;
             float* dst = P.part_o + at * D + c;
             *reinterpret_cast<float4*>(dst) = v;
             if (any)
@@ -519,7 +540,7 @@ __global__ void __launch_bounds__(Narrow8Cfg<D, NT>::THREADS, 2)
           }
         }
       }
-      if (tid == 0) leave_record(P, u);
+      if (tid == 0) leave_record(P, u, block);
       named_sync(1, 32 * C::WARPS);     // ml, merge, seen and nf have been read
     }
   }

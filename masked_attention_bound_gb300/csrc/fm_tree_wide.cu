@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS, CODES>::THREADS, WideCfg<D, 
   // block has the time: 50 us by their copies, 53 by TMA.)
   const bool q_tma = SLOTS == 2 && !CODES && P.q_tma;
 
-  if (warp == 2) touch_memory<D>(P, lane);
+  if (warp == 2) touch_memory<D>(P, lane, blockIdx.x);
   if (tid == 0) {
     for (int s = 0; s < 2; ++s) {
       mbar_init(bar(W_QFULL + s), q_tma ? 1 : 4);   // else one arrival per softmax warp of the slot
@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS, CODES>::THREADS, WideCfg<D, 
   grid_launch_dependents();
   grid_dependency_wait();
   tc_fence_before();
-  TreeWalk<typename C::Geo> u(tree_run<typename C::Geo>(P));
+  TreeWalk<typename C::Geo> u(tree_run<typename C::Geo>(P, blockIdx.x));
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = *tmem_slot;
@@ -1058,7 +1058,7 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS, CODES>::THREADS, WideCfg<D, 
           }
         }
       }
-      if (tid == 0) leave_record(P, u);
+      if (tid == 0) leave_record(P, u, blockIdx.x);
       e0 += w.n;
       ++pieces;
       slots_sync<SLOTS>();        // ml and nf have been read, and S of both slots
