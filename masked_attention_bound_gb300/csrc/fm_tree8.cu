@@ -22,8 +22,8 @@ namespace fm {
 
 // HEADS_FIRST: with the blocks numbered as below, the heads of a sequence are
 // read at about the same time.  A token's codes of a head are 128 bytes (64),
-// and the next heads' follow: fetched alone, 128 at a time, they came at 5.8
-// TB/s.
+// and the next heads' follow: a step of 128 sequences of up to 8192 tokens
+// (d = 128) takes 270 us so, 279 with a sequence's heads one after another.
 struct Narrow8Geo {
   static constexpr bool HEADS_FIRST = true;
   static constexpr int R = 16, KT = 128, LEAST = 2;
