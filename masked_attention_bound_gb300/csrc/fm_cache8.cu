@@ -253,10 +253,12 @@ __global__ void __launch_bounds__(kRotThreads, CODES ? 3 : 4)
       unpack8(b[0], f + 8);
     }
     if (rotates) {
+      if (inter) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        if (inter) turn_pair(f[2 * e], f[2 * e + 1], w[e]);
-        else turn_pair(f[e], f[8 + e], w[e]);
+        for (int e = 0; e < 8; ++e) turn_pair(f[2 * e], f[2 * e + 1], w[e]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) turn_pair(f[e], f[8 + e], w[e]);
       }
     }
     if (!CODES || k.x >= 2) {
@@ -280,10 +282,18 @@ __global__ void __launch_bounds__(kRotThreads, CODES ? 3 : 4)
       const float raw = in && first > 0 ? *sp : 0.f;
       uint32_t top = 0;
       if (active) {
+        float t4[4];                                         // (a NaN is passed over)
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const uint32_t z = __float_as_uint(f[e]) & 0x7fffffffu;
-          top = max(top, z < 0x7f800000u ? z : 0u);          // the finite ones
+        for (int e = 0; e < 4; ++e)
+          t4[e] = fmaxf(fmaxf(fabsf(f[e]), fabsf(f[4 + e])), fmaxf(fabsf(f[8 + e]), fabsf(f[12 + e])));
+        top = __float_as_uint(fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])));
+        if (top >= 0x7f800000u) {                            // the finite ones
+          top = 0;
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const uint32_t z = __float_as_uint(f[e]) & 0x7fffffffu;
+            top = max(top, z < 0x7f800000u ? z : 0u);
+          }
         }
       }
       // over the group
