@@ -101,13 +101,28 @@ __device__ __forceinline__ void turn_pair(float& a, float& b, const Turn& t) {
 // the block, a group of n d / 16 threads (rounded up to a power of two) holds a
 // head's new tokens, 16 elements (two vectors of 8) a thread, so that a block's
 // largest value is known before any is rounded and K and V are read once.  The
-// groups take the heads of q, K and V in turn, each with the next one's loads
+// groups take the heads of q, K and V in turn, each with the next three's loads
 // under way; a thread has the same token and elements throughout, and so its
 // eight angles in registers.
 // Bound by HBM for prompts, by the latency of the lookups for single tokens.  (A
 // warp for all of a head's 16 tokens needed 159 registers: one thread block per
 // SM, 174 us for 16K tokens of 32 + 2 * 8 heads to codes.)
 constexpr int kRotThreads = 256;
+// Heads under way, in shared memory: in registers there was room for one (codes)
+// or two ahead (16K prompt tokens 93 us and 79 us instead of 75 and 71).  Two
+// stages 83 and 74; five 73 and 71, but a batch of single tokens 5.74 us instead
+// of 5.62.  Three thread blocks an SM (four without codes): two (three) 76 and 72,
+// four (five) with three stages 92 and 90.
+constexpr int kRotStages = 4;
+
+__device__ __forceinline__ void copy_async16(void* to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copy_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT>
+__device__ __forceinline__ void copy_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
+}
 
 struct RotArgs {
   Side kv[2];
@@ -141,6 +156,7 @@ __global__ void __launch_bounds__(kRotThreads, CODES ? 3 : 4)
   constexpr int CH = D / 16;               // chunks of 16 elements of a head
   __shared__ Turn turns[16][8][CH];        // [token][element of the chunk's eight angles][chunk]
   __shared__ uint32_t tops[2][kRotThreads / 32];
+  __shared__ uint4 ring[kRotStages][2][kRotThreads];
   grid_launch_dependents();
   grid_dependency_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -205,21 +221,21 @@ __global__ void __launch_bounds__(kRotThreads, CODES ? 3 : 4)
     return k;
   };
   const Job j0{y + group / per * ny, group % per};
-  auto load = [&](Job k, uint4& a, uint4& b) {
-    if (!active || k.hk >= A.Hkv) return;
-    const __nv_bfloat16* src = k.x < 2 ? A.kv[k.x].src + (t0 + i) * A.kv[k.x].tok + k.hk * A.kv[k.x].head
-                                       : A.q + (t0 + i) * A.q_stride[0] + (k.hk * nq + k.x - 2) * A.q_stride[1];
-    a = *reinterpret_cast<const uint4*>(src + va);
-    b = *reinterpret_cast<const uint4*>(src + vb);
+  // A thread's own elements, of this head and the next ones, in shared memory:
+  // nobody waits for another thread's.
+  auto fetch = [&](Job k, int stage) {
+    if (active && k.hk < A.Hkv) {
+      const __nv_bfloat16* src = k.x < 2 ? A.kv[k.x].src + (t0 + i) * A.kv[k.x].tok + k.hk * A.kv[k.x].head
+                                         : A.q + (t0 + i) * A.q_stride[0] + (k.hk * nq + k.x - 2) * A.q_stride[1];
+      copy_async16(&ring[stage][0][tid], src + va);
+      copy_async16(&ring[stage][1][tid], src + vb);
+    }
+    copy_async_commit();
   };
-  // the next AHEAD heads' elements
-  constexpr int AHEAD = CODES ? 1 : 2;
-  uint4 a[AHEAD + 1], b[AHEAD + 1];
   Job ahead = j0;
 #pragma unroll
-  for (int k = 0; k < AHEAD; ++k) {
-    a[k] = b[k] = make_uint4(0u, 0u, 0u, 0u);
-    load(ahead, a[k], b[k]);
+  for (int k = 0; k < kRotStages - 1; ++k) {
+    fetch(ahead, k);
     ahead = next(ahead);
   }
 
@@ -242,15 +258,20 @@ __global__ void __launch_bounds__(kRotThreads, CODES ? 3 : 4)
 #pragma unroll
   for (int e = 0; e < 8; ++e) w[e] = active && turned ? turns[i][e][c] : Turn{0.f, 0.f};
 
+  int stage = 0;
   int which = 0;             // of tops: a group's threads are one barrier apart at most
 #pragma unroll 1
   for (Job k = j0; k.hk < A.Hkv; k = next(k), ahead = next(ahead)) {
-    load(ahead, a[AHEAD], b[AHEAD]);
+    // (into the stage that the head before has been read from)
+    fetch(ahead, (stage + kRotStages - 1) % kRotStages);
+    copy_async_wait<kRotStages - 1>();
+    uint4 a = ring[stage][0][tid], b = ring[stage][1][tid];
+    stage = (stage + 1) % kRotStages;
     float f[16];
     const bool rotates = turned && k.x != 1;
     if (rotates || (CODES && k.x < 2)) {
-      unpack8(a[0], f);
-      unpack8(b[0], f + 8);
+      unpack8(a, f);
+      unpack8(b, f + 8);
     }
     if (rotates) {
       if (inter) {
@@ -263,16 +284,16 @@ __global__ void __launch_bounds__(kRotThreads, CODES ? 3 : 4)
     }
     if (!CODES || k.x >= 2) {
       if (rotates) {
-        a[0] = pack8(f);
-        b[0] = pack8(f + 8);
+        a = pack8(f);
+        b = pack8(f + 8);
       }
       __nv_bfloat16* dst =
           k.x < 2 ? static_cast<__nv_bfloat16*>(A.kv[k.x].pool) + pg * A.kv[k.x].page + (slot0 + i) * A.kv[k.x].slot +
                         k.hk * A.kv[k.x].phead
                   : A.q_out + (t0 + i) * A.o_stride[0] + (k.hk * nq + k.x - 2) * A.o_stride[1];
       if (active && (k.x >= 2 || in)) {
-        *reinterpret_cast<uint4*>(dst + va) = a[0];
-        *reinterpret_cast<uint4*>(dst + vb) = b[0];
+        *reinterpret_cast<uint4*>(dst + va) = a;
+        *reinterpret_cast<uint4*>(dst + vb) = b;
       }
     } else {
       const Side& S = A.kv[k.x];
@@ -336,11 +357,6 @@ __global__ void __launch_bounds__(kRotThreads, CODES ? 3 : 4)
         *reinterpret_cast<uint2*>(dst + vb) =
             make_uint2(pack_e4m3x4(f[8], f[9], f[10], f[11]), pack_e4m3x4(f[12], f[13], f[14], f[15]));
       }
-    }
-#pragma unroll
-    for (int x = 0; x < AHEAD; ++x) {
-      a[x] = a[x + 1];
-      b[x] = b[x + 1];
     }
   }
 }
