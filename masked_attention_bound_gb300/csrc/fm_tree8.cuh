@@ -148,25 +148,36 @@ __device__ __forceinline__ int row_shift(uint32_t top) {
   return top ? min(13 - (static_cast<int>(top >> 7) - 127), 126) : 0;
 }
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
-// Eight bf16 times a factor, as two parts of e4m3 whose sum they are: `hi` the
-// nearest code, `lo` the rest.
-__device__ __forceinline__ void split_e4m3(const uint32_t (&w)[4], float mul, uint2& hi, uint2& lo) {
-  uint32_t h[4], l[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float a = __uint_as_float(w[i] << 16) * mul, b = __uint_as_float(w[i] & 0xffff0000u) * mul;
-    h[i] = pack_e4m3x2(a, b);
-    const float2 r = float2_of_f16x2(f16x2_of_e4m3x2(h[i]));
-    l[i] = pack_e4m3x2(a - r.x, b - r.y);
-  }
-  hi = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
-  lo = make_uint2(l[0] | l[1] << 16, l[2] | l[3] << 16);
-}
 // A factor kept finite, so that a score of 0 stays 0 (NaN stays NaN).
 __device__ __forceinline__ float finite(float x) { return x > 0x1.fffffep127f ? 0x1.fffffep127f : x; }
 // Two bf16 times a factor, as f16.
 __device__ __forceinline__ uint32_t f16x2_of_bf16x2(uint32_t x, float mul) {
   return pack_f16(__uint_as_float(x << 16) * mul, __uint_as_float(x & 0xffff0000u) * mul);
+}
+// Eight bf16 times a factor that brings them below 2^8, as two parts of e4m3
+// whose sum they are: `hi` the nearest code, `lo` the rest's.  In f16, which has
+// all their bits from 2^-14 on; what is less has no code but 0 (the least is
+// 2^-9).  The difference is exact.
+__device__ __forceinline__ uint32_t e4m3x2_of_f16x2(uint32_t x) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(x));
+  return r;
+}
+__device__ __forceinline__ uint32_t sub_f16x2(uint32_t x, uint32_t y) {
+  uint32_t r;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+  return r;
+}
+__device__ __forceinline__ void split_e4m3(const uint32_t (&w)[4], float mul, uint2& hi, uint2& lo) {
+  uint32_t h[4], l[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t x = f16x2_of_bf16x2(w[i], mul);
+    h[i] = e4m3x2_of_f16x2(x);
+    l[i] = e4m3x2_of_f16x2(sub_f16x2(x, f16x2_of_e4m3x2(h[i])));
+  }
+  hi = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
+  lo = make_uint2(l[0] | l[1] << 16, l[2] | l[3] << 16);
 }
 
 // ---------------------------------------------------------------- NaN of V

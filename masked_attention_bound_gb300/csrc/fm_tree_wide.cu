@@ -661,8 +661,8 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS, CODES>::THREADS, WideCfg<D, 
           constexpr int LPR = D / 8, RPI = 32 / LPR;     // lanes a row, rows an instruction
           const unsigned in_rows = __ballot_sync(0xffffffffu, mine);
           if constexpr (CODES) {
-            // to two parts, a power of two per row; lane l keeps what undoes row
-            // l's.  All loads first: behind the stream of K and V each takes some
+            // to two parts, times a power of two per row; lane l keeps what undoes
+            // row l's.  All loads first: behind the stream of K and V each takes some
             // 3000 cycles (four at a time 13000 of a unit's 20000 for its ends).
             uint4 x[32 / RPI];
 #pragma unroll
@@ -672,25 +672,35 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS, CODES>::THREADS, WideCfg<D, 
               x[i] = make_uint4(0u, 0u, 0u, 0u);
               if ((in_rows >> from) & 1u) x[i] = *reinterpret_cast<const uint4*>(row + (lane % LPR) * 16);
             }
+            // a row's largest magnitude: over the words of a lane, then over its
+            // LPR lanes by halves, after which lane l of them has row l RPI's
+            uint32_t top[LPR];
 #pragma unroll
-            for (int i = 0; i < 32 / RPI; ++i) {
+            for (int i = 0; i < LPR; ++i)
+              top[i] = __vmaxu2(__vmaxu2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu),
+                                __vmaxu2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu));
+#pragma unroll
+            for (int o = LPR / 2; o > 0; o >>= 1)
+#pragma unroll
+              for (int i = 0; i < o; ++i) {
+                const uint32_t give = lane & o ? top[i] : top[i + o], keep = lane & o ? top[i + o] : top[i];
+                top[i] = __vmaxu2(keep, __shfl_xor_sync(0xffffffffu, give, o));
+              }
+            const uint32_t most = max(top[0] & 0xffffu, top[0] >> 16);
+            const int up = row_shift(most) - 6;        // the largest at [2^7, 2^8)
+            const float mul = pow2(up);
+            // (an infinity has no code: its row becomes NaN, as its scores are)
+            back = __shfl_sync(0xffffffffu, most < 0x7f80u ? pow2(-up) * P.scale_log2 : __int_as_float(0x7fc00000),
+                               (lane % RPI) * LPR + lane / RPI);
+#pragma unroll
+            for (int i = 0; i < LPR; ++i) {
               const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-              uint32_t top = 0;
-#pragma unroll
-              for (int y = 0; y < 4; ++y) top = max(top, max(w[y] & 0x7fffu, (w[y] >> 16) & 0x7fffu));
-#pragma unroll
-              for (int o = 1; o < LPR; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-              const int up = row_shift(top) - 6;       // the largest at [2^7, 2^8)
               uint2 hi, lo;
-              split_e4m3(w, pow2(up), hi, lo);
+              split_e4m3(w, __shfl_sync(0xffffffffu, mul, (lane & ~(LPR - 1)) + i), hi, lo);
               uint8_t* to = smem + C::OFF_Q + slot * C::QTILE +
                             Load::word16(quarter * 32 + i * RPI + lane / LPR, (lane % LPR) >> 1) + (lane & 1) * 8;
               *reinterpret_cast<uint2*>(to) = hi;
               *reinterpret_cast<uint2*>(to + 128 * D) = lo;
-              // (an infinity has no code: its row becomes NaN, as its scores are)
-              const float undo = top < 0x7f80u ? pow2(-up) * P.scale_log2 : __int_as_float(0x7fc00000);
-              const float of = __shfl_sync(0xffffffffu, undo, (lane % RPI) * LPR);
-              if (lane / RPI == i) back = of;
             }
           } else {
 #pragma unroll 2
