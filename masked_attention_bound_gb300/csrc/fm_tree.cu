@@ -764,7 +764,18 @@ TreeWs tree_ws8(const fm_cache& c, const fm_tree_desc& t, int sms) {
   const int64_t nodes = t.max_nodes < t.total ? t.max_nodes : t.total, rows = nodes * (t.H / c.Hkv);
   TreeWs W;
   const int64_t tokens = static_cast<int64_t>(c.max_pages) * c.page_size;
-  W.kind = rows <= NarrowGeo::R ? NARROW : rows <= MidGeo::R || c.d == 64 || tokens <= 640 ? MID : WIDE;
+  // More than 16 rows on the kernel for 16 where it is little: a tree of 32 rows
+  // over 16000 tokens 16.7 us so and 18.6 by 128 rows, over 40000 21.0 and 20.8;
+  // 64 rows of 2 heads over 10000 18.0 and 19.4, over 20000 22.6 and 20.1; 128
+  // rows of 8 heads over 1200 17.3 and 19.7, over 300 (units left whole) 12.1 and
+  // 11.6; 42 sequences of 18 rows of 4 heads over 318 22.3 and 16.0.
+  const int64_t units = static_cast<int64_t>(c.B) * c.Hkv * ((rows + NarrowGeo::R - 1) / NarrowGeo::R);
+  const bool little = units <= 2 * sms && units * tokens <= 80000 && tokens > 512;
+  // Pairs of tiles of 128 rows (d = 128) beat tiles side by side at every length:
+  // 512 units of 256 rows and 100, 560 and 980 tokens of context 53, 84 and 101 us
+  // against 56, 112 and 142; causal runs of 1920 rows after 100 and 1500 tokens 46
+  // and 81 against 56 and 98.
+  W.kind = rows <= NarrowGeo::R || little ? NARROW : rows <= MidGeo::R || c.d == 64 ? MID : WIDE;
   W.rows = W.kind == NARROW ? NarrowGeo::R
            : W.kind == WIDE ? (rows >= WideGeo::R ? WideGeo::R : (static_cast<int>(rows) + 31) / 32 * 32)
            : rows >= MidGeo::R ? MidGeo::R

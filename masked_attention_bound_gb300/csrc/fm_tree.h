@@ -98,6 +98,9 @@ struct WideGeo {
 struct Wide8Geo {
   static constexpr bool HEADS_FIRST = false;
   static constexpr int R = 256, KT = 64, LEAST = 4;
+  // a tile takes 2200 cycles, a unit's ends some 15000; with 6, 8, 10 and 14 tiles
+  // 64 nodes over 16384 tokens took 200.7, 200.8, 201.6 and 204 us, four prompts'
+  // pieces of 480 tokens 93.1, 92.8, 91.7 and 93.6
   __device__ static __forceinline__ int end(int) { return 10; }
 };
 

@@ -62,6 +62,16 @@ def test_causal_run_longer_than_a_tree(d):
     b.check(o, lse, rows=60)
 
 
+@pytest.mark.parametrize("kind", [None, "random", "padded"])
+@pytest.mark.parametrize("H,Hkv,d,nodes,ctx", [(3, 1, 64, [28, 5], 4000), (4, 4, 128, [200, 17], 600),
+                                               (8, 1, 128, [3, 16], 1250), (1, 1, 64, [17, 256], 2000)])
+def test_little_work_of_more_than_16_rows(kind, H, Hkv, d, nodes, ctx):
+    b = Batch8(29, [ctx + n for n in nodes], nodes, H, Hkv, d, 32, kind)
+    o, lse, code = run(b)
+    assert code == 0
+    b.check(o, lse)
+
+
 @pytest.mark.parametrize("nodes", [1, 40])
 def test_long_context_is_split_and_joined(nodes):
     b = Batch8(5, [131072 - 7, 40000], [nodes] * 2, 8, 2, 128, 128, "random")
@@ -93,9 +103,10 @@ def test_a_batch_with_empty_sequences_and_rows_behind_the_last():
     b.check(o[:4], lse[:, :4])
 
 
-# a kernel each: few rows, up to 16, more
+# a kernel each: few rows, up to 16, more; more on the kernel for 16; pairs of tiles, whole and split
 KERNELS = [(64, 1, 2, 1, 100, 16), (128, 1, 4, 1, 300, 64), (128, 3, 8, 2, 300, 16), (64, 12, 2, 2, 200, 32),
-           (128, 30, 8, 2, 140, 16), (64, 70, 4, 2, 100, 16), (128, 64, 8, 2, 900, 128)]
+           (128, 30, 8, 2, 140, 16), (64, 70, 4, 2, 100, 16), (128, 64, 8, 2, 900, 128),
+           (64, 40, 4, 1, 700, 64), (128, 64, 8, 2, 300, 64), (128, 50, 8, 2, 9000, 32)]
 
 
 @pytest.mark.parametrize("d,nodes,H,Hkv,ctx,page", KERNELS)
