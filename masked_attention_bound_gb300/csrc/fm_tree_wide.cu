@@ -36,7 +36,13 @@
 //
 // CODES: the cache holds e4m3 codes (see fm_tree8.cuh for the arithmetic).  S
 // multiplies K's codes as they are.  V's go to stages of their own and become f16
-// tiles in front of the MMAs, laid out as the bf16 tiles are.
+// tiles in front of the MMAs, laid out as the bf16 tiles are, by warps that do
+// nothing else.  Tiles have 64 keys and S two buffers a slot with SLOTS = 2 as
+// well: the slots take no turns, and always hold rows [128 s, 128 s + 128).  A tile
+// of 256 rows takes 2200 cycles, which is its softmax's chain of tensor memory
+// loads, maximum, weights and barriers in two warps a scheduler: without the second
+// part of Q, half of PV or exp2, each left out by itself, 16 trees of 64 nodes over
+// 16384 tokens took 199, 200 and 206 us instead of 204.
 //
 // TMEM: S/P of slot s at column 128 s (SLOTS = 1: of every second tile at
 // column 64), the O's after the S's.
