@@ -36,7 +36,7 @@ struct Side {
 
 // ------------------------------------------------------------------ angles
 // The angle of position p at frequency f (radians a position) is p f mod 2
-// pi.  It is kept as a 64-bit fraction of a turn: f / 2 pi is rounded to 64
+// pi.  It is kept as a 64-bit fraction of a turn: f / 2 pi is cut off to 64
 // bits once, and the product with p wraps around like the angle does, exactly
 // (2^30 positions on, 2^-34 of a turn is left).  cos and sin come from their
 // Taylor series on an eighth of a turn to either side of a quarter's multiple,
@@ -45,10 +45,26 @@ struct Turn {
   float c, s;
 };
 
+// f / 2 pi as a fraction of a turn, cut off to 64 bits: f is m 2^e with 24 bits of m,
+// and 2^128 / 2 pi times m has the bits that are wanted from 64 - e on.  (In
+// integers: with doubles, of which an SM does two a cycle, 16 trees of 64 nodes took
+// 8.25 us instead of 7.37.)
 __device__ __forceinline__ uint64_t turn_step(float f) {
-  constexpr double kHi = 0.15915494309189535, kLo = -9.839338337591243e-18;   // 1 / 2 pi
-  const double t = f * kHi, low = fma(static_cast<double>(f), kHi, -t) + f * kLo;
-  return static_cast<uint64_t>((t - floor(t)) * 0x1p64) + static_cast<uint64_t>(static_cast<int64_t>(low * 0x1p64));
+  const uint32_t bits = __float_as_uint(f), top = (bits >> 23) & 0xff;
+  const uint32_t m = (bits & 0x7fffff) | (top ? 0x800000 : 0);
+  const int e = static_cast<int>(top ? top : 1) - 150;
+  const uint64_t p0 = 0x7d4d3770ull * m, p1 = 0x7f09d5f4ull * m + (p0 >> 32);
+  const uint64_t p2 = 0x9391054aull * m + (p1 >> 32), p3 = 0x28be60dbull * m + (p2 >> 32);
+  uint64_t step;
+  if (e > -32) {                             // f of 2^-9 and more
+    const uint64_t high = (p3 << 32) | (p2 & 0xffffffffu), low = (p1 << 32) | (p0 & 0xffffffffu);
+    if (e < 0) step = (high >> -e) | ((p3 >> 32) << (64 + e));
+    else if (e == 0) step = high;
+    else step = e < 64 ? (high << e) | (low >> (64 - e)) : low << (e - 64);
+  } else {
+    step = e > -96 ? p3 >> (-32 - e) : 0;
+  }
+  return bits >> 31 ? 0 - step : step;
 }
 
 __device__ __forceinline__ Turn turn_of(int64_t pos, uint64_t step) {

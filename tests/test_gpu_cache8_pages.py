@@ -200,6 +200,20 @@ def test_far_positions(pos, inter):
     assert torch.equal(out[1], q[1])
 
 
+def test_frequencies_of_all_sizes():
+    b = Batch(14, [3], [3], 2, 2, 128, 16)
+    q, k = _new(15, 3, 2, 128), _new(16, 3, 2, 128)
+    f = _freqs(64)
+    sizes = [0.0, -0.0, 1e-42, 2.0 ** -100, 2.0 ** -40 * 1.3, 2.0 ** -9 * 0.999, 2.0 ** -9, -(2.0 ** -8), 1.7, 1e4,
+             2.0 ** 22 + 0.5, 2.0 ** 23 + 1, 2.0 ** 24, -(2.0 ** 24) * 1.1, 2.0 ** 25 * 1.3]
+    f[:len(sizes)] = torch.tensor(sizes)
+    pos = [1000, 3, -999]
+    out = fm.cache_append_rotary(q, k, k, b.cu, f, b.k, b.v, b.table, b.lens_t, positions=ints(pos))
+    want = o8.rotate(to64(q), pos, to64(f), False)
+    # (angles up to 2^36 in the oracle's long doubles, of 2^-64 or less)
+    assert (bf16_excess(out, want, pair_size(to64(q), 64, False)) - 2.0 ** -27 * 8).max() <= 0
+
+
 def test_frequencies_not_finite_make_their_pairs_nan():
     b = Batch(14, [2], [2], 1, 1, 64, 16)
     q, k = _new(15, 2, 1, 64), _new(16, 2, 1, 64)
