@@ -148,6 +148,15 @@ __device__ __forceinline__ int row_shift(uint32_t top) {
   return top ? min(13 - (static_cast<int>(top >> 7) - 127), 126) : 0;
 }
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
+// What takes S to a score, a block's scale times a row's factor, kept within the
+// normal numbers: a masked -inf stays one (times 0 it would be NaN, and sk is
+// 2^-60 where nothing was loaded), a score of 0 stays 0.  NaN stays NaN.
+__device__ __forceinline__ float score_factor(float sk, float back) {
+  float f;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(f) : "f"(sk * back), "f"(0x1p-126f));
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(f) : "f"(f), "f"(0x1.fffffep127f));
+  return f;
+}
 // A factor kept finite, so that a score of 0 stays 0 (NaN stays NaN).
 __device__ __forceinline__ float finite(float x) { return x > 0x1.fffffep127f ? 0x1.fffffep127f : x; }
 // Two bf16 times a factor, as f16.

@@ -785,7 +785,6 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS, CODES>::THREADS, WideCfg<D, 
               auto factors = [&](int b, uint64_t& k, uint64_t& v) {
                 asm("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(k), "=l"(v) : "r"(facts + b * 16));
               };
-              const uint64_t back2 = splat2(back);
               float m_tile = -INFINITY;
 #pragma unroll
               for (int b = 0; b < C::BLOCKS; ++b) {
@@ -796,7 +795,7 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS, CODES>::THREADS, WideCfg<D, 
 #pragma unroll
                 for (int y = 0; y < 4; ++y) a[y] = fmax3(s[y], s[y + 4], s[y + 8]);
                 const float top = fmax3(fmax3(a[0], s[12], a[1]), fmax3(s[13], a[2], s[14]), fmaxf(a[3], s[15]));
-                m_tile = fmaxf(m_tile, fmaf(top, __uint_as_float(static_cast<uint32_t>(k)) * back,
+                m_tile = fmaxf(m_tile, fmaf(top, score_factor(__uint_as_float(static_cast<uint32_t>(k)), back),
                                             __uint_as_float(static_cast<uint32_t>(v))));
               }
               // the reference moves only when the maximum grows by more than
@@ -813,7 +812,8 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS, CODES>::THREADS, WideCfg<D, 
                 float take;
                 factors(b, k, v);
                 asm("ld.shared.f32 %0, [%1];" : "=f"(take) : "r"(takes + b * 4));
-                const uint64_t sc2 = mul2(k, back2), nm2 = add2(v, shift2);
+                const uint64_t sc2 = splat2(score_factor(__uint_as_float(static_cast<uint32_t>(k)), back));
+                const uint64_t nm2 = add2(v, shift2);
                 uint32_t pk[8];
                 float s0 = 0.f, s1 = 0.f;
 #pragma unroll

@@ -1,0 +1,58 @@
+"""Attention over the cache of e4m3 codes where its factors leave the range of fp32 or Q's parts that of a
+code, against the fp64 oracle."""
+import numpy as np
+import pytest
+import torch
+
+from cache8_cases import Batch8
+from test_gpu_cache8_attention import KERNELS, run
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("kind", [None, "beams"])
+@pytest.mark.parametrize("d,nodes,H,Hkv,ctx,page", KERNELS)
+def test_rows_of_tiny_queries(d, nodes, H, Hkv, ctx, page, kind):
+    """A score times its factors is 0 long before bf16 ends; what a row does not see stays unseen."""
+    b = Batch8(40, [ctx + nodes, nodes + 3], [nodes, nodes], H, Hkv, d, page, kind)
+    T = b.q.shape[0]
+    e = torch.tensor([-130.0, -100.0, 0.0, -90.0, -60.0, -120.0, -75.0], dtype=torch.float64, device="cuda")
+    at = (torch.arange(T, device="cuda")[:, None] * 3 + torch.arange(H, device="cuda")) % len(e)
+    b.q = (b.q.double() * torch.exp2(e[at])[..., None]).to(torch.bfloat16)
+    o, lse, code = run(b)
+    assert code == 0
+    b.check(o, lse)
+
+
+@pytest.mark.parametrize("d,nodes,H,Hkv,ctx,page", KERNELS)
+@pytest.mark.parametrize("scale", [1e-30, 2e-38])
+def test_tiny_scales(d, nodes, H, Hkv, ctx, page, scale):
+    b = Batch8(41, [ctx + nodes, nodes + 3], [nodes, nodes], H, Hkv, d, page)
+    b.scale = scale
+    o, lse, code = run(b)
+    assert code == 0
+    b.check(o, lse, rows=12)
+
+
+@pytest.mark.parametrize("d,nodes,H,Hkv,ctx,page", KERNELS)
+def test_large_factors_of_keys_of_zeros(d, nodes, H, Hkv, ctx, page):
+    """Scores of 0 under a factor past the range of fp32."""
+    b = Batch8(42, [ctx + nodes, nodes + 3], [nodes, nodes], H, Hkv, d, page)
+    b.k.view(torch.uint8).zero_()
+    b.k_scale.fill_(2.0 ** 60)
+    b.q[::2] *= 2.0 ** 100
+    o, lse, code = run(b)
+    assert code == 0
+    b.check(o, lse, rows=12)
+
+
+@pytest.mark.parametrize("d,nodes,H,Hkv,ctx,page", KERNELS)
+@pytest.mark.parametrize("e", [-100, 100])
+def test_queries_of_all_sizes_with_keys_and_scale_that_undo_them(d, nodes, H, Hkv, ctx, page, e):
+    b = Batch8(43, [ctx + nodes], [nodes], H, Hkv, d, page)
+    b.q *= 2.0 ** e
+    b.k_scale *= 2.0 ** (-e // 2)
+    b.scale *= 2.0 ** (-e // 2)
+    o, lse, code = run(b)
+    assert code == 0
+    b.check(o, lse, rows=12)
