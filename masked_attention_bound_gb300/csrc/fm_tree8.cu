@@ -221,7 +221,8 @@ __global__ void __launch_bounds__(Narrow8Cfg<D, NT>::THREADS, 2)
         const float mul = pow2(up);
 #pragma unroll
         for (int i = 0; i < D / 8; ++i) qf[nt][i >> 1][i & 1] = f16x2_of_bf16x2(w[i], mul);
-        const float undo = pow2(-up) * P.scale_log2;
+        // (an infinity in a row makes it NaN, also where all its scores would be -inf)
+        const float undo = top < 0x7f80u ? pow2(-up) * P.scale_log2 : __int_as_float(0x7fc00000);
         back[nt][0] = __shfl_sync(0xffffffffu, undo, 8 * tq);
         back[nt][1] = __shfl_sync(0xffffffffu, undo, 8 * tq + 4);
       }

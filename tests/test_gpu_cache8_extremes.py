@@ -56,3 +56,20 @@ def test_queries_of_all_sizes_with_keys_and_scale_that_undo_them(d, nodes, H, Hk
     o, lse, code = run(b)
     assert code == 0
     b.check(o, lse, rows=12)
+
+
+@pytest.mark.parametrize("d,nodes,H,Hkv,ctx,page", KERNELS)
+@pytest.mark.parametrize("inf", [float("inf"), float("-inf")])
+def test_a_row_with_an_infinite_query_is_nan(d, nodes, H, Hkv, ctx, page, inf):
+    """Also where every score is -inf: there is no softmax of them.  Other rows are not touched."""
+    b = Batch8(44, [ctx + nodes], [nodes], H, Hkv, d, page, "beams")
+    k = b.k.view(torch.uint8)
+    k[..., 5] = torch.where(k[..., 5] & 0x7f == 0x7f, k[..., 5], 0x38)
+    want, want_lse, _ = run(b)
+    t, h = nodes // 2, H - 1
+    b.q[t, h, 5] = inf
+    o, lse, code = run(b)
+    assert code == 0
+    assert o[t, h].isnan().all() and lse[h, t].isnan()
+    o[t, h], lse[h, t] = want[t, h], want_lse[h, t]
+    assert torch.equal(o, want) and torch.equal(lse, want_lse)
