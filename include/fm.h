@@ -490,7 +490,10 @@ fm_status fm_cache_append_rotary(const fm_cache* cache, const fm_rotary* rotary,
  *
  * fm_tree_fwd_fp8: as fm_tree_fwd (workspace, masks, split and order
  * included), over the values that the codes stand for.  A NaN code reaches
- * the rows that see its key, and no other.
+ * the rows that see its key, and no other; an infinite query makes its row NaN.
+ * Queries enter with all their bits, but for elements far below their row's
+ * largest: past 2^-13 of it they are off by 2^-21 of it at most (up to 16 rows
+ * of a sequence and K/V head: past 2^-27, by 2^-38).
  *
  * fm_cache_accept_fp8: as fm_cache_accept.  A block that accepted nodes come to
  * gets the largest of its own scale and those of the blocks that they come

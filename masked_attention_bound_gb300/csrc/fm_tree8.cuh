@@ -13,10 +13,12 @@
 // few rows that brings its largest element to 2^13 at least, and it becomes
 // f16: every element within 2^-27 of the largest has all its bits, and what is
 // below is off by 2^-38 of it at most.  For tcgen05, whose operands have one
-// width, Q is the sum of two e4m3 numbers, the nearest one and the rest, with
-// the largest element at 2^7 or more: 4 and 4 of its 8 bits, exactly for
-// elements within 2^-9 of the largest, off by 2^-17 of it below.  (Two products
-// at the 8-bit rate take as long as one of f16, and K needs no conversion: with
+// width, Q is the sum of two 8-bit numbers, with the largest element at 2^7 or
+// more: the nearest e4m3 one (4 of its 8 bits) and the rest, which is at most 8
+// of the bf16's last steps and so has the 3 bits of e5m2, whose range goes on
+// to 2^-16 where e4m3's ends at 2^-9.  Elements within 2^-13 of the largest are
+// exact, and what is below is off by 2^-21 of it at most.  (Two products at the
+// 8-bit rate take as long as one of f16, and K needs no conversion: with
 // f16 tiles of K too, 16 trees of 64 nodes took 373 us.)  P is f16 and offset by
 // 2^7 (R moves when the maximum has grown by more than 2^8), so that f16 holds
 // it with 11 bits down to 2^-21 of the largest and with an error of 2^-32 of
@@ -163,13 +165,18 @@ __device__ __forceinline__ float finite(float x) { return x > 0x1.fffffep127f ? 
 __device__ __forceinline__ uint32_t f16x2_of_bf16x2(uint32_t x, float mul) {
   return pack_f16(__uint_as_float(x << 16) * mul, __uint_as_float(x & 0xffff0000u) * mul);
 }
-// Eight bf16 times a factor that brings them below 2^8, as two parts of e4m3
-// whose sum they are: `hi` the nearest code, `lo` the rest's.  In f16, which has
-// all their bits from 2^-14 on; what is less has no code but 0 (the least is
-// 2^-9).  The difference is exact.
+// Eight bf16 times a factor that brings them below 2^8, as two parts whose sum
+// they are: `hi` the nearest e4m3 code, `lo` the rest's nearest e5m2 code.  f16
+// has all their bits from 2^-17 on, where e5m2 ends too, and the difference is
+// exact in it.  From 2^-6 on, where e4m3 has its 4 bits, so is `lo`.
 __device__ __forceinline__ uint32_t e4m3x2_of_f16x2(uint32_t x) {
   uint16_t r;
   asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(x));
+  return r;
+}
+__device__ __forceinline__ uint32_t e5m2x2_of_f16x2(uint32_t x) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(r) : "r"(x));
   return r;
 }
 __device__ __forceinline__ uint32_t sub_f16x2(uint32_t x, uint32_t y) {
@@ -177,13 +184,13 @@ __device__ __forceinline__ uint32_t sub_f16x2(uint32_t x, uint32_t y) {
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
   return r;
 }
-__device__ __forceinline__ void split_e4m3(const uint32_t (&w)[4], float mul, uint2& hi, uint2& lo) {
+__device__ __forceinline__ void split_q(const uint32_t (&w)[4], float mul, uint2& hi, uint2& lo) {
   uint32_t h[4], l[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const uint32_t x = f16x2_of_bf16x2(w[i], mul);
     h[i] = e4m3x2_of_f16x2(x);
-    l[i] = e4m3x2_of_f16x2(sub_f16x2(x, f16x2_of_e4m3x2(h[i])));
+    l[i] = e5m2x2_of_f16x2(sub_f16x2(x, f16x2_of_e4m3x2(h[i])));
   }
   hi = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
   lo = make_uint2(l[0] | l[1] << 16, l[2] | l[3] << 16);
@@ -215,6 +222,10 @@ static __device__ __noinline__ void fix_row8(const Tree8Params& A, int b, int hk
     }
   }
 }
+
+// Instruction descriptor of an MMA whose A is the second part (e5m2: format 1) and
+// whose B is codes (e4m3: format 0).
+__host__ __device__ constexpr uint32_t idesc_e5m2_e4m3(int M, int N) { return idesc_e4m3(M, N) | (1u << 7); }
 
 fm_status launch_tree8_mid(const Tree8Params& A, int d, const CUtensorMap& tk, const CUtensorMap& tv, int grid,
                            cudaStream_t s);        // up to 128 rows

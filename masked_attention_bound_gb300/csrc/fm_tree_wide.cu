@@ -374,10 +374,11 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS, CODES>::THREADS, WideCfg<D, 
       auto s_step = [&](uint32_t to, uint32_t dK, int i) {
         if constexpr (CODES) {
           const int part = i / (D / 32), kk = i % (D / 32);
+          const uint32_t id = part ? idesc_e5m2_e4m3(128, KT) : idS;
           if constexpr (D == 128)
-            mma_ss_f8(to, sdesc_at(dQ, part * (128 * D) + kk * 32), sdesc_at(dK, kk * 32), idS, i > 0 ? 1u : 0u);
+            mma_ss_f8(to, sdesc_at(dQ, part * (128 * D) + kk * 32), sdesc_at(dK, kk * 32), id, i > 0 ? 1u : 0u);
           else
-            mma_ss_f8(to, sdesc64_at(dQ, part * (128 * D) + kk * 32), sdesc64_at(dK, kk * 32), idS, i > 0 ? 1u : 0u);
+            mma_ss_f8(to, sdesc64_at(dQ, part * (128 * D) + kk * 32), sdesc64_at(dK, kk * 32), id, i > 0 ? 1u : 0u);
         } else {
           mma_ss(to, sdesc_at(dQ, (i >> 2) * (128 * 128) + (i & 3) * 32),
                  sdesc_at(dK, (i >> 2) * (KT * 128) + (i & 3) * 32), idS, i > 0 ? 1u : 0u);
@@ -667,7 +668,7 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS, CODES>::THREADS, WideCfg<D, 
           constexpr int LPR = D / 8, RPI = 32 / LPR;     // lanes a row, rows an instruction
           const unsigned in_rows = __ballot_sync(0xffffffffu, mine);
           if constexpr (CODES) {
-            // to two parts, times a power of two per row; lane l keeps what undoes
+            // to two parts (see split_q), times a power of two per row; lane l keeps what undoes
             // row l's.  All loads first: behind the stream of K and V each takes some
             // 3000 cycles (four at a time 13000 of a unit's 20000 for its ends).
             uint4 x[32 / RPI];
@@ -702,7 +703,7 @@ __global__ void __launch_bounds__(WideCfg<D, SLOTS, CODES>::THREADS, WideCfg<D, 
             for (int i = 0; i < LPR; ++i) {
               const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
               uint2 hi, lo;
-              split_e4m3(w, __shfl_sync(0xffffffffu, mul, (lane & ~(LPR - 1)) + i), hi, lo);
+              split_q(w, __shfl_sync(0xffffffffu, mul, (lane & ~(LPR - 1)) + i), hi, lo);
               uint8_t* to = smem + C::OFF_Q + slot * C::QTILE +
                             Load::word16(quarter * 32 + i * RPI + lane / LPR, (lane % LPR) >> 1) + (lane & 1) * 8;
               *reinterpret_cast<uint2*>(to) = hi;

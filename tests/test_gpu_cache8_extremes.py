@@ -73,3 +73,19 @@ def test_a_row_with_an_infinite_query_is_nan(d, nodes, H, Hkv, ctx, page, inf):
     assert o[t, h].isnan().all() and lse[h, t].isnan()
     o[t, h], lse[h, t] = want[t, h], want_lse[h, t]
     assert torch.equal(o, want) and torch.equal(lse, want_lse)
+
+
+@pytest.mark.parametrize("d,nodes,H,Hkv,ctx,page", KERNELS)
+@pytest.mark.parametrize("ratio", [2.0 ** 10, -(2.0 ** 12)])
+def test_one_element_of_a_row_far_above_the_others(d, nodes, H, Hkv, ctx, page, ratio):
+    """The others decide the scores (K is 0 at the large one).  They are 2^-13 of it or more, which every
+    kernel keeps exactly, so that the tolerance has no term for Q."""
+    b = Batch8(45, [ctx + nodes, nodes + 3], [nodes, nodes], H, Hkv, d, page, "beams")
+    k = b.k.view(torch.uint8)
+    k[..., 9] = torch.where(k[..., 9] & 0x7f == 0x7f, k[..., 9], 0)
+    least = abs(ratio) * 2.0 ** -13
+    b.q = torch.copysign(b.q.abs().clamp_min(least), b.q)
+    b.q[..., 9] = ratio
+    o, lse, code = run(b)
+    assert code == 0
+    b.check(o, lse)
