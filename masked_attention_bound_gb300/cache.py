@@ -121,7 +121,8 @@ def cache_append_rotary(q, k, v, cu, freqs, k_pool, v_pool, table, lens, positio
     of a head's first 2 n, n = len(freqs) (a multiple of 8), turns by position * freqs[i] radians.  Pairs
     are (x[i], x[i + n]), or neighbours with ``interleaved``.  ``positions`` [total]: by default
     a token's place in its sequence; a drafted node has context + depth.  Returns the rotated queries
-    [total][H][d] (``q_out``, which may be ``q``), or None where ``q`` is None."""
+    [total][H][d] (``q_out``, which may be ``q`` and overlaps neither it otherwise nor ``k`` and ``v``), or
+    None where ``q`` is None."""
     return _call("append_rotary", stream, q, k, v, cu, freqs, k_pool, v_pool, table, lens, positions,
                  interleaved, q_out, k_scale, v_scale, status)
 

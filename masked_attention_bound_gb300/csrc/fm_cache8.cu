@@ -524,6 +524,43 @@ Side side_of(const fm_cache& c, int which, void* pool, float* scale) {
   return S;
 }
 
+// Heads of packed tokens, [total][heads][d] with the strides of a call (elements of bf16).
+struct Rows {
+  const void* p;
+  int64_t tok, head, heads;
+  int64_t in_token(int d) const { return (heads - 1) * head + d; }
+  int64_t span(int total, int d) const { return (total - 1) * tok + in_token(d); }
+};
+Rows rows_of(const void* p, const int64_t* stride, int total, int heads) {
+  // what is never stepped along has no stride
+  return Rows{p, total > 1 ? stride[0] : 0, heads > 1 ? stride[1] : 0, heads};
+}
+
+// a and b share no element, as far as that is found out: where their spans cross
+// (slices of one buffer) their token strides must be the same.
+bool rows_apart(const Rows& a, const Rows& b, int total, int d) {
+  if (!overlaps(a.p, 2 * a.span(total, d), b.p, 2 * b.span(total, d))) return true;
+  if (a.tok != b.tok) return false;
+  const int64_t bytes = static_cast<const char*>(b.p) - static_cast<const char*>(a.p);
+  if (bytes % 2 != 0) return false;
+  const int64_t delta = bytes / 2, s = a.tok;
+  if (s > 0) {           // side by side within a token
+    const int64_t off = ((delta % s) + s) % s;
+    if (off >= a.in_token(d) && off + b.in_token(d) <= s) return true;
+  }
+  // element t s + i head + c of a is element t' s + i' head' + c' of b at delta: for each i
+  // and i' the nearest t - t'
+  for (int64_t i = 0; i < a.heads; ++i)
+    for (int64_t k = 0; k < b.heads; ++k) {
+      const int64_t x = delta + k * b.head - i * a.head;
+      int64_t t = s > 0 ? (2 * x + (x < 0 ? -s : s)) / (2 * s) : 0;
+      t = t < 1 - total ? 1 - total : t > total - 1 ? total - 1 : t;
+      const int64_t left = x - t * s;
+      if (left < d && left > -d) return false;
+    }
+  return true;
+}
+
 bool stride_ok(const int64_t* s, int n, int unit) {
   for (int i = 0; i < n; ++i)
     if (s[i] <= 0 || s[i] % unit != 0 || s[i] >= (int64_t(1) << 36)) return false;
@@ -569,6 +606,14 @@ fm_status fm_cache_append_rotary(const fm_cache* c, const fm_rotary* t, const vo
   if (static_cast<int64_t>(total) * (t->H > c->Hkv ? t->H : c->Hkv) > kMaxTokenIndex) return FM_ERR_UNSUPPORTED;
   const int64_t blocks = total / kScaleBlock + 2 * static_cast<int64_t>(c->B);
   if (blocks > 0x7fffffff) return FM_ERR_UNSUPPORTED;
+  if (t->H > 0) {        // other thread blocks read K, V and the queries while one writes its own
+    const Rows q = rows_of(t->q, t->q_stride, total, t->H), o = rows_of(t->q_out, t->o_stride, total, t->H);
+    const bool in_place = q.p == o.p && q.tok == o.tok && q.head == o.head;
+    if ((!in_place && !rows_apart(q, o, total, c->d)) ||
+        !rows_apart(rows_of(k, k_stride, total, c->Hkv), o, total, c->d) ||
+        !rows_apart(rows_of(v, v_stride, total, c->Hkv), o, total, c->d))
+      return FM_ERR_INVALID;
+  }
   RotArgs A{};
   A.kv[0] = side_of(*c, 0, k_pool, k_scale);
   A.kv[1] = side_of(*c, 1, v_pool, v_scale);
