@@ -328,9 +328,11 @@ __global__ void __launch_bounds__(kRotThreads, CODES ? 3 : 4)
           }
         }
       }
-      // over the group
+      // over the group, all of which has read the scale when its first thread writes
+      // the new one
       if (size >= 32) {
         top = __reduce_max_sync(0xffffffffu, top);
+        __syncwarp();
         if (size > 32) {
           which ^= 1;
           if (lane == 0) tops[which][warp] = top;
@@ -341,6 +343,7 @@ __global__ void __launch_bounds__(kRotThreads, CODES ? 3 : 4)
       } else {
         const unsigned peers = ((1u << size) - 1u) << (lane & ~(size - 1));
         for (int o = 1; o < size; o <<= 1) top = max(top, __shfl_xor_sync(peers, top, o));
+        __syncwarp(peers);
       }
       float s = scale_for(__uint_as_float(top));
       uint8_t* pool = static_cast<uint8_t*>(S.pool) + pg * S.page + head * S.phead +
