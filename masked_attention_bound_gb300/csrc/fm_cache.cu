@@ -81,20 +81,6 @@ Pools pools_of(const fm_cache& c, void* k, void* v, float* k_scale = nullptr, fl
   return P;
 }
 
-__device__ __forceinline__ void flag(int* status, int bit) {
-  if (status) atomicOr(status, bit);
-}
-
-// Context length of packed sequence b (tokens before its new ones), or -1 if
-// its lens or cu entries are out of range; n: its new tokens.
-__device__ __forceinline__ int context_of(const int32_t* lens, const int32_t* cu, int b, int total,
-                                          int max_tokens, int& n) {
-  const int c0 = cu[b], c1 = cu[b + 1], len = lens[b];
-  n = c1 - c0;
-  if (c0 < 0 || c1 < c0 || c1 > total || len > max_tokens || len < n) return -1;
-  return len - n;
-}
-
 // ------------------------------------------------------------------ append
 // Each block takes a few consecutive packed tokens.  All threads first load
 // its 16-byte vectors, K and V, which needs no lookup; meanwhile a warp (or, of
@@ -744,8 +730,6 @@ __global__ void __launch_bounds__(kCopyThreads)
     if (!ok) flag(A.status, DEV_CACHE);
   }
 }
-
-fm_status done(cudaError_t e) { return e == cudaSuccess ? FM_OK : FM_ERR_CUDA; }
 
 // Each output is its input itself or does not overlap it.
 bool outputs_apart(const fm_cache& c, const PageArgs& A) {

@@ -1,4 +1,4 @@
-// Host-side declarations of the paged K/V cache's translation units.
+// What the translation units of the paged K/V cache share.
 #pragma once
 #include <atomic>
 
@@ -15,6 +15,22 @@ fm_status check_cache(const fm_cache* c, bool pools);
 // The same of a cache of e4m3 codes, and its pools and scales.
 fm_status check_cache8(const fm_cache* c, const void* k_pool, const void* v_pool, const void* k_scale,
                        const void* v_scale);
+
+__device__ __forceinline__ void flag(int* status, int bit) {
+  if (status) atomicOr(status, bit);
+}
+
+// Context length of packed sequence b (tokens before its new ones), or -1 if
+// its lens or cu entries are out of range; n: its new tokens.
+__device__ __forceinline__ int context_of(const int32_t* lens, const int32_t* cu, int b, int total,
+                                          int max_tokens, int& n) {
+  const int c0 = cu[b], c1 = cu[b + 1], len = lens[b];
+  n = c1 - c0;
+  if (c0 < 0 || c1 < c0 || c1 > total || len > max_tokens || len < n) return -1;
+  return len - n;
+}
+
+inline fm_status done(cudaError_t e) { return e == cudaSuccess ? FM_OK : FM_ERR_CUDA; }
 
 inline int page_shift(int page_size) {
   return page_size == 16 ? 4 : page_size == 32 ? 5 : page_size == 64 ? 6 : 7;

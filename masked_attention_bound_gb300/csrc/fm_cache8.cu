@@ -11,20 +11,6 @@
 namespace fm {
 namespace {
 
-__device__ __forceinline__ void flag(int* status, int bit) {
-  if (status) atomicOr(status, bit);
-}
-
-// Context length of packed sequence b (tokens before its new ones), or -1 if
-// its lens or cu entries are out of range; n: its new tokens.
-__device__ __forceinline__ int context_of(const int32_t* lens, const int32_t* cu, int b, int total,
-                                          int max_tokens, int& n) {
-  const int c0 = cu[b], c1 = cu[b + 1], len = lens[b];
-  n = c1 - c0;
-  if (c0 < 0 || c1 < c0 || c1 > total || len > max_tokens || len < n) return -1;
-  return len - n;
-}
-
 // K or V: its new tokens, its pool (16-byte vectors' units: elements) and scales.
 struct Side {
   const __nv_bfloat16* src;
@@ -513,8 +499,6 @@ __global__ void __launch_bounds__(kAccept8Warps * 32, 8)
     }
   }
 }
-
-fm_status done(cudaError_t e) { return e == cudaSuccess ? FM_OK : FM_ERR_CUDA; }
 
 Side side_of(const fm_cache& c, int which, void* pool, float* scale) {
   const int64_t* st = which ? c.v_stride : c.k_stride;

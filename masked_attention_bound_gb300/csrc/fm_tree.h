@@ -72,6 +72,17 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeParams& P, int b) {
   return s;
 }
 
+// What the kernels of few rows load their operands and meet by.
+__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void named_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
 // Geometry of the kernels: rows of a unit, keys of a tile, a unit's fixed cost
 // in tiles, and the shortest run of a block in tiles (a part of 128 rows is as
 // many bytes as two 64-key tiles, written and read again).  HEADS_FIRST: the
