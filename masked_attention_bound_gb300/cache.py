@@ -8,8 +8,11 @@ elements, or e4m3 codes (torch.float8_e4m3fn, strides multiples of 16).  A
 cache of codes comes with ``k_scale`` and ``v_scale``, contiguous fp32 tensors
 [pages][Hkv][page_size / 16] (with the layers in front where the pools have
 them; ``cache_scales`` makes them): a value is its code times the scale of its
-block of 16 tokens and head.  It takes half the bytes, and attention over it,
-bound by reading them, about half the time.
+block of 16 tokens and head.  It takes half the bytes.  Attention over it takes
+0.5 to 0.65 of the time where reading them is what it waits for (up to 16 rows,
+query tokens times heads, a sequence and K/V head); with more it is bound by
+other things: trees of 32 nodes of 4 heads take about as long as over bf16,
+trees of 64 and pieces of prompts up to a fifth longer.
 ``table`` [B][max_pages], ``lens`` [B], ``ref`` [pages], ``cu`` [B + 1],
 ``parents`` [total] and the other index arrays are contiguous int32 tensors on
 the pools' device.
@@ -151,8 +154,10 @@ def tree_forward(q, k_pool, v_pool, table, lens, cu, scale, parents=None, max_no
     it.  ``max_nodes``: an upper bound of a sequence's query tokens (default: total, with
     ``parents`` at most 256); a close one picks the faster kernel, and a batch of several
     sequences should give it (128 single tokens over up to 255 tokens of context, 4 query heads
-    per K/V head: 31 us with 1, 60 with the default, which plans for 128 tokens a sequence; over
-    up to 8192 tokens 481 and 493)."""
+    per K/V head: 31 us with 1, 41 to 60 with the default, which plans for 128 tokens a sequence; over
+    up to 8192 tokens 482 and 498; over codes 23 and 92, 270 and 616).  The largest sequence picks it
+    for all: pieces of prompts are better a call of their own beside single tokens (a piece of 480
+    tokens and 127 single ones over up to 8192 tokens of codes 751 us together, 82 and 240 apart)."""
     return _call("tree", stream, q, k_pool, v_pool, table, lens, cu, scale, parents, max_nodes, o, lse,
                  ws, k_scale, v_scale, status)
 

@@ -42,7 +42,7 @@ __device__ __forceinline__ uint64_t turn_step(float f) {
   const uint64_t p0 = 0x7d4d3770ull * m, p1 = 0x7f09d5f4ull * m + (p0 >> 32);
   const uint64_t p2 = 0x9391054aull * m + (p1 >> 32), p3 = 0x28be60dbull * m + (p2 >> 32);
   uint64_t step;
-  if (e > -32) {                             // f of 2^-9 and more
+  if (e > -32) {                             // f of 2^-8 and more
     const uint64_t high = (p3 << 32) | (p2 & 0xffffffffu), low = (p1 << 32) | (p0 & 0xffffffffu);
     if (e < 0) step = (high >> -e) | ((p3 >> 32) << (64 + e));
     else if (e == 0) step = high;
