@@ -453,7 +453,7 @@ fm_status fm_pages_compact(const fm_cache* cache, void* k_pool, void* v_pool, co
  *     element (token, head, c) at token*stride[0] + head*stride[1] + c.  q_out
  *     may be q with the same strides; otherwise it shares no element with q,
  *     and none with k and v (FM_ERR_INVALID, and also where their spans cross
- *     with other token strides, which slices of one buffer do not).
+ *     with other strides; slices of one buffer side by side in each token may).
  * Angles are exact to 2^-34 of a turn at any position below 2^30 and any
  * frequency below 2^64.  Sequences
  * with lens or cu out of range are skipped, their rows of q_out with them; a

@@ -524,7 +524,8 @@ Rows rows_of(const void* p, const int64_t* stride, int total, int heads) {
 }
 
 // a and b share no element, as far as that is found out: where their spans cross
-// (slices of one buffer) their token strides must be the same.
+// their token strides must be the same, and their head strides too unless they lie
+// side by side in each token (slices of one buffer do).
 bool rows_apart(const Rows& a, const Rows& b, int total, int d) {
   if (!overlaps(a.p, 2 * a.span(total, d), b.p, 2 * b.span(total, d))) return true;
   if (a.tok != b.tok) return false;
@@ -535,16 +536,17 @@ bool rows_apart(const Rows& a, const Rows& b, int total, int d) {
     const int64_t off = ((delta % s) + s) % s;
     if (off >= a.in_token(d) && off + b.in_token(d) <= s) return true;
   }
-  // element t s + i head + c of a is element t' s + i' head' + c' of b at delta: for each i
-  // and i' the nearest t - t'
-  for (int64_t i = 0; i < a.heads; ++i)
-    for (int64_t k = 0; k < b.heads; ++k) {
-      const int64_t x = delta + k * b.head - i * a.head;
-      int64_t t = s > 0 ? (2 * x + (x < 0 ? -s : s)) / (2 * s) : 0;
-      t = t < 1 - total ? 1 - total : t > total - 1 ? total - 1 : t;
-      const int64_t left = x - t * s;
-      if (left < d && left > -d) return false;
-    }
+  const int64_t head = a.heads > 1 ? a.head : b.head;
+  if (b.heads > 1 && b.head != head) return false;
+  // element t s + i head + c of a is element t' s + i' head + c' of b at delta: for each
+  // i' - i the nearest t - t'
+  for (int64_t i = 1 - a.heads; i < b.heads; ++i) {
+    const int64_t x = delta + i * head;
+    int64_t t = s > 0 ? (2 * x + (x < 0 ? -s : s)) / (2 * s) : 0;
+    t = t < 1 - total ? 1 - total : t > total - 1 ? total - 1 : t;
+    const int64_t left = x - t * s;
+    if (left < d && left > -d) return false;
+  }
   return true;
 }
 

@@ -42,6 +42,18 @@ def test_queries_over_new_keys_or_values_are_refused(L, which, off):  # noqa: F8
     assert _append(L, R=R, ks=(256, 64), vs=(256, 64), **{which: ctypes.c_void_p(1 << 31)}) == INVALID
 
 
+def test_many_heads_are_looked_through_at_once(L):  # noqa: F811
+    """Spans that cross with other head strides are refused without a look at each pair of heads."""
+    C = _cache(Hkv=40000)
+    R = _rotary(H=40000, q=1 << 40, q_out=(1 << 40) + 128)
+    R.q_stride[:] = (40000 * 128, 128)
+    R.o_stride[:] = (40000 * 128, 256)
+    assert _append(L, C=C, R=R, ks=(40000 * 64, 64), vs=(40000 * 64, 64)) == INVALID
+    R.o_stride[:] = (40000 * 128, 128)
+    R.q_out = (1 << 40) + 16
+    assert _append(L, C=C, R=R, ks=(40000 * 64, 64), vs=(40000 * 64, 64)) == INVALID
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("codes", [False, True])
 @pytest.mark.parametrize("T", [1, 23])
@@ -75,6 +87,10 @@ def test_slices_of_one_buffer(T, codes, step):
         pairs[:, :, 0] = q
         call(pairs[:, :, 0], pairs[:, :, 1])
         assert torch.equal(pairs[:, :, 1], want)
+    rows = torch.empty(H, 2, T, d, dtype=torch.bfloat16, device="cuda").permute(1, 2, 0, 3)    # heads before tokens
+    rows[0] = q
+    call(rows[0], rows[1])
+    assert torch.equal(rows[0], q) and torch.equal(rows[1], want)
     call(q, q)
     assert torch.equal(q, want)
     with pytest.raises(fm.FMError):
